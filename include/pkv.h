@@ -11,6 +11,10 @@
  *   pkv_decode_step             a decode step: each sequence's new token appended, then
  *                               attended (one launch where the plan allows)
  *   pkv_decode_step_fp8         the same over an FP8 (E4M3) cache, the new rows quantised
+ *   pkv_decode_step_q4          the same over a 4-bit cache; pkv_kv_append_q4, pkv_kv_gather_q4
+ *                               and pkv_paged_attention_q4 write, read back and attend it
+ *   pkv_block_tables_extend     block tables and slot map of a step built on the GPU from the
+ *                               request lengths; pkv_block_tables_release gives blocks back
  *   pkv_prefill_attention       varlen causal attention over cu_seqlens that also
  *                               writes the cache
  *
@@ -80,6 +84,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
 #define PKV_DEVERR_TIMEOUT    32u   /* a bounded wait for an asynchronous copy gave up */
 #define PKV_DEVERR_LAYOUT     64u   /* a kernel found its shared memory misaligned and did nothing */
 #define PKV_DEVERR_PREFIX    128u   /* a shared-prefix group whose members' prefixes differ (length, blocks) */
+#define PKV_DEVERR_POOL      256u   /* free list or slot map too small for a row, a bad free count, or a block
+                                       given back twice (block_tables_*: the row or list stays as it was) */
 
 /* Static description of a status code. */
 const char *pkv_status_string(pkv_status status);
@@ -376,6 +382,126 @@ pkv_status pkv_decode_step_fp8(float *out, float *lse, const float *q, const voi
  * new rows assumed), or -1 when the call would be rejected; 0 for B == 0. */
 int pkv_decode_step_fp8_kernel_launches(int B, int Hq, int Hkv, int d, int bs, int MBS, int NB, pkv_dtype new_dt,
                                         int num_splits);
+
+/*
+ * 4-bit KV cache (the low-bit trade-off of zwjcode.cn "KV Cache 的增量解码" §14).  A cache is
+ * uint8 [NB][Hkv][bs][row], row = pkv_q4_row_bytes(d, group) = d / 2 + 4 * G bytes, G = d / group
+ * groups of 32, 64 or 128 elements, d a multiple of group and at most 256.  The bs * row bytes of
+ * one (block, KV head) page hold the codes [bs][d / 2] (byte j: element 2j in the low nibble,
+ * 2j + 1 in the high one), then the parameters [bs][G][2] in fp16: (scale, zero).  The cached
+ * value is zero + scale * code.  Blocks move with pkv_kv_block_copy (dt = PKV_FP8_E4M3, d = row).
+ * The caches must be 4-byte aligned; 16-byte alignment (any allocation) runs the fast kernels.
+ */
+/* Bytes of one row (a token's K or V of one KV head), or -1 for sizes that are not supported. */
+int pkv_q4_row_bytes(int d, int group);
+
+/*
+ * pkv_kv_append_q4 -- quantise and scatter new rows.  For each token t with slot_mapping[t] >= 0
+ * and each KV head h, the rows k_new[t][h][:], v_new[t][h][:] (element type new_dt: PKV_BF16 or
+ * PKV_F32) are written into row (slot / bs, h, slot % bs).  Each group of `group` elements x,
+ * clamped to +-65504, is stored as
+ *   zero = min x rounded down to fp16,  scale = (max x - zero) / 15 rounded to fp16 (nearest even),
+ *   code = (x - zero) / scale rounded half to even and clamped to 0 .. 15 (0 where scale is 0),
+ * each from the exact quotient.  A group that holds a NaN stores zero = NaN, scale 0, codes 0.
+ * Slot errors as pkv_kv_append.
+ */
+pkv_status pkv_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype new_dt, uint8_t *k_cache,
+                            uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d, int group,
+                            int bs, int NB, pkv_stream_t stream);
+
+/*
+ * pkv_kv_gather_q4 -- the values of cached rows: k_out[t][h][:] and v_out[t][h][:] (element type
+ * out_dt: PKV_BF16 or PKV_F32) = zero + scale * code of row (slot / bs, h, slot % bs), slot =
+ * slot_mapping[t]; rows of zeros for a negative slot, and for one >= NB * bs, which sets
+ * PKV_DEVERR_SLOT.  Reads a cached prefix into a bf16 cache (with pkv_kv_append) for
+ * pkv_paged_attention's chunked prefill.  A slot may be named more than once.
+ */
+pkv_status pkv_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, const uint8_t *k_cache,
+                            const uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d, int group,
+                            int bs, int NB, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_q4 -- pkv_paged_attention over a 4-bit cache: the attention of the values
+ * zero + scale * code, as if they had been stored in a wider type.  Query rows cu_q (NULL with
+ * Tq == B and max_q == 1: one per sequence), windows, splits, lse, empty sequences and errors as
+ * there; a block id out of range is read as zeros.
+ *   workspace    pkv_paged_attention_q4_workspace_bytes(...) bytes, 16-byte aligned, zeroed once;
+ *                the rules of pkv_paged_decode_attention
+ */
+size_t pkv_paged_attention_q4_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int group, int bs,
+                                              int MBS, int window, int num_splits);
+
+pkv_status pkv_paged_attention_q4(float *out, float *lse, const float *q, const uint8_t *k_cache,
+                                  const uint8_t *v_cache, const int32_t *block_table, const int32_t *context_lens,
+                                  const int32_t *cu_q, int B, int Tq, int max_q, int Hq, int Hkv, int d, int group,
+                                  int bs, int MBS, int NB, float scale, int window, int num_splits, void *workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * pkv_decode_step_q4 -- a decode step over a 4-bit cache: the same results as
+ * pkv_kv_append_q4(k_new, v_new, new_dt, ..., slot_mapping, T = B) followed by
+ * pkv_paged_attention_q4 with one query per sequence on the same arguments (caches, outputs and
+ * lse bit-identical).
+ *   k_new, v_new  [B][Hkv][d], element type new_dt (PKV_BF16 or PKV_F32)
+ *   slot_mapping  int64 [B]: the slot of position context_lens[b] - 1, or < 0 (no new token)
+ *   workspace     pkv_paged_attention_q4_workspace_bytes(B, B, 1, ...) bytes, same rules
+ */
+pkv_status pkv_decode_step_q4(float *out, float *lse, const float *q, const void *k_new, const void *v_new,
+                              pkv_dtype new_dt, const int64_t *slot_mapping, uint8_t *k_cache, uint8_t *v_cache,
+                              const int32_t *block_table, const int32_t *context_lens, int B, int Hq, int Hkv, int d,
+                              int group, int bs, int MBS, int NB, float scale, int window, int num_splits,
+                              void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * Block tables on the GPU, for sequences that own their blocks (a block shared by forks is left to
+ * the host's block manager).  The pool is a list free_list int32 [NB] whose first free_count[0]
+ * entries are the free blocks, the next one handed out last.  No call waits for the host, so a
+ * decode loop with these calls can be captured into a CUDA graph.  *_out arguments may be the
+ * arrays of the same name without _out.
+ *
+ * pkv_block_tables_extend -- room for new tokens.  Row b holds L = context_lens[b] tokens and gets
+ * n = new_tokens[b] more: its table gets the blocks ceil(L / bs) .. ceil((L + n) / bs) - 1 (rows in
+ * order, the i-th block needed being free_list[count - 1 - i]), and with cu_new the exclusive sums
+ * of the n, slot_mapping[cu_new[b] + i] is the slot of position L + i
+ * (block_table[b][pos / bs] * bs + pos % bs; plumephp.com "KV Cache 优化与注意力机制加速" §4.2-§4.3).
+ *   block_table       int32 [B][MBS], written at the new blocks
+ *   context_lens_out  int32 [B]: L + n
+ *   cu_new            int32 [B + 1]; usable as cu_q of pkv_paged_attention*
+ *   slot_mapping      int64 [T], T >= sum n; entries from cu_new[B] on become -1 (padding)
+ *   free_count_out    int32 [1]
+ * A row with L < 0, n < 0 or L + n > MBS * bs sets PKV_DEVERR_LEN.  A row for which the blocks
+ * needed by it and the rows before it exceed the free ones (rows that need none are served all
+ * the same), or the tokens of it and the rows before it exceed T, sets PKV_DEVERR_POOL.  Such a
+ * row stays as it was: no blocks, no slots, its length unchanged.  A listed or tabled block id
+ * outside [0, NB) sets PKV_DEVERR_BLOCK and its slots are -1.
+ *   workspace         pkv_block_tables_extend_workspace_bytes(B, T) bytes, 16-byte aligned, zeroed
+ *                     once (a call that completes leaves it zero); calls that share it must not
+ *                     overlap
+ */
+size_t pkv_block_tables_extend_workspace_bytes(int B, int T);
+
+pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_lens, const int32_t *new_tokens,
+                                   const int32_t *free_list, const int32_t *free_count, int32_t *context_lens_out,
+                                   int32_t *cu_new, int64_t *slot_mapping, int32_t *free_count_out, int B, int T,
+                                   int MBS, int bs, int NB, void *workspace, size_t workspace_bytes,
+                                   pkv_stream_t stream);
+
+/*
+ * pkv_block_tables_release -- blocks back to the pool: the logical blocks first_block[b] ..
+ * end_block[b] - 1 of every row b (first_block NULL: from 0; end <= first: none) go to the list and
+ * their table entries become -1 (an entry that is -1 already is skipped).  A finished sequence gives
+ * back all its blocks, a sliding window those before it.  They are put on top of the list in reverse
+ * order, so that giving back what one extend took restores the list.  The lengths are the caller's
+ * (a finished row's becomes 0).  A range outside [0, MBS] sets PKV_DEVERR_LEN and an entry outside
+ * [0, NB) PKV_DEVERR_BLOCK; those are skipped.  More blocks than the list has room for (some were
+ * given back twice) set PKV_DEVERR_POOL and nothing is given back.
+ *   workspace   pkv_block_tables_release_workspace_bytes(B) bytes, 4-byte aligned (contents free)
+ */
+size_t pkv_block_tables_release_workspace_bytes(int B);
+
+pkv_status pkv_block_tables_release(int32_t *block_table, const int32_t *first_block, const int32_t *end_block,
+                                    int32_t *free_list, const int32_t *free_count, int32_t *free_count_out, int B,
+                                    int MBS, int NB, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /*
  * pkv_paged_decode_attention_noalloc -- pkv_paged_decode_attention without a workspace.

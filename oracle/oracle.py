@@ -237,6 +237,98 @@ def dequantize_fp8(codes, scales) -> np.ndarray:
     return e4m3_decode(to_numpy(codes)) * to_numpy(scales).astype(np.float64)[..., None]
 
 
+# ----------------------------------------------------------------- 4-bit cache
+# The same reading of zwjcode.cn §14 in 4 bits: groups of `group` elements of a row, each with
+# an fp16 zero (the group's minimum rounded down) and an fp16 scale ((max - zero) / 15 rounded
+# to nearest), codes (x - zero) / scale rounded half to even and clamped to 0..15; inputs are
+# clamped to fp16's range, a group with a NaN stores zero NaN, scale 0, codes 0.  A page (block,
+# KV head) holds the packed codes of its rows, then their (scale, zero) pairs.
+
+F16_MAX = 65504.0
+
+
+def quantize_rows_q4(rows, group: int):
+    """(codes uint8 [..., d], params float16 [..., G, 2] = (scale, zero)) of rows [..., d]."""
+    x = to_f64(rows)
+    x = x.reshape(*x.shape[:-1], x.shape[-1] // group, group)
+    x = np.where(np.isnan(x), x, np.clip(x, -F16_MAX, F16_MAX))
+    bad = np.isnan(x).any(-1)
+    y = np.where(bad[..., None], 0.0, x)
+    low = y.min(-1)
+    zero = low.astype(np.float16)
+    zero = np.where(zero.astype(np.float64) > low, np.nextafter(zero, np.float16(-np.inf)), zero).astype(np.float16)
+    scale = ((y.max(-1) - zero.astype(np.float64)) / 15.0).astype(np.float16)
+    s = scale.astype(np.float64)[..., None]
+    code = np.rint((y - zero.astype(np.float64)[..., None]) / np.where(s > 0, s, 1.0))
+    code = np.where(s > 0, np.clip(code, 0, 15), 0).astype(np.uint8)
+    zero = np.where(bad, np.float16(np.nan), zero).astype(np.float16)
+    return code.reshape(*code.shape[:-2], code.shape[-2] * group), np.stack([scale, zero], -1)
+
+
+def _q4_page(cache: np.ndarray, blk: int, head: int, d: int, group: int):
+    """Views of one page's packed codes [bs][d/2] and parameters [bs][G][2]."""
+    bs = cache.shape[2]
+    page = cache[blk, head].reshape(-1)
+    return page[:bs * d // 2].reshape(bs, d // 2), page[bs * d // 2:].view(np.float16).reshape(bs, d // group, 2)
+
+
+def kv_append_q4(k_cache, v_cache, k_new, v_new, slot_mapping, group: int) -> None:
+    """In place: each new row (token t, KV head h) of K and V quantised into its slot of the
+    uint8 caches [NB][Hkv][bs][d/2 + 4*d/group]."""
+    for cache, new in ((to_numpy(k_cache), k_new), (to_numpy(v_cache), v_new)):
+        codes, params = quantize_rows_q4(new, group)
+        d, bs = codes.shape[-1], cache.shape[2]
+        for t, s in enumerate(to_numpy(slot_mapping).tolist()):
+            if s < 0:
+                continue
+            for h in range(codes.shape[1]):
+                pc, pp = _q4_page(cache, s // bs, h, d, group)
+                pc[s % bs] = codes[t, h, 0::2] | (codes[t, h, 1::2] << 4)
+                pp[s % bs] = params[t, h]
+
+
+def dequantize_q4(cache, d: int, group: int) -> np.ndarray:
+    """float64 cache [NB][Hkv][bs][d]: zero + scale * code, exact."""
+    cache = to_numpy(cache)
+    NB, Hkv, bs, _ = cache.shape
+    out = np.empty((NB, Hkv, bs, d), np.float64)
+    for blk in range(NB):
+        for h in range(Hkv):
+            pc, pp = _q4_page(np.ascontiguousarray(cache), blk, h, d, group)
+            c = np.empty((bs, d), np.float64)
+            c[:, 0::2], c[:, 1::2] = pc & 15, pc >> 4
+            p = np.repeat(pp.astype(np.float64), group, axis=1)
+            out[blk, h] = p[..., 1] + p[..., 0] * c
+    return out
+
+
+def block_tables_extend(table, lens, new_tokens, free, count: int, bs: int, T: int):
+    """The step's blocks row by row, in place in ``table`` [B][MBS]: returns (lens, cu_new, slots [T],
+    count).  The i-th block needed is free[count - 1 - i]; a row that the pool, its table or T cannot
+    hold stays as it was."""
+    table = to_numpy(table)
+    lens = [int(x) for x in to_numpy(lens)]
+    free = [int(x) for x in to_numpy(free)]
+    out, cu, slots = list(lens), [0], []
+    asked = wanted = 0
+    for b, (L, n) in enumerate(zip(lens, (int(x) for x in to_numpy(new_tokens)))):
+        have, want = -(-L // bs), -(-(L + n) // bs)
+        valid = L >= 0 and n >= 0 and want <= table.shape[1] and n > 0
+        if valid:
+            asked += n
+            wanted += want - have
+            valid = asked <= T and (want == have or wanted <= len(free[:count]))
+        if valid:
+            for j in range(have, want):
+                table[b, j] = free[count - 1 - (wanted - (want - have)) - (j - have)]
+            slots += [int(table[b, p // bs]) * bs + p % bs for p in range(L, L + n)]
+            out[b] = L + n
+        cu.append(len(slots))
+    served = sum(-(-o // bs) - -(-l // bs) for o, l in zip(out, lens) if o > l)
+    return (np.array(out, np.int32), np.array(cu, np.int32),
+            np.array(slots + [-1] * (T - len(slots)), np.int64), count - served)
+
+
 def kv_cache_bytes(layers: int, batch: int, heads: int, tokens: int, head_dim: int,
                    elem_bytes: int) -> int:
     """2 * L * N * H * T * d * b: K and V for every layer, sequence, head and token."""

@@ -11,6 +11,10 @@ from ._binding import (  # noqa: F401
     PKV_F32,
     PKV_FP8_E4M3,
     PkvError,
+    block_tables_extend,
+    block_tables_extend_workspace_bytes,
+    block_tables_release,
+    block_tables_release_workspace_bytes,
     decode_kernel_launches,
     decode_step,
     decode_step_kernel_launches,
@@ -19,24 +23,30 @@ from ._binding import (  # noqa: F401
     decode_step_shared_prefix_workspace_bytes,
     decode_step_fp8,
     decode_step_fp8_kernel_launches,
+    decode_step_q4,
     decode_workspace_bytes,
     get_device_error,
     header_functions,
     kv_append,
     kv_append_fp8,
+    kv_append_q4,
     kv_block_copy,
+    kv_gather_q4,
     lib,
     library_path,
     paged_attention,
     paged_attention_kernel_launches,
+    paged_attention_q4,
+    paged_attention_q4_workspace_bytes,
     paged_attention_workspace_bytes,
     paged_decode_attention,
     paged_decode_attention_fp8,
     paged_decode_attention_noalloc,
     prefill_attention,
+    q4_row_bytes,
     selftest_bounded_wait,
 )
-from .blocks import BlockManager, OutOfBlocks, PrefixGroups  # noqa: F401
+from .blocks import BlockManager, DeviceBlocks, OutOfBlocks, PrefixGroups  # noqa: F401
 
 
 def build(force: bool = False) -> str:

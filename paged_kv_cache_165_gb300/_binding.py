@@ -20,6 +20,7 @@ PKV_F32, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
 
 DEVERR = {
     "slot": 1, "block": 2, "len": 4, "cu_seqlens": 8, "pair": 16, "timeout": 32, "layout": 64, "prefix": 128,
+    "pool": 256,
 }
 
 _DTYPES = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.uint8: PKV_FP8_E4M3}
@@ -96,6 +97,25 @@ def lib() -> ctypes.CDLL:
     L.pkv_decode_step_shared_prefix_workspace_bytes.restype = Z
     L.pkv_decode_step_shared_prefix_kernel_launches.argtypes = [I] * 13
     L.pkv_decode_step_shared_prefix_kernel_launches.restype = I
+    L.pkv_q4_row_bytes.argtypes = [I, I]
+    L.pkv_q4_row_bytes.restype = I
+    for name in ("pkv_kv_append_q4", "pkv_kv_gather_q4"):
+        getattr(L, name).argtypes = [P, P, I, P, P, P, I, I, I, I, I, I, P]
+        getattr(L, name).restype = I
+    L.pkv_paged_attention_q4_workspace_bytes.argtypes = [I] * 11
+    L.pkv_paged_attention_q4_workspace_bytes.restype = Z
+    L.pkv_paged_attention_q4.argtypes = [P] * 8 + [I] * 10 + [F, I, I, P, Z, P]
+    L.pkv_paged_attention_q4.restype = I
+    L.pkv_decode_step_q4.argtypes = [P, P, P, P, P, I, P, P, P, P, P] + [I] * 8 + [F, I, I, P, Z, P]
+    L.pkv_decode_step_q4.restype = I
+    L.pkv_block_tables_extend_workspace_bytes.argtypes = [I, I]
+    L.pkv_block_tables_extend_workspace_bytes.restype = Z
+    L.pkv_block_tables_extend.argtypes = [P] * 9 + [I] * 5 + [P, Z, P]
+    L.pkv_block_tables_extend.restype = I
+    L.pkv_block_tables_release_workspace_bytes.argtypes = [I]
+    L.pkv_block_tables_release_workspace_bytes.restype = Z
+    L.pkv_block_tables_release.argtypes = [P] * 6 + [I] * 3 + [P, Z, P]
+    L.pkv_block_tables_release.restype = I
     L.pkv_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, I, I, P, P]
     L.pkv_selftest_bounded_wait.restype = I
     L.pkv_prefill_attention.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, P, P, P, I, I, P]
@@ -514,3 +534,173 @@ def decode_step_fp8_kernel_launches(B, Hq, Hkv, d, bs, MBS, NB, new_dtype=torch.
     """Kernels one decode_step_fp8 call with these sizes enqueues (-1: rejected)."""
     return int(lib().pkv_decode_step_fp8_kernel_launches(B, Hq, Hkv, d, bs, MBS, NB, _DTYPES[new_dtype],
                                                          int(num_splits)))
+
+
+# ----------------------------------------------------------------- 4-bit cache
+
+def q4_row_bytes(d, group) -> int:
+    """Bytes of one row of a 4-bit cache (codes and its share of the page's parameters): the
+    last dimension of k_cache and v_cache, uint8 [NB][Hkv][bs][q4_row_bytes(d, group)]."""
+    n = int(lib().pkv_q4_row_bytes(int(d), int(group)))
+    if n < 0:
+        raise ValueError(f"q4_row_bytes: d={d} group={group} (group 32, 64 or 128, d a multiple of it, d <= 256)")
+    return n
+
+
+def _q4_caches(what, k_cache, v_cache, d, group):
+    _cuda("k_cache", k_cache, torch.uint8)
+    _cuda("v_cache", v_cache, torch.uint8)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q4_row_bytes(d, group):
+        raise ValueError(f"{what}: the caches must be [NB][Hkv][bs][{q4_row_bytes(d, group)}] (q4_row_bytes of d={d}, "
+                         f"group={group}), got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    return k_cache.shape[:3]
+
+
+def _q4_rows(what, fn, k_rows, v_rows, k_cache, v_cache, slot_mapping, group, stream):
+    _cuda("k rows", k_rows)
+    dt = _dtype(k_rows)
+    _cuda("v rows", v_rows, k_rows.dtype)
+    _cuda("slot_mapping", slot_mapping, torch.int64)
+    if k_rows.dim() != 3:
+        raise ValueError(f"{what}: rows must be [T][Hkv][d]")
+    T, _, d = k_rows.shape
+    NB, Hkv, bs = _q4_caches(what, k_cache, v_cache, d, group)
+    if tuple(k_rows.shape) != (T, Hkv, d) or tuple(v_rows.shape) != (T, Hkv, d) or slot_mapping.numel() != T:
+        raise ValueError(f"{what}: shapes do not match [T][Hkv][d] / [T]")
+    _check(fn(_ptr(k_rows), _ptr(v_rows), dt, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, d, int(group), bs,
+              NB, _stream(stream)))
+
+
+def kv_append_q4(k_new, v_new, k_cache, v_cache, slot_mapping, group, stream=None) -> None:
+    """Quantise k_new/v_new [T][Hkv][d] (bf16 or fp32) into a 4-bit cache, uint8
+    [NB][Hkv][bs][q4_row_bytes(d, group)], at slot_mapping[t] (int64, <0 skipped)."""
+    _q4_rows("kv_append_q4", lib().pkv_kv_append_q4, k_new, v_new, k_cache, v_cache, slot_mapping, group, stream)
+
+
+def kv_gather_q4(k_out, v_out, k_cache, v_cache, slot_mapping, group, stream=None) -> None:
+    """k_out/v_out [T][Hkv][d] (bf16 or fp32) = the values of the rows at slot_mapping[t]
+    (int64; rows of zeros for negative slots)."""
+    _q4_rows("kv_gather_q4", lib().pkv_kv_gather_q4, k_out, v_out, k_cache, v_cache, slot_mapping, group, stream)
+
+
+def paged_attention_q4_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, group, bs, MBS, window=0, num_splits=0) -> int:
+    return int(lib().pkv_paged_attention_q4_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, group, bs, MBS, window,
+                                                            num_splits))
+
+
+def _q4_attend_args(what, out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace):
+    _cuda("q", q, torch.float32)
+    _cuda("out", out, torch.float32)
+    _cuda("block_table", block_table, torch.int32)
+    _cuda("context_lens", context_lens, torch.int32)
+    if lse is not None:
+        _cuda("lse", lse, torch.float32)
+    if q.dim() != 3:
+        raise ValueError(f"{what}: q must be [rows][Hq][d]")
+    Tq, Hq, d = q.shape
+    B = context_lens.numel()
+    NB, Hkv, bs = _q4_caches(what, k_cache, v_cache, d, group)
+    if tuple(out.shape) != (Tq, Hq, d) or block_table.dim() != 2 or block_table.shape[0] != B or \
+            (lse is not None and lse.numel() != Tq * Hq):
+        raise ValueError(f"{what}: shapes do not match")
+    ws_bytes = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    return B, Tq, Hq, Hkv, d, bs, NB, block_table.shape[1], ws_bytes
+
+
+def paged_attention_q4(out, q, k_cache, v_cache, block_table, context_lens, scale, group, cu_q=None, max_q=1,
+                       window=0, lse=None, num_splits=0, workspace=None, stream=None) -> None:
+    """paged_attention over a 4-bit cache: q, out [Tq][Hq][d] fp32, the newest rows of every
+    sequence (cu_q int32 [B+1]; None: one row per sequence), causal, optional window."""
+    B, Tq, Hq, Hkv, d, bs, NB, MBS, ws_bytes = _q4_attend_args(
+        "paged_attention_q4", out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace)
+    if cu_q is not None:
+        _cuda("cu_q", cu_q, torch.int32)
+    if (cu_q is not None and cu_q.numel() != B + 1) or (cu_q is None and Tq != B):
+        raise ValueError("paged_attention_q4: shapes do not match")
+    _check(lib().pkv_paged_attention_q4(
+        _ptr(out), _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(context_lens), _ptr(cu_q),
+        B, Tq, int(max_q), Hq, Hkv, d, int(group), bs, MBS, NB, float(scale), int(window), int(num_splits),
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def decode_step_q4(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_table, context_lens, scale, group,
+                   window=0, lse=None, num_splits=0, workspace=None, stream=None) -> None:
+    """decode_step over a 4-bit cache: k_new/v_new [B][Hkv][d] (bf16 or fp32) are quantised into
+    slot_mapping[b] (int64, < 0: none), then out [B][Hq][d] fp32 = attention of q over the cache."""
+    B, Tq, Hq, Hkv, d, bs, NB, MBS, ws_bytes = _q4_attend_args(
+        "decode_step_q4", out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace)
+    _cuda("k_new", k_new)
+    new_dt = _dtype(k_new)
+    _cuda("v_new", v_new, k_new.dtype)
+    _cuda("slot_mapping", slot_mapping, torch.int64)
+    if Tq != B or tuple(k_new.shape) != (B, Hkv, d) or tuple(v_new.shape) != (B, Hkv, d) or slot_mapping.numel() != B:
+        raise ValueError("decode_step_q4: shapes do not match")
+    _check(lib().pkv_decode_step_q4(
+        _ptr(out), _ptr(lse), _ptr(q), _ptr(k_new), _ptr(v_new), new_dt, _ptr(slot_mapping), _ptr(k_cache),
+        _ptr(v_cache), _ptr(block_table), _ptr(context_lens), B, Hq, Hkv, d, int(group), bs, MBS, NB, float(scale),
+        int(window), int(num_splits), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------- block tables
+
+def block_tables_extend_workspace_bytes(B, T) -> int:
+    return int(lib().pkv_block_tables_extend_workspace_bytes(int(B), int(T)))
+
+
+def block_tables_release_workspace_bytes(B) -> int:
+    return int(lib().pkv_block_tables_release_workspace_bytes(int(B)))
+
+
+def block_tables_extend(block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
+                        slot_mapping, free_count_out, bs, workspace=None, stream=None) -> None:
+    """Blocks, table entries and slots for new_tokens[b] more tokens of every row (see pkv.h).
+
+    block_table int32 [B][MBS]; context_lens, new_tokens, context_lens_out int32 [B]; free_list
+    int32 [NB]; free_count, free_count_out int32 [1]; cu_new int32 [B+1]; slot_mapping int64 [T]
+    (entries past the new tokens become -1).  The *_out tensors may be their inputs."""
+    for name, t in (("block_table", block_table), ("context_lens", context_lens), ("new_tokens", new_tokens),
+                    ("free_list", free_list), ("free_count", free_count), ("context_lens_out", context_lens_out),
+                    ("cu_new", cu_new), ("free_count_out", free_count_out)):
+        _cuda(name, t, torch.int32)
+    _cuda("slot_mapping", slot_mapping, torch.int64)
+    if block_table.dim() != 2:
+        raise ValueError("block_tables_extend: block_table must be [B][MBS]")
+    B, MBS = block_table.shape
+    if context_lens.numel() != B or new_tokens.numel() != B or context_lens_out.numel() != B or \
+            cu_new.numel() != B + 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("block_tables_extend: shapes do not match")
+    ws_bytes = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pkv_block_tables_extend(
+        _ptr(block_table), _ptr(context_lens), _ptr(new_tokens), _ptr(free_list), _ptr(free_count),
+        _ptr(context_lens_out), _ptr(cu_new), _ptr(slot_mapping), _ptr(free_count_out), B, slot_mapping.numel(), MBS,
+        int(bs), free_list.numel(), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def block_tables_release(block_table, first_block, end_block, free_list, free_count, free_count_out, workspace=None,
+                         stream=None) -> None:
+    """Logical blocks [first_block[b], end_block[b]) of every row (int32 [B]; first_block None: 0)
+    back to the free list, their table entries -1 (see pkv.h)."""
+    for name, t in (("block_table", block_table), ("end_block", end_block), ("free_list", free_list),
+                    ("free_count", free_count), ("free_count_out", free_count_out)):
+        _cuda(name, t, torch.int32)
+    if first_block is not None:
+        _cuda("first_block", first_block, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_tables_release: block_table must be [B][MBS]")
+    B, MBS = block_table.shape
+    if end_block.numel() != B or (first_block is not None and first_block.numel() != B) or free_count.numel() != 1 or \
+            free_count_out.numel() != 1:
+        raise ValueError("block_tables_release: shapes do not match")
+    ws_bytes = 0
+    if workspace is not None:
+        _cuda("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pkv_block_tables_release(
+        _ptr(block_table), _ptr(first_block), _ptr(end_block), _ptr(free_list), _ptr(free_count), _ptr(free_count_out),
+        B, MBS, free_list.numel(), _ptr(workspace), ws_bytes, _stream(stream)))

@@ -2,7 +2,8 @@
 reference counts, fork and copy-on-write.
 
 This is the bookkeeping that sits above the C ABI and produces its inputs
-(block tables, slot mappings, copy pairs); nothing here runs on the GPU.
+(block tables, slot mappings, copy pairs).  BlockManager runs on the host; DeviceBlocks
+keeps the tables of sequences that own their blocks on the GPU.
 
 * Blocks of ``block_size`` tokens are handed out on demand from a free pool; a
   sequence's logical block j maps to a physical block through its table
@@ -254,3 +255,61 @@ class BlockManager:
         for b in range(self.num_blocks):
             if (b in free) != (self.refcount[b] == 0):
                 raise AssertionError(f"block {b}: free-list membership disagrees with its count")
+
+
+class DeviceBlocks:
+    """Block tables, lengths and the free list of a batch kept on the GPU: the state of
+    block_tables_extend and block_tables_release, for sequences that own their blocks.
+
+    ``extend`` and ``release`` only enqueue work on the current stream (no host round trip),
+    so a decode loop over them can be captured into a CUDA graph.  ``rows`` is the batch size,
+    ``max_blocks`` the blocks a row may hold, ``max_tokens`` the most tokens one ``extend``
+    places; ``order`` is the order in which blocks are handed out (default 0..NB-1).
+    """
+
+    def __init__(self, num_blocks: int, block_size: int, rows: int, max_blocks: int, max_tokens: int,
+                 order: Optional[Sequence[int]] = None, device="cuda"):
+        from . import _binding
+        if min(num_blocks, block_size, rows, max_blocks) < 1 or max_tokens < 0:
+            raise ValueError("sizes must be positive")
+        ids = list(range(num_blocks)) if order is None else [int(x) for x in order]
+        if sorted(ids) != list(range(num_blocks)):
+            raise ValueError("order must be a permutation of the block ids")
+        self.block_size = block_size
+        # the top of the list is handed out first
+        self.free_list = torch.tensor(ids[::-1], dtype=torch.int32, device=device)
+        self.free_count = torch.tensor([num_blocks], dtype=torch.int32, device=device)
+        self.block_table = torch.full((rows, max_blocks), -1, dtype=torch.int32, device=device)
+        self.context_lens = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.cu_new = torch.zeros(rows + 1, dtype=torch.int32, device=device)
+        self.slot_mapping = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+        ws = max(16, _binding.block_tables_extend_workspace_bytes(rows, max_tokens),
+                 _binding.block_tables_release_workspace_bytes(rows))
+        # two pieces: extend's stays zero, release's may hold anything
+        self._extend_ws = torch.zeros(16, dtype=torch.uint8, device=device)
+        self._release_ws = torch.empty((ws + 3) // 4 * 4, dtype=torch.uint8, device=device)
+
+    def extend(self, new_tokens: torch.Tensor, num_tokens: Optional[int] = None, stream=None) -> torch.Tensor:
+        """Room for new_tokens[b] (int32 [rows], on the device) more tokens of every row.  Returns
+        slot_mapping[:num_tokens] (default: all of it; -1 past the new tokens); cu_new holds
+        the rows' offsets and context_lens and block_table are up to date."""
+        from . import _binding
+        slots = self.slot_mapping if num_tokens is None else self.slot_mapping[:num_tokens]
+        _binding.block_tables_extend(self.block_table, self.context_lens, new_tokens, self.free_list, self.free_count,
+                                     self.context_lens, self.cu_new, slots, self.free_count, self.block_size,
+                                     workspace=self._extend_ws, stream=stream)
+        return slots
+
+    def release(self, end_block: torch.Tensor, first_block: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Logical blocks [first_block[b], end_block[b]) of every row (int32 [rows], on the
+        device) back to the pool.  The lengths stay; see ``finish``."""
+        from . import _binding
+        _binding.block_tables_release(self.block_table, first_block, end_block, self.free_list, self.free_count,
+                                      self.free_count, workspace=self._release_ws, stream=stream)
+
+    def finish(self, done: torch.Tensor) -> None:
+        """Give back every block of the rows where ``done`` (bool [rows], on the device) holds and
+        set their lengths to 0 (on the current stream)."""
+        end = torch.where(done, self.block_table.shape[1], 0).to(torch.int32)
+        self.release(end)
+        self.context_lens.masked_fill_(done, 0)

@@ -1,0 +1,189 @@
+// cache_q4.cu -- writes into and reads out of the 4-bit paged cache.
+//
+// kv_append_q4: each new token's K and V rows, quantised as q4_codes.cuh says, into the slot
+//   slot_mapping[t] names (limoncc.com "大语言模型研究15——注意力机制优化之KV缓存" §2; the
+//   low-bit trade-off of zwjcode.cn "KV Cache 的增量解码" §14).
+// kv_gather_q4: the values of the rows in given slots, as bf16 or fp32 rows.
+//
+// A thread owns eight consecutive elements (one 32-bit word of codes), so a warp covers 256
+// consecutive elements of the input and a group is 4, 8 or 16 neighbouring lanes, whatever
+// the head size: groups never straddle a warp because 256 is a multiple of each group size.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "q4_codes.cuh"
+
+namespace pkv {
+namespace {
+
+struct Q4Rows {
+    const int64_t *slots;
+    long long words;     // 8-element words of K (and as many of V): T * Hkv * d / 8
+    int Hkv, row_words;  // d / 8
+    int lanes;           // lanes that share a group: group / 8
+    int bs, page_bytes;  // bs * row bytes
+    long long n_slots;
+    unsigned *err;
+};
+
+// Where word w of the new rows lives: its page's byte offset, its row in the page and its
+// position in the row; slot < 0 when the token is padding or its slot is out of range.
+struct Q4Place {
+    long long slot, page;
+    int off, j;
+};
+__device__ __forceinline__ Q4Place q4_place(const Q4Rows &r, long long w) {
+    Q4Place a;
+    a.j = static_cast<int>(w % r.row_words);
+    const long long th = w / r.row_words;   // t * Hkv + h
+    const int h = static_cast<int>(th % r.Hkv);
+    const long long t = th / r.Hkv;
+    a.slot = __ldg(r.slots + t);
+    if (a.slot >= r.n_slots) {
+        if (h == 0 && a.j == 0) raise_error(r.err, PKV_DEVERR_SLOT);
+        a.slot = -1;
+    }
+    const long long blk = a.slot / r.bs;
+    a.off = static_cast<int>(a.slot - blk * r.bs);
+    a.page = (blk * r.Hkv + h) * r.page_bytes;
+    return a;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+    kv_append_q4_kernel(const T *__restrict__ k_new, const T *__restrict__ v_new, uint8_t *__restrict__ kc,
+                        uint8_t *__restrict__ vc, const Q4Rows r) {
+    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+    // whole warps run each turn: the group's lanes exchange their extremes
+    for (long long w0 = blockIdx.x * static_cast<long long>(blockDim.x) + (threadIdx.x & ~31); w0 < r.words;
+         w0 += stride) {
+        const long long w = w0 + (threadIdx.x & 31);
+        const bool live = w < r.words;
+        const Q4Place a = q4_place(r, live ? w : r.words - 1);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            float x[8] = {};
+            if (live) q4_load8<T, VEC>((side ? v_new : k_new) + w * 8, x);
+            __half2 par;
+            const uint32_t code = q4_quantise8(x, r.lanes, par);
+            if (!live || a.slot < 0) continue;
+            uint8_t *page = (side ? vc : kc) + a.page;
+            reinterpret_cast<uint32_t *>(page)[a.off * r.row_words + a.j] = code;
+            if (a.j % r.lanes == 0)
+                reinterpret_cast<__half2 *>(page + r.bs * r.row_words * 4)[a.off * (r.row_words / r.lanes) +
+                                                                            a.j / r.lanes] = par;
+        }
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+    kv_gather_q4_kernel(T *__restrict__ k_out, T *__restrict__ v_out, const uint8_t *__restrict__ kc,
+                        const uint8_t *__restrict__ vc, const Q4Rows r) {
+    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long w = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; w < r.words; w += stride) {
+        const Q4Place a = q4_place(r, w);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            float x[8] = {};
+            if (a.slot >= 0) {
+                const uint8_t *page = (side ? vc : kc) + a.page;
+                const uint32_t code = __ldg(reinterpret_cast<const uint32_t *>(page) + a.off * r.row_words + a.j);
+                const float2 p = __half22float2(
+                    __ldg(reinterpret_cast<const __half2 *>(page + r.bs * r.row_words * 4) +
+                          a.off * (r.row_words / r.lanes) + a.j / r.lanes));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, static_cast<float>((code >> (4 * i)) & 15u), p.y);
+            }
+            T *dst = (side ? v_out : k_out) + w * 8;
+            if constexpr (sizeof(T) == 2) {
+                // the fp32 value (one rounding of zero + scale * code) rounded to bf16
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+                if constexpr (VEC) {
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint16_t *>(dst)[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+                }
+            } else if constexpr (VEC) {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = x[i];
+            }
+        }
+    }
+}
+
+Q4Rows rows_of(const int64_t *slots, int T, int Hkv, int d, int group, int bs, int NB, unsigned *err) {
+    Q4Rows r;
+    r.slots = slots;
+    r.words = static_cast<long long>(T) * Hkv * (d / 8);
+    r.Hkv = Hkv;
+    r.row_words = d / 8;
+    r.lanes = group / 8;
+    r.bs = bs;
+    r.page_bytes = bs * q4_row_bytes(d, group);
+    r.n_slots = static_cast<long long>(NB) * bs;
+    r.err = err;
+    return r;
+}
+
+unsigned grid_of(long long words, int sm_count) {
+    return static_cast<unsigned>(std::min<long long>((words + 255) / 256, 8ll * sm_count));
+}
+
+bool aligned(const void *a, const void *b, unsigned n) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & (n - 1)) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype new_dt, uint8_t *k_cache,
+                                uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d, int group,
+                                int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream) {
+    if (T == 0) return cudaSuccess;
+    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
+    const unsigned grid = grid_of(r.words, sm_count);
+    const bool vec = aligned(k_new, v_new, 16);
+#define PKV_Q4_APPEND(TT, VV)                                                                        \
+    kv_append_q4_kernel<TT, VV><<<grid, 256, 0, stream>>>(static_cast<const TT *>(k_new),            \
+                                                          static_cast<const TT *>(v_new), k_cache, v_cache, r)
+    if (new_dt == PKV_BF16) {
+        if (vec) PKV_Q4_APPEND(__nv_bfloat16, true);
+        else PKV_Q4_APPEND(__nv_bfloat16, false);
+    } else {
+        if (vec) PKV_Q4_APPEND(float, true);
+        else PKV_Q4_APPEND(float, false);
+    }
+#undef PKV_Q4_APPEND
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, const uint8_t *k_cache,
+                                const uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d,
+                                int group, int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream) {
+    if (T == 0) return cudaSuccess;
+    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
+    const unsigned grid = grid_of(r.words, sm_count);
+    const bool vec = aligned(k_out, v_out, 16);
+#define PKV_Q4_GATHER(TT, VV)                                                                     \
+    kv_gather_q4_kernel<TT, VV><<<grid, 256, 0, stream>>>(static_cast<TT *>(k_out),               \
+                                                          static_cast<TT *>(v_out), k_cache, v_cache, r)
+    if (out_dt == PKV_BF16) {
+        if (vec) PKV_Q4_GATHER(__nv_bfloat16, true);
+        else PKV_Q4_GATHER(__nv_bfloat16, false);
+    } else {
+        if (vec) PKV_Q4_GATHER(float, true);
+        else PKV_Q4_GATHER(float, false);
+    }
+#undef PKV_Q4_GATHER
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

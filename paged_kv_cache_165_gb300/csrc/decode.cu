@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(32)
 // of nc/4, and the G partial sums are added through shared memory.  Sequences with at
 // most one chunk were written directly by the attention kernel.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeMaxChunks = 4096;
+constexpr int kMergeMaxChunks = kDecodeMaxChunks;
 constexpr int kMergePrefetch = 6;   // even: the prefetched chunks keep the two sums' order
 
 __global__ void __launch_bounds__(kMergeThreads)
@@ -782,9 +782,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     if (tid == 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kLn2;
 }
 
+}  // namespace
+
 // The merge as a programmatic dependent of the attention kernel just launched on `stream`:
 // its blocks may be scheduled while the attention kernel drains and wait in pdl_wait().
-cudaError_t launch_merge(const DecodeKParams &kp, int d, int bs, unsigned rows_x_heads, cudaStream_t stream) {
+cudaError_t launch_decode_merge(const DecodeKParams &kp, int d, int bs, unsigned rows_x_heads, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows_x_heads);
     cfg.blockDim = dim3(kMergeThreads);
@@ -797,6 +799,8 @@ cudaError_t launch_merge(const DecodeKParams &kp, int d, int bs, unsigned rows_x
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, decode_merge_kernel, kp, d, bs);
 }
+
+namespace {
 
 // ====================================================================== launch
 
@@ -1109,7 +1113,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
         if (plan.umma) {
             e = launch_decode_umma(kp, tk, tv, a.d, a.bs, dim3(plan.splits, a.Hkv, a.B * plan.qtiles), stream);
             if (e != cudaSuccess || plan.splits == 1) return e;
-            return launch_merge(kp, a.d, a.bs, static_cast<unsigned>(rows * a.Hq), stream);
+            return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(rows * a.Hq), stream);
         }
         if (plan.group) {
             const dim3 ggrid(plan.splits, a.Hkv, a.B);
@@ -1123,7 +1127,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
                 else e = launch_group<256, 32, 3>(kp, tk, tv, ggrid, stream);
             }
             if (e != cudaSuccess || plan.splits == 1) return e;
-            return launch_merge(kp, a.d, a.bs, static_cast<unsigned>(a.B * a.Hq), stream);
+            return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(a.B * a.Hq), stream);
         }
         const dim3 grid(static_cast<unsigned>(plan.splits) * kp.head_tiles, a.Hkv, a.B);
         if (a.bs == 16) {
@@ -1143,7 +1147,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
                              : launch_simt<uint8_t>(a, kp, grid, stream);
         if (e != cudaSuccess || plan.splits == 1) return e;
     }
-    return launch_merge(kp, a.d, a.bs, static_cast<unsigned>(rows * a.Hq), stream);
+    return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(rows * a.Hq), stream);
 }
 
 }  // namespace pkv

@@ -165,6 +165,12 @@ cudaError_t launch_shared_prefix(const DecodeKParams &kp, const CUtensorMap &tk,
 cudaError_t launch_shared_prefix_merge(const DecodeKParams &kp, const float *suffix_lse, int d, int bs,
                                        int n_groups, int n_members, cudaStream_t stream);
 
+// Merge of the chunk partials ws_o / ws_lse of every (query row, head) into out and lse by
+// log-sum-exp (decode.cu), as a programmatic dependent of the attention kernel launched before
+// it; at most kDecodeMaxChunks chunks per sequence.
+constexpr int kDecodeMaxChunks = 4096;
+cudaError_t launch_decode_merge(const DecodeKParams &kp, int d, int bs, unsigned rows_x_heads, cudaStream_t stream);
+
 // FP8 (E4M3) decode (decode_fp8.cu): d = 128, bs in {16, 32}, up to 8 query heads per KV
 // head; grid (chunks x head tiles, Hkv, B).  tk / tv are uint8 maps with {128, bs} boxes.
 cudaError_t launch_decode_fp8(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, int bs,

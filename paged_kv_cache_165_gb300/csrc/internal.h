@@ -41,6 +41,15 @@ cudaError_t launch_kv_block_copy(void *k_cache, void *v_cache, int elem_bytes,
                                  const int32_t *pairs, int n, int Hkv, int d, int bs, int NB,
                                  unsigned *err, cudaStream_t stream);
 
+// 4-bit caches (cache_q4.cu): rows quantised into slots, and the values of slots read out.
+// Sizes checked by the caller: d % group == 0, group 32, 64 or 128, caches 4-byte aligned.
+cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype new_dt, uint8_t *k_cache,
+                                uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d, int group,
+                                int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream);
+cudaError_t launch_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, const uint8_t *k_cache,
+                                const uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d,
+                                int group, int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream);
+
 // ------------------------------------------------------------------ decode
 
 struct DecodePlan {
@@ -121,6 +130,65 @@ inline int visible_blocks(int MBS, int bs, int window) {
 
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype dt,
                           cudaStream_t stream);
+
+// ------------------------------------------------- attention over a 4-bit cache
+
+struct Q4Plan {
+    int splits;          // chunks per sequence at most (1: one pass, no workspace)
+    int chunk_pages;     // blocks per chunk
+    size_t workspace_bytes;
+};
+
+// pages: the blocks any row can see; aligned: caches and q on 16-byte boundaries.
+Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int group, int bs, int pages,
+                      int num_splits, int sm_count, bool aligned);
+
+struct AttendQ4Args {
+    float *out;
+    float *lse;
+    const float *q;
+    const uint8_t *k_cache;
+    const uint8_t *v_cache;
+    const int32_t *block_table;
+    const int32_t *context_lens;
+    const int32_t *cu_q;   // query rows per sequence; nullptr: one per sequence
+    int B, rows, Hq, Hkv, d, group, bs, MBS, NB;
+    float scale;
+    int window;
+    void *workspace;
+    unsigned *err;
+};
+
+cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStream_t stream);
+
+// ------------------------------------------------------------------ block tables
+
+struct ExtendArgs {
+    int32_t *block_table;
+    const int32_t *context_lens, *new_tokens, *free_list, *free_count;
+    int32_t *context_lens_out, *cu_new;
+    int64_t *slot_mapping;
+    int32_t *free_count_out;
+    int B, T, MBS, bs, NB;
+    unsigned *arrivals;    // workspace (more than one block): zero before and after
+    unsigned *err;
+};
+
+struct ReleaseArgs {
+    int32_t *block_table;
+    const int32_t *first_block, *end_block;
+    int32_t *free_list;
+    const int32_t *free_count;
+    int32_t *free_count_out;
+    int B, MBS, NB;
+    int32_t *counts;       // workspace [B + 1]: entries given back per row, the count before
+    unsigned *err;
+};
+
+int extend_blocks(int B, int T, int sm_count);           // thread blocks of an extend launch
+bool release_in_one_block(int B, int MBS);
+cudaError_t launch_block_tables_extend(const ExtendArgs &a, int sm_count, cudaStream_t stream);
+cudaError_t launch_block_tables_release(const ReleaseArgs &a, int sm_count, cudaStream_t stream);
 
 // ----------------------------------------------------------------- prefill
 

@@ -1,0 +1,361 @@
+"""4-bit KV cache on the GPU against the fp64 oracle: quantising appends bit-exact, values read
+back, and attention over the values on every kernel path."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_cache_165_gb300 as pkv
+from oracle import oracle as orc
+from paged_kv_cache_165_gb300 import _build
+from workloads import gen
+
+from helpers import assert_attn_close, dev
+
+pytestmark = pytest.mark.gpu
+
+# out and lse in fp32, inputs ~ N(0, 1).  A score is a sum of d terms q * value and is off by at most
+# ~(d / 8 + 16) * 2^-24 * scale * sum |q| (|zero| + 15 scale_g) (fp32 partial sums; the split of q into two
+# f16 parts adds 2^-22 of the same sum): at d = 256, sum |q| * 5 = 1100 / 16, 48 * 6e-8 * 69 = 2e-4.  lse is
+# off by as much; out by twice that times max |value| / 2 in the worst case, and rounding errors that do not
+# all point one way stay well below: one bound for both.
+ATOL = 2e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    _build.build()
+    pkv.lib()
+    pkv.get_device_error()
+
+
+def row_bytes(d, group):
+    return d // 2 + 4 * (d // group)
+
+
+def q4_cache(rows, group):
+    """uint8 cache [NB][Hkv][bs][row] of rows [NB][Hkv][bs][d]."""
+    nb, hkv, bs, d = rows.shape
+    codes, params = orc.quantize_rows_q4(rows, group)
+    packed = (codes[..., 0::2] | (codes[..., 1::2] << 4)).reshape(nb, hkv, -1)
+    out = np.concatenate([packed, np.ascontiguousarray(params).view(np.uint8).reshape(nb, hkv, -1)], -1)
+    return torch.from_numpy(out.reshape(nb, hkv, bs, row_bytes(d, group)))
+
+
+# ------------------------------------------------------------------ append and gather
+
+@pytest.mark.parametrize("dtype,d,group,bs,hkv", [
+    (torch.bfloat16, 128, 64, 16, 4), (torch.bfloat16, 128, 128, 32, 1), (torch.float32, 64, 32, 16, 2),
+    (torch.float32, 96, 32, 8, 3), (torch.bfloat16, 256, 128, 16, 2), (torch.bfloat16, 32, 32, 24, 5),
+])
+@pytest.mark.parametrize("T", [1, 37])
+def test_append_q4_bit_exact_and_gather(dtype, d, group, bs, hkv, T):
+    nb = 9
+    g = gen.generator(d + T)
+    kn = gen.randn(g, (T, hkv, d)) * torch.logspace(-6, 5, T)[:, None, None]
+    vn = gen.randn(g, (T, hkv, d)) + 3.0
+    kn[T // 2, 0] = 0.25                          # a constant group: scale 0
+    vn[T - 1, hkv - 1, 1] = float("nan")
+    kn[0, 0, 0], kn[0, 0, 1] = float("inf"), -1e6
+    kn, vn = kn.to(dtype), vn.to(dtype)
+    slots = torch.tensor(gen.permutation(g, nb * bs)[:T], dtype=torch.int64)
+    if T > 4:
+        slots[4] = -1
+    kc = torch.full((nb, hkv, bs, row_bytes(d, group)), 0x5A, dtype=torch.uint8)
+    vc = kc.clone()
+    gk, gv = dev(kc), dev(vc)
+    pkv.kv_append_q4(dev(kn), dev(vn), gk, gv, dev(slots), group)
+    assert pkv.get_device_error() == 0
+    orc.kv_append_q4(kc, vc, kn, vn, slots, group)
+    # a NaN zero may carry any NaN bits: compare those values as values
+    gkn, gvn = gk.cpu().numpy(), gv.cpu().numpy()
+    assert np.array_equal(gkn, kc.numpy())
+    diff = gvn != vc.numpy()
+    dk, dv = orc.dequantize_q4(kc, d, group), orc.dequantize_q4(gvn, d, group)
+    assert diff.sum() <= 2 and np.isnan(orc.dequantize_q4(vc, d, group)[np.isnan(dv)]).all()
+    # the values read back: fp32 rounds zero + scale * code once (2^-24), bf16 once more (2^-8)
+    for out_dt, tol in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8 * (1 + 2.0 ** -15))):
+        ko = torch.full((T, hkv, d), 7.0, dtype=out_dt, device="cuda")
+        vo = ko.clone()
+        pkv.kv_gather_q4(ko, vo, gk, gv, dev(slots), group)
+        assert pkv.get_device_error() == 0
+        for got, want in ((ko, dk), (vo, dv)):
+            w = np.stack([want[s // bs, :, s % bs] if s >= 0 else np.zeros((hkv, d)) for s in slots.tolist()])
+            x = got.double().cpu().numpy()
+            assert np.array_equal(np.isnan(x), np.isnan(w))
+            ok = ~np.isnan(w)
+            assert np.all(np.abs(x[ok] - w[ok]) <= tol * np.abs(w[ok]))
+
+
+def test_append_q4_at_rounding_boundaries():
+    """Rows whose quotients sit on or one fp32 step beside k + 1/2, and ranges whose fp16 scale does."""
+    g = gen.generator(5)
+    rows = []
+    for i in range(400):
+        s = float(np.float16(0.01 + 0.37 * i))
+        z = float(np.float16(-1.7 * i - 0.3))
+        k = torch.randint(0, 15, (64,), generator=g).double()
+        x = (z + (k + 0.5) * s).float()
+        x = torch.where(torch.arange(64) % 3 == 1, torch.nextafter(x, torch.tensor(1e9)), x)
+        x = torch.where(torch.arange(64) % 3 == 2, torch.nextafter(x, torch.tensor(-1e9)), x)
+        x[0], x[1] = z, z + 15 * s
+        rows.append(x)
+        h = np.float16(0.5 + 0.01 * i)
+        mid = (float(h) + float(np.nextafter(h, np.float16(np.inf)))) / 2      # halfway between two scales
+        y = torch.rand(64, generator=g) * 15 * mid
+        y[0], y[1] = 0.0, 15 * mid
+        if i % 3:
+            y[1] = torch.nextafter(y[1], torch.tensor(1e9 if i % 3 == 1 else -1e9))
+        rows.append(y)
+    new = torch.stack(rows).view(-1, 1, 64)
+    T = new.shape[0]
+    kc = torch.zeros((T // 16, 1, 16, row_bytes(64, 64)), dtype=torch.uint8)
+    vc = kc.clone()
+    gk, gv = dev(kc), dev(vc)
+    slots = torch.arange(T)
+    pkv.kv_append_q4(dev(new), dev(-new), gk, gv, dev(slots), 64)
+    orc.kv_append_q4(kc, vc, new, -new, slots, 64)
+    assert torch.equal(gk.cpu(), kc) and torch.equal(gv.cpu(), vc)
+
+
+def test_append_q4_unaligned_rows_and_out_of_range_slots():
+    g = gen.generator(6)
+    base = gen.randn(g, (3 * 2 * 64 + 1,), torch.bfloat16)
+    new = dev(base)[1:].view(3, 2, 64)            # contiguous, two bytes off a 16-byte boundary
+    kc = torch.zeros((2, 2, 16, row_bytes(64, 32)), dtype=torch.uint8)
+    gk, gv = dev(kc), dev(kc)
+    slots = torch.tensor([3, 32, 17])
+    pkv.kv_append_q4(new, new, gk, gv, dev(slots), 32)
+    assert pkv.get_device_error() & pkv.DEVERR["slot"]
+    vc = kc.clone()
+    orc.kv_append_q4(kc, vc, base[1:].view(3, 2, 64)[[0, 2]], base[1:].view(3, 2, 64)[[0, 2]], slots[[0, 2]], 32)
+    assert torch.equal(gk.cpu(), kc) and torch.equal(gv.cpu(), vc)
+    out = torch.full((3 * 2 * 64 + 1,), 9.0, device="cuda")
+    ko = out[1:].view(3, 2, 64)
+    pkv.kv_gather_q4(ko, torch.empty_like(ko), gk, gv, dev(slots), 32)
+    assert pkv.get_device_error() & pkv.DEVERR["slot"]
+    assert torch.all(ko[1] == 0) and torch.any(ko[0] != 0) and out[0] == 9.0
+
+
+def test_q4_block_copy_moves_pages():
+    g = gen.generator(8)
+    kc = torch.randint(0, 255, (6, 2, 16, 72), generator=g, dtype=torch.uint8)
+    vc = torch.randint(0, 255, (6, 2, 16, 72), generator=g, dtype=torch.uint8)
+    pairs = torch.tensor([[1, 4], [2, 0]], dtype=torch.int32)
+    gk, gv = dev(kc), dev(vc)
+    pkv.kv_block_copy(gk, gv, dev(pairs))
+    oracle.kv_block_copy(kc, vc, pairs)
+    assert torch.equal(gk.cpu(), kc) and torch.equal(gv.cpu(), vc)
+
+
+# ------------------------------------------------------------------------- attention
+
+def q4_case(seed, lens, hq, hkv, d, group, bs, rows=None, spare=3, poison=True):
+    """Caches, tables, lengths and queries; slots past a sequence's end hold NaN parameters."""
+    g = gen.generator(seed)
+    per_seq = [gen.blocks_needed(n, bs) for n in lens]
+    nb = sum(per_seq) + spare
+    table = gen.block_table_from_order(gen.permutation(g, nb), per_seq)
+    k = gen.randn(g, (nb, hkv, bs, d)) + 0.5
+    v = gen.randn(g, (nb, hkv, bs, d))
+    if poison:
+        for b, n in enumerate(lens):
+            for pos in range(n, per_seq[b] * bs):
+                s = oracle.slot_of(table[b], pos, bs)
+                k[s // bs, :, s % bs] = float("nan")
+                v[s // bs, :, s % bs] = float("nan")
+    kc, vc = q4_cache(k, group), q4_cache(v, group)
+    rows = rows or [1] * len(lens)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(rows)]), dtype=torch.int32)
+    q = gen.randn(g, (int(cu[-1]), hq, d))
+    return q, kc, vc, table, torch.tensor(lens, dtype=torch.int32), cu
+
+
+def run_q4(case, group, scale, window=0, num_splits=0, decode=True, max_q=1, stream=None):
+    q, kc, vc, table, lens, cu = case
+    Tq, Hq, d = q.shape
+    NB, Hkv, bs, _ = kc.shape
+    B = lens.numel()
+    out = torch.full((Tq, Hq, d), float("nan"), device="cuda")
+    lse = torch.full((Tq, Hq), float("nan"), device="cuda")
+    n = pkv.paged_attention_q4_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, group, bs, table.shape[1], window, num_splits)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
+    pkv.paged_attention_q4(out, dev(q), dev(kc), dev(vc), dev(table), dev(lens), scale, group,
+                           cu_q=None if decode else dev(cu), max_q=max_q, window=window, lse=lse, num_splits=num_splits,
+                           workspace=ws)
+    torch.cuda.synchronize()
+    assert int(ws[:pkv_counter_bytes(n)].max()) == 0 if n else True
+    return out, lse
+
+
+def pkv_counter_bytes(n):
+    return min(n, 256 << 10)
+
+
+def expect(case, group, scale, window):
+    q, kc, vc, table, lens, cu = case
+    d = q.shape[2]
+    live = [b for b in range(lens.numel()) if int(lens[b]) > 0 and int(cu[b + 1]) > int(cu[b])]
+    rows = np.concatenate([np.arange(int(cu[b]), int(cu[b + 1])) for b in live])
+    n = np.concatenate([[0], np.cumsum([int(cu[b + 1] - cu[b]) for b in live])]).astype(np.int32)
+    kd, vd = (np.nan_to_num(orc.dequantize_q4(c, d, group)) for c in (kc, vc))   # unseen slots: anything finite
+    out, lse = oracle.paged_attention(q[rows], kd, vd, table[live], lens[live], n, scale, window)
+    return rows, out, lse
+
+
+SHAPES = [  # hq, hkv, d, group, bs
+    (8, 8, 128, 64, 16), (16, 4, 128, 128, 16), (64, 8, 128, 64, 16), (16, 2, 128, 32, 32), (8, 2, 64, 64, 16),
+    (6, 2, 64, 32, 32), (7, 1, 128, 128, 32),                       # up to eight query heads per KV head
+    (16, 1, 128, 64, 16), (64, 2, 128, 64, 16), (24, 2, 64, 32, 16), (64, 1, 128, 128, 32), (40, 1, 128, 32, 16),
+    (8, 2, 96, 32, 16), (4, 2, 256, 128, 16), (4, 4, 128, 64, 8), (10, 2, 32, 32, 24), (2, 1, 160, 32, 16),
+    (130, 1, 128, 64, 16),                                            # more heads than a tile
+]
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", SHAPES)
+@pytest.mark.parametrize("window", [0, 50])
+def test_q4_decode_matches_the_oracle(hq, hkv, d, group, bs, window):
+    lens = [1, 15, 16, 17, 100, 0, 257, 1000, 33]
+    case = q4_case(hq + d + bs + window, lens, hq, hkv, d, group, bs)
+    scale = 1 / math.sqrt(d)
+    live, ref, ref_lse = expect(case, group, scale, window)
+    for splits in (1, 3, 0):
+        out, lse = run_q4(case, group, scale, window, splits)
+        assert pkv.get_device_error() == 0
+        assert_attn_close(out[live], ref, f"splits {splits} out", ATOL)
+        assert_attn_close(lse[live], ref_lse, f"splits {splits} lse", ATOL)
+        assert torch.all(out[5] == 0) and torch.all(torch.isneginf(lse[5]))
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(64, 8, 128, 64, 16), (8, 8, 128, 128, 16), (16, 1, 64, 32, 32),
+                                               (4, 2, 96, 32, 16), (64, 1, 128, 64, 16)])
+@pytest.mark.parametrize("window", [0, 37])
+@pytest.mark.parametrize("max_q", [2, 4, 70])
+def test_q4_query_rows_match_the_oracle(hq, hkv, d, group, bs, window, max_q):
+    lens = [1, 16, 90, 17, 300, 0, 75, 1100]
+    rows = [min(n, r) for n, r in zip(lens, [1, max_q, max_q, 1, max_q, 0, 0, max_q - 1])]
+    case = q4_case(hq + d + max_q + window, lens, hq, hkv, d, group, bs, rows)
+    scale = 1 / math.sqrt(d)
+    live, ref, ref_lse = expect(case, group, scale, window)
+    for splits in (1, 3, 0):
+        out, lse = run_q4(case, group, scale, window, splits, decode=False, max_q=max_q)
+        assert pkv.get_device_error() == 0
+        assert_attn_close(out[live], ref, f"splits {splits} out", ATOL)
+        assert_attn_close(lse[live], ref_lse, f"splits {splits} lse", ATOL)
+
+
+def test_q4_rows_beyond_the_sequence_are_flagged():
+    case = list(q4_case(3, [5, 40], 8, 1, 128, 64, 16, [6, 2]))
+    out, lse = run_q4(case, 64, 0.1, decode=False, max_q=6)
+    assert pkv.get_device_error() & pkv.DEVERR["cu_seqlens"]
+    assert torch.all(out[:6] == 0) and torch.all(torch.isneginf(lse[:6]))
+    live, ref, _ = expect((case[0][6:], case[1], case[2], case[3][1:], case[4][1:], torch.tensor([0, 2])), 64, 0.1, 0)
+    assert_attn_close(out[6:], ref, "the good sequence", ATOL)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(16, 2, 128, 16), (64, 1, 128, 16), (4, 2, 96, 16)])
+def test_q4_bad_block_reads_zeros_and_bad_length_is_empty(hq, hkv, d, bs):
+    group = 32
+    case = list(q4_case(5, [200, 300, 64], hq, hkv, d, group, bs, poison=False))
+    q, kc, vc, table, lens, cu = case
+    bad = table.clone()
+    bad[1, 2], bad[1, 3] = kc.shape[0] + 9, -5
+    wrong = lens.clone()
+    wrong[2] = table.shape[1] * bs + 1
+    out, lse = run_q4((q, kc, vc, bad, wrong, cu), group, 0.1)
+    err = pkv.get_device_error()
+    assert err & pkv.DEVERR["block"] and err & pkv.DEVERR["len"]
+    assert torch.all(out[2] == 0) and torch.all(torch.isneginf(lse[2]))
+    # the bad blocks as blocks of zeros: codes and parameters 0
+    z = torch.zeros_like(kc[:1])
+    good = table.clone()
+    good[1, 2] = good[1, 3] = kc.shape[0]
+    live, ref, ref_lse = expect((q[:2], torch.cat([kc, z]), torch.cat([vc, z]), good[:2], lens[:2], cu[:3]), group, 0.1, 0)
+    assert_attn_close(out[:2], ref, "out", ATOL)
+    assert_attn_close(lse[:2], ref_lse, "lse", ATOL)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (64, 1)])
+def test_q4_long_context_many_splits(hq, hkv):
+    lens = [20011, 3, 9000]
+    case = q4_case(11, lens, hq, hkv, 128, 64, 16)
+    scale = 1 / math.sqrt(128)
+    live, ref, ref_lse = expect(case, 64, scale, 0)
+    for splits in (0, 7, 64):
+        out, lse = run_q4(case, 64, scale, 0, splits)
+        assert_attn_close(out[live], ref, f"splits {splits} out", ATOL)
+        assert_attn_close(lse[live], ref_lse, f"splits {splits} lse", ATOL)
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (32, 1)])
+def test_q4_large_and_masked_values(hq, hkv):
+    """Queries and caches far from 1: the scores' range, not their number format, decides."""
+    case = list(q4_case(13, [130, 64], hq, hkv, 128, 64, 16))
+    for f in (1e-20, 1e4, 0.0):
+        q = case[0] * f
+        scale = 0.0883 * (1e-4 if f == 1e4 else 1.0)
+        live, ref, ref_lse = expect((q, *case[1:]), 64, scale, 0)
+        out, lse = run_q4((q, *case[1:]), 64, scale)
+        assert_attn_close(out[live], ref, f"q * {f} out", ATOL)
+        assert_attn_close(lse[live], ref_lse, f"q * {f} lse", ATOL)
+
+
+def test_q4_workspace_too_small_is_refused():
+    case = q4_case(3, [4000], 8, 1, 128, 64, 16)
+    q, kc, vc, table, lens, _ = [dev(t) for t in case]
+    out = torch.zeros_like(q)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.paged_attention_q4(out, q, kc, vc, table, lens, 0.1, 64, num_splits=8)
+    assert e.value.status == 3
+    with pytest.raises(ValueError, match="row_bytes"):
+        pkv.paged_attention_q4(out, q, kc, vc, table, lens, 0.1, 32)
+
+
+# ----------------------------------------------------------------------- decode step
+
+def run_step(case, k_new, v_new, slots, group, scale, window, num_splits, fused):
+    q, kc, vc, table, lens, _ = case
+    B, Hq, d = q.shape
+    NB, Hkv, bs, _ = kc.shape
+    gk, gv = dev(kc), dev(vc)
+    out = torch.full((B, Hq, d), float("nan"), device="cuda")
+    lse = torch.full((B, Hq), float("nan"), device="cuda")
+    n = pkv.paged_attention_q4_workspace_bytes(B, B, 1, Hq, Hkv, d, group, bs, table.shape[1], window, num_splits)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
+    kw = dict(window=window, lse=lse, num_splits=num_splits, workspace=ws)
+    if fused:
+        pkv.decode_step_q4(out, dev(q), dev(k_new), dev(v_new), dev(slots), gk, gv, dev(table), dev(lens), scale, group, **kw)
+    else:
+        pkv.kv_append_q4(dev(k_new), dev(v_new), gk, gv, dev(slots), group)
+        pkv.paged_attention_q4(out, dev(q), gk, gv, dev(table), dev(lens), scale, group, **kw)
+    torch.cuda.synchronize()
+    return out, lse, gk.cpu(), gv.cpu()
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(64, 8, 128, 64, 16), (8, 8, 128, 128, 16), (16, 2, 128, 32, 32),
+                                               (8, 2, 64, 32, 16), (32, 2, 128, 64, 16), (64, 1, 128, 128, 16),
+                                               (4, 2, 96, 32, 8)])
+@pytest.mark.parametrize("new_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("num_splits,window", [(0, 0), (1, 0), (3, 40)])
+def test_q4_decode_step_equals_append_then_attention(hq, hkv, d, group, bs, new_dtype, num_splits, window):
+    lens = [1, 16, 17, 700, 2049, 33, 5, 1000]
+    case = q4_case(hq + bs + num_splits, lens, hq, hkv, d, group, bs)
+    g = gen.generator(77)
+    k_new, v_new = gen.randn(g, (8, hkv, d), new_dtype), gen.randn(g, (8, hkv, d), new_dtype)
+    slots = torch.tensor([oracle.slot_of(case[3][b], n - 1, bs) for b, n in enumerate(lens)])
+    slots[2] = -1                                     # sequence 2 has no new token this step
+    scale = 1 / math.sqrt(d)
+    out, lse, kc, vc = run_step(case, k_new, v_new, slots, group, scale, window, num_splits, True)
+    assert pkv.get_device_error() == 0
+    out2, lse2, kc2, vc2 = run_step(case, k_new, v_new, slots, group, scale, window, num_splits, False)
+    assert torch.equal(kc, kc2) and torch.equal(vc, vc2)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    want_k, want_v = case[1].clone(), case[2].clone()
+    orc.kv_append_q4(want_k, want_v, k_new, v_new, slots, group)
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    live, ref, ref_lse = expect((case[0], want_k, want_v, *case[3:]), group, scale, window)
+    assert_attn_close(out[live], ref, "out", ATOL)
+    assert_attn_close(lse[live], ref_lse, "lse", ATOL)
