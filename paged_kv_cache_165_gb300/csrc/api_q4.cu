@@ -110,6 +110,7 @@ pkv_status attend(const char *what, float *out, float *lse, const float *q, cons
     a.cu_q = cu_q;
     a.B = B;
     a.rows = Tq;
+    a.max_q = max_q;
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.d = d;
@@ -122,7 +123,12 @@ pkv_status attend(const char *what, float *out, float *lse, const float *q, cons
     a.workspace = workspace;
     a.err = err;
     cudaError_t e = cudaSuccess;
-    if (step.slots != nullptr) {
+    if (step.slots != nullptr && q4_fuses_append(plan)) {
+        a.k_new = step.k_new;
+        a.v_new = step.v_new;
+        a.new_dt = step.new_dt;
+        a.new_slots = step.slots;
+    } else if (step.slots != nullptr) {
         e = launch_kv_append_q4(step.k_new, step.v_new, step.new_dt, const_cast<uint8_t *>(k_cache),
                                 const_cast<uint8_t *>(v_cache), step.slots, B, Hkv, d, group, bs, NB, sm_count, err,
                                 stream);

@@ -9,6 +9,7 @@
 //   sum_t p_t v_t = sum_t (p_t scale_tg) code_t + sum_t p_t zero_tg      (element in group g)
 // so codes enter the products as the small integers they are, exactly.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "decode_kparams.cuh"
@@ -19,6 +20,27 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+
+struct AttendQ4Params {
+    DecodeKParams k;     // head_tiles: tiles of eight (query row, head) pairs per sequence and KV head
+    uint8_t *kc, *vc;
+    int rows, max_q;     // query rows of the call, and of a sequence at most
+    int new_bf16;        // type of the step's new rows
+};
+
+template <typename Kernel>
+cudaError_t set_smem_once(Kernel kernel, int bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    return cudaSuccess;
+}
 
 // ================================================================ CUDA-core path
 
@@ -128,6 +150,684 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+// ============================================================== warp-MMA path
+//
+// attend_q4_mma_kernel (d 64 or 128, bs 16 or 32): one CTA per (sequence, KV head, tile of eight
+// query rows x heads, chunk of blocks); four warps take 32 keys at a time, each with a private
+// ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16 f16
+// MMAs and fp32 accumulators:
+//   A code c in 0..15 placed in the low bits of an f16 is the subnormal c * 2^-24, and shifted
+//   left by four bits it is c * 2^-20: both exact, so two masks turn a word of eight codes into
+//   four f16 pairs (three logic operations and a shift per pair of pairs) with no conversion.
+//   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): q is scaled by a power of two per
+//     row and enters as f16 hi + lo (2^-22 relative); the head dimension is taken in the order in
+//     which the masks deliver the codes, each group in MMA steps of its own so that its scale
+//     multiplies the sum; the zeros' term, sum_g zero_g * sum(q in g), is one k8 MMA whose B
+//     operand is the (scale, zero) pairs as they lie in the page against A = (0, sum q).
+//   output O^T = V^T P^T: V^T is the A operand (16 dimensions x 16 keys), words of two keys paired
+//     by byte permutes; P^T is what the lane already holds for its row, times the group's scale,
+//     as f16 hi + lo.  The zeros' term is summed in fp32.
+// The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
+// the largest scale seen so far, E = ceil(log2 max scale): w = 2^(s - m - E + 14); l, O and the
+// zeros' term carry the same factor, which cancels, and a growing E rescales like a growing max.
+
+constexpr int kMmaWarps = 4, kStageKeys = 32, kStages = 2;
+
+template <int D, int BS, int G>
+struct MmaCfg {
+    static constexpr int WORDS = D / 8;              // code words per row
+    static constexpr int PPS = kStageKeys / BS;      // pages per stage
+    static constexpr int kCodeBytes = BS * D / 2;    // a page's codes; its parameters follow
+    static constexpr int kPageBytes = BS * (D / 2 + 4 * G);
+    static constexpr int kStageBytes = 2 * PPS * kPageBytes;   // K pages, then V pages
+    static constexpr int kRingBytes = kMmaWarps * kStages * kStageBytes;
+    static constexpr int kMergeBytes = kMmaWarps * 8 * (2 + D) * 4;
+    static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kSmemBytes = kDataBytes + kMmaWarps * kStages * 8;
+    static_assert(kPageBytes % 16 == 0, "bulk copies");
+};
+
+// D = A(16x16, f16, row) * B(16x8, f16, col) + D, fp32 accumulate.
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x0.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ float2 par_of(uint32_t u) {   // (scale, zero)
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+__device__ __forceinline__ float scale_of(uint32_t u) {
+    return __low2float(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// 2^e as a float, e clamped to the normal range.
+__device__ __forceinline__ float pow2i(int e) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
+}
+
+// A sequence's query rows r0 .. r0 + nq - 1 (checked), its length L and the pages [first, first +
+// pages) that any of them sees; rows [z0, z1) see nothing and are written as out = 0, lse = -inf.
+struct SeqRows {
+    int r0, nq, L, first, pages, z0, z1, z2, z3;
+    bool ok;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const AttendQ4Params &P, int b, int bs, bool report) {
+    const DecodeKParams &p = P.k;
+    SeqRows s{};
+    s.L = checked_len(p, b, bs, report);
+    s.ok = true;
+    if (p.cu_q == nullptr) {
+        s.r0 = b;
+        s.nq = 1;
+        if (s.L == 0) s.z0 = b, s.z1 = b + 1;
+    } else {
+        const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
+        s.r0 = c0;
+        s.nq = c1 - c0;
+        s.ok = c0 >= 0 && c1 >= c0 && c1 <= P.rows && s.nq <= s.L && s.nq <= P.max_q;
+        if (!s.ok) s.z0 = min(max(c0, 0), P.rows), s.z1 = min(max(c1, 0), P.rows);
+        // rows before the first sequence or behind the last one belong to none
+        if (b == 0 && c0 > 0) s.z2 = 0, s.z3 = min(c0, P.rows);
+        if (b == p.B - 1 && c1 < P.rows) s.z2 = max(c1, 0), s.z3 = P.rows;
+        if (report && (!s.ok || s.z3 > s.z2)) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
+    }
+    s.first = p.window > 0 ? max(0, s.L - s.nq + 1 - p.window) / bs : 0;
+    s.pages = s.L > 0 && s.ok ? (s.L + bs - 1) / bs - s.first : 0;
+    return s;
+}
+
+__device__ __forceinline__ void clear_rows(const AttendQ4Params &P, const SeqRows &s, int kvh, int d) {
+    const DecodeKParams &p = P.k;
+    for (int part = 0; part < 2; ++part) {
+        const int z0 = part ? s.z2 : s.z0, z1 = part ? s.z3 : s.z1;
+        for (int r = z0; r < z1; ++r) {
+            const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
+            for (int i = threadIdx.x; i < p.m * d; i += blockDim.x) p.out[at * d + i] = 0.f;
+            if (p.lse != nullptr)
+                for (int i = threadIdx.x; i < p.m; i += blockDim.x) p.lse[at + i] = -INFINITY;
+        }
+    }
+}
+
+// Row v of a tile's (query row, head) pairs: head kvh * m + v % m of the sequence's query row
+// v / m, which sees tokens [lo, len).  A row past the sequence's last repeats that one's span,
+// with bi = -1.
+struct RowSpan {
+    int bi;        // (query row) * Hq + head
+    int lo, len;
+};
+__device__ __forceinline__ RowSpan tile_row(const AttendQ4Params &P, const SeqRows &s, int kvh, int v) {
+    const DecodeKParams &p = P.k;
+    const int i = min(v / p.m, s.nq - 1);
+    RowSpan r;
+    r.len = s.L - s.nq + i + 1;
+    r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
+    r.bi = v < s.nq * p.m ? (s.r0 + i) * p.Hq + kvh * p.m + v % p.m : -1;
+    return r;
+}
+
+// The warps' states of a tile's eight rows, in shared memory ([NW][8] references and sums, then
+// [NW][8][D] outputs), merged and written: the result where the sequence has one chunk, else the
+// chunk's normalised partial; with arrival counters the unit's last chunk merges them all.
+template <int D, int NW>
+__device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params &P, const RowSpan *rows, int unit,
+                                            int split, int nc) {
+    const DecodeKParams &p = P.k;
+    float *mw = reinterpret_cast<float *>(smem);
+    float *lw = mw + NW * 8;
+    float *ow = lw + NW * 8;
+    for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
+        const int h = idx / (D / 4), c = idx % (D / 4) * 4;
+        if (rows[h].bi < 0) continue;
+        const size_t bi = rows[h].bi;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * 8 + h]);
+        const float base = M == -INFINITY ? 0.f : M;   // the row sees none of this chunk's keys
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2f(mw[w * 8 + h] - base);
+            const float4 o = *reinterpret_cast<const float4 *>(ow + (w * 8 + h) * D + c);
+            L += lw[w * 8 + h] * f;
+            acc.x += o.x * f;
+            acc.y += o.y * f;
+            acc.z += o.z * f;
+            acc.w += o.w * f;
+        }
+        const float inv = M == -INFINITY ? 0.f : 1.f / L;
+        const float4 r = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const float lse2 = M == -INFINITY ? -INFINITY : M + log2f(L);
+        if (nc == 1) {
+            *reinterpret_cast<float4 *>(p.out + bi * D + c) = r;
+            if (c == 0 && p.lse != nullptr) p.lse[bi] = lse2 * kDecLn2;
+        } else {
+            *reinterpret_cast<float4 *>(p.ws_o + (bi * p.splits + split) * D + c) = r;
+            if (c == 0) p.ws_lse[bi * p.splits + split] = lse2;
+        }
+    }
+    if (nc == 1 || p.counters == nullptr) return;
+    __shared__ int s_last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned prev = atomicAdd(p.counters + unit, 1u);
+        s_last = prev + 1 == static_cast<unsigned>(nc);
+        if (s_last) p.counters[unit] = 0u;   // every chunk of this call has arrived
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
+        const int h = idx / (D / 4), c = idx % (D / 4) * 4;
+        if (rows[h].bi < 0) continue;
+        const size_t bi = rows[h].bi;
+        const float *ls = p.ws_lse + bi * p.splits, *po = p.ws_o + bi * p.splits * D + c;
+        float M = -INFINITY;
+        for (int i = 0; i < nc; ++i) M = fmaxf(M, __ldcg(ls + i));
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < nc; ++i) {
+            const float w = exp2f(__ldcg(ls + i) - M);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * D));
+            L += w;
+            acc.x += w * o.x;
+            acc.y += w * o.y;
+            acc.z += w * o.z;
+            acc.w += w * o.w;
+        }
+        const float inv = 1.f / L;
+        *reinterpret_cast<float4 *>(p.out + bi * D + c) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (c == 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kDecLn2;
+    }
+}
+
+// Words per thread and group of `N` consecutive 32-bit words from shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        w[0] = u.x, w[1] = u.y;
+    } else if constexpr (N == 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p), v = *reinterpret_cast<const uint4 *>(p + 16);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// A step's new token (K: side 0, V: side 1) quantised into its row by one warp.
+template <int D, int G>
+__device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, int kvh, long long row_page, int off, int bs,
+                                              int side, int lane) {
+    constexpr int WORDS = D / 8, LANES = WORDS / G;
+    const size_t src = (static_cast<size_t>(b) * p.k.Hkv + kvh) * D + lane * 8;
+    float x[8] = {};
+    if (lane < WORDS) {
+        if (p.new_bf16) q4_load8<__nv_bfloat16, false>(static_cast<const __nv_bfloat16 *>(side ? p.k.v_new : p.k.k_new) + src, x);
+        else q4_load8<float, false>(static_cast<const float *>(side ? p.k.v_new : p.k.k_new) + src, x);
+    }
+    __half2 par;
+    const uint32_t code = q4_quantise8(x, LANES, par);
+    if (lane >= WORDS) return;
+    uint8_t *page = (side ? p.vc : p.kc) + row_page;
+    reinterpret_cast<uint32_t *>(page)[off * WORDS + lane] = code;
+    if (lane % LANES == 0) reinterpret_cast<__half2 *>(page + bs * WORDS * 4)[off * G + lane / LANES] = par;
+}
+
+template <int D, int BS, int G>
+__global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const __grid_constant__ AttendQ4Params P) {
+    using Cfg = MmaCfg<D, BS, G>;
+    constexpr int NW = kMmaWarps, NT = kStageKeys / 8, PPS = Cfg::PPS, WORDS = Cfg::WORDS;
+    constexpr int WPT = WORDS / (4 * G);         // K: words per lane and group
+    constexpr int KSTEPS = D / 16;
+    constexpr int HALVES = D / 32;               // V: half words (four codes) per lane and key
+    constexpr int HPG = HALVES / G;              // ... per group
+    static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
+    const DecodeKParams &p = P.k;
+
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kDataBytes);
+    __shared__ RowSpan s_rows[8];
+
+    pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int tile = blockIdx.x % p.head_tiles, split = blockIdx.x / p.head_tiles;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const bool report = threadIdx.x == 0 && split == 0 && kvh == 0 && tile == 0;
+
+    // ---- the sequence's rows and this tile's
+    const SeqRows sq = seq_rows(P, b, BS, report);
+    if (split == 0 && tile == 0) clear_rows(P, sq, kvh, D);
+    if (!sq.ok || 8 * tile >= sq.nq * p.m) return;
+    if (threadIdx.x < 8) s_rows[threadIdx.x] = tile_row(P, sq, kvh, 8 * tile + threadIdx.x);
+    // pages that any row of the sequence sees; this chunk's, and those that this tile sees
+    const int c0 = sq.first + split * p.chunk_pages, c1 = min(sq.first + sq.pages, c0 + p.chunk_pages);
+    if (c0 >= c1) {
+        // a new token for a sequence that holds none has no position: flagged, not written
+        if (split == 0 && p.new_slots != nullptr && threadIdx.x == 0 && sq.L == 0 && __ldg(p.new_slots + b) >= 0)
+            raise_error(p.err, PKV_DEVERR_SLOT);
+        return;
+    }
+    const RowSpan t_first = tile_row(P, sq, kvh, 8 * tile), t_last = tile_row(P, sq, kvh, min(8 * tile + 7, sq.nq * p.m - 1));
+    const int pg0 = max(c0, t_first.lo / BS), pg1 = min(c1, (t_last.len + BS - 1) / BS);
+    const int tok_end = pg1 * BS;   // the chunk's keys end here
+
+    if (p.new_slots != nullptr && c1 == sq.first + sq.pages) {
+        // the step's new token: the CTA that reads the sequence's last page writes its K and V
+        // rows there before any copy of the page
+        if (warp < 2) {
+            const long long slot = __ldg(p.new_slots + b);
+            if (slot >= 0) {
+                const int pos = sq.L - 1, phys = __ldg(p.block_table + static_cast<size_t>(b) * p.MBS + pos / BS);
+                if (phys < 0 || phys >= p.NB || slot != static_cast<long long>(phys) * BS + pos % BS) {
+                    if (warp == 0 && lane == 0) raise_error(p.err, PKV_DEVERR_SLOT);
+                } else {
+                    write_new_row<D, G>(P, b, kvh, (static_cast<long long>(phys) * p.Hkv + kvh) * Cfg::kPageBytes, pos % BS,
+                                        BS, warp, lane);
+                }
+            }
+            fence_proxy_async_global();
+        }
+        __syncthreads();
+        fence_proxy_async_global();
+    }
+
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(smem_addr(&bars[warp * kStages + s]), 1);
+        fence_barrier_init();
+    }
+    __syncthreads();   // s_rows; the barriers are the warp's own
+
+    // ---- this warp's stages: units of PPS pages warp, warp + NW, ... of [pg0, pg1)
+    const int units = pg1 > pg0 ? (pg1 - pg0 + PPS - 1) / PPS : 0;
+    const int n_my = units > warp ? (units - warp + NW - 1) / NW : 0;
+    const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
+    int tcur[PPS], tnext[PPS];
+    auto load_ids = [&](int k, int (&t)[PPS]) {
+#pragma unroll
+        for (int i = 0; i < PPS; ++i) {
+            const int pg = pg0 + (warp + k * NW) * PPS + i;
+            t[i] = k < n_my && pg < pg1 ? __ldg(tbl + pg) : -1;
+        }
+    };
+    load_ids(lane, tcur);
+    load_ids(32 + lane, tnext);
+    int tbase = 0;
+    unsigned bad = 0;   // bit (stage * PPS + page): a page to be read as zeros
+    auto issue = [&](int k) {   // the whole warp; lane 0 starts the copies
+        while (k >= tbase + 32) {
+            tbase += 32;
+#pragma unroll
+            for (int i = 0; i < PPS; ++i) tcur[i] = tnext[i];
+            load_ids(tbase + 32 + lane, tnext);
+        }
+        const int st = k % kStages;
+        uint8_t *stage = smem + (warp * kStages + st) * Cfg::kStageBytes;
+        const uint32_t bar = smem_addr(&bars[warp * kStages + st]);
+        int phys[PPS];
+        unsigned bytes = 0;
+#pragma unroll
+        for (int i = 0; i < PPS; ++i) {
+            phys[i] = __shfl_sync(kFull, tcur[i], k & 31);
+            const bool there = pg0 + (warp + k * NW) * PPS + i < pg1, ok = phys[i] >= 0 && phys[i] < p.NB;
+            const unsigned bit = 1u << (st * PPS + i);
+            bad = there && !ok ? bad | bit : bad & ~bit;
+            if (there && !ok && lane == 0) raise_error(p.err, PKV_DEVERR_BLOCK);
+            if (!there || !ok) phys[i] = -1;
+            bytes += phys[i] >= 0 ? 2 * Cfg::kPageBytes : 0;
+        }
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int i = 0; i < PPS; ++i) {
+                if (phys[i] < 0) continue;
+                const size_t at = (static_cast<size_t>(phys[i]) * p.Hkv + kvh) * Cfg::kPageBytes;
+                bulk_load(smem_addr(stage + i * Cfg::kPageBytes), P.kc + at, Cfg::kPageBytes, bar);
+                bulk_load(smem_addr(stage + (PPS + i) * Cfg::kPageBytes), P.vc + at, Cfg::kPageBytes, bar);
+            }
+        }
+    };
+    int issued = min(kStages, n_my);
+    for (int k = 0; k < issued; ++k) issue(k);
+
+    // ---- query fragments.  MMA step 2u (codes' even nibbles) and 2u + 1 (odd nibbles, 16 times
+    // the value) of word u = gi * WPT + i: elements 8 * word + {0, 4}, {2, 6} and {1, 5}, {3, 7}
+    const RowSpan me = s_rows[g];
+    uint32_t qa[KSTEPS][4], za[2] = {0, 0};
+    float f;   // score (base 2) = MMA sum * f
+    {
+        const float *qrow = p.q + static_cast<size_t>(me.bi >= 0 ? me.bi : 0) * D;
+        float x[G * WPT][8], amax = 0.f, zsum = 0.f;
+#pragma unroll
+        for (int u = 0; u < G * WPT; ++u) {
+            const int word = (u / WPT) * (WORDS / G) + t4 * WPT + u % WPT;
+            const float2 *src = reinterpret_cast<const float2 *>(qrow + 8 * word);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
+                x[u][2 * e] = v.x;
+                x[u][2 * e + 1] = v.y;
+                amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        // |q| * 2^sq in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
+        const int sq = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
+        const float up = pow2i(sq);
+        f = (p.scale_log2 * 0x1p24f) * pow2i(-sq);
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPT; ++i) {
+                const int u = gi * WPT + i;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[u][e] *= up;
+                    sum += x[u][e];
+                }
+                split2(x[u][0], x[u][4], qa[2 * u][0], qa[2 * u][1]);
+                split2(x[u][2], x[u][6], qa[2 * u][2], qa[2 * u][3]);
+                split2(x[u][1] * 0.0625f, x[u][5] * 0.0625f, qa[2 * u + 1][0], qa[2 * u + 1][1]);
+                split2(x[u][3] * 0.0625f, x[u][7] * 0.0625f, qa[2 * u + 1][2], qa[2 * u + 1][3]);
+            }
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            if (gi == t4) zsum = sum;
+        }
+        // (0, sum of q over group t4) * 2^-8, which keeps 128 elements below 2^14; zero beyond G
+        split2(0.f, zsum * 0x1p-8f, za[0], za[1]);
+    }
+
+    float oT[D / 16][4];
+    float zo[G];   // sum of weight * zero over this lane's keys
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) oT[mt][0] = oT[mt][1] = oT[mt][2] = oT[mt][3] = 0.f;
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) zo[gi] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
+    float ref = -INFINITY;                  // m_run + E - 14
+    float vs_max = 0x1p-24f;                // the largest V scale seen (fp16's smallest to begin with)
+
+    int k = 0;
+    for (; k < n_my; ++k) {
+        const int st = k % kStages;
+        const bool arrived = mbar_wait_bounded(smem_addr(&bars[warp * kStages + st]), (k / kStages) & 1);
+        if (!__all_sync(kFull, arrived)) {
+            if (lane == 0) raise_error(p.err, PKV_DEVERR_TIMEOUT);
+            break;
+        }
+        uint8_t *kpages = smem + (warp * kStages + st) * Cfg::kStageBytes;
+        uint8_t *vpages = kpages + PPS * Cfg::kPageBytes;
+        const int tok0 = (pg0 + (warp + k * NW) * PPS) * BS;
+        if (const unsigned zero = (bad >> (st * PPS)) & ((1u << PPS) - 1); zero != 0) {
+#pragma unroll
+            for (int i = 0; i < 2 * PPS; ++i)
+                if (zero >> (i % PPS) & 1)
+                    for (int c = lane * 16; c < Cfg::kPageBytes; c += 512)
+                        *reinterpret_cast<uint4 *>(kpages + i * Cfg::kPageBytes + c) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();   // before a later copy into this stage
+            __syncwarp();
+        }
+        // does every row of the tile see every key of the stage?
+        const bool whole = tok0 >= t_last.lo && tok0 + kStageKeys <= min(t_first.len, tok_end);
+        if (!whole) {
+            // parameters of V rows that no row of the tile sees may be anything: zero them, so that
+            // weight 0 contributes 0 (codes are finite whatever they are)
+            const int tok = tok0 + lane, off = lane % BS;
+            if (tok < t_first.lo || tok >= min(t_last.len, tok_end)) {
+#pragma unroll
+                for (int gi = 0; gi < G; ++gi)
+                    reinterpret_cast<uint32_t *>(vpages + (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes)[off * G + gi] = 0;
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+        }
+
+        // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
+        float s[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint8_t *page = kpages + (nt * 8 / BS) * Cfg::kPageBytes;
+            const uint32_t *par = reinterpret_cast<const uint32_t *>(page + Cfg::kCodeBytes);
+            const int r0 = nt * 8 % BS;
+            const uint8_t *krow = page + (r0 + g) * (D / 2) + t4 * WPT * 4;
+            float zacc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma8(zacc, za[0], za[1], t4 < G ? par[(r0 + g) * G + t4] : 0u);
+            uint32_t sc[2 * G];
+            lds_words<2 * G>(reinterpret_cast<const uint8_t *>(par + (r0 + 2 * t4) * G), sc);
+            float x0 = (zacc[0] + zacc[2]) * 0x1p-16f, x1 = (zacc[1] + zacc[3]) * 0x1p-16f;
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) {
+                uint32_t w[WPT];
+                lds_words<WPT>(krow + gi * (D / 2 / G), w);
+                float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < WPT; ++i) {
+                    const uint32_t(&qe)[4] = qa[2 * (gi * WPT + i)];
+                    const uint32_t(&qo)[4] = qa[2 * (gi * WPT + i) + 1];
+                    const uint32_t y = w[i] >> 8;
+                    mma16(a0, qe[0], qe[1], qe[2], qe[3], w[i] & 0x000f000fu, y & 0x000f000fu);
+                    mma16(G == 1 ? a1 : a0, qo[0], qo[1], qo[2], qo[3], w[i] & 0x00f000f0u, y & 0x00f000f0u);
+                }
+                x0 = fmaf(scale_of(sc[gi]), (a0[0] + a0[2]) + (a1[0] + a1[2]), x0);
+                x1 = fmaf(scale_of(sc[G + gi]), (a0[1] + a0[3]) + (a1[1] + a1[3]), x1);
+            }
+            s[nt][0] = x0 * f;
+            s[nt][1] = x1 * f;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = tok0 + nt * 8 + 2 * t4 + e;
+                    if (tok < me.lo || tok >= min(me.len, tok_end)) s[nt][e] = -INFINITY;
+                }
+        }
+
+        // ---- V scales of this lane's keys and the running reference
+        uint32_t vp[NT][2 * G];
+        __half2 top = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+        float mx = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint8_t *page = vpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes;
+            lds_words<2 * G>(page + ((nt * 8 % BS) + 2 * t4) * G * 4, vp[nt]);
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&vp[nt][i]));
+            mx = fmaxf(mx, fmaxf(s[nt][0], s[nt][1]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        m_run = fmaxf(m_run, mx);
+        const float vs_new = __low2float(top);
+        if (__any_sync(kFull, vs_new > vs_max)) {   // rarely after the first stage
+            float v = fmaxf(vs_new, vs_max);
+            v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+            // the next power of two, so that E moves seldom
+            vs_max = pow2i(static_cast<int>((__float_as_uint(v) + 0x7fffffu) >> 23) - 127);
+        }
+        const float ref_new = m_run + (static_cast<float>(static_cast<int>(__float_as_uint(vs_max) >> 23) - 127) - 14.f);
+        // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
+        const float base = ref_new == -INFINITY ? 0.f : ref_new;
+        const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
+        ref = ref_new;
+        float psum = 0.f;
+        float w[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[nt][e] = ex2_approx(s[nt][e] - base);
+                psum += w[nt][e];
+            }
+        }
+        l_run = l_run * alpha + psum;
+        if (__any_sync(kFull, alpha != 1.f)) {
+            const float alpha_a = __shfl_sync(kFull, alpha, 8 * t4);
+            const float alpha_b = __shfl_sync(kFull, alpha, 8 * t4 + 4);
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                oT[mt][0] *= alpha_a;
+                oT[mt][1] *= alpha_b;
+                oT[mt][2] *= alpha_a;
+                oT[mt][3] *= alpha_b;
+            }
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) zo[gi] *= alpha;
+        }
+
+        // ---- O^T += V^T P^T, 16 keys per step
+#pragma unroll
+        for (int kt = 0; kt < kStageKeys / 16; ++kt) {
+            const uint8_t *page = vpages + (kt * 16 / BS) * Cfg::kPageBytes;
+            const int r0 = kt * 16 % BS + 2 * t4;
+            // lane g's half words of keys r0, r0 + 1, r0 + 8, r0 + 9: group gi's are words
+            // gi * WORDS / G + ...; with four words to a group two lanes share a word
+            constexpr int WPL = HPG == 1 ? 1 : HPG / 2;   // words per lane and group
+            const int wsel = HPG == 1 ? g >> 1 : g * WPL;
+            const uint32_t sel_lo = HPG == 1 && (g & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) {
+                uint32_t bh0, bl0, bh1, bl1;
+                {
+                    const float2 p0 = par_of(vp[2 * kt][gi]), p1 = par_of(vp[2 * kt][G + gi]);
+                    const float2 p2 = par_of(vp[2 * kt + 1][gi]), p3 = par_of(vp[2 * kt + 1][G + gi]);
+                    const float w0 = w[2 * kt][0], w1 = w[2 * kt][1], w2 = w[2 * kt + 1][0], w3 = w[2 * kt + 1][1];
+                    split2(w0 * p0.x, w1 * p1.x, bh0, bl0);
+                    split2(w2 * p2.x, w3 * p3.x, bh1, bl1);
+                    zo[gi] = fmaf(w0, p0.y, fmaf(w1, p1.y, fmaf(w2, p2.y, fmaf(w3, p3.y, zo[gi]))));
+                }
+                const uint8_t *src = page + r0 * (D / 2) + (gi * (WORDS / G) + wsel) * 4;
+                uint32_t v0[WPL], v1[WPL], v2[WPL], v3[WPL];
+                lds_words<WPL>(src, v0);
+                lds_words<WPL>(src + D / 2, v1);
+                lds_words<WPL>(src + 8 * (D / 2), v2);
+                lds_words<WPL>(src + 9 * (D / 2), v3);
+#pragma unroll
+                for (int h = 0; h < HPG; ++h) {
+                    const uint32_t sel = (h & 1) ? 0x7632u : sel_lo;
+                    const uint32_t x = __byte_perm(v0[h / 2], v1[h / 2], sel), y = __byte_perm(v2[h / 2], v3[h / 2], sel);
+                    const uint32_t x8 = x >> 8, y8 = y >> 8;
+                    const int mt = 2 * (gi * HPG + h);
+                    const uint32_t e0 = x & 0x000f000fu, e1 = x8 & 0x000f000fu, e2 = y & 0x000f000fu, e3 = y8 & 0x000f000fu;
+                    const uint32_t d0 = x & 0x00f000f0u, d1 = x8 & 0x00f000f0u, d2 = y & 0x00f000f0u, d3 = y8 & 0x00f000f0u;
+                    mma16(oT[mt], e0, e1, e2, e3, bh0, bh1);
+                    mma16(oT[mt + 1], d0, d1, d2, d3, bh0, bh1);
+                    mma16(oT[mt], e0, e1, e2, e3, bl0, bl1);
+                    mma16(oT[mt + 1], d0, d1, d2, d3, bl0, bl1);
+                }
+            }
+        }
+        __syncwarp();
+        if (k + kStages < n_my) {
+            issue(k + kStages);
+            issued = k + kStages + 1;
+        }
+    }
+    if (k < n_my) {
+        // A copy did not arrive in time: wait (bounded) for the copies still in flight so that
+        // none lands after the block exits.
+        for (int kk = k; kk < issued; ++kk)
+            mbar_wait_bounded(smem_addr(&bars[warp * kStages + kk % kStages]), (kk / kStages) & 1);
+    }
+
+    l_run += __shfl_xor_sync(kFull, l_run, 1);
+    l_run += __shfl_xor_sync(kFull, l_run, 2);
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) {
+        zo[gi] += __shfl_xor_sync(kFull, zo[gi], 1);
+        zo[gi] += __shfl_xor_sync(kFull, zo[gi], 2);
+    }
+
+    // ---- the warps' (ref, l, O) through shared memory (the ring is free now)
+    __syncthreads();
+    float *mw = reinterpret_cast<float *>(smem);
+    float *lw = mw + NW * 8;
+    float *ow = lw + NW * 8;
+    if (t4 == 0) {
+        mw[warp * 8 + g] = ref;
+        lw[warp * 8 + g] = l_run;
+    }
+    constexpr int WPL = HPG == 1 ? 1 : HPG / 2;
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) {
+        const float za_ = __shfl_sync(kFull, zo[gi], 8 * t4), zb_ = __shfl_sync(kFull, zo[gi], 8 * t4 + 4);
+#pragma unroll
+        for (int h = 0; h < HPG; ++h) {
+            const int word = gi * (WORDS / G) + (HPG == 1 ? g >> 1 : g * WPL + h / 2);
+            const int dim = 8 * word + 4 * (HPG == 1 ? g & 1 : h & 1), mt = 2 * (gi * HPG + h);
+            // even codes were c * 2^-24, odd ones c * 2^-20
+            float *oa = ow + (warp * 8 + 2 * t4) * D + dim, *ob = oa + D;
+            oa[0] = fmaf(oT[mt][0], 0x1p24f, za_);
+            oa[1] = fmaf(oT[mt + 1][0], 0x1p20f, za_);
+            oa[2] = fmaf(oT[mt][2], 0x1p24f, za_);
+            oa[3] = fmaf(oT[mt + 1][2], 0x1p20f, za_);
+            ob[0] = fmaf(oT[mt][1], 0x1p24f, zb_);
+            ob[1] = fmaf(oT[mt + 1][1], 0x1p20f, zb_);
+            ob[2] = fmaf(oT[mt][3], 0x1p24f, zb_);
+            ob[3] = fmaf(oT[mt + 1][3], 0x1p20f, zb_);
+        }
+    }
+    __syncthreads();
+    finish_rows<D, NW>(smem, P, s_rows, (b * p.Hkv + kvh) * p.head_tiles + tile, split,
+                       (sq.pages + p.chunk_pages - 1) / p.chunk_pages);
+}
+
+template <int D, int BS, int G>
+cudaError_t launch_mma_as(const AttendQ4Params &P, dim3 grid, cudaStream_t stream) {
+    using Cfg = MmaCfg<D, BS, G>;
+    static std::atomic<unsigned long long> done{0};
+    auto kernel = attend_q4_mma_kernel<D, BS, G>;
+    const cudaError_t e = set_smem_once(kernel, Cfg::kSmemBytes, done);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kMmaWarps * 32, Cfg::kSmemBytes, stream>>>(P);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mma(const AttendQ4Params &P, int d, int bs, int G, dim3 grid, cudaStream_t stream) {
+    if (bs == 16) {
+        if (d == 64) return G == 1 ? launch_mma_as<64, 16, 1>(P, grid, stream) : launch_mma_as<64, 16, 2>(P, grid, stream);
+        return G == 1   ? launch_mma_as<128, 16, 1>(P, grid, stream)
+               : G == 2 ? launch_mma_as<128, 16, 2>(P, grid, stream)
+                        : launch_mma_as<128, 16, 4>(P, grid, stream);
+    }
+    if (d == 64) return G == 1 ? launch_mma_as<64, 32, 1>(P, grid, stream) : launch_mma_as<64, 32, 2>(P, grid, stream);
+    return G == 1   ? launch_mma_as<128, 32, 1>(P, grid, stream)
+           : G == 2 ? launch_mma_as<128, 32, 2>(P, grid, stream)
+                    : launch_mma_as<128, 32, 4>(P, grid, stream);
+}
+
 cudaError_t launch_simt(const AttendQ4Args &a, const DecodeKParams &kp, cudaStream_t stream) {
     const long long units = static_cast<long long>(a.rows) * a.Hq;
     const dim3 grid(static_cast<unsigned>((units + 3) / 4), static_cast<unsigned>(kp.splits));
@@ -141,6 +841,9 @@ cudaError_t launch_simt(const AttendQ4Args &a, const DecodeKParams &kp, cudaStre
     return cudaGetLastError();
 }
 
+// Units with at most this many chunks merge in the attention kernel.
+constexpr int kFusedMergeMaxChunks = 8;
+
 size_t partial_bytes(long long rows, int Hq, int splits, int d) {
     return splits > 1 ? PKV_DECODE_COUNTER_BYTES +
                             static_cast<size_t>(rows) * Hq * splits * (static_cast<size_t>(d) + 1) * sizeof(float)
@@ -151,24 +854,37 @@ size_t partial_bytes(long long rows, int Hq, int splits, int d) {
 
 Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int group, int bs, int pages,
                       int num_splits, int sm_count, bool aligned) {
-    (void)B, (void)max_q, (void)Hkv, (void)group, (void)aligned;
     Q4Plan plan{};
+    const int m = Hq / Hkv, sms = std::max(sm_count, 1);
+    const long long tiles = (static_cast<long long>(max_q) * m + 7) / 8;
+    plan.mma = (d == 64 || d == 128) && (bs == 16 || bs == 32) && d / group <= 4 && aligned && tiles < (1 << 18);
+    plan.tiles = plan.mma ? static_cast<int>(tiles) : 1;
+    const long long units = plan.mma ? static_cast<long long>(B) * Hkv * tiles : static_cast<long long>(rows) * Hq;
     int chunk = pages;
     if (num_splits > 1) {
         chunk = (pages + num_splits - 1) / num_splits;
+    } else if (num_splits == 0 && plan.mma) {
+        // about two waves of the CTAs an SM holds, chunks of at least 256 keys; and none of more
+        // than 8192, so that a long sequence among short ones spreads
+        const int least = 256 / bs, most = 8192 / bs;
+        while (chunk > least && units * ((pages + chunk - 1) / chunk) < 8ll * sms) chunk = (chunk + 1) / 2;
+        if (chunk > most) chunk = (pages + (pages + most - 1) / most - 1) / ((pages + most - 1) / most);
     } else if (num_splits == 0) {
         // one warp per (row, head, chunk): several warps for each scheduler, no chunk shorter
         // than 128 keys
-        const long long units = static_cast<long long>(rows) * Hq, target = 32ll * std::max(sm_count, 1);
         const int least = std::max(1, 128 / bs);
-        while (chunk > least && units * ((pages + chunk - 1) / chunk) < target) chunk = (chunk + 1) / 2;
+        while (chunk > least && units * ((pages + chunk - 1) / chunk) < 32ll * sms) chunk = (chunk + 1) / 2;
     }
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
     plan.chunk_pages = std::max(chunk, 1);
     plan.splits = (pages + plan.chunk_pages - 1) / plan.chunk_pages;
+    plan.fused_merge = plan.mma && plan.splits > 1 && plan.splits <= kFusedMergeMaxChunks &&
+                       units <= static_cast<long long>(PKV_DECODE_COUNTER_BYTES / sizeof(unsigned));
     plan.workspace_bytes = partial_bytes(rows, Hq, plan.splits, d);
     return plan;
 }
+
+bool q4_fuses_append(const Q4Plan &plan) { return plan.mma && plan.tiles == 1; }
 
 cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStream_t stream) {
     DecodeKParams kp{};
@@ -194,8 +910,28 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         kp.ws_o = reinterpret_cast<float *>(ws + PKV_DECODE_COUNTER_BYTES);
         kp.ws_lse = kp.ws_o + static_cast<size_t>(a.rows) * a.Hq * plan.splits * a.d;
     }
-    const cudaError_t e = launch_simt(a, kp, stream);
-    if (e != cudaSuccess || plan.splits == 1) return e;
+    cudaError_t e;
+    if (plan.mma) {
+        AttendQ4Params P{};
+        kp.head_tiles = plan.tiles;
+        if (plan.fused_merge) kp.counters = static_cast<unsigned *>(a.workspace);
+        if (a.new_slots != nullptr) {
+            kp.k_new = a.k_new;
+            kp.v_new = a.v_new;
+            kp.new_slots = a.new_slots;
+            P.new_bf16 = a.new_dt == PKV_BF16;
+        }
+        P.k = kp;
+        P.kc = const_cast<uint8_t *>(a.k_cache);   // written only for a step's new tokens
+        P.vc = const_cast<uint8_t *>(a.v_cache);
+        P.rows = a.rows;
+        P.max_q = a.max_q;
+        const dim3 grid(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
+        e = launch_mma(P, a.d, a.bs, a.d / a.group, grid, stream);
+    } else {
+        e = launch_simt(a, kp, stream);
+    }
+    if (e != cudaSuccess || plan.splits == 1 || plan.fused_merge) return e;
     return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(a.rows * a.Hq), stream);
 }
 

@@ -134,6 +134,9 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 // ------------------------------------------------- attention over a 4-bit cache
 
 struct Q4Plan {
+    bool mma;            // d 64 or 128, bs 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
+    int tiles;           // its tiles of eight (query row, head) pairs per sequence and KV head
+    bool fused_merge;    // the last chunk of a unit merges (counters in the workspace)
     int splits;          // chunks per sequence at most (1: one pass, no workspace)
     int chunk_pages;     // blocks per chunk
     size_t workspace_bytes;
@@ -152,12 +155,20 @@ struct AttendQ4Args {
     const int32_t *block_table;
     const int32_t *context_lens;
     const int32_t *cu_q;   // query rows per sequence; nullptr: one per sequence
-    int B, rows, Hq, Hkv, d, group, bs, MBS, NB;
+    int B, rows, max_q, Hq, Hkv, d, group, bs, MBS, NB;
     float scale;
     int window;
     void *workspace;
     unsigned *err;
+    // a step's new tokens, written inside the attention launch (q4_fuses_append)
+    const void *k_new, *v_new;
+    pkv_dtype new_dt;
+    const int64_t *new_slots;
 };
+
+// Whether the attention launch writes a step's new tokens itself: exactly one thread block reads
+// the page that holds a sequence's last position for each KV head.
+bool q4_fuses_append(const Q4Plan &plan);
 
 cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStream_t stream);
 
