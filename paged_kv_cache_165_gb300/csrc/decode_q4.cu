@@ -190,14 +190,14 @@ struct MmaCfg {
 // D = A(16x16, f16, row) * B(16x8, f16, col) + D, fp32 accumulate.
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(b0));
@@ -210,6 +210,30 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
     const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    const float2 f = __half22float2(h);
+    const float2 r = add2(x, make_float2(-f.x, -f.y));
+    const __half2 l = __floats2half2_rn(r.x, r.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ void ldsm_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
 __device__ __forceinline__ float2 par_of(uint32_t u) {   // (scale, zero)
@@ -406,8 +430,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
     constexpr int NW = kMmaWarps, NT = kStageKeys / 8, PPS = Cfg::PPS, WORDS = Cfg::WORDS;
     constexpr int WPT = WORDS / (4 * G);         // K: words per lane and group
     constexpr int KSTEPS = D / 16;
-    constexpr int HALVES = D / 32;               // V: half words (four codes) per lane and key
-    constexpr int HPG = HALVES / G;              // ... per group
+    constexpr int HPG = D / 32 / G;              // V: 32-dimension columns per group
     static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
     const DecodeKParams &p = P.k;
 
@@ -568,11 +591,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
     }
 
     float oT[D / 16][4];
-    float zo[G];   // sum of weight * zero over this lane's keys
+    float2 zo[G];   // sums of weight * zero over this lane's keys
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) oT[mt][0] = oT[mt][1] = oT[mt][2] = oT[mt][3] = 0.f;
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) zo[gi] = 0.f;
+    for (int gi = 0; gi < G; ++gi) zo[gi] = make_float2(0.f, 0.f);
     float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
     float ref = -INFINITY;                  // m_run + E - 14
     float vs_max = 0x1p-24f;                // the largest V scale seen (fp16's smallest to begin with)
@@ -613,7 +636,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         }
 
         // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
-        float s[NT][2];
+        float2 s[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint8_t *page = kpages + (nt * 8 / BS) * Cfg::kPageBytes;
@@ -624,34 +647,33 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
             mma8(zacc, za[0], za[1], t4 < G ? par[(r0 + g) * G + t4] : 0u);
             uint32_t sc[2 * G];
             lds_words<2 * G>(reinterpret_cast<const uint8_t *>(par + (r0 + 2 * t4) * G), sc);
-            float x0 = (zacc[0] + zacc[2]) * 0x1p-16f, x1 = (zacc[1] + zacc[3]) * 0x1p-16f;
+            float2 x = mul2(add2(make_float2(zacc[0], zacc[1]), make_float2(zacc[2], zacc[3])), make_float2(0x1p-16f, 0x1p-16f));
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
                 uint32_t w[WPT];
                 lds_words<WPT>(krow + gi * (D / 2 / G), w);
-                float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+                float a[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};   // two chains where a group is long
 #pragma unroll
                 for (int i = 0; i < WPT; ++i) {
                     const uint32_t(&qe)[4] = qa[2 * (gi * WPT + i)];
                     const uint32_t(&qo)[4] = qa[2 * (gi * WPT + i) + 1];
                     const uint32_t y = w[i] >> 8;
-                    mma16(a0, qe[0], qe[1], qe[2], qe[3], w[i] & 0x000f000fu, y & 0x000f000fu);
-                    mma16(G == 1 ? a1 : a0, qo[0], qo[1], qo[2], qo[3], w[i] & 0x00f000f0u, y & 0x00f000f0u);
+                    mma16(a, qe[0], qe[1], qe[2], qe[3], w[i] & 0x000f000fu, y & 0x000f000fu);
+                    mma16(G == 1 ? a1 : a, qo[0], qo[1], qo[2], qo[3], w[i] & 0x00f000f0u, y & 0x00f000f0u);
                 }
-                x0 = fmaf(scale_of(sc[gi]), (a0[0] + a0[2]) + (a1[0] + a1[2]), x0);
-                x1 = fmaf(scale_of(sc[G + gi]), (a0[1] + a0[3]) + (a1[1] + a1[3]), x1);
+                float2 sum = add2(make_float2(a[0], a[1]), make_float2(a[2], a[3]));
+                if (G == 1) sum = add2(sum, add2(make_float2(a1[0], a1[1]), make_float2(a1[2], a1[3])));
+                x = fma2(make_float2(scale_of(sc[gi]), scale_of(sc[G + gi])), sum, x);
             }
-            s[nt][0] = x0 * f;
-            s[nt][1] = x1 * f;
+            s[nt] = mul2(x, make_float2(f, f));
         }
         if (!whole) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = tok0 + nt * 8 + 2 * t4 + e;
-                    if (tok < me.lo || tok >= min(me.len, tok_end)) s[nt][e] = -INFINITY;
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                const int tok = tok0 + nt * 8 + 2 * t4, end = min(me.len, tok_end);
+                if (tok < me.lo || tok >= end) s[nt].x = -INFINITY;
+                if (tok + 1 < me.lo || tok + 1 >= end) s[nt].y = -INFINITY;
+            }
         }
 
         // ---- V scales of this lane's keys and the running reference
@@ -664,7 +686,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
             lds_words<2 * G>(page + ((nt * 8 % BS) + 2 * t4) * G * 4, vp[nt]);
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&vp[nt][i]));
-            mx = fmaxf(mx, fmaxf(s[nt][0], s[nt][1]));
+            mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
         }
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
@@ -682,17 +704,14 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         const float base = ref_new == -INFINITY ? 0.f : ref_new;
         const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
         ref = ref_new;
-        float psum = 0.f;
-        float w[NT][2];
+        float2 psum = make_float2(0.f, 0.f), w[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                w[nt][e] = ex2_approx(s[nt][e] - base);
-                psum += w[nt][e];
-            }
+            const float2 e = add2(s[nt], make_float2(-base, -base));
+            w[nt] = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            psum = add2(psum, w[nt]);
         }
-        l_run = l_run * alpha + psum;
+        l_run = l_run * alpha + (psum.x + psum.y);
         if (__any_sync(kFull, alpha != 1.f)) {
             const float alpha_a = __shfl_sync(kFull, alpha, 8 * t4);
             const float alpha_b = __shfl_sync(kFull, alpha, 8 * t4 + 4);
@@ -704,48 +723,45 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
                 oT[mt][3] *= alpha_b;
             }
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi) zo[gi] *= alpha;
+            for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
         }
 
-        // ---- O^T += V^T P^T, 16 keys per step
+        // ---- O^T += V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit units
+        // (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1 in
+        // one register: the pairs along the keys that the A operand wants
+        const uint32_t vrow = smem_addr(vpages) + (lane & 15) * (D / 2) + (lane >> 4) * 16;
 #pragma unroll
         for (int kt = 0; kt < kStageKeys / 16; ++kt) {
-            const uint8_t *page = vpages + (kt * 16 / BS) * Cfg::kPageBytes;
-            const int r0 = kt * 16 % BS + 2 * t4;
-            // lane g's half words of keys r0, r0 + 1, r0 + 8, r0 + 9: group gi's are words
-            // gi * WORDS / G + ...; with four words to a group two lanes share a word
-            constexpr int WPL = HPG == 1 ? 1 : HPG / 2;   // words per lane and group
-            const int wsel = HPG == 1 ? g >> 1 : g * WPL;
-            const uint32_t sel_lo = HPG == 1 && (g & 1) ? 0x7632u : 0x5410u;
+            const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2);
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
                 uint32_t bh0, bl0, bh1, bl1;
                 {
                     const float2 p0 = par_of(vp[2 * kt][gi]), p1 = par_of(vp[2 * kt][G + gi]);
                     const float2 p2 = par_of(vp[2 * kt + 1][gi]), p3 = par_of(vp[2 * kt + 1][G + gi]);
-                    const float w0 = w[2 * kt][0], w1 = w[2 * kt][1], w2 = w[2 * kt + 1][0], w3 = w[2 * kt + 1][1];
-                    split2(w0 * p0.x, w1 * p1.x, bh0, bl0);
-                    split2(w2 * p2.x, w3 * p3.x, bh1, bl1);
-                    zo[gi] = fmaf(w0, p0.y, fmaf(w1, p1.y, fmaf(w2, p2.y, fmaf(w3, p3.y, zo[gi]))));
+                    const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
+                    split2(mul2(wa, make_float2(p0.x, p1.x)), bh0, bl0);
+                    split2(mul2(wb, make_float2(p2.x, p3.x)), bh1, bl1);
+                    zo[gi] = fma2(wa, make_float2(p0.y, p1.y), fma2(wb, make_float2(p2.y, p3.y), zo[gi]));
                 }
-                const uint8_t *src = page + r0 * (D / 2) + (gi * (WORDS / G) + wsel) * 4;
-                uint32_t v0[WPL], v1[WPL], v2[WPL], v3[WPL];
-                lds_words<WPL>(src, v0);
-                lds_words<WPL>(src + D / 2, v1);
-                lds_words<WPL>(src + 8 * (D / 2), v2);
-                lds_words<WPL>(src + 9 * (D / 2), v3);
 #pragma unroll
-                for (int h = 0; h < HPG; ++h) {
-                    const uint32_t sel = (h & 1) ? 0x7632u : sel_lo;
-                    const uint32_t x = __byte_perm(v0[h / 2], v1[h / 2], sel), y = __byte_perm(v2[h / 2], v3[h / 2], sel);
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-                    const int mt = 2 * (gi * HPG + h);
-                    const uint32_t e0 = x & 0x000f000fu, e1 = x8 & 0x000f000fu, e2 = y & 0x000f000fu, e3 = y8 & 0x000f000fu;
-                    const uint32_t d0 = x & 0x00f000f0u, d1 = x8 & 0x00f000f0u, d2 = y & 0x00f000f0u, d3 = y8 & 0x00f000f0u;
-                    mma16(oT[mt], e0, e1, e2, e3, bh0, bh1);
-                    mma16(oT[mt + 1], d0, d1, d2, d3, bh0, bh1);
-                    mma16(oT[mt], e0, e1, e2, e3, bl0, bl1);
-                    mma16(oT[mt + 1], d0, d1, d2, d3, bl0, bl1);
+                for (int h = 0; h < HPG; h += 2) {
+                    // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
+                    const int c = gi * HPG + h;
+                    uint32_t v[4];
+                    if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
+                    else ldsm_x2_trans(rows - (lane >> 4) * 16 + c * 16, v[0], v[1]);
+#pragma unroll
+                    for (int i = 0; i < (HPG >= 2 ? 2 : 1); ++i) {
+                        const uint32_t x = v[2 * i], y = v[2 * i + 1], x8 = x >> 8, y8 = y >> 8;
+                        const int mt = 2 * (c + i);
+                        const uint32_t e0 = x & 0x000f000fu, e1 = x8 & 0x000f000fu, e2 = y & 0x000f000fu, e3 = y8 & 0x000f000fu;
+                        const uint32_t d0 = x & 0x00f000f0u, d1 = x8 & 0x00f000f0u, d2 = y & 0x00f000f0u, d3 = y8 & 0x00f000f0u;
+                        mma16(oT[mt], e0, e1, e2, e3, bh0, bh1);
+                        mma16(oT[mt + 1], d0, d1, d2, d3, bh0, bh1);
+                        mma16(oT[mt], e0, e1, e2, e3, bl0, bl1);
+                        mma16(oT[mt + 1], d0, d1, d2, d3, bl0, bl1);
+                    }
                 }
             }
         }
@@ -766,8 +782,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
     l_run += __shfl_xor_sync(kFull, l_run, 2);
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-        zo[gi] += __shfl_xor_sync(kFull, zo[gi], 1);
-        zo[gi] += __shfl_xor_sync(kFull, zo[gi], 2);
+        zo[gi].x += zo[gi].y;
+        zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 1);
+        zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 2);
     }
 
     // ---- the warps' (ref, l, O) through shared memory (the ring is free now)
@@ -779,14 +796,12 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         mw[warp * 8 + g] = ref;
         lw[warp * 8 + g] = l_run;
     }
-    constexpr int WPL = HPG == 1 ? 1 : HPG / 2;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-        const float za_ = __shfl_sync(kFull, zo[gi], 8 * t4), zb_ = __shfl_sync(kFull, zo[gi], 8 * t4 + 4);
+        const float za_ = __shfl_sync(kFull, zo[gi].x, 8 * t4), zb_ = __shfl_sync(kFull, zo[gi].x, 8 * t4 + 4);
 #pragma unroll
         for (int h = 0; h < HPG; ++h) {
-            const int word = gi * (WORDS / G) + (HPG == 1 ? g >> 1 : g * WPL + h / 2);
-            const int dim = 8 * word + 4 * (HPG == 1 ? g & 1 : h & 1), mt = 2 * (gi * HPG + h);
+            const int c = gi * HPG + h, dim = 32 * c + 4 * g, mt = 2 * c;
             // even codes were c * 2^-24, odd ones c * 2^-20
             float *oa = ow + (warp * 8 + 2 * t4) * D + dim, *ob = oa + D;
             oa[0] = fmaf(oT[mt][0], 0x1p24f, za_);
