@@ -183,7 +183,9 @@ struct MmaCfg {
     static constexpr int kRingBytes = kMmaWarps * kStages * kStageBytes;
     static constexpr int kMergeBytes = kMmaWarps * 8 * (2 + D) * 4;
     static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-    static constexpr int kSmemBytes = kDataBytes + kMmaWarps * kStages * 8;
+    static constexpr int kQOff = kDataBytes;          // query fragments, the sums' ones, the rows' factors
+    static constexpr int kBarOff = kQOff + (D / 16) * 512 + 256 + 32;
+    static constexpr int kSmemBytes = kBarOff + kMmaWarps * kStages * 8;
     static_assert(kPageBytes % 16 == 0, "bulk copies");
 };
 
@@ -203,15 +205,7 @@ __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(b0));
 }
 
-// x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x0.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
+// x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x.x.
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x.x, x.y);
     const float2 f = __half22float2(h);
@@ -219,6 +213,10 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     const __half2 l = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    split2(make_float2(x0, x1), hi, lo);
 }
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
     const DecodeKParams &p = P.k;
 
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kDataBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
     __shared__ RowSpan s_rows[8];
 
     pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
@@ -514,38 +512,37 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         const int st = k % kStages;
         uint8_t *stage = smem + (warp * kStages + st) * Cfg::kStageBytes;
         const uint32_t bar = smem_addr(&bars[warp * kStages + st]);
-        int phys[PPS];
-        unsigned bytes = 0;
-#pragma unroll
-        for (int i = 0; i < PPS; ++i) {
-            phys[i] = __shfl_sync(kFull, tcur[i], k & 31);
-            const bool there = pg0 + (warp + k * NW) * PPS + i < pg1, ok = phys[i] >= 0 && phys[i] < p.NB;
-            const unsigned bit = 1u << (st * PPS + i);
-            bad = there && !ok ? bad | bit : bad & ~bit;
-            if (there && !ok && lane == 0) raise_error(p.err, PKV_DEVERR_BLOCK);
-            if (!there || !ok) phys[i] = -1;
-            bytes += phys[i] >= 0 ? 2 * Cfg::kPageBytes : 0;
+        // lane l: copy l of the stage's 2 * PPS (K pages, then V pages)
+        const int i = lane % PPS, pg = pg0 + (warp + k * NW) * PPS + i;
+        int phys = __shfl_sync(kFull, tcur[0], k & 31);
+        if (PPS == 2) {
+            const int second = __shfl_sync(kFull, tcur[PPS - 1], k & 31);
+            if (i == 1) phys = second;
         }
+        const bool there = lane < 2 * PPS && pg < pg1, ok = there && phys >= 0 && phys < p.NB;
+        const unsigned copies = __ballot_sync(kFull, ok), absent = __ballot_sync(kFull, there && !ok);
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-            for (int i = 0; i < PPS; ++i) {
-                if (phys[i] < 0) continue;
-                const size_t at = (static_cast<size_t>(phys[i]) * p.Hkv + kvh) * Cfg::kPageBytes;
-                bulk_load(smem_addr(stage + i * Cfg::kPageBytes), P.kc + at, Cfg::kPageBytes, bar);
-                bulk_load(smem_addr(stage + (PPS + i) * Cfg::kPageBytes), P.vc + at, Cfg::kPageBytes, bar);
-            }
+            mbar_arrive_expect_tx(bar, __popc(copies) * Cfg::kPageBytes);
+            if (absent != 0) raise_error(p.err, PKV_DEVERR_BLOCK);
         }
+        bad = (bad & ~(((1u << PPS) - 1) << (st * PPS))) | ((absent & ((1u << PPS) - 1)) << (st * PPS));
+        __syncwarp();   // the expected bytes are announced before any copy
+        if (ok)
+            bulk_load(smem_addr(stage + lane * Cfg::kPageBytes),
+                      (lane < PPS ? P.kc : P.vc) + (static_cast<size_t>(phys) * p.Hkv + kvh) * Cfg::kPageBytes,
+                      Cfg::kPageBytes, bar);
     };
     int issued = min(kStages, n_my);
     for (int k = 0; k < issued; ++k) issue(k);
 
-    // ---- query fragments.  MMA step 2u (codes' even nibbles) and 2u + 1 (odd nibbles, 16 times
-    // the value) of word u = gi * WPT + i: elements 8 * word + {0, 4}, {2, 6} and {1, 5}, {3, 7}
+    // ---- query fragments, for all warps, by warp 0 while the copies fly.  MMA step 2u (codes' even
+    // nibbles) and 2u + 1 (odd nibbles, 16 times the value) of word u = gi * WPT + i: elements
+    // 8 * word + {0, 4}, {2, 6} and {1, 5}, {3, 7}
+    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff) + lane;    // [step][lane]
+    uint2 *zfrag = reinterpret_cast<uint2 *>(smem + Cfg::kQOff + KSTEPS * 512) + lane;
+    float *ffrag = reinterpret_cast<float *>(smem + Cfg::kQOff + KSTEPS * 512 + 256) + g;
     const RowSpan me = s_rows[g];
-    uint32_t qa[KSTEPS][4], za[2] = {0, 0};
-    float f;   // score (base 2) = MMA sum * f
-    {
+    if (warp == 0) {
         const float *qrow = p.q + static_cast<size_t>(me.bi >= 0 ? me.bi : 0) * D;
         float x[G * WPT][8], amax = 0.f, zsum = 0.f;
 #pragma unroll
@@ -565,30 +562,38 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         // |q| * 2^sq in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
         const int sq = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
         const float up = pow2i(sq);
-        f = (p.scale_log2 * 0x1p24f) * pow2i(-sq);
+        if (t4 == 0) *ffrag = (p.scale_log2 * 0x1p24f) * pow2i(-sq);   // score (base 2) = MMA sum * this
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < WPT; ++i) {
                 const int u = gi * WPT + i;
+                uint4 qe, qo;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     x[u][e] *= up;
                     sum += x[u][e];
                 }
-                split2(x[u][0], x[u][4], qa[2 * u][0], qa[2 * u][1]);
-                split2(x[u][2], x[u][6], qa[2 * u][2], qa[2 * u][3]);
-                split2(x[u][1] * 0.0625f, x[u][5] * 0.0625f, qa[2 * u + 1][0], qa[2 * u + 1][1]);
-                split2(x[u][3] * 0.0625f, x[u][7] * 0.0625f, qa[2 * u + 1][2], qa[2 * u + 1][3]);
+                split2(x[u][0], x[u][4], qe.x, qe.y);
+                split2(x[u][2], x[u][6], qe.z, qe.w);
+                split2(x[u][1] * 0.0625f, x[u][5] * 0.0625f, qo.x, qo.y);
+                split2(x[u][3] * 0.0625f, x[u][7] * 0.0625f, qo.z, qo.w);
+                qfrag[(2 * u) * 32] = qe;
+                qfrag[(2 * u + 1) * 32] = qo;
             }
             sum += __shfl_xor_sync(kFull, sum, 1);
             sum += __shfl_xor_sync(kFull, sum, 2);
             if (gi == t4) zsum = sum;
         }
         // (0, sum of q over group t4) * 2^-8, which keeps 128 elements below 2^14; zero beyond G
-        split2(0.f, zsum * 0x1p-8f, za[0], za[1]);
+        uint2 z;
+        split2(0.f, zsum * 0x1p-8f, z.x, z.y);
+        *zfrag = z;
     }
+    __syncthreads();
+    const uint2 za = *zfrag;
+    const float f = *ffrag;
 
     float oT[D / 16][4];
     float2 zo[G];   // sums of weight * zero over this lane's keys
@@ -598,7 +603,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
     for (int gi = 0; gi < G; ++gi) zo[gi] = make_float2(0.f, 0.f);
     float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
     float ref = -INFINITY;                  // m_run + E - 14
-    float vs_max = 0x1p-24f;                // the largest V scale seen (fp16's smallest to begin with)
+    unsigned vs_bits = 0;                   // the largest V scale seen (f16 bits)
+    float vs_exp = -24.f;                   // E: its exponent, rounded up (fp16's smallest to begin with)
 
     int k = 0;
     for (; k < n_my; ++k) {
@@ -639,34 +645,43 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
         float2 s[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint8_t *page = kpages + (nt * 8 / BS) * Cfg::kPageBytes;
-            const uint32_t *par = reinterpret_cast<const uint32_t *>(page + Cfg::kCodeBytes);
-            const int r0 = nt * 8 % BS;
-            const uint8_t *krow = page + (r0 + g) * (D / 2) + t4 * WPT * 4;
-            float zacc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma8(zacc, za[0], za[1], t4 < G ? par[(r0 + g) * G + t4] : 0u);
-            uint32_t sc[2 * G];
-            lds_words<2 * G>(reinterpret_cast<const uint8_t *>(par + (r0 + 2 * t4) * G), sc);
-            float2 x = mul2(add2(make_float2(zacc[0], zacc[1]), make_float2(zacc[2], zacc[3])), make_float2(0x1p-16f, 0x1p-16f));
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                uint32_t w[WPT];
-                lds_words<WPT>(krow + gi * (D / 2 / G), w);
-                float a[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};   // two chains where a group is long
-#pragma unroll
-                for (int i = 0; i < WPT; ++i) {
-                    const uint32_t(&qe)[4] = qa[2 * (gi * WPT + i)];
-                    const uint32_t(&qo)[4] = qa[2 * (gi * WPT + i) + 1];
-                    const uint32_t y = w[i] >> 8;
-                    mma16(a, qe[0], qe[1], qe[2], qe[3], w[i] & 0x000f000fu, y & 0x000f000fu);
-                    mma16(G == 1 ? a1 : a, qo[0], qo[1], qo[2], qo[3], w[i] & 0x00f000f0u, y & 0x00f000f0u);
-                }
-                float2 sum = add2(make_float2(a[0], a[1]), make_float2(a[2], a[3]));
-                if (G == 1) sum = add2(sum, add2(make_float2(a1[0], a1[1]), make_float2(a1[2], a1[3])));
-                x = fma2(make_float2(scale_of(sc[gi]), scale_of(sc[G + gi])), sum, x);
-            }
-            s[nt] = mul2(x, make_float2(f, f));
+            const uint32_t *par = reinterpret_cast<const uint32_t *>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes);
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            mma8(z, za.x, za.y, t4 < G ? par[(nt * 8 % BS + g) * G + t4] : 0u);
+            s[nt] = mul2(add2(make_float2(z[0], z[1]), make_float2(z[2], z[3])), make_float2(0x1p-16f, 0x1p-16f));
         }
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) {
+            float a[NT][4];
+            uint32_t c[NT][WPT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
+                lds_words<WPT>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + (nt * 8 % BS + g) * (D / 2) + gi * (D / 2 / G) +
+                                   t4 * WPT * 4,
+                               c[nt]);
+            }
+#pragma unroll
+            for (int i = 0; i < WPT; ++i) {
+                const uint4 qe = qfrag[(2 * (gi * WPT + i)) * 32], qo = qfrag[(2 * (gi * WPT + i) + 1) * 32];
+                // the tiles' chains side by side
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16(a[nt], qe.x, qe.y, qe.z, qe.w, c[nt][i] & 0x000f000fu, (c[nt][i] >> 8) & 0x000f000fu);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16(a[nt], qo.x, qo.y, qo.z, qo.w, c[nt][i] & 0x00f000f0u, (c[nt][i] >> 8) & 0x00f000f0u);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t *par = reinterpret_cast<const uint32_t *>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes) +
+                                      (nt * 8 % BS + 2 * t4) * G + gi;
+                s[nt] = fma2(make_float2(scale_of(par[0]), scale_of(par[G])),
+                             add2(make_float2(a[nt][0], a[nt][1]), make_float2(a[nt][2], a[nt][3])), s[nt]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt] = mul2(s[nt], make_float2(f, f));
         if (!whole) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -676,30 +691,27 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
             }
         }
 
-        // ---- V scales of this lane's keys and the running reference
-        uint32_t vp[NT][2 * G];
-        __half2 top = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
-        float mx = -INFINITY;
+        // ---- the running reference: the rows' maxima and the largest V scale (lane: one key)
+        float mx = fmaxf(s[0].x, s[0].y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint8_t *page = vpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes;
-            lds_words<2 * G>(page + ((nt * 8 % BS) + 2 * t4) * G * 4, vp[nt]);
-#pragma unroll
-            for (int i = 0; i < 2 * G; ++i) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&vp[nt][i]));
-            mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
-        }
+        for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
         m_run = fmaxf(m_run, mx);
-        const float vs_new = __low2float(top);
-        if (__any_sync(kFull, vs_new > vs_max)) {   // rarely after the first stage
-            float v = fmaxf(vs_new, vs_max);
-            v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(kFull, v, 2));
-            // the next power of two, so that E moves seldom
-            vs_max = pow2i(static_cast<int>((__float_as_uint(v) + 0x7fffffu) >> 23) - 127);
+        unsigned top = 0;   // positive f16 order like their bits
+        {
+            uint32_t v[G];
+            lds_words<G>(vpages + (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes + (lane % BS) * G * 4, v);
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) top = max(top, v[gi] & 0xffffu);
+            top = __reduce_max_sync(kFull, top);
         }
-        const float ref_new = m_run + (static_cast<float>(static_cast<int>(__float_as_uint(vs_max) >> 23) - 127) - 14.f);
+        if (top > vs_bits) {   // rarely after the first stage: the next power of two, E = its exponent
+            vs_bits = top;
+            const uint32_t v = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+            vs_exp = static_cast<float>(static_cast<int>((v + 0x7fffffu) >> 23) - 127);
+        }
+        const float ref_new = m_run + (vs_exp - 14.f);
         // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
         const float base = ref_new == -INFINITY ? 0.f : ref_new;
         const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
@@ -737,8 +749,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
             for (int gi = 0; gi < G; ++gi) {
                 uint32_t bh0, bl0, bh1, bl1;
                 {
-                    const float2 p0 = par_of(vp[2 * kt][gi]), p1 = par_of(vp[2 * kt][G + gi]);
-                    const float2 p2 = par_of(vp[2 * kt + 1][gi]), p3 = par_of(vp[2 * kt + 1][G + gi]);
+                    const uint32_t *par = reinterpret_cast<const uint32_t *>(vpages + (kt * 16 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes) +
+                                          (kt * 16 % BS + 2 * t4) * G + gi;
+                    const float2 p0 = par_of(par[0]), p1 = par_of(par[G]), p2 = par_of(par[8 * G]), p3 = par_of(par[9 * G]);
                     const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
                     split2(mul2(wa, make_float2(p0.x, p1.x)), bh0, bl0);
                     split2(mul2(wb, make_float2(p2.x, p3.x)), bh1, bl1);
@@ -751,16 +764,17 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const 
                     uint32_t v[4];
                     if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
                     else ldsm_x2_trans(rows - (lane >> 4) * 16 + c * 16, v[0], v[1]);
+                    constexpr int N = HPG >= 2 ? 2 : 1;
 #pragma unroll
-                    for (int i = 0; i < (HPG >= 2 ? 2 : 1); ++i) {
-                        const uint32_t x = v[2 * i], y = v[2 * i + 1], x8 = x >> 8, y8 = y >> 8;
-                        const int mt = 2 * (c + i);
-                        const uint32_t e0 = x & 0x000f000fu, e1 = x8 & 0x000f000fu, e2 = y & 0x000f000fu, e3 = y8 & 0x000f000fu;
-                        const uint32_t d0 = x & 0x00f000f0u, d1 = x8 & 0x00f000f0u, d2 = y & 0x00f000f0u, d3 = y8 & 0x00f000f0u;
-                        mma16(oT[mt], e0, e1, e2, e3, bh0, bh1);
-                        mma16(oT[mt + 1], d0, d1, d2, d3, bh0, bh1);
-                        mma16(oT[mt], e0, e1, e2, e3, bl0, bl1);
-                        mma16(oT[mt + 1], d0, d1, d2, d3, bl0, bl1);
+                    for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
+                        const uint32_t b0 = lo ? bl0 : bh0, b1 = lo ? bl1 : bh1;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const uint32_t x = v[2 * i], y = v[2 * i + 1], x8 = x >> 8, y8 = y >> 8;
+                            const int mt = 2 * (c + i);
+                            mma16(oT[mt], x & 0x000f000fu, x8 & 0x000f000fu, y & 0x000f000fu, y8 & 0x000f000fu, b0, b1);
+                            mma16(oT[mt + 1], x & 0x00f000f0u, x8 & 0x00f000f0u, y & 0x00f000f0u, y8 & 0x00f000f0u, b0, b1);
+                        }
                     }
                 }
             }
