@@ -26,7 +26,11 @@ struct AttendQ4Params {
     uint8_t *kc, *vc;
     int rows, max_q;     // query rows of the call, and of a sequence at most
     int new_bf16;        // type of the step's new rows
+    int balanced;        // the thread blocks share all sequences' keys evenly (else grid (splits x tiles, Hkv, B))
 };
+
+constexpr int kMaxBalanced = 1024;   // sequences of a balanced launch
+constexpr int kLeastSteps = 4;       // 32-key steps that a warp of one takes at least (128 keys)
 
 template <typename Kernel>
 cudaError_t set_smem_once(Kernel kernel, int bytes, std::atomic<unsigned long long> &done) {
@@ -152,24 +156,35 @@ __global__ void __launch_bounds__(128)
 
 // ============================================================== warp-MMA path
 //
-// attend_q4_mma_kernel (d 64 or 128, bs 16 or 32): one CTA per (sequence, KV head, tile of eight
-// query rows x heads, chunk of blocks); four warps take 32 keys at a time, each with a private
-// ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16 f16
-// MMAs and fp32 accumulators:
-//   A code c in 0..15 placed in the low bits of an f16 is the subnormal c * 2^-24, and shifted
-//   left by four bits it is c * 2^-20: both exact, so two masks turn a word of eight codes into
-//   four f16 pairs (three logic operations and a shift per pair of pairs) with no conversion.
-//   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): q is scaled by a power of two per
-//     row and enters as f16 hi + lo (2^-22 relative); the head dimension is taken in the order in
-//     which the masks deliver the codes, each group in MMA steps of its own so that its scale
-//     multiplies the sum; the zeros' term, sum_g zero_g * sum(q in g), is one k8 MMA whose B
-//     operand is the (scale, zero) pairs as they lie in the page against A = (0, sum q).
-//   output O^T = V^T P^T: V^T is the A operand (16 dimensions x 16 keys), words of two keys paired
-//     by byte permutes; P^T is what the lane already holds for its row, times the group's scale,
-//     as f16 hi + lo.  The zeros' term is summed in fp32.
+// attend_q4_mma_kernel (d 64 or 128, bs 16 or 32).  A unit is a tile of eight (query row, head)
+// pairs of one sequence and KV head with the keys they see; a warp takes 32 keys at a time from a
+// private ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16
+// f16 MMAs and fp32 accumulators:
+//   Integers below 2048 in the low bits of an f16 are the subnormals n * 2^-24, exactly, so codes
+//   need no conversion.  The bytes of a code word (two codes: c + 16 c') are masked to 16-bit
+//   lanes, E = c + 16 c' and O = 16 c', four logic operations for eight codes; with the pair
+//   (x, x') on the other side, x c + x' c' = x E + (x' / 16 - x) O.
+//   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): q is scaled by a power of two per row
+//     and its coefficients enter as f16 hi + lo (2^-22 relative, times 16 for the difference); the
+//     head dimension is taken in the order in which the masks deliver the codes, each group in MMA
+//     steps of its own so that its scale multiplies the sum; zero * sum(q in group) is added in fp32.
+//   output O^T = V^T P^T: V^T is the A operand (16 dimensions x 16 keys), pairs of keys from a
+//     transposing ldmatrix over 16-bit units; P^T is what the lane already holds for its row, times
+//     the group's scale, as f16 hi + lo.  The E sums minus the O sums are the even dimensions.
+//     The zeros' term is summed in fp32.
+//   Scales and zeros are widened to fp32 once per key by the lane of that number and read back
+//   from shared memory in pairs of keys.
 // The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
 // the largest scale seen so far, E = ceil(log2 max scale): w = 2^(s - m - E + 14); l, O and the
 // zeros' term carry the same factor, which cancels, and a growing E rescales like a growing max.
+//
+// Two ways to share the work:
+//   balanced: the 32-key steps of all units in a row (sequence, tile, KV head), an equal range for
+//     every warp that the device holds at once; a range may end one unit and begin the next.  A
+//     unit's parts meet in the workspace and the last to arrive merges them.  Nothing in a block
+//     waits for another warp, so the start of a warp's next unit hides behind its neighbours.
+//   chunks: one block for each unit and chunk, its four warps taking the steps in turn and merging
+//     in shared memory; a few chunks merge in place, many in decode_merge_kernel.
 
 constexpr int kMmaWarps = 4, kStageKeys = 32, kStages = 2;
 
@@ -182,10 +197,17 @@ struct MmaCfg {
     static constexpr int kStageBytes = 2 * PPS * kPageBytes;   // K pages, then V pages
     static constexpr int kRingBytes = kMmaWarps * kStages * kStageBytes;
     static constexpr int kMergeBytes = kMmaWarps * 8 * (2 + D) * 4;
-    static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-    static constexpr int kQOff = kDataBytes;          // query fragments, the sums' ones, the rows' factors
-    static constexpr int kBarOff = kQOff + (D / 16) * 512 + 256 + 32;
+    static constexpr int kScanBytes = (kMaxBalanced + 1) * 4;
+    static constexpr int kUsed = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kDataBytes = (kUsed > kScanBytes ? kUsed : kScanBytes) + 15 & ~15;
+    static constexpr int kQOff = kDataBytes;                            // query fragments [warp][step][lane]
+    static constexpr int kQBytes = (D / 16) * 512;
+    static constexpr int kParOff = kQOff + kMmaWarps * kQBytes;         // [warp][group][scale, zero][key]
+    static constexpr int kParBytes = G * 2 * kStageKeys * 4;
+    static constexpr int kBarOff = kParOff + kMmaWarps * kParBytes;
     static constexpr int kSmemBytes = kBarOff + kMmaWarps * kStages * 8;
+    // 228 KB of shared memory less 1 KB a block: four blocks per SM where they fit
+    static constexpr int kBlocksPerSm = kSmemBytes + 512 <= 56 * 1024 ? 4 : 3;
     static_assert(kPageBytes % 16 == 0, "bulk copies");
 };
 
@@ -198,13 +220,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm(
-        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(b0));
-}
-
 // x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x.x.
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x.x, x.y);
@@ -232,13 +247,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 __device__ __forceinline__ void ldsm_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
-}
-
-__device__ __forceinline__ float2 par_of(uint32_t u) {   // (scale, zero)
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-__device__ __forceinline__ float scale_of(uint32_t u) {
-    return __low2float(*reinterpret_cast<const __half2 *>(&u));
 }
 
 // 2^e as a float, e clamped to the normal range.
@@ -308,12 +316,18 @@ __device__ __forceinline__ RowSpan tile_row(const AttendQ4Params &P, const SeqRo
     return r;
 }
 
+// The parts of a unit (the rows of a tile over ranges of its keys).
+struct Parts {
+    int first;   // balanced: the warp that holds part 0; warp first + i holds part i
+    int own, n;  // this part and their number
+    unsigned *counter;
+};
+
 // The warps' states of a tile's eight rows, in shared memory ([NW][8] references and sums, then
-// [NW][8][D] outputs), merged and written: the result where the sequence has one chunk, else the
-// chunk's normalised partial; with arrival counters the unit's last chunk merges them all.
+// [NW][8][D] outputs), merged and written: the result where the unit has one part, else this
+// normalised part; with arrival counters the unit's last part merges them all.
 template <int D, int NW>
-__device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params &P, const RowSpan *rows, int unit,
-                                            int split, int nc) {
+__device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params &P, const RowSpan *rows, const Parts &u) {
     const DecodeKParams &p = P.k;
     float *mw = reinterpret_cast<float *>(smem);
     float *lw = mw + NW * 8;
@@ -321,11 +335,10 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
     for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
         const int h = idx / (D / 4), c = idx % (D / 4) * 4;
         if (rows[h].bi < 0) continue;
-        const size_t bi = rows[h].bi;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * 8 + h]);
-        const float base = M == -INFINITY ? 0.f : M;   // the row sees none of this chunk's keys
+        const float base = M == -INFINITY ? 0.f : M;   // the row sees none of this part's keys
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -341,22 +354,23 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
         const float inv = M == -INFINITY ? 0.f : 1.f / L;
         const float4 r = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         const float lse2 = M == -INFINITY ? -INFINITY : M + log2f(L);
-        if (nc == 1) {
-            *reinterpret_cast<float4 *>(p.out + bi * D + c) = r;
-            if (c == 0 && p.lse != nullptr) p.lse[bi] = lse2 * kDecLn2;
+        if (u.n == 1) {
+            *reinterpret_cast<float4 *>(p.out + static_cast<size_t>(rows[h].bi) * D + c) = r;
+            if (c == 0 && p.lse != nullptr) p.lse[rows[h].bi] = lse2 * kDecLn2;
         } else {
-            *reinterpret_cast<float4 *>(p.ws_o + (bi * p.splits + split) * D + c) = r;
-            if (c == 0) p.ws_lse[bi * p.splits + split] = lse2;
+            const size_t at = static_cast<size_t>(rows[h].bi) * p.splits + u.own;
+            *reinterpret_cast<float4 *>(p.ws_o + at * D + c) = r;
+            if (c == 0) p.ws_lse[at] = lse2;
         }
     }
-    if (nc == 1 || p.counters == nullptr) return;
+    if (u.n == 1 || u.counter == nullptr) return;
     __shared__ int s_last;
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        const unsigned prev = atomicAdd(p.counters + unit, 1u);
-        s_last = prev + 1 == static_cast<unsigned>(nc);
-        if (s_last) p.counters[unit] = 0u;   // every chunk of this call has arrived
+        const unsigned prev = atomicAdd(u.counter, 1u);
+        s_last = prev + 1 == static_cast<unsigned>(u.n);
+        if (s_last) *u.counter = 0u;   // every part of this call has arrived
     }
     __syncthreads();
     if (!s_last) return;
@@ -364,16 +378,15 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
     for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
         const int h = idx / (D / 4), c = idx % (D / 4) * 4;
         if (rows[h].bi < 0) continue;
-        const size_t bi = rows[h].bi;
-        const float *ls = p.ws_lse + bi * p.splits, *po = p.ws_o + bi * p.splits * D + c;
+        const size_t at = static_cast<size_t>(rows[h].bi) * p.splits;
         float M = -INFINITY;
-        for (int i = 0; i < nc; ++i) M = fmaxf(M, __ldcg(ls + i));
+        for (int i = 0; i < u.n; ++i) M = fmaxf(M, __ldcg(p.ws_lse + at + i));
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = 0; i < nc; ++i) {
-            const float w = exp2f(__ldcg(ls + i) - M);
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * D));
+        for (int i = 0; i < u.n; ++i) {
+            const float w = exp2f(__ldcg(p.ws_lse + at + i) - M);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (at + i) * D + c));
             L += w;
             acc.x += w * o.x;
             acc.y += w * o.y;
@@ -381,8 +394,61 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
             acc.w += w * o.w;
         }
         const float inv = 1.f / L;
-        *reinterpret_cast<float4 *>(p.out + bi * D + c) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (c == 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kDecLn2;
+        *reinterpret_cast<float4 *>(p.out + static_cast<size_t>(rows[h].bi) * D + c) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (c == 0 && p.lse != nullptr) p.lse[rows[h].bi] = (M + log2f(L)) * kDecLn2;
+    }
+}
+
+// Row h of a balanced part, in units of D floats of ws_o and of one float of ws_lse: a warp's first
+// unit may have begun in the warp before (slot 0), its last may go on (slot 1).
+__device__ __forceinline__ size_t part_at(const Parts &u, int h, int i) {
+    return (static_cast<size_t>(u.first + i) * 2 + (i == 0)) * 8 + h;
+}
+
+// The last warp to arrive merges a balanced unit's parts: lane l holds row l % 8 of every fourth
+// part's weight, and every lane four columns of all rows.
+template <int D>
+__device__ __forceinline__ void merge_unit(const AttendQ4Params &P, const RowSpan &me, const Parts &u, int lane) {
+    const DecodeKParams &p = P.k;
+    const int row = lane & 7, sub = lane >> 3, col = lane * 4;
+    float M = -INFINITY, L = 0.f;
+    for (int i = sub; i < u.n; i += 4) M = fmaxf(M, __ldcg(p.ws_lse + part_at(u, row, i)));
+    M = fmaxf(M, __shfl_xor_sync(kFull, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(kFull, M, 16));
+    const float base = M == -INFINITY ? 0.f : M;   // a row past the sequence's last
+    float4 acc[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < u.n; i0 += 4) {
+        const float w = i0 + sub < u.n ? exp2f(__ldcg(p.ws_lse + part_at(u, row, i0 + sub)) - base) : 0.f;
+        L += w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i0 + j >= u.n) break;
+            const float *src = p.ws_o + part_at(u, 0, i0 + j) * D + col;
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const float f = __shfl_sync(kFull, w, j * 8 + h);
+                const float4 o = col < D ? __ldcg(reinterpret_cast<const float4 *>(src + h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                acc[h].x = fmaf(f, o.x, acc[h].x);
+                acc[h].y = fmaf(f, o.y, acc[h].y);
+                acc[h].z = fmaf(f, o.z, acc[h].z);
+                acc[h].w = fmaf(f, o.w, acc[h].w);
+            }
+        }
+    }
+    L += __shfl_xor_sync(kFull, L, 8);
+    L += __shfl_xor_sync(kFull, L, 16);
+    const int bi = __shfl_sync(kFull, me.bi, row * 4);   // lane 4 * r holds row r's
+    if (lane < 8 && bi >= 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kDecLn2;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+        const float inv = 1.f / __shfl_sync(kFull, L, h);
+        const int at = __shfl_sync(kFull, bi, h);
+        if (at >= 0 && col < D)
+            *reinterpret_cast<float4 *>(p.out + static_cast<size_t>(at) * D + col) =
+                make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
     }
 }
 
@@ -423,414 +489,531 @@ __device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, in
 }
 
 template <int D, int BS, int G>
-__global__ void __launch_bounds__(kMmaWarps * 32, 4) attend_q4_mma_kernel(const __grid_constant__ AttendQ4Params P) {
+__global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerSm))
+    attend_q4_mma_kernel(const __grid_constant__ AttendQ4Params P) {
     using Cfg = MmaCfg<D, BS, G>;
     constexpr int NW = kMmaWarps, NT = kStageKeys / 8, PPS = Cfg::PPS, WORDS = Cfg::WORDS;
     constexpr int WPT = WORDS / (4 * G);         // K: words per lane and group
-    constexpr int KSTEPS = D / 16;
     constexpr int HPG = D / 32 / G;              // V: 32-dimension columns per group
     static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
     const DecodeKParams &p = P.k;
 
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
-    __shared__ RowSpan s_rows[8];
+    __shared__ RowSpan s_rows[8];   // chunks: the tile's rows
 
     pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const int tile = blockIdx.x % p.head_tiles, split = blockIdx.x / p.head_tiles;
-    const int kvh = blockIdx.y, b = blockIdx.z;
-    const bool report = threadIdx.x == 0 && split == 0 && kvh == 0 && tile == 0;
-
-    // ---- the sequence's rows and this tile's
-    const SeqRows sq = seq_rows(P, b, BS, report);
-    if (split == 0 && tile == 0) clear_rows(P, sq, kvh, D);
-    if (!sq.ok || 8 * tile >= sq.nq * p.m) return;
-    if (threadIdx.x < 8) s_rows[threadIdx.x] = tile_row(P, sq, kvh, 8 * tile + threadIdx.x);
-    // pages that any row of the sequence sees; this chunk's, and those that this tile sees
-    const int c0 = sq.first + split * p.chunk_pages, c1 = min(sq.first + sq.pages, c0 + p.chunk_pages);
-    if (c0 >= c1) {
-        // a new token for a sequence that holds none has no position: flagged, not written
-        if (split == 0 && p.new_slots != nullptr && threadIdx.x == 0 && sq.L == 0 && __ldg(p.new_slots + b) >= 0)
-            raise_error(p.err, PKV_DEVERR_SLOT);
-        return;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff) + warp * kStages;
+    uint8_t *ring = smem + warp * kStages * Cfg::kStageBytes;
+    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff + warp * Cfg::kQBytes) + lane;   // [step][lane]
+    float *par = reinterpret_cast<float *>(smem + Cfg::kParOff + warp * Cfg::kParBytes);
+    if (lane == 0) {
+        for (int st = 0; st < kStages; ++st) mbar_init(smem_addr(&bars[st]), 1);
+        fence_barrier_init();
     }
-    const RowSpan t_first = tile_row(P, sq, kvh, 8 * tile), t_last = tile_row(P, sq, kvh, min(8 * tile + 7, sq.nq * p.m - 1));
-    const int pg0 = max(c0, t_first.lo / BS), pg1 = min(c1, (t_last.len + BS - 1) / BS);
-    const int tok_end = pg1 * BS;   // the chunk's keys end here
+    int cnt = 0;        // stages this warp has consumed
+    unsigned bad = 0;   // bit (stage * PPS + page): a page to be read as zeros
 
-    if (p.new_slots != nullptr && c1 == sq.first + sq.pages) {
-        // the step's new token: the CTA that reads the sequence's last page writes its K and V
-        // rows there before any copy of the page
-        if (warp < 2) {
+    // ---- balanced: this warp's share [x, x1) of the steps of all units.  Warps are as many as fit
+    // the device at once; fewer when that would leave them less than kLeastSteps each, but one for
+    // every unit.  They are numbered so that neighbours lie in different blocks.
+    const int wid = warp * gridDim.x + blockIdx.x;
+    int x = 0, x1 = 1, Q = 1, warps = 1, b = 0, unit = 0, step = 0;
+    if (P.balanced) {
+        int *pre = reinterpret_cast<int *>(smem);   // steps before each sequence
+        __shared__ int s_sum[2][NW];
+        const int per = (p.B + NW * 32 - 1) / (NW * 32), first = threadIdx.x * per;
+        int steps = 0, units = 0;
+        for (int i = first; i < min(p.B, first + per); ++i) {
+            const SeqRows sq = seq_rows(P, i, BS, false);
+            const int n = sq.pages > 0 ? p.Hkv * ((sq.nq * p.m + 7) / 8) : 0;
+            pre[i + 1] = n * ((sq.pages + PPS - 1) / PPS);
+            steps += pre[i + 1];
+            units += n;
+        }
+        int before = steps;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int y = __shfl_up_sync(kFull, before, sh);
+            if (lane >= sh) before += y;
+            units += __shfl_xor_sync(kFull, units, sh);
+        }
+        if (lane == 31) s_sum[0][warp] = before, s_sum[1][warp] = units;
+        __syncthreads();
+        Q = units = 0;
+        before -= steps;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += s_sum[0][w];
+            Q += s_sum[0][w];
+            units += s_sum[1][w];
+        }
+        if (threadIdx.x == 0) pre[0] = 0;
+        for (int i = first; i < min(p.B, first + per); ++i) pre[i + 1] = before += pre[i + 1];
+        warps = min(static_cast<int>(gridDim.x) * NW, max(units, Q / kLeastSteps));
+        x = static_cast<int>(min(static_cast<long long>(Q), static_cast<long long>(wid) * Q / max(warps, 1)));
+        x1 = static_cast<int>(min(static_cast<long long>(Q), (wid + 1ll) * Q / max(warps, 1)));
+        __syncthreads();
+        for (int st = kMaxBalanced / 2; st > 0; st >>= 1)
+            if (b + st < p.B && pre[b + st] <= x) b += st;
+        if (x < x1) {
+            const SeqRows sq = seq_rows(P, b, BS, false);
+            const int len = (sq.pages + PPS - 1) / PPS;
+            unit = (x - pre[b]) / len;
+            step = (x - pre[b]) - unit * len;
+        }
+        // rows that see nothing, bad lengths and rows
+        for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
+            const SeqRows sq = seq_rows(P, i, BS, threadIdx.x == 0);
+            for (int h = 0; h < p.Hkv; ++h) clear_rows(P, sq, h, D);
+            if (threadIdx.x == 0 && p.new_slots != nullptr && sq.L == 0 && __ldg(p.new_slots + i) >= 0)
+                raise_error(p.err, PKV_DEVERR_SLOT);
+        }
+        __syncthreads();   // the scan's memory becomes the ring
+    }
+
+    while (x < x1) {
+        // ---- the next segment: a unit and its pages [c0, c1)
+        int kvh, tile, c0, c1, turn = 0, turns = 1;   // this warp takes every turns-th step from turn on
+        Parts part{};
+        SeqRows sq;
+        if (P.balanced) {
+            sq = seq_rows(P, b, BS, false);
+            int len = (sq.pages + PPS - 1) / PPS, units = p.Hkv * ((sq.nq * p.m + 7) / 8);
+            while (sq.pages == 0 || unit == units) {   // on to the next sequence that has keys
+                ++b;
+                unit = 0;
+                sq = seq_rows(P, b, BS, false);
+                len = (sq.pages + PPS - 1) / PPS;
+                units = p.Hkv * ((sq.nq * p.m + 7) / 8);
+            }
+            kvh = unit % p.Hkv;
+            tile = unit / p.Hkv;
+            const int end = min(len, step + (x1 - x)), start = x - step;
+            c0 = sq.first + step * PPS;
+            c1 = min(sq.first + sq.pages, sq.first + end * PPS);
+            // the warp whose share holds position y is ((y + 1) * warps - 1) / Q
+            part.first = static_cast<int>(((start + 1ll) * warps - 1) / Q);
+            part.n = static_cast<int>((static_cast<long long>(start + len) * warps - 1) / Q) - part.first + 1;
+            part.own = wid - part.first;
+            part.counter = p.counters + part.first;   // at most one unit goes on from a warp into the next
+            x += end - step;
+            step = 0;
+            ++unit;
+        } else {
+            tile = blockIdx.x % p.head_tiles;
+            const int split = blockIdx.x / p.head_tiles;
+            kvh = blockIdx.y;
+            b = blockIdx.z;
+            sq = seq_rows(P, b, BS, threadIdx.x == 0 && split == 0 && kvh == 0 && tile == 0);
+            if (split == 0 && tile == 0) clear_rows(P, sq, kvh, D);
+            if (!sq.ok || 8 * tile >= sq.nq * p.m) return;
+            // pages that any row of the sequence sees; this chunk's
+            c0 = sq.first + split * p.chunk_pages;
+            c1 = min(sq.first + sq.pages, c0 + p.chunk_pages);
+            if (c0 >= c1) {
+                // a new token for a sequence that holds none has no position: flagged, not written
+                if (split == 0 && p.new_slots != nullptr && threadIdx.x == 0 && sq.L == 0 && __ldg(p.new_slots + b) >= 0)
+                    raise_error(p.err, PKV_DEVERR_SLOT);
+                return;
+            }
+            part.own = split;
+            part.n = (sq.pages + p.chunk_pages - 1) / p.chunk_pages;
+            part.counter = p.counters == nullptr ? nullptr : p.counters + (b * p.Hkv + kvh) * p.head_tiles + tile;
+            x = x1;
+            turn = warp;
+            turns = NW;
+            if (threadIdx.x < 8) s_rows[threadIdx.x] = tile_row(P, sq, kvh, 8 * tile + threadIdx.x);
+        }
+        const RowSpan t_first = tile_row(P, sq, kvh, 8 * tile), t_last = tile_row(P, sq, kvh, min(8 * tile + 7, sq.nq * p.m - 1));
+        const RowSpan me = tile_row(P, sq, kvh, 8 * tile + g);
+        const int pg0 = max(c0, t_first.lo / BS), pg1 = min(c1, (t_last.len + BS - 1) / BS);
+        const int tok_end = pg1 * BS;   // the segment's keys end here
+
+        if (p.new_slots != nullptr && c1 == sq.first + sq.pages) {
+            // the step's new token: the warp (chunks: the block's first two) whose segment holds the
+            // sequence's last page writes its K and V rows there before any copy of the page
             const long long slot = __ldg(p.new_slots + b);
             if (slot >= 0) {
                 const int pos = sq.L - 1, phys = __ldg(p.block_table + static_cast<size_t>(b) * p.MBS + pos / BS);
                 if (phys < 0 || phys >= p.NB || slot != static_cast<long long>(phys) * BS + pos % BS) {
-                    if (warp == 0 && lane == 0) raise_error(p.err, PKV_DEVERR_SLOT);
+                    if (turn == 0 && lane == 0) raise_error(p.err, PKV_DEVERR_SLOT);
                 } else {
-                    write_new_row<D, G>(P, b, kvh, (static_cast<long long>(phys) * p.Hkv + kvh) * Cfg::kPageBytes, pos % BS,
-                                        BS, warp, lane);
+                    for (int side = turn; side < 2; side += turns)
+                        write_new_row<D, G>(P, b, kvh, (static_cast<long long>(phys) * p.Hkv + kvh) * Cfg::kPageBytes,
+                                            pos % BS, BS, side, lane);
                 }
             }
             fence_proxy_async_global();
-        }
-        __syncthreads();
-        fence_proxy_async_global();
-    }
-
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(smem_addr(&bars[warp * kStages + s]), 1);
-        fence_barrier_init();
-    }
-    __syncthreads();   // s_rows; the barriers are the warp's own
-
-    // ---- this warp's stages: units of PPS pages warp, warp + NW, ... of [pg0, pg1)
-    const int units = pg1 > pg0 ? (pg1 - pg0 + PPS - 1) / PPS : 0;
-    const int n_my = units > warp ? (units - warp + NW - 1) / NW : 0;
-    const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
-    int tcur[PPS], tnext[PPS];
-    auto load_ids = [&](int k, int (&t)[PPS]) {
-#pragma unroll
-        for (int i = 0; i < PPS; ++i) {
-            const int pg = pg0 + (warp + k * NW) * PPS + i;
-            t[i] = k < n_my && pg < pg1 ? __ldg(tbl + pg) : -1;
-        }
-    };
-    load_ids(lane, tcur);
-    load_ids(32 + lane, tnext);
-    int tbase = 0;
-    unsigned bad = 0;   // bit (stage * PPS + page): a page to be read as zeros
-    auto issue = [&](int k) {   // the whole warp; lane 0 starts the copies
-        while (k >= tbase + 32) {
-            tbase += 32;
-#pragma unroll
-            for (int i = 0; i < PPS; ++i) tcur[i] = tnext[i];
-            load_ids(tbase + 32 + lane, tnext);
-        }
-        const int st = k % kStages;
-        uint8_t *stage = smem + (warp * kStages + st) * Cfg::kStageBytes;
-        const uint32_t bar = smem_addr(&bars[warp * kStages + st]);
-        // lane l: copy l of the stage's 2 * PPS (K pages, then V pages)
-        const int i = lane % PPS, pg = pg0 + (warp + k * NW) * PPS + i;
-        int phys = __shfl_sync(kFull, tcur[0], k & 31);
-        if (PPS == 2) {
-            const int second = __shfl_sync(kFull, tcur[PPS - 1], k & 31);
-            if (i == 1) phys = second;
-        }
-        const bool there = lane < 2 * PPS && pg < pg1, ok = there && phys >= 0 && phys < p.NB;
-        const unsigned copies = __ballot_sync(kFull, ok), absent = __ballot_sync(kFull, there && !ok);
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar, __popc(copies) * Cfg::kPageBytes);
-            if (absent != 0) raise_error(p.err, PKV_DEVERR_BLOCK);
-        }
-        bad = (bad & ~(((1u << PPS) - 1) << (st * PPS))) | ((absent & ((1u << PPS) - 1)) << (st * PPS));
-        __syncwarp();   // the expected bytes are announced before any copy
-        if (ok)
-            bulk_load(smem_addr(stage + lane * Cfg::kPageBytes),
-                      (lane < PPS ? P.kc : P.vc) + (static_cast<size_t>(phys) * p.Hkv + kvh) * Cfg::kPageBytes,
-                      Cfg::kPageBytes, bar);
-    };
-    int issued = min(kStages, n_my);
-    for (int k = 0; k < issued; ++k) issue(k);
-
-    // ---- query fragments, for all warps, by warp 0 while the copies fly.  MMA step 2u (codes' even
-    // nibbles) and 2u + 1 (odd nibbles, 16 times the value) of word u = gi * WPT + i: elements
-    // 8 * word + {0, 4}, {2, 6} and {1, 5}, {3, 7}
-    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff) + lane;    // [step][lane]
-    uint2 *zfrag = reinterpret_cast<uint2 *>(smem + Cfg::kQOff + KSTEPS * 512) + lane;
-    float *ffrag = reinterpret_cast<float *>(smem + Cfg::kQOff + KSTEPS * 512 + 256) + g;
-    const RowSpan me = s_rows[g];
-    if (warp == 0) {
-        const float *qrow = p.q + static_cast<size_t>(me.bi >= 0 ? me.bi : 0) * D;
-        float x[G * WPT][8], amax = 0.f, zsum = 0.f;
-#pragma unroll
-        for (int u = 0; u < G * WPT; ++u) {
-            const int word = (u / WPT) * (WORDS / G) + t4 * WPT + u % WPT;
-            const float2 *src = reinterpret_cast<const float2 *>(qrow + 8 * word);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 v = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
-                x[u][2 * e] = v.x;
-                x[u][2 * e + 1] = v.y;
-                amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-            }
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-        // |q| * 2^sq in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
-        const int sq = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
-        const float up = pow2i(sq);
-        if (t4 == 0) *ffrag = (p.scale_log2 * 0x1p24f) * pow2i(-sq);   // score (base 2) = MMA sum * this
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < WPT; ++i) {
-                const int u = gi * WPT + i;
-                uint4 qe, qo;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[u][e] *= up;
-                    sum += x[u][e];
-                }
-                split2(x[u][0], x[u][4], qe.x, qe.y);
-                split2(x[u][2], x[u][6], qe.z, qe.w);
-                split2(x[u][1] * 0.0625f, x[u][5] * 0.0625f, qo.x, qo.y);
-                split2(x[u][3] * 0.0625f, x[u][7] * 0.0625f, qo.z, qo.w);
-                qfrag[(2 * u) * 32] = qe;
-                qfrag[(2 * u + 1) * 32] = qo;
-            }
-            sum += __shfl_xor_sync(kFull, sum, 1);
-            sum += __shfl_xor_sync(kFull, sum, 2);
-            if (gi == t4) zsum = sum;
-        }
-        // (0, sum of q over group t4) * 2^-8, which keeps 128 elements below 2^14; zero beyond G
-        uint2 z;
-        split2(0.f, zsum * 0x1p-8f, z.x, z.y);
-        *zfrag = z;
-    }
-    __syncthreads();
-    const uint2 za = *zfrag;
-    const float f = *ffrag;
-
-    float oT[D / 16][4];
-    float2 zo[G];   // sums of weight * zero over this lane's keys
-#pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) oT[mt][0] = oT[mt][1] = oT[mt][2] = oT[mt][3] = 0.f;
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi) zo[gi] = make_float2(0.f, 0.f);
-    float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
-    float ref = -INFINITY;                  // m_run + E - 14
-    unsigned vs_bits = 0;                   // the largest V scale seen (f16 bits)
-    float vs_exp = -24.f;                   // E: its exponent, rounded up (fp16's smallest to begin with)
-
-    int k = 0;
-    for (; k < n_my; ++k) {
-        const int st = k % kStages;
-        const bool arrived = mbar_wait_bounded(smem_addr(&bars[warp * kStages + st]), (k / kStages) & 1);
-        if (!__all_sync(kFull, arrived)) {
-            if (lane == 0) raise_error(p.err, PKV_DEVERR_TIMEOUT);
-            break;
-        }
-        uint8_t *kpages = smem + (warp * kStages + st) * Cfg::kStageBytes;
-        uint8_t *vpages = kpages + PPS * Cfg::kPageBytes;
-        const int tok0 = (pg0 + (warp + k * NW) * PPS) * BS;
-        if (const unsigned zero = (bad >> (st * PPS)) & ((1u << PPS) - 1); zero != 0) {
-#pragma unroll
-            for (int i = 0; i < 2 * PPS; ++i)
-                if (zero >> (i % PPS) & 1)
-                    for (int c = lane * 16; c < Cfg::kPageBytes; c += 512)
-                        *reinterpret_cast<uint4 *>(kpages + i * Cfg::kPageBytes + c) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();   // before a later copy into this stage
-            __syncwarp();
-        }
-        // does every row of the tile see every key of the stage?
-        const bool whole = tok0 >= t_last.lo && tok0 + kStageKeys <= min(t_first.len, tok_end);
-        if (!whole) {
-            // parameters of V rows that no row of the tile sees may be anything: zero them, so that
-            // weight 0 contributes 0 (codes are finite whatever they are)
-            const int tok = tok0 + lane, off = lane % BS;
-            if (tok < t_first.lo || tok >= min(t_last.len, tok_end)) {
-#pragma unroll
-                for (int gi = 0; gi < G; ++gi)
-                    reinterpret_cast<uint32_t *>(vpages + (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes)[off * G + gi] = 0;
-                fence_proxy_async_smem();
-            }
-            __syncwarp();
+            if (turns > 1) __syncthreads();
+            else __syncwarp();
+            fence_proxy_async_global();
         }
 
-        // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
-        float2 s[NT];
+        // ---- this warp's stages: steps of PPS pages turn, turn + turns, ... of [pg0, pg1)
+        const int steps = pg1 > pg0 ? (pg1 - pg0 + PPS - 1) / PPS : 0;
+        const int n_my = steps > turn ? (steps - turn + turns - 1) / turns : 0;
+        const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
+        int tcur[PPS], tnext[PPS];
+        auto load_ids = [&](int k, int (&t)[PPS]) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t *par = reinterpret_cast<const uint32_t *>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes);
-            float z[4] = {0.f, 0.f, 0.f, 0.f};
-            mma8(z, za.x, za.y, t4 < G ? par[(nt * 8 % BS + g) * G + t4] : 0u);
-            s[nt] = mul2(add2(make_float2(z[0], z[1]), make_float2(z[2], z[3])), make_float2(0x1p-16f, 0x1p-16f));
-        }
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) {
-            float a[NT][4];
-            uint32_t c[NT][WPT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
-                lds_words<WPT>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + (nt * 8 % BS + g) * (D / 2) + gi * (D / 2 / G) +
-                                   t4 * WPT * 4,
-                               c[nt]);
+            for (int i = 0; i < PPS; ++i) {
+                const int pg = pg0 + (turn + k * turns) * PPS + i;
+                t[i] = k < n_my && pg < pg1 ? __ldg(tbl + pg) : -1;
             }
+        };
+        load_ids(lane, tcur);
+        load_ids(32 + lane, tnext);
+        int tbase = 0;
+        auto issue = [&](int k) {   // the whole warp
+            while (k >= tbase + 32) {
+                tbase += 32;
 #pragma unroll
-            for (int i = 0; i < WPT; ++i) {
-                const uint4 qe = qfrag[(2 * (gi * WPT + i)) * 32], qo = qfrag[(2 * (gi * WPT + i) + 1) * 32];
-                // the tiles' chains side by side
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16(a[nt], qe.x, qe.y, qe.z, qe.w, c[nt][i] & 0x000f000fu, (c[nt][i] >> 8) & 0x000f000fu);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16(a[nt], qo.x, qo.y, qo.z, qo.w, c[nt][i] & 0x00f000f0u, (c[nt][i] >> 8) & 0x00f000f0u);
+                for (int i = 0; i < PPS; ++i) tcur[i] = tnext[i];
+                load_ids(tbase + 32 + lane, tnext);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t *par = reinterpret_cast<const uint32_t *>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes) +
-                                      (nt * 8 % BS + 2 * t4) * G + gi;
-                s[nt] = fma2(make_float2(scale_of(par[0]), scale_of(par[G])),
-                             add2(make_float2(a[nt][0], a[nt][1]), make_float2(a[nt][2], a[nt][3])), s[nt]);
+            const int st = (cnt + k) % kStages;
+            const uint32_t bar = smem_addr(&bars[st]);
+            // lane l: copy l of the stage's 2 * PPS (K pages, then V pages)
+            const int i = lane % PPS, pg = pg0 + (turn + k * turns) * PPS + i;
+            int phys = __shfl_sync(kFull, tcur[0], k & 31);
+            if (PPS == 2) {
+                const int second = __shfl_sync(kFull, tcur[PPS - 1], k & 31);
+                if (i == 1) phys = second;
             }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt] = mul2(s[nt], make_float2(f, f));
-        if (!whole) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int tok = tok0 + nt * 8 + 2 * t4, end = min(me.len, tok_end);
-                if (tok < me.lo || tok >= end) s[nt].x = -INFINITY;
-                if (tok + 1 < me.lo || tok + 1 >= end) s[nt].y = -INFINITY;
+            const bool there = lane < 2 * PPS && pg < pg1, ok = there && phys >= 0 && phys < p.NB;
+            const unsigned copies = __ballot_sync(kFull, ok), absent = __ballot_sync(kFull, there && !ok);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, __popc(copies) * Cfg::kPageBytes);
+                if (absent != 0) raise_error(p.err, PKV_DEVERR_BLOCK);
             }
-        }
+            bad = (bad & ~(((1u << PPS) - 1) << (st * PPS))) | ((absent & ((1u << PPS) - 1)) << (st * PPS));
+            __syncwarp();   // the expected bytes are announced before any copy
+            if (ok)
+                bulk_load(smem_addr(ring + st * Cfg::kStageBytes + lane * Cfg::kPageBytes),
+                          (lane < PPS ? P.kc : P.vc) + (static_cast<size_t>(phys) * p.Hkv + kvh) * Cfg::kPageBytes,
+                          Cfg::kPageBytes, bar);
+        };
+        int issued = min(kStages, n_my);
+        for (int k = 0; k < issued; ++k) issue(k);
 
-        // ---- the running reference: the rows' maxima and the largest V scale (lane: one key)
-        float mx = fmaxf(s[0].x, s[0].y);
-#pragma unroll
-        for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-        m_run = fmaxf(m_run, mx);
-        unsigned top = 0;   // positive f16 order like their bits
+        // ---- query fragments, while the copies fly.  MMA steps 2u (E) and 2u + 1 (O) of word u =
+        // gi * WPT + i: elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours' differences
+        float f, qsum[G];   // score (base 2) = MMA sum * f; the groups' sums of q in the MMAs' units
         {
-            uint32_t v[G];
-            lds_words<G>(vpages + (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes + (lane % BS) * G * 4, v);
+            const float *qrow = p.q + static_cast<size_t>(me.bi >= 0 ? me.bi : 0) * D;
+            float v[G * WPT][8], amax = 0.f;
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi) top = max(top, v[gi] & 0xffffu);
-            top = __reduce_max_sync(kFull, top);
-        }
-        if (top > vs_bits) {   // rarely after the first stage: the next power of two, E = its exponent
-            vs_bits = top;
-            const uint32_t v = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
-            vs_exp = static_cast<float>(static_cast<int>((v + 0x7fffffu) >> 23) - 127);
-        }
-        const float ref_new = m_run + (vs_exp - 14.f);
-        // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
-        const float base = ref_new == -INFINITY ? 0.f : ref_new;
-        const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
-        ref = ref_new;
-        float2 psum = make_float2(0.f, 0.f), w[NT];
+            for (int u = 0; u < G * WPT; ++u) {
+                const int word = (u / WPT) * (WORDS / G) + t4 * WPT + u % WPT;
+                const float2 *src = reinterpret_cast<const float2 *>(qrow + 8 * word);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float2 e = add2(s[nt], make_float2(-base, -base));
-            w[nt] = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            psum = add2(psum, w[nt]);
-        }
-        l_run = l_run * alpha + (psum.x + psum.y);
-        if (__any_sync(kFull, alpha != 1.f)) {
-            const float alpha_a = __shfl_sync(kFull, alpha, 8 * t4);
-            const float alpha_b = __shfl_sync(kFull, alpha, 8 * t4 + 4);
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                oT[mt][0] *= alpha_a;
-                oT[mt][1] *= alpha_b;
-                oT[mt][2] *= alpha_a;
-                oT[mt][3] *= alpha_b;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
+                    v[u][2 * e] = y.x;
+                    v[u][2 * e + 1] = y.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+                }
             }
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
-        }
-
-        // ---- O^T += V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit units
-        // (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1 in
-        // one register: the pairs along the keys that the A operand wants
-        const uint32_t vrow = smem_addr(vpages) + (lane & 15) * (D / 2) + (lane >> 4) * 16;
-#pragma unroll
-        for (int kt = 0; kt < kStageKeys / 16; ++kt) {
-            const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2);
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+            // |q| * 2^up in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
+            const int up = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
+            const float scale = pow2i(up);
+            f = (p.scale_log2 * 0x1p24f) * pow2i(-up);
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
-                uint32_t bh0, bl0, bh1, bl1;
-                {
-                    const uint32_t *par = reinterpret_cast<const uint32_t *>(vpages + (kt * 16 / BS) * Cfg::kPageBytes + Cfg::kCodeBytes) +
-                                          (kt * 16 % BS + 2 * t4) * G + gi;
-                    const float2 p0 = par_of(par[0]), p1 = par_of(par[G]), p2 = par_of(par[8 * G]), p3 = par_of(par[9 * G]);
-                    const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
-                    split2(mul2(wa, make_float2(p0.x, p1.x)), bh0, bl0);
-                    split2(mul2(wb, make_float2(p2.x, p3.x)), bh1, bl1);
-                    zo[gi] = fma2(wa, make_float2(p0.y, p1.y), fma2(wb, make_float2(p2.y, p3.y), zo[gi]));
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < WPT; ++i) {
+                    const int u = gi * WPT + i;
+                    uint4 e, o;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[u][j] *= scale;
+                        sum += v[u][j];
+                    }
+#pragma unroll
+                    for (int j = 1; j < 8; j += 2) v[u][j] = fmaf(v[u][j], 0.0625f, -v[u][j - 1]);
+                    split2(v[u][0], v[u][4], e.x, e.y);
+                    split2(v[u][2], v[u][6], e.z, e.w);
+                    split2(v[u][1], v[u][5], o.x, o.y);
+                    split2(v[u][3], v[u][7], o.z, o.w);
+                    qfrag[(2 * u) * 32] = e;
+                    qfrag[(2 * u + 1) * 32] = o;
+                }
+                sum += __shfl_xor_sync(kFull, sum, 1);
+                sum += __shfl_xor_sync(kFull, sum, 2);
+                qsum[gi] = sum * 0x1p-24f;
+            }
+        }
+
+        float oT[D / 16][4];
+        float2 zo[G];   // sums of weight * zero over this lane's keys
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) oT[mt][0] = oT[mt][1] = oT[mt][2] = oT[mt][3] = 0.f;
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) zo[gi] = make_float2(0.f, 0.f);
+        float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
+        float ref = -INFINITY;                  // m_run + E - 14
+        float vs_max = 0.f, vs_exp = -24.f;     // the largest V scale seen; E, its exponent rounded up
+
+        int k = 0;
+        for (; k < n_my; ++k) {
+            const int st = (cnt + k) % kStages;
+            const bool arrived = mbar_wait_bounded(smem_addr(&bars[st]), ((cnt + k) / kStages) & 1);
+            if (!__all_sync(kFull, arrived)) {
+                if (lane == 0) raise_error(p.err, PKV_DEVERR_TIMEOUT);
+                break;
+            }
+            const uint8_t *kpages = ring + st * Cfg::kStageBytes;
+            const uint8_t *vpages = kpages + PPS * Cfg::kPageBytes;
+            const int tok0 = (pg0 + (turn + k * turns) * PPS) * BS;
+            // does every row of the tile see every key of the stage?
+            const bool whole = tok0 >= t_last.lo && tok0 + kStageKeys <= min(t_first.len, tok_end);
+            // this lane's key: parameters of keys that no row sees (which may be anything) and of
+            // pages that are not there become 0; codes are finite whatever they are
+            const bool seen = tok0 + lane >= t_first.lo && tok0 + lane < min(t_last.len, tok_end) &&
+                              !(bad >> (st * PPS + lane / BS) & 1);
+            const int par_at = (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes + (lane % BS) * G * 4;
+            auto widen = [&](const uint8_t *pages) {
+                uint32_t v[G];
+                lds_words<G>(pages + par_at, v);
+                float top = 0.f;
+#pragma unroll
+                for (int gi = 0; gi < G; ++gi) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v[gi]));
+                    par[gi * 64 + lane] = seen ? y.x : 0.f;
+                    par[gi * 64 + 32 + lane] = seen ? y.y : 0.f;
+                    top = fmaxf(top, seen ? y.x : 0.f);
+                }
+                return top;
+            };
+
+            // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
+            widen(kpages);
+            __syncwarp();
+            float2 s[NT];
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) {
+                float a[NT][4];
+                uint32_t c[NT][WPT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
+                    lds_words<WPT>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + (nt * 8 % BS + g) * (D / 2) + gi * (D / 2 / G) +
+                                       t4 * WPT * 4,
+                                   c[nt]);
                 }
 #pragma unroll
-                for (int h = 0; h < HPG; h += 2) {
-                    // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
-                    const int c = gi * HPG + h;
-                    uint32_t v[4];
-                    if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
-                    else ldsm_x2_trans(rows - (lane >> 4) * 16 + c * 16, v[0], v[1]);
-                    constexpr int N = HPG >= 2 ? 2 : 1;
+                for (int i = 0; i < WPT; ++i) {
+                    const uint4 e = qfrag[(2 * (gi * WPT + i)) * 32], o = qfrag[(2 * (gi * WPT + i) + 1) * 32];
+                    uint32_t lo[NT], hi[NT];
+                    // the tiles' chains side by side
 #pragma unroll
-                    for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
-                        const uint32_t b0 = lo ? bl0 : bh0, b1 = lo ? bl1 : bh1;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        lo[nt] = c[nt][i] & 0x00ff00ffu;
+                        hi[nt] = __byte_perm(c[nt][i], 0, 0x4341);
+                        mma16(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
+                    }
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const uint32_t x = v[2 * i], y = v[2 * i + 1], x8 = x >> 8, y8 = y >> 8;
-                            const int mt = 2 * (c + i);
-                            mma16(oT[mt], x & 0x000f000fu, x8 & 0x000f000fu, y & 0x000f000fu, y8 & 0x000f000fu, b0, b1);
-                            mma16(oT[mt + 1], x & 0x00f000f0u, x8 & 0x00f000f0u, y & 0x00f000f0u, y8 & 0x00f000f0u, b0, b1);
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16(a[nt], o.x, o.y, o.z, o.w, lo[nt] & 0x00f000f0u, hi[nt] & 0x00f000f0u);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 sc = *reinterpret_cast<const float2 *>(par + gi * 64 + nt * 8 + 2 * t4);
+                    const float2 ze = *reinterpret_cast<const float2 *>(par + gi * 64 + 32 + nt * 8 + 2 * t4);
+                    const float2 qz = make_float2(qsum[gi], qsum[gi]);
+                    const float2 y = gi == 0 ? mul2(ze, qz) : fma2(ze, qz, s[nt]);
+                    s[nt] = fma2(sc, add2(make_float2(a[nt][0], a[nt][1]), make_float2(a[nt][2], a[nt][3])), y);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt] = mul2(s[nt], make_float2(f, f));
+            if (!whole) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int tok = tok0 + nt * 8 + 2 * t4, end = min(me.len, tok_end);
+                    if (tok < me.lo || tok >= end) s[nt].x = -INFINITY;
+                    if (tok + 1 < me.lo || tok + 1 >= end) s[nt].y = -INFINITY;
+                }
+            }
+            __syncwarp();   // K's parameters have been read
+
+            // ---- the running reference: the rows' maxima and the largest V scale
+            const float top = widen(vpages);
+            float mx = fmaxf(s[0].x, s[0].y);
+#pragma unroll
+            for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            m_run = fmaxf(m_run, mx);
+            if (__any_sync(kFull, top > vs_max)) {   // rarely after the first stage: the next power of two
+                // non-negative floats order like their bits
+                vs_max = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(top, vs_max))));
+                vs_exp = fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(vs_max) + 0x7fffffu) >> 23) - 127), -24.f);
+            }
+            const float ref_new = m_run + (vs_exp - 14.f);
+            // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
+            const float base = ref_new == -INFINITY ? 0.f : ref_new;
+            const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
+            ref = ref_new;
+            float2 psum = make_float2(0.f, 0.f), w[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 e = add2(s[nt], make_float2(-base, -base));
+                w[nt] = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                psum = add2(psum, w[nt]);
+            }
+            l_run = l_run * alpha + (psum.x + psum.y);
+            if (__any_sync(kFull, alpha != 1.f)) {
+                const float alpha_a = __shfl_sync(kFull, alpha, 8 * t4);
+                const float alpha_b = __shfl_sync(kFull, alpha, 8 * t4 + 4);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    oT[mt][0] *= alpha_a;
+                    oT[mt][1] *= alpha_b;
+                    oT[mt][2] *= alpha_a;
+                    oT[mt][3] *= alpha_b;
+                }
+#pragma unroll
+                for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
+            }
+            __syncwarp();   // V's parameters have been written
+
+            // ---- O^T += V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit units
+            // (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1
+            // in one register: the pairs along the keys that the A operand wants
+            const uint32_t vrow = smem_addr(vpages) + (lane & 15) * (D / 2) + (HPG >= 2 ? (lane >> 4) * 16 : 0);
+#pragma unroll
+            for (int kt = 0; kt < kStageKeys / 16; ++kt) {
+                const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2);
+#pragma unroll
+                for (int gi = 0; gi < G; ++gi) {
+                    uint32_t bh0, bl0, bh1, bl1;
+                    {
+                        const float *src = par + gi * 64 + kt * 16 + 2 * t4;
+                        const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
+                        split2(mul2(wa, *reinterpret_cast<const float2 *>(src)), bh0, bl0);
+                        split2(mul2(wb, *reinterpret_cast<const float2 *>(src + 8)), bh1, bl1);
+                        zo[gi] = fma2(wa, *reinterpret_cast<const float2 *>(src + 32),
+                                      fma2(wb, *reinterpret_cast<const float2 *>(src + 40), zo[gi]));
+                    }
+#pragma unroll
+                    for (int h = 0; h < HPG; h += 2) {
+                        // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
+                        constexpr int N = HPG >= 2 ? 2 : 1;
+                        const int c = gi * HPG + h;
+                        uint32_t v[4], hi[4];
+                        if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
+                        else ldsm_x2_trans(rows + c * 16, v[0], v[1]);
+#pragma unroll
+                        for (int i = 0; i < 2 * N; ++i) {
+                            hi[i] = __byte_perm(v[i], 0, 0x4341);
+                            v[i] &= 0x00ff00ffu;
+                        }
+#pragma unroll
+                        for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
+                            const uint32_t b0 = lo ? bl0 : bh0, b1 = lo ? bl1 : bh1;
+#pragma unroll
+                            for (int i = 0; i < N; ++i)
+                                mma16(oT[2 * (c + i)], v[2 * i], hi[2 * i], v[2 * i + 1], hi[2 * i + 1], b0, b1);
+#pragma unroll
+                            for (int i = 0; i < N; ++i)
+                                mma16(oT[2 * (c + i) + 1], v[2 * i] & 0x00f000f0u, hi[2 * i] & 0x00f000f0u,
+                                      v[2 * i + 1] & 0x00f000f0u, hi[2 * i + 1] & 0x00f000f0u, b0, b1);
                         }
                     }
                 }
             }
+            __syncwarp();
+            if (k + kStages < n_my) {
+                issue(k + kStages);
+                issued = k + kStages + 1;
+            }
         }
-        __syncwarp();
-        if (k + kStages < n_my) {
-            issue(k + kStages);
-            issued = k + kStages + 1;
+        const bool gave_up = k < n_my;
+        if (gave_up) {
+            // A copy did not arrive in time: wait (bounded) for the copies still in flight so that
+            // none lands after the block exits.
+            for (int kk = k; kk < issued; ++kk) mbar_wait_bounded(smem_addr(&bars[(cnt + kk) % kStages]), ((cnt + kk) / kStages) & 1);
         }
-    }
-    if (k < n_my) {
-        // A copy did not arrive in time: wait (bounded) for the copies still in flight so that
-        // none lands after the block exits.
-        for (int kk = k; kk < issued; ++kk)
-            mbar_wait_bounded(smem_addr(&bars[warp * kStages + kk % kStages]), (kk / kStages) & 1);
-    }
+        cnt += n_my;
 
-    l_run += __shfl_xor_sync(kFull, l_run, 1);
-    l_run += __shfl_xor_sync(kFull, l_run, 2);
+        l_run += __shfl_xor_sync(kFull, l_run, 1);
+        l_run += __shfl_xor_sync(kFull, l_run, 2);
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) {
-        zo[gi].x += zo[gi].y;
-        zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 1);
-        zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 2);
-    }
-
-    // ---- the warps' (ref, l, O) through shared memory (the ring is free now)
-    __syncthreads();
-    float *mw = reinterpret_cast<float *>(smem);
-    float *lw = mw + NW * 8;
-    float *ow = lw + NW * 8;
-    if (t4 == 0) {
-        mw[warp * 8 + g] = ref;
-        lw[warp * 8 + g] = l_run;
-    }
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi) {
-        const float za_ = __shfl_sync(kFull, zo[gi].x, 8 * t4), zb_ = __shfl_sync(kFull, zo[gi].x, 8 * t4 + 4);
-#pragma unroll
-        for (int h = 0; h < HPG; ++h) {
-            const int c = gi * HPG + h, dim = 32 * c + 4 * g, mt = 2 * c;
-            // even codes were c * 2^-24, odd ones c * 2^-20
-            float *oa = ow + (warp * 8 + 2 * t4) * D + dim, *ob = oa + D;
-            oa[0] = fmaf(oT[mt][0], 0x1p24f, za_);
-            oa[1] = fmaf(oT[mt + 1][0], 0x1p20f, za_);
-            oa[2] = fmaf(oT[mt][2], 0x1p24f, za_);
-            oa[3] = fmaf(oT[mt + 1][2], 0x1p20f, za_);
-            ob[0] = fmaf(oT[mt][1], 0x1p24f, zb_);
-            ob[1] = fmaf(oT[mt + 1][1], 0x1p20f, zb_);
-            ob[2] = fmaf(oT[mt][3], 0x1p24f, zb_);
-            ob[3] = fmaf(oT[mt + 1][3], 0x1p20f, zb_);
+        for (int gi = 0; gi < G; ++gi) {
+            zo[gi].x += zo[gi].y;
+            zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 1);
+            zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 2);
         }
+        // this lane's outputs of rows 2 * t4 + r: dimensions 32 * c + 4 * g + {0, 1, 2, 3}.  E sums are
+        // (even + 16 odd) * 2^-24, O sums 16 odd * 2^-24
+        auto outputs = [&](int c, int r) {
+            const float z = __shfl_sync(kFull, zo[c / HPG].x, 8 * t4 + 4 * r);
+            const float (&e)[4] = oT[2 * c], (&o)[4] = oT[2 * c + 1];
+            return make_float4(fmaf(e[r] - o[r], 0x1p24f, z), fmaf(o[r], 0x1p20f, z), fmaf(e[2 + r] - o[2 + r], 0x1p24f, z),
+                               fmaf(o[2 + r], 0x1p20f, z));
+        };
+
+        if (P.balanced) {
+            if (gave_up) return;   // lanes together; the block's other warps go on
+            const float inv = ref == -INFINITY ? 0.f : 1.f / l_run;   // no key of this part for the row
+            const float lse2 = ref == -INFINITY ? -INFINITY : ref + log2f(l_run);
+            if (t4 == 0 && me.bi >= 0) {
+                if (part.n > 1) p.ws_lse[part_at(part, g, part.own)] = lse2;
+                else if (p.lse != nullptr) p.lse[me.bi] = lse2 * kDecLn2;
+            }
+            if (t4 == 0 && me.bi < 0 && part.n > 1) p.ws_lse[part_at(part, g, part.own)] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float il = __shfl_sync(kFull, inv, 8 * t4 + 4 * r);
+                const int bi = __shfl_sync(kFull, me.bi, 8 * t4 + 4 * r);
+                float *dst = part.n > 1 ? p.ws_o + part_at(part, 2 * t4 + r, part.own) * D
+                                        : p.out + static_cast<size_t>(max(bi, 0)) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const float4 y = outputs(c, r);
+                    if (part.n > 1 || bi >= 0)
+                        *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(y.x * il, y.y * il, y.z * il, y.w * il);
+                }
+            }
+            if (part.n > 1) {
+                __threadfence();
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    last = atomicAdd(part.counter, 1u) + 1 == static_cast<unsigned>(part.n);
+                    if (last) *part.counter = 0u;   // every part of this call has arrived
+                }
+                if (__shfl_sync(kFull, last, 0)) {
+                    __threadfence();
+                    merge_unit<D>(P, me, part, lane);
+                }
+            }
+            continue;
+        }
+
+        // ---- the warps' (ref, l, O) through shared memory (the ring is free now)
+        if (__syncthreads_or(gave_up)) return;
+        float *mw = reinterpret_cast<float *>(smem);
+        float *lw = mw + NW * 8;
+        float *ow = lw + NW * 8;
+        if (t4 == 0) {
+            mw[warp * 8 + g] = ref;
+            lw[warp * 8 + g] = l_run;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+                *reinterpret_cast<float4 *>(ow + (warp * 8 + 2 * t4 + r) * D + 32 * c + 4 * g) = outputs(c, r);
+        __syncthreads();
+        finish_rows<D, NW>(smem, P, s_rows, part);
     }
-    __syncthreads();
-    finish_rows<D, NW>(smem, P, s_rows, (b * p.Hkv + kvh) * p.head_tiles + tile, split,
-                       (sq.pages + p.chunk_pages - 1) / p.chunk_pages);
 }
 
 template <int D, int BS, int G>
@@ -881,6 +1064,17 @@ size_t partial_bytes(long long rows, int Hq, int splits, int d) {
 
 }  // namespace
 
+namespace {
+int q4_blocks_per_sm(int d, int bs, int G) {
+    if (bs == 16) {
+        if (d == 64) return G == 1 ? MmaCfg<64, 16, 1>::kBlocksPerSm : MmaCfg<64, 16, 2>::kBlocksPerSm;
+        return G == 1 ? MmaCfg<128, 16, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 16, 2>::kBlocksPerSm : MmaCfg<128, 16, 4>::kBlocksPerSm;
+    }
+    if (d == 64) return G == 1 ? MmaCfg<64, 32, 1>::kBlocksPerSm : MmaCfg<64, 32, 2>::kBlocksPerSm;
+    return G == 1 ? MmaCfg<128, 32, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 32, 2>::kBlocksPerSm : MmaCfg<128, 32, 4>::kBlocksPerSm;
+}
+}  // namespace
+
 Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int group, int bs, int pages,
                       int num_splits, int sm_count, bool aligned) {
     Q4Plan plan{};
@@ -893,11 +1087,15 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     if (num_splits > 1) {
         chunk = (pages + num_splits - 1) / num_splits;
     } else if (num_splits == 0 && plan.mma) {
-        // about two waves of the CTAs an SM holds, chunks of at least 256 keys; and none of more
-        // than 8192, so that a long sequence among short ones spreads
-        const int least = 256 / bs, most = 8192 / bs;
-        while (chunk > least && units * ((pages + chunk - 1) / chunk) < 8ll * sms) chunk = (chunk + 1) / 2;
-        if (chunk > most) chunk = (pages + (pages + most - 1) / most - 1) / ((pages + most - 1) / most);
+        // An equal share for every warp the device holds at once, unless the units are so few that
+        // one would be left to merge parts from many warps: then, or with more sequences than a
+        // block scans, equal chunks for one wave of blocks and a merge over many blocks.
+        plan.blocks = q4_blocks_per_sm(d, bs, d / group) * sms;
+        plan.balanced = B <= kMaxBalanced && plan.blocks * kMmaWarps <= 24 * units &&
+                        units * (static_cast<long long>(pages) * bs / kStageKeys + 1) < (1ll << 30);
+        const int least = 256 / bs;
+        const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
+        chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
     } else if (num_splits == 0) {
         // one warp per (row, head, chunk): several warps for each scheduler, no chunk shorter
         // than 128 keys
@@ -907,6 +1105,11 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
     plan.chunk_pages = std::max(chunk, 1);
     plan.splits = (pages + plan.chunk_pages - 1) / plan.chunk_pages;
+    if (plan.balanced) {
+        plan.splits = 1;   // the parts' number is known on the device only
+        plan.workspace_bytes = PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(plan.blocks) * kMmaWarps * 2 * 8 * (d + 1) * sizeof(float);
+        return plan;
+    }
     plan.fused_merge = plan.mma && plan.splits > 1 && plan.splits <= kFusedMergeMaxChunks &&
                        units <= static_cast<long long>(PKV_DECODE_COUNTER_BYTES / sizeof(unsigned));
     plan.workspace_bytes = partial_bytes(rows, Hq, plan.splits, d);
@@ -934,16 +1137,18 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
     kp.scale_log2 = a.scale * kDecLog2e;
     kp.window = a.window;
     kp.cu_q = a.cu_q;
-    if (plan.splits > 1) {
+    if (plan.workspace_bytes > 0) {
         uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+        const size_t parts = plan.balanced ? static_cast<size_t>(plan.blocks) * kMmaWarps * 2 * 8
+                                           : static_cast<size_t>(a.rows) * a.Hq * plan.splits;
         kp.ws_o = reinterpret_cast<float *>(ws + PKV_DECODE_COUNTER_BYTES);
-        kp.ws_lse = kp.ws_o + static_cast<size_t>(a.rows) * a.Hq * plan.splits * a.d;
+        kp.ws_lse = kp.ws_o + parts * a.d;
     }
     cudaError_t e;
     if (plan.mma) {
         AttendQ4Params P{};
         kp.head_tiles = plan.tiles;
-        if (plan.fused_merge) kp.counters = static_cast<unsigned *>(a.workspace);
+        if (plan.fused_merge || plan.balanced) kp.counters = static_cast<unsigned *>(a.workspace);
         if (a.new_slots != nullptr) {
             kp.k_new = a.k_new;
             kp.v_new = a.v_new;
@@ -955,7 +1160,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         P.vc = const_cast<uint8_t *>(a.v_cache);
         P.rows = a.rows;
         P.max_q = a.max_q;
-        const dim3 grid(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
+        P.balanced = plan.balanced;
+        const dim3 grid = plan.balanced ? dim3(plan.blocks) : dim3(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
         e = launch_mma(P, a.d, a.bs, a.d / a.group, grid, stream);
     } else {
         e = launch_simt(a, kp, stream);

@@ -136,6 +136,8 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 struct Q4Plan {
     bool mma;            // d 64 or 128, bs 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
     int tiles;           // its tiles of eight (query row, head) pairs per sequence and KV head
+    bool balanced;       // even shares of all sequences' keys for `blocks` thread blocks
+    int blocks;
     bool fused_merge;    // the last chunk of a unit merges (counters in the workspace)
     int splits;          // chunks per sequence at most (1: one pass, no workspace)
     int chunk_pages;     // blocks per chunk
