@@ -17,12 +17,30 @@
 namespace pkv {
 namespace {
 
+// n / d for 0 <= n < 2^31 by a multiplication: mul = ceil(2^(31 + s) / d), s = ceil(log2 d), is off
+// by less than d <= 2^s over 2^(31 + s), which n < 2^31 cannot make visible.
+struct FastDiv {
+    uint32_t d, mul;
+    int shift;   // s - 1; -1: d is 1
+};
+FastDiv fast_div(uint32_t d) {
+    int s = 0;
+    while ((1ull << s) < d) ++s;
+    return {d, static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv &f) {
+    return f.shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), f.mul) >> f.shift);
+}
+
+// 64-bit divisions would cost as much as the rest: words are numbered in 32 bits (a launch takes
+// fewer than 2^31), and slots too unless the cache holds more than 2^31 of them.
 struct Q4Rows {
     const int64_t *slots;
-    long long words;     // 8-element words of K (and as many of V): T * Hkv * d / 8
+    int words;           // 8-element words of K (and as many of V): T * Hkv * d / 8
     int Hkv, row_words;  // d / 8
     int lanes;           // lanes that share a group: group / 8
     int bs, page_bytes;  // bs * row bytes
+    FastDiv by_row, by_head, by_bs;
     long long n_slots;
     unsigned *err;
 };
@@ -33,18 +51,17 @@ struct Q4Place {
     long long slot, page;
     int off, j;
 };
-__device__ __forceinline__ Q4Place q4_place(const Q4Rows &r, long long w) {
+__device__ __forceinline__ Q4Place q4_place(const Q4Rows &r, int w) {
     Q4Place a;
-    a.j = static_cast<int>(w % r.row_words);
-    const long long th = w / r.row_words;   // t * Hkv + h
-    const int h = static_cast<int>(th % r.Hkv);
-    const long long t = th / r.Hkv;
+    const int th = div_by(w, r.by_row);   // t * Hkv + h
+    a.j = w - th * r.row_words;
+    const int t = div_by(th, r.by_head), h = th - t * r.Hkv;
     a.slot = __ldg(r.slots + t);
     if (a.slot >= r.n_slots) {
         if (h == 0 && a.j == 0) raise_error(r.err, PKV_DEVERR_SLOT);
         a.slot = -1;
     }
-    const long long blk = a.slot / r.bs;
+    const long long blk = r.n_slots <= 0x7fffffffll ? div_by(static_cast<int>(max(a.slot, 0ll)), r.by_bs) : max(a.slot, 0ll) / r.bs;
     a.off = static_cast<int>(a.slot - blk * r.bs);
     a.page = (blk * r.Hkv + h) * r.page_bytes;
     return a;
@@ -58,16 +75,18 @@ __global__ void __launch_bounds__(256)
     // whole warps run each turn: the group's lanes exchange their extremes
     for (long long w0 = blockIdx.x * static_cast<long long>(blockDim.x) + (threadIdx.x & ~31); w0 < r.words;
          w0 += stride) {
-        const long long w = w0 + (threadIdx.x & 31);
-        const bool live = w < r.words;
-        const Q4Place a = q4_place(r, live ? w : r.words - 1);
+        const int w = static_cast<int>(w0) + static_cast<int>(threadIdx.x & 31);
+        const Q4Place a = q4_place(r, min(w, r.words - 1));
+        const bool live = w < r.words && a.slot >= 0;
+        __half2 pars[2];
+        uint32_t codes[2];
+        codes[0] = q4_quantise_at<VEC>(live ? k_new + static_cast<size_t>(w) * 8 : nullptr, r.lanes, pars[0]);
+        codes[1] = q4_quantise_at<VEC>(live ? v_new + static_cast<size_t>(w) * 8 : nullptr, r.lanes, pars[1]);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            float x[8] = {};
-            if (live) q4_load8<T, VEC>((side ? v_new : k_new) + w * 8, x);
-            __half2 par;
-            const uint32_t code = q4_quantise8(x, r.lanes, par);
-            if (!live || a.slot < 0) continue;
+            const uint32_t code = codes[side];
+            const __half2 par = pars[side];
+            if (!live) continue;
             uint8_t *page = (side ? vc : kc) + a.page;
             reinterpret_cast<uint32_t *>(page)[a.off * r.row_words + a.j] = code;
             if (a.j % r.lanes == 0)
@@ -82,21 +101,39 @@ __global__ void __launch_bounds__(256)
     kv_gather_q4_kernel(T *__restrict__ k_out, T *__restrict__ v_out, const uint8_t *__restrict__ kc,
                         const uint8_t *__restrict__ vc, const Q4Rows r) {
     const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long w = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; w < r.words; w += stride) {
+    for (long long w0 = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; w0 < r.words; w0 += stride) {
+        const int w = static_cast<int>(w0);
         const Q4Place a = q4_place(r, w);
+        uint32_t code[2] = {0, 0};
+        __half2 par[2];
+        par[0] = par[1] = __floats2half2_rn(0.f, 0.f);
+        if (a.slot >= 0) {
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const uint8_t *page = (side ? vc : kc) + a.page;
+                code[side] = __ldg(reinterpret_cast<const uint32_t *>(page) + a.off * r.row_words + a.j);
+                par[side] = __ldg(reinterpret_cast<const __half2 *>(page + r.bs * r.row_words * 4) +
+                                  a.off * (r.row_words / r.lanes) + a.j / r.lanes);
+            }
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            float x[8] = {};
-            if (a.slot >= 0) {
-                const uint8_t *page = (side ? vc : kc) + a.page;
-                const uint32_t code = __ldg(reinterpret_cast<const uint32_t *>(page) + a.off * r.row_words + a.j);
-                const float2 p = __half22float2(
-                    __ldg(reinterpret_cast<const __half2 *>(page + r.bs * r.row_words * 4) +
-                          a.off * (r.row_words / r.lanes) + a.j / r.lanes));
+            // A code in the low bits of an f16 is the subnormal code * 2^-24, four bits further up
+            // code * 2^-20: widened to fp32 exactly, the power of two goes into the scale.
+            const float2 p = __half22float2(par[side]);
+            const float s0 = p.x * 0x1p24f, s1 = p.x * 0x1p20f;
+            float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, static_cast<float>((code >> (4 * i)) & 15u), p.y);
+            for (int i = 0; i < 2; ++i) {   // elements 2i, 2i + 4 and 2i + 1, 2i + 5
+                const uint32_t u = code[side] >> (8 * i), lo = u & 0x000f000fu, hi = u & 0x00f000f0u;
+                const float2 a0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+                const float2 a1 = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                x[2 * i] = fmaf(s0, a0.x, p.y);
+                x[2 * i + 4] = fmaf(s0, a0.y, p.y);
+                x[2 * i + 1] = fmaf(s1, a1.x, p.y);
+                x[2 * i + 5] = fmaf(s1, a1.y, p.y);
             }
-            T *dst = (side ? v_out : k_out) + w * 8;
+            T *dst = (side ? v_out : k_out) + static_cast<size_t>(w) * 8;
             if constexpr (sizeof(T) == 2) {
                 // the fp32 value (one rounding of zero + scale * code) rounded to bf16
                 uint32_t u[4];
@@ -123,7 +160,10 @@ __global__ void __launch_bounds__(256)
 Q4Rows rows_of(const int64_t *slots, int T, int Hkv, int d, int group, int bs, int NB, unsigned *err) {
     Q4Rows r;
     r.slots = slots;
-    r.words = static_cast<long long>(T) * Hkv * (d / 8);
+    r.words = T * Hkv * (d / 8);
+    r.by_row = fast_div(d / 8);
+    r.by_head = fast_div(Hkv);
+    r.by_bs = fast_div(bs);
     r.Hkv = Hkv;
     r.row_words = d / 8;
     r.lanes = group / 8;
@@ -133,6 +173,9 @@ Q4Rows rows_of(const int64_t *slots, int T, int Hkv, int d, int group, int bs, i
     r.err = err;
     return r;
 }
+
+// Tokens of one launch: fewer than 2^31 words (Hkv * d / 8 is below 2^21).
+int tokens_per_launch(int Hkv, int d) { return std::max(1, (0x7fffffff - 256) / (Hkv * (d / 8))); }
 
 unsigned grid_of(long long words, int sm_count) {
     return static_cast<unsigned>(std::min<long long>((words + 255) / 256, 8ll * sm_count));
@@ -148,6 +191,15 @@ cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype 
                                 uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d, int group,
                                 int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
+    if (const int most = tokens_per_launch(Hkv, d); T > most) {
+        const size_t skip = static_cast<size_t>(most) * Hkv * d * (new_dt == PKV_BF16 ? 2 : 4);
+        const cudaError_t e = launch_kv_append_q4(k_new, v_new, new_dt, k_cache, v_cache, slot_mapping, most, Hkv, d, group,
+                                                  bs, NB, sm_count, err, stream);
+        if (e != cudaSuccess) return e;
+        return launch_kv_append_q4(static_cast<const uint8_t *>(k_new) + skip, static_cast<const uint8_t *>(v_new) + skip,
+                                   new_dt, k_cache, v_cache, slot_mapping + most, T - most, Hkv, d, group, bs, NB, sm_count,
+                                   err, stream);
+    }
     const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
     const unsigned grid = grid_of(r.words, sm_count);
     const bool vec = aligned(k_new, v_new, 16);
@@ -169,6 +221,15 @@ cudaError_t launch_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, cons
                                 const uint8_t *v_cache, const int64_t *slot_mapping, int T, int Hkv, int d,
                                 int group, int bs, int NB, int sm_count, unsigned *err, cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
+    if (const int most = tokens_per_launch(Hkv, d); T > most) {
+        const size_t skip = static_cast<size_t>(most) * Hkv * d * (out_dt == PKV_BF16 ? 2 : 4);
+        const cudaError_t e = launch_kv_gather_q4(k_out, v_out, out_dt, k_cache, v_cache, slot_mapping, most, Hkv, d, group,
+                                                  bs, NB, sm_count, err, stream);
+        if (e != cudaSuccess) return e;
+        return launch_kv_gather_q4(static_cast<uint8_t *>(k_out) + skip, static_cast<uint8_t *>(v_out) + skip, out_dt,
+                                   k_cache, v_cache, slot_mapping + most, T - most, Hkv, d, group, bs, NB, sm_count, err,
+                                   stream);
+    }
     const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
     const unsigned grid = grid_of(r.words, sm_count);
     const bool vec = aligned(k_out, v_out, 16);

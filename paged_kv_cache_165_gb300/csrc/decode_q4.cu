@@ -220,6 +220,15 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with C = 0, so that no registers are cleared first.
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x.x.
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x.x, x.y);
@@ -475,13 +484,11 @@ __device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, in
                                               int side, int lane) {
     constexpr int WORDS = D / 8, LANES = WORDS / G;
     const size_t src = (static_cast<size_t>(b) * p.k.Hkv + kvh) * D + lane * 8;
-    float x[8] = {};
-    if (lane < WORDS) {
-        if (p.new_bf16) q4_load8<__nv_bfloat16, false>(static_cast<const __nv_bfloat16 *>(side ? p.k.v_new : p.k.k_new) + src, x);
-        else q4_load8<float, false>(static_cast<const float *>(side ? p.k.v_new : p.k.k_new) + src, x);
-    }
+    const void *rows = side ? p.k.v_new : p.k.k_new;
     __half2 par;
-    const uint32_t code = q4_quantise8(x, LANES, par);
+    uint32_t code;
+    if (p.new_bf16) code = q4_quantise_at<false>(lane < WORDS ? static_cast<const __nv_bfloat16 *>(rows) + src : nullptr, LANES, par);
+    else code = q4_quantise_at<false>(lane < WORDS ? static_cast<const float *>(rows) + src : nullptr, LANES, par);
     if (lane >= WORDS) return;
     uint8_t *page = (side ? p.vc : p.kc) + row_page;
     reinterpret_cast<uint32_t *>(page)[off * WORDS + lane] = code;
@@ -801,7 +808,6 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                 uint32_t c[NT][WPT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
                     lds_words<WPT>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + (nt * 8 % BS + g) * (D / 2) + gi * (D / 2 / G) +
                                        t4 * WPT * 4,
                                    c[nt]);
@@ -815,7 +821,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                     for (int nt = 0; nt < NT; ++nt) {
                         lo[nt] = c[nt][i] & 0x00ff00ffu;
                         hi[nt] = __byte_perm(c[nt][i], 0, 0x4341);
-                        mma16(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
+                        if (i == 0) mma16_first(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
+                        else mma16(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -906,13 +913,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                         // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
                         constexpr int N = HPG >= 2 ? 2 : 1;
                         const int c = gi * HPG + h;
-                        uint32_t v[4], hi[4];
+                        uint32_t v[4], hi[4], vo[4], ho[4];
                         if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
                         else ldsm_x2_trans(rows + c * 16, v[0], v[1]);
 #pragma unroll
                         for (int i = 0; i < 2 * N; ++i) {
                             hi[i] = __byte_perm(v[i], 0, 0x4341);
                             v[i] &= 0x00ff00ffu;
+                            vo[i] = v[i] & 0x00f000f0u;
+                            ho[i] = hi[i] & 0x00f000f0u;
                         }
 #pragma unroll
                         for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
@@ -922,8 +931,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                                 mma16(oT[2 * (c + i)], v[2 * i], hi[2 * i], v[2 * i + 1], hi[2 * i + 1], b0, b1);
 #pragma unroll
                             for (int i = 0; i < N; ++i)
-                                mma16(oT[2 * (c + i) + 1], v[2 * i] & 0x00f000f0u, hi[2 * i] & 0x00f000f0u,
-                                      v[2 * i + 1] & 0x00f000f0u, hi[2 * i + 1] & 0x00f000f0u, b0, b1);
+                                mma16(oT[2 * (c + i) + 1], vo[2 * i], ho[2 * i], vo[2 * i + 1], ho[2 * i + 1], b0, b1);
                         }
                     }
                 }

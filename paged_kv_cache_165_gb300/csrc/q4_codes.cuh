@@ -13,15 +13,17 @@
 //   scale = fp16((max x - zero) / 15) rounded to nearest,
 //   code = clamp(round half to even((x - zero) / scale), 0, 15), 0 where scale is 0,
 // every quotient exact before its one rounding.  The kernels compute in fp32, whose error
-// could move a quotient across a rounding boundary: a quotient closer to a boundary than
-// that error is decided in fp64, where the comparison is exact (fp64 is slow on this part,
-// and about one element in 10^5 gets there).  A group that holds a NaN stores zero = NaN,
-// scale 0 and codes 0, so every value read back from it is NaN.
+// could move a quotient across a rounding boundary: one that comes closer to a boundary than
+// that error is decided by q4_side, exactly (bf16 rows sit on a lattice: ties are common, about
+// one element in a thousand).  A group that holds a NaN stores zero = NaN, scale 0 and codes 0,
+// so every value read back from it is NaN.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+
+#include "common.cuh"
 
 namespace pkv {
 
@@ -29,95 +31,159 @@ constexpr float kQ4Max = 65504.f;   // fp16's largest finite value
 
 __host__ __device__ constexpr int q4_row_bytes(int d, int group) { return d / 2 + 4 * (d / group); }
 
+// The sign of (x - z) - c for c near x - z, c a number of at most 16 bits, exactly: the difference d
+// of x and z in fp32 and its error e (Knuth's two-sum); d - c is exact (c is within a factor of two
+// of d) and, when it is not 0, a multiple of d's last place, which |e| stays below.
+__device__ __forceinline__ float q4_side(float x, float z, float c) {
+    const float d = x - z, y = d - x;
+    const float r = d - c;
+    return r != 0.f ? r : (x - (d - y)) + (-z - y);
+}
+
 // Scale of a group: fp16 nearest to (hi - zero) / 15.  The fp32 quotient is within 2^-22 of
-// the exact one; unless both ends of that interval round to the same fp16 the exact quotient
+// the exact one; unless both ends of a wider interval round to the same fp16 the exact quotient
 // is compared with the value halfway between the two candidates.
 __device__ __forceinline__ __half q4_scale(float hi, __half zero) {
-    const float z = __half2float(zero);
-    const float r = (hi - z) * (1.f / 15.f);
-    const __half a = __float2half_rn(r * (1.f - 0x1p-21f)), b = __float2half_rn(r * (1.f + 0x1p-21f));
-    if (__half_as_ushort(a) == __half_as_ushort(b)) return a;
-    const double exact = static_cast<double>(hi) - static_cast<double>(z);   // 24- and 11-bit terms
-    const double mid = 0.5 * (static_cast<double>(__half2float(a)) + static_cast<double>(__half2float(b)));
-    const double cut = 15.0 * mid;
-    if (exact != cut) return exact < cut ? a : b;
-    return (__half_as_ushort(a) & 1) == 0 ? a : b;
-}
-
-// Code of x (already clamped, x >= zero) for scale s > 0 with inv = 1 / s in fp32.
-__device__ __forceinline__ uint32_t q4_code(float x, float z, float s, float inv) {
-    const float t = (x - z) * inv;
-    float k = rintf(t);
-    if (fabsf(t - k) > 0.5f - 1e-5f) {   // fp32 may be on the wrong side of k +- 1/2
-        const float lo = floorf(t);
-        const double edge = (static_cast<double>(lo) + 0.5) * static_cast<double>(s);   // exact
-        const double dx = static_cast<double>(x) - static_cast<double>(z);
-        if (dx != edge) k = dx > edge ? lo + 1.f : lo;
-        else k = (static_cast<int>(lo) & 1) ? lo + 1.f : lo;
+    const float z = __half2float(zero), r = (hi - z) * (1.f / 15.f);
+    __half a = __float2half_rn(r * (1.f - 0x1p-21f));
+    const __half b = __float2half_rn(r * (1.f + 0x1p-21f));
+    if (__half_as_ushort(a) != __half_as_ushort(b)) {
+        const float side = q4_side(hi, z, 7.5f * (__half2float(a) + __half2float(b)));
+        if (side > 0.f || (side == 0.f && (__half_as_ushort(a) & 1))) a = b;
     }
-    return static_cast<uint32_t>(fminf(fmaxf(k, 0.f), 15.f));
+    return a;
 }
 
-// Eight consecutive elements of a group spread over `lanes` consecutive lanes of the warp
-// (4, 8 or 16: group / 8), every lane of the warp taking part.  Returns the lane's eight codes
-// (element i in bits 4i .. 4i+3) and the group's (scale, zero).
-__device__ __forceinline__ uint32_t q4_quantise8(const float (&in)[8], int lanes, __half2 &par) {
-    float x[8];
-    float lo = INFINITY, hi = -INFINITY;
-    bool nan = false;
+__device__ __forceinline__ float q4_min_nan(float a, float b) {   // NaN if either is
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// The least and the largest of a group spread over `lanes` consecutive lanes (4, 8 or 16), each with
+// eight elements; lo is NaN if an element is.
+__device__ __forceinline__ void q4_extremes(const float (&x)[8], int lanes, float &lo, float &hi) {
+    lo = hi = x[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        nan |= in[i] != in[i];
-        x[i] = fminf(fmaxf(in[i], -kQ4Max), kQ4Max);
-        lo = fminf(lo, x[i]);
+    for (int i = 1; i < 8; ++i) {
+        lo = q4_min_nan(lo, x[i]);
         hi = fmaxf(hi, x[i]);
     }
-    if (nan) lo = -INFINITY;   // below every clamped value: marks the group
-    for (int sh = lanes >> 1; sh > 0; sh >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, sh));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, sh));
+#pragma unroll
+    for (int sh = 8; sh > 0; sh >>= 1) {
+        if (sh < lanes) {
+            lo = q4_min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, sh));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, sh));
+        }
     }
-    if (lo == -INFINITY) {
+}
+// The same of bf16 elements, two to a word: pairs at a time, then (lo, -hi) in one word.
+__device__ __forceinline__ void q4_extremes(const uint32_t (&w)[4], int lanes, float &lo, float &hi) {
+    auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+    auto bits = [](__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); };
+    const uint32_t least = bits(__hmin2_nan(__hmin2_nan(bf(w[0]), bf(w[1])), __hmin2_nan(bf(w[2]), bf(w[3]))));
+    const uint32_t most = bits(__hmax2_nan(__hmax2_nan(bf(w[0]), bf(w[1])), __hmax2_nan(bf(w[2]), bf(w[3])))) ^ 0x80008000u;
+    uint32_t m = bits(__hmin2_nan(bf(__byte_perm(least, most, 0x5410)), bf(__byte_perm(least, most, 0x7632))));
+#pragma unroll
+    for (int sh = 8; sh > 0; sh >>= 1)
+        if (sh < lanes) m = bits(__hmin2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, sh))));
+    lo = __uint_as_float(m << 16);
+    hi = -__uint_as_float(m & 0xffff0000u);
+}
+
+// Eight consecutive elements of a group with extremes lo and hi: returns their codes (element i in
+// bits 4i .. 4i+3) and the group's (scale, zero).  Quotients are rounded by adding and taking away
+// 1.5 * 2^23 and packed as fp32 integers, four codes (below 2^16) at a time.
+__device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float hi, __half2 &par) {
+    if (lo != lo) {
         par = __halves2half2(__ushort_as_half(0), __ushort_as_half(0x7fff));
         return 0;
+    }
+    if (lo < -kQ4Max || hi > kQ4Max) {
+        lo = fminf(fmaxf(lo, -kQ4Max), kQ4Max);
+        hi = fminf(fmaxf(hi, -kQ4Max), kQ4Max);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kQ4Max), kQ4Max);
     }
     const __half zero = __float2half_rd(lo);
     const __half scale = q4_scale(hi, zero);
     par = __halves2half2(scale, zero);
     const float s = __half2float(scale), z = __half2float(zero);
     if (!(s > 0.f)) return 0;
-    const float inv = 1.f / s;
-    uint32_t w = 0;
+    if (s < 0x1p-14f) {
+        // a subnormal scale may be rounded by more than a part in 2^11: quotients can pass 15.5
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= q4_code(x[i], z, s, inv) << (4 * i);
-    return w;
+        for (int i = 0; i < 8; ++i) x[i] = fminf(x[i], fmaf(15.f, s, z));
+    }
+    float inv;   // within 2^-23, quotients within 2^-22 (4e-6 at 16)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    constexpr float kMagic = 12582912.f;
+    const float2 mz = make_float2(-z, -z), up = make_float2(kMagic, kMagic), down = make_float2(-kMagic, -kMagic);
+    float k[8], worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 d = add2(make_float2(x[i], x[i + 1]), mz);
+        const float2 t = make_float2(d.x * inv, d.y * inv);   // never below 0
+        const float2 r = add2(add2(t, up), down);
+        const float2 off = add2(t, make_float2(-r.x, -r.y));
+        worst = fmaxf(worst, fmaxf(fabsf(off.x), fabsf(off.y)));
+        k[i] = r.x;
+        k[i + 1] = r.y;
+    }
+    if (worst > 0.5f - 1e-5f) {   // fp32 may be on the wrong side of a boundary
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = (x[i] - z) * inv, n = floorf(t);
+            const float side = q4_side(x[i], z, (n + 0.5f) * s);
+            const float odd = n - 2.f * floorf(n * 0.5f);   // ties to the even code
+            const float e = n + (side > 0.f ? 1.f : side < 0.f ? 0.f : odd);
+            if (fabsf(t - k[i]) > 0.5f - 1e-5f) k[i] = e;
+        }
+    }
+    const float a = fmaf(fmaf(fmaf(k[3], 16.f, k[2]), 16.f, k[1]), 16.f, k[0]);
+    const float b = fmaf(fmaf(fmaf(k[7], 16.f, k[6]), 16.f, k[5]), 16.f, k[4]);
+    // the integers below 2^16 stand in the low halves of a + 2^23 and b + 2^23
+    return __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
 }
 
-template <typename T>
-__device__ __forceinline__ float q4_in(T x);
-template <>
-__device__ __forceinline__ float q4_in<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float q4_in<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Eight elements from p (16-byte loads where the caller has checked the alignment).
-template <typename T, bool VEC>
-__device__ __forceinline__ void q4_load8(const T *p, float (&x)[8]) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight elements at p with their group's extremes and codes; every lane of the warp takes part,
+// those whose p is null with a row of zeros.  VEC: p is on a 16-byte boundary.
+template <bool VEC>
+__device__ __forceinline__ uint32_t q4_quantise_at(const __nv_bfloat16 *p, int lanes, __half2 &par) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (p != nullptr) {
+        if constexpr (VEC) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+            const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // a bf16 is the top half of an fp32
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < 4; ++i) w[i] = q[2 * i] | static_cast<uint32_t>(q[2 * i + 1]) << 16;
         }
-    } else if constexpr (VEC) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = q4_in(p[i]);
     }
+    float lo, hi, x[8];
+    q4_extremes(w, lanes, lo, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // a bf16 is the top half of an fp32
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return q4_quantise8(x, lo, hi, par);
+}
+template <bool VEC>
+__device__ __forceinline__ uint32_t q4_quantise_at(const float *p, int lanes, __half2 &par) {
+    float lo, hi, x[8] = {};
+    if (p != nullptr) {
+        if constexpr (VEC) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = p[i];
+        }
+    }
+    q4_extremes(x, lanes, lo, hi);
+    return q4_quantise8(x, lo, hi, par);
 }
 
 }  // namespace pkv
