@@ -8,6 +8,7 @@ the library's kernels; there is no fallback when the library is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -141,19 +142,27 @@ def _check(status: int) -> None:
         raise PkvError(status, lib().pkv_last_error().decode(errors="replace"))
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The current stream's handle without the Stream object around it, which costs microseconds to make.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _cuda(name, t, dtype=None):
+    if type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -538,6 +547,7 @@ def decode_step_fp8_kernel_launches(B, Hq, Hkv, d, bs, MBS, NB, new_dtype=torch.
 
 # ----------------------------------------------------------------- 4-bit cache
 
+@functools.lru_cache(maxsize=None)
 def q4_row_bytes(d, group) -> int:
     """Bytes of one row of a 4-bit cache (codes and its share of the page's parameters): the
     last dimension of k_cache and v_cache, uint8 [NB][Hkv][bs][q4_row_bytes(d, group)]."""
@@ -550,10 +560,11 @@ def q4_row_bytes(d, group) -> int:
 def _q4_caches(what, k_cache, v_cache, d, group):
     _cuda("k_cache", k_cache, torch.uint8)
     _cuda("v_cache", v_cache, torch.uint8)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q4_row_bytes(d, group):
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or shape[3] != q4_row_bytes(d, group):
         raise ValueError(f"{what}: the caches must be [NB][Hkv][bs][{q4_row_bytes(d, group)}] (q4_row_bytes of d={d}, "
-                         f"group={group}), got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    return k_cache.shape[:3]
+                         f"group={group}), got {tuple(shape)} and {tuple(v_cache.shape)}")
+    return shape[:3]
 
 
 def _q4_rows(what, fn, k_rows, v_rows, k_cache, v_cache, slot_mapping, group, stream):
