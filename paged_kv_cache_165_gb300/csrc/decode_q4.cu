@@ -11,40 +11,14 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.cuh"
-#include "decode_kparams.cuh"
-#include "internal.h"
-#include "q4_codes.cuh"
+#include "decode_q4.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-struct AttendQ4Params {
-    DecodeKParams k;     // head_tiles: tiles of eight (query row, head) pairs per sequence and KV head
-    uint8_t *kc, *vc;
-    int rows, max_q;     // query rows of the call, and of a sequence at most
-    int new_bf16;        // type of the step's new rows
-    int balanced;        // the thread blocks share all sequences' keys evenly (else grid (splits x tiles, Hkv, B))
-};
-
-constexpr int kMaxBalanced = 1024;   // sequences of a balanced launch
 constexpr int kLeastSteps = 4;       // 32-key steps that a warp of one takes at least (128 keys)
-
-template <typename Kernel>
-cudaError_t set_smem_once(Kernel kernel, int bytes, std::atomic<unsigned long long> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(done.load() & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit);
-    }
-    return cudaSuccess;
-}
 
 // ================================================================ CUDA-core path
 
@@ -229,108 +203,9 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// x ~= hi + lo, hi = rn_f16(x), lo = rn_f16(x - hi); the low half holds x.x.
-__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(x.x, x.y);
-    const float2 f = __half22float2(h);
-    const float2 r = add2(x, make_float2(-f.x, -f.y));
-    const __half2 l = __floats2half2_rn(r.x, r.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    split2(make_float2(x0, x1), hi, lo);
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\t"
-        "mov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 __device__ __forceinline__ void ldsm_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
-
-// 2^e as a float, e clamped to the normal range.
-__device__ __forceinline__ float pow2i(int e) {
-    return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
-}
-
-// A sequence's query rows r0 .. r0 + nq - 1 (checked), its length L and the pages [first, first +
-// pages) that any of them sees; rows [z0, z1) see nothing and are written as out = 0, lse = -inf.
-struct SeqRows {
-    int r0, nq, L, first, pages, z0, z1, z2, z3;
-    bool ok;
-};
-
-__device__ __forceinline__ SeqRows seq_rows(const AttendQ4Params &P, int b, int bs, bool report) {
-    const DecodeKParams &p = P.k;
-    SeqRows s{};
-    s.L = checked_len(p, b, bs, report);
-    s.ok = true;
-    if (p.cu_q == nullptr) {
-        s.r0 = b;
-        s.nq = 1;
-        if (s.L == 0) s.z0 = b, s.z1 = b + 1;
-    } else {
-        const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
-        s.r0 = c0;
-        s.nq = c1 - c0;
-        s.ok = c0 >= 0 && c1 >= c0 && c1 <= P.rows && s.nq <= s.L && s.nq <= P.max_q;
-        if (!s.ok) s.z0 = min(max(c0, 0), P.rows), s.z1 = min(max(c1, 0), P.rows);
-        // rows before the first sequence or behind the last one belong to none
-        if (b == 0 && c0 > 0) s.z2 = 0, s.z3 = min(c0, P.rows);
-        if (b == p.B - 1 && c1 < P.rows) s.z2 = max(c1, 0), s.z3 = P.rows;
-        if (report && (!s.ok || s.z3 > s.z2)) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
-    }
-    s.first = p.window > 0 ? max(0, s.L - s.nq + 1 - p.window) / bs : 0;
-    s.pages = s.L > 0 && s.ok ? (s.L + bs - 1) / bs - s.first : 0;
-    return s;
-}
-
-__device__ __forceinline__ void clear_rows(const AttendQ4Params &P, const SeqRows &s, int kvh, int d) {
-    const DecodeKParams &p = P.k;
-    for (int part = 0; part < 2; ++part) {
-        const int z0 = part ? s.z2 : s.z0, z1 = part ? s.z3 : s.z1;
-        for (int r = z0; r < z1; ++r) {
-            const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
-            for (int i = threadIdx.x; i < p.m * d; i += blockDim.x) p.out[at * d + i] = 0.f;
-            if (p.lse != nullptr)
-                for (int i = threadIdx.x; i < p.m; i += blockDim.x) p.lse[at + i] = -INFINITY;
-        }
-    }
-}
-
-// Row v of a tile's (query row, head) pairs: head kvh * m + v % m of the sequence's query row
-// v / m, which sees tokens [lo, len).  A row past the sequence's last repeats that one's span,
-// with bi = -1.
-struct RowSpan {
-    int bi;        // (query row) * Hq + head
-    int lo, len;
-};
-__device__ __forceinline__ RowSpan tile_row(const AttendQ4Params &P, const SeqRows &s, int kvh, int v) {
-    const DecodeKParams &p = P.k;
-    const int i = min(v / p.m, s.nq - 1);
-    RowSpan r;
-    r.len = s.L - s.nq + i + 1;
-    r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
-    r.bi = v < s.nq * p.m ? (s.r0 + i) * p.Hq + kvh * p.m + v % p.m : -1;
-    return r;
-}
-
-// The parts of a unit (the rows of a tile over ranges of its keys).
-struct Parts {
-    int first;   // balanced: the warp that holds part 0; warp first + i holds part i
-    int own, n;  // this part and their number
-    unsigned *counter;
-};
 
 // The warps' states of a tile's eight rows, in shared memory ([NW][8] references and sums, then
 // [NW][8][D] outputs), merged and written: the result where the unit has one part, else this
@@ -1081,26 +956,33 @@ int q4_blocks_per_sm(int d, int bs, int G) {
     if (d == 64) return G == 1 ? MmaCfg<64, 32, 1>::kBlocksPerSm : MmaCfg<64, 32, 2>::kBlocksPerSm;
     return G == 1 ? MmaCfg<128, 32, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 32, 2>::kBlocksPerSm : MmaCfg<128, 32, 4>::kBlocksPerSm;
 }
+// Rows of partial results of a balanced launch: two units for every warp or block.
+size_t balanced_rows(const Q4Plan &plan) {
+    return static_cast<size_t>(plan.blocks) * 2 * (plan.umma ? kQ4UmmaSlots : kMmaWarps * 8);
+}
 }  // namespace
 
 Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int group, int bs, int pages,
                       int num_splits, int sm_count, bool aligned) {
     Q4Plan plan{};
     const int m = Hq / Hkv, sms = std::max(sm_count, 1);
-    const long long tiles = (static_cast<long long>(max_q) * m + 7) / 8;
-    plan.mma = (d == 64 || d == 128) && (bs == 16 || bs == 32) && d / group <= 4 && aligned && tiles < (1 << 18);
-    plan.tiles = plan.mma ? static_cast<int>(tiles) : 1;
-    const long long units = plan.mma ? static_cast<long long>(B) * Hkv * tiles : static_cast<long long>(rows) * Hq;
+    const long long slots = static_cast<long long>(max_q) * m;
+    plan.umma = q4_umma_shape(d, group, bs) && aligned && slots > 8 && slots < (1 << 20);
+    plan.mma = !plan.umma && (d == 64 || d == 128) && (bs == 16 || bs == 32) && d / group <= 4 && aligned && slots < (1 << 20);
+    const int per_tile = plan.umma ? kQ4UmmaSlots : 8;
+    plan.tiles = plan.umma || plan.mma ? static_cast<int>((slots + per_tile - 1) / per_tile) : 1;
+    const long long units = plan.umma || plan.mma ? static_cast<long long>(B) * Hkv * plan.tiles : static_cast<long long>(rows) * Hq;
     int chunk = pages;
     if (num_splits > 1) {
         chunk = (pages + num_splits - 1) / num_splits;
-    } else if (num_splits == 0 && plan.mma) {
-        // An equal share for every warp the device holds at once, unless the units are so few that
-        // one would be left to merge parts from many warps: then, or with more sequences than a
+    } else if (num_splits == 0 && (plan.umma || plan.mma)) {
+        // An equal share for every warp (umma: block) the device holds at once, unless the units are
+        // so few that one would be left to merge parts from many: then, or with more sequences than a
         // block scans, equal chunks for one wave of blocks and a merge over many blocks.
-        plan.blocks = q4_blocks_per_sm(d, bs, d / group) * sms;
-        plan.balanced = B <= kMaxBalanced && plan.blocks * kMmaWarps <= 24 * units &&
-                        units * (static_cast<long long>(pages) * bs / kStageKeys + 1) < (1ll << 30);
+        const int step = plan.umma ? 128 / (d / group) : kStageKeys;
+        plan.blocks = plan.umma ? sms : q4_blocks_per_sm(d, bs, d / group) * sms;
+        plan.balanced = B <= kMaxBalanced && (plan.umma ? plan.blocks <= 8 * units : plan.blocks * kMmaWarps <= 24 * units) &&
+                        units * (static_cast<long long>(pages) * bs / step + 1) < (1ll << 30);
         const int least = 256 / bs;
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
         chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
@@ -1111,11 +993,15 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         while (chunk > least && units * ((pages + chunk - 1) / chunk) < 32ll * sms) chunk = (chunk + 1) / 2;
     }
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
+    if (plan.umma) {   // whole key tiles
+        const int per = 128 / (d / group) / bs;
+        chunk = (chunk + per - 1) / per * per;
+    }
     plan.chunk_pages = std::max(chunk, 1);
     plan.splits = (pages + plan.chunk_pages - 1) / plan.chunk_pages;
     if (plan.balanced) {
         plan.splits = 1;   // the parts' number is known on the device only
-        plan.workspace_bytes = PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(plan.blocks) * kMmaWarps * 2 * 8 * (d + 1) * sizeof(float);
+        plan.workspace_bytes = PKV_DECODE_COUNTER_BYTES + balanced_rows(plan) * (d + 1) * sizeof(float);
         return plan;
     }
     plan.fused_merge = plan.mma && plan.splits > 1 && plan.splits <= kFusedMergeMaxChunks &&
@@ -1147,13 +1033,13 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
     kp.cu_q = a.cu_q;
     if (plan.workspace_bytes > 0) {
         uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-        const size_t parts = plan.balanced ? static_cast<size_t>(plan.blocks) * kMmaWarps * 2 * 8
+        const size_t parts = plan.balanced ? balanced_rows(plan)
                                            : static_cast<size_t>(a.rows) * a.Hq * plan.splits;
         kp.ws_o = reinterpret_cast<float *>(ws + PKV_DECODE_COUNTER_BYTES);
         kp.ws_lse = kp.ws_o + parts * a.d;
     }
     cudaError_t e;
-    if (plan.mma) {
+    if (plan.mma || plan.umma) {
         AttendQ4Params P{};
         kp.head_tiles = plan.tiles;
         if (plan.fused_merge || plan.balanced) kp.counters = static_cast<unsigned *>(a.workspace);
@@ -1170,7 +1056,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         P.max_q = a.max_q;
         P.balanced = plan.balanced;
         const dim3 grid = plan.balanced ? dim3(plan.blocks) : dim3(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
-        e = launch_mma(P, a.d, a.bs, a.d / a.group, grid, stream);
+        e = plan.umma ? launch_attend_q4_umma(P, a.d, a.bs, a.d / a.group, grid, stream)
+                      : launch_mma(P, a.d, a.bs, a.d / a.group, grid, stream);
     } else {
         e = launch_simt(a, kp, stream);
     }

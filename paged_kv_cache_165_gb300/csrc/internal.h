@@ -134,8 +134,9 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 // ------------------------------------------------- attention over a 4-bit cache
 
 struct Q4Plan {
+    bool umma;           // more than 8 (query row, head) pairs per sequence and KV head: the tcgen05 kernel
     bool mma;            // d 64 or 128, bs 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
-    int tiles;           // its tiles of eight (query row, head) pairs per sequence and KV head
+    int tiles;           // tiles of 64 (umma) or 8 pairs per sequence and KV head
     bool balanced;       // even shares of all sequences' keys for `blocks` thread blocks
     int blocks;
     bool fused_merge;    // the last chunk of a unit merges (counters in the workspace)
