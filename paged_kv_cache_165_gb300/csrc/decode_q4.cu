@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(128)
 //     in shared memory; a few chunks merge in place, many in decode_merge_kernel.
 
 constexpr int kMmaWarps = 4, kStageKeys = 32, kStages = 2;
+constexpr int kUnitCost = 3;   // a unit's start (queries, first copies, its part written) in 32-key steps
 
 template <int D, int BS, int G>
 struct MmaCfg {
@@ -180,8 +181,10 @@ struct MmaCfg {
     static constexpr int kParBytes = G * 2 * kStageKeys * 4;
     static constexpr int kBarOff = kParOff + kMmaWarps * kParBytes;
     static constexpr int kSmemBytes = kBarOff + kMmaWarps * kStages * 8;
-    // 228 KB of shared memory less 1 KB a block: four blocks per SM where they fit
-    static constexpr int kBlocksPerSm = kSmemBytes + 512 <= 56 * 1024 ? 4 : 3;
+    // Three blocks (12 warps, 168 registers a thread) against four (128, with spills): 70B-shaped step
+    // 91.4 against 94.2 us, MHA step 76.4 against 79.0, four sequences of 131072 tokens 142 against 139.
+    static constexpr int kBlocksPerSm = 3;
+    static_assert(kBlocksPerSm * (kSmemBytes + 2048) <= 228 * 1024, "three blocks fit an SM");
     static_assert(kPageBytes % 16 == 0, "bulk copies");
 };
 
@@ -397,9 +400,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
     int cnt = 0;        // stages this warp has consumed
     unsigned bad = 0;   // bit (stage * PPS + page): a page to be read as zeros
 
-    // ---- balanced: this warp's share [x, x1) of the steps of all units.  Warps are as many as fit
-    // the device at once; fewer when that would leave them less than kLeastSteps each, but one for
-    // every unit.  They are numbered so that neighbours lie in different blocks.
+    // ---- balanced: this warp's share [x, x1) of the steps of all units, each unit kUnitCost steps
+    // longer than its keys for its start.  Warps are as many as fit the device at once; fewer when
+    // that would leave them less than kLeastSteps each, but one for every unit.  They are numbered so
+    // that neighbours lie in different blocks.
     const int wid = warp * gridDim.x + blockIdx.x;
     int x = 0, x1 = 1, Q = 1, warps = 1, b = 0, unit = 0, step = 0;
     if (P.balanced) {
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         for (int i = first; i < min(p.B, first + per); ++i) {
             const SeqRows sq = seq_rows(P, i, BS, false);
             const int n = sq.pages > 0 ? p.Hkv * ((sq.nq * p.m + 7) / 8) : 0;
-            pre[i + 1] = n * ((sq.pages + PPS - 1) / PPS);
+            pre[i + 1] = n * ((sq.pages + PPS - 1) / PPS + kUnitCost);
             steps += pre[i + 1];
             units += n;
         }
@@ -441,9 +445,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             if (b + st < p.B && pre[b + st] <= x) b += st;
         if (x < x1) {
             const SeqRows sq = seq_rows(P, b, BS, false);
-            const int len = (sq.pages + PPS - 1) / PPS;
-            unit = (x - pre[b]) / len;
-            step = (x - pre[b]) - unit * len;
+            const int span = (sq.pages + PPS - 1) / PPS + kUnitCost;
+            unit = (x - pre[b]) / span;
+            step = (x - pre[b]) - unit * span;
         }
         // rows that see nothing, bad lengths and rows
         for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
@@ -462,27 +466,29 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         SeqRows sq;
         if (P.balanced) {
             sq = seq_rows(P, b, BS, false);
-            int len = (sq.pages + PPS - 1) / PPS, units = p.Hkv * ((sq.nq * p.m + 7) / 8);
+            int units = p.Hkv * ((sq.nq * p.m + 7) / 8);
             while (sq.pages == 0 || unit == units) {   // on to the next sequence that has keys
                 ++b;
                 unit = 0;
                 sq = seq_rows(P, b, BS, false);
-                len = (sq.pages + PPS - 1) / PPS;
                 units = p.Hkv * ((sq.nq * p.m + 7) / 8);
             }
             kvh = unit % p.Hkv;
             tile = unit / p.Hkv;
-            const int end = min(len, step + (x1 - x)), start = x - step;
-            c0 = sq.first + step * PPS;
-            c1 = min(sq.first + sq.pages, sq.first + end * PPS);
-            // the warp whose share holds position y is ((y + 1) * warps - 1) / Q
-            part.first = static_cast<int>(((start + 1ll) * warps - 1) / Q);
-            part.n = static_cast<int>((static_cast<long long>(start + len) * warps - 1) / Q) - part.first + 1;
-            part.own = wid - part.first;
-            part.counter = p.counters + part.first;   // at most one unit goes on from a warp into the next
+            // positions [step, end) of the unit's span, the first kUnitCost of which hold no keys
+            const int len = (sq.pages + PPS - 1) / PPS, end = min(len + kUnitCost, step + (x1 - x));
+            const int first = x - step + kUnitCost;   // the position of the unit's first keys
+            c0 = sq.first + max(0, step - kUnitCost) * PPS;
+            c1 = min(sq.first + sq.pages, sq.first + max(0, end - kUnitCost) * PPS);
             x += end - step;
             step = 0;
             ++unit;
+            if (c0 >= c1) continue;   // the share ends before the unit's keys
+            // the warp whose share holds position y is ((y + 1) * warps - 1) / Q
+            part.first = static_cast<int>(((first + 1ll) * warps - 1) / Q);
+            part.n = static_cast<int>((static_cast<long long>(first + len) * warps - 1) / Q) - part.first + 1;
+            part.own = wid - part.first;
+            part.counter = p.counters + part.first;   // at most one unit goes on from a warp into the next
         } else {
             tile = blockIdx.x % p.head_tiles;
             const int split = blockIdx.x / p.head_tiles;
@@ -531,6 +537,20 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             if (turns > 1) __syncthreads();
             else __syncwarp();
             fence_proxy_async_global();
+        }
+
+        // the queries' loads start before the block table's
+        float qv[G * WPT][8];
+#pragma unroll
+        for (int u = 0; u < G * WPT; ++u) {
+            const float2 *src = reinterpret_cast<const float2 *>(p.q + static_cast<size_t>(max(me.bi, 0)) * D +
+                                                                 8 * ((u / WPT) * (WORDS / G) + t4 * WPT + u % WPT));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
+                qv[u][2 * e] = y.x;
+                qv[u][2 * e + 1] = y.y;
+            }
         }
 
         // ---- this warp's stages: steps of PPS pages turn, turn + turns, ... of [pg0, pg1)
@@ -584,20 +604,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         // gi * WPT + i: elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours' differences
         float f, qsum[G];   // score (base 2) = MMA sum * f; the groups' sums of q in the MMAs' units
         {
-            const float *qrow = p.q + static_cast<size_t>(me.bi >= 0 ? me.bi : 0) * D;
-            float v[G * WPT][8], amax = 0.f;
+            float(&v)[G * WPT][8] = qv, amax = 0.f;
 #pragma unroll
-            for (int u = 0; u < G * WPT; ++u) {
-                const int word = (u / WPT) * (WORDS / G) + t4 * WPT + u % WPT;
-                const float2 *src = reinterpret_cast<const float2 *>(qrow + 8 * word);
+            for (int u = 0; u < G * WPT; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
-                    v[u][2 * e] = y.x;
-                    v[u][2 * e + 1] = y.y;
-                    amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
-                }
-            }
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[u][e]));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
             // |q| * 2^up in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
@@ -956,6 +967,13 @@ int q4_blocks_per_sm(int d, int bs, int G) {
     if (d == 64) return G == 1 ? MmaCfg<64, 32, 1>::kBlocksPerSm : MmaCfg<64, 32, 2>::kBlocksPerSm;
     return G == 1 ? MmaCfg<128, 32, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 32, 2>::kBlocksPerSm : MmaCfg<128, 32, 4>::kBlocksPerSm;
 }
+// (Query row, head) pairs of a sequence and KV head that the warp-MMA kernel, which takes eight at a
+// time, is faster for than the tcgen05 kernel, whose time hardly depends on them: 4 x 65536 tokens, one
+// scale group a row: 24 pairs 34.6 against 33.0 us, 32 44.2 against 33.2; 64 x 2048 tokens, four KV
+// heads: 61.9 against 71.9 and 76.1 against 74.3.  Two groups: 32 pairs 44.9 against 45.8, 40 53.7
+// against 46.1 (4 x 65536), 79.4 against 99.5 and 95.5 against 101.8 (64 x 2048).
+int q4_mma_slots(int G) { return G == 1 ? 24 : 40; }
+
 // Rows of partial results of a balanced launch: two units for every warp or block.
 size_t balanced_rows(const Q4Plan &plan) {
     return static_cast<size_t>(plan.blocks) * 2 * (plan.umma ? kQ4UmmaSlots : kMmaWarps * 8);
@@ -967,7 +985,7 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     Q4Plan plan{};
     const int m = Hq / Hkv, sms = std::max(sm_count, 1);
     const long long slots = static_cast<long long>(max_q) * m;
-    plan.umma = q4_umma_shape(d, group, bs) && aligned && slots > 8 && slots < (1 << 20);
+    plan.umma = q4_umma_shape(d, group, bs) && aligned && slots > q4_mma_slots(d / group) && slots < (1 << 20);
     plan.mma = !plan.umma && (d == 64 || d == 128) && (bs == 16 || bs == 32) && d / group <= 4 && aligned && slots < (1 << 20);
     const int per_tile = plan.umma ? kQ4UmmaSlots : 8;
     plan.tiles = plan.umma || plan.mma ? static_cast<int>((slots + per_tile - 1) / per_tile) : 1;
@@ -982,7 +1000,7 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         const int step = plan.umma ? 128 / (d / group) : kStageKeys;
         plan.blocks = plan.umma ? sms : q4_blocks_per_sm(d, bs, d / group) * sms;
         plan.balanced = B <= kMaxBalanced && (plan.umma ? plan.blocks <= 8 * units : plan.blocks * kMmaWarps <= 24 * units) &&
-                        units * (static_cast<long long>(pages) * bs / step + 1) < (1ll << 30);
+                        units * (static_cast<long long>(pages) * bs / step + 1 + kUnitCost) < (1ll << 30);
         const int least = 256 / bs;
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
         chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
