@@ -67,7 +67,7 @@ __device__ __forceinline__ Q4Place q4_place(const Q4Rows &r, int w) {
     return a;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int LANES>
 __global__ void __launch_bounds__(256)
     kv_append_q4_kernel(const T *__restrict__ k_new, const T *__restrict__ v_new, uint8_t *__restrict__ kc,
                         uint8_t *__restrict__ vc, const Q4Rows r) {
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(256)
         const bool live = w < r.words && a.slot >= 0;
         __half2 pars[2];
         uint32_t codes[2];
-        codes[0] = q4_quantise_at<VEC>(live ? k_new + static_cast<size_t>(w) * 8 : nullptr, r.lanes, pars[0]);
-        codes[1] = q4_quantise_at<VEC>(live ? v_new + static_cast<size_t>(w) * 8 : nullptr, r.lanes, pars[1]);
+        codes[0] = q4_quantise_at<VEC, LANES>(live ? k_new + static_cast<size_t>(w) * 8 : nullptr, pars[0]);
+        codes[1] = q4_quantise_at<VEC, LANES>(live ? v_new + static_cast<size_t>(w) * 8 : nullptr, pars[1]);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             const uint32_t code = codes[side];
@@ -89,9 +89,8 @@ __global__ void __launch_bounds__(256)
             if (!live) continue;
             uint8_t *page = (side ? vc : kc) + a.page;
             reinterpret_cast<uint32_t *>(page)[a.off * r.row_words + a.j] = code;
-            if (a.j % r.lanes == 0)
-                reinterpret_cast<__half2 *>(page + r.bs * r.row_words * 4)[a.off * (r.row_words / r.lanes) +
-                                                                            a.j / r.lanes] = par;
+            if (a.j % LANES == 0)
+                reinterpret_cast<__half2 *>(page + r.bs * r.row_words * 4)[a.off * (r.row_words / LANES) + a.j / LANES] = par;
         }
     }
 }
@@ -203,16 +202,23 @@ cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype 
     const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
     const unsigned grid = grid_of(r.words, sm_count);
     const bool vec = aligned(k_new, v_new, 16);
-#define PKV_Q4_APPEND(TT, VV)                                                                        \
-    kv_append_q4_kernel<TT, VV><<<grid, 256, 0, stream>>>(static_cast<const TT *>(k_new),            \
-                                                          static_cast<const TT *>(v_new), k_cache, v_cache, r)
-    if (new_dt == PKV_BF16) {
-        if (vec) PKV_Q4_APPEND(__nv_bfloat16, true);
-        else PKV_Q4_APPEND(__nv_bfloat16, false);
-    } else {
-        if (vec) PKV_Q4_APPEND(float, true);
-        else PKV_Q4_APPEND(float, false);
+#define PKV_Q4_APPEND(TT, VV, LL)                                                                     \
+    kv_append_q4_kernel<TT, VV, LL><<<grid, 256, 0, stream>>>(static_cast<const TT *>(k_new),         \
+                                                              static_cast<const TT *>(v_new), k_cache, v_cache, r)
+#define PKV_Q4_APPEND_L(TT, VV)                       \
+    switch (r.lanes) {                                \
+        case 4: PKV_Q4_APPEND(TT, VV, 4); break;      \
+        case 8: PKV_Q4_APPEND(TT, VV, 8); break;      \
+        default: PKV_Q4_APPEND(TT, VV, 16); break;    \
     }
+    if (new_dt == PKV_BF16) {
+        if (vec) PKV_Q4_APPEND_L(__nv_bfloat16, true)
+        else PKV_Q4_APPEND_L(__nv_bfloat16, false)
+    } else {
+        if (vec) PKV_Q4_APPEND_L(float, true)
+        else PKV_Q4_APPEND_L(float, false)
+    }
+#undef PKV_Q4_APPEND_L
 #undef PKV_Q4_APPEND
     return cudaGetLastError();
 }

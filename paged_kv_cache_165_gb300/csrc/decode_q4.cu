@@ -365,8 +365,8 @@ __device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, in
     const void *rows = side ? p.k.v_new : p.k.k_new;
     __half2 par;
     uint32_t code;
-    if (p.new_bf16) code = q4_quantise_at<false>(lane < WORDS ? static_cast<const __nv_bfloat16 *>(rows) + src : nullptr, LANES, par);
-    else code = q4_quantise_at<false>(lane < WORDS ? static_cast<const float *>(rows) + src : nullptr, LANES, par);
+    if (p.new_bf16) code = q4_quantise_at<false, LANES>(lane < WORDS ? static_cast<const __nv_bfloat16 *>(rows) + src : nullptr, par);
+    else code = q4_quantise_at<false, LANES>(lane < WORDS ? static_cast<const float *>(rows) + src : nullptr, par);
     if (lane >= WORDS) return;
     uint8_t *page = (side ? p.vc : p.kc) + row_page;
     reinterpret_cast<uint32_t *>(page)[off * WORDS + lane] = code;

@@ -12,11 +12,14 @@
 //   zero = fp16(min x) rounded towards -inf, so that no element lies below it,
 //   scale = fp16((max x - zero) / 15) rounded to nearest,
 //   code = clamp(round half to even((x - zero) / scale), 0, 15), 0 where scale is 0,
-// every quotient exact before its one rounding.  The kernels compute in fp32, whose error
-// could move a quotient across a rounding boundary: one that comes closer to a boundary than
-// that error is decided by q4_side, exactly (bf16 rows sit on a lattice: ties are common, about
-// one element in a thousand).  A group that holds a NaN stores zero = NaN, scale 0 and codes 0,
-// so every value read back from it is NaN.
+// every quotient exact before its one rounding.  The kernels compute in fp32: with d = x - zero
+// exact and the quotient t = d / scale correctly rounded (a reciprocal and a quotient refined by
+// their exact remainders, after Markstein), t is k + 1/2 only where the exact quotient is, and
+// never on the other side of it: the boundary p = (k + 1/2) scale has 16 bits, d != p differ by
+// at least d's last place, and that is more than half of t's last place away from k + 1/2.  Where
+// d is not exact its error decides a t of k + 1/2 (bf16 rows sit on a lattice: ties are common,
+// about one element in a thousand).  A group that holds a NaN stores zero = NaN, scale 0 and
+// codes 0, so every value read back from it is NaN.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -60,9 +63,10 @@ __device__ __forceinline__ float q4_min_nan(float a, float b) {   // NaN if eith
     return d;
 }
 
-// The least and the largest of a group spread over `lanes` consecutive lanes (4, 8 or 16), each with
+// The least and the largest of a group spread over LANES consecutive lanes (4, 8 or 16), each with
 // eight elements; lo is NaN if an element is.
-__device__ __forceinline__ void q4_extremes(const float (&x)[8], int lanes, float &lo, float &hi) {
+template <int LANES>
+__device__ __forceinline__ void q4_extremes(const float (&x)[8], float &lo, float &hi) {
     lo = hi = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
@@ -70,30 +74,29 @@ __device__ __forceinline__ void q4_extremes(const float (&x)[8], int lanes, floa
         hi = fmaxf(hi, x[i]);
     }
 #pragma unroll
-    for (int sh = 8; sh > 0; sh >>= 1) {
-        if (sh < lanes) {
-            lo = q4_min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, sh));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, sh));
-        }
+    for (int sh = LANES / 2; sh > 0; sh >>= 1) {
+        lo = q4_min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, sh));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, sh));
     }
 }
 // The same of bf16 elements, two to a word: pairs at a time, then (lo, -hi) in one word.
-__device__ __forceinline__ void q4_extremes(const uint32_t (&w)[4], int lanes, float &lo, float &hi) {
+template <int LANES>
+__device__ __forceinline__ void q4_extremes(const uint32_t (&w)[4], float &lo, float &hi) {
     auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
     auto bits = [](__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); };
     const uint32_t least = bits(__hmin2_nan(__hmin2_nan(bf(w[0]), bf(w[1])), __hmin2_nan(bf(w[2]), bf(w[3]))));
     const uint32_t most = bits(__hmax2_nan(__hmax2_nan(bf(w[0]), bf(w[1])), __hmax2_nan(bf(w[2]), bf(w[3])))) ^ 0x80008000u;
     uint32_t m = bits(__hmin2_nan(bf(__byte_perm(least, most, 0x5410)), bf(__byte_perm(least, most, 0x7632))));
 #pragma unroll
-    for (int sh = 8; sh > 0; sh >>= 1)
-        if (sh < lanes) m = bits(__hmin2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, sh))));
+    for (int sh = LANES / 2; sh > 0; sh >>= 1) m = bits(__hmin2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, sh))));
     lo = __uint_as_float(m << 16);
     hi = -__uint_as_float(m & 0xffff0000u);
 }
 
-// Eight consecutive elements of a group with extremes lo and hi: returns their codes (element i in
+// Eight consecutive elements of a group with extremes lo and hi (BF16: they are bf16 values): their codes (element i in
 // bits 4i .. 4i+3) and the group's (scale, zero).  Quotients are rounded by adding and taking away
 // 1.5 * 2^23 and packed as fp32 integers, four codes (below 2^16) at a time.
+template <bool BF16>
 __device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float hi, __half2 &par) {
     if (lo != lo) {
         par = __halves2half2(__ushort_as_half(0), __ushort_as_half(0x7fff));
@@ -115,29 +118,38 @@ __device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float 
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fminf(x[i], fmaf(15.f, s, z));
     }
-    float inv;   // within 2^-23, quotients within 2^-22 (4e-6 at 16)
+    float inv;   // 1 / s, correctly rounded: one Newton step from within a last place, checked for all 11-bit s
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = fmaf(inv, fmaf(-s, inv, 1.f), inv);
     constexpr float kMagic = 12582912.f;
-    const float2 mz = make_float2(-z, -z), up = make_float2(kMagic, kMagic), down = make_float2(-kMagic, -kMagic);
-    float k[8], worst = 0.f;
+    const float2 mz = make_float2(-z, -z), ms = make_float2(-s, -s), i2 = make_float2(inv, inv);
+    const float2 up = make_float2(kMagic, kMagic), down = make_float2(-kMagic, -kMagic);
+    float k[8], off[8], worst = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const float2 d = add2(make_float2(x[i], x[i + 1]), mz);
-        const float2 t = make_float2(d.x * inv, d.y * inv);   // never below 0
+        const float2 d = add2(make_float2(x[i], x[i + 1]), mz);   // never below 0
+        const float2 q = make_float2(d.x * inv, d.y * inv);
+        const float2 t = fma2(fma2(q, ms, d), i2, q);
         const float2 r = add2(add2(t, up), down);
-        const float2 off = add2(t, make_float2(-r.x, -r.y));
-        worst = fmaxf(worst, fmaxf(fabsf(off.x), fabsf(off.y)));
-        k[i] = r.x;
-        k[i + 1] = r.y;
+        const float2 o = add2(t, make_float2(-r.x, -r.y));
+        worst = fmaxf(worst, fmaxf(fabsf(o.x), fabsf(o.y)));
+        k[i] = r.x, k[i + 1] = r.y;
+        off[i] = o.x, off[i + 1] = o.y;
     }
-    if (worst > 0.5f - 1e-5f) {   // fp32 may be on the wrong side of a boundary
+    bool inexact = worst == 0.5f;   // a tie in fp32: the error of x - z, where there is one, decides
+    if (BF16 && inexact) {
+        // 8- and 11-bit terms: exact unless one of them lies far below the difference
+        float least = INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) least = fminf(least, x[i] != 0.f ? fabsf(x[i]) : INFINITY);
+        inexact = least < s * 0x1p-9f || (z != 0.f && fabsf(z) < s * 0x1p-7f);   // differences are below 16 s
+    }
+    if (inexact) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float t = (x[i] - z) * inv, n = floorf(t);
-            const float side = q4_side(x[i], z, (n + 0.5f) * s);
-            const float odd = n - 2.f * floorf(n * 0.5f);   // ties to the even code
-            const float e = n + (side > 0.f ? 1.f : side < 0.f ? 0.f : odd);
-            if (fabsf(t - k[i]) > 0.5f - 1e-5f) k[i] = e;
+            const float d = x[i] - z, y = d - x[i], e = (x[i] - (d - y)) + (-z - y);   // Knuth's two-sum
+            if (off[i] == 0.5f && e > 0.f) k[i] += 1.f;       // t = k + 1/2 went down to k
+            if (off[i] == -0.5f && e < 0.f) k[i] -= 1.f;      // t = k - 1/2 went up to k
         }
     }
     const float a = fmaf(fmaf(fmaf(k[3], 16.f, k[2]), 16.f, k[1]), 16.f, k[0]);
@@ -148,8 +160,8 @@ __device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float 
 
 // Eight elements at p with their group's extremes and codes; every lane of the warp takes part,
 // those whose p is null with a row of zeros.  VEC: p is on a 16-byte boundary.
-template <bool VEC>
-__device__ __forceinline__ uint32_t q4_quantise_at(const __nv_bfloat16 *p, int lanes, __half2 &par) {
+template <bool VEC, int LANES>
+__device__ __forceinline__ uint32_t q4_quantise_at(const __nv_bfloat16 *p, __half2 &par) {
     uint32_t w[4] = {0, 0, 0, 0};
     if (p != nullptr) {
         if constexpr (VEC) {
@@ -162,16 +174,16 @@ __device__ __forceinline__ uint32_t q4_quantise_at(const __nv_bfloat16 *p, int l
         }
     }
     float lo, hi, x[8];
-    q4_extremes(w, lanes, lo, hi);
+    q4_extremes<LANES>(w, lo, hi);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {   // a bf16 is the top half of an fp32
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    return q4_quantise8(x, lo, hi, par);
+    return q4_quantise8<true>(x, lo, hi, par);
 }
-template <bool VEC>
-__device__ __forceinline__ uint32_t q4_quantise_at(const float *p, int lanes, __half2 &par) {
+template <bool VEC, int LANES>
+__device__ __forceinline__ uint32_t q4_quantise_at(const float *p, __half2 &par) {
     float lo, hi, x[8] = {};
     if (p != nullptr) {
         if constexpr (VEC) {
@@ -182,8 +194,8 @@ __device__ __forceinline__ uint32_t q4_quantise_at(const float *p, int lanes, __
             for (int i = 0; i < 8; ++i) x[i] = p[i];
         }
     }
-    q4_extremes(x, lanes, lo, hi);
-    return q4_quantise8(x, lo, hi, par);
+    q4_extremes<LANES>(x, lo, hi);
+    return q4_quantise8<false>(x, lo, hi, par);
 }
 
 }  // namespace pkv
