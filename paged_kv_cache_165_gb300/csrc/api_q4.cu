@@ -242,7 +242,7 @@ size_t pkv_block_tables_extend_workspace_bytes(int B, int T) {
     int sm_count = 0;
     unsigned *err = nullptr;
     if (B < 0 || T < 0 || current_device_info(&sm_count, &err) != PKV_OK) return 0;
-    return extend_blocks(B, T, sm_count) > 1 ? 16 : 0;
+    return extend_blocks(T, sm_count) > 1 ? 16 : 0;
 }
 
 pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_lens, const int32_t *new_tokens,
@@ -259,7 +259,7 @@ pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_
     unsigned *err = nullptr;
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
-    if (extend_blocks(B, T, sm_count) > 1 && (workspace == nullptr || workspace_bytes < 16 || !aligned_to(workspace, 16)))
+    if (extend_blocks(T, sm_count) > 1 && (workspace == nullptr || workspace_bytes < 16 || !aligned_to(workspace, 16)))
         return fail(PKV_ERR_WORKSPACE, "block_tables_extend: needs 16 bytes of 16-byte aligned workspace, got %zu",
                     workspace == nullptr ? size_t(0) : workspace_bytes);
     const ExtendArgs a{block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,

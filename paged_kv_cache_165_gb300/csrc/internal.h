@@ -199,7 +199,7 @@ struct ReleaseArgs {
     unsigned *err;
 };
 
-int extend_blocks(int B, int T, int sm_count);           // thread blocks of an extend launch
+int extend_blocks(int T, int sm_count);                  // thread blocks of an extend launch
 bool release_in_one_block(int B, int MBS);
 cudaError_t launch_block_tables_extend(const ExtendArgs &a, int sm_count, cudaStream_t stream);
 cudaError_t launch_block_tables_release(const ReleaseArgs &a, int sm_count, cudaStream_t stream);
