@@ -134,18 +134,20 @@ __global__ void __launch_bounds__(128)
 // pairs of one sequence and KV head with the keys they see; a warp takes 32 keys at a time from a
 // private ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16
 // f16 MMAs and fp32 accumulators:
-//   Integers below 2048 in the low bits of an f16 are the subnormals n * 2^-24, exactly, so codes
-//   need no conversion.  The bytes of a code word (two codes: c + 16 c') are masked to 16-bit
-//   lanes, E = c + 16 c' and O = 16 c', four logic operations for eight codes; with the pair
-//   (x, x') on the other side, x c + x' c' = x E + (x' / 16 - x) O.
-//   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): q is scaled by a power of two per row
-//     and its coefficients enter as f16 hi + lo (2^-22 relative, times 16 for the difference); the
-//     head dimension is taken in the order in which the masks deliver the codes, each group in MMA
-//     steps of its own so that its scale multiplies the sum; zero * sum(q in group) is added in fp32.
+//   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): a code c in the low bits of an f16 is the
+//     subnormal c * 2^-24, four bits further up c * 2^-20, exactly: four masks and a shift turn a word
+//     of eight codes into MMA operands, no conversion.  q is scaled by a power of two per row (odd
+//     elements by another 1/16) and enters as f16 hi + lo (2^-23 relative); the head dimension is taken
+//     in the order in which the masks deliver the codes, each group in MMA steps of its own so that its
+//     scale multiplies the sum; zero * sum(q in group) is added in fp32.
 //   output O^T = V^T P^T: V^T is the A operand (16 dimensions x 16 keys), pairs of keys from a
 //     transposing ldmatrix over 16-bit units; P^T is what the lane already holds for its row, times
-//     the group's scale, as f16 hi + lo.  The E sums minus the O sums are the even dimensions.
-//     The zeros' term is summed in fp32.
+//     the group's scale, as f16 hi + lo.  The tensor core cuts its sums off instead of rounding them,
+//     relative to its operands' exponents.  Over many keys that adds up, and the zeros' term cancels
+//     most of a sum of non-negative codes (subnormal codes summed over a warp's range, 4 x 131072
+//     tokens: 1.1e-3 of the result).  So V's codes are centred and brought into the normal range by
+//     one multiply-add, and a stage's 32 keys are summed and added to O in fp32, together with the
+//     rescaling: 1e-7 of the result, for 10% of the time.  The zeros' term is summed in fp32.
 //   Scales and zeros are widened to fp32 once per key by the lane of that number and read back
 //   from shared memory in pairs of keys.
 // The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
@@ -600,8 +602,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         int issued = min(kStages, n_my);
         for (int k = 0; k < issued; ++k) issue(k);
 
-        // ---- query fragments, while the copies fly.  MMA steps 2u (E) and 2u + 1 (O) of word u =
-        // gi * WPT + i: elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours' differences
+        // ---- query fragments, while the copies fly.  MMA steps 2u and 2u + 1 of word u = gi * WPT + i:
+        // elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours / 16
         float f, qsum[G];   // score (base 2) = MMA sum * f; the groups' sums of q in the MMAs' units
         {
             float(&v)[G * WPT][8] = qv, amax = 0.f;
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                         sum += v[u][j];
                     }
 #pragma unroll
-                    for (int j = 1; j < 8; j += 2) v[u][j] = fmaf(v[u][j], 0.0625f, -v[u][j - 1]);
+                    for (int j = 1; j < 8; j += 2) v[u][j] *= 0.0625f;
                     split2(v[u][0], v[u][4], e.x, e.y);
                     split2(v[u][2], v[u][6], e.z, e.w);
                     split2(v[u][1], v[u][5], o.x, o.y);
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             const bool seen = tok0 + lane >= t_first.lo && tok0 + lane < min(t_last.len, tok_end) &&
                               !(bad >> (st * PPS + lane / BS) & 1);
             const int par_at = (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes + (lane % BS) * G * 4;
-            auto widen = [&](const uint8_t *pages) {
+            auto widen = [&](const uint8_t *pages, float centred) {
                 uint32_t v[G];
                 lds_words<G>(pages + par_at, v);
                 float top = 0.f;
@@ -678,14 +680,14 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                 for (int gi = 0; gi < G; ++gi) {
                     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v[gi]));
                     par[gi * 64 + lane] = seen ? y.x : 0.f;
-                    par[gi * 64 + 32 + lane] = seen ? y.y : 0.f;
+                    par[gi * 64 + 32 + lane] = seen ? fmaf(centred, y.x, y.y) : 0.f;
                     top = fmaxf(top, seen ? y.x : 0.f);
                 }
                 return top;
             };
 
             // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
-            widen(kpages);
+            widen(kpages, 0.f);
             __syncwarp();
             float2 s[NT];
 #pragma unroll
@@ -701,18 +703,16 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
 #pragma unroll
                 for (int i = 0; i < WPT; ++i) {
                     const uint4 e = qfrag[(2 * (gi * WPT + i)) * 32], o = qfrag[(2 * (gi * WPT + i) + 1) * 32];
-                    uint32_t lo[NT], hi[NT];
                     // the tiles' chains side by side
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        lo[nt] = c[nt][i] & 0x00ff00ffu;
-                        hi[nt] = __byte_perm(c[nt][i], 0, 0x4341);
-                        if (i == 0) mma16_first(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
-                        else mma16(a[nt], e.x, e.y, e.z, e.w, lo[nt], hi[nt]);
+                        const uint32_t x = c[nt][i] & 0x000f000fu, y = (c[nt][i] >> 8) & 0x000f000fu;
+                        if (i == 0) mma16_first(a[nt], e.x, e.y, e.z, e.w, x, y);
+                        else mma16(a[nt], e.x, e.y, e.z, e.w, x, y);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma16(a[nt], o.x, o.y, o.z, o.w, lo[nt] & 0x00f000f0u, hi[nt] & 0x00f000f0u);
+                        mma16(a[nt], o.x, o.y, o.z, o.w, c[nt][i] & 0x00f000f0u, (c[nt][i] >> 8) & 0x00f000f0u);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             __syncwarp();   // K's parameters have been read
 
             // ---- the running reference: the rows' maxima and the largest V scale
-            const float top = widen(vpages);
+            const float top = widen(vpages, 8.f);
             float mx = fmaxf(s[0].x, s[0].y);
 #pragma unroll
             for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
@@ -761,65 +761,68 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                 psum = add2(psum, w[nt]);
             }
             l_run = l_run * alpha + (psum.x + psum.y);
-            if (__any_sync(kFull, alpha != 1.f)) {
-                const float alpha_a = __shfl_sync(kFull, alpha, 8 * t4);
-                const float alpha_b = __shfl_sync(kFull, alpha, 8 * t4 + 4);
+            const float2 rescale = make_float2(__shfl_sync(kFull, alpha, 8 * t4), __shfl_sync(kFull, alpha, 8 * t4 + 4));
 #pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    oT[mt][0] *= alpha_a;
-                    oT[mt][1] *= alpha_b;
-                    oT[mt][2] *= alpha_a;
-                    oT[mt][3] *= alpha_b;
-                }
-#pragma unroll
-                for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
-            }
+            for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
             __syncwarp();   // V's parameters have been written
 
-            // ---- O^T += V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit units
-            // (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1
+            // ---- O^T = O^T alpha + V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit
+            // units (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1
             // in one register: the pairs along the keys that the A operand wants
+            constexpr int KT = kStageKeys / 16, N = HPG >= 2 ? 2 : 1;   // N columns of 32 dimensions at a time
             const uint32_t vrow = smem_addr(vpages) + (lane & 15) * (D / 2) + (HPG >= 2 ? (lane >> 4) * 16 : 0);
 #pragma unroll
-            for (int kt = 0; kt < kStageKeys / 16; ++kt) {
-                const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2);
+            for (int gi = 0; gi < G; ++gi) {
+                uint32_t ph[KT][2], pl[KT][2];
 #pragma unroll
-                for (int gi = 0; gi < G; ++gi) {
-                    uint32_t bh0, bl0, bh1, bl1;
-                    {
-                        const float *src = par + gi * 64 + kt * 16 + 2 * t4;
-                        const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
-                        split2(mul2(wa, *reinterpret_cast<const float2 *>(src)), bh0, bl0);
-                        split2(mul2(wb, *reinterpret_cast<const float2 *>(src + 8)), bh1, bl1);
-                        zo[gi] = fma2(wa, *reinterpret_cast<const float2 *>(src + 32),
-                                      fma2(wb, *reinterpret_cast<const float2 *>(src + 40), zo[gi]));
-                    }
+                for (int kt = 0; kt < KT; ++kt) {
+                    const float *src = par + gi * 64 + kt * 16 + 2 * t4;
+                    const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
+                    split2(mul2(wa, *reinterpret_cast<const float2 *>(src)), ph[kt][0], pl[kt][0]);
+                    split2(mul2(wb, *reinterpret_cast<const float2 *>(src + 8)), ph[kt][1], pl[kt][1]);
+                    zo[gi] = fma2(wa, *reinterpret_cast<const float2 *>(src + 32),
+                                  fma2(wb, *reinterpret_cast<const float2 *>(src + 40), zo[gi]));
+                }
 #pragma unroll
-                    for (int h = 0; h < HPG; h += 2) {
+                for (int h = 0; h < HPG; h += N) {
+                    const int c = gi * HPG + h;
+                    float sum[2 * N][4];   // even and odd elements of each column
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
                         // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
-                        constexpr int N = HPG >= 2 ? 2 : 1;
-                        const int c = gi * HPG + h;
-                        uint32_t v[4], hi[4], vo[4], ho[4];
-                        if constexpr (HPG >= 2) ldsm_x4_trans(rows + c * 16, v[0], v[1], v[2], v[3]);
-                        else ldsm_x2_trans(rows + c * 16, v[0], v[1]);
+                        const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2) + c * 16;
+                        uint32_t v[4], e[2 * N][2], o[2 * N][2];
+                        if constexpr (N == 2) ldsm_x4_trans(rows, v[0], v[1], v[2], v[3]);
+                        else ldsm_x2_trans(rows, v[0], v[1]);
 #pragma unroll
                         for (int i = 0; i < 2 * N; ++i) {
-                            hi[i] = __byte_perm(v[i], 0, 0x4341);
-                            v[i] &= 0x00ff00ffu;
-                            vo[i] = v[i] & 0x00f000f0u;
-                            ho[i] = hi[i] & 0x00f000f0u;
+                            centre(v[i], e[i][0], o[i][0]);
+                            centre(v[i] >> 8, e[i][1], o[i][1]);
                         }
 #pragma unroll
                         for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
-                            const uint32_t b0 = lo ? bl0 : bh0, b1 = lo ? bl1 : bh1;
+                            const uint32_t b0 = lo ? pl[kt][0] : ph[kt][0], b1 = lo ? pl[kt][1] : ph[kt][1];
 #pragma unroll
-                            for (int i = 0; i < N; ++i)
-                                mma16(oT[2 * (c + i)], v[2 * i], hi[2 * i], v[2 * i + 1], hi[2 * i + 1], b0, b1);
-#pragma unroll
-                            for (int i = 0; i < N; ++i)
-                                mma16(oT[2 * (c + i) + 1], vo[2 * i], ho[2 * i], vo[2 * i + 1], ho[2 * i + 1], b0, b1);
+                            for (int i = 0; i < N; ++i) {
+                                if (kt == 0 && lo == 0) {
+                                    mma16_first(sum[2 * i], e[2 * i][0], e[2 * i][1], e[2 * i + 1][0], e[2 * i + 1][1], b0, b1);
+                                    mma16_first(sum[2 * i + 1], o[2 * i][0], o[2 * i][1], o[2 * i + 1][0], o[2 * i + 1][1], b0, b1);
+                                } else {
+                                    mma16(sum[2 * i], e[2 * i][0], e[2 * i][1], e[2 * i + 1][0], e[2 * i + 1][1], b0, b1);
+                                    mma16(sum[2 * i + 1], o[2 * i][0], o[2 * i][1], o[2 * i + 1][0], o[2 * i + 1][1], b0, b1);
+                                }
+                            }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < 2 * N; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; r += 2) {
+                            float(&acc)[4] = oT[2 * c + i];
+                            const float2 y = fma2(make_float2(acc[r], acc[r + 1]), rescale, make_float2(sum[i][r], sum[i][r + 1]));
+                            acc[r] = y.x;
+                            acc[r + 1] = y.y;
+                        }
                 }
             }
             __syncwarp();
@@ -844,13 +847,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 1);
             zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 2);
         }
-        // this lane's outputs of rows 2 * t4 + r: dimensions 32 * c + 4 * g + {0, 1, 2, 3}.  E sums are
-        // (even + 16 odd) * 2^-24, O sums 16 odd * 2^-24
+        // this lane's outputs of rows 2 * t4 + r: dimensions 32 * c + 4 * g + {0, 1, 2, 3}
         auto outputs = [&](int c, int r) {
             const float z = __shfl_sync(kFull, zo[c / HPG].x, 8 * t4 + 4 * r);
             const float (&e)[4] = oT[2 * c], (&o)[4] = oT[2 * c + 1];
-            return make_float4(fmaf(e[r] - o[r], 0x1p24f, z), fmaf(o[r], 0x1p20f, z), fmaf(e[2 + r] - o[2 + r], 0x1p24f, z),
-                               fmaf(o[2 + r], 0x1p20f, z));
+            return make_float4(fmaf(e[r], 0x1p9f, z), fmaf(o[r], 0x1p9f, z), fmaf(e[2 + r], 0x1p9f, z), fmaf(o[2 + r], 0x1p9f, z));
         };
 
         if (P.balanced) {
@@ -968,11 +969,11 @@ int q4_blocks_per_sm(int d, int bs, int G) {
     return G == 1 ? MmaCfg<128, 32, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 32, 2>::kBlocksPerSm : MmaCfg<128, 32, 4>::kBlocksPerSm;
 }
 // (Query row, head) pairs of a sequence and KV head that the warp-MMA kernel, which takes eight at a
-// time, is faster for than the tcgen05 kernel, whose time hardly depends on them: 4 x 65536 tokens, one
-// scale group a row: 24 pairs 34.6 against 33.0 us, 32 44.2 against 33.2; 64 x 2048 tokens, four KV
-// heads: 61.9 against 71.9 and 76.1 against 74.3.  Two groups: 32 pairs 44.9 against 45.8, 40 53.7
-// against 46.1 (4 x 65536), 79.4 against 99.5 and 95.5 against 101.8 (64 x 2048).
-int q4_mma_slots(int G) { return G == 1 ? 24 : 40; }
+// time, is faster for than the tcgen05 kernel, whose time hardly depends on them.  4 x 65536 tokens, one
+// scale group a row: 24 pairs 37.3 us, the tcgen05 kernel 34.0 (32 pairs); 64 x 2048 tokens, four KV heads:
+// 66.5 and 74.1.  Two groups: 32 pairs 48.7 us, 40 58.7, the tcgen05 kernel 47.5 (40 pairs); 87.3, 105.4
+// and 100.9 (64 x 2048).
+int q4_mma_slots(int G) { return G == 1 ? 24 : 32; }
 
 // Rows of partial results of a balanced launch: two units for every warp or block.
 size_t balanced_rows(const Q4Plan &plan) {

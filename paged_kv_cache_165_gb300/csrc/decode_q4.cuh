@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode_kparams.cuh"
@@ -46,6 +47,16 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     split2(make_float2(x0, x1), hi, lo);
+}
+
+// V's codes less 8 (their scale then belongs to zero + 8 * scale): sums of weights times codes that
+// average out.  Codes 0 and 4 of w's eight as (c - 8) * 2^-9 in `even`, codes 1 and 5 in `odd`,
+// exactly.  The tensor core aligns the products by their operands' exponents, and a subnormal's is
+// the smallest normal one: as c * 2^-24 the sums would lose the last 7 of their 24 bits.
+__device__ __forceinline__ void centre(uint32_t w, uint32_t &even, uint32_t &odd) {
+    // f16: 2^15, 2^11, -2^-6
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(even) : "r"(w & 0x000f000fu), "r"(0x78007800u), "r"(0xa400a400u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(odd) : "r"(w & 0x00f000f0u), "r"(0x68006800u), "r"(0xa400a400u));
 }
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {

@@ -10,11 +10,11 @@
 // a key tile's G scale groups fill one 128-column buffer.  One block per SM, 14 warps:
 //   warp 9 (loader): the pages' runs (codes and parameters) into a ring of packed tiles, one bulk
 //     copy per K or V page.
-//   warps 10-13 (converters): codes to f16 without a conversion -- a code masked into the low bits
-//     of an f16 is the subnormal code * 2^-24, four bits further up code * 2^-20 -- written as
-//     128-byte-swizzled K and V tiles, four masks and a shift for eight codes; parameters widened to
-//     fp32.  A word's elements lie in the order 0 4 1 5 2 6 3 7 (as the masks deliver them), the odd
-//     ones 16 times too large: the queries are laid out and scaled to match, the outputs unscaled.
+//   warps 10-13 (converters): codes to f16 -- K's by masks alone: in the low bits of an f16 a code is
+//     the subnormal code * 2^-24, four bits further up code * 2^-20; V's centred and brought into the
+//     normal range by one more multiply-add -- written as 128-byte-swizzled tiles; parameters widened
+//     to fp32.  A word's elements lie in the order 0 4 1 5 2 6 3 7 (as the masks deliver them); K's odd
+//     ones are 16 times too large: the queries are laid out and scaled to match.
 //   warp 8 (one lane issues): S = Q K^T per group into one of two buffers, and O_g += P_g V_g, with Q
 //     and P in tensor memory.
 //   warps 0-7 (softmax): thread (w, lane) owns slot 8 g + lane / 4 of lane group g = 2 (w % 4) + w / 4
@@ -23,6 +23,9 @@
 // The f16 range: queries are scaled by a power of two per slot; the weights' reference is shifted by
 // E = ceil(log2 of the largest V scale) - 7, so that weight * scale stays below 2^15 although O is
 // rescaled only when the running maximum grew by more than 2^8.
+// The tensor core cuts its sums off instead of rounding them, so it adds up 1024 keys; the softmax warps
+// then take O into fp32 sums in shared memory (4 x 131072 tokens: off by 2e-7 of the result instead of
+// 2.2e-6, in the same time).
 //
 // Work: balanced (an equal range of all units' key tiles for every block, which may end one unit and
 // begin the next; the loader and the converters run ahead into it) or one block per unit and chunk,
@@ -43,7 +46,10 @@ struct Cfg {
     static constexpr int kParRow = TK + 16;                     // parameters: four runs of TK / 4, padded apart
     static constexpr int kParFloats = 4 * G * kParRow;          // K scale, K zero, V scale, V zero
     static constexpr int NT = kTileBytes > 16384 ? 2 : 4;       // f16 tiles of a ring: 64 KB
-    static constexpr int NS = 4;                                // packed tiles
+    static constexpr int kFold = 1024 / TK;                     // key tiles that the tensor core sums up
+    static constexpr int kSumBytes = kQ4UmmaSlots * D * 4;      // the sums of those before, in fp32
+    static constexpr int kRest = 232448 - 1024 - 64 - 256 - 4 * 16384 * 2 - kSumBytes - NT * (kParFloats + 4) * 4;
+    static constexpr int NS = kRest >= 4 * kPackedBytes ? 4 : 3;   // packed tiles
     static constexpr int kOffK = 0, kOffV = kOffK + NT * kTileBytes, kOffS = kOffV + NT * kTileBytes;
     static constexpr int kOffPar = kOffS + NS * kPackedBytes;
     static constexpr int kOffMax = kOffPar + NT * kParFloats * 4;   // V's largest scale [tile][converter warp]
@@ -51,7 +57,8 @@ struct Cfg {
     static constexpr int kSFull = 0, kSFree = NS, kKFull = 2 * NS, kKFree = kKFull + NT, kVFull = kKFree + NT,
                          kVFree = kVFull + NT, kQ = kVFree + NT, kScore = kQ + 1, kP = kScore + 2, kO = kP + 1,
                          kDrain = kO + 1, kBars = kDrain + 2;
-    static constexpr int kOffMisc = kOffBar + kBars * 8;   // TMEM address, abort flag, bad pages [NS], the share
+    static constexpr int kOffSum = kOffBar + (kBars * 8 + 15) / 16 * 16;
+    static constexpr int kOffMisc = kOffSum + kSumBytes;   // TMEM address, abort flag, bad pages [NS], the share
     static constexpr int kSmemBytes = 1024 + kOffMisc + 64;
     static constexpr int kSCol = 0, kOCol = 256, kPCol = kOCol + D, kQCol = kPCol + 64;
     static constexpr int kThreads = 448;
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
         // swizzled tile: d = 128: pieces 0, 1 of two keys with pieces 2, 3 of their neighbours
         const int w = warp - 10, ct = threadIdx.x - 320;
         bool alive = true;
-        auto convert = [&](const uint8_t *pages, uint8_t *tile) {
+        auto convert = [&](const uint8_t *pages, uint8_t *tile, auto centred) {
 #pragma unroll
             for (int i = 0; i < TK * WORDS / 4 / 128; ++i) {
                 int key, piece;
@@ -305,8 +312,9 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t y = c[j] >> 8;
-                    *reinterpret_cast<uint4 *>(tile + swz128(TK, key, (4 * piece + j) * 8)) =
-                        make_uint4(c[j] & 0x000f000fu, c[j] & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u);
+                    uint4 z = make_uint4(c[j] & 0x000f000fu, c[j] & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u);
+                    if constexpr (decltype(centred)::value) centre(c[j], z.x, z.y), centre(y, z.z, z.w);
+                    *reinterpret_cast<uint4 *>(tile + swz128(TK, key, (4 * piece + j) * 8)) = z;
                 }
             }
             fence_proxy_async_smem();   // before the MMAs read the tile
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                 alive = __all_sync(kFull, wait_or_abort(bar(C::kSFull + st), (r / NS) & 1, abort, p.err));
                 if (alive && r >= NT) alive = __all_sync(kFull, wait_or_abort(bar(C::kKFree + sl), (r / NT - 1) & 1, abort, p.err));
                 if (!alive) break;
-                convert(sS(st), sK(sl));
+                convert(sS(st), sK(sl), std::false_type{});
                 if (lane == 0) mbar_arrive(bar(C::kKFull + sl));
                 if (r >= NT) alive = __all_sync(kFull, wait_or_abort(bar(C::kVFree + sl), (r / NT - 1) & 1, abort, p.err));
                 if (!alive) break;
@@ -338,13 +346,13 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                         const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&raw));
                         float *dst = par + sl * C::kParFloats + (2 * side * G + gi) * C::kParRow + at;
                         dst[0] = y.x;
-                        dst[G * C::kParRow] = y.y;
+                        dst[G * C::kParRow] = side == 1 ? fmaf(8.f, y.x, y.y) : y.y;   // V's codes are centred
                         if (side == 1) top = fmaxf(top, y.x);
                     }
                 }
                 top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));   // non-negative floats order like their bits
                 if (lane == 0) vmax[sl * 4 + w] = top;
-                convert(sS(st) + PPT * C::kPageBytes, sV(sl));
+                convert(sS(st) + PPT * C::kPageBytes, sV(sl), std::true_type{});
                 if (lane == 0) {
                     mbar_arrive(bar(C::kVFull + sl));
                     mbar_arrive(bar(C::kSFree + st));
@@ -401,7 +409,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                     if (alive) scores(T);
                     for (int t = 0; t < n && alive; ++t) {
                         if (t + 1 < n) scores(T + t + 1);
-                        if (alive) products(T + t, t == 0);
+                        if (alive) products(T + t, t % C::kFold == 0);
                     }
                 }
                 T += n;
@@ -415,6 +423,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
         // ---- softmax
         const int c4 = lane & 3, grp = 2 * (warp & 3) + (warp >> 2), slot = 8 * grp + (lane >> 2);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(16 * grp) << 16);
+        float *sums = reinterpret_cast<float *>(smem + C::kOffSum) + threadIdx.x;   // [32 of a slot's sums][thread]
         bool ok = true;   // warp-uniform; a failed wait skips the warp's remaining work
         while (next_segment<BS, PPT>(P, share, g, threadIdx.x == 0)) {
             const int n = max(0, (g.pg1 - g.pg0 + PPT - 1) / PPT);
@@ -559,15 +568,27 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                     ok = __all_sync(kFull, wait_or_abort(bar(C::kO), (r - 1) & 1, abort, p.err));
                     if (!ok) continue;
                     tc_fence_after_sync();
-                    if (__any_sync(kFull, alpha != 1.f)) {
+                    const bool fold = t % C::kFold == 0;   // the products of this tile start O anew
+                    if (fold || __any_sync(kFull, alpha != 1.f)) {
 #pragma unroll
                         for (int cc = 0; cc < D / 64; ++cc) {
                             uint32_t o[32];
                             tmem_ld_16x256b_x8(lane_base + C::kOCol + cc * 64, o);
                             tmem_ld_wait();
+                            if (fold || t > C::kFold) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st_16x256b_x8(lane_base + C::kOCol + cc * 64, o);
+                                for (int e = 0; e < 16; ++e) {
+                                    float *q = sums + (cc * 16 + e) * 256;
+                                    float x = t > C::kFold ? *q : 0.f;
+                                    if (fold) x += __uint_as_float(o[e / 2 * 4 + e % 2]) + __uint_as_float(o[e / 2 * 4 + 2 + e % 2]);
+                                    *q = x * alpha;
+                                }
+                            }
+                            if (!fold) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st_16x256b_x8(lane_base + C::kOCol + cc * 64, o);
+                            }
                         }
                     }
                 }
@@ -606,13 +627,18 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                const float back = c4 & 1 ? 0x1p20f : 0x1p24f;
                 if (store)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {   // word 8 cc + k: elements c4 and c4 + 4
                         float *q = dst + cc * 64 + 8 * k + c4;
-                        q[0] = fmaf(__uint_as_float(o[4 * k]) + __uint_as_float(o[4 * k + 2]), back, z) * inv;
-                        q[4] = fmaf(__uint_as_float(o[4 * k + 1]) + __uint_as_float(o[4 * k + 3]), back, z) * inv;
+                        float x = __uint_as_float(o[4 * k]) + __uint_as_float(o[4 * k + 2]);
+                        float y = __uint_as_float(o[4 * k + 1]) + __uint_as_float(o[4 * k + 3]);
+                        if (n > C::kFold) {
+                            x += sums[(cc * 16 + 2 * k) * 256];
+                            y += sums[(cc * 16 + 2 * k + 1) * 256];
+                        }
+                        q[0] = fmaf(x, 0x1p9f, z) * inv;
+                        q[4] = fmaf(y, 0x1p9f, z) * inv;
                     }
             }
             if (store && c4 == 0) {

@@ -290,6 +290,28 @@ def test_q4_long_context_many_splits(hq, hkv):
     assert pkv.get_device_error() == 0
 
 
+# Equal weights over n keys: out is the mean of values zero + scale * code, |scale * (code - 8)| <= 2.4 for
+# values ~ N(0, 1).  A weight times scale in two f16 parts is off by 2^-22; a tensor core's sum of 32 keys
+# takes four additions cut off at 2^-23 of at most 32 * 2.4 (of 1024 keys: 128, of at most four standard
+# deviations 4 * sqrt(1024) * 0.9 once the codes are centred); adding those in fp32 to a running sum of at most
+# 4 * sqrt(n) * 0.9 costs 2^-24 of it n / 32 times; the zeros' running sums (mean 0.15) 5 * sqrt(n / 16) * 2^-24
+# * 0.15.  Relative to n weights, n = 40003: 6e-7 + 1.2e-6 (1.8e-6) + 1.4e-6 + 2e-6 < 6e-6.  Sums whose
+# error grows with n (uncentred codes added up by the tensor core) are off by 1e-5 and more.
+ATOL_MEAN = 6e-6
+
+
+@pytest.mark.parametrize("hq,d,group,bs", [(8, 128, 64, 16), (4, 128, 32, 32), (1, 64, 64, 16), (64, 128, 128, 16),
+                                           (64, 128, 64, 32), (64, 64, 64, 16), (2, 96, 32, 16)])
+def test_q4_errors_do_not_grow_with_the_context(hq, d, group, bs):
+    case = q4_case(12, [40003], hq, 1, d, group, bs)
+    case = (torch.zeros_like(case[0]), *case[1:])
+    live, ref, _ = expect((case[0][:, :1], *case[1:]), group, 0.1, 0)
+    for splits in (0, 1):
+        out, lse = run_q4(case, group, 0.1, 0, splits)
+        assert_attn_close(out, np.broadcast_to(ref, out.shape), f"splits {splits} out", ATOL_MEAN)
+        assert_attn_close(lse, np.full(lse.shape, math.log(40003)), f"splits {splits} lse", 4e-6)   # 4 ulp of 10.6
+
+
 @pytest.mark.parametrize("hq,hkv", [(8, 1), (32, 1)])
 def test_q4_large_and_masked_values(hq, hkv):
     """Queries and caches far from 1: the scores' range, not their number format, decides."""
