@@ -336,6 +336,73 @@ def test_q4_workspace_too_small_is_refused():
         pkv.paged_attention_q4(out, q, kc, vc, table, lens, 0.1, 32)
 
 
+@pytest.mark.parametrize("hq,hkv,d,group,bs,max_q", [(2, 1, 64, 64, 16, 1), (40, 1, 64, 64, 16, 1), (2, 1, 96, 32, 16, 1),
+                                                     (4, 1, 64, 32, 32, 3)])
+def test_q4_more_sequences_than_a_block_scans(hq, hkv, d, group, bs, max_q):
+    g = gen.generator(31)
+    lens = torch.randint(0, 41, (1100,), generator=g).tolist()
+    rows = [min(n, b % (max_q + 1)) for b, n in enumerate(lens)] if max_q > 1 else None
+    case = q4_case(31, lens, hq, hkv, d, group, bs, rows)
+    live, ref, ref_lse = expect(case, group, 0.1, 0)
+    out, lse = run_q4(case, group, 0.1, decode=max_q == 1, max_q=max_q)
+    assert_attn_close(out[live], ref, "out", ATOL)
+    assert_attn_close(lse[live], ref_lse, "lse", ATOL)
+    if max_q == 1:
+        empty = [b for b, n in enumerate(lens) if n == 0]
+        assert empty and torch.all(out[empty] == 0) and torch.all(torch.isneginf(lse[empty]))
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 2), (40, 1)])
+def test_q4_pointers_aligned_to_their_elements_only(hq, hkv):
+    """Caches 4 bytes and queries 8 bytes past an aligned address: another kernel, the same results."""
+    d, group, bs = 128, 64, 16
+    case = q4_case(17, [300, 1, 64], hq, hkv, d, group, bs)
+    q, kc, vc, table, lens, cu = case
+    live, ref, ref_lse = expect(case, group, 0.1, 0)
+
+    def shifted(t, by):
+        room = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+        view = room[by:by + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+    out = torch.empty(q.shape, device="cuda")
+    lse = torch.empty(q.shape[:2], device="cuda")
+    ws = torch.zeros(pkv.paged_attention_q4_workspace_bytes(3, 3, 1, hq, hkv, d, group, bs, table.shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    for kk, vv, qq in ((shifted(kc, 4), dev(vc), dev(q)), (dev(kc), dev(vc), shifted(q, 2)), (shifted(kc, 12), shifted(vc, 4), dev(q))):
+        pkv.paged_attention_q4(out, qq, kk, vv, dev(table), dev(lens), 0.1, group, lse=lse, workspace=ws)
+        assert_attn_close(out[live], ref, "out", ATOL)
+        assert_attn_close(lse[live], ref_lse, "lse", ATOL)
+    for kk, qq in ((shifted(kc, 1), dev(q)), (dev(kc), shifted(q, 1))):
+        with pytest.raises(pkv.PkvError, match="aligned"):
+            pkv.paged_attention_q4(out, qq, kk, dev(vc), dev(table), dev(lens), 0.1, group, lse=lse, workspace=ws)
+
+
+def test_q4_streams_and_a_workspace_used_in_turn():
+    """Two streams with workspaces of their own at once; calls of different shapes one after the other in one."""
+    shapes = [(16, 2, 128, 64, 16), (64, 1, 128, 128, 16), (8, 2, 64, 32, 16), (4, 2, 96, 32, 16)]
+    cases = [q4_case(41 + i, [3000, 7, 129], hq, hkv, d, group, bs) for i, (hq, hkv, d, group, bs) in enumerate(shapes)]
+    alone = [run_q4(c, s[3], 0.1) for c, s in zip(cases, shapes)]
+    on_gpu = [[dev(t) for t in c] for c in cases]
+    n = max(pkv.paged_attention_q4_workspace_bytes(3, 3, 1, *s, c[3].shape[1]) for c, s in zip(cases, shapes))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(4):
+        for stream, ws in zip(streams, spaces):
+            with torch.cuda.stream(stream):
+                for i, (q, kc, vc, table, lens, _) in enumerate(on_gpu):
+                    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+                    pkv.paged_attention_q4(out, q, kc, vc, table, lens, 0.1, shapes[i][3], lse=lse, workspace=ws)
+                    got.append((i, out, lse))
+    torch.cuda.synchronize()
+    for i, out, lse in got:
+        assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+    assert pkv.get_device_error() == 0
+
+
 # ----------------------------------------------------------------------- decode step
 
 def run_step(case, k_new, v_new, slots, group, scale, window, num_splits, fused):
@@ -381,3 +448,34 @@ def test_q4_decode_step_equals_append_then_attention(hq, hkv, d, group, bs, new_
     live, ref, ref_lse = expect((case[0], want_k, want_v, *case[3:]), group, scale, window)
     assert_attn_close(out[live], ref, "out", ATOL)
     assert_attn_close(lse[live], ref_lse, "lse", ATOL)
+
+
+@pytest.mark.parametrize("hq,fused", [(8, True), (16, False)])
+def test_q4_decode_step_slots_that_are_not_the_last_position(hq, fused):
+    """Quantised in the attention launch: only the last position's slot is taken.  Else kv_append_q4's rules."""
+    lens = [40, 20, 0, 33]
+    d, group, bs, hkv = 128, 64, 16, 1
+    case = q4_case(19, lens, hq, hkv, d, group, bs, poison=False)
+    g = gen.generator(5)
+    k_new, v_new = gen.randn(g, (4, hkv, d)), gen.randn(g, (4, hkv, d))
+    slots = torch.tensor([oracle.slot_of(case[3][b], max(n, 1) - 1, bs) if n else -1 for b, n in enumerate(lens)])
+    right = slots.clone()
+    slots[1] = oracle.slot_of(case[3][1], 3, bs)      # a position before the last
+    out, _, kc, vc = run_step(case, k_new, v_new, slots, group, 0.1, 0, 0, True)
+    err = pkv.get_device_error()
+    if fused:
+        assert err == pkv.DEVERR["slot"]
+        right[1] = -1
+    else:
+        assert err == 0
+        right[1] = slots[1]
+    want_k, want_v = case[1].clone(), case[2].clone()
+    orc.kv_append_q4(want_k, want_v, k_new, v_new, right, group)
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    live, ref, _ = expect((case[0], want_k, want_v, *case[3:]), group, 0.1, 0)
+    assert_attn_close(out[live], ref, "out", ATOL)
+    assert torch.all(out[2] == 0)
+    slots[1], slots[2] = -1, 0                        # a new token of an empty sequence
+    if fused:
+        _, _, kc, _ = run_step(case, k_new, v_new, slots, group, 0.1, 0, 0, True)
+        assert pkv.get_device_error() == pkv.DEVERR["slot"]
