@@ -5,9 +5,14 @@
 //   low-bit trade-off of zwjcode.cn "KV Cache 的增量解码" §14).
 // kv_gather_q4: the values of the rows in given slots, as bf16 or fp32 rows.
 //
-// A thread owns eight consecutive elements (one 32-bit word of codes), so a warp covers 256
-// consecutive elements of the input and a group is 4, 8 or 16 neighbouring lanes, whatever
-// the head size: groups never straddle a warp because 256 is a multiple of each group size.
+// Append: a thread owns sixteen consecutive elements (two 32-bit words of codes), so a group is 2, 4
+// or 8 neighbouring lanes whatever the head size: groups never straddle a warp because its 512
+// elements are a multiple of each group size.  The arithmetic bounds it (about 17 instructions an
+// element: extremes, an exactly rounded quotient, the pack), so the scale's and the address's share
+// of it counts: with eight elements a thread 17153 tokens of 8 heads x 128 (bf16) took 35.9 us, with
+// sixteen 25.9 (3.5 TB/s; 13.3 at the copy rate), with 32 (two blocks per SM) 29.  Both rows are loaded
+// before either's arithmetic, which costs a few spilled registers at four blocks per SM (three: 26.9).
+// Gather: a thread owns eight; its stores bound it (32768 tokens, 34 us, 5.0 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -36,9 +41,9 @@ __device__ __forceinline__ int div_by(int n, const FastDiv &f) {
 // fewer than 2^31), and slots too unless the cache holds more than 2^31 of them.
 struct Q4Rows {
     const int64_t *slots;
-    int words;           // 8-element words of K (and as many of V): T * Hkv * d / 8
-    int Hkv, row_words;  // d / 8
-    int lanes;           // lanes that share a group: group / 8
+    int words;           // a thread's parts of K (and as many of V): T * Hkv * d / per
+    int Hkv, row_words;  // d / per
+    int lanes;           // threads that share a group: group / per
     int bs, page_bytes;  // bs * row bytes
     FastDiv by_row, by_head, by_bs;
     long long n_slots;
@@ -67,30 +72,35 @@ __device__ __forceinline__ Q4Place q4_place(const Q4Rows &r, int w) {
     return a;
 }
 
+constexpr int kAppendWords = 2;   // of codes, for each thread of an append
+
 template <typename T, bool VEC, int LANES>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     kv_append_q4_kernel(const T *__restrict__ k_new, const T *__restrict__ v_new, uint8_t *__restrict__ kc,
                         uint8_t *__restrict__ vc, const Q4Rows r) {
     const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+    constexpr int W = kAppendWords;
     // whole warps run each turn: the group's lanes exchange their extremes
     for (long long w0 = blockIdx.x * static_cast<long long>(blockDim.x) + (threadIdx.x & ~31); w0 < r.words;
          w0 += stride) {
         const int w = static_cast<int>(w0) + static_cast<int>(threadIdx.x & 31);
         const Q4Place a = q4_place(r, min(w, r.words - 1));
         const bool live = w < r.words && a.slot >= 0;
-        __half2 pars[2];
-        uint32_t codes[2];
-        codes[0] = q4_quantise_at<VEC, LANES>(live ? k_new + static_cast<size_t>(w) * 8 : nullptr, pars[0]);
-        codes[1] = q4_quantise_at<VEC, LANES>(live ? v_new + static_cast<size_t>(w) * 8 : nullptr, pars[1]);
+        Q4Loaded<T, W> x[2];   // both rows' loads before either's arithmetic
+        q4_load<VEC, W>(live ? k_new + static_cast<size_t>(w) * (8 * W) : nullptr, x[0].v);
+        q4_load<VEC, W>(live ? v_new + static_cast<size_t>(w) * (8 * W) : nullptr, x[1].v);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            const uint32_t code = codes[side];
-            const __half2 par = pars[side];
+            __half2 par;
+            uint32_t code[W];
+            q4_quantise_loaded<LANES, W>(x[side].v, par, code);
             if (!live) continue;
             uint8_t *page = (side ? vc : kc) + a.page;
-            reinterpret_cast<uint32_t *>(page)[a.off * r.row_words + a.j] = code;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(page) + (a.off * r.row_words + a.j) * W;
+#pragma unroll
+            for (int i = 0; i < W; ++i) dst[i] = code[i];
             if (a.j % LANES == 0)
-                reinterpret_cast<__half2 *>(page + r.bs * r.row_words * 4)[a.off * (r.row_words / LANES) + a.j / LANES] = par;
+                reinterpret_cast<__half2 *>(page + r.bs * r.row_words * (4 * W))[a.off * (r.row_words / LANES) + a.j / LANES] = par;
         }
     }
 }
@@ -156,16 +166,16 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-Q4Rows rows_of(const int64_t *slots, int T, int Hkv, int d, int group, int bs, int NB, unsigned *err) {
+Q4Rows rows_of(const int64_t *slots, int T, int Hkv, int d, int group, int bs, int NB, int per, unsigned *err) {
     Q4Rows r;
     r.slots = slots;
-    r.words = T * Hkv * (d / 8);
-    r.by_row = fast_div(d / 8);
+    r.words = T * Hkv * (d / per);
+    r.by_row = fast_div(d / per);
     r.by_head = fast_div(Hkv);
     r.by_bs = fast_div(bs);
     r.Hkv = Hkv;
-    r.row_words = d / 8;
-    r.lanes = group / 8;
+    r.row_words = d / per;
+    r.lanes = group / per;
     r.bs = bs;
     r.page_bytes = bs * q4_row_bytes(d, group);
     r.n_slots = static_cast<long long>(NB) * bs;
@@ -199,7 +209,7 @@ cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype 
                                    new_dt, k_cache, v_cache, slot_mapping + most, T - most, Hkv, d, group, bs, NB, sm_count,
                                    err, stream);
     }
-    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
+    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, 8 * kAppendWords, err);
     const unsigned grid = grid_of(r.words, sm_count);
     const bool vec = aligned(k_new, v_new, 16);
 #define PKV_Q4_APPEND(TT, VV, LL)                                                                     \
@@ -207,9 +217,9 @@ cudaError_t launch_kv_append_q4(const void *k_new, const void *v_new, pkv_dtype 
                                                               static_cast<const TT *>(v_new), k_cache, v_cache, r)
 #define PKV_Q4_APPEND_L(TT, VV)                       \
     switch (r.lanes) {                                \
+        case 2: PKV_Q4_APPEND(TT, VV, 2); break;      \
         case 4: PKV_Q4_APPEND(TT, VV, 4); break;      \
-        case 8: PKV_Q4_APPEND(TT, VV, 8); break;      \
-        default: PKV_Q4_APPEND(TT, VV, 16); break;    \
+        default: PKV_Q4_APPEND(TT, VV, 8); break;     \
     }
     if (new_dt == PKV_BF16) {
         if (vec) PKV_Q4_APPEND_L(__nv_bfloat16, true)
@@ -236,7 +246,7 @@ cudaError_t launch_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, cons
                                    k_cache, v_cache, slot_mapping + most, T - most, Hkv, d, group, bs, NB, sm_count, err,
                                    stream);
     }
-    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, err);
+    const Q4Rows r = rows_of(slot_mapping, T, Hkv, d, group, bs, NB, 8, err);
     const unsigned grid = grid_of(r.words, sm_count);
     const bool vec = aligned(k_out, v_out, 16);
 #define PKV_Q4_GATHER(TT, VV)                                                                     \

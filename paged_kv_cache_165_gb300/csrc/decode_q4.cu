@@ -366,12 +366,19 @@ __device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, in
     const size_t src = (static_cast<size_t>(b) * p.k.Hkv + kvh) * D + lane * 8;
     const void *rows = side ? p.k.v_new : p.k.k_new;
     __half2 par;
-    uint32_t code;
-    if (p.new_bf16) code = q4_quantise_at<false, LANES>(lane < WORDS ? static_cast<const __nv_bfloat16 *>(rows) + src : nullptr, par);
-    else code = q4_quantise_at<false, LANES>(lane < WORDS ? static_cast<const float *>(rows) + src : nullptr, par);
+    uint32_t code[1];
+    if (p.new_bf16) {
+        Q4Loaded<__nv_bfloat16, 1> x;
+        q4_load<false, 1>(lane < WORDS ? static_cast<const __nv_bfloat16 *>(rows) + src : nullptr, x.v);
+        q4_quantise_loaded<LANES, 1>(x.v, par, code);
+    } else {
+        Q4Loaded<float, 1> x;
+        q4_load<false, 1>(lane < WORDS ? static_cast<const float *>(rows) + src : nullptr, x.v);
+        q4_quantise_loaded<LANES, 1>(x.v, par, code);
+    }
     if (lane >= WORDS) return;
     uint8_t *page = (side ? p.vc : p.kc) + row_page;
-    reinterpret_cast<uint32_t *>(page)[off * WORDS + lane] = code;
+    reinterpret_cast<uint32_t *>(page)[off * WORDS + lane] = code[0];
     if (lane % LANES == 0) reinterpret_cast<__half2 *>(page + bs * WORDS * 4)[off * G + lane / LANES] = par;
 }
 

@@ -63,13 +63,13 @@ __device__ __forceinline__ float q4_min_nan(float a, float b) {   // NaN if eith
     return d;
 }
 
-// The least and the largest of a group spread over LANES consecutive lanes (4, 8 or 16), each with
-// eight elements; lo is NaN if an element is.
-template <int LANES>
-__device__ __forceinline__ void q4_extremes(const float (&x)[8], float &lo, float &hi) {
+// The least and the largest of a group spread over LANES consecutive lanes, each with N elements; lo is
+// NaN if an element is.
+template <int LANES, int N>
+__device__ __forceinline__ void q4_extremes(const float (&x)[N], float &lo, float &hi) {
     lo = hi = x[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < N; ++i) {
         lo = q4_min_nan(lo, x[i]);
         hi = fmaxf(hi, x[i]);
     }
@@ -80,12 +80,17 @@ __device__ __forceinline__ void q4_extremes(const float (&x)[8], float &lo, floa
     }
 }
 // The same of bf16 elements, two to a word: pairs at a time, then (lo, -hi) in one word.
-template <int LANES>
-__device__ __forceinline__ void q4_extremes(const uint32_t (&w)[4], float &lo, float &hi) {
+template <int LANES, int N>
+__device__ __forceinline__ void q4_extremes(const uint32_t (&w)[N], float &lo, float &hi) {
     auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
     auto bits = [](__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); };
-    const uint32_t least = bits(__hmin2_nan(__hmin2_nan(bf(w[0]), bf(w[1])), __hmin2_nan(bf(w[2]), bf(w[3]))));
-    const uint32_t most = bits(__hmax2_nan(__hmax2_nan(bf(w[0]), bf(w[1])), __hmax2_nan(bf(w[2]), bf(w[3])))) ^ 0x80008000u;
+    __nv_bfloat162 l = bf(w[0]), h = l;
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+        l = __hmin2_nan(l, bf(w[i]));
+        h = __hmax2_nan(h, bf(w[i]));
+    }
+    const uint32_t least = bits(l), most = bits(h) ^ 0x80008000u;
     uint32_t m = bits(__hmin2_nan(bf(__byte_perm(least, most, 0x5410)), bf(__byte_perm(least, most, 0x7632))));
 #pragma unroll
     for (int sh = LANES / 2; sh > 0; sh >>= 1) m = bits(__hmin2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, sh))));
@@ -93,30 +98,32 @@ __device__ __forceinline__ void q4_extremes(const uint32_t (&w)[4], float &lo, f
     hi = -__uint_as_float(m & 0xffff0000u);
 }
 
-// Eight consecutive elements of a group with extremes lo and hi (BF16: they are bf16 values): their codes (element i in
-// bits 4i .. 4i+3) and the group's (scale, zero).  Quotients are rounded by adding and taking away
-// 1.5 * 2^23 and packed as fp32 integers, four codes (below 2^16) at a time.
-template <bool BF16>
-__device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float hi, __half2 &par) {
+// N consecutive elements of a group with extremes lo and hi (BF16: they are bf16 values): their codes
+// (element 8 w + i in bits 4i .. 4i+3 of word w) and the group's (scale, zero).  Quotients are rounded by
+// adding and taking away 1.5 * 2^23 and packed as fp32 integers, four codes (below 2^16) at a time.
+template <bool BF16, int N>
+__device__ __forceinline__ void q4_quantise(float (&x)[N], float lo, float hi, __half2 &par, uint32_t (&code)[N / 8]) {
+#pragma unroll
+    for (int w = 0; w < N / 8; ++w) code[w] = 0;
     if (lo != lo) {
         par = __halves2half2(__ushort_as_half(0), __ushort_as_half(0x7fff));
-        return 0;
+        return;
     }
     if (lo < -kQ4Max || hi > kQ4Max) {
         lo = fminf(fmaxf(lo, -kQ4Max), kQ4Max);
         hi = fminf(fmaxf(hi, -kQ4Max), kQ4Max);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kQ4Max), kQ4Max);
+        for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -kQ4Max), kQ4Max);
     }
     const __half zero = __float2half_rd(lo);
     const __half scale = q4_scale(hi, zero);
     par = __halves2half2(scale, zero);
     const float s = __half2float(scale), z = __half2float(zero);
-    if (!(s > 0.f)) return 0;
+    if (!(s > 0.f)) return;
     if (s < 0x1p-14f) {
         // a subnormal scale may be rounded by more than a part in 2^11: quotients can pass 15.5
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fminf(x[i], fmaf(15.f, s, z));
+        for (int i = 0; i < N; ++i) x[i] = fminf(x[i], fmaf(15.f, s, z));
     }
     float inv;   // 1 / s, correctly rounded: one Newton step from within a last place, checked for all 11-bit s
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -124,78 +131,110 @@ __device__ __forceinline__ uint32_t q4_quantise8(float (&x)[8], float lo, float 
     constexpr float kMagic = 12582912.f;
     const float2 mz = make_float2(-z, -z), ms = make_float2(-s, -s), i2 = make_float2(inv, inv);
     const float2 up = make_float2(kMagic, kMagic), down = make_float2(-kMagic, -kMagic);
-    float k[8], off[8], worst = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    auto quotient = [&](int i) {   // of elements i and i + 1
         const float2 d = add2(make_float2(x[i], x[i + 1]), mz);   // never below 0
         const float2 q = make_float2(d.x * inv, d.y * inv);
-        const float2 t = fma2(fma2(q, ms, d), i2, q);
-        const float2 r = add2(add2(t, up), down);
+        return fma2(fma2(q, ms, d), i2, q);
+    };
+    float k[N], worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 t = quotient(i), r = add2(add2(t, up), down);
         const float2 o = add2(t, make_float2(-r.x, -r.y));
         worst = fmaxf(worst, fmaxf(fabsf(o.x), fabsf(o.y)));
         k[i] = r.x, k[i + 1] = r.y;
-        off[i] = o.x, off[i + 1] = o.y;
     }
     bool inexact = worst == 0.5f;   // a tie in fp32: the error of x - z, where there is one, decides
     if (BF16 && inexact) {
         // 8- and 11-bit terms: exact unless one of them lies far below the difference
         float least = INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) least = fminf(least, x[i] != 0.f ? fabsf(x[i]) : INFINITY);
+        for (int i = 0; i < N; ++i) least = fminf(least, x[i] != 0.f ? fabsf(x[i]) : INFINITY);
         inexact = least < s * 0x1p-9f || (z != 0.f && fabsf(z) < s * 0x1p-7f);   // differences are below 16 s
     }
     if (inexact) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < N; ++i) {
+            const float2 t = quotient(i & ~1);
+            const float off = (i & 1 ? t.y : t.x) - k[i];
             const float d = x[i] - z, y = d - x[i], e = (x[i] - (d - y)) + (-z - y);   // Knuth's two-sum
-            if (off[i] == 0.5f && e > 0.f) k[i] += 1.f;       // t = k + 1/2 went down to k
-            if (off[i] == -0.5f && e < 0.f) k[i] -= 1.f;      // t = k - 1/2 went up to k
+            if (off == 0.5f && e > 0.f) k[i] += 1.f;       // t = k + 1/2 went down to k
+            if (off == -0.5f && e < 0.f) k[i] -= 1.f;      // t = k - 1/2 went up to k
         }
     }
-    const float a = fmaf(fmaf(fmaf(k[3], 16.f, k[2]), 16.f, k[1]), 16.f, k[0]);
-    const float b = fmaf(fmaf(fmaf(k[7], 16.f, k[6]), 16.f, k[5]), 16.f, k[4]);
-    // the integers below 2^16 stand in the low halves of a + 2^23 and b + 2^23
-    return __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
+#pragma unroll
+    for (int w = 0; w < N; w += 8) {
+        const float a = fmaf(fmaf(fmaf(k[w + 3], 16.f, k[w + 2]), 16.f, k[w + 1]), 16.f, k[w]);
+        const float b = fmaf(fmaf(fmaf(k[w + 7], 16.f, k[w + 6]), 16.f, k[w + 5]), 16.f, k[w + 4]);
+        // the integers below 2^16 stand in the low halves of a + 2^23 and b + 2^23
+        code[w / 8] = __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
+    }
 }
 
-// Eight elements at p with their group's extremes and codes; every lane of the warp takes part,
-// those whose p is null with a row of zeros.  VEC: p is on a 16-byte boundary.
-template <bool VEC, int LANES>
-__device__ __forceinline__ uint32_t q4_quantise_at(const __nv_bfloat16 *p, __half2 &par) {
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (p != nullptr) {
-        if constexpr (VEC) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else {
-            const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+// 8 W elements at p as loaded, zeros where p is null.  VEC: p is on a 16-byte boundary.
+template <bool VEC, int W>
+__device__ __forceinline__ void q4_load(const __nv_bfloat16 *p, uint32_t (&w)[4 * W]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = q[2 * i] | static_cast<uint32_t>(q[2 * i + 1]) << 16;
+    for (int i = 0; i < 4 * W; ++i) w[i] = 0;
+    if (p == nullptr) return;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
         }
+    } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 4 * W; ++i) w[i] = q[2 * i] | static_cast<uint32_t>(q[2 * i + 1]) << 16;
     }
-    float lo, hi, x[8];
+}
+template <bool VEC, int W>
+__device__ __forceinline__ void q4_load(const float *p, float (&x)[8 * W]) {
+#pragma unroll
+    for (int i = 0; i < 8 * W; ++i) x[i] = 0.f;
+    if (p == nullptr) return;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = a.z, x[4 * i + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * W; ++i) x[i] = p[i];
+    }
+}
+
+// The codes and parameters of what every lane of a warp has loaded, a group over LANES lanes.
+template <int LANES, int W>
+__device__ __forceinline__ void q4_quantise_loaded(const uint32_t (&w)[4 * W], __half2 &par, uint32_t (&code)[W]) {
+    float lo, hi, x[8 * W];
     q4_extremes<LANES>(w, lo, hi);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {   // a bf16 is the top half of an fp32
+    for (int i = 0; i < 4 * W; ++i) {   // a bf16 is the top half of an fp32
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    return q4_quantise8<true>(x, lo, hi, par);
+    q4_quantise<true>(x, lo, hi, par, code);
 }
-template <bool VEC, int LANES>
-__device__ __forceinline__ uint32_t q4_quantise_at(const float *p, __half2 &par) {
-    float lo, hi, x[8] = {};
-    if (p != nullptr) {
-        if constexpr (VEC) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = p[i];
-        }
-    }
+template <int LANES, int W>
+__device__ __forceinline__ void q4_quantise_loaded(float (&x)[8 * W], __half2 &par, uint32_t (&code)[W]) {
+    float lo, hi;
     q4_extremes<LANES>(x, lo, hi);
-    return q4_quantise8<false>(x, lo, hi, par);
+    q4_quantise<false>(x, lo, hi, par, code);
 }
+
+// How 8 W elements of type T are held between the two.
+template <typename T, int W>
+struct Q4Loaded;
+template <int W>
+struct Q4Loaded<__nv_bfloat16, W> {
+    uint32_t v[4 * W];
+};
+template <int W>
+struct Q4Loaded<float, W> {
+    float v[8 * W];
+};
 
 }  // namespace pkv
