@@ -12,11 +12,11 @@
 #include <atomic>
 
 #include "decode_q4.cuh"
+#include "decode_q4_rows.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
 
 constexpr int kLeastSteps = 4;       // 32-key steps that a warp of one takes at least (128 keys)
 
@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(128)
 
 // ============================================================== warp-MMA path
 //
-// attend_q4_mma_kernel (d 64 or 128, bs 16 or 32).  A unit is a tile of eight (query row, head)
-// pairs of one sequence and KV head with the keys they see; a warp takes 32 keys at a time from a
+// attend_q4_mma_kernel (d 64 or 128, bs 16 or 32).  A unit is a tile of eight, or up to four, (query row,
+// head) pairs of one sequence and KV head with the keys they see; a warp takes 32 keys at a time from a
 // private ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16
 // f16 MMAs and fp32 accumulators:
 //   scores S (rows: 8 query rows hi, 8 lo; 8 keys per tile): a code c in the low bits of an f16 is the
@@ -149,7 +149,10 @@ __global__ void __launch_bounds__(128)
 //     one multiply-add, and a stage's 32 keys are summed and added to O in fp32, together with the
 //     rescaling: 1e-7 of the result, for 10% of the time.  The zeros' term is summed in fp32.
 //   Scales and zeros are widened to fp32 once per key by the lane of that number and read back
-//   from shared memory in pairs of keys.
+//   from shared memory.
+//   Up to four rows (decode_q4_rows.cuh) change the places of K and q, S^T = K Q^T, and need half the
+//   MMAs and exponentials: 4 x 65536 tokens of four KV heads 38.9 us for four rows, 49.1 for five;
+//   MHA step 82.5 -> 68.5 us, windows of 4096 tokens, four heads per KV head, 100.5 -> 78.8.
 // The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
 // the largest scale seen so far, E = ceil(log2 max scale): w = 2^(s - m - E + 14); l, O and the
 // zeros' term carry the same factor, which cancels, and a growing E rescales like a growing max.
@@ -162,79 +165,52 @@ __global__ void __launch_bounds__(128)
 //   chunks: one block for each unit and chunk, its four warps taking the steps in turn and merging
 //     in shared memory; a few chunks merge in place, many in decode_merge_kernel.
 
-constexpr int kMmaWarps = 4, kStageKeys = 32, kStages = 2;
+constexpr int kMmaWarps = 4, kStages = 2;
 constexpr int kUnitCost = 3;   // a unit's start (queries, first copies, its part written) in 32-key steps
 
-template <int D, int BS, int G>
+template <int D, int BS, int G, typename Rows>
 struct MmaCfg {
-    static constexpr int WORDS = D / 8;              // code words per row
     static constexpr int PPS = kStageKeys / BS;      // pages per stage
-    static constexpr int kCodeBytes = BS * D / 2;    // a page's codes; its parameters follow
     static constexpr int kPageBytes = BS * (D / 2 + 4 * G);
     static constexpr int kStageBytes = 2 * PPS * kPageBytes;   // K pages, then V pages
     static constexpr int kRingBytes = kMmaWarps * kStages * kStageBytes;
-    static constexpr int kMergeBytes = kMmaWarps * 8 * (2 + D) * 4;
+    static constexpr int kMergeBytes = kMmaWarps * Rows::ROWS * (2 + D) * 4;
     static constexpr int kScanBytes = (kMaxBalanced + 1) * 4;
     static constexpr int kUsed = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
     static constexpr int kDataBytes = (kUsed > kScanBytes ? kUsed : kScanBytes) + 15 & ~15;
     static constexpr int kQOff = kDataBytes;                            // query fragments [warp][step][lane]
-    static constexpr int kQBytes = (D / 16) * 512;
-    static constexpr int kParOff = kQOff + kMmaWarps * kQBytes;         // [warp][group][scale, zero][key]
+    static constexpr int kParOff = kQOff + kMmaWarps * Rows::kQBytes;         // [warp][group][scale, zero][key]
     static constexpr int kParBytes = G * 2 * kStageKeys * 4;
     static constexpr int kBarOff = kParOff + kMmaWarps * kParBytes;
     static constexpr int kSmemBytes = kBarOff + kMmaWarps * kStages * 8;
-    // Three blocks (12 warps, 168 registers a thread) against four (128, with spills): 70B-shaped step
-    // 91.4 against 94.2 us, MHA step 76.4 against 79.0, four sequences of 131072 tokens 142 against 139.
-    static constexpr int kBlocksPerSm = 3;
-    static_assert(kBlocksPerSm * (kSmemBytes + 2048) <= 228 * 1024, "three blocks fit an SM");
+    static constexpr int kBlocksPerSm = Rows::kBlocksPerSm;
+    static_assert(kBlocksPerSm * (kSmemBytes + 2048) <= 228 * 1024, "the blocks fit an SM");
     static_assert(kPageBytes % 16 == 0, "bulk copies");
 };
 
-// D = A(16x16, f16, row) * B(16x8, f16, col) + D, fp32 accumulate.
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same with C = 0, so that no registers are cleared first.
-__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                            uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ void ldsm_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
-}
-
-// The warps' states of a tile's eight rows, in shared memory ([NW][8] references and sums, then
-// [NW][8][D] outputs), merged and written: the result where the unit has one part, else this
+// The warps' states of a tile's R rows, in shared memory ([NW][R] references and sums, then
+// [NW][R][D] outputs), merged and written: the result where the unit has one part, else this
 // normalised part; with arrival counters the unit's last part merges them all.
-template <int D, int NW>
+template <int D, int NW, int R>
 __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params &P, const RowSpan *rows, const Parts &u) {
     const DecodeKParams &p = P.k;
     float *mw = reinterpret_cast<float *>(smem);
-    float *lw = mw + NW * 8;
-    float *ow = lw + NW * 8;
-    for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
+    float *lw = mw + NW * R;
+    float *ow = lw + NW * R;
+    for (int idx = threadIdx.x; idx < R * (D / 4); idx += NW * 32) {
         const int h = idx / (D / 4), c = idx % (D / 4) * 4;
         if (rows[h].bi < 0) continue;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * 8 + h]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * R + h]);
         const float base = M == -INFINITY ? 0.f : M;   // the row sees none of this part's keys
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = exp2f(mw[w * 8 + h] - base);
-            const float4 o = *reinterpret_cast<const float4 *>(ow + (w * 8 + h) * D + c);
-            L += lw[w * 8 + h] * f;
+            const float f = exp2f(mw[w * R + h] - base);
+            const float4 o = *reinterpret_cast<const float4 *>(ow + (w * R + h) * D + c);
+            L += lw[w * R + h] * f;
             acc.x += o.x * f;
             acc.y += o.y * f;
             acc.z += o.z * f;
@@ -264,7 +240,7 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += NW * 32) {
+    for (int idx = threadIdx.x; idx < R * (D / 4); idx += NW * 32) {
         const int h = idx / (D / 4), c = idx % (D / 4) * 4;
         if (rows[h].bi < 0) continue;
         const size_t at = static_cast<size_t>(rows[h].bi) * p.splits;
@@ -291,34 +267,36 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
 
 // Row h of a balanced part, in units of D floats of ws_o and of one float of ws_lse: a warp's first
 // unit may have begun in the warp before (slot 0), its last may go on (slot 1).
+template <int R>
 __device__ __forceinline__ size_t part_at(const Parts &u, int h, int i) {
-    return (static_cast<size_t>(u.first + i) * 2 + (i == 0)) * 8 + h;
+    return (static_cast<size_t>(u.first + i) * 2 + (i == 0)) * R + h;
 }
 
-// The last warp to arrive merges a balanced unit's parts: lane l holds row l % 8 of every fourth
-// part's weight, and every lane four columns of all rows.
-template <int D>
-__device__ __forceinline__ void merge_unit(const AttendQ4Params &P, const RowSpan &me, const Parts &u, int lane) {
+// The last warp to arrive merges a balanced unit's parts: lane l holds row l % R of every SUB-th part's
+// weight (and bi, that row's place), and every lane four columns of all rows.
+template <int D, int R>
+__device__ __forceinline__ void merge_unit(const AttendQ4Params &P, int bi, const Parts &u, int lane) {
+    constexpr int SUB = 32 / R;
     const DecodeKParams &p = P.k;
-    const int row = lane & 7, sub = lane >> 3, col = lane * 4;
+    const int row = lane % R, sub = lane / R, col = lane * 4;
     float M = -INFINITY, L = 0.f;
-    for (int i = sub; i < u.n; i += 4) M = fmaxf(M, __ldcg(p.ws_lse + part_at(u, row, i)));
-    M = fmaxf(M, __shfl_xor_sync(kFull, M, 8));
-    M = fmaxf(M, __shfl_xor_sync(kFull, M, 16));
-    const float base = M == -INFINITY ? 0.f : M;   // a row past the sequence's last
-    float4 acc[8];
+    for (int i = sub; i < u.n; i += SUB) M = fmaxf(M, __ldcg(p.ws_lse + part_at<R>(u, row, i)));
 #pragma unroll
-    for (int h = 0; h < 8; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < u.n; i0 += 4) {
-        const float w = i0 + sub < u.n ? exp2f(__ldcg(p.ws_lse + part_at(u, row, i0 + sub)) - base) : 0.f;
+    for (int sh = R; sh < 32; sh *= 2) M = fmaxf(M, __shfl_xor_sync(kFull, M, sh));
+    const float base = M == -INFINITY ? 0.f : M;   // a row past the sequence's last
+    float4 acc[R];
+#pragma unroll
+    for (int h = 0; h < R; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < u.n; i0 += SUB) {
+        const float w = i0 + sub < u.n ? exp2f(__ldcg(p.ws_lse + part_at<R>(u, row, i0 + sub)) - base) : 0.f;
         L += w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < SUB; ++j) {
             if (i0 + j >= u.n) break;
-            const float *src = p.ws_o + part_at(u, 0, i0 + j) * D + col;
+            const float *src = p.ws_o + part_at<R>(u, 0, i0 + j) * D + col;
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const float f = __shfl_sync(kFull, w, j * 8 + h);
+            for (int h = 0; h < R; ++h) {
+                const float f = __shfl_sync(kFull, w, j * R + h);
                 const float4 o = col < D ? __ldcg(reinterpret_cast<const float4 *>(src + h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 acc[h].x = fmaf(f, o.x, acc[h].x);
                 acc[h].y = fmaf(f, o.y, acc[h].y);
@@ -327,34 +305,16 @@ __device__ __forceinline__ void merge_unit(const AttendQ4Params &P, const RowSpa
             }
         }
     }
-    L += __shfl_xor_sync(kFull, L, 8);
-    L += __shfl_xor_sync(kFull, L, 16);
-    const int bi = __shfl_sync(kFull, me.bi, row * 4);   // lane 4 * r holds row r's
-    if (lane < 8 && bi >= 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kDecLn2;
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
+    for (int sh = R; sh < 32; sh *= 2) L += __shfl_xor_sync(kFull, L, sh);
+    if (lane < R && bi >= 0 && p.lse != nullptr) p.lse[bi] = (M + log2f(L)) * kDecLn2;
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
         const float inv = 1.f / __shfl_sync(kFull, L, h);
         const int at = __shfl_sync(kFull, bi, h);
         if (at >= 0 && col < D)
             *reinterpret_cast<float4 *>(p.out + static_cast<size_t>(at) * D + col) =
                 make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
-    }
-}
-
-// Words per thread and group of `N` consecutive 32-bit words from shared memory.
-template <int N>
-__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
-    if constexpr (N == 4) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else if constexpr (N == 2) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        w[0] = u.x, w[1] = u.y;
-    } else if constexpr (N == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p), v = *reinterpret_cast<const uint4 *>(p + 16);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
 
@@ -382,25 +342,23 @@ __device__ __forceinline__ void write_new_row(const AttendQ4Params &p, int b, in
     if (lane % LANES == 0) reinterpret_cast<__half2 *>(page + bs * WORDS * 4)[off * G + lane / LANES] = par;
 }
 
-template <int D, int BS, int G>
-__global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerSm))
+template <int D, int BS, int G, typename Rows>
+__global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
     attend_q4_mma_kernel(const __grid_constant__ AttendQ4Params P) {
-    using Cfg = MmaCfg<D, BS, G>;
-    constexpr int NW = kMmaWarps, NT = kStageKeys / 8, PPS = Cfg::PPS, WORDS = Cfg::WORDS;
-    constexpr int WPT = WORDS / (4 * G);         // K: words per lane and group
-    constexpr int HPG = D / 32 / G;              // V: 32-dimension columns per group
-    static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
+    using Cfg = MmaCfg<D, BS, G, Rows>;
+    constexpr int R = Rows::ROWS, NW = kMmaWarps, PPS = Cfg::PPS;
     const DecodeKParams &p = P.k;
 
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ RowSpan s_rows[8];   // chunks: the tile's rows
+    __shared__ RowSpan s_rows[R];   // chunks: the tile's rows
 
     pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t4 = lane & 3;
+    const int g = lane >> 2;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff) + warp * kStages;
     uint8_t *ring = smem + warp * kStages * Cfg::kStageBytes;
-    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff + warp * Cfg::kQBytes) + lane;   // [step][lane]
+    Rows rows;
+    rows.qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff + warp * Rows::kQBytes) + lane;   // [step][lane]
     float *par = reinterpret_cast<float *>(smem + Cfg::kParOff + warp * Cfg::kParBytes);
     if (lane == 0) {
         for (int st = 0; st < kStages; ++st) mbar_init(smem_addr(&bars[st]), 1);
@@ -422,7 +380,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         int steps = 0, units = 0;
         for (int i = first; i < min(p.B, first + per); ++i) {
             const SeqRows sq = seq_rows(P, i, BS, false);
-            const int n = sq.pages > 0 ? p.Hkv * ((sq.nq * p.m + 7) / 8) : 0;
+            const int n = sq.pages > 0 ? p.Hkv * ((sq.nq * p.m + R - 1) / R) : 0;
             pre[i + 1] = n * ((sq.pages + PPS - 1) / PPS + kUnitCost);
             steps += pre[i + 1];
             units += n;
@@ -475,12 +433,12 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         SeqRows sq;
         if (P.balanced) {
             sq = seq_rows(P, b, BS, false);
-            int units = p.Hkv * ((sq.nq * p.m + 7) / 8);
+            int units = p.Hkv * ((sq.nq * p.m + R - 1) / R);
             while (sq.pages == 0 || unit == units) {   // on to the next sequence that has keys
                 ++b;
                 unit = 0;
                 sq = seq_rows(P, b, BS, false);
-                units = p.Hkv * ((sq.nq * p.m + 7) / 8);
+                units = p.Hkv * ((sq.nq * p.m + R - 1) / R);
             }
             kvh = unit % p.Hkv;
             tile = unit / p.Hkv;
@@ -505,7 +463,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             b = blockIdx.z;
             sq = seq_rows(P, b, BS, threadIdx.x == 0 && split == 0 && kvh == 0 && tile == 0);
             if (split == 0 && tile == 0) clear_rows(P, sq, kvh, D);
-            if (!sq.ok || 8 * tile >= sq.nq * p.m) return;
+            if (!sq.ok || R * tile >= sq.nq * p.m) return;
             // pages that any row of the sequence sees; this chunk's
             c0 = sq.first + split * p.chunk_pages;
             c1 = min(sq.first + sq.pages, c0 + p.chunk_pages);
@@ -521,10 +479,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             x = x1;
             turn = warp;
             turns = NW;
-            if (threadIdx.x < 8) s_rows[threadIdx.x] = tile_row(P, sq, kvh, 8 * tile + threadIdx.x);
+            if (threadIdx.x < R) s_rows[threadIdx.x] = tile_row(P, sq, kvh, R * tile + threadIdx.x);
         }
-        const RowSpan t_first = tile_row(P, sq, kvh, 8 * tile), t_last = tile_row(P, sq, kvh, min(8 * tile + 7, sq.nq * p.m - 1));
-        const RowSpan me = tile_row(P, sq, kvh, 8 * tile + g);
+        const RowSpan t_first = tile_row(P, sq, kvh, R * tile), t_last = tile_row(P, sq, kvh, min(R * tile + R - 1, sq.nq * p.m - 1));
+        const RowSpan me = tile_row(P, sq, kvh, R * tile + Rows::row(lane));
         const int pg0 = max(c0, t_first.lo / BS), pg1 = min(c1, (t_last.len + BS - 1) / BS);
         const int tok_end = pg1 * BS;   // the segment's keys end here
 
@@ -549,18 +507,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         }
 
         // the queries' loads start before the block table's
-        float qv[G * WPT][8];
-#pragma unroll
-        for (int u = 0; u < G * WPT; ++u) {
-            const float2 *src = reinterpret_cast<const float2 *>(p.q + static_cast<size_t>(max(me.bi, 0)) * D +
-                                                                 8 * ((u / WPT) * (WORDS / G) + t4 * WPT + u % WPT));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 y = me.bi >= 0 ? __ldg(src + e) : make_float2(0.f, 0.f);
-                qv[u][2 * e] = y.x;
-                qv[u][2 * e + 1] = y.y;
-            }
-        }
+        const int q_bi = tile_row(P, sq, kvh, R * tile + Rows::query_row(lane)).bi;
+        rows.load(q_bi >= 0 ? p.q + static_cast<size_t>(q_bi) * D : nullptr, lane);
 
         // ---- this warp's stages: steps of PPS pages turn, turn + turns, ... of [pg0, pg1)
         const int steps = pg1 > pg0 ? (pg1 - pg0 + PPS - 1) / PPS : 0;
@@ -609,57 +557,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         int issued = min(kStages, n_my);
         for (int k = 0; k < issued; ++k) issue(k);
 
-        // ---- query fragments, while the copies fly.  MMA steps 2u and 2u + 1 of word u = gi * WPT + i:
-        // elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours / 16
-        float f, qsum[G];   // score (base 2) = MMA sum * f; the groups' sums of q in the MMAs' units
-        {
-            float(&v)[G * WPT][8] = qv, amax = 0.f;
-#pragma unroll
-            for (int u = 0; u < G * WPT; ++u)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[u][e]));
-            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-            // |q| * 2^up in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
-            const int up = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
-            const float scale = pow2i(up);
-            f = (p.scale_log2 * 0x1p24f) * pow2i(-up);
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < WPT; ++i) {
-                    const int u = gi * WPT + i;
-                    uint4 e, o;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[u][j] *= scale;
-                        sum += v[u][j];
-                    }
-#pragma unroll
-                    for (int j = 1; j < 8; j += 2) v[u][j] *= 0.0625f;
-                    split2(v[u][0], v[u][4], e.x, e.y);
-                    split2(v[u][2], v[u][6], e.z, e.w);
-                    split2(v[u][1], v[u][5], o.x, o.y);
-                    split2(v[u][3], v[u][7], o.z, o.w);
-                    qfrag[(2 * u) * 32] = e;
-                    qfrag[(2 * u + 1) * 32] = o;
-                }
-                sum += __shfl_xor_sync(kFull, sum, 1);
-                sum += __shfl_xor_sync(kFull, sum, 2);
-                qsum[gi] = sum * 0x1p-24f;
-            }
-        }
-
-        float oT[D / 16][4];
-        float2 zo[G];   // sums of weight * zero over this lane's keys
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) oT[mt][0] = oT[mt][1] = oT[mt][2] = oT[mt][3] = 0.f;
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) zo[gi] = make_float2(0.f, 0.f);
-        float m_run = -INFINITY, l_run = 0.f;   // the running max, and l relative to `ref`
-        float ref = -INFINITY;                  // m_run + E - 14
-        float vs_max = 0.f, vs_exp = -24.f;     // the largest V scale seen; E, its exponent rounded up
+        rows.begin(p.scale_log2, lane);   // while the copies fly
 
         int k = 0;
         for (; k < n_my; ++k) {
@@ -678,160 +576,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
             // pages that are not there become 0; codes are finite whatever they are
             const bool seen = tok0 + lane >= t_first.lo && tok0 + lane < min(t_last.len, tok_end) &&
                               !(bad >> (st * PPS + lane / BS) & 1);
-            const int par_at = (lane / BS) * Cfg::kPageBytes + Cfg::kCodeBytes + (lane % BS) * G * 4;
-            auto widen = [&](const uint8_t *pages, float centred) {
-                uint32_t v[G];
-                lds_words<G>(pages + par_at, v);
-                float top = 0.f;
-#pragma unroll
-                for (int gi = 0; gi < G; ++gi) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v[gi]));
-                    par[gi * 64 + lane] = seen ? y.x : 0.f;
-                    par[gi * 64 + 32 + lane] = seen ? fmaf(centred, y.x, y.y) : 0.f;
-                    top = fmaxf(top, seen ? y.x : 0.f);
-                }
-                return top;
-            };
-
-            // ---- scores of row g for keys 8 * nt + 2 * t4 + {0, 1}
-            widen(kpages, 0.f);
-            __syncwarp();
-            float2 s[NT];
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                float a[NT][4];
-                uint32_t c[NT][WPT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    lds_words<WPT>(kpages + (nt * 8 / BS) * Cfg::kPageBytes + (nt * 8 % BS + g) * (D / 2) + gi * (D / 2 / G) +
-                                       t4 * WPT * 4,
-                                   c[nt]);
-                }
-#pragma unroll
-                for (int i = 0; i < WPT; ++i) {
-                    const uint4 e = qfrag[(2 * (gi * WPT + i)) * 32], o = qfrag[(2 * (gi * WPT + i) + 1) * 32];
-                    // the tiles' chains side by side
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t x = c[nt][i] & 0x000f000fu, y = (c[nt][i] >> 8) & 0x000f000fu;
-                        if (i == 0) mma16_first(a[nt], e.x, e.y, e.z, e.w, x, y);
-                        else mma16(a[nt], e.x, e.y, e.z, e.w, x, y);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16(a[nt], o.x, o.y, o.z, o.w, c[nt][i] & 0x00f000f0u, (c[nt][i] >> 8) & 0x00f000f0u);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float2 sc = *reinterpret_cast<const float2 *>(par + gi * 64 + nt * 8 + 2 * t4);
-                    const float2 ze = *reinterpret_cast<const float2 *>(par + gi * 64 + 32 + nt * 8 + 2 * t4);
-                    const float2 qz = make_float2(qsum[gi], qsum[gi]);
-                    const float2 y = gi == 0 ? mul2(ze, qz) : fma2(ze, qz, s[nt]);
-                    s[nt] = fma2(sc, add2(make_float2(a[nt][0], a[nt][1]), make_float2(a[nt][2], a[nt][3])), y);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt] = mul2(s[nt], make_float2(f, f));
-            if (!whole) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int tok = tok0 + nt * 8 + 2 * t4, end = min(me.len, tok_end);
-                    if (tok < me.lo || tok >= end) s[nt].x = -INFINITY;
-                    if (tok + 1 < me.lo || tok + 1 >= end) s[nt].y = -INFINITY;
-                }
-            }
-            __syncwarp();   // K's parameters have been read
-
-            // ---- the running reference: the rows' maxima and the largest V scale
-            const float top = widen(vpages, 8.f);
-            float mx = fmaxf(s[0].x, s[0].y);
-#pragma unroll
-            for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            m_run = fmaxf(m_run, mx);
-            if (__any_sync(kFull, top > vs_max)) {   // rarely after the first stage: the next power of two
-                // non-negative floats order like their bits
-                vs_max = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(top, vs_max))));
-                vs_exp = fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(vs_max) + 0x7fffffu) >> 23) - 127), -24.f);
-            }
-            const float ref_new = m_run + (vs_exp - 14.f);
-            // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
-            const float base = ref_new == -INFINITY ? 0.f : ref_new;
-            const float alpha = ref == -INFINITY ? 1.f : ex2_approx(ref - base);   // nothing to rescale yet
-            ref = ref_new;
-            float2 psum = make_float2(0.f, 0.f), w[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float2 e = add2(s[nt], make_float2(-base, -base));
-                w[nt] = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                psum = add2(psum, w[nt]);
-            }
-            l_run = l_run * alpha + (psum.x + psum.y);
-            const float2 rescale = make_float2(__shfl_sync(kFull, alpha, 8 * t4), __shfl_sync(kFull, alpha, 8 * t4 + 4));
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
-            __syncwarp();   // V's parameters have been written
-
-            // ---- O^T = O^T alpha + V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit
-            // units (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1
-            // in one register: the pairs along the keys that the A operand wants
-            constexpr int KT = kStageKeys / 16, N = HPG >= 2 ? 2 : 1;   // N columns of 32 dimensions at a time
-            const uint32_t vrow = smem_addr(vpages) + (lane & 15) * (D / 2) + (HPG >= 2 ? (lane >> 4) * 16 : 0);
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
-                uint32_t ph[KT][2], pl[KT][2];
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const float *src = par + gi * 64 + kt * 16 + 2 * t4;
-                    const float2 wa = w[2 * kt], wb = w[2 * kt + 1];
-                    split2(mul2(wa, *reinterpret_cast<const float2 *>(src)), ph[kt][0], pl[kt][0]);
-                    split2(mul2(wb, *reinterpret_cast<const float2 *>(src + 8)), ph[kt][1], pl[kt][1]);
-                    zo[gi] = fma2(wa, *reinterpret_cast<const float2 *>(src + 32),
-                                  fma2(wb, *reinterpret_cast<const float2 *>(src + 40), zo[gi]));
-                }
-#pragma unroll
-                for (int h = 0; h < HPG; h += N) {
-                    const int c = gi * HPG + h;
-                    float sum[2 * N][4];   // even and odd elements of each column
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        // registers: units 8 * c of keys 0..7, of keys 8..15, units 8 * (c + 1) likewise
-                        const uint32_t rows = vrow + (kt * 16 / BS) * Cfg::kPageBytes + (kt * 16 % BS) * (D / 2) + c * 16;
-                        uint32_t v[4], e[2 * N][2], o[2 * N][2];
-                        if constexpr (N == 2) ldsm_x4_trans(rows, v[0], v[1], v[2], v[3]);
-                        else ldsm_x2_trans(rows, v[0], v[1]);
-#pragma unroll
-                        for (int i = 0; i < 2 * N; ++i) {
-                            centre(v[i], e[i][0], o[i][0]);
-                            centre(v[i] >> 8, e[i][1], o[i][1]);
-                        }
-#pragma unroll
-                        for (int lo = 0; lo < 2; ++lo) {   // the weights' high parts, then their low ones
-                            const uint32_t b0 = lo ? pl[kt][0] : ph[kt][0], b1 = lo ? pl[kt][1] : ph[kt][1];
-#pragma unroll
-                            for (int i = 0; i < N; ++i) {
-                                if (kt == 0 && lo == 0) {
-                                    mma16_first(sum[2 * i], e[2 * i][0], e[2 * i][1], e[2 * i + 1][0], e[2 * i + 1][1], b0, b1);
-                                    mma16_first(sum[2 * i + 1], o[2 * i][0], o[2 * i][1], o[2 * i + 1][0], o[2 * i + 1][1], b0, b1);
-                                } else {
-                                    mma16(sum[2 * i], e[2 * i][0], e[2 * i][1], e[2 * i + 1][0], e[2 * i + 1][1], b0, b1);
-                                    mma16(sum[2 * i + 1], o[2 * i][0], o[2 * i][1], o[2 * i + 1][0], o[2 * i + 1][1], b0, b1);
-                                }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * N; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; r += 2) {
-                            float(&acc)[4] = oT[2 * c + i];
-                            const float2 y = fma2(make_float2(acc[r], acc[r + 1]), rescale, make_float2(sum[i][r], sum[i][r + 1]));
-                            acc[r] = y.x;
-                            acc[r + 1] = y.y;
-                        }
-                }
-            }
+            rows.stage(kpages, vpages, par, seen, tok0, whole ? -1 : tok_end, me, lane);
             __syncwarp();
             if (k + kStages < n_my) {
                 issue(k + kStages);
@@ -846,39 +591,25 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         }
         cnt += n_my;
 
-        l_run += __shfl_xor_sync(kFull, l_run, 1);
-        l_run += __shfl_xor_sync(kFull, l_run, 2);
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) {
-            zo[gi].x += zo[gi].y;
-            zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 1);
-            zo[gi].x += __shfl_xor_sync(kFull, zo[gi].x, 2);
-        }
-        // this lane's outputs of rows 2 * t4 + r: dimensions 32 * c + 4 * g + {0, 1, 2, 3}
-        auto outputs = [&](int c, int r) {
-            const float z = __shfl_sync(kFull, zo[c / HPG].x, 8 * t4 + 4 * r);
-            const float (&e)[4] = oT[2 * c], (&o)[4] = oT[2 * c + 1];
-            return make_float4(fmaf(e[r], 0x1p9f, z), fmaf(o[r], 0x1p9f, z), fmaf(e[2 + r], 0x1p9f, z), fmaf(o[2 + r], 0x1p9f, z));
-        };
+        rows.end();
 
         if (P.balanced) {
             if (gave_up) return;   // lanes together; the block's other warps go on
-            const float inv = ref == -INFINITY ? 0.f : 1.f / l_run;   // no key of this part for the row
-            const float lse2 = ref == -INFINITY ? -INFINITY : ref + log2f(l_run);
-            if (t4 == 0 && me.bi >= 0) {
-                if (part.n > 1) p.ws_lse[part_at(part, g, part.own)] = lse2;
-                else if (p.lse != nullptr) p.lse[me.bi] = lse2 * kDecLn2;
+            const bool empty = rows.ref == -INFINITY;   // no key of this part for the row
+            const float inv = empty ? 0.f : 1.f / rows.l, lse2 = empty ? -INFINITY : rows.ref + log2f(rows.l);
+            if (Rows::owner(lane)) {
+                if (part.n > 1) p.ws_lse[part_at<R>(part, Rows::row(lane), part.own)] = me.bi >= 0 ? lse2 : -INFINITY;
+                else if (me.bi >= 0 && p.lse != nullptr) p.lse[me.bi] = lse2 * kDecLn2;
             }
-            if (t4 == 0 && me.bi < 0 && part.n > 1) p.ws_lse[part_at(part, g, part.own)] = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float il = __shfl_sync(kFull, inv, 8 * t4 + 4 * r);
-                const int bi = __shfl_sync(kFull, me.bi, 8 * t4 + 4 * r);
-                float *dst = part.n > 1 ? p.ws_o + part_at(part, 2 * t4 + r, part.own) * D
+            for (int r = 0; r < Rows::OUT; ++r) {
+                const float il = Rows::of_out_row(inv, r, lane);
+                const int bi = Rows::of_out_row(me.bi, r, lane);
+                float *dst = part.n > 1 ? p.ws_o + part_at<R>(part, Rows::out_row(r, lane), part.own) * D
                                         : p.out + static_cast<size_t>(max(bi, 0)) * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    const float4 y = outputs(c, r);
+                    const float4 y = rows.output(c, r, lane);
                     if (part.n > 1 || bi >= 0)
                         *reinterpret_cast<float4 *>(dst + 32 * c + 4 * g) = make_float4(y.x * il, y.y * il, y.z * il, y.w * il);
                 }
@@ -893,7 +624,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
                 }
                 if (__shfl_sync(kFull, last, 0)) {
                     __threadfence();
-                    merge_unit<D>(P, me, part, lane);
+                    merge_unit<D, R>(P, Rows::of_merge_row(me.bi, lane), part, lane);
                 }
             }
             continue;
@@ -902,44 +633,43 @@ __global__ void __launch_bounds__(kMmaWarps * 32, (MmaCfg<D, BS, G>::kBlocksPerS
         // ---- the warps' (ref, l, O) through shared memory (the ring is free now)
         if (__syncthreads_or(gave_up)) return;
         float *mw = reinterpret_cast<float *>(smem);
-        float *lw = mw + NW * 8;
-        float *ow = lw + NW * 8;
-        if (t4 == 0) {
-            mw[warp * 8 + g] = ref;
-            lw[warp * 8 + g] = l_run;
+        float *lw = mw + NW * R;
+        float *ow = lw + NW * R;
+        if (Rows::owner(lane)) {
+            mw[warp * R + Rows::row(lane)] = rows.ref;
+            lw[warp * R + Rows::row(lane)] = rows.l;
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < Rows::OUT; ++r)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
-                *reinterpret_cast<float4 *>(ow + (warp * 8 + 2 * t4 + r) * D + 32 * c + 4 * g) = outputs(c, r);
+                *reinterpret_cast<float4 *>(ow + (warp * R + Rows::out_row(r, lane)) * D + 32 * c + 4 * g) = rows.output(c, r, lane);
         __syncthreads();
-        finish_rows<D, NW>(smem, P, s_rows, part);
+        finish_rows<D, NW, R>(smem, P, s_rows, part);
     }
 }
 
-template <int D, int BS, int G>
+template <int D, int BS, int G, typename Rows>
 cudaError_t launch_mma_as(const AttendQ4Params &P, dim3 grid, cudaStream_t stream) {
-    using Cfg = MmaCfg<D, BS, G>;
+    using Cfg = MmaCfg<D, BS, G, Rows>;
     static std::atomic<unsigned long long> done{0};
-    auto kernel = attend_q4_mma_kernel<D, BS, G>;
+    auto kernel = attend_q4_mma_kernel<D, BS, G, Rows>;
     const cudaError_t e = set_smem_once(kernel, Cfg::kSmemBytes, done);
     if (e != cudaSuccess) return e;
     kernel<<<grid, kMmaWarps * 32, Cfg::kSmemBytes, stream>>>(P);
     return cudaGetLastError();
 }
 
+template <template <int, int, int> class Rows>
 cudaError_t launch_mma(const AttendQ4Params &P, int d, int bs, int G, dim3 grid, cudaStream_t stream) {
+#define PKV_Q4_MMA(DD, BB, GG) launch_mma_as<DD, BB, GG, Rows<DD, BB, GG>>(P, grid, stream)
     if (bs == 16) {
-        if (d == 64) return G == 1 ? launch_mma_as<64, 16, 1>(P, grid, stream) : launch_mma_as<64, 16, 2>(P, grid, stream);
-        return G == 1   ? launch_mma_as<128, 16, 1>(P, grid, stream)
-               : G == 2 ? launch_mma_as<128, 16, 2>(P, grid, stream)
-                        : launch_mma_as<128, 16, 4>(P, grid, stream);
+        if (d == 64) return G == 1 ? PKV_Q4_MMA(64, 16, 1) : PKV_Q4_MMA(64, 16, 2);
+        return G == 1 ? PKV_Q4_MMA(128, 16, 1) : G == 2 ? PKV_Q4_MMA(128, 16, 2) : PKV_Q4_MMA(128, 16, 4);
     }
-    if (d == 64) return G == 1 ? launch_mma_as<64, 32, 1>(P, grid, stream) : launch_mma_as<64, 32, 2>(P, grid, stream);
-    return G == 1   ? launch_mma_as<128, 32, 1>(P, grid, stream)
-           : G == 2 ? launch_mma_as<128, 32, 2>(P, grid, stream)
-                    : launch_mma_as<128, 32, 4>(P, grid, stream);
+    if (d == 64) return G == 1 ? PKV_Q4_MMA(64, 32, 1) : PKV_Q4_MMA(64, 32, 2);
+    return G == 1 ? PKV_Q4_MMA(128, 32, 1) : G == 2 ? PKV_Q4_MMA(128, 32, 2) : PKV_Q4_MMA(128, 32, 4);
+#undef PKV_Q4_MMA
 }
 
 cudaError_t launch_simt(const AttendQ4Args &a, const DecodeKParams &kp, cudaStream_t stream) {
@@ -967,14 +697,6 @@ size_t partial_bytes(long long rows, int Hq, int splits, int d) {
 }  // namespace
 
 namespace {
-int q4_blocks_per_sm(int d, int bs, int G) {
-    if (bs == 16) {
-        if (d == 64) return G == 1 ? MmaCfg<64, 16, 1>::kBlocksPerSm : MmaCfg<64, 16, 2>::kBlocksPerSm;
-        return G == 1 ? MmaCfg<128, 16, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 16, 2>::kBlocksPerSm : MmaCfg<128, 16, 4>::kBlocksPerSm;
-    }
-    if (d == 64) return G == 1 ? MmaCfg<64, 32, 1>::kBlocksPerSm : MmaCfg<64, 32, 2>::kBlocksPerSm;
-    return G == 1 ? MmaCfg<128, 32, 1>::kBlocksPerSm : G == 2 ? MmaCfg<128, 32, 2>::kBlocksPerSm : MmaCfg<128, 32, 4>::kBlocksPerSm;
-}
 // (Query row, head) pairs of a sequence and KV head that the warp-MMA kernel, which takes eight at a
 // time, is faster for than the tcgen05 kernel, whose time hardly depends on them.  4 x 65536 tokens, one
 // scale group a row: 24 pairs 37.3 us, the tcgen05 kernel 34.0 (32 pairs); 64 x 2048 tokens, four KV heads:
@@ -984,7 +706,7 @@ int q4_mma_slots(int G) { return G == 1 ? 24 : 32; }
 
 // Rows of partial results of a balanced launch: two units for every warp or block.
 size_t balanced_rows(const Q4Plan &plan) {
-    return static_cast<size_t>(plan.blocks) * 2 * (plan.umma ? kQ4UmmaSlots : kMmaWarps * 8);
+    return static_cast<size_t>(plan.blocks) * 2 * (plan.umma ? kQ4UmmaSlots : kMmaWarps * plan.mma_rows);
 }
 }  // namespace
 
@@ -995,7 +717,8 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     const long long slots = static_cast<long long>(max_q) * m;
     plan.umma = q4_umma_shape(d, group, bs) && aligned && slots > q4_mma_slots(d / group) && slots < (1 << 20);
     plan.mma = !plan.umma && (d == 64 || d == 128) && (bs == 16 || bs == 32) && d / group <= 4 && aligned && slots < (1 << 20);
-    const int per_tile = plan.umma ? kQ4UmmaSlots : 8;
+    plan.mma_rows = slots <= FourRows<64, 16, 1>::ROWS ? FourRows<64, 16, 1>::ROWS : EightRows<64, 16, 1>::ROWS;
+    const int per_tile = plan.umma ? kQ4UmmaSlots : plan.mma_rows;
     plan.tiles = plan.umma || plan.mma ? static_cast<int>((slots + per_tile - 1) / per_tile) : 1;
     const long long units = plan.umma || plan.mma ? static_cast<long long>(B) * Hkv * plan.tiles : static_cast<long long>(rows) * Hq;
     int chunk = pages;
@@ -1006,7 +729,7 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         // so few that one would be left to merge parts from many: then, or with more sequences than a
         // block scans, equal chunks for one wave of blocks and a merge over many blocks.
         const int step = plan.umma ? 128 / (d / group) : kStageKeys;
-        plan.blocks = plan.umma ? sms : q4_blocks_per_sm(d, bs, d / group) * sms;
+        plan.blocks = sms * (plan.umma ? 1 : plan.mma_rows == 4 ? FourRows<64, 16, 1>::kBlocksPerSm : EightRows<64, 16, 1>::kBlocksPerSm);
         plan.balanced = B <= kMaxBalanced && (plan.umma ? plan.blocks <= 8 * units : plan.blocks * kMmaWarps <= 24 * units) &&
                         units * (static_cast<long long>(pages) * bs / step + 1 + kUnitCost) < (1ll << 30);
         const int least = 256 / bs;
@@ -1083,7 +806,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         P.balanced = plan.balanced;
         const dim3 grid = plan.balanced ? dim3(plan.blocks) : dim3(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
         e = plan.umma ? launch_attend_q4_umma(P, a.d, a.bs, a.d / a.group, grid, stream)
-                      : launch_mma(P, a.d, a.bs, a.d / a.group, grid, stream);
+            : plan.mma_rows == 4 ? launch_mma<FourRows>(P, a.d, a.bs, a.d / a.group, grid, stream)
+                                 : launch_mma<EightRows>(P, a.d, a.bs, a.d / a.group, grid, stream);
     } else {
         e = launch_simt(a, kp, stream);
     }

@@ -134,9 +134,10 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 // ------------------------------------------------- attention over a 4-bit cache
 
 struct Q4Plan {
-    bool umma;           // more than 8 (query row, head) pairs per sequence and KV head: the tcgen05 kernel
+    bool umma;           // many (query row, head) pairs per sequence and KV head: the tcgen05 kernel
     bool mma;            // d 64 or 128, bs 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
-    int tiles;           // tiles of 64 (umma) or 8 pairs per sequence and KV head
+    int mma_rows;        // mma: pairs of a tile, 4 or 8
+    int tiles;           // tiles of 64 (umma) or mma_rows pairs per sequence and KV head
     bool balanced;       // even shares of all sequences' keys for `blocks` thread blocks
     int blocks;
     bool fused_merge;    // the last chunk of a unit merges (counters in the workspace)
