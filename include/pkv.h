@@ -474,6 +474,7 @@ pkv_status pkv_decode_step_q4(float *out, float *lse, const float *q, const void
  *   cu_new            int32 [B + 1]; usable as cu_q of pkv_paged_attention*
  *   slot_mapping      int64 [T], T >= sum n; entries from cu_new[B] on become -1 (padding)
  *   free_count_out    int32 [1]
+ * A free_count outside [0, NB] sets PKV_DEVERR_POOL, counts as no free blocks and is passed on.
  * A row with L < 0, n < 0 or L + n > MBS * bs sets PKV_DEVERR_LEN.  A row for which the blocks
  * needed by it and the rows before it exceed the free ones (rows that need none are served all
  * the same), or the tokens of it and the rows before it exceed T, sets PKV_DEVERR_POOL.  Such a
@@ -500,7 +501,8 @@ pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_
  * (a finished row's becomes 0).  A range outside [0, MBS] sets PKV_DEVERR_LEN and an entry outside
  * [0, NB) PKV_DEVERR_BLOCK; those are skipped.  More blocks than the list has room for (some were
  * given back twice) set PKV_DEVERR_POOL and nothing is given back.
- *   workspace   pkv_block_tables_release_workspace_bytes(B) bytes, 4-byte aligned (contents free)
+ *   workspace   pkv_block_tables_release_workspace_bytes(B) bytes, 4-byte aligned (contents free;
+ *               calls that share it must not overlap)
  */
 size_t pkv_block_tables_release_workspace_bytes(int B);
 

@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
     const long long capacity = static_cast<long long>(a.MBS) * a.bs;
-    int count = __ldg(a.free_count);
+    const int given = __ldg(a.free_count);
+    int count = given;
     if (count < 0 || count > a.NB) {
         if (lead && tid == 0) raise_error(a.err, PKV_DEVERR_POOL);
         count = 0;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
     }
     for (int row = tid; row < a.B; row += kRows)
         a.context_lens_out[row] = a.context_lens[row] + (__ldcg(a.cu_new + row + 1) - __ldcg(a.cu_new + row));
-    if (tid == 0) a.free_count_out[0] = count - taken;
+    if (tid == 0) a.free_count_out[0] = given - taken;
 }
 
 // The row's range of table entries, empty when it is out of bounds (flagged once, by `report`).

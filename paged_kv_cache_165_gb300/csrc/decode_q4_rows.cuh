@@ -259,6 +259,19 @@ struct EightRows {
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) zo[gi] = mul2(zo[gi], make_float2(alpha, alpha));
         __syncwarp();   // V's parameters have been written
+        if (end >= 0) {   // a key that only another row sees may hold a NaN: the zeros' part here, past it
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 z = *reinterpret_cast<const float2 *>(par + gi * 64 + 32 + nt * 8 + 2 * t4);
+                    zo[gi] = fma2(w[nt], make_float2(w[nt].x != 0.f ? z.x : 0.f, w[nt].y != 0.f ? z.y : 0.f), zo[gi]);
+                }
+            __syncwarp();
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) par[gi * 64 + 32 + lane] = 0.f;
+            __syncwarp();
+        }
 
         // ---- O^T = O^T alpha + V^T P^T, 16 keys per step.  ldmatrix with transposition over 16-bit
         // units (four codes of a key) hands lane (g, t4) the units 8 * c + g of keys 2 * t4, 2 * t4 + 1
@@ -503,7 +516,20 @@ struct FourRows {
             sum_w += w[j];
         }
         l = fmaf(l, alpha, sum_w);
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) zo[gi] *= alpha;
         __syncwarp();   // V's parameters have been written
+        if (end >= 0) {   // a key that only another row sees may hold a NaN: the zeros' part here, past it
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (w[j] != 0.f) zo[gi] = fmaf(w[j], pairs[gi * 32 + 8 * j + g].y, zo[gi]);
+            __syncwarp();
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) pairs[gi * 32 + lane].y = 0.f;
+            __syncwarp();
+        }
 
         // O^T = O^T alpha + V^T P^T as for eight rows, N columns of 32 dimensions at a time
         constexpr int KT = kStageKeys / 16, N = HPG >= 2 ? 2 : 1;
@@ -512,7 +538,6 @@ struct FourRows {
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
             uint32_t b[NT];   // B operand of 8 keys
-            zo[gi] *= alpha;
 #pragma unroll
             for (int j = 0; j < NT; j += 2) {
                 const float2 p = pairs[gi * 32 + 8 * j + g], r = pairs[gi * 32 + 8 * j + 8 + g];

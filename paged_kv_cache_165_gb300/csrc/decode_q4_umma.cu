@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                     }
                 }
                 const int tok0 = g.pg0 * BS + t * TK, end = min(me.len, g.tok_end);
-                if (tok0 < me.lo || tok0 + TK > end) {
+                const bool partial = tok0 < me.lo || tok0 + TK > end;   // of a tile
+                if (partial) {
 #pragma unroll
                     for (int k = 0; k < TK / 8; ++k) {
                         const int tok = tok0 + 8 * k + 2 * c4;
@@ -557,7 +558,11 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                     for (int k = 0; k < 8; k += 2) {
                         const int kk = G == 1 ? 8 * h + k : k;
                         const float4 a = *reinterpret_cast<const float4 *>(pv + gi * C::kParRow + 2 * kk);
-                        const float4 z = *reinterpret_cast<const float4 *>(pv + (G + gi) * C::kParRow + 2 * kk);
+                        float4 z = *reinterpret_cast<const float4 *>(pv + (G + gi) * C::kParRow + 2 * kk);
+                        if (partial) {   // a key that another slot sees may hold a NaN
+                            z.x = sc[kk].x != 0.f ? z.x : 0.f, z.y = sc[kk].y != 0.f ? z.y : 0.f;
+                            z.z = sc[kk + 1].x != 0.f ? z.z : 0.f, z.w = sc[kk + 1].y != 0.f ? z.w : 0.f;
+                        }
                         split2(mul2(sc[kk], make_float2(a.x, a.y)), pw[h][2 * k], pw[h][2 * k + 1]);
                         split2(mul2(sc[kk + 1], make_float2(a.z, a.w)), pw[h][2 * k + 2], pw[h][2 * k + 3]);
                         zo[gi] = fma2(sc[kk], make_float2(z.x, z.y), fma2(sc[kk + 1], make_float2(z.z, z.w), zo[gi]));

@@ -108,6 +108,10 @@ def test_extend_flags_bad_block_ids_and_counts():
     got = extend(table[:1], [0], [17], free, 5, 16, 17)      # more free blocks than the list holds
     assert pkv.get_device_error() & pkv.DEVERR["pool"]
     assert got[1].tolist() == [0]
+    for count in (5, -3):                                    # passed on; rows that need no block are served
+        got = extend(np.array([[2, -1]], np.int32), [3], [4], free, count, 16, 4)
+        assert pkv.get_device_error() == pkv.DEVERR["pool"]
+        assert got[1].tolist() == [7] and got[3].tolist() == [35, 36, 37, 38] and got[4] == count
 
 
 def release(table, first, end, free, count):

@@ -325,6 +325,32 @@ def test_q4_large_and_masked_values(hq, hkv):
         assert_attn_close(lse[live], ref_lse, f"q * {f} lse", ATOL)
 
 
+@pytest.mark.parametrize("hq,hkv,d,group,bs,rows,window", [
+    (1, 1, 128, 64, 16, 4, 0), (2, 1, 64, 32, 32, 2, 20), (8, 2, 128, 64, 16, 2, 0), (4, 1, 128, 128, 16, 4, 30),
+    (16, 1, 128, 64, 16, 4, 0), (16, 1, 64, 64, 32, 4, 70), (4, 2, 96, 32, 16, 3, 9)])
+def test_q4_a_nan_reaches_only_the_rows_that_see_it(hq, hkv, d, group, bs, rows, window):
+    """K and V of the last token, and of the token that only the first row's window reaches, are NaN."""
+    n = 150
+    case = q4_case(23, [n, 40], hq, hkv, d, group, bs, [rows, rows])
+    q, kc, vc, table, lens, cu = case
+    bad = [n - 1] + ([n - rows - window + 1] if window else [])
+    pages = row_bytes(d, group) * bs
+    for pos in bad:
+        blk, off = int(table[0, pos // bs]), pos % bs
+        for cache in (kc, vc):
+            page = cache.view(cache.shape[0], hkv, pages)[blk]
+            at = bs * d // 2 + off * 4 * (d // group)
+            page[:, at:at + 4 * (d // group)] = torch.tensor([0, 0, 0xff, 0x7f] * (d // group), dtype=torch.uint8)
+    out, lse = run_q4(case, group, 0.1, window, decode=False, max_q=rows)
+    live, ref, ref_lse = expect(case, group, 0.1, window)   # NaN parameters read as 0 there
+    clean = [i for i in range(2 * rows) if i != rows - 1 and not (window and i == 0)]
+    assert_attn_close(out[clean], ref[clean], "rows that do not see it", ATOL)
+    assert_attn_close(lse[clean], ref_lse[clean], "lse", ATOL)
+    assert torch.isnan(out[rows - 1]).all()
+    if window:
+        assert torch.isnan(out[0]).all()
+
+
 def test_q4_workspace_too_small_is_refused():
     case = q4_case(3, [4000], 8, 1, 128, 64, 16)
     q, kc, vc, table, lens, _ = [dev(t) for t in case]
