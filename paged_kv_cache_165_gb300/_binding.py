@@ -174,6 +174,14 @@ def _cuda(name, t, dtype=None):
     return t
 
 
+def _here(what, *tensors) -> None:
+    """The kernels run on the current device: its tensors only."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{what}: a tensor is on device {t.get_device()}, the current one is {here}")
+
+
 def _dtype(t) -> int:
     if t.dtype not in _DTYPES:
         raise TypeError(f"unsupported element type {t.dtype} (fp32, bf16 or uint8 E4M3 codes)")
@@ -578,6 +586,7 @@ def _q4_rows(what, fn, k_rows, v_rows, k_cache, v_cache, slot_mapping, group, st
     NB, Hkv, bs = _q4_caches(what, k_cache, v_cache, d, group)
     if tuple(k_rows.shape) != (T, Hkv, d) or tuple(v_rows.shape) != (T, Hkv, d) or slot_mapping.numel() != T:
         raise ValueError(f"{what}: shapes do not match [T][Hkv][d] / [T]")
+    _here(what, k_rows, v_rows, k_cache, v_cache, slot_mapping)
     _check(fn(_ptr(k_rows), _ptr(v_rows), dt, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, d, int(group), bs,
               NB, _stream(stream)))
 
@@ -618,6 +627,7 @@ def _q4_attend_args(what, out, q, k_cache, v_cache, block_table, context_lens, g
     if workspace is not None:
         _cuda("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
+    _here(what, q, out, k_cache, v_cache, block_table, context_lens, lse, workspace)
     return B, Tq, Hq, Hkv, d, bs, NB, block_table.shape[1], ws_bytes
 
 
@@ -631,6 +641,7 @@ def paged_attention_q4(out, q, k_cache, v_cache, block_table, context_lens, scal
         _cuda("cu_q", cu_q, torch.int32)
     if (cu_q is not None and cu_q.numel() != B + 1) or (cu_q is None and Tq != B):
         raise ValueError("paged_attention_q4: shapes do not match")
+    _here("paged_attention_q4", cu_q)
     _check(lib().pkv_paged_attention_q4(
         _ptr(out), _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(context_lens), _ptr(cu_q),
         B, Tq, int(max_q), Hq, Hkv, d, int(group), bs, MBS, NB, float(scale), int(window), int(num_splits),
@@ -649,6 +660,7 @@ def decode_step_q4(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_t
     _cuda("slot_mapping", slot_mapping, torch.int64)
     if Tq != B or tuple(k_new.shape) != (B, Hkv, d) or tuple(v_new.shape) != (B, Hkv, d) or slot_mapping.numel() != B:
         raise ValueError("decode_step_q4: shapes do not match")
+    _here("decode_step_q4", k_new, v_new, slot_mapping)
     _check(lib().pkv_decode_step_q4(
         _ptr(out), _ptr(lse), _ptr(q), _ptr(k_new), _ptr(v_new), new_dt, _ptr(slot_mapping), _ptr(k_cache),
         _ptr(v_cache), _ptr(block_table), _ptr(context_lens), B, Hq, Hkv, d, int(group), bs, MBS, NB, float(scale),
@@ -687,6 +699,8 @@ def block_tables_extend(block_table, context_lens, new_tokens, free_list, free_c
     if workspace is not None:
         _cuda("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
+    _here("block_tables_extend", block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
+          slot_mapping, free_count_out, workspace)
     _check(lib().pkv_block_tables_extend(
         _ptr(block_table), _ptr(context_lens), _ptr(new_tokens), _ptr(free_list), _ptr(free_count),
         _ptr(context_lens_out), _ptr(cu_new), _ptr(slot_mapping), _ptr(free_count_out), B, slot_mapping.numel(), MBS,
@@ -712,6 +726,7 @@ def block_tables_release(block_table, first_block, end_block, free_list, free_co
     if workspace is not None:
         _cuda("workspace", workspace)
         ws_bytes = workspace.numel() * workspace.element_size()
+    _here("block_tables_release", block_table, first_block, end_block, free_list, free_count, free_count_out, workspace)
     _check(lib().pkv_block_tables_release(
         _ptr(block_table), _ptr(first_block), _ptr(end_block), _ptr(free_list), _ptr(free_count), _ptr(free_count_out),
         B, MBS, free_list.numel(), _ptr(workspace), ws_bytes, _stream(stream)))

@@ -429,6 +429,23 @@ def test_q4_streams_and_a_workspace_used_in_turn():
     assert pkv.get_device_error() == 0
 
 
+def test_q4_tensors_of_another_device_are_refused(monkeypatch):
+    """On the host, before any launch: the current device is not the tensors'."""
+    case = q4_case(3, [40], 8, 1, 128, 64, 16)
+    q, kc, vc, table, lens, _ = [dev(t) for t in case]
+    rows, slots = torch.zeros(1, 1, 128, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: pkv.paged_attention_q4(torch.empty_like(q), q, kc, vc, table, lens, 0.1, 64),
+                 lambda: pkv.decode_step_q4(torch.empty_like(q), q, rows, rows, slots, kc, vc, table, lens, 0.1, 64),
+                 lambda: pkv.kv_append_q4(rows, rows, kc, vc, slots, 64), lambda: pkv.kv_gather_q4(rows, rows, kc, vc, slots, 64),
+                 lambda: pkv.block_tables_extend(table, lens, one, one, one, one, torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                                 slots, one, 16),
+                 lambda: pkv.block_tables_release(table, None, one, one, one, one)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
 # ----------------------------------------------------------------------- decode step
 
 def run_step(case, k_new, v_new, slots, group, scale, window, num_splits, fused):
