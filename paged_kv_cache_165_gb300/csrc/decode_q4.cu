@@ -151,8 +151,11 @@ __global__ void __launch_bounds__(128)
 //   Scales and zeros are widened to fp32 once per key by the lane of that number and read back
 //   from shared memory.
 //   Up to four rows (decode_q4_rows.cuh) change the places of K and q, S^T = K Q^T, and need half the
-//   MMAs and exponentials: 4 x 65536 tokens of four KV heads 38.9 us for four rows, 49.1 for five;
-//   MHA step 82.5 -> 68.5 us, windows of 4096 tokens, four heads per KV head, 100.5 -> 78.8.
+//   MMAs and exponentials: 4 x 65536 tokens of four KV heads 39.1 us for four rows, 49.9 for five;
+//   MHA step 82.5 -> 70.3 us (4.1 TB/s), windows of 4096 tokens, four heads per KV head, 100.5 -> 78.9
+//   (4.3 TB/s).  Eight rows: four sequences of 131072 tokens 160 us (3.8 TB/s), 70B-shaped step 100 us.
+//   About 750 instructions a stage and warp, 224 of them to take the codes out of their words; half of
+//   the issue slots used, the rest are the latencies of a stage's chain at three warps per scheduler.
 // The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
 // the largest scale seen so far, E = ceil(log2 max scale): w = 2^(s - m - E + 14); l, O and the
 // zeros' term carry the same factor, which cancels, and a growing E rescales like a growing max.
@@ -699,9 +702,9 @@ size_t partial_bytes(long long rows, int Hq, int splits, int d) {
 namespace {
 // (Query row, head) pairs of a sequence and KV head that the warp-MMA kernel, which takes eight at a
 // time, is faster for than the tcgen05 kernel, whose time hardly depends on them.  4 x 65536 tokens, one
-// scale group a row: 24 pairs 37.3 us, the tcgen05 kernel 34.0 (32 pairs); 64 x 2048 tokens, four KV heads:
-// 66.5 and 74.1.  Two groups: 32 pairs 48.7 us, 40 58.7, the tcgen05 kernel 47.5 (40 pairs); 87.3, 105.4
-// and 100.9 (64 x 2048).
+// scale group a row: 24 pairs 38.5 us, the tcgen05 kernel 34.5 (32 pairs); 64 x 2048 tokens, four KV heads:
+// 69 and 77.  Two groups: 32 pairs 49.8 us, 40 58.7, the tcgen05 kernel 48.3 (40 pairs); 89, 105 and 102
+// (64 x 2048).
 int q4_mma_slots(int G) { return G == 1 ? 24 : 32; }
 
 // Rows of partial results of a balanced launch: two units for every warp or block.
