@@ -256,7 +256,8 @@ def quantize_rows_q4(rows, group: int):
     y = np.where(bad[..., None], 0.0, x)
     low = y.min(-1)
     zero = low.astype(np.float16)
-    zero = np.where(zero.astype(np.float64) > low, np.nextafter(zero, np.float16(-np.inf)), zero).astype(np.float16)
+    with np.errstate(over="ignore"):   # below the lowest value: not taken, the rows are clamped
+        zero = np.where(zero.astype(np.float64) > low, np.nextafter(zero, np.float16(-np.inf)), zero).astype(np.float16)
     scale = ((y.max(-1) - zero.astype(np.float64)) / 15.0).astype(np.float16)
     s = scale.astype(np.float64)[..., None]
     code = np.rint((y - zero.astype(np.float64)[..., None]) / np.where(s > 0, s, 1.0))
