@@ -10,6 +10,7 @@
 // so codes enter the products as the small integers they are, exactly.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "decode_q4.cuh"
 #include "decode_q4_rows.cuh"
@@ -517,33 +518,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
         const int steps = pg1 > pg0 ? (pg1 - pg0 + PPS - 1) / PPS : 0;
         const int n_my = steps > turn ? (steps - turn + turns - 1) / turns : 0;
         const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
-        int tcur[PPS], tnext[PPS];
-        auto load_ids = [&](int k, int (&t)[PPS]) {
-#pragma unroll
-            for (int i = 0; i < PPS; ++i) {
-                const int pg = pg0 + (turn + k * turns) * PPS + i;
-                t[i] = k < n_my && pg < pg1 ? __ldg(tbl + pg) : -1;
-            }
-        };
-        load_ids(lane, tcur);
-        load_ids(32 + lane, tnext);
-        int tbase = 0;
-        auto issue = [&](int k) {   // the whole warp
-            while (k >= tbase + 32) {
-                tbase += 32;
-#pragma unroll
-                for (int i = 0; i < PPS; ++i) tcur[i] = tnext[i];
-                load_ids(tbase + 32 + lane, tnext);
-            }
+        // lane l: copy l of a stage's 2 * PPS (K pages, then V pages), its page's id loaded a stage ahead
+        int pg = pg0 + turn * PPS + lane % PPS, phys = pg < pg1 ? __ldg(tbl + pg) : -1;
+        auto issue = [&](int k) {   // the whole warp, k = 0, 1, ...
             const int st = (cnt + k) % kStages;
             const uint32_t bar = smem_addr(&bars[st]);
-            // lane l: copy l of the stage's 2 * PPS (K pages, then V pages)
-            const int i = lane % PPS, pg = pg0 + (turn + k * turns) * PPS + i;
-            int phys = __shfl_sync(kFull, tcur[0], k & 31);
-            if (PPS == 2) {
-                const int second = __shfl_sync(kFull, tcur[PPS - 1], k & 31);
-                if (i == 1) phys = second;
-            }
             const bool there = lane < 2 * PPS && pg < pg1, ok = there && phys >= 0 && phys < p.NB;
             const unsigned copies = __ballot_sync(kFull, ok), absent = __ballot_sync(kFull, there && !ok);
             if (lane == 0) {
@@ -556,11 +535,13 @@ __global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
                 bulk_load(smem_addr(ring + st * Cfg::kStageBytes + lane * Cfg::kPageBytes),
                           (lane < PPS ? P.kc : P.vc) + (static_cast<size_t>(phys) * p.Hkv + kvh) * Cfg::kPageBytes,
                           Cfg::kPageBytes, bar);
+            pg += turns * PPS;
+            phys = pg < pg1 ? __ldg(tbl + pg) : -1;
         };
         int issued = min(kStages, n_my);
         for (int k = 0; k < issued; ++k) issue(k);
 
-        rows.begin(p.scale_log2, lane);   // while the copies fly
+        rows.begin(p.scale_log2, P.q_sign, lane);   // while the copies fly
 
         int k = 0;
         for (; k < n_my; ++k) {
@@ -801,6 +782,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
             kp.new_slots = a.new_slots;
             P.new_bf16 = a.new_dt == PKV_BF16;
         }
+        P.q_sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+        kp.scale_log2 = a.scale == 0.f ? 1.f : std::fabs(kp.scale_log2);
         P.k = kp;
         P.kc = const_cast<uint8_t *>(a.k_cache);   // written only for a step's new tokens
         P.vc = const_cast<uint8_t *>(a.v_cache);

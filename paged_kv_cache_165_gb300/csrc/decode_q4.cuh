@@ -17,6 +17,8 @@ struct AttendQ4Params {
     uint8_t *kc, *vc;
     int rows, max_q;     // query rows of the call, and of a sequence at most
     int new_bf16;        // type of the step's new rows
+    float q_sign;        // the queries are taken times the scale's sign (0, 1, -1) and k.scale_log2 is positive, so
+                         // that masked scores of -inf stay what they are when they are scaled
     int balanced;        // the thread blocks share all sequences' keys evenly (else grid (splits x tiles, Hkv, B))
 };
 

@@ -60,9 +60,10 @@ __device__ __forceinline__ float widen(const uint8_t *params, int page_bytes, fl
     float top = 0.f;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v[gi]));
-        put(gi, seen ? y.x : 0.f, seen ? fmaf(centred, y.x, y.y) : 0.f);
-        top = fmaxf(top, seen ? y.x : 0.f);
+        const uint32_t raw = seen ? v[gi] : 0u;
+        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&raw));
+        put(gi, y.x, fmaf(centred, y.x, y.y));
+        top = fmaxf(top, y.x);
     }
     return top;
 }
@@ -129,7 +130,7 @@ struct EightRows {
         }
     }
 
-    __device__ __forceinline__ void begin(float scale_log2, int lane) {
+    __device__ __forceinline__ void begin(float scale_log2, float q_sign, int lane) {
         // MMA steps 2u and 2u + 1 of word u = gi * WPT + i:
         // elements 8 * word + {0, 4}, {2, 6}, and their odd neighbours / 16
         float amax = 0.f;
@@ -140,7 +141,7 @@ struct EightRows {
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         const int up = q_exponent(amax);
-        const float scale = pow2i(up);
+        const float scale = pow2i(up) * q_sign;
         f = (scale_log2 * 0x1p24f) * pow2i(-up);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
@@ -221,8 +222,6 @@ struct EightRows {
                 s[nt] = fma2(sc, add2(make_float2(a[nt][0], a[nt][1]), make_float2(a[nt][2], a[nt][3])), y);
             }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt] = mul2(s[nt], make_float2(f, f));
         if (end >= 0) {   // some row does not see all of them
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -240,7 +239,7 @@ struct EightRows {
         for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt].x, s[nt].y));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-        m_run = fmaxf(m_run, mx);
+        m_run = fmaxf(m_run, mx * f);   // the scores are in the MMAs' units
         vs.take(top);
         const float ref_new = m_run + (vs.exponent - 14.f);
         // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
@@ -250,7 +249,7 @@ struct EightRows {
         float2 psum = make_float2(0.f, 0.f), w[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float2 e = add2(s[nt], make_float2(-base, -base));
+            const float2 e = fma2(s[nt], make_float2(f, f), make_float2(-base, -base));
             w[nt] = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             psum = add2(psum, w[nt]);
         }
@@ -399,7 +398,7 @@ struct FourRows {
         }
     }
 
-    __device__ __forceinline__ void begin(float scale_log2, int lane) {
+    __device__ __forceinline__ void begin(float scale_log2, float q_sign, int lane) {
         float amax = 0.f;
 #pragma unroll
         for (int u = 0; u < G * WPT; ++u)
@@ -408,7 +407,7 @@ struct FourRows {
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         const int up = q_exponent(amax);
-        const float scale = pow2i(up);
+        const float scale = pow2i(up) * q_sign;
         const int from = 8 * (lane & 3);   // a lane that laid out this lane's row
         f = __shfl_sync(kFull, (scale_log2 * 0x1p24f) * pow2i(-up), from);
         const bool low = lane >> 2 & 1;    // an odd column: the lo parts
@@ -485,8 +484,6 @@ struct FourRows {
                 s[j] = fmaf(p.x, t.x + t.y, y);
             }
         }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s[j] *= f;
         if (end >= 0) {
             const int stop = min(me.len, end);
 #pragma unroll
@@ -503,7 +500,7 @@ struct FourRows {
         for (int j = 1; j < NT; ++j) mx = fmaxf(mx, s[j]);
 #pragma unroll
         for (int sh = 4; sh < 32; sh *= 2) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, sh));
-        m_run = fmaxf(m_run, mx);
+        m_run = fmaxf(m_run, mx * f);   // the scores are in the MMAs' units
         const float ref_new = m_run + (vs.exponent - 14.f);
         // a row that has seen no key yet has ref -inf: its weights are 0 whatever the base
         const float base = ref_new == -INFINITY ? 0.f : ref_new;
@@ -512,7 +509,7 @@ struct FourRows {
         float w[NT], sum_w = 0.f;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            w[j] = ex2_approx(s[j] - base);
+            w[j] = ex2_approx(fmaf(s[j], f, -base));
             sum_w += w[j];
         }
         l = fmaf(l, alpha, sum_w);

@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                 amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
                 // |q| * 2^up in [2^13, 2^14); a row of zeros (or of subnormals) keeps the factor finite
                 const int up = min(13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
-                const float qs = pow2i(up);
+                const float qs = pow2i(up) * P.q_sign;
                 f = (p.scale_log2 * 0x1p24f) * pow2i(-up);
                 // 16 lanes x 128 bits, 8 repeats: repeat k puts r[2k] at lane base + lane / 4, column 4 k + c4
                 // and r[2k + 1] eight lanes further: word k of a half of eight, pair c4

@@ -351,6 +351,17 @@ def test_q4_a_nan_reaches_only_the_rows_that_see_it(hq, hkv, d, group, bs, rows,
         assert torch.isnan(out[0]).all()
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 128), (8, 1, 128), (64, 1, 128), (2, 1, 96)])
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_q4_scales_that_are_not_positive(hq, hkv, d, scale):
+    """Keys past the end and before the window stay masked whatever the sign of the scale."""
+    case = q4_case(29, [150, 1, 40], hq, hkv, d, 32 if d == 96 else 64, 16, [3, 1, 2])
+    live, ref, ref_lse = expect(case, 32 if d == 96 else 64, scale, 37)
+    out, lse = run_q4(case, 32 if d == 96 else 64, scale, 37, decode=False, max_q=3)
+    assert_attn_close(out[live], ref, "out", ATOL)
+    assert_attn_close(lse[live], ref_lse, "lse", ATOL)
+
+
 def test_q4_workspace_too_small_is_refused():
     case = q4_case(3, [4000], 8, 1, 128, 64, 16)
     q, kc, vc, table, lens, _ = [dev(t) for t in case]
