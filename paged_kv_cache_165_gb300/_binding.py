@@ -146,10 +146,10 @@ def _check(status: int) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, here=None) -> int:   # here: the current device, where it is known
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if here is None else here)
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -158,6 +158,13 @@ def _stream(stream) -> int:
 
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _cuda(name, t, dtype=None):
@@ -174,12 +181,35 @@ def _cuda(name, t, dtype=None):
     return t
 
 
-def _here(what, *tensors) -> None:
-    """The kernels run on the current device: its tensors only."""
-    here = torch.cuda.current_device()
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _current_device() -> int:
+    try:
+        return _raw_device()
+    except (RuntimeError, AssertionError):   # no driver: no tensor is there either
+        return -2
+
+
+def _ready(here, tensors) -> bool:
+    """Contiguous tensors of device `here`, all of them (None: left out)?  Eager decode steps are short
+    enough for the checks' cost to show: this is their common outcome, _refuse says what is wrong."""
     for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"{what}: a tensor is on device {t.get_device()}, the current one is {here}")
+        if t is not None and (t.get_device() != here or not t.is_contiguous()):
+            return False
+    return True
+
+
+_OPTIONAL = ("lse", "cu_q", "first_block", "workspace")
+
+
+def _refuse(what, here, **tensors) -> None:
+    """The error of whatever _ready or a type found wrong.  tensors: name=(tensor, its type or None)."""
+    for name, (t, dtype) in tensors.items():
+        if t is not None or name not in _OPTIONAL:
+            _cuda(name, t, dtype)
+            if t.get_device() != here:   # the kernels run on the current device
+                raise ValueError(f"{what}: {name} is on device {t.get_device()}, the current one is {here}")
 
 
 def _dtype(t) -> int:
@@ -566,29 +596,35 @@ def q4_row_bytes(d, group) -> int:
 
 
 def _q4_caches(what, k_cache, v_cache, d, group):
-    _cuda("k_cache", k_cache, torch.uint8)
-    _cuda("v_cache", v_cache, torch.uint8)
     shape = k_cache.shape
     if len(shape) != 4 or shape != v_cache.shape or shape[3] != q4_row_bytes(d, group):
         raise ValueError(f"{what}: the caches must be [NB][Hkv][bs][{q4_row_bytes(d, group)}] (q4_row_bytes of d={d}, "
                          f"group={group}), got {tuple(shape)} and {tuple(v_cache.shape)}")
-    return shape[:3]
+    return shape
 
 
 def _q4_rows(what, fn, k_rows, v_rows, k_cache, v_cache, slot_mapping, group, stream):
-    _cuda("k rows", k_rows)
+    here = _current_device()
+    try:
+        ok = (_ready(here, (k_rows, v_rows, k_cache, v_cache, slot_mapping)) and k_rows.dtype is v_rows.dtype and
+              k_cache.dtype is _U8 and v_cache.dtype is _U8 and slot_mapping.dtype is _I64)
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, k_rows=(k_rows, None), v_rows=(v_rows, getattr(k_rows, "dtype", None)), k_cache=(k_cache, _U8),
+                v_cache=(v_cache, _U8), slot_mapping=(slot_mapping, _I64))
     dt = _dtype(k_rows)
-    _cuda("v rows", v_rows, k_rows.dtype)
-    _cuda("slot_mapping", slot_mapping, torch.int64)
-    if k_rows.dim() != 3:
+    rows = k_rows.shape
+    if len(rows) != 3:
         raise ValueError(f"{what}: rows must be [T][Hkv][d]")
-    T, _, d = k_rows.shape
-    NB, Hkv, bs = _q4_caches(what, k_cache, v_cache, d, group)
-    if tuple(k_rows.shape) != (T, Hkv, d) or tuple(v_rows.shape) != (T, Hkv, d) or slot_mapping.numel() != T:
+    T, H, d = rows
+    NB, Hkv, bs, _ = _q4_caches(what, k_cache, v_cache, d, group)
+    if H != Hkv or v_rows.shape != rows or slot_mapping.numel() != T:
         raise ValueError(f"{what}: shapes do not match [T][Hkv][d] / [T]")
-    _here(what, k_rows, v_rows, k_cache, v_cache, slot_mapping)
-    _check(fn(_ptr(k_rows), _ptr(v_rows), dt, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, d, int(group), bs,
-              NB, _stream(stream)))
+    status = fn(k_rows.data_ptr(), v_rows.data_ptr(), dt, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T,
+                Hkv, d, int(group), bs, NB, _stream(stream, here))
+    if status:
+        _check(status)
 
 
 def kv_append_q4(k_new, v_new, k_cache, v_cache, slot_mapping, group, stream=None) -> None:
@@ -608,63 +644,71 @@ def paged_attention_q4_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, group, bs, MBS,
                                                             num_splits))
 
 
-def _q4_attend_args(what, out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace):
-    _cuda("q", q, torch.float32)
-    _cuda("out", out, torch.float32)
-    _cuda("block_table", block_table, torch.int32)
-    _cuda("context_lens", context_lens, torch.int32)
-    if lse is not None:
-        _cuda("lse", lse, torch.float32)
-    if q.dim() != 3:
+def _q4_attend_sizes(what, out, q, k_cache, v_cache, block_table, context_lens, group, lse):
+    rows = q.shape
+    if len(rows) != 3:
         raise ValueError(f"{what}: q must be [rows][Hq][d]")
-    Tq, Hq, d = q.shape
+    Tq, Hq, d = rows
     B = context_lens.numel()
-    NB, Hkv, bs = _q4_caches(what, k_cache, v_cache, d, group)
-    if tuple(out.shape) != (Tq, Hq, d) or block_table.dim() != 2 or block_table.shape[0] != B or \
-            (lse is not None and lse.numel() != Tq * Hq):
+    NB, Hkv, bs, _ = _q4_caches(what, k_cache, v_cache, d, group)
+    table = block_table.shape
+    if out.shape != rows or len(table) != 2 or table[0] != B or (lse is not None and lse.numel() != Tq * Hq):
         raise ValueError(f"{what}: shapes do not match")
-    ws_bytes = 0
-    if workspace is not None:
-        _cuda("workspace", workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _here(what, q, out, k_cache, v_cache, block_table, context_lens, lse, workspace)
-    return B, Tq, Hq, Hkv, d, bs, NB, block_table.shape[1], ws_bytes
+    return B, Tq, Hq, Hkv, d, bs, NB, table[1]
 
 
 def paged_attention_q4(out, q, k_cache, v_cache, block_table, context_lens, scale, group, cu_q=None, max_q=1,
                        window=0, lse=None, num_splits=0, workspace=None, stream=None) -> None:
     """paged_attention over a 4-bit cache: q, out [Tq][Hq][d] fp32, the newest rows of every
     sequence (cu_q int32 [B+1]; None: one row per sequence), causal, optional window."""
-    B, Tq, Hq, Hkv, d, bs, NB, MBS, ws_bytes = _q4_attend_args(
-        "paged_attention_q4", out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace)
-    if cu_q is not None:
-        _cuda("cu_q", cu_q, torch.int32)
-    if (cu_q is not None and cu_q.numel() != B + 1) or (cu_q is None and Tq != B):
+    what, here = "paged_attention_q4", _current_device()
+    try:
+        ok = (_ready(here, (out, q, k_cache, v_cache, block_table, context_lens, lse, cu_q, workspace)) and q.dtype is _F32 and
+              out.dtype is _F32 and k_cache.dtype is _U8 and v_cache.dtype is _U8 and block_table.dtype is _I32 and
+              context_lens.dtype is _I32 and (lse is None or lse.dtype is _F32) and (cu_q is None or cu_q.dtype is _I32))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, q=(q, _F32), out=(out, _F32), k_cache=(k_cache, _U8), v_cache=(v_cache, _U8),
+                block_table=(block_table, _I32), context_lens=(context_lens, _I32), lse=(lse, _F32), cu_q=(cu_q, _I32),
+                workspace=(workspace, None))
+    B, Tq, Hq, Hkv, d, bs, NB, MBS = _q4_attend_sizes(what, out, q, k_cache, v_cache, block_table, context_lens, group, lse)
+    if cu_q.numel() != B + 1 if cu_q is not None else Tq != B:
         raise ValueError("paged_attention_q4: shapes do not match")
-    _here("paged_attention_q4", cu_q)
-    _check(lib().pkv_paged_attention_q4(
-        _ptr(out), _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(context_lens), _ptr(cu_q),
-        B, Tq, int(max_q), Hq, Hkv, d, int(group), bs, MBS, NB, float(scale), int(window), int(num_splits),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+    status = lib().pkv_paged_attention_q4(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        context_lens.data_ptr(), _ptr(cu_q), B, Tq, int(max_q), Hq, Hkv, d, int(group), bs, MBS, NB, float(scale), int(window),
+        int(num_splits), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
 
 
 def decode_step_q4(out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_table, context_lens, scale, group,
                    window=0, lse=None, num_splits=0, workspace=None, stream=None) -> None:
     """decode_step over a 4-bit cache: k_new/v_new [B][Hkv][d] (bf16 or fp32) are quantised into
     slot_mapping[b] (int64, < 0: none), then out [B][Hq][d] fp32 = attention of q over the cache."""
-    B, Tq, Hq, Hkv, d, bs, NB, MBS, ws_bytes = _q4_attend_args(
-        "decode_step_q4", out, q, k_cache, v_cache, block_table, context_lens, group, lse, workspace)
-    _cuda("k_new", k_new)
-    new_dt = _dtype(k_new)
-    _cuda("v_new", v_new, k_new.dtype)
-    _cuda("slot_mapping", slot_mapping, torch.int64)
-    if Tq != B or tuple(k_new.shape) != (B, Hkv, d) or tuple(v_new.shape) != (B, Hkv, d) or slot_mapping.numel() != B:
+    what, here = "decode_step_q4", _current_device()
+    try:
+        ok = (_ready(here, (out, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_table, context_lens, lse, workspace)) and
+              q.dtype is _F32 and out.dtype is _F32 and k_new.dtype is v_new.dtype and slot_mapping.dtype is _I64 and
+              k_cache.dtype is _U8 and v_cache.dtype is _U8 and block_table.dtype is _I32 and context_lens.dtype is _I32 and
+              (lse is None or lse.dtype is _F32))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, q=(q, _F32), out=(out, _F32), k_new=(k_new, None), v_new=(v_new, getattr(k_new, "dtype", None)),
+                slot_mapping=(slot_mapping, _I64), k_cache=(k_cache, _U8), v_cache=(v_cache, _U8),
+                block_table=(block_table, _I32), context_lens=(context_lens, _I32), lse=(lse, _F32), workspace=(workspace, None))
+    B, Tq, Hq, Hkv, d, bs, NB, MBS = _q4_attend_sizes(what, out, q, k_cache, v_cache, block_table, context_lens, group, lse)
+    new_dt, new = _dtype(k_new), k_new.shape
+    if Tq != B or new != (B, Hkv, d) or v_new.shape != new or slot_mapping.numel() != B:
         raise ValueError("decode_step_q4: shapes do not match")
-    _here("decode_step_q4", k_new, v_new, slot_mapping)
-    _check(lib().pkv_decode_step_q4(
-        _ptr(out), _ptr(lse), _ptr(q), _ptr(k_new), _ptr(v_new), new_dt, _ptr(slot_mapping), _ptr(k_cache),
-        _ptr(v_cache), _ptr(block_table), _ptr(context_lens), B, Hq, Hkv, d, int(group), bs, MBS, NB, float(scale),
-        int(window), int(num_splits), _ptr(workspace), ws_bytes, _stream(stream)))
+    status = lib().pkv_decode_step_q4(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new_dt, slot_mapping.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, Hq, Hkv, d, int(group), bs,
+        MBS, NB, float(scale), int(window), int(num_splits), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
 
 
 # ---------------------------------------------------------------- block tables
@@ -684,49 +728,57 @@ def block_tables_extend(block_table, context_lens, new_tokens, free_list, free_c
     block_table int32 [B][MBS]; context_lens, new_tokens, context_lens_out int32 [B]; free_list
     int32 [NB]; free_count, free_count_out int32 [1]; cu_new int32 [B+1]; slot_mapping int64 [T]
     (entries past the new tokens become -1).  The *_out tensors may be their inputs."""
-    for name, t in (("block_table", block_table), ("context_lens", context_lens), ("new_tokens", new_tokens),
-                    ("free_list", free_list), ("free_count", free_count), ("context_lens_out", context_lens_out),
-                    ("cu_new", cu_new), ("free_count_out", free_count_out)):
-        _cuda(name, t, torch.int32)
-    _cuda("slot_mapping", slot_mapping, torch.int64)
-    if block_table.dim() != 2:
+    what, here = "block_tables_extend", _current_device()
+    ints = (block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new, free_count_out)
+    try:
+        ok = (_ready(here, (*ints, slot_mapping, workspace)) and all([t.dtype is _I32 for t in ints]) and
+              slot_mapping.dtype is _I64)
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, block_table=(block_table, _I32), context_lens=(context_lens, _I32), new_tokens=(new_tokens, _I32),
+                free_list=(free_list, _I32), free_count=(free_count, _I32), context_lens_out=(context_lens_out, _I32),
+                cu_new=(cu_new, _I32), free_count_out=(free_count_out, _I32), slot_mapping=(slot_mapping, _I64),
+                workspace=(workspace, None))
+    table = block_table.shape
+    if len(table) != 2:
         raise ValueError("block_tables_extend: block_table must be [B][MBS]")
-    B, MBS = block_table.shape
+    B, MBS = table
     if context_lens.numel() != B or new_tokens.numel() != B or context_lens_out.numel() != B or \
             cu_new.numel() != B + 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
         raise ValueError("block_tables_extend: shapes do not match")
-    ws_bytes = 0
-    if workspace is not None:
-        _cuda("workspace", workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _here("block_tables_extend", block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
-          slot_mapping, free_count_out, workspace)
-    _check(lib().pkv_block_tables_extend(
-        _ptr(block_table), _ptr(context_lens), _ptr(new_tokens), _ptr(free_list), _ptr(free_count),
-        _ptr(context_lens_out), _ptr(cu_new), _ptr(slot_mapping), _ptr(free_count_out), B, slot_mapping.numel(), MBS,
-        int(bs), free_list.numel(), _ptr(workspace), ws_bytes, _stream(stream)))
+    status = lib().pkv_block_tables_extend(
+        block_table.data_ptr(), context_lens.data_ptr(), new_tokens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
+        context_lens_out.data_ptr(), cu_new.data_ptr(), slot_mapping.data_ptr(), free_count_out.data_ptr(), B,
+        slot_mapping.numel(), MBS, int(bs), free_list.numel(), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
 
 
 def block_tables_release(block_table, first_block, end_block, free_list, free_count, free_count_out, workspace=None,
                          stream=None) -> None:
     """Logical blocks [first_block[b], end_block[b]) of every row (int32 [B]; first_block None: 0)
     back to the free list, their table entries -1 (see pkv.h)."""
-    for name, t in (("block_table", block_table), ("end_block", end_block), ("free_list", free_list),
-                    ("free_count", free_count), ("free_count_out", free_count_out)):
-        _cuda(name, t, torch.int32)
-    if first_block is not None:
-        _cuda("first_block", first_block, torch.int32)
-    if block_table.dim() != 2:
+    what, here = "block_tables_release", _current_device()
+    ints = (block_table, end_block, free_list, free_count, free_count_out)
+    try:
+        ok = (_ready(here, (*ints, first_block, workspace)) and all([t.dtype is _I32 for t in ints]) and
+              (first_block is None or first_block.dtype is _I32))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, block_table=(block_table, _I32), end_block=(end_block, _I32), free_list=(free_list, _I32),
+                free_count=(free_count, _I32), free_count_out=(free_count_out, _I32), first_block=(first_block, _I32),
+                workspace=(workspace, None))
+    table = block_table.shape
+    if len(table) != 2:
         raise ValueError("block_tables_release: block_table must be [B][MBS]")
-    B, MBS = block_table.shape
+    B, MBS = table
     if end_block.numel() != B or (first_block is not None and first_block.numel() != B) or free_count.numel() != 1 or \
             free_count_out.numel() != 1:
         raise ValueError("block_tables_release: shapes do not match")
-    ws_bytes = 0
-    if workspace is not None:
-        _cuda("workspace", workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _here("block_tables_release", block_table, first_block, end_block, free_list, free_count, free_count_out, workspace)
-    _check(lib().pkv_block_tables_release(
-        _ptr(block_table), _ptr(first_block), _ptr(end_block), _ptr(free_list), _ptr(free_count), _ptr(free_count_out),
-        B, MBS, free_list.numel(), _ptr(workspace), ws_bytes, _stream(stream)))
+    status = lib().pkv_block_tables_release(
+        block_table.data_ptr(), _ptr(first_block), end_block.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
+        free_count_out.data_ptr(), B, MBS, free_list.numel(), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)

@@ -440,13 +440,34 @@ def test_q4_streams_and_a_workspace_used_in_turn():
     assert pkv.get_device_error() == 0
 
 
+def test_q4_tensors_of_the_wrong_kind_are_refused():
+    case = q4_case(3, [40], 8, 1, 128, 64, 16)
+    q, kc, vc, table, lens, _ = [dev(t) for t in case]
+    out, rows = torch.empty_like(q), torch.zeros(1, 1, 128, device="cuda")
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    wide = torch.zeros(1, 8, 256, device="cuda")[:, :, ::2]
+    for error, match, call in (
+            (TypeError, "q must be", lambda: pkv.paged_attention_q4(out, q.double(), kc, vc, table, lens, 0.1, 64)),
+            (ValueError, "q must be contiguous", lambda: pkv.paged_attention_q4(out, wide, kc, vc, table, lens, 0.1, 64)),
+            (TypeError, "lse must be", lambda: pkv.paged_attention_q4(out, q, kc, vc, table, lens, 0.1, 64, lse=slots)),
+            (TypeError, "v_cache must be", lambda: pkv.decode_step_q4(out, q, rows, rows, slots, kc, None, table, lens, 0.1, 64)),
+            (TypeError, "v_new must be", lambda: pkv.decode_step_q4(out, q, rows, rows.bfloat16(), slots, kc, vc, table, lens, 0.1, 64)),
+            (ValueError, "context_lens must be on", lambda: pkv.paged_attention_q4(out, q, kc, vc, table, lens.cpu(), 0.1, 64)),
+            (TypeError, "element type", lambda: pkv.kv_append_q4(rows.double(), rows.double(), kc, vc, slots, 64)),
+            (ValueError, "shapes", lambda: pkv.kv_append_q4(rows, rows, kc, vc, slots[:0], 64)),
+            (ValueError, "shapes", lambda: pkv.paged_attention_q4(out[:, :4], q, kc, vc, table, lens, 0.1, 64)),
+            (TypeError, "slot_mapping must be", lambda: pkv.kv_gather_q4(rows, rows, kc, vc, slots.int(), 64))):
+        with pytest.raises(error, match=match):
+            call()
+
+
 def test_q4_tensors_of_another_device_are_refused(monkeypatch):
     """On the host, before any launch: the current device is not the tensors'."""
     case = q4_case(3, [40], 8, 1, 128, 64, 16)
     q, kc, vc, table, lens, _ = [dev(t) for t in case]
     rows, slots = torch.zeros(1, 1, 128, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
     one = torch.zeros(1, dtype=torch.int32, device="cuda")
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(pkv._binding, "_current_device", lambda: 1)
     for call in (lambda: pkv.paged_attention_q4(torch.empty_like(q), q, kc, vc, table, lens, 0.1, 64),
                  lambda: pkv.decode_step_q4(torch.empty_like(q), q, rows, rows, slots, kc, vc, table, lens, 0.1, 64),
                  lambda: pkv.kv_append_q4(rows, rows, kc, vc, slots, 64), lambda: pkv.kv_gather_q4(rows, rows, kc, vc, slots, 64),

@@ -152,6 +152,11 @@ def test_q4_bindings_check_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         pkv.kv_append_q4(cpu, cpu, torch.zeros((1, 2, 16, 72), dtype=torch.uint8),
                          torch.zeros((1, 2, 16, 72), dtype=torch.uint8), torch.zeros(2, dtype=torch.int64), 64)
+    for call in (lambda: pkv.kv_append_q4(None, cpu, cpu, cpu, cpu, 64), lambda: pkv.kv_gather_q4(cpu.numpy(), cpu, cpu, cpu, cpu, 64),
+                 lambda: pkv.paged_attention_q4(cpu, None, cpu, cpu, cpu, cpu, 0.1, 64),
+                 lambda: pkv.block_tables_release(None, None, cpu, cpu, cpu, cpu)):
+        with pytest.raises((TypeError, ValueError), match="torch.Tensor|CUDA"):
+            call()
     with pytest.raises(ValueError, match="q4_row_bytes"):
         pkv.q4_row_bytes(128, 48)
     with pytest.raises(ValueError, match="permutation"):
