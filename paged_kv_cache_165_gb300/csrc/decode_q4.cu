@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(128)
 //   from shared memory.
 //   Up to four rows (decode_q4_rows.cuh) change the places of K and q, S^T = K Q^T, and need half the
 //   MMAs and exponentials: 4 x 65536 tokens of four KV heads 39.1 us for four rows, 49.9 for five;
-//   MHA step 82.5 -> 70.3 us (4.1 TB/s), windows of 4096 tokens, four heads per KV head, 100.5 -> 78.9
-//   (4.3 TB/s).  Eight rows: four sequences of 131072 tokens 160 us (3.8 TB/s), 70B-shaped step 100 us.
+//   MHA step 82.5 -> 68.3 us (4.2 TB/s), windows of 4096 tokens, four heads per KV head, 100.5 -> 78.9
+//   (4.3 TB/s).  Eight rows: four sequences of 131072 tokens 162 us (3.7 TB/s), 70B-shaped step 99 us.
 //   About 750 instructions a stage and warp, 224 of them to take the codes out of their words; half of
 //   the issue slots used, the rest are the latencies of a stage's chain at three warps per scheduler.
 // The f16 range of the weights: p * scale is kept below 2^14 by shifting the softmax reference by
