@@ -23,111 +23,184 @@ constexpr int kLeastSteps = 4;       // 32-key steps that a warp of one takes at
 
 // ================================================================ CUDA-core path
 
-// One warp per (query row, query head, chunk).  W lanes (a power of two, W * 8 >= d) hold one
-// key's row, eight elements each, so 32 / W keys are taken at a time; every such slice of the
-// warp keeps its own online softmax and they merge at the end.
-template <int W>
+// Query heads that a warp takes together, so that they share the codes' way into fp32.
+int simt_heads(int m) { return m <= 2 ? m : 4; }
+
+// One warp per (query row, H query heads of a KV head, chunk).  W lanes (a power of two, W * 8 >= d)
+// hold one key's row, eight elements each, so 32 / W keys are taken at a time, kSimtBatch such steps
+// between two updates of the softmax; every such slice of the warp keeps its own online softmax and
+// they merge at the end.  Bound by its arithmetic (64 x 2048 tokens, 32 heads on 8 of 96: SIMT_US).
+constexpr int kSimtBatch = 4;
+
+// A word's codes less 8, times 2^-9: elements (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ void centred8(uint32_t w, float2 (&e)[4]) {
+    uint32_t h[4];
+    centre(w, h[0], h[1]);
+    centre(w >> 8, h[2], h[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+}
+
+template <int W, int H>
 __global__ void __launch_bounds__(128)
     attend_q4_simt_kernel(const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc, const DecodeKParams p,
                           int d, int bs, int lanes, int rows) {
-    constexpr int KEYS = 32 / W;
+    constexpr int KEYS = 32 / W, U = kSimtBatch;
     pdl_launch_dependents();   // the merge kernel after this one waits for the whole grid
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, tiles = (p.m + H - 1) / H;
     const long long unit = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (unit >= static_cast<long long>(rows) * p.Hq) return;
-    const int row = static_cast<int>(unit / p.Hq), i = static_cast<int>(unit % p.Hq), split = blockIdx.y;
-    const int kvh = i / p.m, j = lane % W, slice = lane / W;
-    const SeqSpan sp = row_span(p, row, bs, lane == 0 && split == 0 && i == 0);
+    if (unit >= static_cast<long long>(rows) * p.Hkv * tiles) return;
+    const int row = static_cast<int>(unit / (p.Hkv * tiles)), part = static_cast<int>(unit % (p.Hkv * tiles));
+    const int kvh = part / tiles, h0 = part % tiles * H, split = blockIdx.y, j = lane % W, slice = lane / W;
+    const SeqSpan sp = row_span(p, row, bs, lane == 0 && split == 0 && part == 0);
     const int nc = (sp.cnpages + p.chunk_pages - 1) / p.chunk_pages;
     const int c0 = sp.cpfirst + split * p.chunk_pages;
     const int c1 = min(sp.cpfirst + sp.cnpages, c0 + p.chunk_pages);
     const int pg0 = max(c0, sp.pfirst), pg1 = min(c1, sp.pfirst + sp.npages);
-    const size_t bi = static_cast<size_t>(row) * p.Hq + i;
-    if (c0 >= c1) {
-        if (split == 0) {   // an empty sequence: out = 0, lse = -inf
-            for (int e = lane; e < d; e += 32) p.out[bi * d + e] = 0.f;
-            if (lane == 0 && p.lse != nullptr) p.lse[bi] = -INFINITY;
+    const size_t bi0 = static_cast<size_t>(row) * p.Hq + kvh * p.m + h0;
+    const int heads = min(H, p.m - h0);
+    if (c0 >= c1 || pg0 >= pg1) {
+        // an empty sequence: out = 0, lse = -inf; a chunk with none of this row's keys: an empty partial
+        if (c0 >= c1 && split > 0) return;
+        for (int h = 0; h < heads; ++h) {
+            const size_t at = c0 >= c1 ? bi0 + h : (bi0 + h) * p.splits + split;
+            for (int e = lane; e < d; e += 32) (c0 >= c1 ? p.out : p.ws_o)[at * d + e] = 0.f;
+            float *lse = c0 >= c1 ? p.lse : p.ws_lse;
+            if (lane == 0 && lse != nullptr) lse[at] = -INFINITY;
         }
-        return;
-    }
-    if (pg0 >= pg1) {   // the chunk holds none of this row's keys: an empty partial
-        for (int e = lane; e < d; e += 32) p.ws_o[(bi * p.splits + split) * d + e] = 0.f;
-        if (lane == 0) p.ws_lse[bi * p.splits + split] = -INFINITY;
         return;
     }
     const int words = d / 8, G = words / lanes;
     const bool mine = j < words;
-    float q[8], acc[8], qsum = 0.f;
+    float2 q[H][4], acc[H][4];
+    float qsum[H], zero_sum[H], m_run[H], l_run[H];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        q[e] = mine ? p.q[bi * d + j * 8 + e] : 0.f;
-        qsum += q[e];
-        acc[e] = 0.f;
+    for (int h = 0; h < H; ++h) {
+        const float *src = p.q + (bi0 + min(h, heads - 1)) * d + j * 8;
+        qsum[h] = zero_sum[h] = l_run[h] = 0.f;
+        m_run[h] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q[h][e] = mine ? make_float2(src[e], src[e + 4]) : make_float2(0.f, 0.f);
+            qsum[h] += q[h][e].x + q[h][e].y;
+            acc[h][e] = make_float2(0.f, 0.f);
+        }
     }
-    float m_run = -INFINITY, l_run = 0.f;
     const int page_bytes = bs * (words * 4 + G * 4);
+    const int32_t *table = p.block_table + static_cast<size_t>(sp.b) * p.MBS;
+    int next = __ldg(table + pg0);
     for (int pg = pg0; pg < pg1; ++pg) {
-        const int phys = __ldg(p.block_table + static_cast<size_t>(sp.b) * p.MBS + pg);
+        const int phys = next;
+        if (pg + 1 < pg1) next = __ldg(table + pg + 1);
         const bool bad = phys < 0 || phys >= p.NB;
         if (bad && lane == 0) raise_error(p.err, PKV_DEVERR_BLOCK);
         const size_t base = bad ? 0 : (static_cast<size_t>(phys) * p.Hkv + kvh) * page_bytes;
         const uint32_t *kw = reinterpret_cast<const uint32_t *>(kc + base);
         const uint32_t *vw = reinterpret_cast<const uint32_t *>(vc + base);
         const int first = max(0, sp.lo - pg * bs), valid = min(bs, sp.len - pg * bs);
-        for (int t0 = first; t0 < valid; t0 += KEYS) {
-            const int t = t0 + slice;
-            const bool see = t < valid, read = see && mine && !bad;
-            uint32_t kcode = 0, vcode = 0;
-            float2 kp = make_float2(0.f, 0.f), vp = kp;
-            if (read) {
-                kcode = __ldg(kw + t * words + j);
-                vcode = __ldg(vw + t * words + j);
-                kp = __half22float2(__ldg(reinterpret_cast<const __half2 *>(kw + bs * words) + t * G + j / lanes));
-                vp = __half22float2(__ldg(reinterpret_cast<const __half2 *>(vw + bs * words) + t * G + j / lanes));
+        for (int t0 = first + slice; t0 - slice < valid; t0 += KEYS * U) {
+            uint32_t kcode[U], vcode[U];
+            float2 kp[U], vp[U];   // scale * 2^9 and the centred codes' zero
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + u * KEYS;
+                kcode[u] = vcode[u] = 0;
+                kp[u] = vp[u] = make_float2(0.f, 0.f);
+                if (t < valid && mine && !bad) {
+                    kcode[u] = __ldg(kw + t * words + j);
+                    vcode[u] = __ldg(vw + t * words + j);
+                    kp[u] = __half22float2(__ldg(reinterpret_cast<const __half2 *>(kw + bs * words) + t * G + j / lanes));
+                    vp[u] = __half22float2(__ldg(reinterpret_cast<const __half2 *>(vw + bs * words) + t * G + j / lanes));
+                }
             }
-            float dot = 0.f;
+            float s[H][U];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(q[e], static_cast<float>((kcode >> (4 * e)) & 15u), dot);
-            dot = read ? fmaf(dot, kp.x, qsum * kp.y) : 0.f;
+            for (int u = 0; u < U; ++u) {
+                float2 e[4];
+                centred8(kcode[u], e);
+                const float zero = fmaf(8.f, kp[u].x, kp[u].y), scale = kp[u].x * 0x1p9f;
 #pragma unroll
-            for (int sh = W / 2; sh > 0; sh >>= 1) dot += __shfl_xor_sync(kFull, dot, sh);
-            const float s = see ? dot * p.scale_log2 : -INFINITY;
-            const float m_new = fmaxf(m_run, s);
-            const float alpha = m_run == -INFINITY ? 0.f : exp2f(m_run - m_new);
-            const float w = see ? exp2f(s - m_new) : 0.f;
-            l_run = l_run * alpha + w;
-            const float ws = read ? w * vp.x : 0.f, wz = read ? w * vp.y : 0.f;
+                for (int h = 0; h < H; ++h) {
+                    const float2 y = fma2(q[h][0], e[0], fma2(q[h][1], e[1], fma2(q[h][2], e[2], mul2(q[h][3], e[3]))));
+                    s[h][u] = fmaf(scale, y.x + y.y, zero * qsum[h]);
+                }
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                acc[e] = fmaf(acc[e], alpha, fmaf(ws, static_cast<float>((vcode >> (4 * e)) & 15u), wz));
-            m_run = m_new;
+            for (int sh = W / 2; sh > 0; sh >>= 1)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) s[h][u] += __shfl_xor_sync(kFull, s[h][u], sh);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                float m_new = m_run[h];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    s[h][u] = t0 + u * KEYS < valid ? s[h][u] * p.scale_log2 : -INFINITY;
+                    m_new = fmaxf(m_new, s[h][u]);
+                }
+                const float base = m_new == -INFINITY ? 0.f : m_new;   // the slice has seen no key yet: weights 0
+                const float alpha = m_run[h] == -INFINITY ? 0.f : ex2_approx(m_run[h] - base);
+                m_run[h] = m_new;
+                l_run[h] *= alpha;
+                zero_sum[h] *= alpha;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    s[h][u] = ex2_approx(s[h][u] - base);
+                    l_run[h] += s[h][u];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[h][e] = mul2(acc[h][e], make_float2(alpha, alpha));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float2 e[4];
+                centred8(vcode[u], e);
+                const float zero = fmaf(8.f, vp[u].x, vp[u].y);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const float w = s[h][u] * vp[u].x;
+                    zero_sum[h] = fmaf(s[h][u], zero, zero_sum[h]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[h][i] = fma2(make_float2(w, w), e[i], acc[h][i]);
+                }
+            }
         }
     }
     // the slices' states, lanes j of every slice
-    float M = m_run;
 #pragma unroll
-    for (int sh = W; sh < 32; sh <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, sh));
-    const float f = m_run == -INFINITY ? 0.f : exp2f(m_run - M);
-    float L = l_run * f;
+    for (int h = 0; h < H; ++h) {
+        float M = m_run[h];
 #pragma unroll
-    for (int sh = W; sh < 32; sh <<= 1) L += __shfl_xor_sync(kFull, L, sh);
+        for (int sh = W; sh < 32; sh <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, sh));
+        const float f = m_run[h] == -INFINITY ? 0.f : exp2f(m_run[h] - M);
+        float L = l_run[h] * f, z = zero_sum[h] * f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        acc[e] *= f;
+        for (int sh = W; sh < 32; sh <<= 1) {
+            L += __shfl_xor_sync(kFull, L, sh);
+            z += __shfl_xor_sync(kFull, z, sh);
+        }
+        const size_t bi = bi0 + h;
+        float *dst = nc == 1 ? p.out + bi * d : p.ws_o + (bi * p.splits + split) * d;
 #pragma unroll
-        for (int sh = W; sh < 32; sh <<= 1) acc[e] += __shfl_xor_sync(kFull, acc[e], sh);
-    }
-    float *dst = nc == 1 ? p.out + bi * d : p.ws_o + (bi * p.splits + split) * d;
-    if (mine && slice == 0) {
+        for (int e = 0; e < 4; ++e) {
+            float2 y = mul2(acc[h][e], make_float2(f, f));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[j * 8 + e] = acc[e] / L;
-    }
-    if (lane == 0) {
-        const float lse2 = M + log2f(L);
-        if (nc > 1) p.ws_lse[bi * p.splits + split] = lse2;
-        else if (p.lse != nullptr) p.lse[bi] = lse2 * kDecLn2;
+            for (int sh = W; sh < 32; sh <<= 1)
+                y = add2(y, make_float2(__shfl_xor_sync(kFull, y.x, sh), __shfl_xor_sync(kFull, y.y, sh)));
+            if (mine && slice == 0 && h < heads) {
+                dst[j * 8 + e] = fmaf(y.x, 0x1p9f, z) / L;
+                dst[j * 8 + e + 4] = fmaf(y.y, 0x1p9f, z) / L;
+            }
+        }
+        if (lane == 0 && h < heads) {
+            const float lse2 = M + log2f(L);
+            if (nc > 1) p.ws_lse[bi * p.splits + split] = lse2;
+            else if (p.lse != nullptr) p.lse[bi] = lse2 * kDecLn2;
+        }
     }
 }
+
 
 // ============================================================== warp-MMA path
 //
@@ -656,17 +729,23 @@ cudaError_t launch_mma(const AttendQ4Params &P, int d, int bs, int G, dim3 grid,
 #undef PKV_Q4_MMA
 }
 
-cudaError_t launch_simt(const AttendQ4Args &a, const DecodeKParams &kp, cudaStream_t stream) {
-    const long long units = static_cast<long long>(a.rows) * a.Hq;
+template <int H>
+cudaError_t launch_simt_as(const AttendQ4Args &a, const DecodeKParams &kp, cudaStream_t stream) {
+    const long long units = static_cast<long long>(a.rows) * a.Hkv * ((kp.m + H - 1) / H);
     const dim3 grid(static_cast<unsigned>((units + 3) / 4), static_cast<unsigned>(kp.splits));
     const int words = a.d / 8, lanes = a.group / 8;
-#define PKV_Q4_SIMT(WW) attend_q4_simt_kernel<WW><<<grid, 128, 0, stream>>>(a.k_cache, a.v_cache, kp, a.d, a.bs, lanes, a.rows)
+#define PKV_Q4_SIMT(WW) attend_q4_simt_kernel<WW, H><<<grid, 128, 0, stream>>>(a.k_cache, a.v_cache, kp, a.d, a.bs, lanes, a.rows)
     if (words <= 4) PKV_Q4_SIMT(4);
     else if (words <= 8) PKV_Q4_SIMT(8);
     else if (words <= 16) PKV_Q4_SIMT(16);
     else PKV_Q4_SIMT(32);
 #undef PKV_Q4_SIMT
     return cudaGetLastError();
+}
+
+cudaError_t launch_simt(const AttendQ4Args &a, const DecodeKParams &kp, cudaStream_t stream) {
+    const int heads = simt_heads(kp.m);
+    return heads == 1 ? launch_simt_as<1>(a, kp, stream) : heads == 2 ? launch_simt_as<2>(a, kp, stream) : launch_simt_as<4>(a, kp, stream);
 }
 
 // Units with at most this many chunks merge in the attention kernel.
@@ -704,7 +783,8 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     plan.mma_rows = slots <= FourRows<64, 16, 1>::ROWS ? FourRows<64, 16, 1>::ROWS : EightRows<64, 16, 1>::ROWS;
     const int per_tile = plan.umma ? kQ4UmmaSlots : plan.mma_rows;
     plan.tiles = plan.umma || plan.mma ? static_cast<int>((slots + per_tile - 1) / per_tile) : 1;
-    const long long units = plan.umma || plan.mma ? static_cast<long long>(B) * Hkv * plan.tiles : static_cast<long long>(rows) * Hq;
+    const long long units = plan.umma || plan.mma ? static_cast<long long>(B) * Hkv * plan.tiles
+                                                      : static_cast<long long>(rows) * Hkv * ((m + simt_heads(m) - 1) / simt_heads(m));
     int chunk = pages;
     if (num_splits > 1) {
         chunk = (pages + num_splits - 1) / num_splits;
@@ -720,7 +800,7 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
         chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
     } else if (num_splits == 0) {
-        // one warp per (row, head, chunk): several warps for each scheduler, no chunk shorter
+        // one warp per (row, heads, chunk): several warps for each scheduler, no chunk shorter
         // than 128 keys
         const int least = std::max(1, 128 / bs);
         while (chunk > least && units * ((pages + chunk - 1) / chunk) < 32ll * sms) chunk = (chunk + 1) / 2;
