@@ -12,6 +12,12 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStageKeys = 32;
 
+// Blocks of an SM for tiles of 4 or 8 rows: what registers (128, 168, 255 a thread) and the stages of wider
+// heads leave.
+__host__ __device__ constexpr int mma_blocks_per_sm(int rows, int d) {
+    return rows == 4 ? (d <= 128 ? 4 : d <= 192 ? 3 : 2) : d <= 128 ? 3 : 2;
+}
+
 // D = A(16x16, f16, row) * B(16x8, f16, col) + D, fp32 accumulate.
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
@@ -47,7 +53,8 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
         const uint2 u = *reinterpret_cast<const uint2 *>(p);
         w[0] = u.x, w[1] = u.y;
     } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
     }
 }
 
@@ -97,7 +104,7 @@ struct EightRows {
     // Three blocks (12 warps, 168 registers a thread) against four (128, with spills): 70B-shaped step 91.4
     // against 94.2 us, four sequences of 131072 tokens 142 against 139 (before V's codes were centred).
     // 16 rows a warp in two blocks (255 registers) take 10% less from 25 rows on and more below: not kept.
-    static constexpr int kBlocksPerSm = 3;
+    static constexpr int kBlocksPerSm = mma_blocks_per_sm(8, D);
     static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
 
     uint4 *qfrag;    // [step][lane] of the warp, in shared memory
@@ -365,7 +372,7 @@ struct FourRows {
     static constexpr int WORDS = D / 8, WPT = WORDS / (4 * G), HPG = D / 32 / G, NT = kStageKeys / 8;
     static constexpr int kCodeBytes = BS * D / 2, kPageBytes = BS * (D / 2 + 4 * G);
     static constexpr int kQBytes = 0;
-    static constexpr int kBlocksPerSm = 4;   // 128 registers a thread
+    static constexpr int kBlocksPerSm = mma_blocks_per_sm(4, D);
     static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
 
     uint4 *qfrag;   // not used
