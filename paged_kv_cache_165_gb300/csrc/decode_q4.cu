@@ -24,12 +24,10 @@ namespace {
 int simt_heads(int m) { return m <= 2 ? m : 4; }
 
 // One warp per (query row, H query heads of a KV head, chunk).  W lanes (a power of two, W * 8 >= d)
-// hold one key's row, eight elements each, so 32 / W keys are taken at a time, kSimtBatch such steps
+// hold one key's row, eight elements each, so 32 / W keys are taken at a time, U such steps (16 keys at most)
 // between two updates of the softmax; every such slice of the warp keeps its own online softmax and
 // they merge at the end.  Bound by its arithmetic, shuffles most of all (64 x 2048 tokens, 32 heads on 8 of
 // 128, bs 8: 248 us).
-constexpr int kSimtBatch = 4;
-
 // A word's codes less 8, times 2^-9: elements (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ void centred8(uint32_t w, float2 (&e)[4]) {
     uint32_t h[4];
@@ -43,7 +41,7 @@ template <int W, int H>
 __global__ void __launch_bounds__(128)
     attend_q4_simt_kernel(const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc, const DecodeKParams p,
                           int d, int bs, int lanes, int rows) {
-    constexpr int KEYS = 32 / W, U = kSimtBatch;
+    constexpr int KEYS = 32 / W, U = W == 4 ? 2 : 4;
     pdl_launch_dependents();   // the merge kernel after this one waits for the whole grid
     const int lane = threadIdx.x & 31, tiles = (p.m + H - 1) / H;
     const long long unit = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;

@@ -146,7 +146,7 @@ struct Parts {
     unsigned *counter;
 };
 
-// The warp-MMA kernel for head sizes of 96 (groups of 32), 160 (32), 192 (32, 64) and 256 (64, 128), tiles
+// The warp-MMA kernel for head sizes of 32, 96, 160 (groups of 32), 192 (32, 64) and 256 (64, 128), tiles
 // of `rows` 4 or 8 (decode_q4_wide.cu).
 bool q4_wide_shape(int d, int group, int bs);
 cudaError_t launch_attend_q4_wide(const AttendQ4Params &P, int rows, int d, int bs, int G, dim3 grid, cudaStream_t stream);

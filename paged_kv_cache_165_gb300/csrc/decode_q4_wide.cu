@@ -6,7 +6,7 @@
 namespace pkv {
 
 bool q4_wide_shape(int d, int group, int bs) {
-    return (bs == 16 || bs == 32) && (((d == 96 || d == 160) && group == 32) || (d == 192 && group <= 64) || (d == 256 && group >= 64));
+    return (bs == 16 || bs == 32) && (((d == 32 || d == 96 || d == 160) && group == 32) || (d == 192 && group <= 64) || (d == 256 && group >= 64));
 }
 
 namespace {
@@ -14,6 +14,7 @@ template <template <int, int, int> class Rows, int BS>
 cudaError_t launch_as(const AttendQ4Params &P, int d, int G, dim3 grid, cudaStream_t stream) {
 #define PKV_Q4_WIDE(DD, GG) \
     if (d == DD && G == GG) return launch_mma_as<DD, BS, GG, Rows<DD, BS, GG>>(P, grid, stream)
+    PKV_Q4_WIDE(32, 1);
     PKV_Q4_WIDE(96, 3);
     PKV_Q4_WIDE(160, 5);
     PKV_Q4_WIDE(192, 3);
