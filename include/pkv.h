@@ -445,7 +445,7 @@ pkv_status pkv_paged_attention_q4(float *out, float *lse, const float *q, const 
  *   k_new, v_new  [B][Hkv][d], element type new_dt (PKV_BF16 or PKV_F32)
  *   slot_mapping  int64 [B]: the slot of position context_lens[b] - 1, or < 0 (no new token); its
  *                 block must belong to sequence b alone, as for pkv_decode_step.  Up to eight
- *                 query heads per KV head (bs in {16, 32}, d other than 224, with d = 256 groups of
+ *                 query heads per KV head (bs in {8, 16, 32}, d other than 224, with d = 256 groups of
  *                 64 or 128, 16-byte aligned caches, q and out) the attention launch
  *                 quantises the new rows itself; then a slot other than the last position's (or any
  *                 slot for an empty sequence) sets PKV_DEVERR_SLOT and is not written.  Otherwise

@@ -27,7 +27,7 @@ int simt_heads(int m) { return m <= 2 ? m : 4; }
 // hold one key's row, eight elements each, so 32 / W keys are taken at a time, U such steps (16 keys at most)
 // between two updates of the softmax; every such slice of the warp keeps its own online softmax and
 // they merge at the end.  Bound by its arithmetic, shuffles most of all (64 x 2048 tokens, 32 heads on 8 of
-// 128, bs 8: 248 us).
+// 128: 248 us, the warp-MMA kernel 45).
 // A word's codes less 8, times 2^-9: elements (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ void centred8(uint32_t w, float2 (&e)[4]) {
     uint32_t h[4];
@@ -260,8 +260,8 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     const int m = Hq / Hkv, sms = std::max(sm_count, 1);
     const long long slots = static_cast<long long>(max_q) * m;
     plan.umma = q4_umma_shape(d, group, bs) && aligned && slots > q4_mma_slots(d / group) && slots < (1 << 20);
-    const bool wide = q4_wide_shape(d, group, bs);
-    plan.mma = !plan.umma && (wide || ((d == 64 || d == 128) && (bs == 16 || bs == 32))) && aligned && slots < (1 << 20);
+    plan.mma = !plan.umma && (d == 64 || d == 128 || q4_wide_shape(d, group)) && (bs == 8 || bs == 16 || bs == 32) && aligned &&
+               slots < (1 << 20);
     plan.mma_rows = slots <= 4 ? 4 : 8;
     const int per_tile = plan.umma ? kQ4UmmaSlots : plan.mma_rows;
     plan.tiles = plan.umma || plan.mma ? static_cast<int>((slots + per_tile - 1) / per_tile) : 1;
@@ -354,7 +354,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         P.balanced = plan.balanced;
         const dim3 grid = plan.balanced ? dim3(plan.blocks) : dim3(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
         e = plan.umma ? launch_attend_q4_umma(P, a.d, a.bs, a.d / a.group, grid, stream)
-            : q4_wide_shape(a.d, a.group, a.bs) ? launch_attend_q4_wide(P, plan.mma_rows, a.d, a.bs, a.d / a.group, grid, stream)
+            : a.bs == 8 ? launch_attend_q4_bs8(P, plan.mma_rows, a.d, a.d / a.group, grid, stream)
+            : q4_wide_shape(a.d, a.group) ? launch_attend_q4_wide(P, plan.mma_rows, a.d, a.bs, a.d / a.group, grid, stream)
             : plan.mma_rows == 4 ? launch_mma<FourRows>(P, a.d, a.bs, a.d / a.group, grid, stream)
                                  : launch_mma<EightRows>(P, a.d, a.bs, a.d / a.group, grid, stream);
     } else {

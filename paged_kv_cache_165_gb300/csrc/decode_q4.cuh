@@ -146,10 +146,11 @@ struct Parts {
     unsigned *counter;
 };
 
-// The warp-MMA kernel for head sizes of 32, 96, 160 (groups of 32), 192 (32, 64) and 256 (64, 128), tiles
-// of `rows` 4 or 8 (decode_q4_wide.cu).
-bool q4_wide_shape(int d, int group, int bs);
+// The warp-MMA kernel, tiles of `rows` 4 or 8, for head sizes of 32, 96, 160 (groups of 32), 192 (32, 64) and
+// 256 (64, 128) with pages of 16 or 32 tokens (decode_q4_wide.cu), and for pages of eight (decode_q4_bs8.cu).
+bool q4_wide_shape(int d, int group);
 cudaError_t launch_attend_q4_wide(const AttendQ4Params &P, int rows, int d, int bs, int G, dim3 grid, cudaStream_t stream);
+cudaError_t launch_attend_q4_bs8(const AttendQ4Params &P, int rows, int d, int G, dim3 grid, cudaStream_t stream);
 
 // The tcgen05 kernel (decode_q4_umma.cu): 9 and more query rows x heads for each KV head.
 constexpr int kQ4UmmaSlots = 64;   // (query row, head) pairs of a tile

@@ -12,7 +12,7 @@ namespace {
 constexpr int kLeastSteps = 4;       // 32-key steps that a warp of one takes at least (128 keys)
 // ============================================================== warp-MMA path
 //
-// attend_q4_mma_kernel (d a multiple of 32, bs 16 or 32).  A unit is a tile of eight, or up to four, (query row,
+// attend_q4_mma_kernel (d a multiple of 32, bs 8, 16 or 32).  A unit is a tile of eight, or up to four, (query row,
 // head) pairs of one sequence and KV head with the keys they see; a warp takes 32 keys at a time from a
 // private ring of bulk copies (a page is one contiguous run).  Per 32 keys and warp, with m16n8k16
 // f16 MMAs and fp32 accumulators:

@@ -5,8 +5,8 @@
 
 namespace pkv {
 
-bool q4_wide_shape(int d, int group, int bs) {
-    return (bs == 16 || bs == 32) && (((d == 32 || d == 96 || d == 160) && group == 32) || (d == 192 && group <= 64) || (d == 256 && group >= 64));
+bool q4_wide_shape(int d, int group) {
+    return ((d == 32 || d == 96 || d == 160) && group == 32) || (d == 192 && group <= 64) || (d == 256 && group >= 64);
 }
 
 namespace {

@@ -135,7 +135,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 
 struct Q4Plan {
     bool umma;           // many (query row, head) pairs per sequence and KV head: the tcgen05 kernel
-    bool mma;            // most d and group sizes with bs 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
+    bool mma;            // most d and group sizes with bs 8, 16 or 32, aligned: the warp-MMA kernel; else CUDA cores
     int mma_rows;        // mma: pairs of a tile, 4 or 8
     int tiles;           // tiles of 64 (umma) or mma_rows pairs per sequence and KV head
     bool balanced;       // even shares of all sequences' keys for `blocks` thread blocks

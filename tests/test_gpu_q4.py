@@ -213,6 +213,7 @@ SHAPES = [  # hq, hkv, d, group, bs
     (130, 1, 128, 64, 16),                                            # more heads than a tile
     (8, 1, 96, 32, 32), (24, 2, 192, 64, 16), (3, 1, 192, 32, 32), (16, 2, 256, 64, 16), (2, 2, 256, 64, 32),
     (12, 2, 160, 32, 32), (6, 2, 256, 32, 16), (5, 1, 224, 32, 16), (1, 1, 96, 32, 8), (3, 1, 32, 32, 16),
+    (8, 1, 128, 32, 8), (5, 1, 256, 128, 8), (20, 1, 64, 32, 8), (6, 2, 128, 64, 24),
 ]
 
 
@@ -304,7 +305,7 @@ ATOL_MEAN = 6e-6
 
 @pytest.mark.parametrize("hq,d,group,bs", [(8, 128, 64, 16), (4, 128, 32, 32), (1, 64, 64, 16), (64, 128, 128, 16),
                                            (64, 128, 64, 32), (64, 64, 64, 16), (2, 96, 32, 16), (2, 96, 32, 8),
-                                           (8, 256, 64, 16), (5, 224, 32, 16)])
+                                           (8, 256, 64, 16), (5, 224, 32, 16), (1, 128, 128, 24)])
 def test_q4_errors_do_not_grow_with_the_context(hq, d, group, bs):
     case = q4_case(12, [40003], hq, 1, d, group, bs)
     case = (torch.zeros_like(case[0]), *case[1:])
@@ -506,7 +507,8 @@ def run_step(case, k_new, v_new, slots, group, scale, window, num_splits, fused)
 @pytest.mark.parametrize("hq,hkv,d,group,bs", [(64, 8, 128, 64, 16), (8, 8, 128, 128, 16), (16, 2, 128, 32, 32),
                                                (8, 2, 64, 32, 16), (32, 2, 128, 64, 16), (64, 1, 128, 128, 16),
                                                (4, 2, 96, 32, 8), (8, 2, 96, 32, 16), (4, 2, 256, 64, 16),
-                                               (16, 2, 192, 64, 32), (16, 2, 256, 128, 16), (10, 2, 160, 32, 16)])
+                                               (16, 2, 192, 64, 32), (16, 2, 256, 128, 16), (10, 2, 160, 32, 16),
+                                               (8, 1, 128, 64, 8), (4, 2, 128, 64, 24)])
 @pytest.mark.parametrize("new_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("num_splits,window", [(0, 0), (1, 0), (3, 40)])
 def test_q4_decode_step_equals_append_then_attention(hq, hkv, d, group, bs, new_dtype, num_splits, window):
