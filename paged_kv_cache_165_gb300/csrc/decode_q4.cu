@@ -271,16 +271,24 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
     if (num_splits > 1) {
         chunk = (pages + num_splits - 1) / num_splits;
     } else if (num_splits == 0 && (plan.umma || plan.mma)) {
-        // An equal share for every warp (umma: block) the device holds at once, unless the units are
-        // so few that one would be left to merge parts from many: then, or with more sequences than a
-        // block scans, equal chunks for one wave of blocks and a merge over many blocks.
+        // An equal share for every warp (umma: block) the device holds at once, or equal chunks, at most
+        // one wave of blocks.  Chunks where the units are so few that one would be left to merge parts
+        // from many, with more sequences than a block scans, and for warp MMAs where the shares are
+        // short, because a chunk's warps merge in shared memory: below 16 steps of 32 keys a warp (256
+        // units of four rows: 512 tokens 16.3 us in equal shares, 10.6 in chunks, 2048 33.5 and 26.9, 4096,
+        // 13.5 steps, 46.9 and 44.2; eight rows, 4096, 18 steps: 53.5 and 62.7), or 8 where one wave does
+        // not hold the units (1024 of four rows: 256 tokens 21.6 and 16.7; 512 of eight: 19.4 and 18.0, 1024
+        // tokens, 9 steps, 34.5 and 38.6).
         const int step = plan.umma ? 128 / (d / group) : kStageKeys;
         plan.blocks = sms * (plan.umma ? 1 : mma_blocks_per_sm(plan.mma_rows, d));
-        plan.balanced = B <= kMaxBalanced && (plan.umma ? plan.blocks <= 8 * units : plan.blocks * kMmaWarps <= 24 * units) &&
-                        units * (static_cast<long long>(pages) * bs / step + 1 + kUnitCost) < (1ll << 30);
-        const int least = 256 / bs;
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
+        const int least = (plan.mma && per_unit <= 8 ? 512 : 256) / bs;
         chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
+        const long long share = units * (static_cast<long long>(pages) * bs / step) / (static_cast<long long>(plan.blocks) * kMmaWarps);
+        const bool few = plan.umma ? plan.blocks > 8 * units : plan.blocks > 6 * units;
+        const bool brief = plan.mma && (share < 8 ? units <= 2 * plan.blocks : share < 16 && units <= plan.blocks);
+        plan.balanced = B <= kMaxBalanced && !few && !brief &&
+                        units * (static_cast<long long>(pages) * bs / step + 1 + kUnitCost) < (1ll << 30);
     } else if (num_splits == 0) {
         // one warp per (row, heads, chunk): several warps for each scheduler, no chunk shorter
         // than 128 keys

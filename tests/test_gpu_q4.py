@@ -421,6 +421,26 @@ def test_q4_pointers_aligned_to_their_elements_only(hq, hkv):
             pkv.paged_attention_q4(out, qq, kk, dev(vc), dev(table), dev(lens), 0.1, group, lse=lse, workspace=ws)
 
 
+@pytest.mark.parametrize("hq,hkv,d,group,bs,rows,window", [
+    (16, 8, 128, 64, 16, 1, 0), (64, 8, 128, 64, 16, 1, 0), (8, 8, 256, 128, 16, 1, 0), (32, 8, 96, 32, 16, 1, 70), (8, 8, 64, 64, 8, 2, 0),
+    (16, 4, 128, 32, 32, 4, 0), (40, 4, 64, 64, 16, 1, 0), (64, 4, 128, 64, 16, 3, 100)])
+def test_q4_shares_of_many_sequences(hq, hkv, d, group, bs, rows, window):
+    """Tables much longer than the sequences and many of those: equal shares for every warp or block, which
+    begin and end inside units."""
+    g = gen.generator(61)
+    lens = torch.randint(0, 400, (70 if hkv == 8 else 150,), generator=g).tolist()
+    lens[3], lens[10], lens[-1] = 1, 2500, 700
+    case = list(q4_case(61, lens, hq, hkv, d, group, bs, [min(rows, n) for n in lens] if rows > 1 else None))
+    case[3] = torch.cat([case[3], torch.full((len(lens), 8000 // bs - case[3].shape[1]), -1, dtype=torch.int32)], 1)
+    live, ref, ref_lse = expect(case, group, 0.1, window)
+    out, lse = run_q4(case, group, 0.1, window, decode=rows == 1, max_q=rows)
+    assert_attn_close(out[live], ref, "out", ATOL)
+    assert_attn_close(lse[live], ref_lse, "lse", ATOL)
+    again = run_q4(case, group, 0.1, window, decode=rows == 1, max_q=rows)
+    assert torch.equal(out[live], again[0][live]) and torch.equal(lse[live], again[1][live])
+    assert pkv.get_device_error() == 0
+
+
 def test_q4_streams_and_a_workspace_used_in_turn():
     """Two streams with workspaces of their own at once; calls of different shapes one after the other in one."""
     shapes = [(16, 2, 128, 64, 16), (64, 1, 128, 128, 16), (8, 2, 64, 32, 16), (4, 2, 96, 32, 16)]
