@@ -282,9 +282,14 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         const int step = plan.umma ? 128 / (d / group) : kStageKeys;
         plan.blocks = sms * (plan.umma ? 1 : mma_blocks_per_sm(plan.mma_rows, d));
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));
-        const int least = (plan.mma && per_unit <= 8 ? 512 : 256) / bs;
+        // Tokens of a chunk: 512 where units fill the device (256 units of 2048: 26.9 us, in more chunks 31),
+        // else 256, and down to 128 while at most eight chunks merge in place (two sequences of 512, four
+        // units: four chunks 7.3 us, two 8.3; eight units of 1000: 7.8 in eight, 8.5 in four; 300 tokens: 6.0 in one
+        // chunk, 6.5 in three).
+        const long long tokens = static_cast<long long>(pages) * bs;
+        const int least = (!plan.mma ? 256 : per_unit <= 8 || tokens <= 384 ? 512 : tokens <= 1024 ? 128 : 256) / bs;
         chunk = static_cast<int>(std::max<long long>(least, (pages + per_unit - 1) / per_unit));
-        const long long share = units * (static_cast<long long>(pages) * bs / step) / (static_cast<long long>(plan.blocks) * kMmaWarps);
+        const long long share = units * (tokens / step) / (static_cast<long long>(plan.blocks) * kMmaWarps);
         const bool few = plan.umma ? plan.blocks > 8 * units : plan.blocks > 6 * units;
         const bool brief = plan.mma && (share < 8 ? units <= 2 * plan.blocks : share < 16 && units <= plan.blocks);
         plan.balanced = B <= kMaxBalanced && !few && !brief &&
