@@ -307,7 +307,7 @@ int pkv_decode_step_shared_prefix_kernel_launches(int B, int Hq, int Hkv, int d,
  *                rules as pkv_paged_decode_attention.
  * One query per sequence runs the decode kernels (tensor cores where they apply);
  * several run a CUDA-core kernel, one warp per (query row, head, chunk).  An
- * inconsistent cu_q or a row count above its sequence length sets
+ * inconsistent cu_q, or a row count above max_q or its sequence length, sets
  * PKV_DEVERR_CU_SEQLENS and those rows get out = 0, lse = -inf.  Requires
  * Tq <= B * max_q and Tq * Hq < 2^31.
  */

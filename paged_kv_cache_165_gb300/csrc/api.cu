@@ -391,6 +391,7 @@ pkv_status pkv_paged_attention(float *out, float *lse, const float *q, const voi
     a.window = window;
     a.cu_q = one_per_seq ? nullptr : cu_q;
     a.rows = one_per_seq ? B : Tq;
+    a.max_q = max_q;
     cudaError_t e = launch_decode(a, plan, dt, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "paged_attention launch");
 }

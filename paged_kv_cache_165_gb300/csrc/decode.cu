@@ -1046,6 +1046,8 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
     kp.scale_log2 = a.scale * kLog2e;
     kp.window = a.window;
     kp.cu_q = a.cu_q;
+    kp.rows = rows;
+    kp.max_q = a.max_q;
     kp.k_scale = a.k_scale;
     kp.v_scale = a.v_scale;
     kp.q_per_tile = plan.q_per_tile;

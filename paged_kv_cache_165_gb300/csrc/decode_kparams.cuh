@@ -27,6 +27,7 @@ struct DecodeKParams {
     float scale_log2; // scale * log2(e): scores are kept in the base-2 domain
     int window;       // > 0: only the most recent `window` tokens are visible
     const int32_t *cu_q;   // query rows per sequence [B+1]; nullptr: row b = sequence b
+    int rows, max_q;       // with cu_q: query rows of the call, and of a sequence at most
     const float *k_scale, *v_scale;   // FP8 caches: fp32 scale per row [NB][Hkv][bs]
     int q_per_tile;   // tcgen05 kernel: query rows of a sequence per block (1 for decode)
     int qtiles;       // tcgen05 kernel: query tiles per sequence (grid z = B * qtiles)
@@ -115,8 +116,16 @@ __device__ __forceinline__ SeqSpan seq_span(const DecodeKParams &p, int b, int b
     return span_of(p, b, checked_len(p, b, bs, report), bs);
 }
 
+// Whether a sequence of L tokens may own the query rows [c0, c1).  Every kernel of a call asks
+// this, the merge of its partials too: the plan's chunks and workspace are sized by rows and
+// max_q (with a window W a sequence's rows see at most W + max_q - 1 tokens), so that the rows of
+// a sequence that passes have at most `splits` chunks, and a refused one's partials are never read.
+__device__ __forceinline__ bool query_rows_ok(const DecodeKParams &p, int c0, int c1, int L) {
+    return c0 >= 0 && c1 >= c0 && c1 <= p.rows && c1 - c0 <= min(L, p.max_q);
+}
+
 // Query row r (cu_q != nullptr): its sequence by binary search over cu_q, its position,
-// its span.  An inconsistent cu_q or a row count above the sequence length raises
+// its span.  An inconsistent cu_q, or a row count above max_q or the sequence length, raises
 // PKV_DEVERR_CU_SEQLENS and the row sees nothing (out = 0, lse = -inf).
 __device__ __forceinline__ SeqSpan row_span(const DecodeKParams &p, int r, int bs, bool report) {
     if (p.cu_q == nullptr) return seq_span(p, r, bs, report);
@@ -130,7 +139,7 @@ __device__ __forceinline__ SeqSpan row_span(const DecodeKParams &p, int r, int b
     const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
     const int L = checked_len(p, b, bs, report);
     const int nq = c1 - c0;
-    if (r < c0 || r >= c1 || nq > L) {
+    if (r < c0 || r >= c1 || !query_rows_ok(p, c0, c1, L)) {
         if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
         return span_of(p, b, 0, bs);
     }

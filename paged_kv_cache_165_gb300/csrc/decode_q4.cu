@@ -339,6 +339,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
     kp.scale_log2 = a.scale * kDecLog2e;
     kp.window = a.window;
     kp.cu_q = a.cu_q;
+    kp.rows = a.rows;
+    kp.max_q = a.max_q;
     if (plan.workspace_bytes > 0) {
         uint8_t *ws = static_cast<uint8_t *>(a.workspace);
         const size_t parts = plan.balanced ? balanced_rows(plan)
@@ -362,8 +364,6 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, const Q4Plan &plan, cudaStre
         P.k = kp;
         P.kc = const_cast<uint8_t *>(a.k_cache);   // written only for a step's new tokens
         P.vc = const_cast<uint8_t *>(a.v_cache);
-        P.rows = a.rows;
-        P.max_q = a.max_q;
         P.balanced = plan.balanced;
         const dim3 grid = plan.balanced ? dim3(plan.blocks) : dim3(static_cast<unsigned>(plan.splits) * plan.tiles, a.Hkv, a.B);
         e = plan.umma ? launch_attend_q4_umma(P, a.d, a.bs, a.d / a.group, grid, stream)

@@ -15,7 +15,6 @@ namespace pkv {
 struct AttendQ4Params {
     DecodeKParams k;     // head_tiles: tiles of eight (query row, head) pairs per sequence and KV head
     uint8_t *kc, *vc;
-    int rows, max_q;     // query rows of the call, and of a sequence at most
     int new_bf16;        // type of the step's new rows
     float q_sign;        // the queries are taken times the scale's sign (0, 1, -1) and k.scale_log2 is positive, so
                          // that masked scores of -inf stay what they are when they are scaled
@@ -97,11 +96,11 @@ __device__ __forceinline__ SeqRows seq_rows(const AttendQ4Params &P, int b, int 
         const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
         s.r0 = c0;
         s.nq = c1 - c0;
-        s.ok = c0 >= 0 && c1 >= c0 && c1 <= P.rows && s.nq <= s.L && s.nq <= P.max_q;
-        if (!s.ok) s.z0 = min(max(c0, 0), P.rows), s.z1 = min(max(c1, 0), P.rows);
+        s.ok = query_rows_ok(p, c0, c1, s.L);
+        if (!s.ok) s.z0 = min(max(c0, 0), p.rows), s.z1 = min(max(c1, 0), p.rows);
         // rows before the first sequence or behind the last one belong to none
-        if (b == 0 && c0 > 0) s.z2 = 0, s.z3 = min(c0, P.rows);
-        if (b == p.B - 1 && c1 < P.rows) s.z2 = max(c1, 0), s.z3 = P.rows;
+        if (b == 0 && c0 > 0) s.z2 = 0, s.z3 = min(c0, p.rows);
+        if (b == p.B - 1 && c1 < p.rows) s.z2 = max(c1, 0), s.z3 = p.rows;
         if (report && (!s.ok || s.z3 > s.z2)) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
     }
     s.first = p.window > 0 ? max(0, s.L - s.nq + 1 - p.window) / bs : 0;

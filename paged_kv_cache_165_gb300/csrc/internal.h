@@ -107,6 +107,7 @@ struct DecodeArgs {
     const float *v_scale = nullptr;
     const int32_t *cu_q = nullptr;   // query rows per sequence; nullptr: one per sequence
     int rows = -1;                   // query rows (B when cu_q is nullptr)
+    int max_q = 1;                   // query rows of a sequence at most
     // the step's new tokens, appended inside the decode launch (decode_fuses_append)
     const void *k_new = nullptr, *v_new = nullptr;   // [B][Hkv][d], bf16
     const int64_t *new_slots = nullptr;              // [B]; < 0: no new token

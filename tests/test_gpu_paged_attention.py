@@ -248,3 +248,46 @@ def test_prefix_chunk_prefill_at_full_size():
     ref, ref_lse = oracle.paged_attention(q, kc, vc, table, clens, cu, scale, nthreads=os.cpu_count() or 1)
     assert_attn_close(out, ref, "chunk out")
     assert_attn_close(lse, ref_lse, "chunk lse")
+
+
+def refused(q, kc, vc, table, lens, cu, max_q, window, splits):
+    """run() with max_q given, over a workspace whose partials hold NaN."""
+    Tq, Hq, d = q.shape
+    NB, Hkv, bs, _ = kc.shape
+    out = torch.full((Tq, Hq, d), float("nan"), device="cuda")
+    lse = torch.full((Tq, Hq), float("nan"), device="cuda")
+    n = pkv.paged_attention_workspace_bytes(lens.numel(), Tq, max_q, Hq, Hkv, d, bs, table.shape[1], window, splits)
+    ws = torch.full((max(16, n),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256 << 10] = 0
+    pkv.paged_attention(out, dev(q), dev(kc), dev(vc), dev(table), dev(lens), 0.1, cu_q=dev(cu), max_q=max_q,
+                        window=window, lse=lse, num_splits=splits, workspace=ws)
+    assert pkv.get_device_error() == pkv.DEVERR["cu_seqlens"]
+    return out, lse
+
+
+CUDA_CORE_REFUSALS = [(8, 2, 40, torch.float32, 8, 20, 1), (8, 2, 40, torch.float32, 8, 0, 0),
+                      (4, 1, 96, torch.bfloat16, 16, 100, 3)]
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs,window,splits", CUDA_CORE_REFUSALS)
+def test_more_rows_than_max_q_are_flagged(hq, hkv, d, dtype, bs, window, splits):
+    q, kc, vc, table, lens, cu = make_case(71, [500, 900, 70, 33], [5, 2, 1, 0], hq, hkv, d, bs, dtype)
+    out, lse = refused(q, kc, vc, table, lens, cu, 2, window, splits)
+    assert torch.all(out[:5] == 0) and torch.all(torch.isneginf(lse[:5]))
+    ref, ref_lse = oracle.paged_attention(q[5:], kc, vc, table[1:], lens[1:], cu[1:] - 5, 0.1, window)
+    assert_attn_close(out[5:], ref, "the other sequences")
+    assert_attn_close(lse[5:], ref_lse, "the other sequences' lse")
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs,window,splits", CUDA_CORE_REFUSALS)
+@pytest.mark.parametrize("bounds", [(0, 2, 9), (-3, 2, 4)])
+def test_rows_outside_the_call_are_flagged(hq, hkv, d, dtype, bs, window, splits, bounds):
+    q, kc, vc, table, lens, _ = make_case(73, [700, 900], [2, 2], hq, hkv, d, bs, dtype)
+    out, lse = refused(q, kc, vc, table, lens, torch.tensor(bounds, dtype=torch.int32), 8, window, splits)
+    good, bad = (0, 1) if bounds[0] == 0 else (1, 0)
+    assert torch.all(out[2 * bad:2 * bad + 2] == 0) and torch.all(torch.isneginf(lse[2 * bad:2 * bad + 2]))
+    at = slice(2 * good, 2 * good + 2)
+    ref, ref_lse = oracle.paged_attention(q[at], kc, vc, table[good:good + 1], lens[good:good + 1],
+                                          torch.tensor([0, 2], dtype=torch.int32), 0.1, window)
+    assert_attn_close(out[at], ref, "the good sequence")
+    assert_attn_close(lse[at], ref_lse, "the good sequence's lse")

@@ -581,3 +581,42 @@ def test_q4_decode_step_slots_that_are_not_the_last_position(hq, fused):
     if fused:
         _, _, kc, _ = run_step(case, k_new, v_new, slots, group, 0.1, 0, 0, True)
         assert pkv.get_device_error() == pkv.DEVERR["slot"]
+
+
+# ------------------------------------------------------------------ rows that a call refuses
+
+REFUSALS = [  # hq, hkv, d, group, bs, window, num_splits: the kernel that attends, and how its parts meet
+    (4, 1, 128, 64, 24, 24, 1), (4, 1, 128, 64, 24, 24, 3), (4, 1, 128, 64, 24, 0, 0), (2, 2, 224, 32, 16, 100, 0),   # CUDA cores
+    (8, 1, 128, 64, 16, 0, 20), (4, 2, 96, 32, 8, 0, 20), (8, 1, 128, 64, 16, 0, 3), (8, 1, 128, 64, 16, 50, 0),      # warp MMAs
+    (64, 1, 128, 64, 16, 0, 5), (64, 2, 64, 64, 16, 40, 0), (64, 1, 128, 128, 32, 0, 1)]                             # tcgen05
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs,window,splits", REFUSALS)
+def test_q4_more_rows_than_max_q_are_flagged_on_every_path(hq, hkv, d, group, bs, window, splits):
+    """Five rows where max_q says two: refused whichever kernel attends and whichever one merges."""
+    case = q4_case(71, [500, 2000, 70, 33], hq, hkv, d, group, bs, [5, 2, 1, 0])
+    q, kc, vc, table, lens, cu = case
+    out, lse = run_q4(case, group, 0.1, window, splits, decode=False, max_q=2)
+    assert pkv.get_device_error() == pkv.DEVERR["cu_seqlens"]
+    assert torch.all(out[:5] == 0) and torch.all(torch.isneginf(lse[:5]))
+    live, ref, ref_lse = expect((q[5:], kc, vc, table[1:], lens[1:], cu[1:] - 5), group, 0.1, window)
+    assert_attn_close(out[5:], ref, "the other sequences", ATOL)
+    assert_attn_close(lse[5:], ref_lse, "the other sequences' lse", ATOL)
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs,window,splits", REFUSALS)
+@pytest.mark.parametrize("bounds", [(0, 2, 9), (-3, 2, 4)])
+def test_q4_rows_outside_the_call_are_flagged_on_every_path(hq, hkv, d, group, bs, window, splits, bounds):
+    """Offsets that leave [0, Tq]: that sequence's rows within the call are refused, the other's are not."""
+    case = list(q4_case(73, [700, 2000], hq, hkv, d, group, bs, [2, 2]))
+    q, kc, vc, table, lens, _ = case
+    case[5] = torch.tensor(bounds, dtype=torch.int32)
+    out, lse = run_q4(case, group, 0.1, window, splits, decode=False, max_q=8)
+    assert pkv.get_device_error() == pkv.DEVERR["cu_seqlens"]
+    good, bad = (0, 1) if bounds[0] == 0 else (1, 0)
+    assert torch.all(out[2 * bad:2 * bad + 2] == 0) and torch.all(torch.isneginf(lse[2 * bad:2 * bad + 2]))
+    at = slice(2 * good, 2 * good + 2)
+    live, ref, ref_lse = expect((q[at], kc, vc, table[good:good + 1], lens[good:good + 1], torch.tensor([0, 2], dtype=torch.int32)),
+                                group, 0.1, window)
+    assert_attn_close(out[at], ref, "the good sequence", ATOL)
+    assert_attn_close(lse[at], ref_lse, "the good sequence's lse", ATOL)
