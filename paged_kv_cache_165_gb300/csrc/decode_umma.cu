@@ -128,13 +128,21 @@ __global__ void __launch_bounds__(384, 1)
     // L-1; this block takes rows q0 .. q0+nqt-1 of them, slot = (row - q0) * m + head
     const int L = checked_len(p, b, BS, report);
     int c0 = b, nq = 1;
-    bool rows_ok = true;
     if (p.cu_q != nullptr) {
         c0 = __ldg(p.cu_q + b);
-        nq = __ldg(p.cu_q + b + 1) - c0;
-        if (nq < 0 || nq > L) {
+        const int c1 = __ldg(p.cu_q + b + 1);
+        nq = c1 - c0;
+        if (!query_rows_ok(p, c0, c1, L)) {   // those of its rows that the call has: out = 0, lse = -inf
             if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
-            rows_ok = false;
+            if (qt == 0 && split == 0) {
+                for (int r = max(c0, 0); r < min(c1, p.rows); ++r) {
+                    const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
+                    for (int i = threadIdx.x; i < p.m * D; i += blockDim.x) p.out[at * D + i] = 0.f;
+                    if (p.lse != nullptr)
+                        for (int i = threadIdx.x; i < p.m; i += blockDim.x) p.lse[at + i] = -INFINITY;
+                }
+            }
+            return;
         }
     }
     const int q0 = qt * p.q_per_tile;
@@ -155,11 +163,11 @@ __global__ void __launch_bounds__(384, 1)
     const int apg1 = min(cp1, (hi_tile + BS - 1) / BS);
     auto row_of = [&](int slot) { return static_cast<size_t>(c0 + q0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m; };
     if (nqt <= 0) return;
-    if (!rows_ok || cp0 >= cp1) {
+    if (cp0 >= cp1) {
         // a new token for a sequence that holds none has no position: flagged, not written
         if (p.new_slots != nullptr && split == 0 && threadIdx.x == 0 && L == 0 && __ldg(p.new_slots + b) >= 0)
             raise_error(p.err, PKV_DEVERR_SLOT);
-        if (split == 0) {   // an empty sequence or inconsistent rows: out = 0, lse = -inf
+        if (split == 0) {   // an empty sequence: out = 0, lse = -inf
             for (int idx = threadIdx.x; idx < slots * D; idx += blockDim.x) p.out[row_of(idx / D) * D + idx % D] = 0.f;
             if (p.lse != nullptr)
                 for (int sl = threadIdx.x; sl < slots; sl += blockDim.x) p.lse[row_of(sl)] = -INFINITY;

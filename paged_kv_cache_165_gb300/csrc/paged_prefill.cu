@@ -137,10 +137,13 @@ __device__ __forceinline__ PPItem pp_item(const DecodeKParams &p, int it, int gx
         w.b = z;
         const int L = checked_len(p, w.b, BS, report);
         w.c0 = __ldg(p.cu_q + w.b);
-        w.nq = __ldg(p.cu_q + w.b + 1) - w.c0;
+        const int c1 = __ldg(p.cu_q + w.b + 1);
+        w.nq = c1 - w.c0;
         w.r0 = qt * BM;                     // the tile's first query row
-        if (w.nq < 0 || w.nq > L) {
+        if (!query_rows_ok(p, w.c0, c1, L)) {
             if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
+            w.c0 = max(w.c0, 0);            // those of its rows that the call has
+            w.nq = max(min(c1, p.rows) - w.c0, 0);
             if (w.r0 == 0) w.kind = kBadRows;
             return w;
         }
@@ -639,10 +642,10 @@ __global__ void __launch_bounds__(512, 1)
             }
             if (w.kind == kBadRows) {
                 // inconsistent rows: out = 0, lse = -inf (as the other query-row kernels)
-                for (int idx = et; idx < min(max(w.nq, 0), BM) * D; idx += 128) {
-                    const size_t bi = static_cast<size_t>(w.c0 + idx / D) * p.Hq + w.head;
-                    p.out[bi * D + idx % D] = 0.f;
-                    if (idx % D == 0 && p.lse != nullptr) p.lse[bi] = -INFINITY;
+                for (int r = 0; r < w.nq; ++r) {
+                    const size_t bi = static_cast<size_t>(w.c0 + r) * p.Hq + w.head;
+                    if (et < D) p.out[bi * D + et] = 0.f;
+                    if (et == 0 && p.lse != nullptr) p.lse[bi] = -INFINITY;
                 }
                 continue;
             }

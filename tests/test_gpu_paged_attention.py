@@ -291,3 +291,38 @@ def test_rows_outside_the_call_are_flagged(hq, hkv, d, dtype, bs, window, splits
                                           torch.tensor([0, 2], dtype=torch.int32), 0.1, window)
     assert_attn_close(out[at], ref, "the good sequence")
     assert_attn_close(lse[at], ref_lse, "the good sequence's lse")
+
+
+TENSOR_CORE_REFUSALS = [  # hq, hkv, d, bs, window, splits, max_q: tcgen05 decode, then the chunked prefill
+    (16, 2, 128, 16, 0, 5, 2), (64, 1, 64, 32, 100, 0, 2), (8, 2, 128, 16, 0, 1, 2), (8, 2, 128, 16, 0, 0, 64), (4, 1, 64, 32, 0, 0, 64)]
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,window,splits,max_q", TENSOR_CORE_REFUSALS)
+def test_more_rows_than_max_q_are_flagged_on_tensor_cores(hq, hkv, d, bs, window, splits, max_q):
+    n = 2 * max_q + 30
+    q, kc, vc, table, lens, cu = make_case(75, [500, 900, 70, 33], [n, max_q, 1, 0], hq, hkv, d, bs, torch.bfloat16)
+    cu5 = torch.cat([cu, cu[-1:]])                # room for the rows: B * max_q >= Tq
+    more = [torch.cat([t, t[-1:]]) for t in (table, lens)]
+    while cu5[-1] > (cu5.numel() - 1) * max_q:
+        cu5 = torch.cat([cu5, cu5[-1:]])
+        more = [torch.cat([t, t[-1:]]) for t in more]
+    out, lse = refused(q, kc, vc, *more, cu5, max_q, window, splits)
+    assert torch.all(out[:n] == 0) and torch.all(torch.isneginf(lse[:n]))
+    ref, ref_lse = oracle.paged_attention(q[n:], kc, vc, table[1:], lens[1:], cu[1:] - n, 0.1, window)
+    assert_attn_close(out[n:], ref, "the other sequences")
+    assert_attn_close(lse[n:], ref_lse, "the other sequences' lse")
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,window,splits,max_q", TENSOR_CORE_REFUSALS)
+@pytest.mark.parametrize("below", [False, True])
+def test_rows_outside_the_call_are_flagged_on_tensor_cores(hq, hkv, d, bs, window, splits, max_q, below):
+    q, kc, vc, table, lens, _ = make_case(77, [700, 900], [max_q, max_q], hq, hkv, d, bs, torch.bfloat16)
+    cu = torch.tensor([-3 if below else 0, max_q, 2 * max_q + (0 if below else 5)], dtype=torch.int32)
+    out, lse = refused(q, kc, vc, table, lens, cu, max_q + 6, window, splits)
+    good, bad = (1, 0) if below else (0, 1)
+    refused_rows, at = (slice(i * max_q, (i + 1) * max_q) for i in (bad, good))
+    assert torch.all(out[refused_rows] == 0) and torch.all(torch.isneginf(lse[refused_rows]))
+    ref, ref_lse = oracle.paged_attention(q[at], kc, vc, table[good:good + 1], lens[good:good + 1],
+                                          torch.tensor([0, max_q], dtype=torch.int32), 0.1, window)
+    assert_attn_close(out[at], ref, "the good sequence")
+    assert_attn_close(lse[at], ref_lse, "the good sequence's lse")
