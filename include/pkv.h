@@ -472,7 +472,7 @@ pkv_status pkv_decode_step_q4(float *out, float *lse, const float *q, const void
  * (block_table[b][pos / bs] * bs + pos % bs; plumephp.com "KV Cache 优化与注意力机制加速" §4.2-§4.3).
  *   block_table       int32 [B][MBS], written at the new blocks
  *   context_lens_out  int32 [B]: L + n
- *   cu_new            int32 [B + 1]; usable as cu_q of pkv_paged_attention*
+ *   cu_new            int32 [B + 1]; usable as cu_q of a pkv_paged_attention* call on cu_new[B] rows
  *   slot_mapping      int64 [T], T >= sum n; entries from cu_new[B] on become -1 (padding)
  *   free_count_out    int32 [1]
  * A free_count outside [0, NB] sets PKV_DEVERR_POOL, counts as no free blocks and is passed on.
@@ -481,6 +481,9 @@ pkv_status pkv_decode_step_q4(float *out, float *lse, const float *q, const void
  * the same), or the tokens of it and the rows before it exceed T, sets PKV_DEVERR_POOL.  Such a
  * row stays as it was: no blocks, no slots, its length unchanged.  A listed or tabled block id
  * outside [0, NB) sets PKV_DEVERR_BLOCK and its slots are -1.
+ * slot_mapping holds the new tokens of the rows one after the other, as pkv_kv_append* take them: a
+ * row that got none (n = 0, or refused) has no place in it.  A decode step, whose slot_mapping has one
+ * entry for every sequence, takes the step_slots of pkv_block_tables_extend_step.
  *   workspace         pkv_block_tables_extend_workspace_bytes(B, T) bytes, 16-byte aligned, zeroed
  *                     once (a call that completes leaves it zero); calls that share it must not
  *                     overlap
@@ -492,6 +495,18 @@ pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_
                                    int32_t *cu_new, int64_t *slot_mapping, int32_t *free_count_out, int B, int T,
                                    int MBS, int bs, int NB, void *workspace, size_t workspace_bytes,
                                    pkv_stream_t stream);
+
+/*
+ * pkv_block_tables_extend_step -- pkv_block_tables_extend that also writes the slots of a decode step:
+ *   step_slots        int64 [B]: the slot of row b's last new position, context_lens_out[b] - 1, or -1
+ *                     where it got none (n = 0, refused, or a bad block id); the slot_mapping of
+ *                     pkv_decode_step*
+ */
+pkv_status pkv_block_tables_extend_step(int32_t *block_table, const int32_t *context_lens, const int32_t *new_tokens,
+                                        const int32_t *free_list, const int32_t *free_count, int32_t *context_lens_out,
+                                        int32_t *cu_new, int64_t *slot_mapping, int64_t *step_slots,
+                                        int32_t *free_count_out, int B, int T, int MBS, int bs, int NB, void *workspace,
+                                        size_t workspace_bytes, pkv_stream_t stream);
 
 /*
  * pkv_block_tables_release -- blocks back to the pool: the logical blocks first_block[b] ..

@@ -113,6 +113,8 @@ def lib() -> ctypes.CDLL:
     L.pkv_block_tables_extend_workspace_bytes.restype = Z
     L.pkv_block_tables_extend.argtypes = [P] * 9 + [I] * 5 + [P, Z, P]
     L.pkv_block_tables_extend.restype = I
+    L.pkv_block_tables_extend_step.argtypes = [P] * 10 + [I] * 5 + [P, Z, P]
+    L.pkv_block_tables_extend_step.restype = I
     L.pkv_block_tables_release_workspace_bytes.argtypes = [I]
     L.pkv_block_tables_release_workspace_bytes.restype = Z
     L.pkv_block_tables_release.argtypes = [P] * 6 + [I] * 3 + [P, Z, P]
@@ -200,7 +202,7 @@ def _ready(here, tensors) -> bool:
     return True
 
 
-_OPTIONAL = ("lse", "cu_q", "first_block", "workspace")
+_OPTIONAL = ("lse", "cu_q", "first_block", "step_slots", "workspace")
 
 
 def _refuse(what, here, **tensors) -> None:
@@ -722,35 +724,42 @@ def block_tables_release_workspace_bytes(B) -> int:
 
 
 def block_tables_extend(block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
-                        slot_mapping, free_count_out, bs, workspace=None, stream=None) -> None:
+                        slot_mapping, free_count_out, bs, workspace=None, stream=None, step_slots=None) -> None:
     """Blocks, table entries and slots for new_tokens[b] more tokens of every row (see pkv.h).
 
     block_table int32 [B][MBS]; context_lens, new_tokens, context_lens_out int32 [B]; free_list
     int32 [NB]; free_count, free_count_out int32 [1]; cu_new int32 [B+1]; slot_mapping int64 [T]
-    (entries past the new tokens become -1).  The *_out tensors may be their inputs."""
+    (the new tokens row after row; entries past them become -1).  step_slots: int64 [B], the
+    slot of each row's last new token, -1 where it got none (what decode_step* take; None: left out).
+    The *_out tensors may be their inputs."""
     what, here = "block_tables_extend", _current_device()
     ints = (block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new, free_count_out)
     try:
-        ok = (_ready(here, (*ints, slot_mapping, workspace)) and all([t.dtype is _I32 for t in ints]) and
-              slot_mapping.dtype is _I64)
+        ok = (_ready(here, (*ints, slot_mapping, step_slots, workspace)) and all([t.dtype is _I32 for t in ints]) and
+              slot_mapping.dtype is _I64 and (step_slots is None or step_slots.dtype is _I64))
     except AttributeError:   # not a tensor
         ok = False
     if not ok:
         _refuse(what, here, block_table=(block_table, _I32), context_lens=(context_lens, _I32), new_tokens=(new_tokens, _I32),
                 free_list=(free_list, _I32), free_count=(free_count, _I32), context_lens_out=(context_lens_out, _I32),
                 cu_new=(cu_new, _I32), free_count_out=(free_count_out, _I32), slot_mapping=(slot_mapping, _I64),
-                workspace=(workspace, None))
+                step_slots=(step_slots, _I64), workspace=(workspace, None))
     table = block_table.shape
     if len(table) != 2:
         raise ValueError("block_tables_extend: block_table must be [B][MBS]")
     B, MBS = table
     if context_lens.numel() != B or new_tokens.numel() != B or context_lens_out.numel() != B or \
-            cu_new.numel() != B + 1 or free_count.numel() != 1 or free_count_out.numel() != 1:
+            cu_new.numel() != B + 1 or free_count.numel() != 1 or free_count_out.numel() != 1 or \
+            (step_slots is not None and step_slots.numel() != B):
         raise ValueError("block_tables_extend: shapes do not match")
-    status = lib().pkv_block_tables_extend(
-        block_table.data_ptr(), context_lens.data_ptr(), new_tokens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
-        context_lens_out.data_ptr(), cu_new.data_ptr(), slot_mapping.data_ptr(), free_count_out.data_ptr(), B,
-        slot_mapping.numel(), MBS, int(bs), free_list.numel(), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    tables = (block_table.data_ptr(), context_lens.data_ptr(), new_tokens.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
+              context_lens_out.data_ptr(), cu_new.data_ptr(), slot_mapping.data_ptr())
+    sizes = (free_count_out.data_ptr(), B, slot_mapping.numel(), MBS, int(bs), free_list.numel(), _ptr(workspace),
+             _bytes(workspace), _stream(stream, here))
+    if step_slots is None:
+        status = lib().pkv_block_tables_extend(*tables, *sizes)
+    else:
+        status = lib().pkv_block_tables_extend_step(*tables, step_slots.data_ptr(), *sizes)
     if status:
         _check(status)
 

@@ -283,6 +283,7 @@ class DeviceBlocks:
         self.context_lens = torch.zeros(rows, dtype=torch.int32, device=device)
         self.cu_new = torch.zeros(rows + 1, dtype=torch.int32, device=device)
         self.slot_mapping = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+        self.step_slots = torch.full((rows,), -1, dtype=torch.int64, device=device)
         ws = max(16, _binding.block_tables_extend_workspace_bytes(rows, max_tokens),
                  _binding.block_tables_release_workspace_bytes(rows))
         # two pieces: extend's stays zero, release's may hold anything
@@ -291,13 +292,15 @@ class DeviceBlocks:
 
     def extend(self, new_tokens: torch.Tensor, num_tokens: Optional[int] = None, stream=None) -> torch.Tensor:
         """Room for new_tokens[b] (int32 [rows], on the device) more tokens of every row.  Returns
-        slot_mapping[:num_tokens] (default: all of it; -1 past the new tokens); cu_new holds
-        the rows' offsets and context_lens and block_table are up to date."""
+        slot_mapping[:num_tokens] (default: all of it): the new tokens row after row, -1 past
+        them, for kv_append*.  step_slots[b] is the slot of row b's last new token, -1 for a row
+        that got none (no new token, or refused): what decode_step* take.  cu_new holds the rows'
+        offsets, and context_lens and block_table are up to date."""
         from . import _binding
         slots = self.slot_mapping if num_tokens is None else self.slot_mapping[:num_tokens]
         _binding.block_tables_extend(self.block_table, self.context_lens, new_tokens, self.free_list, self.free_count,
                                      self.context_lens, self.cu_new, slots, self.free_count, self.block_size,
-                                     workspace=self._extend_ws, stream=stream)
+                                     step_slots=self.step_slots, workspace=self._extend_ws, stream=stream)
         return slots
 
     def release(self, end_block: torch.Tensor, first_block: Optional[torch.Tensor] = None, stream=None) -> None:

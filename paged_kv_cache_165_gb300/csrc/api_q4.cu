@@ -245,27 +245,46 @@ size_t pkv_block_tables_extend_workspace_bytes(int B, int T) {
     return extend_blocks(T, sm_count) > 1 ? 16 : 0;
 }
 
+static pkv_status extend_tables(const char *what, ExtendArgs a, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    pkv_status s = check_tables(what, a.B, a.T, a.MBS, a.bs, a.NB);
+    if (s != PKV_OK) return s;
+    if (!a.free_list || !a.free_count || !a.free_count_out || !a.cu_new ||
+        (a.B > 0 && (!a.block_table || !a.context_lens || !a.new_tokens || !a.context_lens_out)) || (a.T > 0 && !a.slot_mapping))
+        return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+    int sm_count = 0;
+    unsigned *err = nullptr;
+    s = current_device_info(&sm_count, &err);
+    if (s != PKV_OK) return s;
+    if (extend_blocks(a.T, sm_count) > 1 && (workspace == nullptr || workspace_bytes < 16 || !aligned_to(workspace, 16)))
+        return fail(PKV_ERR_WORKSPACE, "%s: needs 16 bytes of 16-byte aligned workspace, got %zu", what,
+                    workspace == nullptr ? size_t(0) : workspace_bytes);
+    a.arrivals = static_cast<unsigned *>(workspace);
+    a.err = err;
+    const cudaError_t e = launch_block_tables_extend(a, sm_count, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, what);
+}
+
 pkv_status pkv_block_tables_extend(int32_t *block_table, const int32_t *context_lens, const int32_t *new_tokens,
                                    const int32_t *free_list, const int32_t *free_count, int32_t *context_lens_out,
                                    int32_t *cu_new, int64_t *slot_mapping, int32_t *free_count_out, int B, int T,
                                    int MBS, int bs, int NB, void *workspace, size_t workspace_bytes,
                                    pkv_stream_t stream) {
-    pkv_status s = check_tables("block_tables_extend", B, T, MBS, bs, NB);
-    if (s != PKV_OK) return s;
-    if (!free_list || !free_count || !free_count_out || !cu_new ||
-        (B > 0 && (!block_table || !context_lens || !new_tokens || !context_lens_out)) || (T > 0 && !slot_mapping))
-        return fail(PKV_ERR_INVALID_ARG, "block_tables_extend: null pointer");
-    int sm_count = 0;
-    unsigned *err = nullptr;
-    s = current_device_info(&sm_count, &err);
-    if (s != PKV_OK) return s;
-    if (extend_blocks(T, sm_count) > 1 && (workspace == nullptr || workspace_bytes < 16 || !aligned_to(workspace, 16)))
-        return fail(PKV_ERR_WORKSPACE, "block_tables_extend: needs 16 bytes of 16-byte aligned workspace, got %zu",
-                    workspace == nullptr ? size_t(0) : workspace_bytes);
-    const ExtendArgs a{block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
-                       slot_mapping, free_count_out, B, T, MBS, bs, NB, static_cast<unsigned *>(workspace), err};
-    const cudaError_t e = launch_block_tables_extend(a, sm_count, stream);
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "block_tables_extend launch");
+    return extend_tables("block_tables_extend",
+                         ExtendArgs{block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
+                                    slot_mapping, nullptr, free_count_out, B, T, MBS, bs, NB, nullptr, nullptr},
+                         workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_block_tables_extend_step(int32_t *block_table, const int32_t *context_lens, const int32_t *new_tokens,
+                                        const int32_t *free_list, const int32_t *free_count, int32_t *context_lens_out,
+                                        int32_t *cu_new, int64_t *slot_mapping, int64_t *step_slots,
+                                        int32_t *free_count_out, int B, int T, int MBS, int bs, int NB, void *workspace,
+                                        size_t workspace_bytes, pkv_stream_t stream) {
+    if (B > 0 && !step_slots) return fail(PKV_ERR_INVALID_ARG, "block_tables_extend_step: null pointer");
+    return extend_tables("block_tables_extend_step",
+                         ExtendArgs{block_table, context_lens, new_tokens, free_list, free_count, context_lens_out, cu_new,
+                                    slot_mapping, step_slots, free_count_out, B, T, MBS, bs, NB, nullptr, nullptr},
+                         workspace, workspace_bytes, stream);
 }
 
 size_t pkv_block_tables_release_workspace_bytes(int B) { return B < 0 ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int32_t); }

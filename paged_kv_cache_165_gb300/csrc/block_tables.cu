@@ -124,7 +124,10 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
         if (tid == 0) s_cu[0] = s_need[0] = 0;
         __syncthreads();
         const int tokens = s_cu[kRows], blocks = s_need[kRows];
-        if (lead && row < a.B) a.cu_new[row + 1] = placed + s_cu[tid + 1];
+        if (lead && row < a.B) {
+            a.cu_new[row + 1] = placed + s_cu[tid + 1];
+            if (a.step_slots != nullptr && n == 0) a.step_slots[row] = -1;
+        }
         const int at = blockIdx.x * kRows + tid, step = gridDim.x * kRows;
         const int top = count - 1 - taken;
         for (int i = at; i < blocks; i += step) {
@@ -145,6 +148,7 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
             if (blk < 0 || blk >= a.NB) raise_error(a.err, PKV_DEVERR_BLOCK);
             else slot = static_cast<long long>(blk) * a.bs + (pos - j * a.bs);
             a.slot_mapping[placed + t] = slot;
+            if (a.step_slots != nullptr && t + 1 == s_cu[r + 1]) a.step_slots[r0 + r] = slot;   // the row's last
         }
         placed += tokens;
         taken += blocks;

@@ -184,6 +184,7 @@ struct ExtendArgs {
     const int32_t *context_lens, *new_tokens, *free_list, *free_count;
     int32_t *context_lens_out, *cu_new;
     int64_t *slot_mapping;
+    int64_t *step_slots;   // nullptr: not wanted
     int32_t *free_count_out;
     int B, T, MBS, bs, NB;
     unsigned *arrivals;    // workspace (more than one block): zero before and after

@@ -251,3 +251,100 @@ def test_serving_loop_over_a_4_bit_cache(graph):
     blocks.finish(torch.ones(rows, dtype=torch.bool, device="cuda"))
     assert int(blocks.free_count) == nb and sorted(blocks.free_list.tolist()) == list(range(nb))
     assert pkv.get_device_error() == 0
+
+
+# ------------------------------------------------------------------------ slots of a decode step
+
+@pytest.mark.parametrize("B,nhi,T,spare", [(1, 1, None, 9), (40, 3, None, 200), (40, 3, 50, 200), (40, 3, None, 12), (40, 9, None, 3),
+                                           (1500, 2, None, 900), (1500, 2, None, 40), (8, 2000, None, 1200)])
+def test_step_slots_name_every_row_by_itself(B, nhi, T, spare):
+    """Rows with none, one or many new tokens; too small a slot map (T) or pool (spare) refuses some."""
+    rng = np.random.default_rng(B + spare)
+    bs, mbs = 16, 140
+    lens, new = rng.integers(0, 100, B), rng.integers(0, nhi + 1, B)
+    table, free, count = pool(rng, lens.tolist(), bs, mbs, spare)
+    t, l, n, f = (torch.from_numpy(x.astype(np.int32)).cuda() for x in (table, lens, new, free))
+    c = torch.tensor([count], dtype=torch.int32, device="cuda")
+    T = int(new.sum()) if T is None else T
+    cu = torch.empty(B + 1, dtype=torch.int32, device="cuda")
+    slots, steps = torch.empty(T, dtype=torch.int64, device="cuda"), torch.full((B,), -9, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    pkv.block_tables_extend(t, l, n, f, c, l, cu, slots, c, bs, workspace=ws, step_slots=steps)
+    want = table.copy()
+    olens, ocu, oslots, left = orc.block_tables_extend(want, lens.tolist(), new.tolist(), free, count, bs, T)
+    refused = any(olens[b] != lens[b] + new[b] for b in range(B))
+    assert refused == (spare in (3, 40) or T == 50) and pkv.get_device_error() == (pkv.DEVERR["pool"] if refused else 0)
+    assert np.array_equal(t.cpu().numpy(), want) and np.array_equal(l.cpu().numpy(), olens) and int(c) == left
+    assert np.array_equal(cu.cpu().numpy(), ocu) and np.array_equal(slots.cpu().numpy(), oslots)
+    last = [oracle.slot_of(want[b], int(olens[b]) - 1, bs) if olens[b] > lens[b] else -1 for b in range(B)]
+    assert steps.tolist() == last
+
+
+def test_step_slots_of_bad_block_ids_are_padding():
+    table = torch.tensor([[99, -1], [2, -1]], dtype=torch.int32, device="cuda")
+    l = torch.tensor([3, 3], dtype=torch.int32, device="cuda")
+    one = torch.ones_like(l)
+    free, c = torch.tensor([0, 1, -7, -7], dtype=torch.int32, device="cuda"), torch.tensor([2], dtype=torch.int32, device="cuda")
+    slots, steps = torch.empty(2, dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int64, device="cuda")
+    pkv.block_tables_extend(table, l, one, free, c, l, torch.empty(3, dtype=torch.int32, device="cuda"), slots, c, 16,
+                            step_slots=steps)
+    assert pkv.get_device_error() == pkv.DEVERR["block"]
+    assert slots.tolist() == [-1, 35] and steps.tolist() == [-1, 35]
+
+
+@pytest.mark.parametrize("hq,bs", [(8, 16), (32, 16), (8, 24), (128, 16)])   # one launch; append and attention in two
+@pytest.mark.parametrize("graph", [False, True])
+def test_decode_loop_with_idle_and_refused_rows(hq, bs, graph):
+    """Row 2 is idle, and row 1 finds the pool empty when its block is full: the rows behind them keep
+    writing their own slots, and nobody else's."""
+    rows, hkv, d, group, mbs = 4, 2, 128, 64, 6
+    g = gen.generator(83)
+    start = [5, 3 * bs - 1, bs, 2 * bs - 6]
+    nb = sum(-(-n // bs) for n in start)
+    blocks = pkv.DeviceBlocks(nb, bs, rows, mbs, 160, order=gen.permutation(g, nb))
+    caches = [torch.zeros((nb, hkv, bs, pkv.q4_row_bytes(d, group)), dtype=torch.uint8) for _ in range(2)]
+    gk, gv = (dev(t) for t in caches)
+    prompt = [gen.randn(g, (sum(start), hkv, d), torch.bfloat16) for _ in range(2)]
+    slots = blocks.extend(torch.tensor(start, dtype=torch.int32, device="cuda"), sum(start))
+    pkv.kv_append_q4(*(dev(t) for t in prompt), gk, gv, slots, group)
+    orc.kv_append_q4(*caches, *prompt, slots.cpu(), group)
+    new = torch.tensor([1, 1, 0, 1], dtype=torch.int32, device="cuda")
+    q, kn, vn = (torch.zeros((rows, h, d), dtype=t, device="cuda") for h, t in
+                 ((hq, torch.float32), (hkv, torch.bfloat16), (hkv, torch.bfloat16)))
+    out, lse = torch.zeros_like(q), torch.zeros((rows, hq), device="cuda")
+    ws = torch.zeros(max(16, pkv.paged_attention_q4_workspace_bytes(rows, rows, 1, hq, hkv, d, group, bs, mbs)),
+                     dtype=torch.uint8, device="cuda")
+
+    def step():
+        blocks.extend(new, rows)
+        pkv.decode_step_q4(out, q, kn, vn, blocks.step_slots, gk, gv, blocks.block_table, blocks.context_lens, 0.1, group,
+                           lse=lse, workspace=ws)
+
+    held = list(start)
+    captured = None
+    for i in range(5):
+        x = [gen.randn(g, t.shape).to(t.dtype) for t in (q, kn, vn)]
+        for t, y in zip((q, kn, vn), x):
+            t.copy_(y)
+        if graph and i >= 1:
+            if captured is None:
+                captured = torch.cuda.CUDAGraph()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(captured):
+                    step()
+            captured.replay()
+        else:
+            step()
+        served = [True, held[1] < 3 * bs, False, True]
+        assert pkv.get_device_error() == (0 if served[1] else pkv.DEVERR["pool"])
+        held = [n + s for n, s in zip(held, served)]
+        assert blocks.context_lens.tolist() == held
+        table = blocks.block_table.cpu()
+        mine = torch.tensor([oracle.slot_of(table[b], held[b] - 1, bs) if served[b] else -1 for b in range(rows)])
+        assert blocks.step_slots.tolist() == mine.tolist()
+        orc.kv_append_q4(*caches, x[1], x[2], mine, group)
+        assert torch.equal(gk.cpu(), caches[0]) and torch.equal(gv.cpu(), caches[1])
+        ref, ref_lse = oracle.paged_decode(x[0], *(orc.dequantize_q4(c, d, group) for c in caches), table,
+                                           torch.tensor(held, dtype=torch.int32), 0.1)
+        assert_attn_close(out, ref, f"step {i} out", 2e-4)
+        assert_attn_close(lse, ref_lse, f"step {i} lse", 2e-4)

@@ -161,3 +161,10 @@ def test_q4_bindings_check_tensors():
         pkv.q4_row_bytes(128, 48)
     with pytest.raises(ValueError, match="permutation"):
         pkv.DeviceBlocks(4, 16, 2, 2, 4, order=[0, 1, 1, 2], device="cpu")
+
+
+def test_extend_step_rejects_bad_arguments_before_any_launch(L):
+    def extend(B=2, T=2, MBS=4, bs=16, NB=8, lens=P16, steps=P16):
+        return L.pkv_block_tables_extend_step(P16, lens, P16, P16, P16, P16, P16, P16, steps, P16, B, T, MBS, bs, NB, None, 0, None)
+    for bad in (dict(B=-1), dict(T=-1), dict(MBS=0), dict(bs=0), dict(NB=0), dict(lens=None), dict(steps=None)):
+        assert extend(**bad) == _binding.PKV_ERR_INVALID_ARG, bad
