@@ -101,9 +101,10 @@ __device__ __forceinline__ void finish_rows(uint8_t *smem, const AttendQ4Params 
             acc.z += o.z * f;
             acc.w += o.w * f;
         }
-        const float inv = M == -INFINITY ? 0.f : 1.f / L;
+        const bool empty = M == -INFINITY && L == 0.f;   // else scores of NaN, which the maximum ignores: lse NaN
+        const float inv = empty ? 0.f : 1.f / L;
         const float4 r = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        const float lse2 = M == -INFINITY ? -INFINITY : M + log2f(L);
+        const float lse2 = empty ? -INFINITY : M + log2f(L);
         if (u.n == 1) {
             *reinterpret_cast<float4 *>(p.out + static_cast<size_t>(rows[h].bi) * D + c) = r;
             if (c == 0 && p.lse != nullptr) p.lse[rows[h].bi] = lse2 * kDecLn2;
@@ -464,7 +465,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
 
         if (P.balanced) {
             if (gave_up) return;   // lanes together; the block's other warps go on
-            const bool empty = rows.ref == -INFINITY;   // no key of this part for the row
+            // no key of this part for the row; a sum of NaN has keys whose scores are NaN, which ref ignores
+            const bool empty = rows.ref == -INFINITY && rows.l == 0.f;
             const float inv = empty ? 0.f : 1.f / rows.l, lse2 = empty ? -INFINITY : rows.ref + log2f(rows.l);
             if (Rows::owner(lane)) {
                 if (part.n > 1) p.ws_lse[part_at<R>(part, Rows::row(lane), part.own)] = me.bi >= 0 ? lse2 : -INFINITY;

@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
             // ---- the slot's sums over its four threads; O_hi + O_lo, unscaled, plus the zeros' part
             l += __shfl_xor_sync(kFull, l, 1);
             l += __shfl_xor_sync(kFull, l, 2);
-            const bool empty = ref == -INFINITY;   // the slot sees no key of this segment
+            // the slot sees no key of this segment; a sum of NaN: it does, and ref ignores their scores
+            const bool empty = ref == -INFINITY && l == 0.f;
             const float inv = empty ? 0.f : 1.f / l, lse2 = empty ? -INFINITY : ref + log2f(l);
             const bool whole = g.part.n == 1;
             const size_t at = whole        ? static_cast<size_t>(me.bi)

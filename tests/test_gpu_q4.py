@@ -620,3 +620,41 @@ def test_q4_rows_outside_the_call_are_flagged_on_every_path(hq, hkv, d, group, b
                                 group, 0.1, window)
     assert_attn_close(out[at], ref, "the good sequence", ATOL)
     assert_attn_close(lse[at], ref_lse, "the good sequence's lse", ATOL)
+
+
+# ------------------------------------------------------------------------ scores of NaN
+
+def poison_tokens(cache, table_row, positions, d, group, heads=slice(None)):
+    """NaN zeros (scale 0) in the rows at these positions, as an append of NaN writes them."""
+    nb, hkv, bs, _ = cache.shape
+    for pos in positions:
+        page = cache.view(nb, hkv, -1)[int(table_row[pos // bs])]
+        at = bs * d // 2 + pos % bs * 4 * (d // group)
+        page[heads, at:at + 4 * (d // group)] = torch.tensor([0, 0, 0xff, 0x7f] * (d // group), dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(8, 1, 128, 64, 16), (4, 1, 128, 64, 16), (64, 1, 128, 64, 16), (40, 1, 64, 64, 32),
+                                               (4, 2, 96, 32, 16), (8, 1, 128, 32, 8), (3, 1, 224, 32, 16), (4, 1, 128, 128, 24)])
+@pytest.mark.parametrize("many", [False, True])   # many: equal shares of a table much longer than the sequences
+def test_q4_lse_of_scores_that_are_nan(hq, hkv, d, group, bs, many):
+    """A row's lse is NaN exactly where a key that it sees is, whatever the split, as its out is; NaN in V
+    alone leaves the lse as it is."""
+    lens = [1, 600, 70, 33, 2, 300] + ([40] * 150 if many else [])
+    case = list(q4_case(91, lens, hq, hkv, d, group, bs))
+    q, kc, vc, table, clens, cu = case
+    if many:
+        case[3] = torch.cat([table, torch.full((len(lens), 16000 // bs - table.shape[1]), -1, dtype=torch.int32)], 1)
+    live, ref, ref_lse = expect(case, group, 0.1, 0)
+    bad = {0: range(1), 1: range(256), 3: range(33), 4: range(1, 2)}
+    for b, positions in bad.items():
+        poison_tokens(kc, table[b], positions, d, group)
+    poison_tokens(vc, table[5], range(300), d, group)
+    clean = [b for b in range(len(lens)) if b not in bad and b != 5]
+    for splits in ((0,) if many else (0, 1, 3, 20)):
+        out, lse = run_q4(case, group, 0.1, 0, splits)
+        assert torch.isnan(out[list(bad)]).all() and torch.isnan(lse[list(bad)]).all()
+        assert torch.isnan(out[5]).all()
+        assert_attn_close(lse[5], ref_lse[5], "lse of clean keys", ATOL)
+        assert_attn_close(out[clean], ref[clean], "clean rows", ATOL)
+        assert_attn_close(lse[clean], ref_lse[clean], "clean rows' lse", ATOL)
+    assert pkv.get_device_error() == 0
