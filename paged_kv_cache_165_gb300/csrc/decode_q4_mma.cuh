@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
             if (threadIdx.x == 0 && p.new_slots != nullptr && sq.L == 0 && __ldg(p.new_slots + i) >= 0)
                 raise_error(p.err, PKV_DEVERR_SLOT);
         }
-        __syncthreads();   // the scan's memory becomes the ring
+        fence_proxy_async_smem();   // the copies that will land there come after these writes and reads
+        __syncthreads();            // the scan's memory becomes the ring
     }
 
     while (x < x1) {

@@ -658,3 +658,20 @@ def test_q4_lse_of_scores_that_are_nan(hq, hkv, d, group, bs, many):
         assert_attn_close(out[clean], ref[clean], "clean rows", ATOL)
         assert_attn_close(lse[clean], ref_lse[clean], "clean rows' lse", ATOL)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(2, 1, 64, 64, 16), (8, 1, 128, 64, 32), (40, 1, 64, 64, 16)])
+def test_q4_equal_shares_of_as_many_sequences_as_a_block_scans(hq, hkv, d, group, bs):
+    """1024 sequences: the scan fills its part of the shared memory that the page copies then use."""
+    g = gen.generator(67)
+    lens = torch.randint(0, 60, (1024,), generator=g).tolist()
+    case = list(q4_case(67, lens, hq, hkv, d, group, bs))
+    case[3] = torch.cat([case[3], torch.full((1024, 4096 // bs - case[3].shape[1]), -1, dtype=torch.int32)], 1)
+    live, ref, ref_lse = expect(case, group, 0.1, 0)
+    first = run_q4(case, group, 0.1)
+    assert_attn_close(first[0][live], ref, "out", ATOL)
+    assert_attn_close(first[1][live], ref_lse, "lse", ATOL)
+    for _ in range(5):
+        out, lse = run_q4(case, group, 0.1)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert pkv.get_device_error() == 0
