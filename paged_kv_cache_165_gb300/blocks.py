@@ -261,8 +261,8 @@ class DeviceBlocks:
     """Block tables, lengths and the free list of a batch kept on the GPU: the state of
     block_tables_extend and block_tables_release, for sequences that own their blocks.
 
-    ``extend`` and ``release`` only enqueue work on the current stream (no host round trip),
-    so a decode loop over them can be captured into a CUDA graph.  ``rows`` is the batch size,
+    ``extend``, ``release`` and ``finish`` only enqueue work on the given stream (default: the
+    current one; no host round trip), so a decode loop over them can be captured into a CUDA graph.  ``rows`` is the batch size,
     ``max_blocks`` the blocks a row may hold, ``max_tokens`` the most tokens one ``extend``
     places; ``order`` is the order in which blocks are handed out (default 0..NB-1).
     """
@@ -310,9 +310,12 @@ class DeviceBlocks:
         _binding.block_tables_release(self.block_table, first_block, end_block, self.free_list, self.free_count,
                                       self.free_count, workspace=self._release_ws, stream=stream)
 
-    def finish(self, done: torch.Tensor) -> None:
+    def finish(self, done: torch.Tensor, stream=None) -> None:
         """Give back every block of the rows where ``done`` (bool [rows], on the device) holds and
-        set their lengths to 0 (on the current stream)."""
-        end = torch.where(done, self.block_table.shape[1], 0).to(torch.int32)
-        self.release(end)
-        self.context_lens.masked_fill_(done, 0)
+        set their lengths to 0."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):   # None: the current one
+            end = torch.where(done, self.block_table.shape[1], 0).to(torch.int32)
+            self.release(end)
+            self.context_lens.masked_fill_(done, 0)

@@ -348,3 +348,24 @@ def test_decode_loop_with_idle_and_refused_rows(hq, bs, graph):
                                            torch.tensor(held, dtype=torch.int32), 0.1)
         assert_attn_close(out, ref, f"step {i} out", 2e-4)
         assert_attn_close(lse, ref_lse, f"step {i} lse", 2e-4)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_loop_on_a_stream_of_its_own(raw):
+    """extend and finish enqueued behind other work of a side stream, given as a Stream or as its handle."""
+    blocks = pkv.DeviceBlocks(40, 16, 3, 20, 300)
+    new = torch.tensor([100, 3, 60], dtype=torch.int32, device="cuda")
+    done = torch.tensor([True, False, True], device="cuda")
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)         # a few milliseconds
+    blocks.extend(new, 163, stream=stream)
+    blocks.finish(done, stream=stream)
+    blocks.extend(new, 163, stream=stream)
+    side.synchronize()
+    assert pkv.get_device_error() == 0
+    assert blocks.context_lens.tolist() == [100, 6, 60] and int(blocks.free_count) == 40 - 7 - 1 - 4
+    held = [x for row in blocks.block_table.tolist() for x in row if x >= 0]
+    assert sorted(held + blocks.free_list[:28].tolist()) == list(range(40))
