@@ -297,6 +297,8 @@ class DeviceBlocks:
         that got none (no new token, or refused): what decode_step* take.  cu_new holds the rows'
         offsets, and context_lens and block_table are up to date."""
         from . import _binding
+        if num_tokens is not None and not 0 <= num_tokens <= self.slot_mapping.numel():
+            raise ValueError(f"num_tokens={num_tokens}: the slot map holds {self.slot_mapping.numel()} (max_tokens)")
         slots = self.slot_mapping if num_tokens is None else self.slot_mapping[:num_tokens]
         _binding.block_tables_extend(self.block_table, self.context_lens, new_tokens, self.free_list, self.free_count,
                                      self.context_lens, self.cu_new, slots, self.free_count, self.block_size,

@@ -168,3 +168,12 @@ def test_extend_step_rejects_bad_arguments_before_any_launch(L):
         return L.pkv_block_tables_extend_step(P16, lens, P16, P16, P16, P16, P16, P16, steps, P16, B, T, MBS, bs, NB, None, 0, None)
     for bad in (dict(B=-1), dict(T=-1), dict(MBS=0), dict(bs=0), dict(NB=0), dict(lens=None), dict(steps=None)):
         assert extend(**bad) == _binding.PKV_ERR_INVALID_ARG, bad
+
+
+def test_device_blocks_refuse_more_tokens_than_their_slot_map_holds(L):
+    blocks = pkv.DeviceBlocks(4, 16, 2, 2, 4, device="cpu")
+    for n in (5, -1):
+        with pytest.raises(ValueError, match="max_tokens"):
+            blocks.extend(torch.ones(2, dtype=torch.int32), n)
+    with pytest.raises(ValueError, match="CUDA"):
+        blocks.extend(torch.ones(2, dtype=torch.int32), 4)
