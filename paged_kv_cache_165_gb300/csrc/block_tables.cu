@@ -28,6 +28,9 @@ namespace {
 constexpr int kRows = 1024;   // rows per scan, and threads per block
 constexpr unsigned kFull = 0xffffffffu;
 
+// Rows, tokens and blocks number up to 2^31 - 1; loops over them count in unsigned, whose next step
+// (at most a grid of threads further) does not wrap.
+
 // Inclusive sums of N numbers over the block's threads; totals[i] are the block's sums.
 template <int N>
 __device__ __forceinline__ void block_scan(unsigned long long (&x)[N], unsigned long long (&warp_sums)[N][32],
@@ -90,10 +93,11 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
     // tokens asked for, tokens placed, blocks asked for and blocks handed out by earlier scans
     unsigned long long asked = 0, wanted = 0;
     int placed = 0, taken = 0;
-    for (int r0 = 0; r0 < a.B; r0 += kRows) {
-        const int row = r0 + tid;
+    const unsigned B = a.B;
+    for (unsigned r0 = 0; r0 < B; r0 += kRows) {
+        const unsigned row = r0 + tid;
         int L = 0, n = 0;
-        if (row < a.B) {
+        if (row < B) {
             L = a.context_lens[row];
             n = __ldg(a.new_tokens + row);
             if (L < 0 || n < 0 || static_cast<long long>(L) + n > capacity) {
@@ -123,15 +127,15 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
         s_len[tid] = L;
         if (tid == 0) s_cu[0] = s_need[0] = 0;
         __syncthreads();
-        const int tokens = s_cu[kRows], blocks = s_need[kRows];
-        if (lead && row < a.B) {
+        const unsigned tokens = s_cu[kRows], blocks = s_need[kRows];
+        if (lead && row < B) {
             a.cu_new[row + 1] = placed + s_cu[tid + 1];
             if (a.step_slots != nullptr && n == 0) a.step_slots[row] = -1;
         }
-        const int at = blockIdx.x * kRows + tid, step = gridDim.x * kRows;
+        const unsigned at = blockIdx.x * kRows + tid, step = gridDim.x * kRows;
         const int top = count - 1 - taken;
-        for (int i = at; i < blocks; i += step) {
-            const int r = row_of(s_need, i), j = (s_len[r] + a.bs - 1) / a.bs + i - s_need[r];
+        for (unsigned k = at; k < blocks; k += step) {
+            const int i = k, r = row_of(s_need, i), j = (s_len[r] + a.bs - 1) / a.bs + i - s_need[r];
             int blk = __ldg(a.free_list + top - i);
             if (blk < 0 || blk >= a.NB) {
                 raise_error(a.err, PKV_DEVERR_BLOCK);
@@ -139,8 +143,8 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
             }
             a.block_table[static_cast<size_t>(r0 + r) * a.MBS + j] = blk;
         }
-        for (int t = at; t < tokens; t += step) {
-            const int r = row_of(s_cu, t), pos = s_len[r] + t - s_cu[r], j = pos / a.bs;
+        for (unsigned k = at; k < tokens; k += step) {
+            const int t = k, r = row_of(s_cu, t), pos = s_len[r] + t - s_cu[r], j = pos / a.bs;
             const int owned = (s_len[r] + a.bs - 1) / a.bs;
             const int blk = j < owned ? a.block_table[static_cast<size_t>(r0 + r) * a.MBS + j]
                                       : __ldg(a.free_list + top - (s_need[r] + j - owned));
@@ -150,8 +154,8 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
             a.slot_mapping[placed + t] = slot;
             if (a.step_slots != nullptr && t + 1 == s_cu[r + 1]) a.step_slots[r0 + r] = slot;   // the row's last
         }
-        placed += tokens;
-        taken += blocks;
+        placed += static_cast<int>(tokens);
+        taken += static_cast<int>(blocks);
         __syncthreads();   // the scan's arrays are read before the next one writes them
     }
     for (long long t = placed + static_cast<long long>(blockIdx.x) * kRows + tid; t < a.T;
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
     } else {
         __syncthreads();
     }
-    for (int row = tid; row < a.B; row += kRows)
+    for (unsigned row = tid; row < B; row += kRows)
         a.context_lens_out[row] = a.context_lens[row] + (__ldcg(a.cu_new + row + 1) - __ldcg(a.cu_new + row));
     if (tid == 0) a.free_count_out[0] = given - taken;
 }
@@ -236,9 +240,10 @@ __global__ void __launch_bounds__(kRows) block_tables_release_kernel(const Relea
     }
     // every row's count first: the first row's first block goes on top of the list
     unsigned long long all = 0;
-    for (int r0 = 0; r0 < a.B; r0 += kRows) {
-        const int row = r0 + tid;
-        const int n = row < a.B ? (ONE ? s_count[row] : a.counts[row]) : 0;
+    const unsigned B = a.B;
+    for (unsigned r0 = 0; r0 < B; r0 += kRows) {
+        const unsigned row = r0 + tid;
+        const int n = row < B ? (ONE ? s_count[row] : a.counts[row]) : 0;
         unsigned long long end[1] = {static_cast<unsigned>(n)}, total[1];
         block_scan(end, warp_sums, total);
         if (ONE) s_off[tid] = static_cast<int>(end[0]) - n;
@@ -258,14 +263,14 @@ __global__ void __launch_bounds__(kRows) block_tables_release_kernel(const Relea
         for (int row = warp; row < a.B; row += 32) give_back_row(a, row, top - s_off[row], lane);
     } else {
         int before = 0;
-        for (int r0 = 0; r0 < a.B; r0 += kRows) {
-            const int row = r0 + tid;
-            const int n = row < a.B ? a.counts[row] : 0;
+        for (unsigned r0 = 0; r0 < B; r0 += kRows) {
+            const unsigned row = r0 + tid;
+            const int n = row < B ? a.counts[row] : 0;
             unsigned long long end[1] = {static_cast<unsigned>(n)}, total[1];
             block_scan(end, warp_sums, total);
             s_off[tid] = before + static_cast<int>(end[0]) - n;
             __syncthreads();
-            for (int r = r0 + blockIdx.x * 32 + warp; r < min(a.B, r0 + kRows); r += gridDim.x * 32)
+            for (unsigned r = r0 + blockIdx.x * 32 + warp; r < min(B, r0 + kRows); r += gridDim.x * 32)
                 give_back_row(a, r, top - s_off[r - r0], lane);
             before += static_cast<int>(total[0]);
             __syncthreads();
@@ -277,7 +282,8 @@ __global__ void __launch_bounds__(kRows) block_tables_release_kernel(const Relea
 __global__ void __launch_bounds__(256) block_tables_count_kernel(const ReleaseArgs a) {
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x == 0) a.counts[a.B] = __ldg(a.free_count);
-    for (int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < a.B; row += (gridDim.x * blockDim.x) >> 5) {
+    for (unsigned row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < static_cast<unsigned>(a.B);
+         row += (gridDim.x * blockDim.x) >> 5) {
         const int n = count_row(a, row, lane);
         if (lane == 0) a.counts[row] = n;
     }

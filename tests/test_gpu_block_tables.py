@@ -369,3 +369,27 @@ def test_a_loop_on_a_stream_of_its_own(raw):
     assert blocks.context_lens.tolist() == [100, 6, 60] and int(blocks.free_count) == 40 - 7 - 1 - 4
     held = [x for row in blocks.block_table.tolist() for x in row if x >= 0]
     assert sorted(held + blocks.free_list[:28].tolist()) == list(range(40))
+
+
+def test_extend_of_as_many_tokens_as_fit_32_bits():
+    """2^31 - 1 tokens of two rows (a slot map of 17 GB): the last token's number plus a grid of threads passes 2^31."""
+    bs, mbs, nb = 1 << 16, 1 << 14, 40000
+    T = (1 << 31) - 1
+    table = torch.full((2, mbs), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    new = torch.tensor([1 << 30, (1 << 30) - 1], dtype=torch.int32, device="cuda")
+    free = torch.randperm(nb, dtype=torch.int32, device="cuda")
+    count = torch.tensor([nb], dtype=torch.int32, device="cuda")
+    cu, steps = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int64, device="cuda")
+    slots = torch.full((T,), -9, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    pkv.block_tables_extend(table, lens, new, free, count, lens, cu, slots, count, bs, workspace=ws, step_slots=steps)
+    assert pkv.get_device_error() == 0
+    assert lens.tolist() == new.tolist() and cu.tolist() == [0, 1 << 30, T] and int(count) == nb - 2 * mbs
+    assert torch.equal(table.flatten(), free.flip(0)[:2 * mbs])
+    pos = torch.arange(bs, device="cuda")
+    for lo in range(0, 2 * mbs, 1024):                        # block by block, in the rows' order
+        want = (table.flatten()[lo:lo + 1024, None].long() * bs + pos).flatten()
+        got = slots[lo * bs:(lo + 1024) * bs]
+        assert torch.equal(got, want[:got.numel()])
+    assert steps.tolist() == [int(slots[(1 << 30) - 1]), int(slots[-1])]
