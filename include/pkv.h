@@ -389,7 +389,8 @@ int pkv_decode_step_fp8_kernel_launches(int B, int Hq, int Hkv, int d, int bs, i
  * groups of 32, 64 or 128 elements, d a multiple of group and at most 256.  The bs * row bytes of
  * one (block, KV head) page hold the codes [bs][d / 2] (byte j: element 2j in the low nibble,
  * 2j + 1 in the high one), then the parameters [bs][G][2] in fp16: (scale, zero).  The cached
- * value is zero + scale * code.  Blocks move with pkv_kv_block_copy (dt = PKV_FP8_E4M3, d = row).
+ * value is zero + scale * code.  A cache that was not written by pkv_kv_append_q4 may hold any finite
+ * scale, of either sign, and any zero.  Blocks move with pkv_kv_block_copy (dt = PKV_FP8_E4M3, d = row).
  * The caches must be 4-byte aligned; 16-byte alignment (any allocation) runs the fast kernels.
  */
 /* Bytes of one row (a token's K or V of one KV head), or -1 for sizes that are not supported. */

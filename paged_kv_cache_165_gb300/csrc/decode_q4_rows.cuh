@@ -59,7 +59,7 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
 }
 
 // The parameters of the stage's key `lane`, widened to fp32 and handed to put(group, scale, zero +
-// centred * scale); 0 for a key that is not seen.  Returns the largest scale.
+// centred * scale); 0 for a key that is not seen.  Returns the largest |scale|.
 template <int BS, int G, typename Put>
 __device__ __forceinline__ float widen(const uint8_t *params, int page_bytes, float centred, bool seen, int lane, Put put) {
     uint32_t v[G];
@@ -70,12 +70,12 @@ __device__ __forceinline__ float widen(const uint8_t *params, int page_bytes, fl
         const uint32_t raw = seen ? v[gi] : 0u;
         const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&raw));
         put(gi, y.x, fmaf(centred, y.x, y.y));
-        top = fmaxf(top, y.x);
+        top = fmaxf(top, fabsf(y.x));
     }
     return top;
 }
 
-// The largest V scale seen so far and its exponent rounded up; `top`: a lane's of this stage.
+// The largest V scale (by magnitude) seen so far and its exponent rounded up; `top`: a lane's of this stage.
 struct ScaleTop {
     float most = 0.f, exponent = -24.f;
     __device__ __forceinline__ void take(float top) {

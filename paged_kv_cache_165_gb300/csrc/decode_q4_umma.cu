@@ -56,7 +56,7 @@ struct Cfg {
     static constexpr int NS = kRest >= 4 * kPackedBytes ? 4 : 3;   // packed tiles
     static constexpr int kOffK = 0, kOffV = kOffK + NT * kTileBytes, kOffS = kOffV + NT * kTileBytes;
     static constexpr int kOffPar = kOffS + NS * kPackedBytes;
-    static constexpr int kOffMax = kOffPar + NT * kParFloats * 4;   // V's largest scale [tile][converter warp]
+    static constexpr int kOffMax = kOffPar + NT * kParFloats * 4;   // V's largest |scale| [tile][converter warp]
     static constexpr int kOffBar = kOffMax + NT * 4 * 4;
     static constexpr int kSFull = 0, kSFree = NS, kKFull = 2 * NS, kKFree = kKFull + NT, kVFull = kKFree + NT,
                          kVFree = kVFull + NT, kQ = kVFree + NT, kScore = kQ + 1, kP = kScore + 2, kO = kP + 1,
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(448, 1) attend_q4_umma_kernel(const __grid_con
                         float *dst = par + sl * C::kParFloats + (2 * side * G + gi) * C::kParRow + at;
                         dst[0] = y.x;
                         dst[G * C::kParRow] = side == 1 ? fmaf(8.f, y.x, y.y) : y.y;   // V's codes are centred
-                        if (side == 1) top = fmaxf(top, y.x);
+                        if (side == 1) top = fmaxf(top, fabsf(y.x));
                     }
                 }
                 top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));   // non-negative floats order like their bits

@@ -675,3 +675,29 @@ def test_q4_equal_shares_of_as_many_sequences_as_a_block_scans(hq, hkv, d, group
         out, lse = run_q4(case, group, 0.1)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(8, 1, 128, 64, 16), (4, 1, 128, 32, 16), (1, 1, 64, 32, 8), (64, 1, 128, 64, 16),
+                                               (64, 1, 128, 128, 32), (5, 1, 224, 32, 16), (4, 1, 256, 64, 16)])
+@pytest.mark.parametrize("sign", [-1, 0])   # all scales negative, or of either sign
+def test_q4_caches_with_negative_scales(hq, hkv, d, group, bs, sign):
+    """A cache from elsewhere: zero + scale * code with scales below 0, the same values ~ N(0, 1)."""
+    case = list(q4_case(37, [300, 1, 64, 77], hq, hkv, d, group, bs, poison=False))
+    g = gen.generator(38)
+    for i in (1, 2):
+        cache = case[i]
+        nb = cache.shape[0]
+        page = cache.view(nb, hkv, -1)
+        par = page[:, :, bs * d // 2:].clone().view(torch.float16).view(nb, hkv, bs, d // group, 2)
+        codes = page[:, :, :bs * d // 2].view(nb, hkv, bs, d // group, group // 2)
+        flip = torch.ones(par.shape[:-1], dtype=torch.bool) if sign else torch.rand(par.shape[:-1], generator=g) < 0.5
+        s, z = par[..., 0].float(), par[..., 1].float()
+        par[..., 1] = torch.where(flip, z + 15 * s, z).half()          # code c becomes 15 - c
+        par[..., 0] = torch.where(flip, -s, s).half()
+        codes.copy_(torch.where(flip[..., None], 255 - codes, codes))
+        page[:, :, bs * d // 2:] = par.reshape(nb, hkv, -1).view(torch.uint8)
+    live, ref, ref_lse = expect(case, group, 1 / math.sqrt(d), 0)
+    for splits in (0, 1, 3):
+        out, lse = run_q4(case, group, 1 / math.sqrt(d), 0, splits)
+        assert_attn_close(out[live], ref, f"splits {splits} out", ATOL)
+        assert_attn_close(lse[live], ref_lse, f"splits {splits} lse", ATOL)
