@@ -701,3 +701,98 @@ def test_q4_caches_with_negative_scales(hq, hkv, d, group, bs, sign):
         out, lse = run_q4(case, group, 1 / math.sqrt(d), 0, splits)
         assert_attn_close(out[live], ref, f"splits {splits} out", ATOL)
         assert_attn_close(lse[live], ref_lse, f"splits {splits} lse", ATOL)
+
+
+# ------------------------------------------------------------------------ values far from 1 and mixed
+
+def scaled_case(kind, lens, hq, hkv, d, group, bs):
+    """q4_case's inputs with K and V scaled by `kind`, and a scale that keeps the scores ~ N(0, 1)."""
+    g = gen.generator(97)
+    per_seq = [gen.blocks_needed(n, bs) for n in lens]
+    nb = sum(per_seq) + 2
+    table = gen.block_table_from_order(gen.permutation(g, nb), per_seq)
+    k, v = gen.randn(g, (nb, hkv, bs, d)) + 0.5, gen.randn(g, (nb, hkv, bs, d))
+    q = gen.randn(g, (len(lens), hq, d))
+    fk, fv = torch.ones((nb, 1, bs, d)), torch.ones((nb, 1, bs, d))
+    if kind in ("tiny", "huge"):
+        fk *= 1e-5 if kind == "tiny" else 1e4
+        fv *= 1e-5 if kind == "tiny" else 1e4
+    elif kind == "one group":
+        fk[..., :group] = fv[..., :group] = 1e4
+    else:                                            # V grows, or falls, by 2^10 three fifths into every sequence
+        for b, n in enumerate(lens):
+            for pos in range(3 * n // 5, n):
+                fv[int(table[b, pos // bs]), :, pos % bs] = 2.0 ** (10 if kind == "growing" else -10)
+    scale = {"tiny": 1e5, "huge": 1e-4, "one group": 1e-4}.get(kind, 1.0) / math.sqrt(d)
+    cu = torch.arange(len(lens) + 1, dtype=torch.int32)
+    return (q, q4_cache(k * fk, group), q4_cache(v * fv, group), table, torch.tensor(lens, dtype=torch.int32), cu), scale
+
+
+def bounds(case, group, scale, ref_lse):
+    """Error bounds of out, by row, head and group, and of lse, by row and head.
+
+    A score is off by ds = (d / 8 + 20) * 2^-24 * scale * sum |q| (|zero| + 15 |scale_t|) at most, of the key
+    where that is largest (as ATOL above).  That moves lse by ds and out by 2 ds times the largest |value| A of
+    its group; sums, exponentials and divisions in fp32 by 8e-6 of A (ATOL_MEAN's account).  A weight times
+    scale, in two f16 parts, is kept to 2^-22 of it and to no less than half of f16's least step, 2^-25, in units
+    where 1 stands for a weight of at least 2^-7 / (2 max scale) (the tcgen05 kernel's reference; 2^-14 on warp
+    MMAs): with centred codes of at most 8, n keys and sum p = exp(lse - max score) that is
+    n / sum p * 8 * 2^-25 * 2^-7 * 2 max scale = n / sum p * 2^-28 max scale."""
+    q, kc, vc, table, lens, _ = case
+    B, hq, d = q.shape
+    nb, hkv, bs, _ = kc.shape
+    m, G = hq // hkv, d // group
+    kd, vd = orc.dequantize_q4(kc, d, group), orc.dequantize_q4(vc, d, group)
+    par = [c.view(nb, hkv, -1)[:, :, bs * d // 2:].contiguous().view(torch.float16).view(nb, hkv, bs, G, 2).double().numpy()
+           for c in (kc, vc)]
+    out, lse = np.zeros((B, hq, d)), np.zeros((B, hq))
+    for b in range(B):
+        L = int(lens[b])
+        at = [(int(table[b, p // bs]), p % bs) for p in range(L)]
+        blk, off = np.array([x[0] for x in at]), np.array([x[1] for x in at])
+        for h in range(hq):
+            j, x = h // m, q[b, h].double().numpy()
+            K, V = kd[blk, j, off], vd[blk, j, off]
+            reach = (np.abs(par[0][blk, j, off][..., 1]) + 15 * np.abs(par[0][blk, j, off][..., 0])).repeat(group, -1)
+            ds = (d / 8 + 20) * 2.0 ** -24 * scale * (reach * np.abs(x)).sum(-1).max()
+            n_by_p = L / math.exp(ref_lse[b, h] - (K @ x * scale).max())
+            A = np.abs(V).reshape(L, G, group).max((0, 2)).repeat(group)
+            out[b, h] = (2 * ds + 8e-6) * A + n_by_p * 2.0 ** -28 * np.abs(par[1][blk, j, off][..., 0]).max()
+            lse[b, h] = ds + 4e-6
+    return out, lse
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(8, 1, 128, 64, 16), (4, 1, 128, 32, 16), (1, 1, 64, 32, 8), (64, 1, 128, 64, 16),
+                                               (64, 1, 128, 128, 32), (5, 1, 224, 32, 16), (4, 2, 256, 64, 16), (16, 2, 128, 64, 24)])
+@pytest.mark.parametrize("kind", ["tiny", "huge", "growing", "falling", "one group"])
+def test_q4_values_far_from_1_and_mixed(hq, hkv, d, group, bs, kind):
+    """Every group as exact as its own values allow, beside groups and keys of other sizes."""
+    case, scale = scaled_case(kind, [700, 1, 90, 2000], hq, hkv, d, group, bs)
+    live, ref, ref_lse = expect(case, group, scale, 0)
+    tol, lse_tol = bounds(case, group, scale, ref_lse)
+    for splits in (0, 1, 3):
+        out, lse = run_q4(case, group, scale, 0, splits)
+        worst = np.abs(out.double().cpu().numpy() - ref) / tol
+        assert worst.max() <= 1, f"splits {splits}: {worst.max():.2f} of the bound"
+        worst = np.abs(lse.double().cpu().numpy() - ref_lse) / lse_tol
+        assert worst.max() <= 1, f"splits {splits} lse: {worst.max():.2f} of the bound"
+
+
+@pytest.mark.parametrize("hq,hkv,d,group,bs", [(8, 1, 128, 64, 16), (4, 1, 128, 32, 16), (1, 1, 64, 32, 8), (64, 1, 128, 64, 16),
+                                               (64, 1, 64, 64, 32), (5, 1, 224, 32, 16), (4, 2, 256, 64, 16), (3, 1, 96, 32, 16)])
+def test_q4_scores_keep_their_bits(hq, hkv, d, group, bs):
+    """Queries with one element each: a score is one product, whatever the kernel adds up besides zeros.  Of
+    scale * |q| (|zero| + 15 scale_t) it may lose 2^-22 to the two parts of q, 2^-23 to each of three cut-off
+    sums of a tensor core, and 2^-24 to each of six roundings (scale, zero, their sums, the base-2 factor): 16 * 2^-24."""
+    case = list(q4_case(59, [700, 3, 90, 1100], hq, hkv, d, group, bs))
+    q, kc, vc, table, lens, cu = case
+    at = torch.arange(hq * 4).view(4, hq) * 37 % d
+    x = torch.where(torch.arange(d) == at[..., None], torch.linspace(-3.7, 4.1, hq * 4).view(4, hq, 1), 0.0)
+    case[0] = x
+    live, ref, ref_lse = expect(case, group, 1.0, 0)
+    kd, vd = (np.nan_to_num(orc.dequantize_q4(c, d, group)) for c in (kc, vc))
+    ds = 16 * 2.0 ** -24 * x.abs().amax(-1).double().numpy() * 2 * np.abs(kd).max()     # |zero| + 15 scale_t: twice the largest
+    for splits in (0, 1, 3):
+        out, lse = run_q4(case, group, 1.0, 0, splits)
+        assert np.all(np.abs(lse.double().cpu().numpy() - ref_lse) <= ds + 4e-6)
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= (2 * ds[..., None] + 8e-6) * np.abs(vd).max())
