@@ -283,10 +283,12 @@ def prepare(case, seed):
         if own:
             import paged_kv_cache_165_gb300 as pkv
             ws = max(pkv.block_tables_extend_workspace_bytes(B, s["T"]), pkv.block_tables_release_workspace_bytes(B))
-            s.update(lens_out=torch.empty_like(s["lens"]), cu=torch.empty(B + 1, dtype=torch.int32, device="cuda"),
+            both = torch.stack([s["lens"], s["lens"]])   # the lengths before and after, next to each other
+            blocks = torch.empty_like(both)
+            s.update(both=both, lens=both[0], lens_out=both[1], blocks=blocks, first=blocks[0], end=blocks[1],
+                     cu=torch.empty(B + 1, dtype=torch.int32, device="cuda"),
                      slots=torch.empty(s["T"], dtype=torch.int64, device="cuda"), count1=torch.empty_like(s["free_count"]),
-                     count2=torch.empty_like(s["free_count"]), first=dev(have.astype(np.int32)), end=dev(want.astype(np.int32)),
-                     ws=torch.zeros(max(16, ws), dtype=torch.uint8, device="cuda"))
+                     count2=torch.empty_like(s["free_count"]), ws=torch.zeros(max(16, ws), dtype=torch.uint8, device="cuda"))
         return s
     d, group, hkv = case["d"], case["group"], case["hkv"]
     if case["kind"] in ("append", "gather"):
@@ -373,6 +375,8 @@ def _run_own(s):
                                 s["cu"], s["slots"], s["count1"], c["bs"], workspace=s["ws"])
         got = dict(lens=s["lens_out"], cu=s["cu"], slots=s["slots"], count=s["count1"])
         if kind == "cycle":
+            # the blocks that the tokens took: ceil(length / bs) before and after, of lengths that the GPU holds
+            torch.add(s["both"], c["bs"] - 1, out=s["blocks"]).floor_divide_(c["bs"])
             pkv.block_tables_release(s["table"], s["first"], s["end"], s["free_list"], s["count1"], s["count2"],
                                      workspace=s["ws"])
             got["count_back"] = s["count2"]
