@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kRows) block_tables_extend_kernel(const Extend
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
     const long long capacity = static_cast<long long>(a.MBS) * a.bs;
-    const int given = __ldg(a.free_count);
+    const int given = *a.free_count;   // plain loads of what the call may write at its end (*_out)
     int count = given;
     if (count < 0 || count > a.NB) {
         if (lead && tid == 0) raise_error(a.err, PKV_DEVERR_POOL);
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kRows) block_tables_release_kernel(const Relea
     __shared__ int s_off[kRows];
     __shared__ int s_count[ONE ? kRows : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int count = ONE ? __ldg(a.free_count) : a.counts[a.B];
+    const int count = ONE ? *a.free_count : a.counts[a.B];
     if (ONE) {
         for (int row = warp; row < a.B; row += 32) {
             const int n = count_row(a, row, lane);
