@@ -305,8 +305,8 @@ int pkv_decode_step_shared_prefix_kernel_launches(int B, int Hq, int Hkv, int d,
  *   caches, block_table, context_lens, scale, num_splits: as pkv_paged_decode_attention
  *   workspace    pkv_paged_attention_workspace_bytes(...) bytes, zeroed once, same
  *                rules as pkv_paged_decode_attention.
- * One query per sequence runs the decode kernels (tensor cores where they apply);
- * several run a CUDA-core kernel, one warp per (query row, head, chunk).  An
+ * One query per sequence runs the decode kernels; several run on tensor cores for bf16
+ * caches of the decode's shapes, else on a CUDA-core kernel.  An
  * inconsistent cu_q, or a row count above max_q or its sequence length, sets
  * PKV_DEVERR_CU_SEQLENS and those rows get out = 0, lse = -inf.  Requires
  * Tq <= B * max_q and Tq * Hq < 2^31.
@@ -425,7 +425,9 @@ pkv_status pkv_kv_gather_q4(void *k_out, void *v_out, pkv_dtype out_dt, const ui
  * pkv_paged_attention_q4 -- pkv_paged_attention over a 4-bit cache: the attention of the values
  * zero + scale * code, as if they had been stored in a wider type.  Query rows cu_q (NULL with
  * Tq == B and max_q == 1: one per sequence), windows, splits, lse, empty sequences and errors as
- * there; a block id out of range is read as zeros.
+ * there; a block id out of range is read as zeros.  With num_splits = 0 the work is split by what the
+ * tables can hold (MBS * bs, or the window), not by the lengths, which are on the device: a table much
+ * wider than the sequences costs time (four sequences of 8192 tokens with a table for 131072: 4.5 times).
  *   workspace    pkv_paged_attention_q4_workspace_bytes(...) bytes, 16-byte aligned, zeroed once;
  *                the rules of pkv_paged_decode_attention
  */

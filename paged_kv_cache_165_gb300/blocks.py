@@ -262,9 +262,11 @@ class DeviceBlocks:
     block_tables_extend and block_tables_release, for sequences that own their blocks.
 
     ``extend``, ``release`` and ``finish`` only enqueue work on the given stream (default: the
-    current one; no host round trip), so a decode loop over them can be captured into a CUDA graph.  ``rows`` is the batch size,
-    ``max_blocks`` the blocks a row may hold, ``max_tokens`` the most tokens one ``extend``
-    places; ``order`` is the order in which blocks are handed out (default 0..NB-1).
+    current one; no host round trip), so a decode loop over them can be captured into a CUDA
+    graph.  ``rows`` is the batch size, ``max_blocks`` the blocks a row may hold (no more than
+    the contexts need: the attention's plan goes by the table's width), ``max_tokens`` the most
+    tokens one ``extend`` places; ``order`` is the order in which blocks are handed out (default
+    0..NB-1).
     """
 
     def __init__(self, num_blocks: int, block_size: int, rows: int, max_blocks: int, max_tokens: int,

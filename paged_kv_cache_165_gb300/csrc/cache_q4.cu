@@ -7,9 +7,10 @@
 //
 // Append: a thread owns sixteen consecutive elements (two 32-bit words of codes), so a group is 2, 4
 // or 8 neighbouring lanes whatever the head size: groups never straddle a warp because its 512
-// elements are a multiple of each group size.  The arithmetic bounds it (about 17 instructions an
-// element: extremes, an exactly rounded quotient, the pack), so the scale's and the address's share
-// of it counts: with eight elements a thread 17153 tokens of 8 heads x 128 (bf16) took 35.9 us, with
+// elements are a multiple of each group size.  Bound by its instructions (about 17 an element: extremes,
+// an exactly rounded quotient, the pack; 15 us of them for the case below) and by its loads, which a
+// thread waits for before its arithmetic with none of the next turn in flight (issue 64%, most stalls
+// on loads).  The scale's and the address's share counts: with eight elements a thread 17153 tokens of 8 heads x 128 (bf16) took 35.9 us, with
 // sixteen 25.9 (3.5 TB/s; 13.3 at the copy rate), with 32 (two blocks per SM) 29.  Both rows are loaded
 // before either's arithmetic, which costs a few spilled registers at four blocks per SM (three: 26.9).
 // Gather: a thread owns eight; its stores bound it (32768 tokens, 34 us, 5.0 TB/s).

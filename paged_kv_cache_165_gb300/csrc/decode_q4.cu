@@ -23,11 +23,6 @@ namespace {
 // Query heads that a warp takes together, so that they share the codes' way into fp32.
 int simt_heads(int m) { return m <= 2 ? m : 4; }
 
-// One warp per (query row, H query heads of a KV head, chunk).  W lanes (a power of two, W * 8 >= d)
-// hold one key's row, eight elements each, so 32 / W keys are taken at a time, U such steps (16 keys at most)
-// between two updates of the softmax; every such slice of the warp keeps its own online softmax and
-// they merge at the end.  Bound by its arithmetic, shuffles most of all (64 x 2048 tokens, 32 heads on 8 of
-// 128: 248 us, the warp-MMA kernel 45).
 // A word's codes less 8, times 2^-9: elements (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ void centred8(uint32_t w, float2 (&e)[4]) {
     uint32_t h[4];
@@ -37,6 +32,11 @@ __device__ __forceinline__ void centred8(uint32_t w, float2 (&e)[4]) {
     for (int i = 0; i < 4; ++i) e[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
 }
 
+// One warp per (query row, H query heads of a KV head, chunk).  W lanes (a power of two, W * 8 >= d)
+// hold one key's row, eight elements each, so 32 / W keys are taken at a time, U such steps (16 keys at most)
+// between two updates of the softmax; every such slice of the warp keeps its own online softmax and
+// they merge at the end.  Bound by its arithmetic, shuffles most of all (64 x 2048 tokens, 32 heads on 8 of
+// 128: 248 us, the warp-MMA kernel 45).
 template <int W, int H>
 __global__ void __launch_bounds__(128)
     attend_q4_simt_kernel(const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc, const DecodeKParams p,
@@ -241,11 +241,12 @@ size_t partial_bytes(long long rows, int Hq, int splits, int d) {
 }  // namespace
 
 namespace {
-// (Query row, head) pairs of a sequence and KV head that the warp-MMA kernel, which takes eight at a
-// time, is faster for than the tcgen05 kernel, whose time hardly depends on them.  4 x 65536 tokens, one
-// scale group a row: 24 pairs 38.5 us, the tcgen05 kernel 34.5 (32 pairs); 64 x 2048 tokens, four KV heads:
-// 69 and 77.  Two groups: 32 pairs 49.8 us, 40 58.7, the tcgen05 kernel 48.3 (40 pairs); 89, 105 and 102
-// (64 x 2048).
+// (Query row, head) pairs of a sequence and KV head that go to the warp-MMA kernel, which takes eight at a
+// time; the tcgen05 kernel's time hardly depends on them.  Measured, one scale group a row: 24 pairs over
+// 4 x 65536 tokens 38.5 us, tcgen05 (32 pairs) 34.5; over 64 x 2048 tokens of four KV heads 69 and 77.  Two
+// groups: 32 pairs 49.8 us, 40 pairs 58.7, tcgen05 (40 pairs) 48.3; over 64 x 2048 89, 105 and 102.  So the
+// border lies lower for few long sequences than for many short ones, and one number is a compromise: at 24
+// pairs and one group the long case gives up 4 us for 8 us of the short one.
 int q4_mma_slots(int G) { return G == 1 ? 24 : 32; }
 
 // Rows of partial results of a balanced launch: two units for every warp or block.
@@ -279,6 +280,10 @@ Q4Plan plan_attend_q4(int B, int rows, int max_q, int Hq, int Hkv, int d, int gr
         // 13.5 steps, 46.9 and 44.2; eight rows, 4096, 18 steps: 53.5 and 62.7), or 8 where one wave does
         // not hold the units (1024 of four rows: 256 tokens 21.6 and 16.7; 512 of eight: 19.4 and 18.0, 1024
         // tokens, 9 steps, 34.5 and 38.6).
+        // All these go by the tokens that the table has room for: the lengths are on the device.  The figures
+        // are those of tables as wide as the longest sequence.  Much wider ones get chunks and shares for sequences
+        // that are not there: 4 x 8192 tokens, 64 heads on 8 of 128, 26.6 us, with a table for 131072 120.8; 32 x 512,
+        // 32 heads on 8, 14.4 and 20.5; 64 x 2048, 64 heads on 8, 57.3 both.
         const int step = plan.umma ? 128 / (d / group) : kStageKeys;
         plan.blocks = sms * (plan.umma ? 1 : mma_blocks_per_sm(plan.mma_rows, d));
         const long long per_unit = std::max(1ll, plan.blocks / std::max(units, 1ll));

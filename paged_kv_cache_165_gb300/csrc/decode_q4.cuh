@@ -13,7 +13,7 @@
 namespace pkv {
 
 struct AttendQ4Params {
-    DecodeKParams k;     // head_tiles: tiles of eight (query row, head) pairs per sequence and KV head
+    DecodeKParams k;     // head_tiles: tiles of (query row, head) pairs per sequence and KV head (4, 8 or 64 each)
     uint8_t *kc, *vc;
     int new_bf16;        // type of the step's new rows
     float q_sign;        // the queries are taken times the scale's sign (0, 1, -1) and k.scale_log2 is positive, so
@@ -151,7 +151,8 @@ bool q4_wide_shape(int d, int group);
 cudaError_t launch_attend_q4_wide(const AttendQ4Params &P, int rows, int d, int bs, int G, dim3 grid, cudaStream_t stream);
 cudaError_t launch_attend_q4_bs8(const AttendQ4Params &P, int rows, int d, int G, dim3 grid, cudaStream_t stream);
 
-// The tcgen05 kernel (decode_q4_umma.cu): 9 and more query rows x heads for each KV head.
+// The tcgen05 kernel (decode_q4_umma.cu): more query rows x heads for each KV head than the warp-MMA kernel
+// is faster for (24 with one scale group a row, 32 with two; q4_mma_slots in decode_q4.cu).
 constexpr int kQ4UmmaSlots = 64;   // (query row, head) pairs of a tile
 bool q4_umma_shape(int d, int group, int bs);
 cudaError_t launch_attend_q4_umma(const AttendQ4Params &P, int d, int bs, int G, dim3 grid, cudaStream_t stream);

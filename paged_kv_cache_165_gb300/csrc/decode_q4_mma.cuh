@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, Rows::kBlocksPerSm)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff) + warp * kStages;
     uint8_t *ring = smem + warp * kStages * Cfg::kStageBytes;
     Rows rows;
-    rows.qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff + warp * Rows::kQBytes) + lane;   // [step][lane]
+    if constexpr (Rows::kQBytes > 0)
+        rows.qfrag = reinterpret_cast<uint4 *>(smem + Cfg::kQOff + warp * Rows::kQBytes) + lane;   // [step][lane]
     float *par = reinterpret_cast<float *>(smem + Cfg::kParOff + warp * Cfg::kParBytes);
     if (lane == 0) {
         for (int st = 0; st < kStages; ++st) mbar_init(smem_addr(&bars[st]), 1);

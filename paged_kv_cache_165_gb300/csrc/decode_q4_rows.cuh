@@ -1,6 +1,6 @@
-// decode_q4_rows.cuh -- the arithmetic of decode_q4.cu's warp-MMA kernel for a tile of query rows: how
-// eight (query row, head) pairs, or up to four, are laid out over a warp, and what they do with a
-// stage of 32 keys in shared memory.  Layouts and ranges: decode_q4.cu.
+// decode_q4_rows.cuh -- the arithmetic of the warp-MMA kernel (decode_q4_mma.cuh) for a tile of query
+// rows: how eight (query row, head) pairs, or up to four, are laid out over a warp, and what they do
+// with a stage of 32 keys in shared memory.  Layouts and ranges: decode_q4_mma.cuh.
 #pragma once
 
 #include "common.cuh"
@@ -375,7 +375,6 @@ struct FourRows {
     static constexpr int kBlocksPerSm = mma_blocks_per_sm(4, D);
     static_assert(WPT >= 1 && HPG >= 1, "a group has at least 32 elements");
 
-    uint4 *qfrag;   // not used
     float f, qsum[G];
     float v[G * WPT][8];
     uint32_t q[G * WPT][2][2];   // B operands: [word][even, odd elements][k half]
