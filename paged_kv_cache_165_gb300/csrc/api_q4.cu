@@ -57,15 +57,9 @@ pkv_status check_attend(const char *what, int B, int Tq, int max_q, int Hq, int 
     return PKV_OK;
 }
 
-// Blocks that the rows of a call can see.
-int seen_pages(int MBS, int bs, int window, int max_q) {
-    const long long w = window > 0 ? static_cast<long long>(window) + max_q - 1 : 0;
-    return visible_blocks(MBS, bs, static_cast<int>(w < 0x7fffffff ? w : 0x7fffffff));
-}
-
 size_t workspace_bound(int B, int Tq, int max_q, int Hq, int Hkv, int d, int group, int bs, int MBS, int window,
                        int num_splits, int sm_count) {
-    const int pages = seen_pages(MBS, bs, window, max_q);
+    const int pages = visible_blocks_of_rows(MBS, bs, window, max_q);
     size_t most = 0;   // whatever the pointers' alignment
     for (bool aligned : {false, true}) {
         const size_t n = plan_attend_q4(B, Tq, max_q, Hq, Hkv, d, group, bs, pages, num_splits, sm_count, aligned)
@@ -93,7 +87,7 @@ pkv_status attend(const char *what, float *out, float *lse, const float *q, cons
     const pkv_status s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     const bool aligned = aligned_to(k_cache, 16) && aligned_to(v_cache, 16) && aligned_to(q, 16) && aligned_to(out, 16);
-    const Q4Plan plan = plan_attend_q4(B, Tq, max_q, Hq, Hkv, d, group, bs, seen_pages(MBS, bs, window, max_q),
+    const Q4Plan plan = plan_attend_q4(B, Tq, max_q, Hq, Hkv, d, group, bs, visible_blocks_of_rows(MBS, bs, window, max_q),
                                        num_splits, sm_count, aligned);
     if (plan.workspace_bytes > 0 &&
         (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned_to(workspace, 16)))

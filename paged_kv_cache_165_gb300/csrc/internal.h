@@ -129,6 +129,12 @@ inline int visible_blocks(int MBS, int bs, int window) {
     return static_cast<int>(w < MBS ? w : MBS);
 }
 
+// Blocks that the rows of a sequence, max_q at most, can see together.
+inline int visible_blocks_of_rows(int MBS, int bs, int window, int max_q) {
+    const long long w = window > 0 ? static_cast<long long>(window) + max_q - 1 : 0;
+    return visible_blocks(MBS, bs, static_cast<int>(w < 0x7fffffff ? w : 0x7fffffff));
+}
+
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype dt,
                           cudaStream_t stream);
 

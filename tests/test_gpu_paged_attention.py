@@ -326,3 +326,16 @@ def test_rows_outside_the_call_are_flagged_on_tensor_cores(hq, hkv, d, bs, windo
                                           torch.tensor([0, max_q], dtype=torch.int32), 0.1, window)
     assert_attn_close(out[at], ref, "the good sequence")
     assert_attn_close(lse[at], ref_lse, "the good sequence's lse")
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs", [(16, 2, 128, torch.bfloat16, 16), (8, 2, 40, torch.float32, 8)])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_the_largest_window_is_no_window(hq, hkv, d, dtype, bs, splits):
+    """window + max_q - 1 passes 2^31 - 1."""
+    lens, nqs = [50, 300, 900], [4, 1, 3]
+    q, kc, vc, table, clens, cu = make_case(79, lens, nqs, hq, hkv, d, bs, dtype)
+    ref, ref_lse = oracle.paged_attention(q, kc, vc, table, clens, cu, 0.1, 0)
+    out, lse = run(q, kc, vc, table, clens, cu, 0.1, (1 << 31) - 1, splits, one_per_seq=False)
+    assert pkv.get_device_error() == 0
+    assert_attn_close(out, ref, "out")
+    assert_attn_close(lse, ref_lse, "lse")
