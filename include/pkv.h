@@ -15,6 +15,12 @@
  *                               and pkv_paged_attention_q4 write, read back and attend it
  *   pkv_block_tables_extend     block tables and slot map of a step built on the GPU from the
  *                               request lengths; pkv_block_tables_release gives blocks back
+ *   pkv_block_tables_fork       rows that share blocks: forks, beams, shorter rows; pkv_block_tables_compact
+ *                               moves the blocks in use to the lowest ids, pkv_kv_block_copy_counted copies
+ *   pkv_rope_append             rotary positions of q and K, K and V written into the cache; pkv_rope the
+ *                               rotation alone, both ways
+ *   pkv_paged_attention_sinks   a sliding window with a few first tokens that stay visible
+ *   pkv_verify_drafts           drafted tokens accepted or replaced by the target's probabilities
  *   pkv_prefill_attention       varlen causal attention over cu_seqlens that also
  *                               writes the cache
  *
@@ -80,12 +86,14 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
 #define PKV_DEVERR_BLOCK       2u   /* block_table entry outside [0, NB) (block read as zeros) */
 #define PKV_DEVERR_LEN         4u   /* context length < 0 or > MBS * bs (sequence treated as empty) */
 #define PKV_DEVERR_CU_SEQLENS  8u   /* cu_seqlens decreasing, > T, or a sequence > max_seqlen */
-#define PKV_DEVERR_PAIR       16u   /* kv_block_copy pair outside [0, NB) (pair skipped) */
+#define PKV_DEVERR_PAIR       16u   /* kv_block_copy pair outside [0, NB) (pair skipped), a bad pair count, or a
+                                       parent row outside the batch (block_tables_fork) */
 #define PKV_DEVERR_TIMEOUT    32u   /* a bounded wait for an asynchronous copy gave up */
 #define PKV_DEVERR_LAYOUT     64u   /* a kernel found its shared memory misaligned and did nothing */
 #define PKV_DEVERR_PREFIX    128u   /* a shared-prefix group whose members' prefixes differ (length, blocks) */
 #define PKV_DEVERR_POOL      256u   /* free list or slot map too small for a row, a bad free count, or a block
                                        given back twice (block_tables_*: the row or list stays as it was) */
+#define PKV_DEVERR_PROBS     512u   /* a drafted token outside the vocabulary, or probabilities without mass */
 
 /* Static description of a status code. */
 const char *pkv_status_string(pkv_status status);
@@ -528,6 +536,161 @@ size_t pkv_block_tables_release_workspace_bytes(int B);
 pkv_status pkv_block_tables_release(int32_t *block_table, const int32_t *first_block, const int32_t *end_block,
                                     int32_t *free_list, const int32_t *free_count, int32_t *free_count_out, int B,
                                     int MBS, int NB, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * pkv_block_tables_fork -- block tables whose rows share blocks (forks for parallel sampling, beams), kept
+ * on the GPU (what plumephp.com "KV Cache 优化与注意力机制加速" §4.3 BlockTable.fork and its copy-on-write
+ * do on the host).  Row b of the result takes the sequence of row parents[b] (-1: none, length 0; parents
+ * NULL: every row its own), so that with p = parents[b] and L = context_lens[p]:
+ *   block_table_out[b][j] = block_table[p][j] for j < ceil(L / bs), -1 from there on;  context_lens_out[b] = L
+ * and blocks are shared, but for one that will be written: where L % bs != 0 the row's last block is its own.
+ * Of the rows that end, partly filled, in a block, the lowest keeps it when no row has it inside its sequence
+ * and it is not held; the others get a fresh block each, in row order, the lowest free id first, and
+ * pairs lists (old, fresh) for pkv_kv_block_copy_counted, to run on every layer's caches before the next write.
+ *
+ * References are counted anew from the result: blocks that it does not name come free.  With parents NULL
+ * the call therefore gives back what shorter lengths (rejected drafts, context_lens from
+ * pkv_verify_drafts), lengths of zero (finished rows) and entries of -1 (blocks outside a window) no longer
+ * name, and unshares the last blocks.  The rows must be all that uses the pool, but for blocks marked in held.
+ *
+ *   block_table_out, context_lens_out   [B][MBS], [B]; may be block_table and context_lens
+ *   held          int32 [NB] or NULL: blocks other than 0 are in use whatever the tables say (a prefix kept
+ *                 for later requests)
+ *   refs          int32 [NB], written: entries that name the block, plus one where it is held; 0: free
+ *   free_list     int32 [NB], written: the free blocks in descending order (the lowest is handed out first),
+ *                 -1 past free_count[0] of them
+ *   pairs         int32 [B][2], written: pair_count[0] pairs (8-byte aligned), (-1, -1) past them
+ *   workspace     pkv_block_tables_share_workspace_bytes(B, MBS, NB) bytes, 4-byte aligned, contents free; calls
+ *                 that share it must not overlap
+ * A parent outside [-1, B) sets PKV_DEVERR_PAIR and a length outside [0, MBS * bs] PKV_DEVERR_LEN: the row is
+ * empty.  An entry outside [-1, NB) sets PKV_DEVERR_BLOCK and becomes -1.  Rows for which no fresh block is
+ * left set PKV_DEVERR_POOL and are empty (what only they named comes free with the next call).
+ */
+size_t pkv_block_tables_share_workspace_bytes(int B, int MBS, int NB);
+
+pkv_status pkv_block_tables_fork(const int32_t *block_table, const int32_t *context_lens, const int32_t *parents,
+                                 const int32_t *held, int32_t *block_table_out, int32_t *context_lens_out, int32_t *refs,
+                                 int32_t *free_list, int32_t *free_count, int32_t *pairs, int32_t *pair_count, int B,
+                                 int MBS, int bs, int NB, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * pkv_block_tables_compact -- the blocks in use moved to the lowest ids, so that the pool ends in free
+ * blocks: with n blocks in use, the i-th of those from id n on that are not held (ascending) becomes the i-th
+ * free id below n (ascending).  pairs lists (old, new) for pkv_kv_block_copy_counted; no block is both.
+ *   block_table_out   [B][MBS], may be block_table: the new ids; -1 from ceil(context_lens[b] / bs) on
+ *   pairs             int32 [NB / 2][2], 8-byte aligned
+ *   refs, free_list, free_count, pair_count, held, workspace and errors as for pkv_block_tables_fork
+ */
+pkv_status pkv_block_tables_compact(const int32_t *block_table, const int32_t *context_lens, const int32_t *held,
+                                    int32_t *block_table_out, int32_t *refs, int32_t *free_list, int32_t *free_count,
+                                    int32_t *pairs, int32_t *pair_count, int B, int MBS, int bs, int NB, void *workspace,
+                                    size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * pkv_kv_block_copy_counted -- pkv_kv_block_copy of the first count[0] pairs (int32 [1], device memory), of at
+ * most n.  A count outside [0, n] sets PKV_DEVERR_PAIR and is cut to it.
+ */
+pkv_status pkv_kv_block_copy_counted(void *k_cache, void *v_cache, pkv_dtype dt, const int32_t *pairs, int n,
+                                     const int32_t *count, int Hkv, int d, int bs, int NB, pkv_stream_t stream);
+
+/*
+ * Rotary positions.  Dimension pair j of rot / 2 at position p turns by p * f_j:
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos),
+ * pairs (j, j + rot / 2), or (2j, 2j + 1) when interleaved; dimensions from rot on stay as they are.
+ *
+ * pkv_rope_turns -- the angles per position of the pairs, as fractions of a turn in 2^-64 units (turns: HOST
+ * memory, [rot / 2]; f_j = base^(-2j / rot) / (2 pi) turns, computed in fp64).  The product of a position and
+ * such a number, modulo 2^64, is the position's angle to within fp64's rounding of f_j, for every 32-bit
+ * position.  Scaled for contexts `factor` times as long:
+ *   PKV_ROPE_LINEAR   f_j / factor
+ *   PKV_ROPE_BASE     base * factor^(rot / (rot - 2)) in place of base (rot > 2)
+ *   PKV_ROPE_PARTS    f_j (r + (1 - r) / factor), r = (n - low) / (high - low) cut to [0, 1], n = original * f_j
+ *                     the turns of the pair over the original context: fast pairs stay, slow ones are interpolated
+ *   rot even, >= 2; base > 0; factor > 0; original > 0 and low < high for PKV_ROPE_PARTS.
+ */
+typedef enum { PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_BASE = 2, PKV_ROPE_PARTS = 3 } pkv_rope_scaling;
+
+pkv_status pkv_rope_turns(uint64_t *turns, int rot, double base, pkv_rope_scaling scaling, double factor,
+                          double original, double low, double high);
+
+/*
+ * pkv_rope_append -- q and K of T new tokens rotated by their positions, q into rows, K and V into their slots
+ * (pkv_kv_append of the rotated K).
+ *   q_out      [T][Hq][d] of type q_out_dt (PKV_F32, what decode takes, or PKV_BF16); may be q when the types
+ *              are the same and q_stride = Hq * d
+ *   q, k_new, v_new   type dt (PKV_F32 or PKV_BF16): token t's heads [H][d] start at element t * q_stride
+ *              (k_stride, v_stride), so that rows of a packed projection need no copy; strides >= H * d
+ *   positions  int32 [T], any value
+ *   turns      uint64 [rot / 2] in device memory (pkv_rope_turns); rot even, 2 <= rot <= d
+ *   slot_mapping  int64 [T]: < 0: K and V of the token are not written (padding; q is rotated all the same);
+ *              >= NB * bs sets PKV_DEVERR_SLOT, likewise
+ *   k_cache, v_cache  [NB][Hkv][bs][d] of type dt
+ * Angles as above; cosine and sine, products and their sum in fp32, rounded once to the output's type.  V and
+ * K's dimensions past rot are copied bit by bit.  1 <= d <= 256.
+ */
+pkv_status pkv_rope_append(void *q_out, pkv_dtype q_out_dt, const void *q, const void *k_new, const void *v_new,
+                           pkv_dtype dt, long long q_stride, long long k_stride, long long v_stride,
+                           const int32_t *positions, const uint64_t *turns, int rot, int interleaved, float mscale,
+                           void *k_cache, void *v_cache, const int64_t *slot_mapping, int T, int Hq, int Hkv, int d,
+                           int bs, int NB, pkv_stream_t stream);
+
+/*
+ * pkv_rope -- the rotation alone: q into q_out (as above) and k into k_out [T][Hkv][d] of type dt (k and k_out
+ * NULL: q alone; k_out may be k when k_stride = Hkv * d), for rows that a quantising append or a decode step
+ * takes.  inverse != 0 turns by -p * f_j (mscale as given): the gradient of the rotation.
+ */
+pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q, const void *k, pkv_dtype dt,
+                    long long q_stride, long long k_stride, const int32_t *positions, const uint64_t *turns, int rot,
+                    int interleaved, float mscale, int inverse, int T, int Hq, int Hkv, int d, pkv_stream_t stream);
+
+/*
+ * pkv_verify_drafts -- drafted tokens checked against the target's probabilities, from given random numbers,
+ * so that what comes out is distributed as the target alone.  Sequence b has k = cu_drafts[b+1] - cu_drafts[b]
+ * drafts x_i with the draft's probabilities q_i, and k + 1 rows p_i of the target's and numbers u_i, all from
+ * row cu_drafts[b] (of D) or cu_drafts[b] + b (of D + B) on.
+ *   draft i is accepted while u_i * q_i(x_i) < p_i(x_i)   (exact products);  accepted[b] = a, the first
+ *   that fails;  the next token is the lowest v with r_0 + .. + r_v > u_k * (r_0 + .. + r_{V-1}), where
+ *   r = max(p_a - q_a, 0) for a < k (p_a itself where that is 0 everywhere) and r = p_k for a = k.
+ * Sums are of whole multiples of 2^-58, to which each probability is rounded down (exact from 2^-34 on), so that
+ * the token depends neither on the order of summation nor on the GPU.
+ *   accepted      int32 [B]
+ *   tokens        int32 [D + B]: the accepted drafts of a sequence, its next token, -1 in the rest of its k + 1 places
+ *   target_probs  [D + B][V] of type dt (PKV_F32 or PKV_BF16), rows target_stride >= V elements apart
+ *   draft_probs   [D][V] of type dt, rows draft_stride apart; NULL: the drafts were not drawn but chosen (q is 1 at
+ *                 x_i, and r is p_a without x_a)
+ *   draft_tokens  int32 [D];  uniforms  fp32 [D + B], in [0, 1)
+ *   cu_drafts     int32 [B + 1], non-decreasing from 0 to D; k = 0: one token drawn from p_0
+ *   context_lens, context_lens_out   int32 [B] or NULL both; may be the same: L - (k - a), the length of a cache
+ *                 that holds the drafts' K and V without those of the rejected ones
+ * A drafted token outside [0, V) is rejected and sets PKV_DEVERR_PROBS; probabilities without mass (zero,
+ * negative or NaN everywhere) set it too, and the token is -1.  Probabilities count as at most 1.  An
+ * inconsistent cu_drafts sets PKV_DEVERR_CU_SEQLENS: the sequence accepts nothing, its length stays and its
+ * tokens are not written.  B <= 65535, V < 2^30.
+ */
+pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *target_probs, const void *draft_probs,
+                             pkv_dtype dt, long long target_stride, long long draft_stride, const int32_t *draft_tokens,
+                             const int32_t *cu_drafts, const float *uniforms, const int32_t *context_lens,
+                             int32_t *context_lens_out, int B, int D, int V, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_sinks -- pkv_paged_attention with a sliding window and a few first tokens that stay
+ * visible: the query row at position p sees the keys t <= p with t < sinks or t > p - window.
+ *   window, sinks   >= 0.  window = 0: none (every key up to p, whatever sinks says); sinks = 0: the window alone,
+ *              exactly pkv_paged_attention
+ * Blocks that lie wholly behind the sinks and before every row's window are never read, so a caller may
+ * free them (entries of -1).  Keys that no row of a sequence sees may hold anything in blocks that are read,
+ * NaN and infinities among them; those that some row of the sequence sees must be finite.
+ *   workspace  pkv_paged_attention_sinks_workspace_bytes(...) bytes, the rules of pkv_paged_attention
+ *   everything else as pkv_paged_attention (PKV_F32 and PKV_BF16 caches).
+ */
+size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
+                                                 int window, int sinks, int num_splits);
+
+pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, const void *k_cache, const void *v_cache,
+                                     pkv_dtype dt, const int32_t *block_table, const int32_t *context_lens,
+                                     const int32_t *cu_q, int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
+                                     int NB, float scale, int window, int sinks, int num_splits, void *workspace,
+                                     size_t workspace_bytes, pkv_stream_t stream);
 
 /*
  * pkv_paged_decode_attention_noalloc -- pkv_paged_decode_attention without a workspace.

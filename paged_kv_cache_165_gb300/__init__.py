@@ -11,10 +11,13 @@ from ._binding import (  # noqa: F401
     PKV_F32,
     PKV_FP8_E4M3,
     PkvError,
+    block_tables_compact,
     block_tables_extend,
     block_tables_extend_workspace_bytes,
+    block_tables_fork,
     block_tables_release,
     block_tables_release_workspace_bytes,
+    block_tables_share_workspace_bytes,
     decode_kernel_launches,
     decode_step,
     decode_step_kernel_launches,
@@ -38,13 +41,19 @@ from ._binding import (  # noqa: F401
     paged_attention_kernel_launches,
     paged_attention_q4,
     paged_attention_q4_workspace_bytes,
+    paged_attention_sinks,
+    paged_attention_sinks_workspace_bytes,
     paged_attention_workspace_bytes,
     paged_decode_attention,
     paged_decode_attention_fp8,
     paged_decode_attention_noalloc,
     prefill_attention,
     q4_row_bytes,
+    rope,
+    rope_append,
+    rope_turns,
     selftest_bounded_wait,
+    verify_drafts,
 )
 from .blocks import BlockManager, DeviceBlocks, OutOfBlocks, PrefixGroups  # noqa: F401
 

@@ -21,7 +21,7 @@ PKV_F32, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
 
 DEVERR = {
     "slot": 1, "block": 2, "len": 4, "cu_seqlens": 8, "pair": 16, "timeout": 32, "layout": 64, "prefix": 128,
-    "pool": 256,
+    "pool": 256, "probs": 512,
 }
 
 _DTYPES = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.uint8: PKV_FP8_E4M3}
@@ -119,6 +119,27 @@ def lib() -> ctypes.CDLL:
     L.pkv_block_tables_release_workspace_bytes.restype = Z
     L.pkv_block_tables_release.argtypes = [P] * 6 + [I] * 3 + [P, Z, P]
     L.pkv_block_tables_release.restype = I
+    L.pkv_block_tables_share_workspace_bytes.argtypes = [I, I, I]
+    L.pkv_block_tables_share_workspace_bytes.restype = Z
+    L.pkv_block_tables_fork.argtypes = [P] * 11 + [I] * 4 + [P, Z, P]
+    L.pkv_block_tables_fork.restype = I
+    L.pkv_block_tables_compact.argtypes = [P] * 9 + [I] * 4 + [P, Z, P]
+    L.pkv_block_tables_compact.restype = I
+    L.pkv_kv_block_copy_counted.argtypes = [P, P, I, P, I, P, I, I, I, I, P]
+    L.pkv_kv_block_copy_counted.restype = I
+    LL, D = ctypes.c_longlong, ctypes.c_double
+    L.pkv_rope_turns.argtypes = [P, I, D, I, D, D, D, D]
+    L.pkv_rope_turns.restype = I
+    L.pkv_rope_append.argtypes = [P, I, P, P, P, I, LL, LL, LL, P, P, I, I, F, P, P, P] + [I] * 6 + [P]
+    L.pkv_rope_append.restype = I
+    L.pkv_rope.argtypes = [P, I, P, P, P, I, LL, LL, P, P, I, I, F, I, I, I, I, I, P]
+    L.pkv_rope.restype = I
+    L.pkv_verify_drafts.argtypes = [P, P, P, P, I, LL, LL, P, P, P, P, P, I, I, I, P]
+    L.pkv_verify_drafts.restype = I
+    L.pkv_paged_attention_sinks_workspace_bytes.argtypes = [I] * 11
+    L.pkv_paged_attention_sinks_workspace_bytes.restype = Z
+    L.pkv_paged_attention_sinks.argtypes = [P, P, P, P, P, I, P, P, P] + [I] * 9 + [F, I, I, I, P, Z, P]
+    L.pkv_paged_attention_sinks.restype = I
     L.pkv_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, I, I, P, P]
     L.pkv_selftest_bounded_wait.restype = I
     L.pkv_prefill_attention.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, P, P, P, I, I, P]
@@ -202,7 +223,7 @@ def _ready(here, tensors) -> bool:
     return True
 
 
-_OPTIONAL = ("lse", "cu_q", "first_block", "step_slots", "workspace")
+_OPTIONAL = ("lse", "cu_q", "first_block", "step_slots", "workspace", "parents", "held", "draft_probs", "context_lens_out")
 
 
 def _refuse(what, here, **tensors) -> None:
@@ -289,14 +310,24 @@ def paged_decode_attention_fp8(out, q, k_codes, v_codes, k_scale, v_scale, block
         int(window), int(num_splits), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-def kv_block_copy(k_cache, v_cache, pairs, stream=None) -> None:
-    """Copy whole blocks: for each (src, dst) row of int32 pairs [n][2]."""
+def kv_block_copy(k_cache, v_cache, pairs, stream=None, count=None) -> None:
+    """Copy whole blocks: for each (src, dst) row of int32 pairs [n][2].  count: int32 [1] on the
+    device, the number of leading pairs to copy (pkv_kv_block_copy_counted)."""
     _cuda("k_cache", k_cache)
     dt = _dtype(k_cache)
     _cuda("v_cache", v_cache, k_cache.dtype)
     _cuda("pairs", pairs, torch.int32)
     NB, Hkv, bs, d = k_cache.shape
     n = pairs.numel() // 2
+    if count is not None:
+        here = _current_device()
+        _refuse("kv_block_copy", here, k_cache=(k_cache, None), v_cache=(v_cache, k_cache.dtype), pairs=(pairs, _I32),
+                count=(count, _I32))
+        if v_cache.shape != k_cache.shape or count.numel() != 1:
+            raise ValueError("kv_block_copy: shapes do not match")
+        _check(lib().pkv_kv_block_copy_counted(_ptr(k_cache), _ptr(v_cache), dt, _ptr(pairs), n, _ptr(count), Hkv, d, bs,
+                                               NB, _stream(stream, here)))
+        return
     _check(lib().pkv_kv_block_copy(_ptr(k_cache), _ptr(v_cache), dt, _ptr(pairs), n, Hkv, d, bs,
                                    NB, _stream(stream)))
 
@@ -789,5 +820,244 @@ def block_tables_release(block_table, first_block, end_block, free_list, free_co
     status = lib().pkv_block_tables_release(
         block_table.data_ptr(), _ptr(first_block), end_block.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
         free_count_out.data_ptr(), B, MBS, free_list.numel(), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
+
+
+def block_tables_share_workspace_bytes(B, MBS, NB) -> int:
+    return int(lib().pkv_block_tables_share_workspace_bytes(int(B), int(MBS), int(NB)))
+
+
+def _share(what, **tensors):
+    """Checks of block_tables_fork and block_tables_compact; returns (B, MBS, NB, current device)."""
+    here = _current_device()
+    try:
+        ok = _ready(here, tensors.values()) and all([t is None or name == "workspace" or t.dtype is _I32
+                                                     for name, t in tensors.items()])
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok or any([t is None and name not in _OPTIONAL for name, t in tensors.items()]):
+        _refuse(what, here, **{name: (t, None if name == "workspace" else _I32) for name, t in tensors.items()})
+    table = tensors["block_table"].shape
+    if len(table) != 2:
+        raise ValueError(f"{what}: block_table must be [B][MBS]")
+    B, NB = table[0], tensors["free_list"].numel()
+    want = {"block_table_out": table[0] * table[1], "context_lens": B, "context_lens_out": B, "parents": B, "held": NB,
+            "refs": NB, "free_count": 1, "pair_count": 1}
+    for name, n in want.items():
+        t = tensors.get(name)
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what}: {name} must hold {n} numbers, got {t.numel()}")
+    return B, table[1], NB, here
+
+
+def block_tables_fork(block_table, context_lens, parents, block_table_out, context_lens_out, refs, free_list, free_count,
+                      pairs, pair_count, bs, held=None, workspace=None, stream=None) -> None:
+    """Row b takes the sequence of row parents[b] (int32 [B], -1: none; None: every row its own), sharing
+    its blocks but for a partly filled last one; references counted anew, blocks without any free
+    (see pkv.h).  refs, free_list int32 [NB], free_count, pair_count int32 [1], pairs int32 [B][2]:
+    the copies to run with kv_block_copy(..., pairs, count=pair_count).  held: int32 [NB] or None."""
+    B, MBS, NB, here = _share("block_tables_fork", block_table=block_table, context_lens=context_lens, parents=parents,
+                              block_table_out=block_table_out, context_lens_out=context_lens_out, refs=refs,
+                              free_list=free_list, free_count=free_count, pairs=pairs, pair_count=pair_count, held=held,
+                              workspace=workspace)
+    if context_lens_out is None:
+        raise TypeError("context_lens_out must be a torch.Tensor")
+    if pairs.numel() != 2 * B:
+        raise ValueError(f"block_tables_fork: pairs must be [{B}][2]")
+    status = lib().pkv_block_tables_fork(
+        block_table.data_ptr(), context_lens.data_ptr(), _ptr(parents), _ptr(held), block_table_out.data_ptr(),
+        context_lens_out.data_ptr(), refs.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(),
+        pair_count.data_ptr(), B, MBS, int(bs), NB, _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
+
+
+def block_tables_compact(block_table, context_lens, block_table_out, refs, free_list, free_count, pairs, pair_count, bs,
+                         held=None, workspace=None, stream=None) -> None:
+    """The blocks in use moved to the lowest ids (see pkv.h); pairs int32 [NB // 2][2], the other
+    tensors as block_tables_fork."""
+    B, MBS, NB, here = _share("block_tables_compact", block_table=block_table, context_lens=context_lens,
+                              block_table_out=block_table_out, refs=refs, free_list=free_list, free_count=free_count,
+                              pairs=pairs, pair_count=pair_count, held=held, workspace=workspace)
+    if pairs.numel() != NB // 2 * 2:
+        raise ValueError(f"block_tables_compact: pairs must be [{NB // 2}][2]")
+    status = lib().pkv_block_tables_compact(
+        block_table.data_ptr(), context_lens.data_ptr(), _ptr(held), block_table_out.data_ptr(), refs.data_ptr(),
+        free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(), pair_count.data_ptr(), B, MBS, int(bs), NB,
+        _ptr(workspace), _bytes(workspace), _stream(stream, here))
+    if status:
+        _check(status)
+
+
+# ------------------------------------------------------------- rotary positions
+
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def rope_turns(rot, base=10000.0, scaling="none", factor=1.0, original=1, low=1.0, high=32.0, device="cuda") -> torch.Tensor:
+    """The angles per position of rot // 2 dimension pairs, as fractions of a turn in 2^-64 units (int64
+    [rot // 2], the bits of uint64): the `turns` of rope and rope_append, made once.  scaling: "none",
+    "linear", "base" or "parts", for contexts `factor` times `original` tokens (see pkv.h)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"rope_turns: scaling {scaling!r} (one of {', '.join(_SCALINGS)})")
+    turns = torch.zeros(max(1, int(rot) // 2), dtype=_I64)
+    _check(lib().pkv_rope_turns(turns.data_ptr(), int(rot), float(base), _SCALINGS[scaling], float(factor), float(original),
+                                float(low), float(high)))
+    return turns.to(device)
+
+
+def _heads(what, name, t, d=None):
+    """Elements between the tokens of t [T][H][d], whose rows [H][d] are contiguous."""
+    if t.dim() != 3 or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{what}: {name} must be [T][heads][{'d' if d is None else d}]")
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else H * d
+
+
+def _rope_check(what, q_out, q, positions, turns, here, **more):
+    for name, (t, dtype, strided) in {"q_out": (q_out, None, False), "q": (q, None, True), "positions": (positions, _I32, False),
+                                      "turns": (turns, _I64, False), **more}.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+        if t.get_device() != here:   # the kernels run on the current device
+            raise ValueError(f"{what}: {name} is on device {t.get_device()}, the current one is {here}")
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if q.dim() != 3 or q_out.shape != q.shape or positions.numel() != q.shape[0]:
+        raise ValueError(f"{what}: shapes do not match [T][Hq][d] / [T]")
+
+
+def rope_append(q_out, q, k_new, v_new, k_cache, v_cache, positions, slot_mapping, turns, interleaved=False, mscale=1.0,
+                stream=None) -> None:
+    """q [T][Hq][d] rotated by positions[t] (int32) into q_out (fp32 or bf16); k_new [T][Hkv][d] rotated
+    and v_new as it is into cache slots slot_mapping[t] (int64, < 0: none).  The tokens of q, k_new and
+    v_new may be any distance apart (views of packed rows).  turns: rope_turns(rot), of the first rot
+    dimensions; pairs (j, j + rot / 2), or (2j, 2j + 1) when interleaved."""
+    what, here = "rope_append", _current_device()
+    dt = getattr(q, "dtype", None)
+    _rope_check(what, q_out, q, positions, turns, here, k_new=(k_new, dt, True), v_new=(v_new, dt, True),
+                k_cache=(k_cache, dt, False), v_cache=(v_cache, dt, False), slot_mapping=(slot_mapping, _I64, False))
+    T, Hq, d = q.shape
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != d or slot_mapping.numel() != T:
+        raise ValueError("rope_append: shapes do not match")
+    NB, Hkv, bs, _ = k_cache.shape
+    if tuple(k_new.shape) != (T, Hkv, d) or tuple(v_new.shape) != (T, Hkv, d):
+        raise ValueError("rope_append: k_new and v_new must be [T][Hkv][d]")
+    status = lib().pkv_rope_append(
+        q_out.data_ptr(), _dtype(q_out), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype(q), _heads(what, "q", q),
+        _heads(what, "k_new", k_new), _heads(what, "v_new", v_new), positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
+        1 if interleaved else 0, float(mscale), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv,
+        d, bs, NB, _stream(stream, here))
+    if status:
+        _check(status)
+
+
+def rope(q_out, q, k_out, k, positions, turns, interleaved=False, mscale=1.0, inverse=False, stream=None) -> None:
+    """q [T][Hq][d] rotated into q_out (fp32 or bf16) and k [T][Hkv][d] into k_out (its type; both None:
+    q alone), as rope_append does.  inverse: rotated back (the gradient of the rotation)."""
+    what, here = "rope", _current_device()
+    dt = getattr(q, "dtype", None)
+    more = {} if k is None and k_out is None else {"k": (k, dt, True), "k_out": (k_out, dt, False)}
+    _rope_check(what, q_out, q, positions, turns, here, **more)
+    T, Hq, d = q.shape
+    Hkv = 1
+    if more:
+        if k.dim() != 3 or k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("rope: k and k_out must be [T][Hkv][d]")
+        Hkv = k.shape[1]
+    status = lib().pkv_rope(
+        q_out.data_ptr(), _dtype(q_out), _ptr(k_out), q.data_ptr(), _ptr(k), _dtype(q), _heads(what, "q", q),
+        _heads(what, "k", k) if more else 0, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(), 1 if interleaved else 0,
+        float(mscale), 1 if inverse else 0, T, Hq, Hkv, d, _stream(stream, here))
+    if status:
+        _check(status)
+
+
+# --------------------------------------------------------------- drafted tokens
+
+def verify_drafts(accepted, tokens, target_probs, draft_tokens, cu_drafts, uniforms, draft_probs=None, context_lens=None,
+                  context_lens_out=None, stream=None) -> None:
+    """Drafts accepted against the target's probabilities, and a next token for every sequence (see pkv.h).
+
+    accepted int32 [B]; tokens int32 [D + B]; target_probs [D + B][V] and draft_probs [D][V] (or None: the
+    drafts were chosen, not drawn), fp32 or bf16, rows any distance apart; draft_tokens int32 [D];
+    cu_drafts int32 [B + 1]; uniforms fp32 [D + B]; context_lens, context_lens_out int32 [B]: the
+    lengths with the drafts, and without the rejected ones (may be the same)."""
+    what, here = "verify_drafts", _current_device()
+    _refuse(what, here, accepted=(accepted, _I32), tokens=(tokens, _I32), draft_tokens=(draft_tokens, _I32),
+            cu_drafts=(cu_drafts, _I32), uniforms=(uniforms, _F32), context_lens_out=(context_lens_out, _I32))
+    if context_lens is not None:
+        _refuse(what, here, context_lens=(context_lens, _I32))
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is None and name == "draft_probs":
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.get_device() != here:
+            raise ValueError(f"{what}: {name} is on {t.device}, the current device is {here}")
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what}: {name} must be rows of contiguous probabilities")
+        if t.dtype is not target_probs.dtype:
+            raise TypeError(f"{name} must be {target_probs.dtype}, got {t.dtype}")
+    B, D = accepted.numel(), draft_tokens.numel()
+    V = target_probs.shape[1]
+    if target_probs.shape[0] != D + B or tokens.numel() != D + B or uniforms.numel() != D + B or cu_drafts.numel() != B + 1 or \
+            (draft_probs is not None and tuple(draft_probs.shape) != (D, V)) or \
+            (context_lens is not None and context_lens.numel() != B) or \
+            (context_lens_out is not None and context_lens_out.numel() != B):
+        raise ValueError("verify_drafts: shapes do not match")
+    apart = lambda t: t.stride(0) if t is not None and t.shape[0] > 1 else V
+    status = lib().pkv_verify_drafts(
+        accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(), _ptr(draft_probs) if D > 0 else 0, _dtype(target_probs),
+        apart(target_probs), apart(draft_probs), draft_tokens.data_ptr(), cu_drafts.data_ptr(), uniforms.data_ptr(),
+        _ptr(context_lens), _ptr(context_lens_out), B, D, V, _stream(stream, here))
+    if status:
+        _check(status)
+
+
+# ----------------------------------------------------- windows with first tokens
+
+def paged_attention_sinks_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits=0) -> int:
+    return int(lib().pkv_paged_attention_sinks_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits))
+
+
+def paged_attention_sinks(out, q, k_cache, v_cache, block_table, context_lens, scale, window, sinks, cu_q=None, max_q=1,
+                          lse=None, num_splits=0, workspace=None, stream=None) -> None:
+    """paged_attention with a sliding window whose first `sinks` tokens stay visible: the row at position p
+    sees the keys t <= p with t < sinks or t > p - window.
+
+    q, out [Tq][Hq][d] fp32; cu_q int32 [B+1] (None: one query per sequence)."""
+    what, here = "paged_attention_sinks", _current_device()
+    try:
+        ok = (_ready(here, (out, q, k_cache, v_cache, block_table, context_lens, lse, cu_q, workspace)) and q.dtype is _F32 and
+              out.dtype is _F32 and v_cache.dtype is k_cache.dtype and block_table.dtype is _I32 and context_lens.dtype is _I32 and
+              (lse is None or lse.dtype is _F32) and (cu_q is None or cu_q.dtype is _I32))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, q=(q, _F32), out=(out, _F32), k_cache=(k_cache, None),
+                v_cache=(v_cache, getattr(k_cache, "dtype", None)), block_table=(block_table, _I32),
+                context_lens=(context_lens, _I32), lse=(lse, _F32), cu_q=(cu_q, _I32), workspace=(workspace, None))
+    dt = _dtype(k_cache)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError(f"{what}: q must be [rows][Hq][d] and the caches [NB][Hkv][bs][d]")
+    NB, Hkv, bs, d = k_cache.shape
+    Tq, Hq, dq = q.shape
+    B = context_lens.numel()
+    table = block_table.shape
+    if dq != d or out.shape != q.shape or v_cache.shape != k_cache.shape or len(table) != 2 or table[0] != B or \
+            (cu_q.numel() != B + 1 if cu_q is not None else Tq != B) or (lse is not None and lse.numel() != Tq * Hq):
+        raise ValueError(f"{what}: shapes do not match")
+    status = lib().pkv_paged_attention_sinks(
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dt, block_table.data_ptr(),
+        context_lens.data_ptr(), _ptr(cu_q), B, Tq, int(max_q), Hq, Hkv, d, bs, table[1], NB, float(scale), int(window),
+        int(sinks), int(num_splits), _ptr(workspace), _bytes(workspace), _stream(stream, here))
     if status:
         _check(status)

@@ -3,7 +3,8 @@ reference counts, fork and copy-on-write.
 
 This is the bookkeeping that sits above the C ABI and produces its inputs
 (block tables, slot mappings, copy pairs).  BlockManager runs on the host; DeviceBlocks
-keeps the tables of sequences that own their blocks on the GPU.
+keeps the tables on the GPU: of sequences that own their blocks (``release``, ``finish``) or
+share them (``fork``, ``settle``, ``compact``).
 
 * Blocks of ``block_size`` tokens are handed out on demand from a free pool; a
   sequence's logical block j maps to a physical block through its table
@@ -18,7 +19,8 @@ keeps the tables of sequences that own their blocks on the GPU.
 * With a sliding window of W tokens (zwjcode.cn "KV Cache 的增量解码" §10;
   plumephp.com §5.2) ``release_outside_window`` gives back the blocks that hold
   only positions before the window: no later query of the sequence sees them.
-  Their table entries become -1 and are never read.
+  Their table entries become -1 and are never read.  With ``sinks`` first tokens that
+  stay visible, their blocks are kept.
 * ``audit`` checks the invariant that every block's count equals the number of
   table entries that reference it (0539edu.com §5.2 suggests logging and checking
   every cache read/write per request).
@@ -129,16 +131,17 @@ class BlockManager:
                 self._release(blk)
         del self.lengths[seq]
 
-    def release_outside_window(self, seq: int, window: int) -> List[int]:
+    def release_outside_window(self, seq: int, window: int, sinks: int = 0) -> List[int]:
         """Give back the blocks of ``seq`` that hold only positions before its last
-        ``window`` tokens; returns their ids.  The current query (position len - 1) sees
-        positions len - window .. len - 1, and later queries see later ones."""
+        ``window`` tokens and none of the first ``sinks``; returns their ids.  The current
+        query (position len - 1) sees positions len - window .. len - 1, and later queries
+        see later ones."""
         if window <= 0:
             return []
         lo = self.lengths[seq] - window
         table = self.tables[seq]
         released = []
-        for j in range(max(0, lo) // self.block_size):   # blocks ending at or before lo
+        for j in range(-(-sinks // self.block_size), max(0, lo) // self.block_size):   # blocks ending at or before lo
             if table[j] >= 0:
                 self._release(table[j])
                 released.append(table[j])
@@ -259,11 +262,12 @@ class BlockManager:
 
 class DeviceBlocks:
     """Block tables, lengths and the free list of a batch kept on the GPU: the state of
-    block_tables_extend and block_tables_release, for sequences that own their blocks.
+    block_tables_extend, block_tables_release, block_tables_fork and block_tables_compact.
 
-    ``extend``, ``release`` and ``finish`` only enqueue work on the given stream (default: the
-    current one; no host round trip), so a decode loop over them can be captured into a CUDA
-    graph.  ``rows`` is the batch size, ``max_blocks`` the blocks a row may hold (no more than
+    Every method only enqueues work on the given stream (default: the current one; no host
+    round trip), so a decode loop over them can be captured into a CUDA graph.  While rows
+    share blocks (from a ``fork`` on), blocks go back through ``settle``, which counts who uses
+    them; ``release`` and ``finish`` are for rows that own their blocks.  ``rows`` is the batch size, ``max_blocks`` the blocks a row may hold (no more than
     the contexts need: the attention's plan goes by the table's width), ``max_tokens`` the most
     tokens one ``extend`` places; ``order`` is the order in which blocks are handed out (default
     0..NB-1).
@@ -288,6 +292,13 @@ class DeviceBlocks:
         self.step_slots = torch.full((rows,), -1, dtype=torch.int64, device=device)
         ws = max(16, _binding.block_tables_extend_workspace_bytes(rows, max_tokens),
                  _binding.block_tables_release_workspace_bytes(rows))
+        self.refs = torch.zeros(num_blocks, dtype=torch.int32, device=device)
+        self.fork_pairs = torch.full((rows, 2), -1, dtype=torch.int32, device=device)
+        self.compact_pairs = torch.full((num_blocks // 2, 2), -1, dtype=torch.int32, device=device)
+        self.pair_count = torch.zeros(1, dtype=torch.int32, device=device)
+        self._share_ws = torch.empty(_binding.block_tables_share_workspace_bytes(rows, max_blocks, num_blocks) // 4,
+                                     dtype=torch.int32, device=device)
+        self._pairs = self.fork_pairs
         # two pieces: extend's stays zero, release's may hold anything
         self._extend_ws = torch.zeros(16, dtype=torch.uint8, device=device)
         self._release_ws = torch.empty((ws + 3) // 4 * 4, dtype=torch.uint8, device=device)
@@ -323,3 +334,35 @@ class DeviceBlocks:
             end = torch.where(done, self.block_table.shape[1], 0).to(torch.int32)
             self.release(end)
             self.context_lens.masked_fill_(done, 0)
+
+    # ------------------------------------------------------- rows that share blocks
+    def fork(self, parents: Optional[torch.Tensor], held: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Row b takes the sequence of row parents[b] (int32 [rows] on the device; -1: none), sharing its
+        blocks but for a last one that is partly filled (block_tables_fork).  The copies that this asks
+        for are run by ``copy``, on every layer's caches, before anything is written.  Blocks that no row
+        names any more are free; ``held`` (int32 [num_blocks]): blocks that stay in use besides."""
+        from . import _binding
+        self._pairs = self.fork_pairs
+        _binding.block_tables_fork(self.block_table, self.context_lens, parents, self.block_table, self.context_lens,
+                                   self.refs, self.free_list, self.free_count, self.fork_pairs, self.pair_count,
+                                   self.block_size, held=held, workspace=self._share_ws, stream=stream)
+
+    def settle(self, held: Optional[torch.Tensor] = None, stream=None) -> None:
+        """After context_lens got shorter (drafts rejected: verify_drafts writes them there; rows
+        finished: zero) or table entries became -1: blocks that no row needs any more are free, and every
+        row's last block is its own.  ``copy`` as after ``fork``."""
+        self.fork(None, held, stream)
+
+    def compact(self, held: Optional[torch.Tensor] = None, stream=None) -> None:
+        """The blocks in use move to the lowest ids; ``copy`` moves their contents."""
+        from . import _binding
+        self._pairs = self.compact_pairs
+        _binding.block_tables_compact(self.block_table, self.context_lens, self.block_table, self.refs, self.free_list,
+                                      self.free_count, self.compact_pairs, self.pair_count, self.block_size, held=held,
+                                      workspace=self._share_ws, stream=stream)
+
+    def copy(self, k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
+        """The block copies of the last ``fork``, ``settle`` or ``compact``, in one layer's caches
+        ([num_blocks][Hkv][bs][d]; quantised ones as kv_block_copy takes them)."""
+        from . import _binding
+        _binding.kv_block_copy(k_cache, v_cache, self._pairs, stream=stream, count=self.pair_count)

@@ -329,22 +329,76 @@ int pkv_decode_step_kernel_launches(int B, int Hq, int Hkv, int d, int bs, int M
     return n + (decode_fuses_append(plan, dt, dt, Hq, Hkv, &aligned, &aligned) ? 0 : 1);
 }
 
-size_t pkv_paged_attention_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs,
-                                           int MBS, int window, int num_splits) {
+// What pkv_paged_attention and pkv_paged_attention_sinks share.  sinks > 0 comes with a window.
+static size_t attention_workspace(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS, int window, int sinks,
+                                  int num_splits) {
     if (check_decode_sizes(B, Hq, Hkv, d, bs, MBS) != PKV_OK || Tq < 0 || max_q < 0 || window < 0 ||
         num_splits < 0)
         return 0;
     DeviceState *st = nullptr;
     if (device_state(&st) != PKV_OK) return 0;
     if (Tq == B && max_q <= 1)
-        return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, visible_blocks(MBS, bs, window), num_splits,
-                                            st->sm_count);
+        return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, visible_blocks_with_sinks(MBS, bs, window, sinks, 1),
+                                            num_splits, st->sm_count);
     // query rows: cover the tcgen05 and the CUDA-core plans
-    const int vis = visible_blocks_of_rows(MBS, bs, window, max_q);
+    const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, max_q);
     return std::max(plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, window, num_splits,
                                         st->sm_count, true, true).workspace_bytes,
                     plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits,
                                         st->sm_count, false, false).workspace_bytes);
+}
+
+static pkv_status attention(const char *what, float *out, float *lse, const float *q, const void *k_cache, const void *v_cache,
+                            pkv_dtype dt, const int32_t *block_table, const int32_t *context_lens, const int32_t *cu_q, int B,
+                            int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS, int NB, float scale, int window,
+                            int sinks, int num_splits, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    int eb = 0;
+    if (!elem_size(dt, &eb) || !attention_dtype(dt))
+        return fail(PKV_ERR_UNSUPPORTED, "%s: element type %d", what, dt);
+    pkv_status s = check_decode_sizes(B, Hq, Hkv, d, bs, MBS);
+    if (s != PKV_OK) return s;
+    if (NB < 1 || num_splits < 0 || window < 0 || Tq < 0 || max_q < 0 ||
+        static_cast<long long>(Tq) > static_cast<long long>(B) * max_q ||
+        static_cast<long long>(Tq) * Hq > 0x7fffffffll)
+        return fail(PKV_ERR_INVALID_ARG, "%s: NB=%d num_splits=%d window=%d Tq=%d max_q=%d",
+                    what, NB, num_splits, window, Tq, max_q);
+    if (B == 0 || Tq == 0) return PKV_OK;
+    const bool one_per_seq = Tq == B && max_q == 1;
+    if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens || (!one_per_seq && !cu_q))
+        return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (reinterpret_cast<uintptr_t>(q) % 8 != 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: q must be 8-byte aligned", what);
+    DeviceState *st = nullptr;
+    s = device_state(&st);
+    if (s != PKV_OK) return s;
+    const bool caches_aligned = aligned16(k_cache) && aligned16(v_cache);
+    const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
+    const pkv_dtype plan_dt = sinks > 0 ? PKV_F32 : dt;   // with sinks on CUDA cores
+    const DecodePlan plan =
+        one_per_seq ? plan_decode(B, Hq, Hkv, d, bs, vis, NB, plan_dt, num_splits, st->sm_count, caches_aligned, aligned16(q))
+                    : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, plan_dt, window, num_splits, st->sm_count,
+                                          caches_aligned, aligned16(q));
+    if (plan.workspace_bytes > 0 &&
+        (workspace == nullptr || workspace_bytes < plan.workspace_bytes ||
+         reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+        return fail(PKV_ERR_WORKSPACE,
+                    "%s: needs %zu bytes of 16-byte aligned workspace, got %zu",
+                    what, plan.workspace_bytes, workspace == nullptr ? size_t(0) : workspace_bytes);
+    DecodeArgs a{out, lse, q, k_cache, v_cache, block_table, context_lens,
+                 B, Hq, Hkv, d, bs, MBS, NB, scale, workspace, st->err};
+    a.window = window;
+    a.sinks = sinks;
+    a.cu_q = one_per_seq ? nullptr : cu_q;
+    a.rows = one_per_seq ? B : Tq;
+    a.max_q = max_q;
+    const cudaError_t e = launch_decode(a, plan, dt, stream);
+    if (e == cudaSuccess) return PKV_OK;
+    return fail(PKV_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
+size_t pkv_paged_attention_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs,
+                                           int MBS, int window, int num_splits) {
+    return attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, 0, num_splits);
 }
 
 pkv_status pkv_paged_attention(float *out, float *lse, const float *q, const void *k_cache,
@@ -353,47 +407,38 @@ pkv_status pkv_paged_attention(float *out, float *lse, const float *q, const voi
                                int max_q, int Hq, int Hkv, int d, int bs, int MBS, int NB, float scale,
                                int window, int num_splits, void *workspace, size_t workspace_bytes,
                                pkv_stream_t stream) {
-    int eb = 0;
-    if (!elem_size(dt, &eb) || !attention_dtype(dt))
-        return fail(PKV_ERR_UNSUPPORTED, "paged_attention: element type %d", dt);
-    pkv_status s = check_decode_sizes(B, Hq, Hkv, d, bs, MBS);
-    if (s != PKV_OK) return s;
-    if (NB < 1 || num_splits < 0 || window < 0 || Tq < 0 || max_q < 0 ||
-        static_cast<long long>(Tq) > static_cast<long long>(B) * max_q ||
-        static_cast<long long>(Tq) * Hq > 0x7fffffffll)
-        return fail(PKV_ERR_INVALID_ARG, "paged_attention: NB=%d num_splits=%d window=%d Tq=%d max_q=%d",
-                    NB, num_splits, window, Tq, max_q);
-    if (B == 0 || Tq == 0) return PKV_OK;
-    const bool one_per_seq = Tq == B && max_q == 1;
-    if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens || (!one_per_seq && !cu_q))
-        return fail(PKV_ERR_INVALID_ARG, "paged_attention: null pointer");
-    if (reinterpret_cast<uintptr_t>(q) % 8 != 0)
-        return fail(PKV_ERR_INVALID_ARG, "paged_attention: q must be 8-byte aligned");
-    DeviceState *st = nullptr;
-    s = device_state(&st);
-    if (s != PKV_OK) return s;
-    const bool caches_aligned = aligned16(k_cache) && aligned16(v_cache);
-    const DecodePlan plan =
-        one_per_seq
-            ? plan_decode(B, Hq, Hkv, d, bs, visible_blocks(MBS, bs, window), NB, dt, num_splits, st->sm_count,
-                          caches_aligned, aligned16(q))
-            : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs,
-                                  visible_blocks_of_rows(MBS, bs, window, max_q), NB, dt, window,
-                                  num_splits, st->sm_count, caches_aligned, aligned16(q));
-    if (plan.workspace_bytes > 0 &&
-        (workspace == nullptr || workspace_bytes < plan.workspace_bytes ||
-         reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
-        return fail(PKV_ERR_WORKSPACE,
-                    "paged_attention: needs %zu bytes of 16-byte aligned workspace, got %zu",
-                    plan.workspace_bytes, workspace == nullptr ? size_t(0) : workspace_bytes);
-    DecodeArgs a{out, lse, q, k_cache, v_cache, block_table, context_lens,
-                 B, Hq, Hkv, d, bs, MBS, NB, scale, workspace, st->err};
-    a.window = window;
-    a.cu_q = one_per_seq ? nullptr : cu_q;
-    a.rows = one_per_seq ? B : Tq;
-    a.max_q = max_q;
-    cudaError_t e = launch_decode(a, plan, dt, stream);
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "paged_attention launch");
+    return attention("paged_attention", out, lse, q, k_cache, v_cache, dt, block_table, context_lens, cu_q, B, Tq, max_q, Hq,
+                     Hkv, d, bs, MBS, NB, scale, window, 0, num_splits, workspace, workspace_bytes, stream);
+}
+
+// Sinks are needed only where a table can hold a token behind them and before a window; otherwise the call
+// is the plain attention, without a window where a window and the sinks cover every table.
+static void without_needless_sinks(int bs, int MBS, int *window, int *sinks) {
+    if (*window > 0 && static_cast<long long>(*window) + *sinks >= static_cast<long long>(MBS) * bs) *window = 0;
+    if (*window == 0) *sinks = 0;
+}
+
+size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
+                                                 int window, int sinks, int num_splits) {
+    if (window < 0 || sinks < 0 || bs < 1 || MBS < 1) return 0;
+    without_needless_sinks(bs, MBS, &window, &sinks);
+    return attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits);
+}
+
+pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, const void *k_cache, const void *v_cache,
+                                     pkv_dtype dt, const int32_t *block_table, const int32_t *context_lens,
+                                     const int32_t *cu_q, int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
+                                     int NB, float scale, int window, int sinks, int num_splits, void *workspace,
+                                     size_t workspace_bytes, pkv_stream_t stream) {
+    if (sinks < 0 || window < 0)
+        return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: window=%d sinks=%d", window, sinks);
+    if (bs >= 1 && MBS >= 1) {
+        if (static_cast<long long>(MBS) * bs > 0x7fffffffll - bs)
+            return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: MBS=%d bs=%d", MBS, bs);
+        without_needless_sinks(bs, MBS, &window, &sinks);
+    }
+    return attention("paged_attention_sinks", out, lse, q, k_cache, v_cache, dt, block_table, context_lens, cu_q, B, Tq, max_q,
+                     Hq, Hkv, d, bs, MBS, NB, scale, window, sinks, num_splits, workspace, workspace_bytes, stream);
 }
 
 pkv_status pkv_kv_append_fp8(const void *k_new, const void *v_new, pkv_dtype new_dt, uint8_t *k_codes,

@@ -26,6 +26,7 @@ struct DecodeKParams {
     int splits;       // chunks per sequence at most (partial slots per sequence)
     float scale_log2; // scale * log2(e): scores are kept in the base-2 domain
     int window;       // > 0: only the most recent `window` tokens are visible
+    int sinks;        // > 0 (with a window): the first `sinks` tokens stay visible (the SINKS kernels)
     const int32_t *cu_q;   // query rows per sequence [B+1]; nullptr: row b = sequence b
     int rows, max_q;       // with cu_q: query rows of the call, and of a sequence at most
     const float *k_scale, *v_scale;   // FP8 caches: fp32 scale per row [NB][Hkv][bs]
@@ -93,10 +94,32 @@ __device__ __forceinline__ int checked_len(const DecodeKParams &p, int b, int bs
 // Chunks of a sequence cover the pages [cpfirst, cpfirst + cnpages) that any of its query
 // rows sees (the same boundaries for every row, so that chunk partials line up); a row
 // whose own keys miss a chunk writes an empty partial there.
+//
+// With sinks (SINKS) a row also sees the first p.sinks tokens.  The `gap` pages that lie wholly between
+// them and the sequence's first window are left out of the count: every number of the span is of the
+// sequence without those pages (positions less gap * bs), whose pages start at 0, of which the first
+// `spages` hold the sinks, and whose page i is table entry page_entry(i).  A row sees the tokens below
+// p.sinks and those of [lo, len).
 struct SeqSpan {
     int b, len, lo, pfirst, npages;
     int cpfirst, cnpages;
+    int spages, gap;
 };
+
+__device__ __forceinline__ int page_entry(const SeqSpan &s, int page) { return page < s.spages ? page : page + s.gap; }
+
+// lo_seq: the window start of the sequence's first row (positions of the whole sequence).
+__device__ __forceinline__ SeqSpan sinks_span(const DecodeKParams &p, int b, int len, int lo_seq, int bs) {
+    SeqSpan s;
+    s.b = b;
+    s.spages = (p.sinks + bs - 1) / bs;
+    s.gap = max(0, lo_seq / bs - s.spages);
+    s.len = len > 0 ? len - s.gap * bs : 0;
+    s.lo = max(0, len - p.window) - s.gap * bs;
+    s.pfirst = s.cpfirst = 0;
+    s.npages = s.cnpages = (s.len + bs - 1) / bs;
+    return s;
+}
 
 __device__ __forceinline__ SeqSpan span_of(const DecodeKParams &p, int b, int len, int bs) {
     SeqSpan s;
@@ -109,11 +132,15 @@ __device__ __forceinline__ SeqSpan span_of(const DecodeKParams &p, int b, int le
     s.npages = len > 0 ? (len + bs - 1) / bs - s.pfirst : 0;
     s.cpfirst = s.pfirst;
     s.cnpages = s.npages;
+    s.spages = s.gap = 0;
     return s;
 }
 
+template <bool SINKS = false>
 __device__ __forceinline__ SeqSpan seq_span(const DecodeKParams &p, int b, int bs, bool report) {
-    return span_of(p, b, checked_len(p, b, bs, report), bs);
+    const int len = checked_len(p, b, bs, report);
+    if constexpr (SINKS) return sinks_span(p, b, len, max(0, len - p.window), bs);
+    else return span_of(p, b, len, bs);
 }
 
 // Whether a sequence of L tokens may own the query rows [c0, c1).  Every kernel of a call asks
@@ -127,8 +154,9 @@ __device__ __forceinline__ bool query_rows_ok(const DecodeKParams &p, int c0, in
 // Query row r (cu_q != nullptr): its sequence by binary search over cu_q, its position,
 // its span.  An inconsistent cu_q, or a row count above max_q or the sequence length, raises
 // PKV_DEVERR_CU_SEQLENS and the row sees nothing (out = 0, lse = -inf).
+template <bool SINKS = false>
 __device__ __forceinline__ SeqSpan row_span(const DecodeKParams &p, int r, int bs, bool report) {
-    if (p.cu_q == nullptr) return seq_span(p, r, bs, report);
+    if (p.cu_q == nullptr) return seq_span<SINKS>(p, r, bs, report);
     int lo = 0, hi = p.B;   // find b with cu_q[b] <= r < cu_q[b+1]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -142,6 +170,12 @@ __device__ __forceinline__ SeqSpan row_span(const DecodeKParams &p, int r, int b
     if (r < c0 || r >= c1 || !query_rows_ok(p, c0, c1, L)) {
         if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
         return span_of(p, b, 0, bs);
+    }
+    if constexpr (SINKS) {   // all rows of a sequence leave out the same pages, those of its first one
+        const int lo_seq = max(0, L - nq + 1 - p.window);
+        SeqSpan s = sinks_span(p, b, L - nq + (r - c0) + 1, lo_seq, bs);
+        s.cnpages = (L - s.gap * bs + bs - 1) / bs;
+        return s;
     }
     SeqSpan s = span_of(p, b, L - nq + (r - c0) + 1, bs);
     // the sequence's chunk range: from the first row's window start to the last key

@@ -103,6 +103,7 @@ struct DecodeArgs {
     void *workspace;
     unsigned *err;
     int window = 0;                  // > 0: sliding window of this many tokens
+    int sinks = 0;                   // > 0 (with a window): as many first tokens stay visible
     const float *k_scale = nullptr;  // FP8 caches: per-row scales [NB][Hkv][bs]
     const float *v_scale = nullptr;
     const int32_t *cu_q = nullptr;   // query rows per sequence; nullptr: one per sequence
@@ -133,6 +134,12 @@ inline int visible_blocks(int MBS, int bs, int window) {
 inline int visible_blocks_of_rows(int MBS, int bs, int window, int max_q) {
     const long long w = window > 0 ? static_cast<long long>(window) + max_q - 1 : 0;
     return visible_blocks(MBS, bs, static_cast<int>(w < 0x7fffffff ? w : 0x7fffffff));
+}
+
+// The same with the first `sinks` tokens visible too: their blocks beside the windows'.
+inline int visible_blocks_with_sinks(int MBS, int bs, int window, int sinks, int max_q) {
+    const long long n = visible_blocks_of_rows(MBS, bs, window, max_q) + (static_cast<long long>(sinks) + bs - 1) / bs;
+    return static_cast<int>(n < MBS ? n : MBS);
 }
 
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype dt,
@@ -212,6 +219,68 @@ int extend_blocks(int T, int sm_count);                  // thread blocks of an 
 bool release_in_one_block(int B, int MBS);
 cudaError_t launch_block_tables_extend(const ExtendArgs &a, int sm_count, cudaStream_t stream);
 cudaError_t launch_block_tables_release(const ReleaseArgs &a, int sm_count, cudaStream_t stream);
+
+// Block tables with shared blocks (share_tables.cu).
+struct ShareArgs {
+    const int32_t *table;        // [B][MBS]
+    const int32_t *lens;         // [B]
+    const int32_t *parents;      // [B]; nullptr: every row its own
+    const int32_t *held;         // [NB] blocks in use beside the tables; nullptr: none
+    int32_t *table_out;          // may be `table`
+    int32_t *lens_out;           // fork; may be `lens`
+    int32_t *refs, *free_list;   // [NB]
+    int32_t *free_count, *pair_count;
+    int32_t *pairs;              // [B][2] (fork), [NB / 2][2] (compact)
+    int B, MBS, bs, NB;
+    int32_t *first, *place, *fresh, *rows;   // scratch, set by the launch
+    unsigned *err;
+};
+
+size_t share_workspace_bytes(int B, int MBS, int NB);
+// aside: the rows are built in the workspace (table_out replaces the table that other rows still read)
+cudaError_t launch_fork(ShareArgs a, void *workspace, bool aside, cudaStream_t stream);
+cudaError_t launch_compact(ShareArgs a, void *workspace, cudaStream_t stream);
+cudaError_t launch_kv_block_copy_counted(void *k_cache, void *v_cache, int elem_bytes, const int32_t *pairs, int n,
+                                         const int32_t *count, int Hkv, int d, int bs, int NB, int sm_count, unsigned *err,
+                                         cudaStream_t stream);
+
+// ------------------------------------------------------------------- rotary positions
+
+struct RopeArgs {
+    void *q_out;                 // [T][Hq][d]
+    const void *q, *k, *v;       // [T][heads][d], rows of a token at the strides (elements); k, v may be nullptr
+    long long q_stride, k_stride, v_stride;
+    void *k_dst, *v_dst;         // caches (with slots), or k_dst [T][Hkv][d]
+    const int32_t *positions;
+    const unsigned long long *turns;   // [rot / 2]
+    const int64_t *slots;        // nullptr: rows
+    int T, Hq, Hkv, d, rot, bs;
+    long long n_slots;
+    float mscale;
+    bool inverse;
+    int block_tokens;            // set by the launch
+    unsigned *err;
+};
+
+cudaError_t launch_rope(const RopeArgs &a, pkv_dtype dt, pkv_dtype q_out_dt, bool interleaved, int sm_count,
+                        cudaStream_t stream);
+void rope_turns(uint64_t *turns, int rot, double base, int scaling, double factor, double original, double low, double high);
+
+// ------------------------------------------------------------------- drafted tokens
+
+struct VerifyArgs {
+    int32_t *accepted, *tokens;  // [B], [D + B]
+    const void *target, *draft;  // [D + B][V], [D][V] or nullptr, rows at the strides (elements)
+    long long target_stride, draft_stride;
+    const int32_t *draft_tokens, *cu_drafts;
+    const float *uniforms;       // [D + B]
+    const int32_t *lens;
+    int32_t *lens_out;           // nullptr: not wanted
+    int B, D, V;
+    unsigned *err;
+};
+
+cudaError_t launch_verify(const VerifyArgs &a, pkv_dtype dt, int sm_count, cudaStream_t stream);
 
 // ----------------------------------------------------------------- prefill
 

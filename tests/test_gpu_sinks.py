@@ -1,0 +1,186 @@
+"""pkv_paged_attention_sinks on the GPU against the 64-bit definition: every path, windows and first tokens that
+meet, miss and share a block, several rows, NaN in keys that nobody sees, blocks given back between the two."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_165_gb300 as pkv
+from oracle import serve
+from paged_kv_cache_165_gb300 import _build
+from workloads import gen
+
+from helpers import assert_attn_close, assert_bits_equal, dev
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    _build.build()
+    pkv.lib()
+    pkv.get_device_error()
+
+
+def make_case(seed, lens, nqs, hq, hkv, d, bs, dtype, window, sinks):
+    """Caches in which everything that no row of a sequence sees is NaN, and blocks that hold nothing else gone (-1)."""
+    g = gen.generator(seed)
+    per = [gen.blocks_needed(n, bs) for n in lens]
+    nb = sum(per) + 3
+    table = gen.block_table_from_order(gen.permutation(g, nb), per)
+    kc, vc = (gen.randn(g, (nb, hkv, bs, d), dtype) for _ in range(2))
+    q = gen.randn(g, (sum(nqs), hq, d), F32)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(nqs)]), dtype=torch.int32)
+    seen_slots = torch.zeros(nb * bs, dtype=torch.bool)
+    for b, (L, nq) in enumerate(zip(lens, nqs)):
+        for t in range(L):
+            if nq and (window == 0 or t < sinks or t > L - nq - window):
+                seen_slots[int(table[b, t // bs]) * bs + t % bs] = True
+    seen = seen_slots.view(nb, bs)
+    kp, vp = (torch.where(seen[:, None, :, None], x, torch.full_like(x, float("nan"))) for x in (kc, vc))
+    tp = table.clone()
+    for b, L in enumerate(lens):
+        for j in range(per[b]):
+            if not seen[int(table[b, j])].any():
+                tp[b, j] = -1
+    return q, kc, vc, kp, vp, table, tp, torch.tensor(lens, dtype=torch.int32), cu
+
+
+def run(q, kc, vc, table, lens, cu, window, sinks, splits=0, scale=None, max_q=None, bare=False):
+    Tq, Hq, d = q.shape
+    NB, Hkv, bs, _ = kc.shape
+    B = lens.numel()
+    one = bool(((cu[1:] - cu[:-1]) == 1).all())
+    max_q = int((cu[1:] - cu[:-1]).max()) if max_q is None else max_q
+    out, lse = torch.full((Tq, Hq, d), float("nan"), device="cuda"), torch.full((Tq, Hq), float("nan"), device="cuda")
+    n = pkv.paged_attention_sinks_workspace_bytes(B, Tq, max_q, Hq, Hkv, d, bs, table.shape[1], window, sinks, splits)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
+    pkv.paged_attention_sinks(out, dev(q), dev(kc), dev(vc), dev(table), dev(lens), scale or 1 / math.sqrt(d), window, sinks,
+                              cu_q=None if one else dev(cu), max_q=max_q, lse=lse, num_splits=splits, workspace=ws)
+    torch.cuda.synchronize()
+    assert not ws[:1024].any() or ws.numel() <= 16        # the counters are zero again
+    return out, lse
+
+
+PATHS = [
+    (8, 8, 128, BF16, 16),      # one head a KV head
+    (16, 2, 128, BF16, 32),     # eight heads a KV head
+    (12, 4, 64, BF16, 16),
+    (64, 1, 128, BF16, 16),     # many heads a KV head
+    (32, 2, 64, BF16, 32),
+    (32, 2, 256, BF16, 16),
+    (4, 2, 256, BF16, 32),
+    (8, 2, 96, BF16, 24),       # CUDA cores
+    (8, 2, 64, F32, 16),
+    (80, 1, 64, BF16, 16),      # more than 64 heads a KV head
+]
+# q enters the tensor cores in two bf16 parts (2^-16 of it) and so do the weights: a score is off by at most
+# 2^-16 sum |q k| scale, some 1.5e-4 here, an output by that times the spread of V (below 8): 1.2e-3, below the
+# suite's 2e-3.  fp32 on CUDA cores: sums of at most 256 terms and 300 keys, 2e-5.
+ATOL = {BF16: 2e-3, F32: 2e-5}
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs", PATHS)
+@pytest.mark.parametrize("window,sinks", [(1, 1), (5, 4), (16, 16), (33, 3), (100, 17), (64, 70), (1000, 4)])
+def test_one_row_on_every_path(hq, hkv, d, dtype, bs, window, sinks):
+    lens = [1, 15, 16, 17, 100, 257, 700, 33, 2]
+    q, kc, vc, kp, vp, table, tp, clens, cu = make_case(hq + d + window, lens, [1] * len(lens), hq, hkv, d, bs, dtype, window, sinks)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / math.sqrt(d), window, sinks)
+    for splits in (1, 3, 0):
+        out, lse = run(q, kp, vp, tp, clens, cu, window, sinks, splits)
+        assert pkv.get_device_error() == 0
+        assert_attn_close(out, ref, f"splits {splits} out", ATOL[dtype])
+        assert_attn_close(lse, ref_lse, f"splits {splits} lse", ATOL[dtype])
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs", PATHS)
+@pytest.mark.parametrize("window,sinks", [(1, 1), (7, 4), (40, 20), (64, 3)])
+def test_several_rows(hq, hkv, d, dtype, bs, window, sinks):
+    lens = [50, 300, 17, 9, 400, 64, 1]
+    nqs = [4, 1, 0, 9, 33, 5, 1]
+    q, kc, vc, kp, vp, table, tp, clens, cu = make_case(hq * 3 + window, lens, nqs, hq, hkv, d, bs, dtype, window, sinks)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / math.sqrt(d), window, sinks)
+    for splits in (1, 2, 0):
+        out, lse = run(q, kp, vp, tp, clens, cu, window, sinks, splits)
+        assert pkv.get_device_error() == 0
+        assert_attn_close(out, ref, f"splits {splits} out", ATOL[dtype])
+        assert_attn_close(lse, ref_lse, f"splits {splits} lse", ATOL[dtype])
+
+
+def test_many_rows_and_a_long_sequence():
+    # a chunk of new tokens on a cached prefix, and contexts many times the window
+    lens, nqs = [900, 130, 3000], [70, 130, 2]
+    q, kc, vc, kp, vp, table, tp, clens, cu = make_case(1, lens, nqs, 8, 2, 128, 16, BF16, 200, 10)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / math.sqrt(128), 200, 10)
+    out, lse = run(q, kp, vp, tp, clens, cu, 200, 10)
+    assert pkv.get_device_error() == 0
+    assert_attn_close(out, ref, "out")
+    assert_attn_close(lse, ref_lse, "lse")
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 4), (50, 0), (400, 300), (2 ** 31 - 1, 2 ** 31 - 1), (700, 5)])
+@pytest.mark.parametrize("nq", [1, 3])
+def test_what_needs_no_sinks_is_the_plain_attention(window, sinks, nq):
+    lens = [600, 17, 320]
+    q, kc, vc, _, _, table, _, clens, cu = make_case(5, lens, [nq] * 3, 16, 2, 128, 16, BF16, 0, 0)
+    out, lse = run(q, kc, vc, table, clens, cu, window, sinks)
+    plain = window if sinks == 0 else 0
+    want, want_lse = torch.empty_like(out), torch.empty_like(lse)
+    n = pkv.paged_attention_workspace_bytes(3, 3 * nq, nq, 16, 2, 128, 16, table.shape[1], plain)
+    pkv.paged_attention(want, dev(q), dev(kc), dev(vc), dev(table), dev(clens), 1 / math.sqrt(128), cu_q=dev(cu) if nq > 1 else None,
+                        max_q=nq, window=plain, lse=want_lse, workspace=torch.zeros(max(n, 16), dtype=torch.uint8, device="cuda"))
+    assert_bits_equal(out, want)
+    assert_bits_equal(lse, want_lse)
+
+
+def test_empty_sequences_and_bad_lengths_and_blocks():
+    lens = [100, 0, 60]
+    q, kc, vc, _, _, table, _, clens, cu = make_case(8, [100, 16, 60], [1, 1, 1], 8, 2, 64, 16, BF16, 20, 4)
+    out, lse = run(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32), cu, 20, 4)
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all() and torch.isfinite(out[[0, 2]]).all()
+    assert pkv.get_device_error() == 0
+    out, lse = run(q, kc, vc, table, torch.tensor([100, -3, 10000], dtype=torch.int32), cu, 20, 4)
+    assert (out[1:] == 0).all() and (lse[1:] == -math.inf).all()
+    assert pkv.get_device_error() == pkv.DEVERR["len"]
+    bad = table.clone()
+    bad[0, 0], bad[2, 3] = 10 ** 6, -5
+    out, _ = run(q, kc, vc, bad, clens, cu, 20, 4)
+    assert pkv.get_device_error() == pkv.DEVERR["block"] and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype,hq", [(BF16, 16), (F32, 16)])
+def test_rows_that_a_sequence_may_not_own(dtype, hq):
+    lens, nqs = [40, 90, 30], [3, 2, 4]
+    q, kc, vc, _, _, table, _, clens, cu = make_case(8, lens, nqs, hq, 2, 64, 16, dtype, 20, 4)
+    ref, _ = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / 8, 20, 4)
+    out, lse = run(q, kc, vc, table, clens, cu, 20, 4, max_q=3)      # the last sequence's four rows are one too many
+    assert pkv.get_device_error() == pkv.DEVERR["cu_seqlens"]
+    assert_attn_close(out[:5], ref[:5], "served rows")
+    assert (out[5:] == 0).all() and (lse[5:] == -math.inf).all()
+
+
+def test_streams_and_a_graph_over_growing_lengths():
+    lens = [70, 200]
+    q, kc, vc, _, _, table, _, clens, cu = make_case(8, lens, [1, 1], 16, 2, 128, 16, BF16, 32, 5)
+    qd, kd, vd, td, ld = dev(q), dev(kc), dev(vc), dev(table), dev(clens) - 20
+    out, lse = torch.empty_like(qd), torch.empty(2, 16, device="cuda")
+    n = pkv.paged_attention_sinks_workspace_bytes(2, 2, 1, 16, 2, 128, 16, table.shape[1], 32, 5)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
+    step = lambda **kw: pkv.paged_attention_sinks(out, qd, kd, vd, td, ld, 0.1, 32, 5, lse=lse, workspace=ws, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(stream=s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for n in range(20):
+        ld += 1
+        g.replay()
+        torch.cuda.synchronize()
+        ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, ld.cpu(), cu, 0.1, 32, 5)
+        assert_attn_close(out, ref, f"step {n}")
+        assert_attn_close(lse, ref_lse, f"step {n}")
