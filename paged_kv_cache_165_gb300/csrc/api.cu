@@ -337,11 +337,17 @@ static size_t attention_workspace(int B, int Tq, int max_q, int Hq, int Hkv, int
         return 0;
     DeviceState *st = nullptr;
     if (device_state(&st) != PKV_OK) return 0;
-    if (Tq == B && max_q <= 1)
-        return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, visible_blocks_with_sinks(MBS, bs, window, sinks, 1),
-                                            num_splits, st->sm_count);
+    const bool one_per_seq = Tq == B && max_q <= 1;
+    const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
+    if (sinks > 0) {   // whatever the caches' type and alignment
+        const size_t simt = one_per_seq
+                                ? plan_decode(B, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, false, false).workspace_bytes
+                                : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits,
+                                                      st->sm_count, false, false).workspace_bytes;
+        return std::max(simt, plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, num_splits, st->sm_count, true).workspace_bytes);
+    }
+    if (one_per_seq) return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, vis, num_splits, st->sm_count);
     // query rows: cover the tcgen05 and the CUDA-core plans
-    const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, max_q);
     return std::max(plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, window, num_splits,
                                         st->sm_count, true, true).workspace_bytes,
                     plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits,
@@ -373,17 +379,21 @@ static pkv_status attention(const char *what, float *out, float *lse, const floa
     if (s != PKV_OK) return s;
     const bool caches_aligned = aligned16(k_cache) && aligned16(v_cache);
     const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
-    const pkv_dtype plan_dt = sinks > 0 ? PKV_F32 : dt;   // with sinks on CUDA cores
-    const DecodePlan plan =
-        one_per_seq ? plan_decode(B, Hq, Hkv, d, bs, vis, NB, plan_dt, num_splits, st->sm_count, caches_aligned, aligned16(q))
-                    : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, plan_dt, window, num_splits, st->sm_count,
-                                          caches_aligned, aligned16(q));
-    if (plan.workspace_bytes > 0 &&
-        (workspace == nullptr || workspace_bytes < plan.workspace_bytes ||
-         reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    SinksPlan with_sinks{};
+    if (sinks > 0)
+        with_sinks = plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, dt, num_splits, st->sm_count, caches_aligned);
+    DecodePlan plan{};
+    if (!with_sinks.mma) {
+        const pkv_dtype plan_dt = sinks > 0 ? PKV_F32 : dt;   // sinks: the CUDA-core kernel
+        plan = one_per_seq ? plan_decode(B, Hq, Hkv, d, bs, vis, NB, plan_dt, num_splits, st->sm_count, caches_aligned, aligned16(q))
+                           : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, plan_dt, window, num_splits, st->sm_count,
+                                                 caches_aligned, aligned16(q));
+    }
+    const size_t need = with_sinks.mma ? with_sinks.workspace_bytes : plan.workspace_bytes;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
         return fail(PKV_ERR_WORKSPACE,
                     "%s: needs %zu bytes of 16-byte aligned workspace, got %zu",
-                    what, plan.workspace_bytes, workspace == nullptr ? size_t(0) : workspace_bytes);
+                    what, need, workspace == nullptr ? size_t(0) : workspace_bytes);
     DecodeArgs a{out, lse, q, k_cache, v_cache, block_table, context_lens,
                  B, Hq, Hkv, d, bs, MBS, NB, scale, workspace, st->err};
     a.window = window;
@@ -391,7 +401,7 @@ static pkv_status attention(const char *what, float *out, float *lse, const floa
     a.cu_q = one_per_seq ? nullptr : cu_q;
     a.rows = one_per_seq ? B : Tq;
     a.max_q = max_q;
-    const cudaError_t e = launch_decode(a, plan, dt, stream);
+    const cudaError_t e = with_sinks.mma ? launch_decode_sinks(a, with_sinks, stream) : launch_decode(a, plan, dt, stream);
     if (e == cudaSuccess) return PKV_OK;
     return fail(PKV_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }

@@ -1,0 +1,551 @@
+// decode_sinks.cu -- paged attention with a sliding window whose first tokens stay visible (sinks), for bf16
+// caches of d in {64, 128, 256} and bs in {16, 32}; other caches take the CUDA-core kernel of decode.cu.
+//
+// The query row at position p of a sequence sees the keys t <= p with t < S or t > p - W: two runs of tokens.
+// The pages between them are left out of the count (sinks_span in decode_kparams.cuh), so that a chunk of
+// pages is again a run of consecutive numbers and only table entries and masks know of the gap.
+//
+// One CTA per (sequence, KV head, group of (query row, head) pairs, chunk of pages); every warp streams its own
+// pages (round robin) through a private ring of TMA stages and attends all of the CTA's pairs to each, so
+// that a page leaves HBM once per KV head and no warp waits for another.  Eight pairs make a tile of the
+// m16n8k16 bf16 MMAs.
+//
+// Precision: the results are as exact as fp32 arithmetic on the bf16 cache.  q and the softmax weights enter
+// the tensor cores as three bf16 parts (8 + 8 + 8 bits, all of an fp32 number): rows 0-7 of an MMA hold the
+// first parts of a tile's pairs, rows 8-15 the second ones, and another MMA the third parts (of two tiles at
+// once where there are two).  Sums inside the tensor cores are short -- d products of a score, the tokens of one
+// page of an output -- and the running output is kept and rescaled in fp32 registers, since a long chain of
+// tensor-core sums drifts by its truncations.
+//
+// V rows that no pair of the CTA sees may hold NaN or infinities and are cleared in shared memory (their
+// weights are 0, but 0 times NaN is not); K rows need nothing, their scores are replaced.
+#include <algorithm>
+#include <atomic>
+#include <math.h>
+
+#include "common.cuh"
+#include "decode_kparams.cuh"
+#include "internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// x0, x1 as three bf16 parts each, packed in pairs.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
+    const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xffff0000u);
+    split_bf16x2(r0, r1, mid, lo);
+}
+
+template <int D, int BS, int TILES>
+struct SinksCfg {
+    static constexpr int NW = BS * D <= 2048 ? 4 : 2;                // warps
+    static constexpr int ST = D == 64 && BS == 16 ? 4 : 2;           // stages of a warp's ring
+    static constexpr int NT = BS / 8, KT = BS / 16, KS = D / 16;     // score tiles, k-steps of P.V and of q.K
+    static constexpr int PANELS = D / 64;
+    static constexpr int kPageBytes = BS * D * 2, kStageBytes = 2 * kPageBytes;
+    static constexpr bool kQRegs = TILES == 1 && D <= 128;           // q parts in registers, else in shared memory
+    static constexpr int kPairs = TILES * 8;
+    static constexpr int kRingBytes = NW * ST * kStageBytes;
+    static constexpr int kMergeBytes = NW * kPairs * (D + 2) * 4;    // the warps' states, in the ring
+    static constexpr int kOffQ = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kQBytes = kQRegs ? 0 : TILES * KS * 32 * 24;
+    static constexpr int kOffBar = (kOffQ + kQBytes + 15) / 16 * 16;
+    static constexpr int kSmemBytes = 1024 + kOffBar + NW * ST * 8;
+    static constexpr int kBlocks = TILES == 1 && D <= 128 ? 3 : 2;   // per SM (registers)
+};
+
+template <int D, int BS, int TILES>
+__global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, BS, TILES>::kBlocks)
+    decode_sinks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const DecodeKParams p, const int groups) {
+    using C = SinksCfg<D, BS, TILES>;
+    constexpr int NW = C::NW, ST = C::ST, NT = C::NT, KT = C::KT, KS = C::KS, NP = D / 16;
+    constexpr int LT = (TILES + 1) / 2;   // accumulators of third parts (TILES > 1)
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint4 *s_qhm = reinterpret_cast<uint4 *>(smem + C::kOffQ);                        // [TILES][KS][32]
+    uint2 *s_qlo = reinterpret_cast<uint2 *>(smem + C::kOffQ + TILES * KS * 32 * 16);
+
+    pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int group = blockIdx.x % groups, split = blockIdx.x / groups, kvh = blockIdx.y, b = blockIdx.z;
+    const bool report = threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0;
+    const int L = checked_len(p, b, BS, report);
+    int c0 = b, nq = 1;
+    if (p.cu_q != nullptr) {
+        c0 = __ldg(p.cu_q + b);
+        const int c1 = __ldg(p.cu_q + b + 1);
+        nq = c1 - c0;
+        if (!query_rows_ok(p, c0, c1, L)) {   // those of its rows that the call has: out = 0, lse = -inf
+            if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
+            if (blockIdx.x != 0) return;
+            for (int r = max(c0, 0); r < min(c1, p.rows); ++r) {
+                const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
+                for (int i = threadIdx.x; i < p.m * D; i += NW * 32) p.out[at * D + i] = 0.f;
+                if (p.lse != nullptr)
+                    for (int i = threadIdx.x; i < p.m; i += NW * 32) p.lse[at + i] = -INFINITY;
+            }
+            return;
+        }
+    }
+    // this CTA's pairs: slots slot0 .. slot0 + npairs - 1 of (row, head), row = slot / m
+    const int slot0 = group * C::kPairs, npairs = min(C::kPairs, nq * p.m - slot0);
+    if (npairs <= 0) return;
+    auto row_of = [&](int pair) {   // of out, lse, q
+        const int slot = slot0 + pair;
+        return static_cast<size_t>(c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
+    };
+    if (L == 0) {
+        if (split != 0) return;
+        for (int i = threadIdx.x; i < npairs * D; i += NW * 32) p.out[row_of(i / D) * D + i % D] = 0.f;
+        if (p.lse != nullptr)
+            for (int i = threadIdx.x; i < npairs; i += NW * 32) p.lse[row_of(i)] = -INFINITY;
+        return;
+    }
+    // tokens without the gap's pages: the sequence's (chunks), and those that the CTA's rows see, [0, S) and [lo, hi)
+    const int P0 = L - nq;
+    const SeqSpan sp = sinks_span(p, b, L, max(0, P0 + 1 - p.window), BS);
+    const int shift = sp.gap * BS, S = p.sinks;
+    auto lo_of = [&](int pos) { return max(0, pos + 1 - p.window) - shift; };
+    const int pos_first = P0 + slot0 / p.m, pos_last = P0 + (slot0 + npairs - 1) / p.m;
+    const int lo = lo_of(pos_first), hi = pos_last + 1 - shift;
+    const int all_lo = lo_of(pos_last), all_hi = pos_first + 1 - shift;   // [.., ..) seen by every row
+    const int nc = (sp.npages + p.chunk_pages - 1) / p.chunk_pages;
+    const int cp0 = split * p.chunk_pages, cp1 = min(sp.npages, cp0 + p.chunk_pages);
+    if (cp0 >= cp1) return;   // no such chunk
+    const int pg0 = cp0 < sp.spages ? cp0 : max(cp0, lo / BS), pg1 = min(cp1, (hi + BS - 1) / BS);
+
+    if (lane == 0) {
+        for (int s = 0; s < ST; ++s) mbar_init(smem_addr(&bars[warp * ST + s]), 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+    }
+    __syncwarp();
+
+    // this warp's pages: pg0 + warp + NW * k; table entries 32 at a time ahead of the copies
+    const int n_my = pg1 - pg0 > warp ? (pg1 - pg0 - warp + NW - 1) / NW : 0;
+    const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
+    auto entry = [&](int k) { return k < n_my ? __ldg(tbl + page_entry(sp, pg0 + warp + k * NW)) : 0; };
+    int tcur = entry(lane), tnext = entry(32 + lane), tbase = 0;
+    const int oob_row = p.NB * p.Hkv * BS;   // a row past the end: TMA fills zeros
+    auto issue = [&](int k) {   // whole warp (shuffle); lane 0 issues the copies
+        while (k >= tbase + 32) {
+            tcur = tnext;
+            tbase += 32;
+            tnext = entry(tbase + 32 + lane);
+        }
+        const int phys = __shfl_sync(kFull, tcur, k & 31);
+        if (lane == 0) {
+            int row = oob_row;
+            if (phys < 0 || phys >= p.NB) raise_error(p.err, PKV_DEVERR_BLOCK);
+            else row = (phys * p.Hkv + kvh) * BS;
+            const int st = warp * ST + k % ST;
+            const uint32_t bar = smem_addr(&bars[st]), dst = smem_addr(smem + st * C::kStageBytes);
+            mbar_arrive_expect_tx(bar, C::kStageBytes);
+#pragma unroll
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+                tma_load_2d(dst + pn * BS * 128, &tm_k, pn * 64, row, bar);
+                tma_load_2d(dst + C::kPageBytes + pn * BS * 128, &tm_v, pn * 64, row, bar);
+            }
+        }
+    };
+    int issued = min(ST, n_my);
+    for (int k = 0; k < issued; ++k) issue(k);
+
+    // q parts of tile t, k-step kk: pair 8t + g, elements 16 kk + 2 t4 (+ 8)
+    auto q_part = [&](int t, int kk, uint4 &hm, uint2 &l) {
+        float2 x0 = make_float2(0.f, 0.f), x1 = x0;
+        if (8 * t + g < npairs) {
+            const float *q = p.q + row_of(8 * t + g) * D + kk * 16 + 2 * t4;
+            x0 = __ldg(reinterpret_cast<const float2 *>(q));
+            x1 = __ldg(reinterpret_cast<const float2 *>(q + 8));
+        }
+        split3(x0.x, x0.y, hm.x, hm.y, l.x);
+        split3(x1.x, x1.y, hm.z, hm.w, l.y);
+    };
+    uint4 qhm[C::kQRegs ? KS : 1];
+    uint2 qlo[C::kQRegs ? KS : 1];
+    if constexpr (C::kQRegs) {
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) q_part(0, kk, qhm[kk], qlo[kk]);
+    } else {
+        for (int i = warp; i < TILES * KS; i += NW) {
+            uint4 hm;
+            uint2 l;
+            q_part(i / KS, i % KS, hm, l);
+            s_qhm[i * 32 + lane] = hm;
+            s_qlo[i * 32 + lane] = l;
+        }
+        __syncthreads();
+    }
+
+    float o[TILES][NP * 2][2];   // running outputs of pair 8t + g: columns 8n + 2 t4, + 1
+    float m_run[TILES], l_run[TILES];
+    int lo_r[TILES], hi_r[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+        for (int n = 0; n < NP * 2; ++n) o[t][n][0] = o[t][n][1] = 0.f;
+        m_run[t] = -INFINITY;
+        l_run[t] = 0.f;
+        const int pos = P0 + (slot0 + min(8 * t + g, npairs - 1)) / p.m;
+        lo_r[t] = lo_of(pos);
+        hi_r[t] = pos + 1 - shift;
+    }
+
+    int k = 0;
+    for (; k < n_my; ++k) {
+        const int st = warp * ST + k % ST;
+        const bool arrived = mbar_wait_bounded(smem_addr(&bars[st]), (k / ST) & 1);
+        if (!__all_sync(kFull, arrived)) {
+            if (lane == 0) raise_error(p.err, PKV_DEVERR_TIMEOUT);
+            break;
+        }
+        uint8_t *stage = smem + st * C::kStageBytes;
+        const int v0 = (pg0 + warp + k * NW) * BS;   // the page's first token
+        const bool whole = v0 + BS <= all_hi && (v0 >= all_lo || v0 + BS <= S);   // every row sees all of it
+        if (!whole) {
+            for (int i = lane; i < BS * (D / 8); i += 32) {
+                const int r = i / (D / 8), c16 = i % (D / 8), v = v0 + r;
+                if (v >= hi || (v >= S && v < lo))
+                    *reinterpret_cast<uint4 *>(stage + C::kPageBytes + (c16 >> 3) * BS * 128 + r * 128 + (c16 & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();   // before the stage's next copies
+            __syncwarp();
+        }
+        const uint32_t k_s = smem_addr(stage), v_s = k_s + C::kPageBytes;
+        const int mi = lane >> 3, r8 = lane & 7;
+
+        // scores: rows g (first parts) and g + 8 (second) of each tile, third parts of two tiles in another
+        float s[TILES][NT][4], sl[LT][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+#pragma unroll
+            for (int t = 0; t < LT; ++t) sl[t][n][0] = sl[t][n][1] = sl[t][n][2] = sl[t][n][3] = 0.f;
+        }
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+            uint32_t kb[NT][2];
+#pragma unroll
+            for (int np = 0; np < NT / 2; ++np)
+                ldsm_x4(k_s + swz128(BS, np * 16 + (mi >> 1) * 8 + r8, kk * 16 + (mi & 1) * 8), kb[2 * np][0], kb[2 * np][1],
+                        kb[2 * np + 1][0], kb[2 * np + 1][1]);
+            uint2 l[TILES];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                uint4 a;
+                if constexpr (C::kQRegs) {
+                    a = qhm[kk];
+                    l[t] = qlo[kk];
+                } else {
+                    a = s_qhm[(t * KS + kk) * 32 + lane];
+                    l[t] = s_qlo[(t * KS + kk) * 32 + lane];
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[t][n], a.x, a.y, a.z, a.w, kb[n][0], kb[n][1]);
+            }
+#pragma unroll
+            for (int t = 0; t < LT; ++t) {
+                const uint2 u = 2 * t + 1 < TILES ? l[2 * t + 1 < TILES ? 2 * t + 1 : 0] : make_uint2(0u, 0u);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(sl[t][n], l[2 * t].x, u.x, l[2 * t].y, u.y, kb[n][0], kb[n][1]);
+            }
+        }
+
+        // online softmax (base 2) of pair 8t + g; weights in three parts
+        uint32_t phm[TILES][KT][4], plo[TILES][KT][2];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            float sc[NT][2], mx = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[n][e] = (s[t][n][e] + (s[t][n][2 + e] + sl[t / 2][n][(t & 1) * 2 + e])) * p.scale_log2;
+                    if (!whole) {
+                        const int v = v0 + n * 8 + 2 * t4 + e;
+                        if (v >= hi_r[t] || (v >= S && v < lo_r[t])) sc[n][e] = -INFINITY;
+                    }
+                    mx = fmaxf(mx, sc[n][e]);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            const float m_new = fmaxf(m_run[t], mx);
+            const float m_ref = m_new == -INFINITY ? 0.f : m_new;   // a row that has seen no key yet
+            const float alpha = exp2f(m_run[t] - m_ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[n][e] = exp2f(sc[n][e] - m_ref);
+                    sum += sc[n][e];
+                }
+            l_run[t] = l_run[t] * alpha + sum;
+            m_run[t] = m_new;
+            if (__any_sync(kFull, alpha != 1.f)) {   // only when a running maximum moved
+#pragma unroll
+                for (int n = 0; n < NP * 2; ++n) {
+                    o[t][n][0] *= alpha;
+                    o[t][n][1] *= alpha;
+                }
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                split3(sc[2 * kt][0], sc[2 * kt][1], phm[t][kt][0], phm[t][kt][1], plo[t][kt][0]);
+                split3(sc[2 * kt + 1][0], sc[2 * kt + 1][1], phm[t][kt][2], phm[t][kt][3], plo[t][kt][1]);
+            }
+        }
+
+        // O += P V, the page's part summed apart
+#pragma unroll
+        for (int np = 0; np < NP; ++np) {
+            uint32_t vb[KT][4];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+                ldsm_x4_trans(v_s + swz128(BS, kt * 16 + (mi & 1) * 8 + r8, np * 16 + (mi >> 1) * 8), vb[kt][0], vb[kt][1], vb[kt][2],
+                              vb[kt][3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float cl[LT][4];
+#pragma unroll
+                for (int t = 0; t < LT; ++t) {
+                    cl[t][0] = cl[t][1] = cl[t][2] = cl[t][3] = 0.f;
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        constexpr int last = TILES - 1;
+                        const int u = 2 * t + 1 <= last ? 2 * t + 1 : last;
+                        mma_bf16_16816(cl[t], plo[2 * t][kt][0], 2 * t + 1 <= last ? plo[u][kt][0] : 0u, plo[2 * t][kt][1],
+                                       2 * t + 1 <= last ? plo[u][kt][1] : 0u, vb[kt][2 * h], vb[kt][2 * h + 1]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+                        mma_bf16_16816(c, phm[t][kt][0], phm[t][kt][1], phm[t][kt][2], phm[t][kt][3], vb[kt][2 * h],
+                                       vb[kt][2 * h + 1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        o[t][2 * np + h][e] += c[e] + (c[2 + e] + cl[t / 2][(t & 1) * 2 + e]);
+                }
+            }
+        }
+        __syncwarp();
+        if (k + ST < n_my) {
+            issue(k + ST);
+            issued = k + ST + 1;
+        }
+    }
+    if (k < n_my) {
+        // a copy did not arrive in time: wait (bounded) for those in flight, so that none lands later
+        for (int kk = k; kk < issued; ++kk) mbar_wait_bounded(smem_addr(&bars[warp * ST + kk % ST]), (kk / ST) & 1);
+    }
+
+    // ---- the warps' states meet in shared memory (the ring is free now)
+    __syncthreads();
+    float *mw = reinterpret_cast<float *>(smem);   // [NW][pairs]
+    float *lw = mw + NW * C::kPairs;
+    float *ow = lw + NW * C::kPairs;               // [NW][pairs][D]
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        float l = l_run[t];
+        l += __shfl_xor_sync(kFull, l, 1);
+        l += __shfl_xor_sync(kFull, l, 2);
+        const int at = warp * C::kPairs + 8 * t + g;
+        if (t4 == 0) {
+            mw[at] = m_run[t];
+            lw[at] = l;
+        }
+#pragma unroll
+        for (int n = 0; n < NP * 2; ++n)
+            *reinterpret_cast<float2 *>(ow + at * D + n * 8 + 2 * t4) = make_float2(o[t][n][0], o[t][n][1]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < npairs * D; i += NW * 32) {
+        const int pair = i / D, c = i % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * C::kPairs + pair]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float l = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2f(mw[w * C::kPairs + pair] - ref);
+            l += lw[w * C::kPairs + pair] * f;
+            acc += ow[(w * C::kPairs + pair) * D + c] * f;
+        }
+        // no key of this chunk: an empty partial
+        const float out = l == 0.f ? 0.f : acc / l, lse2 = M + log2f(l);
+        const size_t row = row_of(pair);
+        if (nc == 1) {
+            p.out[row * D + c] = out;
+            if (c == 0 && p.lse != nullptr) p.lse[row] = lse2 * kDecLn2;
+        } else {
+            p.ws_o[(row * p.splits + split) * D + c] = out;
+            if (c == 0) p.ws_lse[row * p.splits + split] = lse2;
+        }
+    }
+    if (nc == 1 || p.counters == nullptr) return;
+
+    // ---- the last chunk of these pairs to finish merges them all (an arrival counter, no waiting)
+    __shared__ int s_last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        unsigned *ctr = p.counters + (static_cast<size_t>(b) * p.Hkv + kvh) * groups + group;
+        s_last = atomicAdd(ctr, 1u) + 1 == static_cast<unsigned>(nc);
+        if (s_last) *ctr = 0u;   // every chunk of this call has arrived
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < npairs * (D / 4); i += NW * 32) {
+        const int pair = i / (D / 4), c4 = i % (D / 4) * 4;
+        const size_t row = row_of(pair);
+        const float *ls = p.ws_lse + row * p.splits, *po = p.ws_o + row * p.splits * D + c4;
+        float M = -INFINITY;
+        for (int c = 0; c < nc; ++c) M = fmaxf(M, __ldcg(ls + c));
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < nc; ++c) {
+            const float w = exp2f(__ldcg(ls + c) - M);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(c) * D));
+            l += w;
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
+        }
+        const float il = 1.f / l;
+        float *dst = p.out + row * D + c4;
+        dst[0] = acc.x * il;
+        dst[1] = acc.y * il;
+        dst[2] = acc.z * il;
+        dst[3] = acc.w * il;
+        if (c4 == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kDecLn2;
+    }
+}
+
+template <int D, int BS, int TILES>
+cudaError_t launch(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, int groups, cudaStream_t stream) {
+    using C = SinksCfg<D, BS, TILES>;
+    static std::atomic<unsigned long long> ready{0};   // one bit a device: shared memory opted in
+    auto kernel = decode_sinks_kernel<D, BS, TILES>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit);
+    }
+    kernel<<<dim3(static_cast<unsigned>(kp.splits) * groups, kp.Hkv, kp.B), C::NW * 32, C::kSmemBytes, stream>>>(tk, tv, kp, groups);
+    return cudaGetLastError();
+}
+
+template <int D, int BS>
+cudaError_t launch_tiles(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, const SinksPlan &plan,
+                         cudaStream_t stream) {
+    if (plan.tiles == 1) return launch<D, BS, 1>(kp, tk, tv, plan.groups, stream);
+    if (plan.tiles == 2) return launch<D, BS, 2>(kp, tk, tv, plan.groups, stream);
+    if constexpr (D <= 128) return launch<D, BS, 4>(kp, tk, tv, plan.groups, stream);
+    else return cudaErrorInvalidValue;
+}
+
+constexpr int kFusedMergeMaxChunks = 8;
+
+}  // namespace
+
+SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs, int pages, int NB, pkv_dtype dt, int num_splits,
+                     int sm_count, bool aligned) {
+    SinksPlan plan{};
+    if (dt != PKV_BF16 || (d != 64 && d != 128 && d != 256) || (bs != 16 && bs != 32) || !aligned ||
+        static_cast<long long>(NB + 1) * Hkv * bs >= (1ll << 31))
+        return plan;
+    const long long pairs = static_cast<long long>(max_q) * (Hq / Hkv), tiles = (pairs + 7) / 8;
+    plan.tiles = tiles == 1 ? 1 : tiles == 2 || d == 256 ? 2 : 4;
+    const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
+    // chunks: eight CTAs an SM, none shorter than 16 pages
+    const long long units = static_cast<long long>(B) * Hkv * groups;
+    int chunk = pages;
+    if (num_splits > 1) chunk = (pages + num_splits - 1) / num_splits;
+    else if (num_splits == 0)
+        while (chunk > 16 && units * ((pages + chunk - 1) / chunk) < 8ll * std::max(sm_count, 1)) chunk = (chunk + 1) / 2;
+    chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
+    const int splits = (pages + chunk - 1) / chunk;
+    if (groups * splits > 0x7fffffffll) return plan;
+    plan.mma = true;
+    plan.groups = static_cast<int>(groups);
+    plan.chunk_pages = chunk;
+    plan.splits = splits;
+    plan.fused_merge = splits > 1 && splits <= kFusedMergeMaxChunks &&
+                       units <= static_cast<long long>(PKV_DECODE_COUNTER_BYTES / sizeof(unsigned));
+    plan.workspace_bytes =
+        splits > 1 ? PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(rows) * Hq * splits * (static_cast<size_t>(d) + 1) * sizeof(float)
+                   : 0;
+    return plan;
+}
+
+cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cudaStream_t stream) {
+    DecodeKParams kp{};
+    kp.out = a.out;
+    kp.lse = a.lse;
+    kp.q = a.q;
+    kp.block_table = a.block_table;
+    kp.context_lens = a.context_lens;
+    kp.err = a.err;
+    kp.B = a.B;
+    kp.Hq = a.Hq;
+    kp.Hkv = a.Hkv;
+    kp.m = a.Hq / a.Hkv;
+    kp.MBS = a.MBS;
+    kp.NB = a.NB;
+    kp.chunk_pages = plan.chunk_pages;
+    kp.splits = plan.splits;
+    kp.scale_log2 = a.scale * kDecLog2e;
+    kp.window = a.window;
+    kp.sinks = a.sinks;
+    kp.cu_q = a.cu_q;
+    kp.rows = a.rows;
+    kp.max_q = a.max_q;
+    if (plan.splits > 1) {
+        uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+        kp.counters = plan.fused_merge ? reinterpret_cast<unsigned *>(ws) : nullptr;
+        kp.ws_o = reinterpret_cast<float *>(ws + PKV_DECODE_COUNTER_BYTES);
+        kp.ws_lse = kp.ws_o + static_cast<size_t>(a.rows) * a.Hq * plan.splits * a.d;
+    }
+    CUtensorMap tk, tv;
+    const uint64_t dims[2] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.NB) * a.Hkv * a.bs};
+    const uint64_t strides[1] = {static_cast<uint64_t>(a.d) * 2};
+    const uint32_t box[2] = {64, static_cast<uint32_t>(a.bs)};
+    if (!encode_map_bf16(&tk, a.k_cache, 2, dims, strides, box) || !encode_map_bf16(&tv, a.v_cache, 2, dims, strides, box))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (a.bs == 16)
+        e = a.d == 64    ? launch_tiles<64, 16>(kp, tk, tv, plan, stream)
+            : a.d == 128 ? launch_tiles<128, 16>(kp, tk, tv, plan, stream)
+                         : launch_tiles<256, 16>(kp, tk, tv, plan, stream);
+    else
+        e = a.d == 64    ? launch_tiles<64, 32>(kp, tk, tv, plan, stream)
+            : a.d == 128 ? launch_tiles<128, 32>(kp, tk, tv, plan, stream)
+                         : launch_tiles<256, 32>(kp, tk, tv, plan, stream);
+    if (e != cudaSuccess || plan.splits == 1 || plan.fused_merge) return e;
+    return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(a.rows * a.Hq), stream);
+}
+
+}  // namespace pkv

@@ -145,6 +145,20 @@ inline int visible_blocks_with_sinks(int MBS, int bs, int window, int sinks, int
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype dt,
                           cudaStream_t stream);
 
+// Windows with first tokens that stay visible (decode_sinks.cu); mma false: the CUDA-core kernel.
+struct SinksPlan {
+    bool mma;
+    int tiles, groups;   // tiles of 8 (query row, head) pairs of a block, blocks for the pairs of a KV head
+    int splits, chunk_pages;
+    bool fused_merge;
+    size_t workspace_bytes;
+};
+
+// pages: the blocks any row can see; aligned: caches on 16-byte boundaries (q on 8).
+SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs, int pages, int NB, pkv_dtype dt, int num_splits,
+                     int sm_count, bool aligned);
+cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cudaStream_t stream);
+
 // ------------------------------------------------- attention over a 4-bit cache
 
 struct Q4Plan {
