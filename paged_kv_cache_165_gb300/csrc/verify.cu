@@ -29,7 +29,7 @@ namespace {
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr u64 kMost = 1ull << 63;   // sums of more than 32 (no distribution) stay there
 
@@ -43,11 +43,17 @@ __device__ __forceinline__ unsigned bits_of(__nv_bfloat16 x) {
     return static_cast<unsigned>(__bfloat16_as_ushort(x)) << 16;
 }
 
-// A probability in units of 2^-58: 0 for a negative one or NaN, 2^58 from 1 on.
+// A probability in units of 2^-58: 0 for a negative one or NaN, 2^58 from 1 on.  Below 1 it is
+// 2^(e - 127) (1 + m 2^-23), e <= 126: (2^23 + m) 2^34 shifted right by 126 - e, whose upper word is
+// (2^23 + m) 2^2 and whose lower word is 0; PTX shifts by 32 and more give 0.
 __device__ __forceinline__ u64 units(unsigned b) {
     if (b >= 0x3f800000u) return b <= 0x7f800000u ? 1ull << 58 : 0ull;
-    const unsigned e = b >> 23;                            // below 1: 2^(e - 127) (1 + m 2^-23), e <= 126
-    return (static_cast<u64>((b & 0x7fffffu) | 0x800000u) << 34) >> min(126u - e, 63u);
+    const unsigned e = b >> 23, top = ((b & 0x7fffffu) | 0x800000u) << 2;
+    unsigned hi, lo, lo2;
+    asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(top), "r"(126u - e));
+    asm("shl.b32 %0, %1, %2;" : "=r"(lo) : "r"(top), "r"(e - 94u));    // less than 32 to the right
+    asm("shr.u32 %0, %1, %2;" : "=r"(lo2) : "r"(top), "r"(94u - e));   // more
+    return static_cast<u64>(hi) << 32 | (lo | lo2);
 }
 
 // u in [0, 1) in units of 2^-64 (rounded down).
@@ -75,36 +81,47 @@ __device__ __forceinline__ u64 rest_of(const Row<T> &r, T p, T q, int v) {
     return v == r.not_this || x <= y ? 0 : x - y;
 }
 
+// Elements v .. v + N - 1 of the row (those from hi on count as 0): their sum, in units.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Piece { T x[N]; };
+
+template <typename T, int N>
+__device__ __forceinline__ void load_pieces(const Row<T> &r, int v, int hi, Piece<T, N> &p, Piece<T, N> &q) {
+    if (v + N <= hi) {
+        p = *reinterpret_cast<const Piece<T, N> *>(r.p + v);
+        if (r.q != nullptr) q = *reinterpret_cast<const Piece<T, N> *>(r.q + v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            p.x[j] = v + j < hi ? r.p[v + j] : T(0.f);
+            q.x[j] = v + j < hi && r.q != nullptr ? r.q[v + j] : T(0.f);
+        }
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ u64 sum_piece(const Row<T> &r, int v, const Piece<T, N> &p, const Piece<T, N> &q) {
+    u64 s = 0;      // at most 8 elements of 2^58
+#pragma unroll
+    for (int j = 0; j < N; ++j) s += rest_of(r, p.x[j], q.x[j], v + j);
+    return s;
+}
+
+// Pieces a lane loads before it uses the first; a step of a warp covers 32 * N * kAhead elements.
+template <int N>
+constexpr int ahead() { return N == 1 ? 8 : 2; }
+
 // The sum over elements [lo, hi) of the row by one warp; N elements a lane side by side.
 template <typename T, int N>
 __device__ __forceinline__ u64 warp_sum(const Row<T> &r, int lo, int hi, int lane) {
-    struct alignas(sizeof(T) * N) Piece { T x[N]; };
+    constexpr int kAhead = ahead<N>(), span = 32 * N;
     u64 sum = 0;
-    constexpr int kAhead = 4;
-    const int span = 32 * N;
-    for (int v0 = lo; v0 < hi; v0 += kAhead * span) {
-        Piece p[kAhead], q[kAhead];
+    for (int v0 = lo + lane * N; v0 - lane * N < hi; v0 += kAhead * span) {
+        Piece<T, N> p[kAhead], q[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int v = v0 + i * span + lane * N;
-            if (v + N <= hi) {
-                p[i] = *reinterpret_cast<const Piece *>(r.p + v);
-                if (r.q != nullptr) q[i] = *reinterpret_cast<const Piece *>(r.q + v);
-            } else {
+        for (int i = 0; i < kAhead; ++i) load_pieces<T, N>(r, v0 + i * span, hi, p[i], q[i]);
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    p[i].x[j] = v + j < hi ? r.p[v + j] : T(0.f);
-                    q[i].x[j] = v + j < hi && r.q != nullptr ? r.q[v + j] : T(0.f);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            u64 s = 0;      // at most 8 elements of 2^58
-#pragma unroll
-            for (int j = 0; j < N; ++j) s += rest_of(r, p[i].x[j], q[i].x[j], v0 + i * span + lane * N + j);
-            sum = capped(sum, s);
-        }
+        for (int i = 0; i < kAhead; ++i) sum = capped(sum, sum_piece<T, N>(r, v0 + i * span, p[i], q[i]));
     }
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) sum = capped(sum, __shfl_xor_sync(kFull, sum, sh));
@@ -112,21 +129,39 @@ __device__ __forceinline__ u64 warp_sum(const Row<T> &r, int lo, int hi, int lan
 }
 
 // The lowest v of [lo, hi) whose sum from lo on exceeds `left` (which the whole run's does).
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ int find(const Row<T> &r, int lo, int hi, u64 left, int lane) {
+    constexpr int kAhead = ahead<N>(), span = 32 * N;
     u64 before = 0;
-    for (int v0 = lo; v0 < hi; v0 += 32) {
-        const int v = v0 + lane;
-        u64 s = 0;
-        if (v < hi) s = rest_of(r, r.p[v], r.q != nullptr ? r.q[v] : T(0.f), v);
+    for (int w0 = lo; w0 < hi; w0 += kAhead * span) {
+        Piece<T, N> p[kAhead], q[kAhead];
 #pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-            const u64 y = __shfl_up_sync(kFull, s, sh);
-            if (lane >= sh) s = capped(s, y);
+        for (int i = 0; i < kAhead; ++i) load_pieces<T, N>(r, w0 + lane * N + i * span, hi, p[i], q[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int v = w0 + lane * N + i * span;
+            const u64 mine = sum_piece<T, N>(r, v, p[i], q[i]);
+            u64 s = mine;
+#pragma unroll
+            for (int sh = 1; sh < 32; sh <<= 1) {
+                const u64 y = __shfl_up_sync(kFull, s, sh);
+                if (lane >= sh) s = capped(s, y);
+            }
+            const unsigned over = __ballot_sync(kFull, capped(before, s) > left);
+            if (over != 0) {
+                const int first = __ffs(over) - 1;
+                const u64 others = __shfl_up_sync(kFull, s, 1);
+                u64 run = lane > 0 ? capped(before, others) : before;
+                int at = v + N - 1;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    run = capped(run, rest_of(r, p[i].x[j], q[i].x[j], v + j));
+                    if (run > left) at = min(at, v + j);
+                }
+                return __shfl_sync(kFull, at, first);
+            }
+            before = capped(before, __shfl_sync(kFull, s, 31));
         }
-        const unsigned over = __ballot_sync(kFull, capped(before, s) > left);
-        if (over != 0) return v0 + __ffs(over) - 1;
-        before = capped(before, __shfl_sync(kFull, s, 31));
     }
     return hi - 1;
 }
@@ -141,7 +176,7 @@ __device__ __forceinline__ bool accepts(const VerifyArgs &a, long long target_ro
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
     __shared__ u64 s_warp[kWarps], s_block;   // sums of the warps' runs; of the block's
     __shared__ int s_accepted;
     cg::cluster_group cluster = cg::this_cluster();
@@ -215,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
             for (int w = 0; w < warp; ++w) before = capped(before, s_warp[w]);
             if (before <= border && capped(before, sum) > border) {
                 mine = true;
-                token = find(r, lo, hi, border - before, lane);
+                token = find<T, N>(r, lo, hi, border - before, lane);
             }
             break;
         }
