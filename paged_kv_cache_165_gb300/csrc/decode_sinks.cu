@@ -39,6 +39,13 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_
     split_bf16x2(r0, r1, mid, lo);
 }
 
+// D = A B (+ C) of m16n8k16 with the accumulator apart, so that a zero one costs no moves.
+__device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <int D, int BS, int TILES>
 struct SinksCfg {
     static constexpr int NW = BS * D <= 2048 ? 4 : 2;                // warps
@@ -46,90 +53,51 @@ struct SinksCfg {
     static constexpr int NT = BS / 8, KT = BS / 16, KS = D / 16;     // score tiles, k-steps of P.V and of q.K
     static constexpr int PANELS = D / 64;
     static constexpr int kPageBytes = BS * D * 2, kStageBytes = 2 * kPageBytes;
-    static constexpr bool kQRegs = TILES == 1 && D <= 128;           // q parts in registers, else in shared memory
+    static constexpr bool kQShared = TILES > 1 || D == 256;          // q parts in shared memory (else in registers)
     static constexpr int kPairs = TILES * 8;
     static constexpr int kRingBytes = NW * ST * kStageBytes;
     static constexpr int kMergeBytes = NW * kPairs * (D + 2) * 4;    // the warps' states, in the ring
     static constexpr int kOffQ = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-    static constexpr int kQBytes = kQRegs ? 0 : TILES * KS * 32 * 24;
+    static constexpr int kQBytes = kQShared ? TILES * KS * 32 * 24 : 0;
     static constexpr int kOffBar = (kOffQ + kQBytes + 15) / 16 * 16;
     static constexpr int kSmemBytes = 1024 + kOffBar + NW * ST * 8;
     static constexpr int kBlocks = TILES == 1 && D <= 128 ? 3 : 2;   // per SM (registers)
 };
 
-template <int D, int BS, int TILES>
-__global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, BS, TILES>::kBlocks)
-    decode_sinks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const DecodeKParams p, const int groups) {
-    using C = SinksCfg<D, BS, TILES>;
+// What a CTA attends: pairs slot0 .. slot0 + npairs - 1 of sequence b's (row, head) slots for one KV head, over
+// pages pg0 .. pg1 - 1 (numbered without the gap).  Its rows see the tokens [0, S) and [lo, hi) between them,
+// and each of them all of [.., S) and [all_lo, all_hi).
+struct Stream {
+    uint8_t *smem;
+    uint64_t *bars;
+    int b, kvh, slot0, npairs, c0, P0;
+    int pg0, pg1, lo, hi, all_lo, all_hi;
+    SeqSpan sp;
+};
+
+// One warp's pages for T tiles of pairs (MAXT: of the CTA's layout); leaves its states (running maximum and sum in
+// base 2, unnormalised outputs) in shared memory.
+template <int D, int BS, int MAXT, int T>
+__device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const DecodeKParams &p,
+                                             const Stream &w) {
+    using C = SinksCfg<D, BS, MAXT>;
     constexpr int NW = C::NW, ST = C::ST, NT = C::NT, KT = C::KT, KS = C::KS, NP = D / 16;
-    constexpr int LT = (TILES + 1) / 2;   // accumulators of third parts (TILES > 1)
-
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint4 *s_qhm = reinterpret_cast<uint4 *>(smem + C::kOffQ);                        // [TILES][KS][32]
-    uint2 *s_qlo = reinterpret_cast<uint2 *>(smem + C::kOffQ + TILES * KS * 32 * 16);
-
-    pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
+    constexpr int LT = T / 2;                                // accumulators of third parts, two tiles each
+    constexpr bool kQRegs = T == 1 && D <= 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int group = blockIdx.x % groups, split = blockIdx.x / groups, kvh = blockIdx.y, b = blockIdx.z;
-    const bool report = threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0;
-    const int L = checked_len(p, b, BS, report);
-    int c0 = b, nq = 1;
-    if (p.cu_q != nullptr) {
-        c0 = __ldg(p.cu_q + b);
-        const int c1 = __ldg(p.cu_q + b + 1);
-        nq = c1 - c0;
-        if (!query_rows_ok(p, c0, c1, L)) {   // those of its rows that the call has: out = 0, lse = -inf
-            if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
-            if (blockIdx.x != 0) return;
-            for (int r = max(c0, 0); r < min(c1, p.rows); ++r) {
-                const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
-                for (int i = threadIdx.x; i < p.m * D; i += NW * 32) p.out[at * D + i] = 0.f;
-                if (p.lse != nullptr)
-                    for (int i = threadIdx.x; i < p.m; i += NW * 32) p.lse[at + i] = -INFINITY;
-            }
-            return;
-        }
-    }
-    // this CTA's pairs: slots slot0 .. slot0 + npairs - 1 of (row, head), row = slot / m
-    const int slot0 = group * C::kPairs, npairs = min(C::kPairs, nq * p.m - slot0);
-    if (npairs <= 0) return;
-    auto row_of = [&](int pair) {   // of out, lse, q
-        const int slot = slot0 + pair;
-        return static_cast<size_t>(c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
-    };
-    if (L == 0) {
-        if (split != 0) return;
-        for (int i = threadIdx.x; i < npairs * D; i += NW * 32) p.out[row_of(i / D) * D + i % D] = 0.f;
-        if (p.lse != nullptr)
-            for (int i = threadIdx.x; i < npairs; i += NW * 32) p.lse[row_of(i)] = -INFINITY;
-        return;
-    }
-    // tokens without the gap's pages: the sequence's (chunks), and those that the CTA's rows see, [0, S) and [lo, hi)
-    const int P0 = L - nq;
-    const SeqSpan sp = sinks_span(p, b, L, max(0, P0 + 1 - p.window), BS);
-    const int shift = sp.gap * BS, S = p.sinks;
+    const int b = w.b, kvh = w.kvh, slot0 = w.slot0, npairs = w.npairs, P0 = w.P0, pg0 = w.pg0, pg1 = w.pg1;
+    const int lo = w.lo, hi = w.hi, all_lo = w.all_lo, all_hi = w.all_hi, S = p.sinks;
+    const SeqSpan sp = w.sp;
+    const int shift = sp.gap * BS;
+    uint8_t *smem = w.smem;
+    uint64_t *bars = w.bars;
+    uint4 *s_qhm = reinterpret_cast<uint4 *>(smem + C::kOffQ);                      // [tiles][KS][32]
+    uint2 *s_qlo = reinterpret_cast<uint2 *>(smem + C::kOffQ + MAXT * KS * 32 * 16);
     auto lo_of = [&](int pos) { return max(0, pos + 1 - p.window) - shift; };
-    const int pos_first = P0 + slot0 / p.m, pos_last = P0 + (slot0 + npairs - 1) / p.m;
-    const int lo = lo_of(pos_first), hi = pos_last + 1 - shift;
-    const int all_lo = lo_of(pos_last), all_hi = pos_first + 1 - shift;   // [.., ..) seen by every row
-    const int nc = (sp.npages + p.chunk_pages - 1) / p.chunk_pages;
-    const int cp0 = split * p.chunk_pages, cp1 = min(sp.npages, cp0 + p.chunk_pages);
-    if (cp0 >= cp1) return;   // no such chunk
-    const int pg0 = cp0 < sp.spages ? cp0 : max(cp0, lo / BS), pg1 = min(cp1, (hi + BS - 1) / BS);
-
-    if (lane == 0) {
-        for (int s = 0; s < ST; ++s) mbar_init(smem_addr(&bars[warp * ST + s]), 1);
-        fence_barrier_init();
-    }
-    if (threadIdx.x == 0) {
-        tma_prefetch_map(&tm_k);
-        tma_prefetch_map(&tm_v);
-    }
-    __syncwarp();
-
+    auto row_of = [&](int pair) {
+        const int slot = slot0 + pair;
+        return static_cast<size_t>(w.c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
+    };
     // this warp's pages: pg0 + warp + NW * k; table entries 32 at a time ahead of the copies
     const int n_my = pg1 - pg0 > warp ? (pg1 - pg0 - warp + NW - 1) / NW : 0;
     const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
@@ -171,13 +139,13 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         split3(x0.x, x0.y, hm.x, hm.y, l.x);
         split3(x1.x, x1.y, hm.z, hm.w, l.y);
     };
-    uint4 qhm[C::kQRegs ? KS : 1];
-    uint2 qlo[C::kQRegs ? KS : 1];
-    if constexpr (C::kQRegs) {
+    uint4 qhm[kQRegs ? KS : 1];
+    uint2 qlo[kQRegs ? KS : 1];
+    if constexpr (kQRegs) {
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) q_part(0, kk, qhm[kk], qlo[kk]);
     } else {
-        for (int i = warp; i < TILES * KS; i += NW) {
+        for (int i = warp; i < T * KS; i += NW) {
             uint4 hm;
             uint2 l;
             q_part(i / KS, i % KS, hm, l);
@@ -187,13 +155,13 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         __syncthreads();
     }
 
-    float o[TILES][NP * 2][2];   // running outputs of pair 8t + g: columns 8n + 2 t4, + 1
-    float m_run[TILES], l_run[TILES];
-    int lo_r[TILES], hi_r[TILES];
+    float2 o[T][NP * 2];   // running outputs of pair 8t + g: columns 8n + 2 t4, + 1
+    float m_run[T], l_run[T];
+    int lo_r[T], hi_r[T];
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
+    for (int t = 0; t < T; ++t) {
 #pragma unroll
-        for (int n = 0; n < NP * 2; ++n) o[t][n][0] = o[t][n][1] = 0.f;
+        for (int n = 0; n < NP * 2; ++n) o[t][n] = make_float2(0.f, 0.f);
         m_run[t] = -INFINITY;
         l_run[t] = 0.f;
         const int pos = P0 + (slot0 + min(8 * t + g, npairs - 1)) / p.m;
@@ -225,15 +193,9 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         const uint32_t k_s = smem_addr(stage), v_s = k_s + C::kPageBytes;
         const int mi = lane >> 3, r8 = lane & 7;
 
-        // scores: rows g (first parts) and g + 8 (second) of each tile, third parts of two tiles in another
-        float s[TILES][NT][4], sl[LT][NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
-#pragma unroll
-            for (int t = 0; t < LT; ++t) sl[t][n][0] = sl[t][n][1] = sl[t][n][2] = sl[t][n][3] = 0.f;
-        }
+        // scores: rows g (first parts) and g + 8 (second) of each tile; third parts of two tiles in another
+        // accumulator, of a single one onto its own
+        float s[T][NT][4], sl[LT > 0 ? LT : 1][NT][4];
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
             uint32_t kb[NT][2];
@@ -241,11 +203,11 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
             for (int np = 0; np < NT / 2; ++np)
                 ldsm_x4(k_s + swz128(BS, np * 16 + (mi >> 1) * 8 + r8, kk * 16 + (mi & 1) * 8), kb[2 * np][0], kb[2 * np][1],
                         kb[2 * np + 1][0], kb[2 * np + 1][1]);
-            uint2 l[TILES];
+            uint2 l[T];
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) {
+            for (int t = 0; t < T; ++t) {
                 uint4 a;
-                if constexpr (C::kQRegs) {
+                if constexpr (kQRegs) {
                     a = qhm[kk];
                     l[t] = qlo[kk];
                 } else {
@@ -253,26 +215,37 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
                     l[t] = s_qlo[(t * KS + kk) * 32 + lane];
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[t][n], a.x, a.y, a.z, a.w, kb[n][0], kb[n][1]);
+                for (int n = 0; n < NT; ++n) {
+                    if (kk == 0) mma_new(s[t][n], a.x, a.y, a.z, a.w, kb[n][0], kb[n][1]);
+                    else mma_bf16_16816(s[t][n], a.x, a.y, a.z, a.w, kb[n][0], kb[n][1]);
+                }
             }
+            if constexpr (T == 1) {
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {
-                const uint2 u = 2 * t + 1 < TILES ? l[2 * t + 1 < TILES ? 2 * t + 1 : 0] : make_uint2(0u, 0u);
+                for (int n = 0; n < NT; ++n) mma_bf16_16816(s[0][n], l[0].x, 0u, l[0].y, 0u, kb[n][0], kb[n][1]);
+            } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16_16816(sl[t][n], l[2 * t].x, u.x, l[2 * t].y, u.y, kb[n][0], kb[n][1]);
+                for (int t = 0; t < LT; ++t)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (kk == 0) mma_new(sl[t][n], l[2 * t].x, l[2 * t + 1].x, l[2 * t].y, l[2 * t + 1].y, kb[n][0], kb[n][1]);
+                        else mma_bf16_16816(sl[t][n], l[2 * t].x, l[2 * t + 1].x, l[2 * t].y, l[2 * t + 1].y, kb[n][0], kb[n][1]);
+                    }
             }
         }
 
         // online softmax (base 2) of pair 8t + g; weights in three parts
-        uint32_t phm[TILES][KT][4], plo[TILES][KT][2];
+        uint32_t phm[T][KT][4], plo[T][KT][2];
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
+        for (int t = 0; t < T; ++t) {
             float sc[NT][2], mx = -INFINITY;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sc[n][e] = (s[t][n][e] + (s[t][n][2 + e] + sl[t / 2][n][(t & 1) * 2 + e])) * p.scale_log2;
+                    float x = s[t][n][2 + e];
+                    if constexpr (T > 1) x += sl[t / 2][n][(t & 1) * 2 + e];
+                    sc[n][e] = (s[t][n][e] + x) * p.scale_log2;
                     if (!whole) {
                         const int v = v0 + n * 8 + 2 * t4 + e;
                         if (v >= hi_r[t] || (v >= S && v < lo_r[t])) sc[n][e] = -INFINITY;
@@ -283,13 +256,13 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
             const float m_new = fmaxf(m_run[t], mx);
             const float m_ref = m_new == -INFINITY ? 0.f : m_new;   // a row that has seen no key yet
-            const float alpha = exp2f(m_run[t] - m_ref);
+            const float alpha = ex2_approx(m_run[t] - m_ref);
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sc[n][e] = exp2f(sc[n][e] - m_ref);
+                    sc[n][e] = ex2_approx(sc[n][e] - m_ref);
                     sum += sc[n][e];
                 }
             l_run[t] = l_run[t] * alpha + sum;
@@ -297,8 +270,8 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
             if (__any_sync(kFull, alpha != 1.f)) {   // only when a running maximum moved
 #pragma unroll
                 for (int n = 0; n < NP * 2; ++n) {
-                    o[t][n][0] *= alpha;
-                    o[t][n][1] *= alpha;
+                    o[t][n].x *= alpha;
+                    o[t][n].y *= alpha;
                 }
             }
 #pragma unroll
@@ -318,28 +291,30 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
                               vb[kt][3]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float cl[LT][4];
+                float c[T][4], cl[LT > 0 ? LT : 1][4];
 #pragma unroll
-                for (int t = 0; t < LT; ++t) {
-                    cl[t][0] = cl[t][1] = cl[t][2] = cl[t][3] = 0.f;
+                for (int kt = 0; kt < KT; ++kt) {
+                    const uint32_t b0 = vb[kt][2 * h], b1 = vb[kt][2 * h + 1];
 #pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        constexpr int last = TILES - 1;
-                        const int u = 2 * t + 1 <= last ? 2 * t + 1 : last;
-                        mma_bf16_16816(cl[t], plo[2 * t][kt][0], 2 * t + 1 <= last ? plo[u][kt][0] : 0u, plo[2 * t][kt][1],
-                                       2 * t + 1 <= last ? plo[u][kt][1] : 0u, vb[kt][2 * h], vb[kt][2 * h + 1]);
+                    for (int t = 0; t < T; ++t) {
+                        if (kt == 0) mma_new(c[t], phm[t][kt][0], phm[t][kt][1], phm[t][kt][2], phm[t][kt][3], b0, b1);
+                        else mma_bf16_16816(c[t], phm[t][kt][0], phm[t][kt][1], phm[t][kt][2], phm[t][kt][3], b0, b1);
+                    }
+                    if constexpr (T == 1) {
+                        mma_bf16_16816(c[0], plo[0][kt][0], 0u, plo[0][kt][1], 0u, b0, b1);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < LT; ++t) {
+                            if (kt == 0) mma_new(cl[t], plo[2 * t][kt][0], plo[2 * t + 1][kt][0], plo[2 * t][kt][1], plo[2 * t + 1][kt][1], b0, b1);
+                            else mma_bf16_16816(cl[t], plo[2 * t][kt][0], plo[2 * t + 1][kt][0], plo[2 * t][kt][1], plo[2 * t + 1][kt][1], b0, b1);
+                        }
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt)
-                        mma_bf16_16816(c, phm[t][kt][0], phm[t][kt][1], phm[t][kt][2], phm[t][kt][3], vb[kt][2 * h],
-                                       vb[kt][2 * h + 1]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        o[t][2 * np + h][e] += c[e] + (c[2 + e] + cl[t / 2][(t & 1) * 2 + e]);
+                for (int t = 0; t < T; ++t) {
+                    float2 x = make_float2(c[t][2], c[t][3]);
+                    if constexpr (T > 1) x = add2(x, make_float2(cl[t / 2][(t & 1) * 2], cl[t / 2][(t & 1) * 2 + 1]));
+                    o[t][2 * np + h] = add2(o[t][2 * np + h], add2(make_float2(c[t][0], c[t][1]), x));
                 }
             }
         }
@@ -356,11 +331,11 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
 
     // ---- the warps' states meet in shared memory (the ring is free now)
     __syncthreads();
-    float *mw = reinterpret_cast<float *>(smem);   // [NW][pairs]
+    float *mw = reinterpret_cast<float *>(w.smem);   // [NW][pairs]
     float *lw = mw + NW * C::kPairs;
-    float *ow = lw + NW * C::kPairs;               // [NW][pairs][D]
+    float *ow = lw + NW * C::kPairs;                 // [NW][pairs][D]
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
+    for (int t = 0; t < T; ++t) {
         float l = l_run[t];
         l += __shfl_xor_sync(kFull, l, 1);
         l += __shfl_xor_sync(kFull, l, 2);
@@ -371,8 +346,106 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         }
 #pragma unroll
         for (int n = 0; n < NP * 2; ++n)
-            *reinterpret_cast<float2 *>(ow + at * D + n * 8 + 2 * t4) = make_float2(o[t][n][0], o[t][n][1]);
+            *reinterpret_cast<float2 *>(ow + at * D + n * 8 + 2 * t4) = o[t][n];
     }
+    __syncthreads();
+}
+
+template <int D, int BS, int TILES>
+__global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, BS, TILES>::kBlocks)
+    decode_sinks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const DecodeKParams p, const int groups) {
+    using C = SinksCfg<D, BS, TILES>;
+    constexpr int NW = C::NW, ST = C::ST;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+
+    pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = blockIdx.x % groups, split = blockIdx.x / groups, kvh = blockIdx.y, b = blockIdx.z;
+    const bool report = threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0;
+    const int L = checked_len(p, b, BS, report);
+    int c0 = b, nq = 1;
+    if (p.cu_q != nullptr) {
+        c0 = __ldg(p.cu_q + b);
+        const int c1 = __ldg(p.cu_q + b + 1);
+        nq = c1 - c0;
+        if (!query_rows_ok(p, c0, c1, L)) {   // those of its rows that the call has: out = 0, lse = -inf
+            if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
+            if (blockIdx.x != 0) return;
+            for (int r = max(c0, 0); r < min(c1, p.rows); ++r) {
+                const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
+                for (int i = threadIdx.x; i < p.m * D; i += NW * 32) p.out[at * D + i] = 0.f;
+                if (p.lse != nullptr)
+                    for (int i = threadIdx.x; i < p.m; i += NW * 32) p.lse[at + i] = -INFINITY;
+            }
+            return;
+        }
+    }
+    // this CTA's pairs: slots slot0 .. slot0 + npairs - 1 of (row, head), row = slot / m
+    const int slot0 = group * C::kPairs, npairs = min(C::kPairs, nq * p.m - slot0);
+    if (npairs <= 0) return;
+    auto row_of = [&](int pair) {   // of out, lse, q
+        const int slot = slot0 + pair;
+        return static_cast<size_t>(c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
+    };
+    if (L == 0) {
+        if (split != 0) return;
+        for (int i = threadIdx.x; i < npairs * D; i += NW * 32) p.out[row_of(i / D) * D + i % D] = 0.f;
+        if (p.lse != nullptr)
+            for (int i = threadIdx.x; i < npairs; i += NW * 32) p.lse[row_of(i)] = -INFINITY;
+        return;
+    }
+    // tokens without the gap's pages: the sequence's (chunks), and those that the CTA's rows see, [0, S) and [lo, hi)
+    const int P0 = L - nq;
+    const SeqSpan sp = sinks_span(p, b, L, max(0, P0 + 1 - p.window), BS);
+    const int shift = sp.gap * BS;
+    auto lo_of = [&](int pos) { return max(0, pos + 1 - p.window) - shift; };
+    const int pos_first = P0 + slot0 / p.m, pos_last = P0 + (slot0 + npairs - 1) / p.m;
+    const int lo = lo_of(pos_first), hi = pos_last + 1 - shift;
+    const int all_lo = lo_of(pos_last), all_hi = pos_first + 1 - shift;   // [.., ..) seen by every row
+    const int nc = (sp.npages + p.chunk_pages - 1) / p.chunk_pages;
+    const int cp0 = split * p.chunk_pages, cp1 = min(sp.npages, cp0 + p.chunk_pages);
+    if (cp0 >= cp1) return;   // no such chunk
+    const int pg0 = cp0 < sp.spages ? cp0 : max(cp0, lo / BS), pg1 = min(cp1, (hi + BS - 1) / BS);
+
+    if (lane == 0) {
+        for (int s = 0; s < ST; ++s) mbar_init(smem_addr(&bars[warp * ST + s]), 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+    }
+    __syncwarp();
+
+    Stream w;
+    w.smem = smem;
+    w.bars = bars;
+    w.b = b;
+    w.kvh = kvh;
+    w.slot0 = slot0;
+    w.npairs = npairs;
+    w.c0 = c0;
+    w.P0 = P0;
+    w.pg0 = pg0;
+    w.pg1 = pg1;
+    w.lo = lo;
+    w.hi = hi;
+    w.all_lo = all_lo;
+    w.all_hi = all_hi;
+    w.sp = sp;
+    // only as many tiles as the CTA has pairs for (rows of a sequence and heads of a KV head differ)
+    if (npairs <= 8) attend_pages<D, BS, TILES, 1>(tm_k, tm_v, p, w);
+    else if constexpr (TILES > 1) {
+        if (npairs <= 16) attend_pages<D, BS, TILES, 2>(tm_k, tm_v, p, w);
+        else if constexpr (TILES > 2) attend_pages<D, BS, TILES, TILES>(tm_k, tm_v, p, w);
+    }
+    float *mw = reinterpret_cast<float *>(smem);   // [NW][pairs]
+    float *lw = mw + NW * C::kPairs;
+    float *ow = lw + NW * C::kPairs;               // [NW][pairs][D]
     __syncthreads();
     for (int i = threadIdx.x; i < npairs * D; i += NW * 32) {
         const int pair = i / D, c = i % D;
