@@ -651,8 +651,8 @@ pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q,
  *   draft i is accepted while u_i * q_i(x_i) < p_i(x_i)   (exact products);  accepted[b] = a, the first
  *   that fails;  the next token is the lowest v with r_0 + .. + r_v > u_k * (r_0 + .. + r_{V-1}), where
  *   r = max(p_a - q_a, 0) for a < k (p_a itself where that is 0 everywhere) and r = p_k for a = k.
- * Sums are of whole multiples of 2^-58, to which each probability is rounded down (exact from 2^-34 on), so that
- * the token depends neither on the order of summation nor on the GPU.
+ * Sums are of whole multiples of 2^-46, to the nearest of which each probability is rounded (ties to even; exact
+ * from 2^-22 on), so that the token depends neither on the order of summation nor on the GPU.
  *   accepted      int32 [B]
  *   tokens        int32 [D + B]: the accepted drafts of a sequence, its next token, -1 in the rest of its k + 1 places
  *   target_probs  [D + B][V] of type dt (PKV_F32 or PKV_BF16), rows target_stride >= V elements apart

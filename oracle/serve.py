@@ -73,14 +73,14 @@ def paged_attention_sinks(q, k_cache, v_cache, block_table, context_lens, cu_q, 
 
 # --------------------------------------------------------------- drafted tokens
 
-UNIT = 58   # probabilities are summed as whole multiples of 2^-58
+UNIT = 46   # probabilities are summed as whole multiples of 2^-46
 
 
 def units(p) -> list:
-    """Probabilities as whole multiples of 2^-58, rounded down; at most 1, 0 for negative ones and NaN."""
+    """Probabilities as the nearest whole multiples of 2^-46 (ties to even); at most 1, 0 for negative ones and NaN."""
     x = np.asarray(p, np.float64)
     x = np.where(x > 0, np.minimum(x, 1.0), 0.0)
-    return [int(v) for v in np.floor(np.ldexp(x, UNIT))]   # a scaled power of two: exact before the floor
+    return [int(v) for v in np.rint(np.ldexp(x, UNIT))]   # scaled by a power of two: exact before the rounding
 
 
 def verify_drafts(target, draft, draft_tokens, cu_drafts, uniforms):

@@ -220,12 +220,14 @@ pkv_status pkv_block_tables_fork(const int32_t *block_table, const int32_t *cont
     const size_t bytes = static_cast<size_t>(B) * MBS * sizeof(int32_t);
     const bool same = block_table == block_table_out, over = overlap(block_table, bytes, block_table_out, bytes);
     if (over && !same) return fail(PKV_ERR_INVALID_ARG, "block_tables_fork: block_table_out overlaps block_table");
+    if (context_lens != context_lens_out && overlap(context_lens, B * sizeof(int32_t), context_lens_out, B * sizeof(int32_t)))
+        return fail(PKV_ERR_INVALID_ARG, "block_tables_fork: context_lens_out overlaps context_lens");
     int sm_count = 0;
     unsigned *err = nullptr;
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, parents, held, block_table_out, context_lens_out, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, 0, err};
     return done(launch_fork(a, workspace, same && parents != nullptr, stream), "block_tables_fork");
 }
 
@@ -244,7 +246,7 @@ pkv_status pkv_block_tables_compact(const int32_t *block_table, const int32_t *c
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, nullptr, held, block_table_out, nullptr, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, 0, err};
     return done(launch_compact(a, workspace, stream), "block_tables_compact");
 }
 

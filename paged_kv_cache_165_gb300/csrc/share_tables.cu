@@ -13,10 +13,14 @@
 //   a fresh block (the pair list).  Fresh blocks are the lowest free ids, in row order.
 // compact: with n blocks in use, the i-th used block from id n on moves to the i-th free id below n.
 //
-// Both run as one cluster of 8 x 1024 threads, whose phases (clear, count, scan, write) are separated by
-// hardware cluster barriers, in place of four launches: tables of a serving batch are some 10^4 to 10^5
-// entries, bound by the latency of the phases.
+// Both run as one cluster of 8 x 1024 threads in place of four or five launches.  Every block of the cluster
+// owns a run of the ids and keeps their counts (and the rows that end in them, or where they move) in its
+// shared memory, which the others reach as distributed shared memory: counting is remote atomics, scanning is
+// local, and a phase (clear, count, scan, write) ends with a hardware cluster barrier and no trip to L2.  Pools
+// of more than kSharedIds ids keep the same numbers in global memory.  Tables of a serving batch are some 10^4
+// to 10^5 entries: bound by the latency of the phases.
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -32,6 +36,8 @@ constexpr int kThreads = 1024, kBlocks = 8;
 constexpr unsigned kAll = kThreads * kBlocks;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNobody = 0x7fffffff;
+constexpr int kSharedShift = 14;                           // at most 2^14 ids a block in shared memory (128 KB)
+constexpr unsigned kSharedIds = kBlocks << kSharedShift;
 
 // Exclusive ranks of N flags counted over a block's threads; totals[i]: the block's.  All threads call it.
 template <int N>
@@ -71,42 +77,81 @@ __device__ __forceinline__ void block_ranks(int (&x)[N], int (&s_warp)[N][32], i
     }
 }
 
-// The block's part of n items, as [begin, end).
-__device__ __forceinline__ uint2 part_of(unsigned n, unsigned rank) {
-    const unsigned each = (n + kBlocks - 1) / kBlocks;
-    return make_uint2(min(n, rank * each), min(n, (rank + 1) * each));
+// Two numbers for every id: the owner of id i is block i >> shift of the cluster.  SHARED: in its shared
+// memory; else in global memory.
+template <bool SHARED>
+struct Ids {
+    cg::cluster_group &cluster;
+    int *a_, *b_;      // this block's shared arrays, or the global ones
+    int shift;
+
+    __device__ __forceinline__ int *at(int *base, unsigned i) const {
+        if constexpr (SHARED) return cluster.map_shared_rank(base, i >> shift) + (i & ((1u << shift) - 1));
+        else return base + i;
+    }
+    __device__ __forceinline__ int *a(unsigned i) const { return at(a_, i); }
+    __device__ __forceinline__ int *b(unsigned i) const { return at(b_, i); }
+    // an id of this block's own
+    __device__ __forceinline__ int &own_a(unsigned i) const { return SHARED ? a_[i & ((1u << shift) - 1)] : a_[i]; }
+    __device__ __forceinline__ int &own_b(unsigned i) const { return SHARED ? b_[i & ((1u << shift) - 1)] : b_[i]; }
+};
+
+// Items [begin, end) in index order, four a thread: flags(i, f) says which of N kinds an item is, use(i, f, rank)
+// gets its rank among them, counted on from `rank0`.  All threads call it.
+template <int N, typename Flags, typename Use>
+__device__ __forceinline__ void rank_items(unsigned begin, unsigned end, int (&rank0)[N], int (&s_warp)[N][32], Flags flags, Use use) {
+    for (unsigned i0 = begin; i0 < end; i0 += 4 * kThreads) {
+        int f[4][N], r[N] = {}, total[N];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned i = i0 + 4 * threadIdx.x + k;
+#pragma unroll
+            for (int n = 0; n < N; ++n) f[k][n] = 0;
+            if (i < end) flags(i, f[k]);
+#pragma unroll
+            for (int n = 0; n < N; ++n) r[n] += f[k][n];
+        }
+        block_ranks<N>(r, s_warp, total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned i = i0 + 4 * threadIdx.x + k;
+            int at[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                at[n] = rank0[n] + r[n];
+                r[n] += f[k][n];
+            }
+            if (i < end) use(i, f[k], at);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) rank0[n] += total[n];
+    }
 }
 
-// Counts of N kinds of items in the block's part [begin, end): every block learns the sums before its part
-// (before) and over all parts (all).
-template <int N, typename Flags>
-__device__ __forceinline__ void count_parts(cg::cluster_group &cluster, uint2 part, Flags flags, int (&s_warp)[N][32],
-                                            int (&s_part)[N], int (&before)[N], int (&all)[N]) {
-    int mine[N] = {};
-    for (unsigned i = part.x + threadIdx.x; i < part.y; i += kThreads) {
-        int f[N];
-        flags(i, f);
-#pragma unroll
-        for (int k = 0; k < N; ++k) mine[k] += f[k];
-    }
-    int total[N];
-    block_ranks<N>(mine, s_warp, total);
+// The sums of N counts over the blocks before this one (before) and over all (all), by way of s_part, which
+// is not written again.  Ends with a cluster barrier.
+template <int N>
+__device__ __forceinline__ void share_counts(cg::cluster_group &cluster, const int (&mine)[N], int (&s_part)[N], int (&before)[N],
+                                             int (&all)[N]) {
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) s_part[k] = total[k];
+        for (int n = 0; n < N; ++n) s_part[n] = mine[n];
     }
     cluster.sync();
+    int theirs[kBlocks][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) before[k] = all[k] = 0;
-    for (unsigned c = 0; c < kBlocks; ++c) {
-        const int *theirs = cluster.map_shared_rank(&s_part[0], c);
+    for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if (c == cluster.block_rank()) before[k] = all[k];
-            all[k] += theirs[k];
+        for (int n = 0; n < N; ++n) theirs[c][n] = cluster.map_shared_rank(&s_part[0], c)[n];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        before[n] = all[n] = 0;
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c) {
+            if (c < static_cast<int>(cluster.block_rank())) before[n] += theirs[c][n];
+            all[n] += theirs[c][n];
         }
     }
-    cluster.sync();   // the sums have been read
 }
 
 // What row b of the result holds.
@@ -131,196 +176,218 @@ __device__ __forceinline__ Source source_of(const ShareArgs &a, int b, bool repo
 }
 
 // A table entry, -1 where it names no block (-1: given back before; anything else is flagged).
-__device__ __forceinline__ int entry_of(const ShareArgs &a, size_t at) {
-    const int x = a.table[at];
+__device__ __forceinline__ int checked(const ShareArgs &a, int x) {
     if (x >= 0 && x < a.NB) return x;
     if (x != -1) raise_error(a.err, PKV_DEVERR_BLOCK);
     return -1;
 }
 
+// Every entry of the B rows, 256 of a row to a warp at a time, eight a lane: first all are loaded
+// (x = load(source, b, j)), then all looked up (x = map(x)), then all put to use (at(source, b, j, x)), so that
+// a lane's eight loads overlap.
+constexpr int kAhead = 8, kSegment = 32 * kAhead;
+
+template <typename From, typename Load, typename Map, typename At>
+__device__ __forceinline__ void for_entries(const ShareArgs &a, unsigned warp, unsigned lane, unsigned warps, From from, Load load,
+                                            Map map, At at) {
+    const unsigned MBS = a.MBS, segments = (MBS + kSegment - 1) / kSegment;
+    const unsigned long long items = static_cast<unsigned long long>(a.B) * segments;
+    for (unsigned long long i = warp; i < items; i += warps) {
+        const unsigned b = static_cast<unsigned>(i / segments);
+        const unsigned j0 = static_cast<unsigned>(i - static_cast<unsigned long long>(b) * segments) * kSegment + lane;
+        const Source s = from(b, j0 == 0);
+        int x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j0 + 32 * k < MBS) at(s, b, j0 + 32 * k, x[k]);
+    }
+}
+
+__device__ __forceinline__ unsigned blocks_of(const ShareArgs &a, int len) {
+    return static_cast<unsigned>((static_cast<long long>(len) + a.bs - 1) / a.bs);
+}
+
+template <bool SHARED>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
-    __shared__ int s_warp[1][32], s_part[1];
+    extern __shared__ int s_ids[];
+    __shared__ int s_warp[1][32], s_part[2];
     cg::cluster_group cluster = cg::this_cluster();
     const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
-    const unsigned NB = a.NB, B = a.B;
-    const unsigned warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
-    int *first = a.first;     // [NB] the lowest row that ends, partly filled, in a block
-    for (unsigned i = tid; i < NB; i += kAll) {
-        a.refs[i] = a.held != nullptr && __ldg(a.held + i) != 0 ? 1 : 0;
-        first[i] = kNobody;
+    const unsigned NB = a.NB, B = a.B, warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
+    // refs: entries that name a block inside a row, or hold it (a); first: the lowest row that ends in it, partly filled (b)
+    const Ids<SHARED> ids{cluster, SHARED ? s_ids : a.refs, SHARED ? s_ids + (1 << a.shift) : a.first, a.shift};
+    const unsigned i_begin = min(NB, rank << a.shift), i_end = min(NB, (rank + 1) << a.shift);
+    const unsigned rows_each = (B + kBlocks - 1) / kBlocks, b_begin = min(B, rank * rows_each), b_end = min(B, (rank + 1) * rows_each);
+    for (unsigned i = i_begin + threadIdx.x; i < i_end; i += kThreads) {
+        ids.own_a(i) = a.held != nullptr && __ldg(a.held + i) != 0 ? 1 : 0;
+        ids.own_b(i) = kNobody;
     }
     cluster.sync();
-    // rows of the result: their entries, and the references of blocks that will not be written
-    int32_t *rows = a.rows;   // [B][MBS], the table itself where the parents' rows are read no more
-    for (unsigned b = warp; b < B; b += warps) {
-        const Source s = source_of(a, b, lane == 0);
-        const int n = static_cast<int>((static_cast<long long>(s.len) + a.bs - 1) / a.bs);
-        const bool partly = s.len % a.bs != 0;
-        const size_t to = static_cast<size_t>(b) * a.MBS, from = static_cast<size_t>(max(s.row, 0)) * a.MBS;
-        for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) {
-            int x = -1;
-            if (j < static_cast<unsigned>(n)) {
-                x = entry_of(a, from + j);
-                if (x >= 0) {
-                    if (partly && j == static_cast<unsigned>(n) - 1) atomicMin(first + x, static_cast<int>(b));
-                    else atomicAdd(a.refs + x, 1);
-                }
-            }
-            rows[to + j] = x;
-        }
-    }
+    int32_t *rows = a.rows;   // [B][MBS] of the result: the table itself where nothing reads the parents' rows any more
+    auto same = [](int x) { return x; };
+    for_entries(a, warp, lane, warps, [&](unsigned b, bool report) { return source_of(a, b, report); },
+                [&](const Source &s, unsigned, unsigned j) {
+                    return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(max(s.row, 0)) * a.MBS + j] : -1;
+                }, same,
+                [&](const Source &s, unsigned b, unsigned j, int x) {
+                    x = checked(a, x);
+                    if (x >= 0) {
+                        if (s.len % a.bs != 0 && j == static_cast<unsigned>(s.len / a.bs)) atomicMin(ids.b(x), static_cast<int>(b));
+                        else atomicAdd(ids.a(x), 1);
+                    }
+                    rows[static_cast<size_t>(b) * a.MBS + j] = x;
+                });
     cluster.sync();
-    // rows that get a copy of their last block
-    auto copied = [&](unsigned b) -> int2 {   // (its block, its place in the row), or (-1, 0)
+    // rows that get a copy of their last block, and free blocks: place[b] remembers the first
+    int mine[2] = {0, 0}, before[2], all[2], total[1];
+    for (unsigned b = b_begin + threadIdx.x; b < b_end; b += kThreads) {
         const Source s = source_of(a, b, false);
-        if (s.len % a.bs == 0) return make_int2(-1, 0);
-        const int j = s.len / a.bs, x = rows[static_cast<size_t>(b) * a.MBS + j];
-        if (x < 0 || (a.refs[x] == 0 && first[x] == static_cast<int>(b))) return make_int2(-1, 0);
-        return make_int2(x, j);
-    };
-    const uint2 row_part = part_of(B, rank), block_part = part_of(NB, rank);
-    int copies_before[1], copies[1], free_before[1], free_all[1];
-    count_parts<1>(cluster, row_part, [&](unsigned b, int (&f)[1]) { f[0] = copied(b).x >= 0; }, s_warp, s_part,
-                   copies_before, copies);
-    count_parts<1>(cluster, block_part, [&](unsigned i, int (&f)[1]) { f[0] = a.refs[i] == 0 && first[i] == kNobody; }, s_warp,
-                   s_part, free_before, free_all);
-    // which row gets which fresh block, before the references change
-    int at = copies_before[0];
-    for (unsigned b0 = row_part.x; b0 < row_part.y; b0 += kThreads) {
-        const unsigned b = b0 + threadIdx.x;
-        const int2 c = b < row_part.y ? copied(b) : make_int2(-1, 0);
-        int r[1] = {c.x >= 0}, total[1];
-        block_ranks<1>(r, s_warp, total);
-        if (b < row_part.y) a.place[b] = c.x >= 0 ? at + r[0] : -1;
-        at += total[0];
-    }
-    cluster.sync();
-    const int served = min(copies[0], free_all[0]), left = free_all[0] - served;
-    at = free_before[0];
-    for (unsigned i0 = block_part.x; i0 < block_part.y; i0 += kThreads) {
-        const unsigned i = i0 + threadIdx.x;
-        bool free = false, kept = false;
-        if (i < block_part.y) {
-            kept = a.refs[i] == 0 && first[i] != kNobody;
-            free = a.refs[i] == 0 && !kept;
+        int copied = 0;
+        if (s.len % a.bs != 0) {
+            const int x = rows[static_cast<size_t>(b) * a.MBS + s.len / a.bs];
+            copied = x >= 0 && (*ids.a(x) != 0 || *ids.b(x) != static_cast<int>(b));
         }
-        int r[1] = {free}, total[1];
-        block_ranks<1>(r, s_warp, total);
-        const int nth = at + r[0];
-        if (free && nth < served) a.fresh[nth] = static_cast<int>(i);
-        if (free && nth >= served) a.free_list[free_all[0] - 1 - nth] = static_cast<int>(i);
-        if (kept || (free && nth < served)) a.refs[i] = 1;
-        at += total[0];
+        a.place[b] = copied;
+        mine[0] += copied;
     }
-    for (unsigned i = tid; i < NB; i += kAll)
-        if (i >= static_cast<unsigned>(left)) a.free_list[i] = -1;
+    for (unsigned i = i_begin + threadIdx.x; i < i_end; i += kThreads) mine[1] += ids.own_a(i) == 0 && ids.own_b(i) == kNobody;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        int x[1] = {mine[n]};
+        block_ranks<1>(x, s_warp, total);
+        mine[n] = total[0];
+    }
+    share_counts<2>(cluster, mine, s_part, before, all);
+    const int served = min(all[0], all[1]), left = all[1] - served;
+    int row_rank[1] = {before[0]}, id_rank[1] = {before[1]};
+    rank_items<1>(b_begin, b_end, row_rank, s_warp, [&](unsigned b, int (&f)[1]) { f[0] = a.place[b]; },
+                  [&](unsigned b, const int (&f)[1], const int (&at)[1]) { a.place[b] = f[0] ? at[0] : -1; });
+    rank_items<1>(i_begin, i_end, id_rank, s_warp,
+                  [&](unsigned i, int (&f)[1]) { f[0] = ids.own_a(i) == 0 && ids.own_b(i) == kNobody; },
+                  [&](unsigned i, const int (&f)[1], const int (&at)[1]) {
+                      const bool handed = f[0] && at[0] < served;
+                      if (handed) a.fresh[at[0]] = static_cast<int>(i);
+                      else if (f[0]) a.free_list[all[1] - 1 - at[0]] = static_cast<int>(i);
+                      const int inside = ids.own_a(i);   // of the rows that end in a block one at most still names it
+                      a.refs[i] = inside != 0 ? inside : handed || !f[0];
+                  });
+    for (unsigned i = left + tid; i < NB; i += kAll) a.free_list[i] = -1;
+    for (unsigned i = served + tid; i < B; i += kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
         *a.free_count = left;
         *a.pair_count = served;
-        if (served < copies[0]) raise_error(a.err, PKV_DEVERR_POOL);
+        if (served < all[0]) raise_error(a.err, PKV_DEVERR_POOL);
     }
-    for (unsigned i = tid; i < B; i += kAll)
-        if (i >= static_cast<unsigned>(served)) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     cluster.sync();
-    // the rows themselves: a row of B a thread for what changes, then the whole table where it was built aside
     for (unsigned b = tid; b < B; b += kAll) {
-        Source s = source_of(a, b, false);
-        const int nth = a.place[b];
-        const size_t last = static_cast<size_t>(b) * a.MBS + s.len / a.bs;
+        const int len = source_of(a, b, false).len, nth = a.place[b];
+        const size_t last = static_cast<size_t>(b) * a.MBS + len / a.bs;
         if (nth >= 0 && nth < served) {
             reinterpret_cast<int2 *>(a.pairs)[nth] = make_int2(rows[last], a.fresh[nth]);
             rows[last] = a.fresh[nth];
         }
-        a.place[b] = nth >= served ? 0 : s.len;   // its length: none for a row that the pool was too small for
+        a.place[b] = nth >= served ? 0 : len;   // its length: none for a row that the pool was too small for
+    }
+    if (rows == a.table_out && served == all[0] && a.lens_out != a.lens) {
+        for (unsigned b = tid; b < B; b += kAll) a.lens_out[b] = a.place[b];
+        return;   // (its own rows: no other thread wrote them)
     }
     cluster.sync();
     for (unsigned b = tid; b < B; b += kAll) a.lens_out[b] = a.place[b];
-    for (unsigned b = warp; b < B; b += warps) {
-        const bool none = a.place[b] == 0;
-        if (rows == a.table_out && !none) continue;
-        const size_t to = static_cast<size_t>(b) * a.MBS;
-        for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) a.table_out[to + j] = none ? -1 : rows[to + j];
+    if (rows != a.table_out) {
+        for_entries(a, warp, lane, warps, [&](unsigned b, bool) { return Source{0, a.place[b]}; },
+                    [&](const Source &s, unsigned b, unsigned j) {
+                        return s.len == 0 ? -1 : rows[static_cast<size_t>(b) * a.MBS + j];
+                    }, same,
+                    [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
+    } else if (served < all[0]) {   // rows that the pool was too small for
+        for (unsigned b = warp; b < B; b += warps)
+            if (a.place[b] == 0)
+                for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) rows[static_cast<size_t>(b) * a.MBS + j] = -1;
     }
 }
 
+template <bool SHARED>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
+    extern __shared__ int s_ids[];
     __shared__ int s_warp[3][32], s_part[3], s_warp1[1][32], s_part1[1];
     cg::cluster_group cluster = cg::this_cluster();
     const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
-    const unsigned NB = a.NB, B = a.B;
-    const unsigned warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
-    int *moved = a.first;     // [NB] where a block goes
+    const unsigned NB = a.NB, warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
+    // refs: entries that name a block (a); where it goes (b)
+    const Ids<SHARED> ids{cluster, SHARED ? s_ids : a.refs, SHARED ? s_ids + (1 << a.shift) : a.first, a.shift};
+    const unsigned begin = min(NB, rank << a.shift), end = min(NB, (rank + 1) << a.shift);
     auto held = [&](unsigned i) { return a.held != nullptr && __ldg(a.held + i) != 0; };
-    for (unsigned i = tid; i < NB; i += kAll) a.refs[i] = held(i) ? 1 : 0;
+    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) ids.own_a(i) = held(i) ? 1 : 0;
     cluster.sync();
-    for (unsigned b = warp; b < B; b += warps) {
-        const Source s = source_of(a, b, lane == 0);
-        const int n = static_cast<int>((static_cast<long long>(s.len) + a.bs - 1) / a.bs);
-        const size_t row = static_cast<size_t>(b) * a.MBS;
-        for (int j = lane; j < n; j += 32) {
-            const int x = entry_of(a, row + j);
-            if (x >= 0) atomicAdd(a.refs + x, 1);
-        }
+    auto source = [&](unsigned b, bool report) { return source_of(a, b, report); };
+    auto entry = [&](const Source &s, unsigned b, unsigned j) {
+        return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(b) * a.MBS + j] : -1;
+    };
+    for_entries(a, warp, lane, warps, source, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
+        x = checked(a, x);
+        if (x >= 0) atomicAdd(ids.a(x), 1);
+    });
+    cluster.sync();
+    int mine[1] = {0}, before1[1], all1[1];
+    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) mine[0] += ids.own_a(i) != 0;
+    {
+        int total[1];
+        block_ranks<1>(mine, s_warp1, total);
+        mine[0] = total[0];
     }
-    cluster.sync();
-    const uint2 part = part_of(NB, rank);
-    int before1[1], used_[1];
-    count_parts<1>(cluster, part, [&](unsigned i, int (&f)[1]) { f[0] = a.refs[i] != 0; }, s_warp1, s_part1, before1, used_);
-    const unsigned used = used_[0];
+    share_counts<1>(cluster, mine, s_part1, before1, all1);
+    const unsigned used = all1[0];
     // blocks that move (in use, not held, from `used` on), free ids below, free or vacated ids from there on
     auto kinds = [&](unsigned i, int (&f)[3]) {
-        const bool in_use = a.refs[i] != 0, high = i >= used, fixed = held(i);
+        const bool in_use = ids.own_a(i) != 0, high = i >= used, fixed = high && held(i);
         f[0] = in_use && high && !fixed;
         f[1] = !in_use && !high;
         f[2] = high && !fixed;
     };
-    int before[3], all[3];
-    count_parts<3>(cluster, part, kinds, s_warp, s_part, before, all);
+    int count[3] = {0, 0, 0}, before[3], all[3];
+    rank_items<3>(begin, end, count, s_warp, kinds, [](unsigned, const int (&)[3], const int (&)[3]) {});
+    share_counts<3>(cluster, count, s_part, before, all);
     // as many ids are free below `used` as are taken from there on, so every mover has a place
     const int moves = all[0], spare = all[1] - moves, free_all = spare + all[2];
-    for (unsigned i0 = part.x; i0 < part.y; i0 += kThreads) {
-        const unsigned i = i0 + threadIdx.x;
-        int f[3] = {0, 0, 0};
-        if (i < part.y) kinds(i, f);
-        int r[3] = {f[0], f[1], f[2]}, total[3];
-        block_ranks<3>(r, s_warp, total);
-        if (i < part.y) moved[i] = static_cast<int>(i);
-        if (f[0]) reinterpret_cast<int2 *>(a.pairs)[before[0] + r[0]].x = static_cast<int>(i);
+    rank_items<3>(begin, end, before, s_warp, kinds, [&](unsigned i, const int (&f)[3], const int (&at)[3]) {
+        ids.own_b(i) = f[0] ? -1 - at[0] : static_cast<int>(i);   // a mover: its rank for now
         if (f[1]) {
-            const int nth = before[1] + r[1];
-            if (nth < moves) reinterpret_cast<int2 *>(a.pairs)[nth].y = static_cast<int>(i);
-            else a.free_list[free_all - 1 - (nth - moves)] = static_cast<int>(i);
+            if (at[1] < moves) a.fresh[at[1]] = static_cast<int>(i);
+            else a.free_list[free_all - 1 - (at[1] - moves)] = static_cast<int>(i);
         }
-        if (f[2]) a.free_list[free_all - 1 - (spare + before[2] + r[2])] = static_cast<int>(i);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) before[k] += total[k];
-    }
-    for (unsigned i = tid; i < NB; i += kAll)
-        if (i >= static_cast<unsigned>(free_all)) a.free_list[i] = -1;
-    for (unsigned i = tid; i < NB / 2; i += kAll)
-        if (i >= static_cast<unsigned>(moves)) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
+        if (f[2]) a.free_list[free_all - 1 - (spare + at[2])] = static_cast<int>(i);
+    });
+    for (unsigned i = free_all + tid; i < NB; i += kAll) a.free_list[i] = -1;
+    for (unsigned i = moves + tid; i < NB / 2; i += kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
         *a.free_count = free_all;
         *a.pair_count = moves;
     }
     cluster.sync();
-    for (unsigned i = tid; i < static_cast<unsigned>(moves); i += kAll) {
-        const int2 p = reinterpret_cast<const int2 *>(a.pairs)[i];
-        moved[p.x] = p.y;
-        a.refs[p.y] = a.refs[p.x];
-        a.refs[p.x] = 0;
-    }
-    cluster.sync();
-    for (unsigned b = warp; b < B; b += warps) {
-        const Source s = source_of(a, b, false);
-        const unsigned n = static_cast<unsigned>((static_cast<long long>(s.len) + a.bs - 1) / a.bs);
-        const size_t row = static_cast<size_t>(b) * a.MBS;
-        for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) {
-            int x = j < n ? a.table[row + j] : -1;
-            x = x >= 0 && x < a.NB ? moved[x] : -1;
-            a.table_out[row + j] = x;
+    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) {
+        const int refs = ids.own_a(i), nth = -1 - ids.own_b(i);
+        if (nth >= 0) {
+            const int to = a.fresh[nth];
+            ids.own_b(i) = to;
+            reinterpret_cast<int2 *>(a.pairs)[nth] = make_int2(static_cast<int>(i), to);
+            a.refs[to] = refs;
+            a.refs[i] = 0;
+        } else if (SHARED && (refs != 0 || i >= used)) {
+            a.refs[i] = refs;
         }
     }
+    if constexpr (SHARED) {   // free ids below `used` that nothing moves to
+        for (unsigned i = tid; i < static_cast<unsigned>(spare); i += kAll) a.refs[a.free_list[free_all - 1 - i]] = 0;
+    }
+    cluster.sync();
+    for_entries(a, warp, lane, warps, source, entry, [&](int x) { return x >= 0 && x < a.NB ? *ids.b(x) : -1; },
+                [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
+    if constexpr (SHARED) cluster.sync();   // the others' shared memory stays until all have read it
 }
 
 // ---------------------------------------------------------------- copies of a list that the GPU counted
@@ -362,26 +429,61 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 }  // namespace
 
-// Scratch behind a call: a row's length or place [B], fresh blocks [B], one number a block [NB], and the
-// table when it replaces the one that it is built from ([B][MBS]).
+// Scratch behind a call: one number a block [NB], a row's length or place [B], fresh blocks [B] or ids that
+// blocks move to [NB / 2], and the table where it replaces the one that it is built from ([B][MBS]).
 size_t share_workspace_bytes(int B, int MBS, int NB) {
-    return (2 * static_cast<size_t>(B) + static_cast<size_t>(NB) + static_cast<size_t>(B) * MBS) * sizeof(int32_t);
+    return (static_cast<size_t>(NB) + static_cast<size_t>(B) + std::max(static_cast<size_t>(B), static_cast<size_t>(NB) / 2) +
+            static_cast<size_t>(B) * MBS) *
+           sizeof(int32_t);
 }
 
+namespace {
+
+// ids a block: the smallest power of two that covers the pool with eight blocks
+int id_shift(int NB) {
+    int shift = 0;
+    while ((static_cast<long long>(kBlocks) << shift) < NB) ++shift;
+    return shift;
+}
+
+template <typename Kernel>
+cudaError_t launch_cluster(Kernel shared, Kernel global, ShareArgs a, std::atomic<unsigned long long> &ready, cudaStream_t stream) {
+    a.shift = id_shift(a.NB);
+    if (static_cast<unsigned>(a.NB) > kSharedIds) {
+        global<<<kBlocks, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {   // shared memory opted in, once a device
+        e = cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * sizeof(int) << kSharedShift);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit);
+    }
+    shared<<<kBlocks, kThreads, 2 * sizeof(int) << a.shift, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_fork(ShareArgs a, void *workspace, bool aside, cudaStream_t stream) {
+    static std::atomic<unsigned long long> ready{0};
     int32_t *ws = static_cast<int32_t *>(workspace);
     a.first = ws;
     a.place = ws + a.NB;
     a.fresh = a.place + a.B;
-    a.rows = aside ? a.fresh + a.B : a.table_out;
-    fork_kernel<<<kBlocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    a.rows = aside ? a.fresh + std::max(a.B, a.NB / 2) : a.table_out;
+    return launch_cluster(fork_kernel<true>, fork_kernel<false>, a, ready, stream);
 }
 
 cudaError_t launch_compact(ShareArgs a, void *workspace, cudaStream_t stream) {
-    a.first = static_cast<int32_t *>(workspace);
-    compact_kernel<<<kBlocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    static std::atomic<unsigned long long> ready{0};
+    int32_t *ws = static_cast<int32_t *>(workspace);
+    a.first = ws;
+    a.fresh = ws + a.NB + a.B;
+    return launch_cluster(compact_kernel<true>, compact_kernel<false>, a, ready, stream);
 }
 
 cudaError_t launch_kv_block_copy_counted(void *k_cache, void *v_cache, int elem_bytes, const int32_t *pairs, int n,

@@ -6,10 +6,13 @@
 //   r_0 + .. + r_v > u_k (r_0 + .. + r_{V-1}),
 // so that what comes out is distributed as the target alone (rejection sampling).
 //
-// The sums are over whole numbers: a probability becomes its value in units of 2^-58, exactly where it is at
-// least 2^-34 and rounded down below, so that sums do not depend on their order -- which token comes out does
-// not depend on how a row is cut into pieces -- and cost two integer additions where fp64 would be the
-// bottleneck of this GPU.  u times the total is compared exactly.  Products u q are exact in fp64.
+// The sums are over whole numbers: a probability becomes the nearest multiple of 2^-46, so that sums do not depend
+// on their order -- which token comes out does not depend on how a row is cut into pieces.  The number is kept as
+// H 2^23 + L: 1 + p rounds to 1 + H 2^-23 (H are the lower bits of that fp32 number), and what is left of p,
+// times 2^46, onto 1.5 * 2^23 rounds to L likewise: five fp32 operations, where fp64 sums would be this GPU's
+// bottleneck and 64-bit shifts of the mantissa took twice the instructions.  max(p - q, 0) = max(p, q) - q, so a
+// rest is the difference of two such numbers, and the constants of the bit patterns cancel.  u times the total
+// is compared exactly.  Products u q are exact in fp64.
 //
 // One cluster per sequence: each block sums its share of the row (a contiguous run for each warp), the totals
 // meet in distributed shared memory, and the warp whose run holds the border reads it once more, from L2.
@@ -31,30 +34,36 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr u64 kMost = 1ull << 63;   // sums of more than 32 (no distribution) stay there
+constexpr u64 kMost = 1ull << 63;   // sums of more than 2^17 (no distribution) stay there
 
 __device__ __forceinline__ u64 capped(u64 a, u64 b) {   // a, b <= 2^63: associative whatever the order
     const u64 s = a + b;
     return s < a || s > kMost ? kMost : s;
 }
 
-__device__ __forceinline__ unsigned bits_of(float x) { return __float_as_uint(x); }
-__device__ __forceinline__ unsigned bits_of(__nv_bfloat16 x) {
-    return static_cast<unsigned>(__bfloat16_as_ushort(x)) << 16;
-}
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// A probability in units of 2^-58: 0 for a negative one or NaN, 2^58 from 1 on.  Below 1 it is
-// 2^(e - 127) (1 + m 2^-23), e <= 126: (2^23 + m) 2^34 shifted right by 126 - e, whose upper word is
-// (2^23 + m) 2^2 and whose lower word is 0; PTX shifts by 32 and more give 0.
-__device__ __forceinline__ u64 units(unsigned b) {
-    if (b >= 0x3f800000u) return b <= 0x7f800000u ? 1ull << 58 : 0ull;
-    const unsigned e = b >> 23, top = ((b & 0x7fffffu) | 0x800000u) << 2;
-    unsigned hi, lo, lo2;
-    asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(top), "r"(126u - e));
-    asm("shl.b32 %0, %1, %2;" : "=r"(lo) : "r"(top), "r"(e - 94u));    // less than 32 to the right
-    asm("shr.u32 %0, %1, %2;" : "=r"(lo2) : "r"(top), "r"(94u - e));   // more
-    return static_cast<u64>(hi) << 32 | (lo | lo2);
-}
+// Sums of elements' H and L (units of 2^-23 and 2^-46), for at most 128 elements: |H| <= 2^23, |L| <= 2^23 each.
+struct Parts {
+    unsigned h = 0, l = 0;   // modulo 2^32
+    __device__ __forceinline__ void add(float p) {   // p in [0, 1]
+        const float t = p + 1.f;
+        h += __float_as_uint(t);
+        l += __float_as_uint(__fmaf_rn(p - (t - 1.f), 0x1p46f, 0x1.8p23f));
+    }
+    __device__ __forceinline__ void sub(float p) {
+        const float t = p + 1.f;
+        h -= __float_as_uint(t);
+        l -= __float_as_uint(__fmaf_rn(p - (t - 1.f), 0x1p46f, 0x1.8p23f));
+    }
+    // n: elements added less elements subtracted
+    __device__ __forceinline__ u64 units(int n) const {
+        const long long H = static_cast<int>(h - static_cast<unsigned>(n) * 0x3f800000u);
+        const long long L = static_cast<int>(l - static_cast<unsigned>(n) * 0x4b400000u);
+        return static_cast<u64>((H << 23) + L);
+    }
+};
 
 // u in [0, 1) in units of 2^-64 (rounded down).
 __device__ __forceinline__ u64 share_of_turn(float u) {
@@ -72,98 +81,108 @@ struct Row {       // what is drawn from
     int not_this;     // an element that counts as 0, or -1
 };
 
-template <typename T>
-__device__ __forceinline__ float as_float(T x) { return __uint_as_float(bits_of(x)); }
-
-template <typename T>
-__device__ __forceinline__ u64 rest_of(const Row<T> &r, T p, T q, int v) {
-    const u64 x = units(bits_of(p)), y = r.q != nullptr ? units(bits_of(q)) : 0;
-    return v == r.not_this || x <= y ? 0 : x - y;
+// Elements v .. v + N - 1, in units.  Q: q is taken away; else one element may not count.  Saturation makes a
+// probability at most 1, and 0 of a negative one and of NaN.
+template <bool Q, typename T, int N>
+__device__ __forceinline__ u64 rest_of(const Row<T> &r, const T (&p)[N], const T (&q)[N], int v) {
+    Parts s;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float x = __saturatef(as_float(p[j]));
+        if constexpr (Q) {
+            const float y = __saturatef(as_float(q[j]));
+            s.add(fmaxf(x, y));
+            s.sub(y);
+        } else {
+            s.add(v + j == r.not_this ? 0.f : x);
+        }
+    }
+    return s.units(Q ? 0 : N);
 }
 
-// Elements v .. v + N - 1 of the row (those from hi on count as 0): their sum, in units.
+// Elements v .. v + N - 1 of the row, those from hi on 0.
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Piece { T x[N]; };
 
-template <typename T, int N>
+template <bool Q, typename T, int N>
 __device__ __forceinline__ void load_pieces(const Row<T> &r, int v, int hi, Piece<T, N> &p, Piece<T, N> &q) {
     if (v + N <= hi) {
         p = *reinterpret_cast<const Piece<T, N> *>(r.p + v);
-        if (r.q != nullptr) q = *reinterpret_cast<const Piece<T, N> *>(r.q + v);
+        if constexpr (Q) q = *reinterpret_cast<const Piece<T, N> *>(r.q + v);
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             p.x[j] = v + j < hi ? r.p[v + j] : T(0.f);
-            q.x[j] = v + j < hi && r.q != nullptr ? r.q[v + j] : T(0.f);
+            if constexpr (Q) q.x[j] = v + j < hi ? r.q[v + j] : T(0.f);
         }
     }
 }
 
-template <typename T, int N>
-__device__ __forceinline__ u64 sum_piece(const Row<T> &r, int v, const Piece<T, N> &p, const Piece<T, N> &q) {
-    u64 s = 0;      // at most 8 elements of 2^58
-#pragma unroll
-    for (int j = 0; j < N; ++j) s += rest_of(r, p.x[j], q.x[j], v + j);
-    return s;
-}
-
-// Pieces a lane loads before it uses the first; a step of a warp covers 32 * N * kAhead elements.
-template <int N>
-constexpr int ahead() { return N == 1 ? 8 : 2; }
-
-// The sum over elements [lo, hi) of the row by one warp; N elements a lane side by side.
-template <typename T, int N>
+// The sum over elements [lo, hi) of the row by one warp; N elements a lane side by side, a few such pieces loaded
+// before the first is used.
+template <bool Q, typename T, int N>
 __device__ __forceinline__ u64 warp_sum(const Row<T> &r, int lo, int hi, int lane) {
-    constexpr int kAhead = ahead<N>(), span = 32 * N;
+    constexpr int kAhead = N == 1 ? 8 : 4, span = 32 * N;
     u64 sum = 0;
-    for (int v0 = lo + lane * N; v0 - lane * N < hi; v0 += kAhead * span) {
+    for (int v0 = lo; v0 < hi; v0 += kAhead * span) {
         Piece<T, N> p[kAhead], q[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_pieces<T, N>(r, v0 + i * span, hi, p[i], q[i]);
+        for (int i = 0; i < kAhead; ++i) load_pieces<Q, T, N>(r, v0 + lane * N + i * span, hi, p[i], q[i]);
+        u64 s = 0;   // at most 32 elements of 2^46
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) sum = capped(sum, sum_piece<T, N>(r, v0 + i * span, p[i], q[i]));
+        for (int i = 0; i < kAhead; ++i) s += rest_of<Q, T, N>(r, p[i].x, q[i].x, v0 + lane * N + i * span);
+        sum = capped(sum, s);
     }
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) sum = capped(sum, __shfl_xor_sync(kFull, sum, sh));
     return sum;
 }
 
-// The lowest v of [lo, hi) whose sum from lo on exceeds `left` (which the whole run's does).
-template <typename T, int N>
-__device__ __forceinline__ int find(const Row<T> &r, int lo, int hi, u64 left, int lane) {
-    constexpr int kAhead = ahead<N>(), span = 32 * N;
-    u64 before = 0;
-    for (int w0 = lo; w0 < hi; w0 += kAhead * span) {
-        Piece<T, N> p[kAhead], q[kAhead];
+// Whole-warp: the first lane whose inclusive sum over the lanes (of `mine`, after `before`) exceeds `left`, and the
+// sum before it; -1 where none does.
+__device__ __forceinline__ int first_over(u64 mine, u64 left, int lane, u64 &before) {
+    u64 s = mine;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_pieces<T, N>(r, w0 + lane * N + i * span, hi, p[i], q[i]);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int v = w0 + lane * N + i * span;
-            const u64 mine = sum_piece<T, N>(r, v, p[i], q[i]);
-            u64 s = mine;
-#pragma unroll
-            for (int sh = 1; sh < 32; sh <<= 1) {
-                const u64 y = __shfl_up_sync(kFull, s, sh);
-                if (lane >= sh) s = capped(s, y);
-            }
-            const unsigned over = __ballot_sync(kFull, capped(before, s) > left);
-            if (over != 0) {
-                const int first = __ffs(over) - 1;
-                const u64 others = __shfl_up_sync(kFull, s, 1);
-                u64 run = lane > 0 ? capped(before, others) : before;
-                int at = v + N - 1;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    run = capped(run, rest_of(r, p[i].x[j], q[i].x[j], v + j));
-                    if (run > left) at = min(at, v + j);
-                }
-                return __shfl_sync(kFull, at, first);
-            }
-            before = capped(before, __shfl_sync(kFull, s, 31));
-        }
+    for (int sh = 1; sh < 32; sh <<= 1) {
+        const u64 y = __shfl_up_sync(kFull, s, sh);
+        if (lane >= sh) s = capped(s, y);
     }
-    return hi - 1;
+    const unsigned over = __ballot_sync(kFull, capped(before, s) > left);
+    if (over == 0) {
+        before = capped(before, __shfl_sync(kFull, s, 31));
+        return -1;
+    }
+    const int first = __ffs(over) - 1;
+    const u64 lower = __shfl_sync(kFull, s, max(first - 1, 0));
+    if (first > 0) before = capped(before, lower);
+    return first;
+}
+
+// The lowest v of [lo, hi) whose sum from lo on exceeds `left` (which the whole run's does): the 32 consecutive
+// shares of the run first, then the one that holds it, so that two rounds of loads and scans do.
+template <bool Q, typename T>
+__device__ __forceinline__ int find(const Row<T> &r, int lo, int hi, u64 left, int lane) {
+    const int share = (hi - lo + 31) / 32, a = min(hi, lo + lane * share), b = min(hi, a + share);
+    u64 sum = 0, before = 0;
+    for (int v0 = a; v0 < b; v0 += 8) {
+        T p[8], q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            p[j] = v0 + j < b ? r.p[v0 + j] : T(0.f);
+            if constexpr (Q) q[j] = v0 + j < b ? r.q[v0 + j] : T(0.f);
+        }
+        sum = capped(sum, rest_of<Q, T, 8>(r, p, q, v0));
+    }
+    const int holder = first_over(sum, left, lane, before);
+    if (holder < 0) return hi - 1;
+    const int from = lo + holder * share, to = min(hi, from + share);
+    for (int v0 = from; v0 < to; v0 += 32) {
+        const int v = v0 + lane;
+        const T p[1] = {v < to ? r.p[v] : T(0.f)}, q[1] = {Q && v < to ? r.q[v] : T(0.f)};
+        const int first = first_over(rest_of<Q, T, 1>(r, p, q, v), left, lane, before);
+        if (first >= 0) return v0 + first;
+    }
+    return to - 1;
 }
 
 // Whether draft i (of the sequence) is accepted.
@@ -230,30 +249,35 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     int token = -1;
     bool mine = false;   // this warp holds the border
     for (int pass = 0;; ++pass) {
-        const u64 sum = warp_sum<T, N>(r, lo, hi, lane);
+        const bool has_q = r.q != nullptr;
+        const u64 sum = has_q ? warp_sum<true, T, N>(r, lo, hi, lane) : warp_sum<false, T, N>(r, lo, hi, lane);
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
         if (threadIdx.x == 0) {
             u64 t = 0;
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) t = capped(t, s_warp[w]);
             s_block = t;
         }
         cluster.sync();
-        u64 total = 0, before = 0;
-        for (int c = 0; c < blocks; ++c) {
-            if (c == rank) before = total;
-            total = capped(total, *cluster.map_shared_rank(&s_block, c));
+        // lane c holds block c's sum; before: of the blocks before this one, and of its warps before this one
+        const u64 theirs = lane < blocks ? *cluster.map_shared_rank(&s_block, lane) : 0;
+        u64 total = theirs, before = lane < rank ? theirs : (lane >= 16 && lane - 16 < warp ? s_warp[lane - 16] : 0);
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) {
+            total = capped(total, __shfl_xor_sync(kFull, total, sh));
+            before = capped(before, __shfl_xor_sync(kFull, before, sh));
         }
-        cluster.sync();   // every block has read the sums
+        cluster.barrier_arrive();   // every block has read the sums once all have arrived
         if (total > 0) {
             const u64 border = __umul64hi(u, total);   // the sum has to exceed it; below the total
-            for (int w = 0; w < warp; ++w) before = capped(before, s_warp[w]);
             if (before <= border && capped(before, sum) > border) {
                 mine = true;
-                token = find<T, N>(r, lo, hi, border - before, lane);
+                token = has_q ? find<true, T>(r, lo, hi, border - before, lane) : find<false, T>(r, lo, hi, border - before, lane);
             }
-            break;
         }
+        cluster.barrier_wait();
+        if (total > 0) break;
         if (pass == 1 || (r.q == nullptr && r.not_this < 0)) {   // no mass at all: no token
             mine = rank == 0 && warp == 0;
             if (lead) raise_error(a.err, PKV_DEVERR_PROBS);

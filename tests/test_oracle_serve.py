@@ -177,8 +177,8 @@ def test_verify_takes_the_lowest_token_past_the_border():
     assert serve.verify_drafts(two, None, [0], [0, 1], [0.499, 0.0]) == ([1], [0, 0])
     # nothing left over: from the target itself
     assert serve.verify_drafts(np.array([[0.25, 0.0], [1.0, 0]]), np.array([[0.5, 0.5]]), [1], [0, 1], [0.0, 0.9])[1] == [0, -1]
-    assert serve.units([1.0, 2.0 ** -34 * (1 + 2.0 ** -23), 2.0 ** -59, math.nan, -1.0, math.inf]) == \
-        [2 ** 58, 2 ** 24 + 2, 0, 0, 0, 2 ** 58]
+    assert serve.units([1.0, 2.0 ** -22 * (1 + 2.0 ** -23), 2.0 ** -47, 3 * 2.0 ** -47, 2.0 ** -48, math.nan, -1.0, math.inf]) == \
+        [2 ** 46, 2 ** 24 + 2, 0, 2, 0, 0, 0, 2 ** 46]
 
 
 def test_verify_drafts_refuses(L):
