@@ -564,7 +564,7 @@ pkv_status pkv_block_tables_release(int32_t *block_table, const int32_t *first_b
  *                 that share it must not overlap
  * A parent outside [-1, B) sets PKV_DEVERR_PAIR and a length outside [0, MBS * bs] PKV_DEVERR_LEN: the row is
  * empty.  An entry outside [-1, NB) sets PKV_DEVERR_BLOCK and becomes -1.  Rows for which no fresh block is
- * left set PKV_DEVERR_POOL and are empty (what only they named comes free with the next call).
+ * left set PKV_DEVERR_POOL and are empty (what only they named comes free with the next call).  B <= 65536.
  */
 size_t pkv_block_tables_share_workspace_bytes(int B, int MBS, int NB);
 

@@ -313,21 +313,31 @@ def paged_decode_attention_fp8(out, q, k_codes, v_codes, k_scale, v_scale, block
 def kv_block_copy(k_cache, v_cache, pairs, stream=None, count=None) -> None:
     """Copy whole blocks: for each (src, dst) row of int32 pairs [n][2].  count: int32 [1] on the
     device, the number of leading pairs to copy (pkv_kv_block_copy_counted)."""
+    if count is not None:
+        here = _current_device()
+        try:
+            ok = _ready(here, (k_cache, v_cache, pairs, count)) and pairs.dtype is _I32 and count.dtype is _I32 and \
+                v_cache.dtype is k_cache.dtype
+        except AttributeError:   # not a tensor
+            ok = False
+        if not ok:
+            _refuse("kv_block_copy", here, k_cache=(k_cache, None), v_cache=(v_cache, getattr(k_cache, "dtype", None)),
+                    pairs=(pairs, _I32), count=(count, _I32))
+        shape = k_cache.shape
+        if len(shape) != 4 or v_cache.shape != shape or count.numel() != 1:
+            raise ValueError("kv_block_copy: shapes do not match")
+        NB, Hkv, bs, d = shape
+        status = lib().pkv_kv_block_copy_counted(k_cache.data_ptr(), v_cache.data_ptr(), _dtype(k_cache), pairs.data_ptr(),
+                                                 pairs.numel() // 2, count.data_ptr(), Hkv, d, bs, NB, _stream(stream, here))
+        if status:
+            _check(status)
+        return
     _cuda("k_cache", k_cache)
     dt = _dtype(k_cache)
     _cuda("v_cache", v_cache, k_cache.dtype)
     _cuda("pairs", pairs, torch.int32)
     NB, Hkv, bs, d = k_cache.shape
     n = pairs.numel() // 2
-    if count is not None:
-        here = _current_device()
-        _refuse("kv_block_copy", here, k_cache=(k_cache, None), v_cache=(v_cache, k_cache.dtype), pairs=(pairs, _I32),
-                count=(count, _I32))
-        if v_cache.shape != k_cache.shape or count.numel() != 1:
-            raise ValueError("kv_block_copy: shapes do not match")
-        _check(lib().pkv_kv_block_copy_counted(_ptr(k_cache), _ptr(v_cache), dt, _ptr(pairs), n, _ptr(count), Hkv, d, bs,
-                                               NB, _stream(stream, here)))
-        return
     _check(lib().pkv_kv_block_copy(_ptr(k_cache), _ptr(v_cache), dt, _ptr(pairs), n, Hkv, d, bs,
                                    NB, _stream(stream)))
 
@@ -828,27 +838,36 @@ def block_tables_share_workspace_bytes(B, MBS, NB) -> int:
     return int(lib().pkv_block_tables_share_workspace_bytes(int(B), int(MBS), int(NB)))
 
 
-def _share(what, **tensors):
-    """Checks of block_tables_fork and block_tables_compact; returns (B, MBS, NB, current device)."""
+def _share(what, required, optional, workspace):
+    """Checks of block_tables_fork and block_tables_compact: required and optional are name -> int32 tensor
+    (the optional ones may be None); returns (B, MBS, NB, current device)."""
     here = _current_device()
     try:
-        ok = _ready(here, tensors.values()) and all([t is None or name == "workspace" or t.dtype is _I32
-                                                     for name, t in tensors.items()])
+        ok = _ready(here, (workspace, *optional.values()))
+        for t in required.values():
+            ok = ok and t.get_device() == here and t.is_contiguous() and t.dtype is _I32
+        for t in optional.values():
+            ok = ok and (t is None or t.dtype is _I32)
     except AttributeError:   # not a tensor
         ok = False
-    if not ok or any([t is None and name not in _OPTIONAL for name, t in tensors.items()]):
-        _refuse(what, here, **{name: (t, None if name == "workspace" else _I32) for name, t in tensors.items()})
-    table = tensors["block_table"].shape
+    if not ok:
+        for name, t in required.items():
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+        _refuse(what, here, **{name: (t, _I32) for name, t in (*required.items(), *optional.items())}, workspace=(workspace, None))
+    table = required["block_table"].shape
     if len(table) != 2:
         raise ValueError(f"{what}: block_table must be [B][MBS]")
-    B, NB = table[0], tensors["free_list"].numel()
-    want = {"block_table_out": table[0] * table[1], "context_lens": B, "context_lens_out": B, "parents": B, "held": NB,
-            "refs": NB, "free_count": 1, "pair_count": 1}
-    for name, n in want.items():
-        t = tensors.get(name)
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{what}: {name} must hold {n} numbers, got {t.numel()}")
-    return B, table[1], NB, here
+    B, MBS = table
+    NB = required["free_list"].numel()
+    if required["block_table_out"].numel() != B * MBS or required["context_lens"].numel() != B or \
+            required["refs"].numel() != NB or required["free_count"].numel() != 1 or required["pair_count"].numel() != 1:
+        raise ValueError(f"{what}: shapes do not match (block_table, block_table_out [B][MBS], context_lens [B], refs, "
+                         "free_list [NB], free_count, pair_count [1])")
+    for name, t in optional.items():
+        if t is not None and t.numel() != (NB if name == "held" else B):
+            raise ValueError(f"{what}: {name} must hold {NB if name == 'held' else B} numbers, got {t.numel()}")
+    return B, MBS, NB, here
 
 
 def block_tables_fork(block_table, context_lens, parents, block_table_out, context_lens_out, refs, free_list, free_count,
@@ -857,14 +876,12 @@ def block_tables_fork(block_table, context_lens, parents, block_table_out, conte
     its blocks but for a partly filled last one; references counted anew, blocks without any free
     (see pkv.h).  refs, free_list int32 [NB], free_count, pair_count int32 [1], pairs int32 [B][2]:
     the copies to run with kv_block_copy(..., pairs, count=pair_count).  held: int32 [NB] or None."""
-    B, MBS, NB, here = _share("block_tables_fork", block_table=block_table, context_lens=context_lens, parents=parents,
-                              block_table_out=block_table_out, context_lens_out=context_lens_out, refs=refs,
-                              free_list=free_list, free_count=free_count, pairs=pairs, pair_count=pair_count, held=held,
-                              workspace=workspace)
-    if context_lens_out is None:
-        raise TypeError("context_lens_out must be a torch.Tensor")
-    if pairs.numel() != 2 * B:
-        raise ValueError(f"block_tables_fork: pairs must be [{B}][2]")
+    B, MBS, NB, here = _share("block_tables_fork",
+                              dict(block_table=block_table, context_lens=context_lens, block_table_out=block_table_out,
+                                   context_lens_out=context_lens_out, refs=refs, free_list=free_list, free_count=free_count,
+                                   pairs=pairs, pair_count=pair_count), dict(parents=parents, held=held), workspace)
+    if pairs.numel() != 2 * B or context_lens_out.numel() != B:
+        raise ValueError(f"block_tables_fork: pairs must be [{B}][2] and context_lens_out [{B}]")
     status = lib().pkv_block_tables_fork(
         block_table.data_ptr(), context_lens.data_ptr(), _ptr(parents), _ptr(held), block_table_out.data_ptr(),
         context_lens_out.data_ptr(), refs.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(),
@@ -877,15 +894,16 @@ def block_tables_compact(block_table, context_lens, block_table_out, refs, free_
                          held=None, workspace=None, stream=None) -> None:
     """The blocks in use moved to the lowest ids (see pkv.h); pairs int32 [NB // 2][2], the other
     tensors as block_tables_fork."""
-    B, MBS, NB, here = _share("block_tables_compact", block_table=block_table, context_lens=context_lens,
-                              block_table_out=block_table_out, refs=refs, free_list=free_list, free_count=free_count,
-                              pairs=pairs, pair_count=pair_count, held=held, workspace=workspace)
+    B, MBS, NB, here = _share("block_tables_compact",
+                              dict(block_table=block_table, context_lens=context_lens, block_table_out=block_table_out, refs=refs,
+                                   free_list=free_list, free_count=free_count, pairs=pairs, pair_count=pair_count),
+                              dict(held=held), workspace)
     if pairs.numel() != NB // 2 * 2:
         raise ValueError(f"block_tables_compact: pairs must be [{NB // 2}][2]")
     status = lib().pkv_block_tables_compact(
         block_table.data_ptr(), context_lens.data_ptr(), _ptr(held), block_table_out.data_ptr(), refs.data_ptr(),
         free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(), pair_count.data_ptr(), B, MBS, int(bs), NB,
-        _ptr(workspace), _bytes(workspace), _stream(stream, here))
+        workspace.data_ptr(), _bytes(workspace), _stream(stream, here))
     if status:
         _check(status)
 
@@ -907,14 +925,12 @@ def rope_turns(rot, base=10000.0, scaling="none", factor=1.0, original=1, low=1.
     return turns.to(device)
 
 
-def _heads(what, name, t, d=None):
+def _heads(what, name, t, H, d) -> int:
     """Elements between the tokens of t [T][H][d], whose rows [H][d] are contiguous."""
-    if t.dim() != 3 or (d is not None and t.shape[2] != d):
-        raise ValueError(f"{what}: {name} must be [T][heads][{'d' if d is None else d}]")
-    T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+    token, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and H > 1):
         raise ValueError(f"{what}: the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else H * d
+    return token if t.shape[0] > 1 else H * d
 
 
 def _rope_check(what, q_out, q, positions, turns, here, **more):
@@ -941,20 +957,30 @@ def rope_append(q_out, q, k_new, v_new, k_cache, v_cache, positions, slot_mappin
     v_new may be any distance apart (views of packed rows).  turns: rope_turns(rot), of the first rot
     dimensions; pairs (j, j + rot / 2), or (2j, 2j + 1) when interleaved."""
     what, here = "rope_append", _current_device()
-    dt = getattr(q, "dtype", None)
-    _rope_check(what, q_out, q, positions, turns, here, k_new=(k_new, dt, True), v_new=(v_new, dt, True),
-                k_cache=(k_cache, dt, False), v_cache=(v_cache, dt, False), slot_mapping=(slot_mapping, _I64, False))
-    T, Hq, d = q.shape
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != d or slot_mapping.numel() != T:
-        raise ValueError("rope_append: shapes do not match")
-    NB, Hkv, bs, _ = k_cache.shape
-    if tuple(k_new.shape) != (T, Hkv, d) or tuple(v_new.shape) != (T, Hkv, d):
-        raise ValueError("rope_append: k_new and v_new must be [T][Hkv][d]")
+    try:   # the common outcome of the checks below, without their detours
+        dt, shape = q.dtype, q.shape
+        ok = (_ready(here, (q_out, k_cache, v_cache, positions, slot_mapping, turns)) and q.get_device() == here and
+              k_new.get_device() == here and v_new.get_device() == here and k_new.dtype is dt and v_new.dtype is dt and
+              k_cache.dtype is dt and v_cache.dtype is dt and positions.dtype is _I32 and slot_mapping.dtype is _I64 and
+              turns.dtype is _I64 and len(shape) == 3 and q_out.shape == shape and positions.numel() == shape[0])
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        dt = getattr(q, "dtype", None)
+        _rope_check(what, q_out, q, positions, turns, here, k_new=(k_new, dt, True), v_new=(v_new, dt, True),
+                    k_cache=(k_cache, dt, False), v_cache=(v_cache, dt, False), slot_mapping=(slot_mapping, _I64, False))
+        shape = q.shape
+    T, Hq, d = shape
+    cache, new = k_cache.shape, k_new.shape
+    if len(cache) != 4 or v_cache.shape != cache or cache[3] != d or slot_mapping.numel() != T or len(new) != 3 or \
+            v_new.shape != new or new[0] != T or new[1] != cache[1] or new[2] != d:
+        raise ValueError("rope_append: shapes do not match (k_new, v_new [T][Hkv][d], caches [NB][Hkv][bs][d], slot_mapping [T])")
+    NB, Hkv, bs, _ = cache
     status = lib().pkv_rope_append(
-        q_out.data_ptr(), _dtype(q_out), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype(q), _heads(what, "q", q),
-        _heads(what, "k_new", k_new), _heads(what, "v_new", v_new), positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(),
-        1 if interleaved else 0, float(mscale), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv,
-        d, bs, NB, _stream(stream, here))
+        q_out.data_ptr(), _dtype(q_out), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype(q), _heads(what, "q", q, Hq, d),
+        _heads(what, "k_new", k_new, Hkv, d), _heads(what, "v_new", v_new, Hkv, d), positions.data_ptr(), turns.data_ptr(),
+        2 * turns.numel(), 1 if interleaved else 0, float(mscale), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq,
+        Hkv, d, bs, NB, _stream(stream, here))
     if status:
         _check(status)
 
@@ -963,19 +989,30 @@ def rope(q_out, q, k_out, k, positions, turns, interleaved=False, mscale=1.0, in
     """q [T][Hq][d] rotated into q_out (fp32 or bf16) and k [T][Hkv][d] into k_out (its type; both None:
     q alone), as rope_append does.  inverse: rotated back (the gradient of the rotation)."""
     what, here = "rope", _current_device()
-    dt = getattr(q, "dtype", None)
-    more = {} if k is None and k_out is None else {"k": (k, dt, True), "k_out": (k_out, dt, False)}
-    _rope_check(what, q_out, q, positions, turns, here, **more)
-    T, Hq, d = q.shape
-    Hkv = 1
-    if more:
-        if k.dim() != 3 or k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
+    with_k = k is not None or k_out is not None
+    try:
+        dt, shape = q.dtype, q.shape
+        ok = (_ready(here, (q_out, positions, turns, k_out)) and q.get_device() == here and positions.dtype is _I32 and
+              turns.dtype is _I64 and len(shape) == 3 and q_out.shape == shape and positions.numel() == shape[0] and
+              (not with_k or (k.get_device() == here and k.dtype is dt and k_out.dtype is dt)))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        dt = getattr(q, "dtype", None)
+        _rope_check(what, q_out, q, positions, turns, here, **({"k": (k, dt, True), "k_out": (k_out, dt, False)} if with_k else {}))
+        shape = q.shape
+    T, Hq, d = shape
+    Hkv, k_stride = 1, 0
+    if with_k:
+        rows = k.shape
+        if len(rows) != 3 or k_out.shape != rows or rows[0] != T or rows[2] != d:
             raise ValueError("rope: k and k_out must be [T][Hkv][d]")
-        Hkv = k.shape[1]
+        Hkv = rows[1]
+        k_stride = _heads(what, "k", k, Hkv, d)
     status = lib().pkv_rope(
-        q_out.data_ptr(), _dtype(q_out), _ptr(k_out), q.data_ptr(), _ptr(k), _dtype(q), _heads(what, "q", q),
-        _heads(what, "k", k) if more else 0, positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(), 1 if interleaved else 0,
-        float(mscale), 1 if inverse else 0, T, Hq, Hkv, d, _stream(stream, here))
+        q_out.data_ptr(), _dtype(q_out), _ptr(k_out), q.data_ptr(), _ptr(k), _dtype(q), _heads(what, "q", q, Hq, d), k_stride,
+        positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(), 1 if interleaved else 0, float(mscale), 1 if inverse else 0, T, Hq, Hkv,
+        d, _stream(stream, here))
     if status:
         _check(status)
 
@@ -991,32 +1028,49 @@ def verify_drafts(accepted, tokens, target_probs, draft_tokens, cu_drafts, unifo
     cu_drafts int32 [B + 1]; uniforms fp32 [D + B]; context_lens, context_lens_out int32 [B]: the
     lengths with the drafts, and without the rejected ones (may be the same)."""
     what, here = "verify_drafts", _current_device()
-    _refuse(what, here, accepted=(accepted, _I32), tokens=(tokens, _I32), draft_tokens=(draft_tokens, _I32),
-            cu_drafts=(cu_drafts, _I32), uniforms=(uniforms, _F32), context_lens_out=(context_lens_out, _I32))
-    if context_lens is not None:
-        _refuse(what, here, context_lens=(context_lens, _I32))
-    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if t is None and name == "draft_probs":
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != here:
-            raise ValueError(f"{what}: {name} is on {t.device}, the current device is {here}")
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what}: {name} must be rows of contiguous probabilities")
-        if t.dtype is not target_probs.dtype:
-            raise TypeError(f"{name} must be {target_probs.dtype}, got {t.dtype}")
+    ints = (accepted, tokens, draft_tokens, cu_drafts)
+    try:
+        dt = target_probs.dtype
+        ok = (_ready(here, (*ints, uniforms, context_lens, context_lens_out)) and accepted.dtype is _I32 and tokens.dtype is _I32 and
+              draft_tokens.dtype is _I32 and cu_drafts.dtype is _I32 and uniforms.dtype is _F32 and
+              (context_lens is None or context_lens.dtype is _I32) and (context_lens_out is None or context_lens_out.dtype is _I32) and
+              target_probs.get_device() == here and (draft_probs is None or (draft_probs.get_device() == here and draft_probs.dtype is dt)))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(what, here, accepted=(accepted, _I32), tokens=(tokens, _I32), draft_tokens=(draft_tokens, _I32),
+                cu_drafts=(cu_drafts, _I32), uniforms=(uniforms, _F32), context_lens_out=(context_lens_out, _I32))
+        if context_lens is not None:
+            _refuse(what, here, context_lens=(context_lens, _I32))
+        for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+            if t is None and name == "draft_probs":
+                continue
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.get_device() != here:
+                raise ValueError(f"{what}: {name} is on {t.device}, the current device is {here}")
+            if t.dtype is not target_probs.dtype:
+                raise TypeError(f"{name} must be {target_probs.dtype}, got {t.dtype}")
+    rows = target_probs.shape
     B, D = accepted.numel(), draft_tokens.numel()
-    V = target_probs.shape[1]
-    if target_probs.shape[0] != D + B or tokens.numel() != D + B or uniforms.numel() != D + B or cu_drafts.numel() != B + 1 or \
-            (draft_probs is not None and tuple(draft_probs.shape) != (D, V)) or \
+    if len(rows) != 2 or rows[0] != D + B or tokens.numel() != D + B or uniforms.numel() != D + B or cu_drafts.numel() != B + 1 or \
+            (draft_probs is not None and (draft_probs.dim() != 2 or draft_probs.shape[0] != D or draft_probs.shape[1] != rows[1])) or \
             (context_lens is not None and context_lens.numel() != B) or \
             (context_lens_out is not None and context_lens_out.numel() != B):
         raise ValueError("verify_drafts: shapes do not match")
-    apart = lambda t: t.stride(0) if t is not None and t.shape[0] > 1 else V
+    V = rows[1]
+
+    def apart(name, t, n):   # elements between rows
+        row, one = t.stride()
+        if one != 1 and V > 1:
+            raise ValueError(f"verify_drafts: {name} must be rows of contiguous probabilities")
+        return row if n > 1 else V
+
+    target_apart = apart("target_probs", target_probs, D + B)
+    draft_apart = apart("draft_probs", draft_probs, D) if draft_probs is not None else 0
     status = lib().pkv_verify_drafts(
         accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(), _ptr(draft_probs) if D > 0 else 0, _dtype(target_probs),
-        apart(target_probs), apart(draft_probs), draft_tokens.data_ptr(), cu_drafts.data_ptr(), uniforms.data_ptr(),
+        target_apart, draft_apart, draft_tokens.data_ptr(), cu_drafts.data_ptr(), uniforms.data_ptr(),
         _ptr(context_lens), _ptr(context_lens_out), B, D, V, _stream(stream, here))
     if status:
         _check(status)
@@ -1057,7 +1111,7 @@ def paged_attention_sinks(out, q, k_cache, v_cache, block_table, context_lens, s
         raise ValueError(f"{what}: shapes do not match")
     status = lib().pkv_paged_attention_sinks(
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dt, block_table.data_ptr(),
-        context_lens.data_ptr(), _ptr(cu_q), B, Tq, int(max_q), Hq, Hkv, d, bs, table[1], NB, float(scale), int(window),
-        int(sinks), int(num_splits), _ptr(workspace), _bytes(workspace), _stream(stream, here))
+        context_lens.data_ptr(), _ptr(cu_q), B, Tq, int(max_q), Hq, Hkv, d, bs, table[1], NB, float(scale), int(window), int(sinks),
+        int(num_splits), _ptr(workspace), _bytes(workspace), _stream(stream, here))
     if status:
         _check(status)

@@ -69,8 +69,8 @@ pkv_status check_in_place(const char *what, const char *name, const void *out, u
 pkv_status check_share(const char *what, int B, int MBS, int bs, int NB, const void *table, const void *lens, const void *table_out,
                        const void *refs, const void *free_list, const void *free_count, const void *pairs, const void *pair_count,
                        bool want_pairs, const void *workspace, size_t workspace_bytes) {
-    if (B < 0 || MBS < 1 || bs < 1 || NB < 1 || static_cast<long long>(MBS) * bs > 0x7fffffffll - bs)
-        return fail(PKV_ERR_INVALID_ARG, "%s: B=%d MBS=%d bs=%d NB=%d", what, B, MBS, bs, NB);
+    if (B < 0 || B > 65536 || MBS < 1 || bs < 1 || NB < 1 || static_cast<long long>(MBS) * bs > 0x7fffffffll - bs)
+        return fail(PKV_ERR_INVALID_ARG, "%s: B=%d MBS=%d bs=%d NB=%d (need B <= 65536)", what, B, MBS, bs, NB);
     if (!refs || !free_list || !free_count || !pair_count || (want_pairs && !pairs) || (B > 0 && (!table || !lens || !table_out)))
         return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", what);
     if (want_pairs && !aligned_to(pairs, 8)) return fail(PKV_ERR_INVALID_ARG, "%s: pairs must be 8-byte aligned", what);
@@ -227,7 +227,7 @@ pkv_status pkv_block_tables_fork(const int32_t *block_table, const int32_t *cont
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, parents, held, block_table_out, context_lens_out, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, 0, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, 0, err};
     return done(launch_fork(a, workspace, same && parents != nullptr, stream), "block_tables_fork");
 }
 
@@ -246,7 +246,7 @@ pkv_status pkv_block_tables_compact(const int32_t *block_table, const int32_t *c
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, nullptr, held, block_table_out, nullptr, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, 0, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, 0, err};
     return done(launch_compact(a, workspace, stream), "block_tables_compact");
 }
 

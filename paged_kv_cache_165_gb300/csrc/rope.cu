@@ -74,6 +74,7 @@ template <typename T, typename Tq, bool INTER, int N>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     extern __shared__ float2 s_cs[];   // [tokens of the block][rot / 2]
     __shared__ long long s_row[kMaxTokens];   // K/V row of head 0, -1: none
+    pdl_wait();
     const int pairs = a.rot / 2;
     const long long t0 = static_cast<long long>(blockIdx.x) * a.block_tokens;
     const int nt = static_cast<int>(min(static_cast<long long>(a.block_tokens), a.T - t0));
@@ -178,9 +179,8 @@ cudaError_t launch(const RopeArgs &given, int sm_count, cudaStream_t stream) {
     a.block_tokens = static_cast<int>(std::max(1ll, std::min<long long>(kMaxTokens, a.T / want)));
     const dim3 grid(static_cast<unsigned>((a.T + static_cast<long long>(a.block_tokens) - 1) / a.block_tokens),
                     static_cast<unsigned>(split));
-    rope_kernel<T, Tq, INTER, N>
-        <<<grid, kThreads, static_cast<size_t>(a.block_tokens) * pairs * sizeof(float2), stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(rope_kernel<T, Tq, INTER, N>, grid, dim3(kThreads),
+                            static_cast<size_t>(a.block_tokens) * pairs * sizeof(float2), stream, a);
 }
 
 template <typename T, typename Tq, bool INTER>

@@ -36,6 +36,7 @@ constexpr int kThreads = 1024, kBlocks = 8;
 constexpr unsigned kAll = kThreads * kBlocks;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNobody = 0x7fffffff;
+constexpr int kRowsEach = 8;                               // rows of a thread, at most: 65536 of a call
 constexpr int kSharedShift = 14;                           // at most 2^14 ids a block in shared memory (128 KB)
 constexpr unsigned kSharedIds = kBlocks << kSharedShift;
 
@@ -214,6 +215,7 @@ __device__ __forceinline__ unsigned blocks_of(const ShareArgs &a, int len) {
 template <bool SHARED>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     extern __shared__ int s_ids[];
+    pdl_wait();
     __shared__ int s_warp[1][32], s_part[2];
     cg::cluster_group cluster = cg::this_cluster();
     const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
@@ -235,24 +237,29 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
                 }, same,
                 [&](const Source &s, unsigned b, unsigned j, int x) {
                     x = checked(a, x);
+                    const bool last = s.len % a.bs != 0 && j == static_cast<unsigned>(s.len / a.bs);   // partly filled
                     if (x >= 0) {
-                        if (s.len % a.bs != 0 && j == static_cast<unsigned>(s.len / a.bs)) atomicMin(ids.b(x), static_cast<int>(b));
+                        if (last) atomicMin(ids.b(x), static_cast<int>(b));
                         else atomicAdd(ids.a(x), 1);
                     }
+                    if (last) a.last[b] = x;
+                    if (j == 0) a.place[b] = s.len;
                     rows[static_cast<size_t>(b) * a.MBS + j] = x;
                 });
     cluster.sync();
-    // rows that get a copy of their last block, and free blocks: place[b] remembers the first
-    int mine[2] = {0, 0}, before[2], all[2], total[1];
-    for (unsigned b = b_begin + threadIdx.x; b < b_end; b += kThreads) {
-        const Source s = source_of(a, b, false);
-        int copied = 0;
-        if (s.len % a.bs != 0) {
-            const int x = rows[static_cast<size_t>(b) * a.MBS + s.len / a.bs];
-            copied = x >= 0 && (*ids.a(x) != 0 || *ids.b(x) != static_cast<int>(b));
-        }
-        a.place[b] = copied;
-        mine[0] += copied;
+    // rows that get a copy of their last block, and free blocks; a thread keeps its rows to the end
+    int len[kRowsEach], old[kRowsEach], mine[2] = {0, 0}, before[2], all[2], total[1];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+        const unsigned b = b_begin + k * kThreads + threadIdx.x;
+        len[k] = b < b_end ? a.place[b] : 0;
+        old[k] = b < b_end ? a.last[b] : -1;      // written where the length asks for it
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+        const int b = static_cast<int>(b_begin + k * kThreads + threadIdx.x);
+        if (len[k] % a.bs == 0 || old[k] < 0 || (*ids.a(old[k]) == 0 && *ids.b(old[k]) == b)) old[k] = -1;
+        mine[0] += old[k] >= 0;
     }
     for (unsigned i = i_begin + threadIdx.x; i < i_end; i += kThreads) mine[1] += ids.own_a(i) == 0 && ids.own_b(i) == kNobody;
 #pragma unroll
@@ -263,9 +270,15 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
     }
     share_counts<2>(cluster, mine, s_part, before, all);
     const int served = min(all[0], all[1]), left = all[1] - served;
-    int row_rank[1] = {before[0]}, id_rank[1] = {before[1]};
-    rank_items<1>(b_begin, b_end, row_rank, s_warp, [&](unsigned b, int (&f)[1]) { f[0] = a.place[b]; },
-                  [&](unsigned b, const int (&f)[1], const int (&at)[1]) { a.place[b] = f[0] ? at[0] : -1; });
+    int id_rank[1] = {before[1]}, nth[kRowsEach];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+        if (b_begin + k * kThreads >= b_end) break;   // (the whole block)
+        int x[1] = {old[k] >= 0};
+        block_ranks<1>(x, s_warp, total);
+        nth[k] = before[0] + x[0];
+        before[0] += total[0];
+    }
     rank_items<1>(i_begin, i_end, id_rank, s_warp,
                   [&](unsigned i, int (&f)[1]) { f[0] = ids.own_a(i) == 0 && ids.own_b(i) == kNobody; },
                   [&](unsigned i, const int (&f)[1], const int (&at)[1]) {
@@ -283,28 +296,28 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
         if (served < all[0]) raise_error(a.err, PKV_DEVERR_POOL);
     }
     cluster.sync();
-    for (unsigned b = tid; b < B; b += kAll) {
-        const int len = source_of(a, b, false).len, nth = a.place[b];
-        const size_t last = static_cast<size_t>(b) * a.MBS + len / a.bs;
-        if (nth >= 0 && nth < served) {
-            reinterpret_cast<int2 *>(a.pairs)[nth] = make_int2(rows[last], a.fresh[nth]);
-            rows[last] = a.fresh[nth];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+        const unsigned b = b_begin + k * kThreads + threadIdx.x;
+        if (b >= b_end) break;
+        if (old[k] >= 0 && nth[k] < served) {
+            const int to = a.fresh[nth[k]];
+            reinterpret_cast<int2 *>(a.pairs)[nth[k]] = make_int2(old[k], to);
+            rows[static_cast<size_t>(b) * a.MBS + len[k] / a.bs] = to;
+        } else if (old[k] >= 0) {
+            len[k] = 0;   // the pool was too small for this row: it is empty
         }
-        a.place[b] = nth >= served ? 0 : len;   // its length: none for a row that the pool was too small for
+        a.lens_out[b] = a.place[b] = len[k];
     }
-    if (rows == a.table_out && served == all[0] && a.lens_out != a.lens) {
-        for (unsigned b = tid; b < B; b += kAll) a.lens_out[b] = a.place[b];
-        return;   // (its own rows: no other thread wrote them)
-    }
+    if (rows == a.table_out && served == all[0]) return;
     cluster.sync();
-    for (unsigned b = tid; b < B; b += kAll) a.lens_out[b] = a.place[b];
     if (rows != a.table_out) {
         for_entries(a, warp, lane, warps, [&](unsigned b, bool) { return Source{0, a.place[b]}; },
                     [&](const Source &s, unsigned b, unsigned j) {
                         return s.len == 0 ? -1 : rows[static_cast<size_t>(b) * a.MBS + j];
                     }, same,
                     [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
-    } else if (served < all[0]) {   // rows that the pool was too small for
+    } else {   // rows that the pool was too small for
         for (unsigned b = warp; b < B; b += warps)
             if (a.place[b] == 0)
                 for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) rows[static_cast<size_t>(b) * a.MBS + j] = -1;
@@ -314,6 +327,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
 template <bool SHARED>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
     extern __shared__ int s_ids[];
+    pdl_wait();
     __shared__ int s_warp[3][32], s_part[3], s_warp1[1][32], s_part1[1];
     cg::cluster_group cluster = cg::this_cluster();
     const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
@@ -398,6 +412,7 @@ template <typename U>
 __global__ void __launch_bounds__(kCopyThreads)
     kv_block_copy_counted_kernel(U *__restrict__ kc, U *__restrict__ vc, const int32_t *__restrict__ pairs, int n,
                                  const int32_t *__restrict__ count, long long block_units, int NB, unsigned *err) {
+    pdl_wait();
     int live = __ldg(count);
     if (live < 0 || live > n) {
         if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(err, PKV_DEVERR_PAIR);
@@ -429,10 +444,10 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 }  // namespace
 
-// Scratch behind a call: one number a block [NB], a row's length or place [B], fresh blocks [B] or ids that
-// blocks move to [NB / 2], and the table where it replaces the one that it is built from ([B][MBS]).
+// Scratch behind a call: one number a block [NB], a row's length and last block [B] each, fresh blocks [B] or
+// ids that blocks move to [NB / 2], and the table where it replaces the one that it is built from ([B][MBS]).
 size_t share_workspace_bytes(int B, int MBS, int NB) {
-    return (static_cast<size_t>(NB) + static_cast<size_t>(B) + std::max(static_cast<size_t>(B), static_cast<size_t>(NB) / 2) +
+    return (static_cast<size_t>(NB) + 2 * static_cast<size_t>(B) + std::max(static_cast<size_t>(B), static_cast<size_t>(NB) / 2) +
             static_cast<size_t>(B) * MBS) *
            sizeof(int32_t);
 }
@@ -450,8 +465,7 @@ template <typename Kernel>
 cudaError_t launch_cluster(Kernel shared, Kernel global, ShareArgs a, std::atomic<unsigned long long> &ready, cudaStream_t stream) {
     a.shift = id_shift(a.NB);
     if (static_cast<unsigned>(a.NB) > kSharedIds) {
-        global<<<kBlocks, kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+        return launch_dependent(global, dim3(kBlocks), dim3(kThreads), 0, stream, a);
     }
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -462,8 +476,7 @@ cudaError_t launch_cluster(Kernel shared, Kernel global, ShareArgs a, std::atomi
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
-    shared<<<kBlocks, kThreads, 2 * sizeof(int) << a.shift, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(shared, dim3(kBlocks), dim3(kThreads), 2 * sizeof(int) << a.shift, stream, a);
 }
 
 }  // namespace
@@ -473,7 +486,8 @@ cudaError_t launch_fork(ShareArgs a, void *workspace, bool aside, cudaStream_t s
     int32_t *ws = static_cast<int32_t *>(workspace);
     a.first = ws;
     a.place = ws + a.NB;
-    a.fresh = a.place + a.B;
+    a.last = a.place + a.B;
+    a.fresh = a.last + a.B;
     a.rows = aside ? a.fresh + std::max(a.B, a.NB / 2) : a.table_out;
     return launch_cluster(fork_kernel<true>, fork_kernel<false>, a, ready, stream);
 }
@@ -482,7 +496,7 @@ cudaError_t launch_compact(ShareArgs a, void *workspace, cudaStream_t stream) {
     static std::atomic<unsigned long long> ready{0};
     int32_t *ws = static_cast<int32_t *>(workspace);
     a.first = ws;
-    a.fresh = ws + a.NB + a.B;
+    a.fresh = ws + a.NB + 2 * static_cast<size_t>(a.B);
     return launch_cluster(compact_kernel<true>, compact_kernel<false>, a, ready, stream);
 }
 
@@ -496,16 +510,15 @@ cudaError_t launch_kv_block_copy_counted(void *k_cache, void *v_cache, int elem_
     const long long units = static_cast<long long>(bytes / u), span = kCopyThreads * kCopyAhead;
     const unsigned grid = static_cast<unsigned>(std::min(2ll * n * ((units + span - 1) / span), 8ll * std::max(sm_count, 1)));
 #define PKV_COPY(UT)                                                                                                     \
-    kv_block_copy_counted_kernel<UT><<<grid, kCopyThreads, 0, stream>>>(static_cast<UT *>(k_cache),                     \
-                                                                        static_cast<UT *>(v_cache), pairs, n, count, units, NB, err)
+    return launch_dependent(kv_block_copy_counted_kernel<UT>, dim3(grid), dim3(kCopyThreads), 0, stream,                 \
+                            static_cast<UT *>(k_cache), static_cast<UT *>(v_cache), pairs, n, count, units, NB, err)
     switch (u) {
-        case 16: PKV_COPY(uint4); break;
-        case 4: PKV_COPY(uint32_t); break;
-        case 2: PKV_COPY(uint16_t); break;
-        default: PKV_COPY(uint8_t); break;
+        case 16: PKV_COPY(uint4);
+        case 4: PKV_COPY(uint32_t);
+        case 2: PKV_COPY(uint16_t);
+        default: PKV_COPY(uint8_t);
     }
 #undef PKV_COPY
-    return cudaGetLastError();
 }
 
 }  // namespace pkv

@@ -198,6 +198,7 @@ template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
     __shared__ u64 s_warp[kWarps], s_block;   // sums of the warps' runs; of the block's
     __shared__ int s_accepted;
+    pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
     const int b = blockIdx.x / blocks;
@@ -303,12 +304,14 @@ cudaError_t launch(const VerifyArgs &a, int blocks, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_dependent
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, verify_kernel<T, N>, a);
 }
 
