@@ -227,7 +227,7 @@ pkv_status pkv_block_tables_fork(const int32_t *block_table, const int32_t *cont
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, parents, held, block_table_out, context_lens_out, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, 0, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, err};
     return done(launch_fork(a, workspace, same && parents != nullptr, stream), "block_tables_fork");
 }
 
@@ -246,7 +246,7 @@ pkv_status pkv_block_tables_compact(const int32_t *block_table, const int32_t *c
     s = current_device_info(&sm_count, &err);
     if (s != PKV_OK) return s;
     ShareArgs a{block_table, context_lens, nullptr, held, block_table_out, nullptr, refs, free_list, free_count,
-                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, 0, err};
+                pair_count, pairs, B, MBS, bs, NB, nullptr, nullptr, nullptr, nullptr, nullptr, err};
     return done(launch_compact(a, workspace, stream), "block_tables_compact");
 }
 

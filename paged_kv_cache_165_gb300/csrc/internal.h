@@ -247,7 +247,6 @@ struct ShareArgs {
     int32_t *pairs;              // [B][2] (fork), [NB / 2][2] (compact)
     int B, MBS, bs, NB;
     int32_t *first, *place, *last, *fresh, *rows;   // scratch, set by the launch
-    int shift;                   // 2^shift ids to a thread block, likewise
     unsigned *err;
 };
 

@@ -13,12 +13,11 @@
 //   a fresh block (the pair list).  Fresh blocks are the lowest free ids, in row order.
 // compact: with n blocks in use, the i-th used block from id n on moves to the i-th free id below n.
 //
-// Both run as one cluster of 8 x 1024 threads in place of four or five launches.  Every block of the cluster
-// owns a run of the ids and keeps their counts (and the rows that end in them, or where they move) in its
-// shared memory, which the others reach as distributed shared memory: counting is remote atomics, scanning is
-// local, and a phase (clear, count, scan, write) ends with a hardware cluster barrier and no trip to L2.  Pools
-// of more than kSharedIds ids keep the same numbers in global memory.  Tables of a serving batch are some 10^4
-// to 10^5 entries: bound by the latency of the phases.
+// Both are one launch and bound by the latency of their phases (clear, count, scan, write): tables of a serving
+// batch are some 10^2 to 10^5 entries.  Small ones run as one block of 1024 threads that keeps the counts in
+// shared memory, where a phase ends with __syncthreads.  Larger ones run as a cluster of eight such blocks with
+// the counts in global memory and hardware cluster barriers (about 0.9 us each); counts spread over the
+// cluster's shared memories measured no faster (a pool of 25234 ids 25.7 us, 23.4 in global memory).
 #include <algorithm>
 #include <atomic>
 
@@ -32,13 +31,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024, kBlocks = 8;
-constexpr unsigned kAll = kThreads * kBlocks;
+constexpr int kThreads = 1024, kBlocks = 8;                // of the cluster
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNobody = 0x7fffffff;
 constexpr int kRowsEach = 8;                               // rows of a thread, at most: 65536 of a call
-constexpr int kSharedShift = 14;                           // at most 2^14 ids a block in shared memory (128 KB)
-constexpr unsigned kSharedIds = kBlocks << kSharedShift;
+// what one block takes: two numbers an id and two a row in shared memory, four entries a thread
+constexpr int kOneIds = 24576, kOneRows = 2048, kOneEntries = 4096;
 
 // Exclusive ranks of N flags counted over a block's threads; totals[i]: the block's.  All threads call it.
 template <int N>
@@ -78,23 +76,22 @@ __device__ __forceinline__ void block_ranks(int (&x)[N], int (&s_warp)[N][32], i
     }
 }
 
-// Two numbers for every id: the owner of id i is block i >> shift of the cluster.  SHARED: in its shared
-// memory; else in global memory.
-template <bool SHARED>
-struct Ids {
-    cg::cluster_group &cluster;
-    int *a_, *b_;      // this block's shared arrays, or the global ones
-    int shift;
-
-    __device__ __forceinline__ int *at(int *base, unsigned i) const {
-        if constexpr (SHARED) return cluster.map_shared_rank(base, i >> shift) + (i & ((1u << shift) - 1));
-        else return base + i;
+// The blocks of a launch: one, or the cluster.
+template <bool ONE>
+struct Team {
+    static constexpr unsigned kTeam = ONE ? 1 : kBlocks, kAll = kTeam * kThreads;
+    unsigned rank;
+    __device__ __forceinline__ Team() : rank(ONE ? 0u : cg::this_cluster().block_rank()) {}
+    __device__ __forceinline__ unsigned tid() const { return rank * kThreads + threadIdx.x; }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (ONE) __syncthreads();
+        else cg::this_cluster().sync();
     }
-    __device__ __forceinline__ int *a(unsigned i) const { return at(a_, i); }
-    __device__ __forceinline__ int *b(unsigned i) const { return at(b_, i); }
-    // an id of this block's own
-    __device__ __forceinline__ int &own_a(unsigned i) const { return SHARED ? a_[i & ((1u << shift) - 1)] : a_[i]; }
-    __device__ __forceinline__ int &own_b(unsigned i) const { return SHARED ? b_[i & ((1u << shift) - 1)] : b_[i]; }
+    // this block's part of n items
+    __device__ __forceinline__ uint2 part(unsigned n) const {
+        const unsigned each = (n + kTeam - 1) / kTeam;
+        return make_uint2(min(n, rank * each), min(n, (rank + 1) * each));
+    }
 };
 
 // Items [begin, end) in index order, four a thread: flags(i, f) says which of N kinds an item is, use(i, f, rank)
@@ -130,27 +127,36 @@ __device__ __forceinline__ void rank_items(unsigned begin, unsigned end, int (&r
 }
 
 // The sums of N counts over the blocks before this one (before) and over all (all), by way of s_part, which
-// is not written again.  Ends with a cluster barrier.
-template <int N>
-__device__ __forceinline__ void share_counts(cg::cluster_group &cluster, const int (&mine)[N], int (&s_part)[N], int (&before)[N],
+// is not written again.  Ends with a barrier of the team.
+template <bool ONE, int N>
+__device__ __forceinline__ void share_counts(const Team<ONE> &team, const int (&mine)[N], int (&s_part)[N], int (&before)[N],
                                              int (&all)[N]) {
-    if (threadIdx.x == 0) {
+    if constexpr (ONE) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) s_part[n] = mine[n];
-    }
-    cluster.sync();
-    int theirs[kBlocks][N];
+        for (int n = 0; n < N; ++n) {
+            before[n] = 0;
+            all[n] = mine[n];
+        }
+    } else {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (threadIdx.x == 0) {
 #pragma unroll
-    for (int c = 0; c < kBlocks; ++c)
+            for (int n = 0; n < N; ++n) s_part[n] = mine[n];
+        }
+        cluster.sync();
+        int theirs[kBlocks][N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) theirs[c][n] = cluster.map_shared_rank(&s_part[0], c)[n];
+        for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        before[n] = all[n] = 0;
+            for (int n = 0; n < N; ++n) theirs[c][n] = cluster.map_shared_rank(&s_part[0], c)[n];
 #pragma unroll
-        for (int c = 0; c < kBlocks; ++c) {
-            if (c < static_cast<int>(cluster.block_rank())) before[n] += theirs[c][n];
-            all[n] += theirs[c][n];
+        for (int n = 0; n < N; ++n) {
+            before[n] = all[n] = 0;
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) {
+                if (c < static_cast<int>(team.rank)) before[n] += theirs[c][n];
+                all[n] += theirs[c][n];
+            }
         }
     }
 }
@@ -183,55 +189,85 @@ __device__ __forceinline__ int checked(const ShareArgs &a, int x) {
     return -1;
 }
 
-// Every entry of the B rows, 256 of a row to a warp at a time, eight a lane: first all are loaded
-// (x = load(source, b, j)), then all looked up (x = map(x)), then all put to use (at(source, b, j, x)), so that
-// a lane's eight loads overlap.
-constexpr int kAhead = 8, kSegment = 32 * kAhead;
-
-template <typename From, typename Load, typename Map, typename At>
-__device__ __forceinline__ void for_entries(const ShareArgs &a, unsigned warp, unsigned lane, unsigned warps, From from, Load load,
-                                            Map map, At at) {
-    const unsigned MBS = a.MBS, segments = (MBS + kSegment - 1) / kSegment;
-    const unsigned long long items = static_cast<unsigned long long>(a.B) * segments;
-    for (unsigned long long i = warp; i < items; i += warps) {
-        const unsigned b = static_cast<unsigned>(i / segments);
-        const unsigned j0 = static_cast<unsigned>(i - static_cast<unsigned long long>(b) * segments) * kSegment + lane;
-        const Source s = from(b, j0 == 0);
-        int x[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) x[k] = j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (j0 + 32 * k < MBS) at(s, b, j0 + 32 * k, x[k]);
-    }
-}
-
 __device__ __forceinline__ unsigned blocks_of(const ShareArgs &a, int len) {
     return static_cast<unsigned>((static_cast<long long>(len) + a.bs - 1) / a.bs);
 }
 
-template <bool SHARED>
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
-    extern __shared__ int s_ids[];
-    pdl_wait();
-    __shared__ int s_warp[1][32], s_part[2];
-    cg::cluster_group cluster = cg::this_cluster();
-    const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
-    const unsigned NB = a.NB, B = a.B, warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
-    // refs: entries that name a block inside a row, or hold it (a); first: the lowest row that ends in it, partly filled (b)
-    const Ids<SHARED> ids{cluster, SHARED ? s_ids : a.refs, SHARED ? s_ids + (1 << a.shift) : a.first, a.shift};
-    const unsigned i_begin = min(NB, rank << a.shift), i_end = min(NB, (rank + 1) << a.shift);
-    const unsigned rows_each = (B + kBlocks - 1) / kBlocks, b_begin = min(B, rank * rows_each), b_end = min(B, (rank + 1) * rows_each);
-    for (unsigned i = i_begin + threadIdx.x; i < i_end; i += kThreads) {
-        ids.own_a(i) = a.held != nullptr && __ldg(a.held + i) != 0 ? 1 : 0;
-        ids.own_b(i) = kNobody;
+// Every entry of the B rows, eight a thread at a time: first all are loaded (x = load(source, b, j)), then all
+// looked up (x = map(x)), then all put to use (use(source, b, j, x)), so that a thread's loads overlap.
+// ONE: entries one after the other, their rows' sources (s_rows) at hand; else 256 entries of a row to a warp.
+constexpr int kAhead = 8, kSegment = 32 * kAhead;
+
+template <bool ONE, typename Load, typename Map, typename Use>
+__device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> &team, const Source *s_rows, bool report, Load load,
+                                            Map map, Use use) {
+    const unsigned MBS = a.MBS;
+    if constexpr (ONE) {
+        // i / MBS for i, MBS <= 65536 (i < 2^16 where MBS > 1): the rounding of 2^32 / MBS upwards adds less than 1 / MBS
+        const unsigned total = a.B * MBS, inv = MBS > 1 ? 0xffffffffu / MBS + 1 : 0;
+        for (unsigned i0 = threadIdx.x; i0 < total; i0 += kAhead * kThreads) {
+            int x[kAhead];
+            unsigned row[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const unsigned i = i0 + k * kThreads;
+                row[k] = MBS > 1 ? __umulhi(i, inv) : i;
+                x[k] = i < total ? load(s_rows[row[k]], row[k], i - row[k] * MBS) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const unsigned i = i0 + k * kThreads;
+                if (i < total) use(s_rows[row[k]], row[k], i - row[k] * MBS, x[k]);
+            }
+        }
+    } else {
+        const unsigned warp = team.tid() >> 5, lane = threadIdx.x & 31, segments = (MBS + kSegment - 1) / kSegment;
+        const unsigned long long items = static_cast<unsigned long long>(a.B) * segments;
+        for (unsigned long long i = warp; i < items; i += Team<ONE>::kAll / 32) {
+            const unsigned b = static_cast<unsigned>(i / segments);
+            const unsigned j0 = static_cast<unsigned>(i - static_cast<unsigned long long>(b) * segments) * kSegment + lane;
+            const Source s = source_of(a, b, report && j0 == 0);
+            int x[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x[k] = j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (j0 + 32 * k < MBS) use(s, b, j0 + 32 * k, x[k]);
+        }
     }
-    cluster.sync();
+}
+
+// The start of both kernels: the ids' two numbers (in shared memory for one block) cleared to (held, second), and one
+// block's rows' sources.
+template <bool ONE>
+__device__ __forceinline__ void clear(const ShareArgs &a, const Team<ONE> &team, int *refs, int *other, int second, Source *s_rows) {
+    for (unsigned i = team.tid(); i < static_cast<unsigned>(a.NB); i += Team<ONE>::kAll) {
+        refs[i] = a.held != nullptr && __ldg(a.held + i) != 0 ? 1 : 0;
+        other[i] = second;
+    }
+    if constexpr (ONE)
+        for (unsigned b = threadIdx.x; b < static_cast<unsigned>(a.B); b += kThreads) s_rows[b] = source_of(a, b, true);
+    team.sync();
+}
+
+template <bool ONE>
+__global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
+    extern __shared__ int s_ids[];
+    __shared__ int s_warp[1][32], s_part[2];
+    pdl_wait();
+    const Team<ONE> team;
+    const unsigned tid = team.tid(), NB = a.NB, B = a.B;
+    int *refs = ONE ? s_ids : a.refs;              // entries that name a block inside a row, or hold it
+    int *first = ONE ? s_ids + NB : a.first;       // the lowest row that ends, partly filled, in it
+    Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
+    clear(a, team, refs, first, kNobody, s_rows);
     int32_t *rows = a.rows;   // [B][MBS] of the result: the table itself where nothing reads the parents' rows any more
     auto same = [](int x) { return x; };
-    for_entries(a, warp, lane, warps, [&](unsigned b, bool report) { return source_of(a, b, report); },
+    for_entries(a, team, s_rows, true,
                 [&](const Source &s, unsigned, unsigned j) {
                     return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(max(s.row, 0)) * a.MBS + j] : -1;
                 }, same,
@@ -239,67 +275,69 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
                     x = checked(a, x);
                     const bool last = s.len % a.bs != 0 && j == static_cast<unsigned>(s.len / a.bs);   // partly filled
                     if (x >= 0) {
-                        if (last) atomicMin(ids.b(x), static_cast<int>(b));
-                        else atomicAdd(ids.a(x), 1);
+                        if (last) atomicMin(first + x, static_cast<int>(b));
+                        else atomicAdd(refs + x, 1);
                     }
                     if (last) a.last[b] = x;
                     if (j == 0) a.place[b] = s.len;
                     rows[static_cast<size_t>(b) * a.MBS + j] = x;
                 });
-    cluster.sync();
+    team.sync();
     // rows that get a copy of their last block, and free blocks; a thread keeps its rows to the end
+    const uint2 my_rows = team.part(B), my_ids = team.part(NB);
     int len[kRowsEach], old[kRowsEach], mine[2] = {0, 0}, before[2], all[2], total[1];
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const unsigned b = b_begin + k * kThreads + threadIdx.x;
-        len[k] = b < b_end ? a.place[b] : 0;
-        old[k] = b < b_end ? a.last[b] : -1;      // written where the length asks for it
+        const unsigned b = my_rows.x + k * kThreads + threadIdx.x;
+        len[k] = b < my_rows.y ? a.place[b] : 0;
+        old[k] = b < my_rows.y ? a.last[b] : -1;      // written where the length asks for it
     }
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const int b = static_cast<int>(b_begin + k * kThreads + threadIdx.x);
-        if (len[k] % a.bs == 0 || old[k] < 0 || (*ids.a(old[k]) == 0 && *ids.b(old[k]) == b)) old[k] = -1;
+        const int b = static_cast<int>(my_rows.x + k * kThreads + threadIdx.x);
+        if (len[k] % a.bs == 0 || old[k] < 0 || (refs[old[k]] == 0 && first[old[k]] == b)) old[k] = -1;
         mine[0] += old[k] >= 0;
     }
-    for (unsigned i = i_begin + threadIdx.x; i < i_end; i += kThreads) mine[1] += ids.own_a(i) == 0 && ids.own_b(i) == kNobody;
+    auto unused = [&](unsigned i) { return refs[i] == 0 && first[i] == kNobody; };
+#pragma unroll 4
+    for (unsigned i = my_ids.x + threadIdx.x; i < my_ids.y; i += kThreads) mine[1] += unused(i);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         int x[1] = {mine[n]};
         block_ranks<1>(x, s_warp, total);
         mine[n] = total[0];
     }
-    share_counts<2>(cluster, mine, s_part, before, all);
+    share_counts(team, mine, s_part, before, all);
     const int served = min(all[0], all[1]), left = all[1] - served;
     int id_rank[1] = {before[1]}, nth[kRowsEach];
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        if (b_begin + k * kThreads >= b_end) break;   // (the whole block)
+        if (my_rows.x + k * kThreads >= my_rows.y) break;   // (the whole block)
         int x[1] = {old[k] >= 0};
         block_ranks<1>(x, s_warp, total);
         nth[k] = before[0] + x[0];
         before[0] += total[0];
     }
-    rank_items<1>(i_begin, i_end, id_rank, s_warp,
-                  [&](unsigned i, int (&f)[1]) { f[0] = ids.own_a(i) == 0 && ids.own_b(i) == kNobody; },
+    rank_items<1>(my_ids.x, my_ids.y, id_rank, s_warp, [&](unsigned i, int (&f)[1]) { f[0] = unused(i); },
                   [&](unsigned i, const int (&f)[1], const int (&at)[1]) {
                       const bool handed = f[0] && at[0] < served;
                       if (handed) a.fresh[at[0]] = static_cast<int>(i);
                       else if (f[0]) a.free_list[all[1] - 1 - at[0]] = static_cast<int>(i);
-                      const int inside = ids.own_a(i);   // of the rows that end in a block one at most still names it
+                      const int inside = refs[i];   // of the rows that end in a block one at most still names it
                       a.refs[i] = inside != 0 ? inside : handed || !f[0];
                   });
-    for (unsigned i = left + tid; i < NB; i += kAll) a.free_list[i] = -1;
-    for (unsigned i = served + tid; i < B; i += kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
+    for (unsigned i = left + tid; i < NB; i += team.kAll) a.free_list[i] = -1;
+    for (unsigned i = served + tid; i < B; i += team.kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
         *a.free_count = left;
         *a.pair_count = served;
         if (served < all[0]) raise_error(a.err, PKV_DEVERR_POOL);
     }
-    cluster.sync();
+    team.sync();
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const unsigned b = b_begin + k * kThreads + threadIdx.x;
-        if (b >= b_end) break;
+        const unsigned b = my_rows.x + k * kThreads + threadIdx.x;
+        if (b >= my_rows.y) break;
         if (old[k] >= 0 && nth[k] < served) {
             const int to = a.fresh[nth[k]];
             reinterpret_cast<int2 *>(a.pairs)[nth[k]] = make_int2(old[k], to);
@@ -310,98 +348,90 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) fork
         a.lens_out[b] = a.place[b] = len[k];
     }
     if (rows == a.table_out && served == all[0]) return;
-    cluster.sync();
-    if (rows != a.table_out) {
-        for_entries(a, warp, lane, warps, [&](unsigned b, bool) { return Source{0, a.place[b]}; },
-                    [&](const Source &s, unsigned b, unsigned j) {
-                        return s.len == 0 ? -1 : rows[static_cast<size_t>(b) * a.MBS + j];
-                    }, same,
-                    [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
-    } else {   // rows that the pool was too small for
-        for (unsigned b = warp; b < B; b += warps)
-            if (a.place[b] == 0)
-                for (unsigned j = lane; j < static_cast<unsigned>(a.MBS); j += 32) rows[static_cast<size_t>(b) * a.MBS + j] = -1;
+    team.sync();
+    // the rows built aside go into the table; rows that the pool was too small for are empty
+    for (unsigned b = tid >> 5; b < B; b += team.kAll / 32) {
+        const bool none = a.place[b] == 0;
+        if (rows == a.table_out && !none) continue;
+#pragma unroll 8
+        for (unsigned j = threadIdx.x & 31; j < static_cast<unsigned>(a.MBS); j += 32) {
+            const size_t at = static_cast<size_t>(b) * a.MBS + j;
+            a.table_out[at] = none ? -1 : __ldcg(rows + at);
+        }
     }
 }
 
-template <bool SHARED>
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
+template <bool ONE>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
     extern __shared__ int s_ids[];
-    pdl_wait();
     __shared__ int s_warp[3][32], s_part[3], s_warp1[1][32], s_part1[1];
-    cg::cluster_group cluster = cg::this_cluster();
-    const unsigned rank = cluster.block_rank(), tid = rank * kThreads + threadIdx.x;
-    const unsigned NB = a.NB, warp = tid >> 5, lane = tid & 31, warps = kAll / 32;
-    // refs: entries that name a block (a); where it goes (b)
-    const Ids<SHARED> ids{cluster, SHARED ? s_ids : a.refs, SHARED ? s_ids + (1 << a.shift) : a.first, a.shift};
-    const unsigned begin = min(NB, rank << a.shift), end = min(NB, (rank + 1) << a.shift);
+    pdl_wait();
+    const Team<ONE> team;
+    const unsigned tid = team.tid(), NB = a.NB;
+    int *refs = ONE ? s_ids : a.refs;              // entries that name a block
+    int *moved = ONE ? s_ids + NB : a.first;       // where it goes; for now, of one that moves, its rank: -1 - rank
+    Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
     auto held = [&](unsigned i) { return a.held != nullptr && __ldg(a.held + i) != 0; };
-    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) ids.own_a(i) = held(i) ? 1 : 0;
-    cluster.sync();
-    auto source = [&](unsigned b, bool report) { return source_of(a, b, report); };
+    clear(a, team, refs, moved, 0, s_rows);
     auto entry = [&](const Source &s, unsigned b, unsigned j) {
         return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(b) * a.MBS + j] : -1;
     };
-    for_entries(a, warp, lane, warps, source, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
+    for_entries(a, team, s_rows, true, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
         x = checked(a, x);
-        if (x >= 0) atomicAdd(ids.a(x), 1);
+        if (x >= 0) atomicAdd(refs + x, 1);
     });
-    cluster.sync();
-    int mine[1] = {0}, before1[1], all1[1];
-    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) mine[0] += ids.own_a(i) != 0;
-    {
-        int total[1];
-        block_ranks<1>(mine, s_warp1, total);
-        mine[0] = total[0];
-    }
-    share_counts<1>(cluster, mine, s_part1, before1, all1);
+    team.sync();
+    const uint2 part = team.part(NB);
+    int mine[1] = {0}, before1[1], all1[1], total[1];
+#pragma unroll 4
+    for (unsigned i = part.x + threadIdx.x; i < part.y; i += kThreads) mine[0] += refs[i] != 0;
+    block_ranks<1>(mine, s_warp1, total);
+    mine[0] = total[0];
+    share_counts(team, mine, s_part1, before1, all1);
     const unsigned used = all1[0];
     // blocks that move (in use, not held, from `used` on), free ids below, free or vacated ids from there on
     auto kinds = [&](unsigned i, int (&f)[3]) {
-        const bool in_use = ids.own_a(i) != 0, high = i >= used, fixed = high && held(i);
+        const bool in_use = refs[i] != 0, high = i >= used, fixed = high && held(i);
         f[0] = in_use && high && !fixed;
         f[1] = !in_use && !high;
         f[2] = high && !fixed;
     };
     int count[3] = {0, 0, 0}, before[3], all[3];
-    rank_items<3>(begin, end, count, s_warp, kinds, [](unsigned, const int (&)[3], const int (&)[3]) {});
-    share_counts<3>(cluster, count, s_part, before, all);
+    rank_items<3>(part.x, part.y, count, s_warp, kinds, [](unsigned, const int (&)[3], const int (&)[3]) {});
+    share_counts(team, count, s_part, before, all);
     // as many ids are free below `used` as are taken from there on, so every mover has a place
     const int moves = all[0], spare = all[1] - moves, free_all = spare + all[2];
-    rank_items<3>(begin, end, before, s_warp, kinds, [&](unsigned i, const int (&f)[3], const int (&at)[3]) {
-        ids.own_b(i) = f[0] ? -1 - at[0] : static_cast<int>(i);   // a mover: its rank for now
+    rank_items<3>(part.x, part.y, before, s_warp, kinds, [&](unsigned i, const int (&f)[3], const int (&at)[3]) {
+        moved[i] = f[0] ? -1 - at[0] : static_cast<int>(i);
         if (f[1]) {
             if (at[1] < moves) a.fresh[at[1]] = static_cast<int>(i);
             else a.free_list[free_all - 1 - (at[1] - moves)] = static_cast<int>(i);
         }
         if (f[2]) a.free_list[free_all - 1 - (spare + at[2])] = static_cast<int>(i);
+        // what stays; blocks that move write both ends below
+        if (ONE && !f[0] && !(f[1] && at[1] < moves)) a.refs[i] = refs[i];
     });
-    for (unsigned i = free_all + tid; i < NB; i += kAll) a.free_list[i] = -1;
-    for (unsigned i = moves + tid; i < NB / 2; i += kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
+    for (unsigned i = free_all + tid; i < NB; i += team.kAll) a.free_list[i] = -1;
+    for (unsigned i = moves + tid; i < NB / 2; i += team.kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
         *a.free_count = free_all;
         *a.pair_count = moves;
     }
-    cluster.sync();
-    for (unsigned i = begin + threadIdx.x; i < end; i += kThreads) {
-        const int refs = ids.own_a(i), nth = -1 - ids.own_b(i);
+    team.sync();
+#pragma unroll 4
+    for (unsigned i = max(part.x, used) + threadIdx.x; i < part.y; i += kThreads) {
+        const int nth = -1 - moved[i];
         if (nth >= 0) {
             const int to = a.fresh[nth];
-            ids.own_b(i) = to;
+            moved[i] = to;
             reinterpret_cast<int2 *>(a.pairs)[nth] = make_int2(static_cast<int>(i), to);
-            a.refs[to] = refs;
+            a.refs[to] = refs[i];
             a.refs[i] = 0;
-        } else if (SHARED && (refs != 0 || i >= used)) {
-            a.refs[i] = refs;
         }
     }
-    if constexpr (SHARED) {   // free ids below `used` that nothing moves to
-        for (unsigned i = tid; i < static_cast<unsigned>(spare); i += kAll) a.refs[a.free_list[free_all - 1 - i]] = 0;
-    }
-    cluster.sync();
-    for_entries(a, warp, lane, warps, source, entry, [&](int x) { return x >= 0 && x < a.NB ? *ids.b(x) : -1; },
+    team.sync();
+    for_entries(a, team, s_rows, false, entry, [&](int x) { return x >= 0 && x < a.NB ? moved[x] : -1; },
                 [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
-    if constexpr (SHARED) cluster.sync();   // the others' shared memory stays until all have read it
 }
 
 // ---------------------------------------------------------------- copies of a list that the GPU counted
@@ -454,29 +484,33 @@ size_t share_workspace_bytes(int B, int MBS, int NB) {
 
 namespace {
 
-// ids a block: the smallest power of two that covers the pool with eight blocks
-int id_shift(int NB) {
-    int shift = 0;
-    while ((static_cast<long long>(kBlocks) << shift) < NB) ++shift;
-    return shift;
-}
-
 template <typename Kernel>
-cudaError_t launch_cluster(Kernel shared, Kernel global, ShareArgs a, std::atomic<unsigned long long> &ready, cudaStream_t stream) {
-    a.shift = id_shift(a.NB);
-    if (static_cast<unsigned>(a.NB) > kSharedIds) {
-        return launch_dependent(global, dim3(kBlocks), dim3(kThreads), 0, stream, a);
+cudaError_t launch_team(Kernel one, Kernel cluster, const ShareArgs &a, std::atomic<unsigned long long> &ready, cudaStream_t stream) {
+    if (a.NB > kOneIds || a.B > kOneRows || static_cast<long long>(a.B) * a.MBS > kOneEntries) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kBlocks);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kBlocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_dependent
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, cluster, a);
     }
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {   // shared memory opted in, once a device
-        e = cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * sizeof(int) << kSharedShift);
+        e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * (kOneIds + kOneRows));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
-    return launch_dependent(shared, dim3(kBlocks), dim3(kThreads), 2 * sizeof(int) << a.shift, stream, a);
+    return launch_dependent(one, dim3(1), dim3(kThreads), 8 * (static_cast<size_t>(a.NB) + a.B), stream, a);
 }
 
 }  // namespace
@@ -489,7 +523,7 @@ cudaError_t launch_fork(ShareArgs a, void *workspace, bool aside, cudaStream_t s
     a.last = a.place + a.B;
     a.fresh = a.last + a.B;
     a.rows = aside ? a.fresh + std::max(a.B, a.NB / 2) : a.table_out;
-    return launch_cluster(fork_kernel<true>, fork_kernel<false>, a, ready, stream);
+    return launch_team(fork_kernel<true>, fork_kernel<false>, a, ready, stream);
 }
 
 cudaError_t launch_compact(ShareArgs a, void *workspace, cudaStream_t stream) {
@@ -497,7 +531,7 @@ cudaError_t launch_compact(ShareArgs a, void *workspace, cudaStream_t stream) {
     int32_t *ws = static_cast<int32_t *>(workspace);
     a.first = ws;
     a.fresh = ws + a.NB + 2 * static_cast<size_t>(a.B);
-    return launch_cluster(compact_kernel<true>, compact_kernel<false>, a, ready, stream);
+    return launch_team(compact_kernel<true>, compact_kernel<false>, a, ready, stream);
 }
 
 cudaError_t launch_kv_block_copy_counted(void *k_cache, void *v_cache, int elem_bytes, const int32_t *pairs, int n,
