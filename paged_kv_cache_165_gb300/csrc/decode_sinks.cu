@@ -31,6 +31,7 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kFusedMergeMaxChunks = 8;   // merged by the last block; more of them by the merge kernel
 
 // x0, x1 as three bf16 parts each, packed in pairs.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
@@ -48,7 +49,8 @@ __device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1,
 
 template <int D, int BS, int TILES>
 struct SinksCfg {
-    static constexpr int NW = BS * D <= 2048 ? 4 : 2;                // warps
+    // warps: twelve an SM where registers and shared memory allow it, in three blocks or (with q beside the ring) two
+    static constexpr int NW = BS * D <= 2048 ? (TILES > 1 && BS * D == 2048 ? 6 : 4) : 2;
     static constexpr int ST = D == 64 && BS == 16 ? 4 : 2;           // stages of a warp's ring
     static constexpr int NT = BS / 8, KT = BS / 16, KS = D / 16;     // score tiles, k-steps of P.V and of q.K
     static constexpr int PANELS = D / 64;
@@ -56,12 +58,12 @@ struct SinksCfg {
     static constexpr bool kQShared = TILES > 1 || D == 256;          // q parts in shared memory (else in registers)
     static constexpr int kPairs = TILES * 8;
     static constexpr int kRingBytes = NW * ST * kStageBytes;
-    static constexpr int kMergeBytes = NW * kPairs * (D + 2) * 4;    // the warps' states, in the ring
+    static constexpr int kMergeBytes = (NW * (D + 2) + 1) * kPairs * 4;   // the warps' states, in the ring
     static constexpr int kOffQ = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
     static constexpr int kQBytes = kQShared ? TILES * KS * 32 * 24 : 0;
     static constexpr int kOffBar = (kOffQ + kQBytes + 15) / 16 * 16;
     static constexpr int kSmemBytes = 1024 + kOffBar + NW * ST * 8;
-    static constexpr int kBlocks = TILES == 1 && D <= 128 ? 3 : 2;   // per SM (registers)
+    static constexpr int kBlocks = D <= 128 && NW <= 4 ? 3 : 2;      // per SM
 };
 
 // What a CTA attends: pairs slot0 .. slot0 + npairs - 1 of sequence b's (row, head) slots for one KV head, over
@@ -128,31 +130,44 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
     int issued = min(ST, n_my);
     for (int k = 0; k < issued; ++k) issue(k);
 
-    // q parts of tile t, k-step kk: pair 8t + g, elements 16 kk + 2 t4 (+ 8)
-    auto q_part = [&](int t, int kk, uint4 &hm, uint2 &l) {
-        float2 x0 = make_float2(0.f, 0.f), x1 = x0;
-        if (8 * t + g < npairs) {
-            const float *q = p.q + row_of(8 * t + g) * D + kk * 16 + 2 * t4;
-            x0 = __ldg(reinterpret_cast<const float2 *>(q));
-            x1 = __ldg(reinterpret_cast<const float2 *>(q + 8));
-        }
-        split3(x0.x, x0.y, hm.x, hm.y, l.x);
-        split3(x1.x, x1.y, hm.z, hm.w, l.y);
-    };
+    // q parts of a tile's pair 8t + g, k-step kk: elements 16 kk + 2 t4 (+ 8); every load before the first use
+    const float *q_row[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) q_row[t] = 8 * t + g < npairs ? p.q + row_of(8 * t + g) * D + 2 * t4 : nullptr;
     uint4 qhm[kQRegs ? KS : 1];
     uint2 qlo[kQRegs ? KS : 1];
-    if constexpr (kQRegs) {
+    {
+        constexpr int kMine = kQRegs ? KS : (T * KS + NW - 1) / NW;   // (tile, k-step) items of this warp
+        const int first = kQRegs ? 0 : warp * kMine;
+        float2 x[kMine][2];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) q_part(0, kk, qhm[kk], qlo[kk]);
-    } else {
-        for (int i = warp; i < T * KS; i += NW) {
+        for (int i = 0; i < kMine; ++i) {
+            const int t = (first + i) / KS, kk = (first + i) % KS;
+            const float *q = q_row[0];
+#pragma unroll
+            for (int u = 1; u < T; ++u)
+                if (t == u) q = q_row[u];
+            x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+            if (q != nullptr && first + i < T * KS) {
+                x[i][0] = __ldg(reinterpret_cast<const float2 *>(q + kk * 16));
+                x[i][1] = __ldg(reinterpret_cast<const float2 *>(q + kk * 16 + 8));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
             uint4 hm;
             uint2 l;
-            q_part(i / KS, i % KS, hm, l);
-            s_qhm[i * 32 + lane] = hm;
-            s_qlo[i * 32 + lane] = l;
+            split3(x[i][0].x, x[i][0].y, hm.x, hm.y, l.x);
+            split3(x[i][1].x, x[i][1].y, hm.z, hm.w, l.y);
+            if constexpr (kQRegs) {
+                qhm[i] = hm;
+                qlo[i] = l;
+            } else if (first + i < T * KS) {
+                s_qhm[(first + i) * 32 + lane] = hm;
+                s_qlo[(first + i) * 32 + lane] = l;
+            }
         }
-        __syncthreads();
+        if constexpr (!kQRegs) __syncthreads();
     }
 
     float2 o[T][NP * 2];   // running outputs of pair 8t + g: columns 8n + 2 t4, + 1
@@ -329,24 +344,39 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
         for (int kk = k; kk < issued; ++kk) mbar_wait_bounded(smem_addr(&bars[warp * ST + kk % ST]), (kk / ST) & 1);
     }
 
-    // ---- the warps' states meet in shared memory (the ring is free now)
+    // ---- the warps' outputs meet in shared memory (the ring is free now), each scaled to the pairs' common maximum
+    // and sum, so that they only remain to be added
     __syncthreads();
-    float *mw = reinterpret_cast<float *>(w.smem);   // [NW][pairs]
-    float *lw = mw + NW * C::kPairs;
-    float *ow = lw + NW * C::kPairs;                 // [NW][pairs][D]
+    float *ml = reinterpret_cast<float *>(w.smem);       // [NW][pairs][2]
+    float *lse2 = ml + 2 * NW * C::kPairs;               // [pairs]
+    float *ow = lse2 + C::kPairs;                        // [NW][pairs][D]
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         float l = l_run[t];
         l += __shfl_xor_sync(kFull, l, 1);
         l += __shfl_xor_sync(kFull, l, 2);
-        const int at = warp * C::kPairs + 8 * t + g;
-        if (t4 == 0) {
-            mw[at] = m_run[t];
-            lw[at] = l;
-        }
+        if (t4 == 0) *reinterpret_cast<float2 *>(ml + 2 * (warp * C::kPairs + 8 * t + g)) = make_float2(m_run[t], l);
+    }
+    __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NP * 2; ++n)
-            *reinterpret_cast<float2 *>(ow + at * D + n * 8 + 2 * t4) = o[t][n];
+    for (int t = 0; t < T; ++t) {
+        float2 all[NW];
+        float M = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) {
+            all[v] = *reinterpret_cast<const float2 *>(ml + 2 * (v * C::kPairs + 8 * t + g));
+            M = fmaxf(M, all[v].x);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        float l = 0.f;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) l += all[v].y * ex2_approx(all[v].x - ref);
+        if (warp == 0 && t4 == 0) lse2[8 * t + g] = M + log2f(l);
+        // no key of this chunk: an empty partial
+        const float f = l == 0.f ? 0.f : ex2_approx(m_run[t] - ref) / l;
+        float *to = ow + (warp * C::kPairs + 8 * t + g) * D + 2 * t4;
+#pragma unroll
+        for (int n = 0; n < NP * 2; ++n) *reinterpret_cast<float2 *>(to + n * 8) = make_float2(o[t][n].x * f, o[t][n].y * f);
     }
     __syncthreads();
 }
@@ -443,32 +473,36 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         if (npairs <= 16) attend_pages<D, BS, TILES, 2>(tm_k, tm_v, p, w);
         else if constexpr (TILES > 2) attend_pages<D, BS, TILES, TILES>(tm_k, tm_v, p, w);
     }
-    float *mw = reinterpret_cast<float *>(smem);   // [NW][pairs]
-    float *lw = mw + NW * C::kPairs;
-    float *ow = lw + NW * C::kPairs;               // [NW][pairs][D]
-    __syncthreads();
-    for (int i = threadIdx.x; i < npairs * D; i += NW * 32) {
-        const int pair = i / D, c = i % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * C::kPairs + pair]);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float l = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float f = exp2f(mw[w * C::kPairs + pair] - ref);
-            l += lw[w * C::kPairs + pair] * f;
-            acc += ow[(w * C::kPairs + pair) * D + c] * f;
+    const float *lse2 = reinterpret_cast<const float *>(smem) + 2 * NW * C::kPairs, *ow = lse2 + C::kPairs;   // as left there
+    const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+    auto put = [&](float *dst, float4 x) {
+        if (vec) {
+            *reinterpret_cast<float4 *>(dst) = x;
+        } else {
+            dst[0] = x.x;
+            dst[1] = x.y;
+            dst[2] = x.z;
+            dst[3] = x.w;
         }
-        // no key of this chunk: an empty partial
-        const float out = l == 0.f ? 0.f : acc / l, lse2 = M + log2f(l);
+    };
+    for (int i = threadIdx.x; i < npairs * (D / 4); i += NW * 32) {
+        const int pair = i / (D / 4), c = i % (D / 4) * 4;
+        float4 x = *reinterpret_cast<const float4 *>(ow + pair * D + c);
+#pragma unroll
+        for (int v = 1; v < NW; ++v) {
+            const float4 y = *reinterpret_cast<const float4 *>(ow + (v * C::kPairs + pair) * D + c);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+        }
         const size_t row = row_of(pair);
         if (nc == 1) {
-            p.out[row * D + c] = out;
-            if (c == 0 && p.lse != nullptr) p.lse[row] = lse2 * kDecLn2;
+            put(p.out + row * D + c, x);
+            if (c == 0 && p.lse != nullptr) p.lse[row] = lse2[pair] * kDecLn2;
         } else {
-            p.ws_o[(row * p.splits + split) * D + c] = out;
-            if (c == 0) p.ws_lse[row * p.splits + split] = lse2;
+            *reinterpret_cast<float4 *>(p.ws_o + (row * p.splits + split) * D + c) = x;
+            if (c == 0) p.ws_lse[row * p.splits + split] = lse2[pair];
         }
     }
     if (nc == 1 || p.counters == nullptr) return;
@@ -485,31 +519,43 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
     __syncthreads();
     if (!s_last) return;
     __threadfence();
+    float *wt = reinterpret_cast<float *>(smem);   // [pairs][kFusedMergeMaxChunks] the chunks' weights
+    if (threadIdx.x < npairs) {
+        const size_t row = row_of(threadIdx.x);
+        float x[kFusedMergeMaxChunks], M = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
+            x[c] = c < nc ? __ldcg(p.ws_lse + row * p.splits + c) : -INFINITY;
+            M = fmaxf(M, x[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
+            x[c] = ex2_approx(x[c] - M);
+            l += x[c];
+        }
+        const float il = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < kFusedMergeMaxChunks; ++c) wt[threadIdx.x * kFusedMergeMaxChunks + c] = x[c] * il;
+        if (p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kDecLn2;
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < npairs * (D / 4); i += NW * 32) {
         const int pair = i / (D / 4), c4 = i % (D / 4) * 4;
         const size_t row = row_of(pair);
-        const float *ls = p.ws_lse + row * p.splits, *po = p.ws_o + row * p.splits * D + c4;
-        float M = -INFINITY;
-        for (int c = 0; c < nc; ++c) M = fmaxf(M, __ldcg(ls + c));
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = 0; c < nc; ++c) {
-            const float w = exp2f(__ldcg(ls + c) - M);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(c) * D));
-            l += w;
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
+        const float *po = p.ws_o + row * p.splits * D + c4;
+        float4 y[kFusedMergeMaxChunks], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kFusedMergeMaxChunks; ++c)
+            y[c] = c < nc ? __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(c) * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
+            const float f = wt[pair * kFusedMergeMaxChunks + c];
+            acc.x += f * y[c].x;
+            acc.y += f * y[c].y;
+            acc.z += f * y[c].z;
+            acc.w += f * y[c].w;
         }
-        const float il = 1.f / l;
-        float *dst = p.out + row * D + c4;
-        dst[0] = acc.x * il;
-        dst[1] = acc.y * il;
-        dst[2] = acc.z * il;
-        dst[3] = acc.w * il;
-        if (c4 == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kDecLn2;
+        put(p.out + row * D + c4, acc);
     }
 }
 
@@ -535,12 +581,8 @@ template <int D, int BS>
 cudaError_t launch_tiles(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, const SinksPlan &plan,
                          cudaStream_t stream) {
     if (plan.tiles == 1) return launch<D, BS, 1>(kp, tk, tv, plan.groups, stream);
-    if (plan.tiles == 2) return launch<D, BS, 2>(kp, tk, tv, plan.groups, stream);
-    if constexpr (D <= 128) return launch<D, BS, 4>(kp, tk, tv, plan.groups, stream);
-    else return cudaErrorInvalidValue;
+    return launch<D, BS, 2>(kp, tk, tv, plan.groups, stream);
 }
-
-constexpr int kFusedMergeMaxChunks = 8;
 
 }  // namespace
 
@@ -551,16 +593,38 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
         static_cast<long long>(NB + 1) * Hkv * bs >= (1ll << 31))
         return plan;
     const long long pairs = static_cast<long long>(max_q) * (Hq / Hkv), tiles = (pairs + 7) / 8;
-    plan.tiles = tiles == 1 ? 1 : tiles == 2 || d == 256 ? 2 : 4;
+    // two tiles a block at most: four, which read each page once for 32 pairs where two blocks read it from L2, left
+    // too few warps an SM (1 to 4 rows of 64 heads on 8: 187 us; two tiles a block: 173)
+    plan.tiles = tiles == 1 ? 1 : 2;
     const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
-    // chunks: eight CTAs an SM, none shorter than 16 pages
     const long long units = static_cast<long long>(B) * Hkv * groups;
-    int chunk = pages;
-    if (num_splits > 1) chunk = (pages + num_splits - 1) / num_splits;
-    else if (num_splits == 0)
-        while (chunk > 16 && units * ((pages + chunk - 1) / chunk) < 8ll * std::max(sm_count, 1)) chunk = (chunk + 1) / 2;
+    if (units < 1) return plan;
+    const long long slots = static_cast<long long>(std::max(sm_count, 1)) * (d <= 128 ? 3 : 2);   // blocks at a time
+    // Chunks of a sequence by a model of the time in tokens: a block costs its tokens and 128 more a tile; up to one
+    // and two waves of blocks count whole, more of them half a wave over their number; the separate merge of more
+    // than eight chunks as much as 128 tokens.
+    int splits = 1;
+    if (num_splits > 0) {
+        splits = std::min(num_splits, pages);
+    } else {
+        double best = 0;
+        auto consider = [&](long long n) {
+            if (n < 1 || n > pages || n > kDecodeMaxChunks) return;
+            const double waves = static_cast<double>(units) * n / slots;
+            const double cost = (waves <= 1 ? 1 : waves <= 2 ? 2 : waves + 0.5) * (128.0 * plan.tiles + static_cast<double>((pages + n - 1) / n) * bs) +
+                                (n > kFusedMergeMaxChunks ? 128.0 : 0.0);
+            if (best == 0 || cost < best) {
+                best = cost;
+                splits = static_cast<int>(n);
+            }
+        };
+        for (int n = 1; n <= kFusedMergeMaxChunks; ++n) consider(n);
+        if (slots / units > kFusedMergeMaxChunks) consider(slots / units);
+        if (2 * slots / units > kFusedMergeMaxChunks) consider(2 * slots / units);
+    }
+    int chunk = (pages + splits - 1) / splits;
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
-    const int splits = (pages + chunk - 1) / chunk;
+    splits = (pages + chunk - 1) / chunk;
     if (groups * splits > 0x7fffffffll) return plan;
     plan.mma = true;
     plan.groups = static_cast<int>(groups);
