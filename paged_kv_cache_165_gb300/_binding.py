@@ -838,36 +838,17 @@ def block_tables_share_workspace_bytes(B, MBS, NB) -> int:
     return int(lib().pkv_block_tables_share_workspace_bytes(int(B), int(MBS), int(NB)))
 
 
-def _share(what, required, optional, workspace):
-    """Checks of block_tables_fork and block_tables_compact: required and optional are name -> int32 tensor
-    (the optional ones may be None); returns (B, MBS, NB, current device)."""
-    here = _current_device()
-    try:
-        ok = _ready(here, (workspace, *optional.values()))
-        for t in required.values():
-            ok = ok and t.get_device() == here and t.is_contiguous() and t.dtype is _I32
-        for t in optional.values():
-            ok = ok and (t is None or t.dtype is _I32)
-    except AttributeError:   # not a tensor
-        ok = False
-    if not ok:
-        for name, t in required.items():
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must be a torch.Tensor")
-        _refuse(what, here, **{name: (t, _I32) for name, t in (*required.items(), *optional.items())}, workspace=(workspace, None))
+def _share_refuse(what, here, workspace, optional, **required) -> None:
+    """The error of whatever block_tables_fork or block_tables_compact found wrong with its tensors."""
+    for name, t in required.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    _refuse(what, here, **{name: (t, _I32) for name, t in (*required.items(), *optional.items())}, workspace=(workspace, None))
     table = required["block_table"].shape
     if len(table) != 2:
         raise ValueError(f"{what}: block_table must be [B][MBS]")
-    B, MBS = table
-    NB = required["free_list"].numel()
-    if required["block_table_out"].numel() != B * MBS or required["context_lens"].numel() != B or \
-            required["refs"].numel() != NB or required["free_count"].numel() != 1 or required["pair_count"].numel() != 1:
-        raise ValueError(f"{what}: shapes do not match (block_table, block_table_out [B][MBS], context_lens [B], refs, "
-                         "free_list [NB], free_count, pair_count [1])")
-    for name, t in optional.items():
-        if t is not None and t.numel() != (NB if name == "held" else B):
-            raise ValueError(f"{what}: {name} must hold {NB if name == 'held' else B} numbers, got {t.numel()}")
-    return B, MBS, NB, here
+    raise ValueError(f"{what}: shapes do not match (block_table, block_table_out [B][MBS]; context_lens, context_lens_out, parents "
+                     "[B]; refs, free_list, held [NB]; free_count, pair_count [1]; pairs [B][2], to compact [NB // 2][2])")
 
 
 def block_tables_fork(block_table, context_lens, parents, block_table_out, context_lens_out, refs, free_list, free_count,
@@ -876,12 +857,21 @@ def block_tables_fork(block_table, context_lens, parents, block_table_out, conte
     its blocks but for a partly filled last one; references counted anew, blocks without any free
     (see pkv.h).  refs, free_list int32 [NB], free_count, pair_count int32 [1], pairs int32 [B][2]:
     the copies to run with kv_block_copy(..., pairs, count=pair_count).  held: int32 [NB] or None."""
-    B, MBS, NB, here = _share("block_tables_fork",
-                              dict(block_table=block_table, context_lens=context_lens, block_table_out=block_table_out,
-                                   context_lens_out=context_lens_out, refs=refs, free_list=free_list, free_count=free_count,
-                                   pairs=pairs, pair_count=pair_count), dict(parents=parents, held=held), workspace)
-    if pairs.numel() != 2 * B or context_lens_out.numel() != B:
-        raise ValueError(f"block_tables_fork: pairs must be [{B}][2] and context_lens_out [{B}]")
+    here = _current_device()
+    ints = (block_table, context_lens, block_table_out, context_lens_out, refs, free_list, free_count, pairs, pair_count)
+    try:
+        ok = _ready(here, (*ints, parents, held, workspace)) and all([t.dtype is _I32 for t in ints]) and \
+            (parents is None or parents.dtype is _I32) and (held is None or held.dtype is _I32)
+        (B, MBS), NB = block_table.shape, free_list.numel()
+        ok = ok and block_table_out.numel() == B * MBS and context_lens.numel() == B and context_lens_out.numel() == B and \
+            refs.numel() == NB and free_count.numel() == 1 and pair_count.numel() == 1 and pairs.numel() == 2 * B and \
+            (parents is None or parents.numel() == B) and (held is None or held.numel() == NB)
+    except (AttributeError, ValueError):   # not a tensor, or not a table
+        ok = False
+    if not ok:
+        _share_refuse("block_tables_fork", here, workspace, dict(parents=parents, held=held), block_table=block_table,
+                      context_lens=context_lens, block_table_out=block_table_out, context_lens_out=context_lens_out, refs=refs,
+                      free_list=free_list, free_count=free_count, pairs=pairs, pair_count=pair_count)
     status = lib().pkv_block_tables_fork(
         block_table.data_ptr(), context_lens.data_ptr(), _ptr(parents), _ptr(held), block_table_out.data_ptr(),
         context_lens_out.data_ptr(), refs.data_ptr(), free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(),
@@ -894,16 +884,23 @@ def block_tables_compact(block_table, context_lens, block_table_out, refs, free_
                          held=None, workspace=None, stream=None) -> None:
     """The blocks in use moved to the lowest ids (see pkv.h); pairs int32 [NB // 2][2], the other
     tensors as block_tables_fork."""
-    B, MBS, NB, here = _share("block_tables_compact",
-                              dict(block_table=block_table, context_lens=context_lens, block_table_out=block_table_out, refs=refs,
-                                   free_list=free_list, free_count=free_count, pairs=pairs, pair_count=pair_count),
-                              dict(held=held), workspace)
-    if pairs.numel() != NB // 2 * 2:
-        raise ValueError(f"block_tables_compact: pairs must be [{NB // 2}][2]")
+    here = _current_device()
+    ints = (block_table, context_lens, block_table_out, refs, free_list, free_count, pairs, pair_count)
+    try:
+        ok = _ready(here, (*ints, held, workspace)) and all([t.dtype is _I32 for t in ints]) and (held is None or held.dtype is _I32)
+        (B, MBS), NB = block_table.shape, free_list.numel()
+        ok = ok and block_table_out.numel() == B * MBS and context_lens.numel() == B and refs.numel() == NB and \
+            free_count.numel() == 1 and pair_count.numel() == 1 and pairs.numel() == NB // 2 * 2 and (held is None or held.numel() == NB)
+    except (AttributeError, ValueError):   # not a tensor, or not a table
+        ok = False
+    if not ok:
+        _share_refuse("block_tables_compact", here, workspace, dict(held=held), block_table=block_table, context_lens=context_lens,
+                      block_table_out=block_table_out, refs=refs, free_list=free_list, free_count=free_count, pairs=pairs,
+                      pair_count=pair_count)
     status = lib().pkv_block_tables_compact(
         block_table.data_ptr(), context_lens.data_ptr(), _ptr(held), block_table_out.data_ptr(), refs.data_ptr(),
         free_list.data_ptr(), free_count.data_ptr(), pairs.data_ptr(), pair_count.data_ptr(), B, MBS, int(bs), NB,
-        workspace.data_ptr(), _bytes(workspace), _stream(stream, here))
+        _ptr(workspace), _bytes(workspace), _stream(stream, here))
     if status:
         _check(status)
 

@@ -71,7 +71,7 @@ __host__ __device__ __forceinline__ int units_past(int d, int rot) { return (d -
 
 // Unit u of a token is (head u / uh, piece u % uh), uh units a head, heads in the order q, K, V.
 template <typename T, typename Tq, bool INTER, int N>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeArgs a) {
     extern __shared__ float2 s_cs[];   // [tokens of the block][rot / 2]
     __shared__ long long s_row[kMaxTokens];   // K/V row of head 0, -1: none
     pdl_wait();

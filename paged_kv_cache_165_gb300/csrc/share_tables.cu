@@ -418,15 +418,25 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         *a.pair_count = moves;
     }
     team.sync();
-#pragma unroll 4
-    for (unsigned i = max(part.x, used) + threadIdx.x; i < part.y; i += kThreads) {
-        const int nth = -1 - moved[i];
-        if (nth >= 0) {
-            const int to = a.fresh[nth];
-            moved[i] = to;
-            reinterpret_cast<int2 *>(a.pairs)[nth] = make_int2(static_cast<int>(i), to);
-            a.refs[to] = refs[i];
-            a.refs[i] = 0;
+    for (unsigned i0 = max(part.x, used) + threadIdx.x; i0 < part.y; i0 += 4 * kThreads) {   // four a thread: their loads overlap
+        int nth[4], n[4], to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned i = i0 + k * kThreads;
+            nth[k] = i < part.y ? -1 - moved[i] : -1;
+            n[k] = i < part.y ? refs[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = nth[k] >= 0 ? a.fresh[nth[k]] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned i = i0 + k * kThreads;
+            if (nth[k] >= 0) {
+                moved[i] = to[k];
+                reinterpret_cast<int2 *>(a.pairs)[nth[k]] = make_int2(static_cast<int>(i), to[k]);
+                a.refs[to[k]] = n[k];
+                a.refs[i] = 0;
+            }
         }
     }
     team.sync();
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
 
 // ---------------------------------------------------------------- copies of a list that the GPU counted
 
-constexpr int kCopyThreads = 256, kCopyAhead = 4;
+constexpr int kCopyThreads = 256, kCopyAhead = 8;
 
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads)
