@@ -25,20 +25,13 @@
 
 #include "common.cuh"
 #include "decode_kparams.cuh"
+#include "decode_sinks.cuh"
 #include "internal.h"
 
 namespace pkv {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kFusedMergeMaxChunks = 8;   // merged by the last block; more of them by the merge kernel
-
-// x0, x1 as three bf16 parts each, packed in pairs.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
-    const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xffff0000u);
-    split_bf16x2(r0, r1, mid, lo);
-}
 
 // D = A B (+ C) of m16n8k16 with the accumulator apart, so that a zero one costs no moves.
 __device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -49,9 +42,10 @@ __device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1,
 
 template <int D, int BS, int TILES>
 struct SinksCfg {
-    // warps: twelve an SM where registers and shared memory allow it, in three blocks or (with q beside the ring) two
-    static constexpr int NW = BS * D <= 2048 ? (TILES > 1 && BS * D == 2048 ? 6 : 4) : 2;
-    static constexpr int ST = D == 64 && BS == 16 ? 4 : 2;           // stages of a warp's ring
+    // two blocks an SM with 96 KB of rings each (d = 256: 64 KB to 128 KB): a deeper ring and fewer, longer blocks than
+    // three of 64 KB (window decode 171 us against 181)
+    static constexpr int NW = D == 256 ? 2 : BS * D == 4096 ? 3 : 4;                          // warps
+    static constexpr int ST = D == 256 ? 2 : 98304 / (NW * 4 * BS * D);                       // stages of a warp's ring
     static constexpr int NT = BS / 8, KT = BS / 16, KS = D / 16;     // score tiles, k-steps of P.V and of q.K
     static constexpr int PANELS = D / 64;
     static constexpr int kPageBytes = BS * D * 2, kStageBytes = 2 * kPageBytes;
@@ -63,47 +57,27 @@ struct SinksCfg {
     static constexpr int kQBytes = kQShared ? TILES * KS * 32 * 24 : 0;
     static constexpr int kOffBar = (kOffQ + kQBytes + 15) / 16 * 16;
     static constexpr int kSmemBytes = 1024 + kOffBar + NW * ST * 8;
-    static constexpr int kBlocks = D <= 128 && NW <= 4 ? 3 : 2;      // per SM
-};
-
-// What a CTA attends: pairs slot0 .. slot0 + npairs - 1 of sequence b's (row, head) slots for one KV head, over
-// pages pg0 .. pg1 - 1 (numbered without the gap).  Its rows see the tokens [0, S) and [lo, hi) between them,
-// and each of them all of [.., S) and [all_lo, all_hi).
-struct Stream {
-    uint8_t *smem;
-    uint64_t *bars;
-    int b, kvh, slot0, npairs, c0, P0;
-    int pg0, pg1, lo, hi, all_lo, all_hi;
-    SeqSpan sp;
+    static constexpr int kBlocks = 2;                                // per SM
 };
 
 // One warp's pages for T tiles of pairs (MAXT: of the CTA's layout); leaves its states (running maximum and sum in
 // base 2, unnormalised outputs) in shared memory.
 template <int D, int BS, int MAXT, int T>
 __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const DecodeKParams &p,
-                                             const Stream &w) {
+                                             const SinksWork &w, uint8_t *smem, uint64_t *bars) {
     using C = SinksCfg<D, BS, MAXT>;
     constexpr int NW = C::NW, ST = C::ST, NT = C::NT, KT = C::KT, KS = C::KS, NP = D / 16;
     constexpr int LT = T / 2;                                // accumulators of third parts, two tiles each
     constexpr bool kQRegs = T == 1 && D <= 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int b = w.b, kvh = w.kvh, slot0 = w.slot0, npairs = w.npairs, P0 = w.P0, pg0 = w.pg0, pg1 = w.pg1;
-    const int lo = w.lo, hi = w.hi, all_lo = w.all_lo, all_hi = w.all_hi, S = p.sinks;
-    const SeqSpan sp = w.sp;
-    const int shift = sp.gap * BS;
-    uint8_t *smem = w.smem;
-    uint64_t *bars = w.bars;
+    const int kvh = w.kvh, npairs = w.npairs, pg0 = w.pg0, S = p.sinks;
     uint4 *s_qhm = reinterpret_cast<uint4 *>(smem + C::kOffQ);                      // [tiles][KS][32]
     uint2 *s_qlo = reinterpret_cast<uint2 *>(smem + C::kOffQ + MAXT * KS * 32 * 16);
-    auto lo_of = [&](int pos) { return max(0, pos + 1 - p.window) - shift; };
-    auto row_of = [&](int pair) {
-        const int slot = slot0 + pair;
-        return static_cast<size_t>(w.c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
-    };
     // this warp's pages: pg0 + warp + NW * k; table entries 32 at a time ahead of the copies
-    const int n_my = pg1 - pg0 > warp ? (pg1 - pg0 - warp + NW - 1) / NW : 0;
-    const int32_t *tbl = p.block_table + static_cast<size_t>(b) * p.MBS;
-    auto entry = [&](int k) { return k < n_my ? __ldg(tbl + page_entry(sp, pg0 + warp + k * NW)) : 0; };
+    const int n_my = w.pg1 - pg0 > warp ? (w.pg1 - pg0 - warp + NW - 1) / NW : 0;
+    auto entry = [&](int k) {
+        return k < n_my ? __ldg(p.block_table + static_cast<size_t>(w.b) * p.MBS + page_entry(w.sp, pg0 + warp + k * NW)) : 0;
+    };
     int tcur = entry(lane), tnext = entry(32 + lane), tbase = 0;
     const int oob_row = p.NB * p.Hkv * BS;   // a row past the end: TMA fills zeros
     auto issue = [&](int k) {   // whole warp (shuffle); lane 0 issues the copies
@@ -133,7 +107,7 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
     // q parts of a tile's pair 8t + g, k-step kk: elements 16 kk + 2 t4 (+ 8); every load before the first use
     const float *q_row[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) q_row[t] = 8 * t + g < npairs ? p.q + row_of(8 * t + g) * D + 2 * t4 : nullptr;
+    for (int t = 0; t < T; ++t) q_row[t] = 8 * t + g < npairs ? p.q + w.row_of(p, 8 * t + g) * D + 2 * t4 : nullptr;
     uint4 qhm[kQRegs ? KS : 1];
     uint2 qlo[kQRegs ? KS : 1];
     {
@@ -179,9 +153,9 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
         for (int n = 0; n < NP * 2; ++n) o[t][n] = make_float2(0.f, 0.f);
         m_run[t] = -INFINITY;
         l_run[t] = 0.f;
-        const int pos = P0 + (slot0 + min(8 * t + g, npairs - 1)) / p.m;
-        lo_r[t] = lo_of(pos);
-        hi_r[t] = pos + 1 - shift;
+        const int pos = w.position(p, min(8 * t + g, npairs - 1));
+        lo_r[t] = w.lo_of(p, pos);
+        hi_r[t] = w.hi_of(pos);
     }
 
     int k = 0;
@@ -194,11 +168,11 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
         }
         uint8_t *stage = smem + st * C::kStageBytes;
         const int v0 = (pg0 + warp + k * NW) * BS;   // the page's first token
-        const bool whole = v0 + BS <= all_hi && (v0 >= all_lo || v0 + BS <= S);   // every row sees all of it
+        const bool whole = v0 + BS <= w.all_hi && (v0 >= w.all_lo || v0 + BS <= S);   // every row sees all of it
         if (!whole) {
             for (int i = lane; i < BS * (D / 8); i += 32) {
                 const int r = i / (D / 8), c16 = i % (D / 8), v = v0 + r;
-                if (v >= hi || (v >= S && v < lo))
+                if (v >= w.hi || (v >= S && v < w.lo))
                     *reinterpret_cast<uint4 *>(stage + C::kPageBytes + (c16 >> 3) * BS * 128 + r * 128 + (c16 & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
             }
@@ -347,9 +321,9 @@ __device__ __forceinline__ void attend_pages(const CUtensorMap &tm_k, const CUte
     // ---- the warps' outputs meet in shared memory (the ring is free now), each scaled to the pairs' common maximum
     // and sum, so that they only remain to be added
     __syncthreads();
-    float *ml = reinterpret_cast<float *>(w.smem);       // [NW][pairs][2]
-    float *lse2 = ml + 2 * NW * C::kPairs;               // [pairs]
+    float *lse2 = reinterpret_cast<float *>(smem);       // [pairs], as finish_sinks wants it
     float *ow = lse2 + C::kPairs;                        // [NW][pairs][D]
+    float *ml = ow + NW * C::kPairs * D;                 // [NW][pairs][2]
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         float l = l_run[t];
@@ -387,60 +361,17 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
                         const DecodeKParams p, const int groups) {
     using C = SinksCfg<D, BS, TILES>;
     constexpr int NW = C::NW, ST = C::ST;
-
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
 
     pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
+    __shared__ SinksWork s_work;   // what is seldom needed takes no registers
+    SinksWork w;
+    if (!sinks_work<D, BS, C::kPairs>(p, groups, w)) return;
+    if (threadIdx.x == 0) s_work = w;
+    __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = blockIdx.x % groups, split = blockIdx.x / groups, kvh = blockIdx.y, b = blockIdx.z;
-    const bool report = threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0;
-    const int L = checked_len(p, b, BS, report);
-    int c0 = b, nq = 1;
-    if (p.cu_q != nullptr) {
-        c0 = __ldg(p.cu_q + b);
-        const int c1 = __ldg(p.cu_q + b + 1);
-        nq = c1 - c0;
-        if (!query_rows_ok(p, c0, c1, L)) {   // those of its rows that the call has: out = 0, lse = -inf
-            if (report) raise_error(p.err, PKV_DEVERR_CU_SEQLENS);
-            if (blockIdx.x != 0) return;
-            for (int r = max(c0, 0); r < min(c1, p.rows); ++r) {
-                const size_t at = static_cast<size_t>(r) * p.Hq + kvh * p.m;
-                for (int i = threadIdx.x; i < p.m * D; i += NW * 32) p.out[at * D + i] = 0.f;
-                if (p.lse != nullptr)
-                    for (int i = threadIdx.x; i < p.m; i += NW * 32) p.lse[at + i] = -INFINITY;
-            }
-            return;
-        }
-    }
-    // this CTA's pairs: slots slot0 .. slot0 + npairs - 1 of (row, head), row = slot / m
-    const int slot0 = group * C::kPairs, npairs = min(C::kPairs, nq * p.m - slot0);
-    if (npairs <= 0) return;
-    auto row_of = [&](int pair) {   // of out, lse, q
-        const int slot = slot0 + pair;
-        return static_cast<size_t>(c0 + slot / p.m) * p.Hq + kvh * p.m + slot % p.m;
-    };
-    if (L == 0) {
-        if (split != 0) return;
-        for (int i = threadIdx.x; i < npairs * D; i += NW * 32) p.out[row_of(i / D) * D + i % D] = 0.f;
-        if (p.lse != nullptr)
-            for (int i = threadIdx.x; i < npairs; i += NW * 32) p.lse[row_of(i)] = -INFINITY;
-        return;
-    }
-    // tokens without the gap's pages: the sequence's (chunks), and those that the CTA's rows see, [0, S) and [lo, hi)
-    const int P0 = L - nq;
-    const SeqSpan sp = sinks_span(p, b, L, max(0, P0 + 1 - p.window), BS);
-    const int shift = sp.gap * BS;
-    auto lo_of = [&](int pos) { return max(0, pos + 1 - p.window) - shift; };
-    const int pos_first = P0 + slot0 / p.m, pos_last = P0 + (slot0 + npairs - 1) / p.m;
-    const int lo = lo_of(pos_first), hi = pos_last + 1 - shift;
-    const int all_lo = lo_of(pos_last), all_hi = pos_first + 1 - shift;   // [.., ..) seen by every row
-    const int nc = (sp.npages + p.chunk_pages - 1) / p.chunk_pages;
-    const int cp0 = split * p.chunk_pages, cp1 = min(sp.npages, cp0 + p.chunk_pages);
-    if (cp0 >= cp1) return;   // no such chunk
-    const int pg0 = cp0 < sp.spages ? cp0 : max(cp0, lo / BS), pg1 = min(cp1, (hi + BS - 1) / BS);
-
     if (lane == 0) {
         for (int s = 0; s < ST; ++s) mbar_init(smem_addr(&bars[warp * ST + s]), 1);
         fence_barrier_init();
@@ -450,113 +381,10 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
         tma_prefetch_map(&tm_v);
     }
     __syncwarp();
-
-    Stream w;
-    w.smem = smem;
-    w.bars = bars;
-    w.b = b;
-    w.kvh = kvh;
-    w.slot0 = slot0;
-    w.npairs = npairs;
-    w.c0 = c0;
-    w.P0 = P0;
-    w.pg0 = pg0;
-    w.pg1 = pg1;
-    w.lo = lo;
-    w.hi = hi;
-    w.all_lo = all_lo;
-    w.all_hi = all_hi;
-    w.sp = sp;
     // only as many tiles as the CTA has pairs for (rows of a sequence and heads of a KV head differ)
-    if (npairs <= 8) attend_pages<D, BS, TILES, 1>(tm_k, tm_v, p, w);
-    else if constexpr (TILES > 1) {
-        if (npairs <= 16) attend_pages<D, BS, TILES, 2>(tm_k, tm_v, p, w);
-        else if constexpr (TILES > 2) attend_pages<D, BS, TILES, TILES>(tm_k, tm_v, p, w);
-    }
-    const float *lse2 = reinterpret_cast<const float *>(smem) + 2 * NW * C::kPairs, *ow = lse2 + C::kPairs;   // as left there
-    const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-    auto put = [&](float *dst, float4 x) {
-        if (vec) {
-            *reinterpret_cast<float4 *>(dst) = x;
-        } else {
-            dst[0] = x.x;
-            dst[1] = x.y;
-            dst[2] = x.z;
-            dst[3] = x.w;
-        }
-    };
-    for (int i = threadIdx.x; i < npairs * (D / 4); i += NW * 32) {
-        const int pair = i / (D / 4), c = i % (D / 4) * 4;
-        float4 x = *reinterpret_cast<const float4 *>(ow + pair * D + c);
-#pragma unroll
-        for (int v = 1; v < NW; ++v) {
-            const float4 y = *reinterpret_cast<const float4 *>(ow + (v * C::kPairs + pair) * D + c);
-            x.x += y.x;
-            x.y += y.y;
-            x.z += y.z;
-            x.w += y.w;
-        }
-        const size_t row = row_of(pair);
-        if (nc == 1) {
-            put(p.out + row * D + c, x);
-            if (c == 0 && p.lse != nullptr) p.lse[row] = lse2[pair] * kDecLn2;
-        } else {
-            *reinterpret_cast<float4 *>(p.ws_o + (row * p.splits + split) * D + c) = x;
-            if (c == 0) p.ws_lse[row * p.splits + split] = lse2[pair];
-        }
-    }
-    if (nc == 1 || p.counters == nullptr) return;
-
-    // ---- the last chunk of these pairs to finish merges them all (an arrival counter, no waiting)
-    __shared__ int s_last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned *ctr = p.counters + (static_cast<size_t>(b) * p.Hkv + kvh) * groups + group;
-        s_last = atomicAdd(ctr, 1u) + 1 == static_cast<unsigned>(nc);
-        if (s_last) *ctr = 0u;   // every chunk of this call has arrived
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    float *wt = reinterpret_cast<float *>(smem);   // [pairs][kFusedMergeMaxChunks] the chunks' weights
-    if (threadIdx.x < npairs) {
-        const size_t row = row_of(threadIdx.x);
-        float x[kFusedMergeMaxChunks], M = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
-            x[c] = c < nc ? __ldcg(p.ws_lse + row * p.splits + c) : -INFINITY;
-            M = fmaxf(M, x[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
-            x[c] = ex2_approx(x[c] - M);
-            l += x[c];
-        }
-        const float il = 1.f / l;
-#pragma unroll
-        for (int c = 0; c < kFusedMergeMaxChunks; ++c) wt[threadIdx.x * kFusedMergeMaxChunks + c] = x[c] * il;
-        if (p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kDecLn2;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < npairs * (D / 4); i += NW * 32) {
-        const int pair = i / (D / 4), c4 = i % (D / 4) * 4;
-        const size_t row = row_of(pair);
-        const float *po = p.ws_o + row * p.splits * D + c4;
-        float4 y[kFusedMergeMaxChunks], acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kFusedMergeMaxChunks; ++c)
-            y[c] = c < nc ? __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(c) * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kFusedMergeMaxChunks; ++c) {
-            const float f = wt[pair * kFusedMergeMaxChunks + c];
-            acc.x += f * y[c].x;
-            acc.y += f * y[c].y;
-            acc.z += f * y[c].z;
-            acc.w += f * y[c].w;
-        }
-        put(p.out + row * D + c4, acc);
-    }
+    if (TILES == 1 || w.npairs <= 8) attend_pages<D, BS, TILES, 1>(tm_k, tm_v, p, s_work, smem, bars);
+    else attend_pages<D, BS, TILES, TILES>(tm_k, tm_v, p, s_work, smem, bars);
+    finish_sinks<D, C::kPairs, NW>(smem, p, s_work, groups);
 }
 
 template <int D, int BS, int TILES>
@@ -580,8 +408,10 @@ cudaError_t launch(const DecodeKParams &kp, const CUtensorMap &tk, const CUtenso
 template <int D, int BS>
 cudaError_t launch_tiles(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, const SinksPlan &plan,
                          cudaStream_t stream) {
-    if (plan.tiles == 1) return launch<D, BS, 1>(kp, tk, tv, plan.groups, stream);
-    return launch<D, BS, 2>(kp, tk, tv, plan.groups, stream);
+    if constexpr (D == 256) {
+        if (plan.tiles == 2) return launch<D, BS, 2>(kp, tk, tv, plan.groups, stream);
+    }
+    return launch<D, BS, 1>(kp, tk, tv, plan.groups, stream);
 }
 
 }  // namespace
@@ -593,36 +423,41 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
         static_cast<long long>(NB + 1) * Hkv * bs >= (1ll << 31))
         return plan;
     const long long pairs = static_cast<long long>(max_q) * (Hq / Hkv), tiles = (pairs + 7) / 8;
-    // two tiles a block at most: four, which read each page once for 32 pairs where two blocks read it from L2, left
-    // too few warps an SM (1 to 4 rows of 64 heads on 8: 187 us; two tiles a block: 173)
-    plan.tiles = tiles == 1 ? 1 : 2;
+    plan.umma = pairs > kSinksMmaPairs && d <= 128;
+    // warp MMAs: two tiles a block at most; four, which read each page once for 32 pairs where two blocks read it from
+    // L2, left too few warps an SM (1 to 4 rows of 64 heads on 8: 187 us; two tiles a block: 173)
+    plan.tiles = plan.umma ? kSinksUmmaPairs / 8 : tiles == 1 ? 1 : 2;
     const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
     const long long units = static_cast<long long>(B) * Hkv * groups;
     if (units < 1) return plan;
-    const long long slots = static_cast<long long>(std::max(sm_count, 1)) * (d <= 128 ? 3 : 2);   // blocks at a time
-    // Chunks of a sequence by a model of the time in tokens: a block costs its tokens and 128 more a tile; up to one
-    // and two waves of blocks count whole, more of them half a wave over their number; the separate merge of more
-    // than eight chunks as much as 128 tokens.
+    const long long slots = 2ll * std::max(sm_count, 1);   // blocks at a time
+    // Chunks of a sequence by a model of the time in tokens: a block costs its tokens and 512 more, a wave of blocks
+    // as much as a block, a second wave at least half of one; more chunks than one cost a quarter of a wave where
+    // they make several, and more than eight the merge kernel, 256 tokens.  (512 units of 4112 tokens, 1 to 4
+    // chunks: 172, 187, 190 and 184 us; 64 units of 2096: 37, 25, 24 and 22 us, five chunks 29.)  No chunk is longer
+    // than 16384 tokens, so that a long sequence among short ones does not end the launch alone.
     int splits = 1;
     if (num_splits > 0) {
         splits = std::min(num_splits, pages);
     } else {
         double best = 0;
+        const long long tokens = static_cast<long long>(pages) * bs, least = std::min<long long>((tokens + 16383) / 16384, pages);
         auto consider = [&](long long n) {
-            if (n < 1 || n > pages || n > kDecodeMaxChunks) return;
-            const double waves = static_cast<double>(units) * n / slots;
-            const double cost = (waves <= 1 ? 1 : waves <= 2 ? 2 : waves + 0.5) * (128.0 * plan.tiles + static_cast<double>((pages + n - 1) / n) * bs) +
-                                (n > kFusedMergeMaxChunks ? 128.0 : 0.0);
+            if (n < least || n > pages || n > kDecodeMaxChunks) return;
+            double waves = static_cast<double>(units) * n / slots;
+            waves = waves <= 1 ? 1 : std::max(waves, 1.5) + (n > 1 ? 0.25 : 0.0);
+            const double cost = waves * (512.0 + static_cast<double>((pages + n - 1) / n) * bs) + (n > kSinksFusedChunks ? 256.0 : 0.0);
             if (best == 0 || cost < best) {
                 best = cost;
                 splits = static_cast<int>(n);
             }
         };
-        for (int n = 1; n <= kFusedMergeMaxChunks; ++n) consider(n);
-        if (slots / units > kFusedMergeMaxChunks) consider(slots / units);
-        if (2 * slots / units > kFusedMergeMaxChunks) consider(2 * slots / units);
+        for (int n = 1; n <= kSinksFusedChunks; ++n) consider(n);
+        consider(least);
+        if (slots / units > kSinksFusedChunks) consider(slots / units);
     }
     int chunk = (pages + splits - 1) / splits;
+    if (plan.umma) chunk = (chunk + kSinksUmmaKeys / bs - 1) / (kSinksUmmaKeys / bs) * (kSinksUmmaKeys / bs);   // whole key tiles
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
     splits = (pages + chunk - 1) / chunk;
     if (groups * splits > 0x7fffffffll) return plan;
@@ -630,7 +465,7 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
     plan.groups = static_cast<int>(groups);
     plan.chunk_pages = chunk;
     plan.splits = splits;
-    plan.fused_merge = splits > 1 && splits <= kFusedMergeMaxChunks &&
+    plan.fused_merge = splits > 1 && splits <= kSinksFusedChunks &&
                        units <= static_cast<long long>(PKV_DECODE_COUNTER_BYTES / sizeof(unsigned));
     plan.workspace_bytes =
         splits > 1 ? PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(rows) * Hq * splits * (static_cast<size_t>(d) + 1) * sizeof(float)
@@ -673,7 +508,9 @@ cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cuda
     if (!encode_map_bf16(&tk, a.k_cache, 2, dims, strides, box) || !encode_map_bf16(&tv, a.v_cache, 2, dims, strides, box))
         return cudaErrorInvalidValue;
     cudaError_t e;
-    if (a.bs == 16)
+    if (plan.umma)
+        e = launch_decode_sinks_umma(kp, tk, tv, a.d, a.bs, plan.groups, stream);
+    else if (a.bs == 16)
         e = a.d == 64    ? launch_tiles<64, 16>(kp, tk, tv, plan, stream)
             : a.d == 128 ? launch_tiles<128, 16>(kp, tk, tv, plan, stream)
                          : launch_tiles<256, 16>(kp, tk, tv, plan, stream);

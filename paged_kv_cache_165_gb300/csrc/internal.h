@@ -147,7 +147,8 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
 
 // Windows with first tokens that stay visible (decode_sinks.cu); mma false: the CUDA-core kernel.
 struct SinksPlan {
-    bool mma;
+    bool mma;            // on tensor cores: warp MMAs, or
+    bool umma;           // tcgen05
     int tiles, groups;   // tiles of 8 (query row, head) pairs of a block, blocks for the pairs of a KV head
     int splits, chunk_pages;
     bool fused_merge;
