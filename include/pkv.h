@@ -470,8 +470,8 @@ pkv_status pkv_decode_step_q4(float *out, float *lse, const float *q, const void
                               void *workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /*
- * Block tables on the GPU, for sequences that own their blocks (a block shared by forks is left to
- * the host's block manager).  The pool is a list free_list int32 [NB] whose first free_count[0]
+ * Block tables on the GPU, for sequences that own their blocks (with blocks that rows share,
+ * pkv_block_tables_fork gives back in release's place).  The pool is a list free_list int32 [NB] whose first free_count[0]
  * entries are the free blocks, the next one handed out last.  No call waits for the host, so a
  * decode loop with these calls can be captured into a CUDA graph.  *_out arguments may be the
  * arrays of the same name without _out.
@@ -654,7 +654,8 @@ pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q,
  * Sums are of whole multiples of 2^-46, to the nearest of which each probability is rounded (ties to even; exact
  * from 2^-22 on), so that the token depends neither on the order of summation nor on the GPU.
  *   accepted      int32 [B]
- *   tokens        int32 [D + B]: the accepted drafts of a sequence, its next token, -1 in the rest of its k + 1 places
+ *   tokens        int32 [D + B], apart from draft_tokens: the accepted drafts of a sequence, its next token, -1 in the
+ *                 rest of its k + 1 places
  *   target_probs  [D + B][V] of type dt (PKV_F32 or PKV_BF16), rows target_stride >= V elements apart
  *   draft_probs   [D][V] of type dt, rows draft_stride apart; NULL: the drafts were not drawn but chosen (q is 1 at
  *                 x_i, and r is p_a without x_a)
@@ -675,13 +676,15 @@ pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *tar
 /*
  * pkv_paged_attention_sinks -- pkv_paged_attention with a sliding window and a few first tokens that stay
  * visible: the query row at position p sees the keys t <= p with t < sinks or t > p - window.
- *   window, sinks   >= 0.  window = 0: none (every key up to p, whatever sinks says); sinks = 0: the window alone,
+ *   window, sinks   >= 0.  window = 0 (every key up to p, whatever sinks says) and sinks = 0 (the window alone) are
  *              exactly pkv_paged_attention
  * Blocks that lie wholly behind the sinks and before every row's window are never read, so a caller may
  * free them (entries of -1).  Keys that no row of a sequence sees may hold anything in blocks that are read,
  * NaN and infinities among them; those that some row of the sequence sees must be finite.
  *   workspace  pkv_paged_attention_sinks_workspace_bytes(...) bytes, the rules of pkv_paged_attention
- *   everything else as pkv_paged_attention (PKV_F32 and PKV_BF16 caches).
+ *   MBS * bs < 2^31 - 4096
+ *   everything else as pkv_paged_attention (PKV_F32 and PKV_BF16 caches), but that with window and sinks above 0
+ *              cu_q[B] may be less than Tq: rows behind the last sequence's (a padded batch) are neither read nor written.
  */
 size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
                                                  int window, int sinks, int num_splits);

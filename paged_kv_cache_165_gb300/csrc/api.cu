@@ -421,18 +421,29 @@ pkv_status pkv_paged_attention(float *out, float *lse, const float *q, const voi
                      Hkv, d, bs, MBS, NB, scale, window, 0, num_splits, workspace, workspace_bytes, stream);
 }
 
-// Sinks are needed only where a table can hold a token behind them and before a window; otherwise the call
-// is the plain attention, without a window where a window and the sinks cover every table.
-static void without_needless_sinks(int bs, int MBS, int *window, int *sinks) {
-    if (*window > 0 && static_cast<long long>(*window) + *sinks >= static_cast<long long>(MBS) * bs) *window = 0;
-    if (*window == 0) *sinks = 0;
+// Tokens that a table may hold: the kernels count whole tiles past the last one in 32 bits.
+constexpr long long kSinksTokens = 0x7fffffffll - 4096;
+
+// Sinks without a window, or a window without sinks: the plain attention.  Neither reaches past the tables.
+static void bounded_window(int bs, int MBS, int *window, int *sinks) {
+    const long long tokens = static_cast<long long>(MBS) * bs;
+    *window = static_cast<int>(std::min<long long>(*window, tokens));
+    *sinks = *window == 0 ? 0 : static_cast<int>(std::min<long long>(*sinks, tokens));
+}
+
+// Whether the two cover whatever a table can hold, so that the tensor-core kernels without a window do as well.  (The
+// CUDA-core kernel would not leave a padded batch's rows alone.)
+static bool covers_tables(int bs, int MBS, int window, int sinks) {
+    return sinks > 0 && static_cast<long long>(window) + sinks >= static_cast<long long>(MBS) * bs;
 }
 
 size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
                                                  int window, int sinks, int num_splits) {
-    if (window < 0 || sinks < 0 || bs < 1 || MBS < 1) return 0;
-    without_needless_sinks(bs, MBS, &window, &sinks);
-    return attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits);
+    if (window < 0 || sinks < 0 || bs < 1 || MBS < 1 || static_cast<long long>(MBS) * bs > kSinksTokens) return 0;
+    bounded_window(bs, MBS, &window, &sinks);
+    const size_t n = attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits);
+    if (!covers_tables(bs, MBS, window, sinks)) return n;
+    return std::max(n, attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, 0, 0, num_splits));
 }
 
 pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, const void *k_cache, const void *v_cache,
@@ -443,9 +454,19 @@ pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, con
     if (sinks < 0 || window < 0)
         return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: window=%d sinks=%d", window, sinks);
     if (bs >= 1 && MBS >= 1) {
-        if (static_cast<long long>(MBS) * bs > 0x7fffffffll - bs)
-            return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: MBS=%d bs=%d", MBS, bs);
-        without_needless_sinks(bs, MBS, &window, &sinks);
+        if (static_cast<long long>(MBS) * bs > kSinksTokens)
+            return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: MBS=%d bs=%d (need MBS * bs < 2^31 - 4096)", MBS, bs);
+        bounded_window(bs, MBS, &window, &sinks);
+        // sizes that the call below refuses are not planned for
+        if (covers_tables(bs, MBS, window, sinks) && dt == PKV_BF16 && check_decode_sizes(B, Hq, Hkv, d, bs, MBS) == PKV_OK && NB >= 1 &&
+            num_splits >= 0 && Tq >= 0 && max_q >= 0) {
+            const bool aligned = aligned16(k_cache) && aligned16(v_cache);
+            const DecodePlan plan =
+                Tq == B && max_q == 1
+                    ? plan_decode(B, Hq, Hkv, d, bs, MBS, NB, dt, num_splits, 1, aligned, aligned16(q))
+                    : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, MBS, NB, dt, 0, num_splits, 1, aligned, aligned16(q));
+            if (plan.tensor_core) window = sinks = 0;
+        }
     }
     return attention("paged_attention_sinks", out, lse, q, k_cache, v_cache, dt, block_table, context_lens, cu_q, B, Tq, max_q,
                      Hq, Hkv, d, bs, MBS, NB, scale, window, sinks, num_splits, workspace, workspace_bytes, stream);

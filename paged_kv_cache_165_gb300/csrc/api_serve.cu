@@ -196,6 +196,8 @@ pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *tar
     if (B == 0) return PKV_OK;
     if (!accepted || !tokens || !target_probs || !cu_drafts || !uniforms || (D > 0 && !draft_tokens))
         return fail(PKV_ERR_INVALID_ARG, "verify_drafts: null pointer");
+    if (overlap(tokens, (static_cast<size_t>(D) + B) * 4, draft_tokens, static_cast<size_t>(D) * 4))
+        return fail(PKV_ERR_INVALID_ARG, "verify_drafts: tokens overlaps draft_tokens");
     int sm_count = 0;
     unsigned *err = nullptr;
     const pkv_status s = current_device_info(&sm_count, &err);

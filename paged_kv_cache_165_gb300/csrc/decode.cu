@@ -584,6 +584,10 @@ __global__ void __launch_bounds__(32)
     const int lane = threadIdx.x;
     const int row = blockIdx.x, i = blockIdx.y, split = blockIdx.z;
     const int kvh = i / p.m;
+    if (SINKS && p.cu_q != nullptr) {   // rows behind the last sequence's (a padded batch) are left as they are
+        const int end = __ldg(p.cu_q + p.B);
+        if (row >= end && end >= max(0, __ldg(p.cu_q + p.B - 1))) return;
+    }
     const SeqSpan sp = row_span<SINKS>(p, row, bs, lane == 0 && split == 0 && i == 0);
     const int b = sp.b;
     const int len = sp.len;

@@ -162,6 +162,23 @@ def test_rows_that_a_sequence_may_not_own(dtype, hq):
     assert (out[5:] == 0).all() and (lse[5:] == -math.inf).all()
 
 
+@pytest.mark.parametrize("window", [300, 1000, 2 ** 31 - 1])      # the last two cover the tables
+@pytest.mark.parametrize("dtype,hq,splits", [(BF16, 16, 1), (BF16, 4, 0), (F32, 4, 1), (F32, 4, 3), (BF16, 4, 12), (BF16, 130, 0)])
+def test_rows_behind_the_last_sequence_stay_as_they_are(dtype, hq, splits, window):
+    lens, nqs = [40, 900, 30], [3, 2, 4]
+    q, kc, vc, _, _, table, _, clens, cu = make_case(8, lens, nqs, hq, 2, 64, 16, dtype, window, 4)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / 8, window, 4)
+    padded = torch.cat([q, torch.full((3, hq, 64), float("nan"))])
+    n = pkv.paged_attention_sinks_workspace_bytes(3, 12, 4, hq, 2, 64, 16, table.shape[1], window, 4, splits)
+    out, lse = torch.full((12, hq, 64), 7.0, device="cuda"), torch.full((12, hq), 7.0, device="cuda")
+    pkv.paged_attention_sinks(out, dev(padded), dev(kc), dev(vc), dev(table), dev(clens), 1 / 8, window, 4, cu_q=dev(cu), max_q=4, lse=lse,
+                              num_splits=splits, workspace=torch.zeros(max(16, n), dtype=torch.uint8, device="cuda"))
+    assert pkv.get_device_error() == 0
+    assert_attn_close(out[:9], ref, "rows", ATOL[dtype])
+    assert_attn_close(lse[:9], ref_lse, "lse", ATOL[dtype])
+    assert (out[9:] == 7).all() and (lse[9:] == 7).all()
+
+
 def test_streams_and_a_graph_over_growing_lengths():
     lens = [70, 200]
     q, kc, vc, _, _, table, _, clens, cu = make_case(8, lens, [1, 1], 16, 2, 128, 16, BF16, 32, 5)

@@ -134,7 +134,7 @@ def test_paged_attention_sinks_refuses(L):
         return L.pkv_paged_attention_sinks(NZ, None, q, NZ, NZ, dt, NZ, NZ, None, B, Tq, max_q, Hq, Hkv, d, bs, MBS, NB, 0.1, window,
                                            sinks, splits, None, 0, None)
     for kw in (dict(window=-1), dict(sinks=-1), dict(Hq=9), dict(d=300), dict(NB=0), dict(Tq=3), dict(splits=-1),
-               dict(q=P((1 << 20) + 4)), dict(q=None), dict(MBS=1 << 27, bs=16), dict(Tq=2, max_q=2)):
+               dict(q=P((1 << 20) + 4)), dict(q=None), dict(MBS=1 << 27, bs=16), dict(MBS=(1 << 27) - 200, bs=16), dict(Tq=2, max_q=2)):
         assert call(**kw) == INVALID, kw
     assert call(dt=2) == UNSUPPORTED
     assert call(B=0, Tq=0) == 0
@@ -182,13 +182,14 @@ def test_verify_takes_the_lowest_token_past_the_border():
 
 
 def test_verify_drafts_refuses(L):
-    def call(dt=0, ts=100, ds=100, B=2, D=3, V=100, draft=NZ, toks=NZ, lens=None, lens_out=None, tokens=NZ):
+    def call(dt=0, ts=100, ds=100, B=2, D=3, V=100, draft=NZ, toks=P(1 << 22), lens=None, lens_out=None, tokens=NZ):
         return L.pkv_verify_drafts(NZ, tokens, NZ, draft, dt, ts, ds, toks, NZ, NZ, lens, lens_out, B, D, V, None)
     for kw in (dict(ts=99), dict(ds=99), dict(B=-1), dict(B=65536), dict(D=-1), dict(V=0), dict(V=1 << 30, ts=1 << 30, ds=1 << 30),
                dict(toks=None), dict(tokens=None), dict(lens=NZ), dict(lens_out=NZ), dict(ts=1 << 41)):
         assert call(**kw) == INVALID, kw
     assert call(dt=2) == UNSUPPORTED
     assert call(B=0) == 0
+    assert call(toks=P((1 << 20) + 8)) == INVALID and b"overlaps" in L.pkv_last_error()
 
 
 # --------------------------------------------------------- tables that share blocks
