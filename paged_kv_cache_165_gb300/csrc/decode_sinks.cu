@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(SinksCfg<D, BS, TILES>::NW * 32, SinksCfg<D, B
     // only as many tiles as the CTA has pairs for (rows of a sequence and heads of a KV head differ)
     if (TILES == 1 || w.npairs <= 8) attend_pages<D, BS, TILES, 1>(tm_k, tm_v, p, s_work, smem, bars);
     else attend_pages<D, BS, TILES, TILES>(tm_k, tm_v, p, s_work, smem, bars);
-    finish_sinks<D, C::kPairs, NW>(smem, p, s_work, groups);
+    __shared__ int s_last;
+    finish_sinks<D, C::kPairs, NW>(smem, &s_last, p, s_work, groups);
 }
 
 template <int D, int BS, int TILES>

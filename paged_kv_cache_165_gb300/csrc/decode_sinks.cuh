@@ -94,9 +94,10 @@ __device__ __forceinline__ bool sinks_work(const DecodeKParams &p, int groups, S
 // The end of a block: shared memory holds, from `smem`, the pairs' log-sum-exp (base 2) and NV parts of their
 // normalised outputs, [NV][PAIRS][D], which only remain to be added; the block has synchronised.  A sequence of one
 // chunk writes out and lse; otherwise the chunk's partial goes to the workspace, and where that has arrival
-// counters the block that completes a group of pairs merges its chunks (nobody waits).
+// counters the block that completes a group of pairs merges its chunks (nobody waits).  s_last: a number in shared
+// memory, apart.
 template <int D, int PAIRS, int NV>
-__device__ __forceinline__ void finish_sinks(uint8_t *smem, const DecodeKParams &p, const SinksWork &w, int groups) {
+__device__ __forceinline__ void finish_sinks(uint8_t *smem, int *s_last, const DecodeKParams &p, const SinksWork &w, int groups) {
     const float *lse2 = reinterpret_cast<const float *>(smem), *ow = lse2 + PAIRS;
     const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
     auto put = [&](float *dst, float4 x) {
@@ -131,16 +132,15 @@ __device__ __forceinline__ void finish_sinks(uint8_t *smem, const DecodeKParams 
     }
     if (w.nc == 1 || p.counters == nullptr) return;
 
-    __shared__ int s_last;
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
         unsigned *ctr = p.counters + (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * groups + w.group;
-        s_last = atomicAdd(ctr, 1u) + 1 == static_cast<unsigned>(w.nc);
-        if (s_last) *ctr = 0u;   // every chunk of this call has arrived
+        *s_last = atomicAdd(ctr, 1u) + 1 == static_cast<unsigned>(w.nc);
+        if (*s_last) *ctr = 0u;   // every chunk of this call has arrived
     }
     __syncthreads();
-    if (!s_last) return;
+    if (!*s_last) return;
     __threadfence();
     float *wt = reinterpret_cast<float *>(smem);   // [pairs][chunks] the chunks' weights
     if (threadIdx.x < w.npairs) {

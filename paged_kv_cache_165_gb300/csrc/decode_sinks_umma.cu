@@ -37,14 +37,16 @@ template <int D, int BS>
 struct SinksUmmaCfg {
     static constexpr int kBM = 128, kTK = kSinksUmmaKeys, kPPT = kTK / BS, PANELS = D / 64, kPairs = kSinksUmmaPairs;
     static constexpr int kSlotBytes = kTK * D * 2;                    // one K or V tile: panels of [64][128 B]
-    static constexpr int NT = D == 128 ? 2 : 4;                       // slots of the K ring, and of the V ring
+    static constexpr int NK = D == 128 ? 2 : 6, NV = D == 128 ? 3 : 6;   // slots of the rings; a V tile waits for its weights
     static constexpr int kQBytes = kBM * D * 2;                       // panels of [128][128 B]
-    static constexpr int kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + NT * kSlotBytes, kOffBar = kOffV + NT * kSlotBytes;
+    static constexpr int kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + NK * kSlotBytes, kOffBar = kOffV + NV * kSlotBytes;
     // barriers: Q built; K full / free per slot; V full / free per slot; S full x2; O full x2; P full; drain x2
-    static constexpr int kQ = 0, kKFull = 1, kKFree = kKFull + NT, kVFull = kKFree + NT, kVFree = kVFull + NT,
-                         kSFull = kVFree + NT, kOFull = kSFull + 2, kPFull = kOFull + 2, kDrain = kPFull + 1, kNumBars = kDrain + 2;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;           // TMEM slot, abort flag
-    static constexpr int kSmemBytes = 1024 + kOffMisc + 16;
+    static constexpr int kQ = 0, kKFull = 1, kKFree = kKFull + NK, kVFull = kKFree + NK, kVFree = kVFull + NV,
+                         kSFull = kVFree + NV, kOFull = kSFull + 2, kPFull = kOFull + 2, kDrain = kPFull + 1, kNumBars = kDrain + 2;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;           // TMEM slot, abort flag, and the end's flag
+    static constexpr int kOffWork = (kOffMisc + 16 + 15) / 16 * 16;   // the block's SinksWork
+    // all shared memory is dynamic and starts on the swizzle's 1024 bytes (checked), none of it spent on aligning
+    static constexpr int kSmemBytes = kOffWork + static_cast<int>(sizeof(SinksWork));
     static constexpr int kTmemCols = 256;                             // two S buffers (P over them), O
     static constexpr int kSCol = 0, kOCol = 2 * kTK;
     static constexpr int kThreads = 256;
@@ -60,17 +62,20 @@ __global__ void __launch_bounds__(256, 2)
     decode_sinks_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeKParams p,
                              const int groups) {
     using C = SinksUmmaCfg<D, BS>;
-    constexpr int BM = C::kBM, TK = C::kTK, PPT = C::kPPT, PANELS = C::PANELS, NT = C::NT;
+    constexpr int BM = C::kBM, TK = C::kTK, PPT = C::kPPT, PANELS = C::PANELS, NK = C::NK, NV = C::NV;
 
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     auto bar = [&](int k) { return smem_addr(&bars[k]); };
 
     pdl_launch_dependents();   // a merge kernel after this one waits for the whole grid
-    __shared__ SinksWork s_work;   // for the block's end: its numbers take no registers meanwhile
+    if (smem_addr(smem) % 1024 != 0) {
+        if (threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_LAYOUT);
+        return;
+    }
+    SinksWork &s_work = *reinterpret_cast<SinksWork *>(smem + C::kOffWork);   // for the block's end: no registers meanwhile
     SinksWork w;
     if (!sinks_work<D, BS, C::kPairs>(p, groups, w)) return;
     if (threadIdx.x == 0) s_work = w;
@@ -80,9 +85,11 @@ __global__ void __launch_bounds__(256, 2)
 
     if (threadIdx.x == 0) {
         mbar_init(bar(C::kQ), 4);
-        for (int s = 0; s < NT; ++s) {
+        for (int s = 0; s < NK; ++s) {
             mbar_init(bar(C::kKFull + s), 1);
             mbar_init(bar(C::kKFree + s), 1);
+        }
+        for (int s = 0; s < NV; ++s) {
             mbar_init(bar(C::kVFull + s), 1);
             mbar_init(bar(C::kVFree + s), 1);
         }
@@ -112,9 +119,10 @@ __global__ void __launch_bounds__(256, 2)
     bool ok = true;
 
     if (warp == 4 || warp == 5) {
-        // ---- TMA: tile t into slot t % NT once the slot's last tile is used.  Lane i < PPT * PANELS copies panel
+        // ---- TMA: tile t into slot t % N of its ring once the slot's last tile is used.  Lane i < PPT * PANELS copies panel
         // i % PANELS of page i / PANELS; a page past the chunk is placed outside the cache (zeros)
         const bool is_k = warp == 4;
+        const int N = is_k ? NK : NV;
         const int full0 = is_k ? C::kKFull : C::kVFull, free0 = is_k ? C::kKFree : C::kVFree;
         const CUtensorMap *map = is_k ? &tm_k : &tm_v;
         const int32_t *tbl = p.block_table + static_cast<size_t>(w.b) * p.MBS;
@@ -125,9 +133,9 @@ __global__ void __launch_bounds__(256, 2)
         int t = 0;
         for (; t < ntiles; ++t) {
             bool fr = true;
-            if (lane == 0 && t >= NT) fr = wait_or_abort(bar(free0 + t % NT), ((t - NT) / NT) & 1, abort, p.err);
+            if (lane == 0 && t >= N) fr = wait_or_abort(bar(free0 + t % N), ((t - N) / N) & 1, abort, p.err);
             if (!__shfl_sync(kFull, fr ? 1 : 0, 0)) break;
-            const int s = t % NT;
+            const int s = t % N;
             if (t * PPT >= tbase + 32) {   // a tile never straddles 32 pages
                 tbase += 32;
                 tcur = tnext;
@@ -151,8 +159,8 @@ __global__ void __launch_bounds__(256, 2)
         }
         // before teardown every copy issued must have landed (bounded)
         if (lane == 0)
-            for (int u = max(0, t - NT); u < t; ++u)
-                if (!mbar_wait_bounded(bar(full0 + u % NT), (u / NT) & 1)) raise_error(p.err, PKV_DEVERR_TIMEOUT);
+            for (int u = max(0, t - N); u < t; ++u)
+                if (!mbar_wait_bounded(bar(full0 + u % N), (u / N) & 1)) raise_error(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 6 || warp == 7) {
         // ---- MMA issue.  Warp 6: S_t into buffer t & 1 once K_t has landed and O_{t-2} is done (P_{t-2}, in that
         // buffer, has been read).  Warp 7: O_t once P_t is written (O_{t-1} has then been read) and V_t has landed.
@@ -163,8 +171,8 @@ __global__ void __launch_bounds__(256, 2)
                 const uint32_t idesc = umma_idesc_bf16(BM, TK, 0);
                 alive = wait_or_abort(bar(C::kQ), 0, abort, p.err);
                 for (int t = 0; t < ntiles && alive; ++t) {
-                    const int s = t % NT, x = t & 1;
-                    alive = wait_or_abort(bar(C::kKFull + s), (t / NT) & 1, abort, p.err);
+                    const int s = t % NK, x = t & 1;
+                    alive = wait_or_abort(bar(C::kKFull + s), (t / NK) & 1, abort, p.err);
                     if (alive && t >= 2) alive = wait_or_abort(bar(C::kOFull + x), ((t - 2) >> 1) & 1, abort, p.err);
                     if (!alive) break;
                     tc_fence_after_sync();
@@ -181,9 +189,9 @@ __global__ void __launch_bounds__(256, 2)
             } else {
                 const uint32_t idesc = umma_idesc_bf16(BM, D, 1);
                 for (int t = 0; t < ntiles && alive; ++t) {
-                    const int s = t % NT, x = t & 1;
+                    const int s = t % NV, x = t & 1;
                     alive = wait_or_abort(bar(C::kPFull), t & 1, abort, p.err) &&
-                            wait_or_abort(bar(C::kVFull + s), (t / NT) & 1, abort, p.err);
+                            wait_or_abort(bar(C::kVFull + s), (t / NV) & 1, abort, p.err);
                     if (!alive) break;
                     tc_fence_after_sync();
 #pragma unroll
@@ -261,9 +269,9 @@ __global__ void __launch_bounds__(256, 2)
             const bool whole = v0 + TK <= min(w.all_hi, v_end) && (v0 >= w.all_lo || v0 + TK <= S);
             if (ok && !whole) {
                 // V rows that no pair sees hold whatever the slots hold (NaN, Inf): cleared once they have landed
-                ok = __all_sync(kFull, wait_or_abort(bar(C::kVFull + t % NT), (t / NT) & 1, abort, p.err));
+                ok = __all_sync(kFull, wait_or_abort(bar(C::kVFull + t % NV), (t / NV) & 1, abort, p.err));
                 if (ok) {
-                    uint8_t *vt = smem + C::kOffV + (t % NT) * C::kSlotBytes;
+                    uint8_t *vt = smem + C::kOffV + (t % NV) * C::kSlotBytes;
                     for (int i = threadIdx.x; i < TK * PANELS * 8; i += 128) {
                         const int r = i / (PANELS * 8), c = i % (PANELS * 8), v = v0 + r;
                         if (v >= w.hi || (v >= S && v < w.lo))
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(256, 2)
             *reinterpret_cast<float2 *>(ow + pair * D + (n >> 3) * 64 + (n & 7) * 8 + 2 * c4) = make_float2(o[n].x * f, o[n].y * f);
     }
     __syncthreads();
-    finish_sinks<D, C::kPairs, 1>(smem, p, s_work, groups);
+    finish_sinks<D, C::kPairs, 1>(smem, reinterpret_cast<int *>(smem + C::kOffMisc + 8), p, s_work, groups);
 }
 
 template <int D, int BS>

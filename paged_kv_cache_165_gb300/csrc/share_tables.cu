@@ -196,13 +196,21 @@ __device__ __forceinline__ unsigned blocks_of(const ShareArgs &a, int len) {
 // Every entry of the B rows, eight a thread at a time: first all are loaded (x = load(source, b, j)), then all
 // looked up (x = map(x)), then all put to use (use(source, b, j, x)), so that a thread's loads overlap.
 // ONE: entries one after the other, their rows' sources (s_rows) at hand; else 256 entries of a row to a warp.
+// The first pass (FIRST) starts with the team's barrier, past the loads of the cluster's first entries, which
+// `held` keeps for the second pass.
 constexpr int kAhead = 8, kSegment = 32 * kAhead;
 
-template <bool ONE, typename Load, typename Map, typename Use>
-__device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> &team, const Source *s_rows, bool report, Load load,
+struct Held {
+    Source s;
+    int x[kAhead];
+};
+
+template <bool FIRST, bool ONE, typename Load, typename Map, typename Use>
+__device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> &team, const Source *s_rows, Held &held, Load load,
                                             Map map, Use use) {
     const unsigned MBS = a.MBS;
     if constexpr (ONE) {
+        if constexpr (FIRST) team.sync();
         // i / MBS for i, MBS <= 65536 (i < 2^16 where MBS > 1): the rounding of 2^32 / MBS upwards adds less than 1 / MBS
         const unsigned total = a.B * MBS, inv = MBS > 1 ? 0xffffffffu / MBS + 1 : 0;
         for (unsigned i0 = threadIdx.x; i0 < total; i0 += kAhead * kThreads) {
@@ -225,24 +233,41 @@ __device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> 
     } else {
         const unsigned warp = team.tid() >> 5, lane = threadIdx.x & 31, segments = (MBS + kSegment - 1) / kSegment;
         const unsigned long long items = static_cast<unsigned long long>(a.B) * segments;
-        for (unsigned long long i = warp; i < items; i += Team<ONE>::kAll / 32) {
+        unsigned long long i = warp;
+        do {
             const unsigned b = static_cast<unsigned>(i / segments);
             const unsigned j0 = static_cast<unsigned>(i - static_cast<unsigned long long>(b) * segments) * kSegment + lane;
-            const Source s = source_of(a, b, report && j0 == 0);
+            Source s{-1, 0};
             int x[kAhead];
+            if (FIRST || i != warp) {
+                if (i < items) s = source_of(a, b, FIRST && j0 == 0);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) x[k] = j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
+                for (int k = 0; k < kAhead; ++k) x[k] = i < items && j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
+            } else {
+                s = held.s;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) x[k] = held.x[k];
+            }
+            if (FIRST && i == warp) {
+                held.s = s;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) held.x[k] = x[k];
+                team.sync();
+            }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
+            if (i < items) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (j0 + 32 * k < MBS) use(s, b, j0 + 32 * k, x[k]);
-        }
+                for (int k = 0; k < kAhead; ++k)
+                    if (j0 + 32 * k < MBS) use(s, b, j0 + 32 * k, x[k]);
+            }
+            i += Team<ONE>::kAll / 32;
+        } while (i < items);
     }
 }
 
 // The start of both kernels: the ids' two numbers (in shared memory for one block) cleared to (held, second), and one
-// block's rows' sources.
+// block's rows' sources.  No barrier yet.
 template <bool ONE>
 __device__ __forceinline__ void clear(const ShareArgs &a, const Team<ONE> &team, int *refs, int *other, int second, Source *s_rows) {
     for (unsigned i = team.tid(); i < static_cast<unsigned>(a.NB); i += Team<ONE>::kAll) {
@@ -251,7 +276,6 @@ __device__ __forceinline__ void clear(const ShareArgs &a, const Team<ONE> &team,
     }
     if constexpr (ONE)
         for (unsigned b = threadIdx.x; b < static_cast<unsigned>(a.B); b += kThreads) s_rows[b] = source_of(a, b, true);
-    team.sync();
 }
 
 template <bool ONE>
@@ -266,11 +290,11 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
     clear(a, team, refs, first, kNobody, s_rows);
     int32_t *rows = a.rows;   // [B][MBS] of the result: the table itself where nothing reads the parents' rows any more
-    auto same = [](int x) { return x; };
-    for_entries(a, team, s_rows, true,
+    Held held;
+    for_entries<true>(a, team, s_rows, held,
                 [&](const Source &s, unsigned, unsigned j) {
                     return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(max(s.row, 0)) * a.MBS + j] : -1;
-                }, same,
+                }, [](int x) { return x; },
                 [&](const Source &s, unsigned b, unsigned j, int x) {
                     x = checked(a, x);
                     const bool last = s.len % a.bs != 0 && j == static_cast<unsigned>(s.len / a.bs);   // partly filled
@@ -376,7 +400,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
     auto entry = [&](const Source &s, unsigned b, unsigned j) {
         return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(b) * a.MBS + j] : -1;
     };
-    for_entries(a, team, s_rows, true, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
+    Held first;
+    for_entries<true>(a, team, s_rows, first, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
         x = checked(a, x);
         if (x >= 0) atomicAdd(refs + x, 1);
     });
@@ -440,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         }
     }
     team.sync();
-    for_entries(a, team, s_rows, false, entry, [&](int x) { return x >= 0 && x < a.NB ? moved[x] : -1; },
+    for_entries<false>(a, team, s_rows, first, entry, [&](int x) { return x >= 0 && x < a.NB ? moved[x] : -1; },
                 [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
 }
 
