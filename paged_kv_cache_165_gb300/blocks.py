@@ -267,10 +267,10 @@ class DeviceBlocks:
     Every method only enqueues work on the given stream (default: the current one; no host
     round trip), so a decode loop over them can be captured into a CUDA graph.  While rows
     share blocks (from a ``fork`` on), blocks go back through ``settle``, which counts who uses
-    them; ``release`` and ``finish`` are for rows that own their blocks.  ``rows`` is the batch size, ``max_blocks`` the blocks a row may hold (no more than
-    the contexts need: the attention's plan goes by the table's width), ``max_tokens`` the most
-    tokens one ``extend`` places; ``order`` is the order in which blocks are handed out (default
-    0..NB-1).
+    them; ``release`` and ``finish`` are for rows that own their blocks.  ``rows`` is the batch
+    size, ``max_blocks`` the blocks a row may hold (no more than the contexts need: the
+    attention's plan goes by the table's width), ``max_tokens`` the most tokens one ``extend``
+    places; ``order`` is the order in which blocks are handed out (default 0..NB-1).
     """
 
     def __init__(self, num_blocks: int, block_size: int, rows: int, max_blocks: int, max_tokens: int,

@@ -5,10 +5,12 @@
 // The pages between them are left out of the count (sinks_span in decode_kparams.cuh), so that a chunk of
 // pages is again a run of consecutive numbers and only table entries and masks know of the gap.
 //
-// One CTA per (sequence, KV head, group of (query row, head) pairs, chunk of pages); every warp streams its own
-// pages (round robin) through a private ring of TMA stages and attends all of the CTA's pairs to each, so
-// that a page leaves HBM once per KV head and no warp waits for another.  Eight pairs make a tile of the
-// m16n8k16 bf16 MMAs.
+// This kernel, for up to eight (query row, head) pairs per sequence and KV head (more with d = 256): one CTA per
+// (sequence, KV head, group of pairs, chunk of pages).  Every warp streams its own pages (round robin) through a
+// private ring of TMA stages and attends all of the CTA's pairs to each, so that a page leaves HBM once per KV head
+// and no warp waits for another.  Eight pairs make a tile of the m16n8k16 bf16 MMAs: bound by HBM, tcgen05's 128
+// rows would be a sixteenth used (and measured 188 us where this takes 172).  More pairs: decode_sinks_umma.cu.
+// 64 sequences, window 4096 + 4, 32 heads on 8 of 128: 172 us, 6.25 TB/s, 92% of the measured copy rate.
 //
 // Precision: the results are as exact as fp32 arithmetic on the bf16 cache.  q and the softmax weights enter
 // the tensor cores as three bf16 parts (8 + 8 + 8 bits, all of an fp32 number): rows 0-7 of an MMA hold the
@@ -425,8 +427,8 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
         return plan;
     const long long pairs = static_cast<long long>(max_q) * (Hq / Hkv), tiles = (pairs + 7) / 8;
     plan.umma = pairs > kSinksMmaPairs && d <= 128;
-    // warp MMAs: two tiles a block at most; four, which read each page once for 32 pairs where two blocks read it from
-    // L2, left too few warps an SM (1 to 4 rows of 64 heads on 8: 187 us; two tiles a block: 173)
+    // more than eight pairs on tcgen05 (16 heads a KV head 22.7 us against 24.8 on warp MMAs, 1 to 4 rows of 8 104
+    // against 155), eight and fewer on warp MMAs (above); d = 256 on these alone, two tiles a block at most
     plan.tiles = plan.umma ? kSinksUmmaPairs / 8 : tiles == 1 ? 1 : 2;
     const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
     const long long units = static_cast<long long>(B) * Hkv * groups;

