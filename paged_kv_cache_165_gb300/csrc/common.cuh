@@ -118,7 +118,8 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // ----------------------------------------------------------------------- TMA
 
 // A launch whose blocks may be scheduled while the kernel before it on the stream drains; the kernel calls
-// pdl_wait() before it reads or writes anything that an earlier kernel may touch.
+// pdl_wait() before it reads or writes anything that an earlier kernel may touch, and reads it by plain loads: __ldg and
+// __restrict__ promise memory that does not change, and loads of that may be moved ahead of the wait.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t shared, cudaStream_t stream,
                                     Args... args) {

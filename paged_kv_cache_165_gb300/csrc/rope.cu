@@ -82,12 +82,12 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeArgs a) {
     const int nt = static_cast<int>(min(static_cast<long long>(a.block_tokens), a.T - t0));
     for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
         const int t = i / pairs, j = i - t * pairs;
-        s_cs[i] = turned(__ldg(a.positions + t0 + t), __ldg(a.turns + j), a.inverse, a.mscale);
+        s_cs[i] = turned(a.positions[t0 + t], a.turns[j], a.inverse, a.mscale);
     }
     if (threadIdx.x < nt) {
         long long row = (t0 + threadIdx.x) * a.Hkv;
         if (a.slots != nullptr) {
-            const long long slot = __ldg(a.slots + t0 + threadIdx.x);
+            const long long slot = a.slots[t0 + threadIdx.x];
             const bool ok = slot >= 0 && slot < a.n_slots;   // < 0: padding
             if (slot >= a.n_slots && blockIdx.y == 0) raise_error(a.err, PKV_DEVERR_SLOT);
             row = ok ? slot / a.bs * a.Hkv * a.bs + slot % a.bs : -1;

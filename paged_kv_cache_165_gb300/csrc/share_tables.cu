@@ -170,7 +170,7 @@ struct Source {
 };
 
 __device__ __forceinline__ Source source_of(const ShareArgs &a, int b, bool report) {
-    Source s{a.parents != nullptr ? __ldg(a.parents + b) : b, 0};
+    Source s{a.parents != nullptr ? a.parents[b] : b, 0};
     if (s.row < -1 || s.row >= a.B) {
         if (report) raise_error(a.err, PKV_DEVERR_PAIR);
         s.row = -1;
@@ -274,7 +274,7 @@ __device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> 
 template <bool ONE>
 __device__ __forceinline__ void clear(const ShareArgs &a, const Team<ONE> &team, int *refs, int *other, int second, Source *s_rows) {
     for (unsigned i = team.tid(); i < static_cast<unsigned>(a.NB); i += Team<ONE>::kAll) {
-        refs[i] = a.held != nullptr && __ldg(a.held + i) != 0 ? 1 : 0;
+        refs[i] = a.held != nullptr && a.held[i] != 0 ? 1 : 0;
         other[i] = second;
     }
     if constexpr (ONE)
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
     int *refs = ONE ? s_ids : a.refs;              // entries that name a block
     int *moved = ONE ? s_ids + NB : a.first;       // where it goes; for now, of one that moves, its rank: -1 - rank
     Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
-    auto held = [&](unsigned i) { return a.held != nullptr && __ldg(a.held + i) != 0; };
+    auto held = [&](unsigned i) { return a.held != nullptr && a.held[i] != 0; };
     clear(a, team, refs, moved, 0, s_rows);
     auto entry = [&](const Source &s, unsigned b, unsigned j) {
         return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(b) * a.MBS + j] : -1;
@@ -478,10 +478,10 @@ constexpr int kCopyThreads = 256, kCopyAhead = 8;
 
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads)
-    kv_block_copy_counted_kernel(U *__restrict__ kc, U *__restrict__ vc, const int32_t *__restrict__ pairs, int n,
-                                 const int32_t *__restrict__ count, long long block_units, int NB, unsigned *err) {
+    kv_block_copy_counted_kernel(U *kc, U *vc, const int32_t *pairs, int n, const int32_t *count, long long block_units, int NB,
+                                 unsigned *err) {
     pdl_wait();
-    int live = __ldg(count);
+    int live = *count;
     if (live < 0 || live > n) {
         if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(err, PKV_DEVERR_PAIR);
         live = max(0, min(live, n));
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     const long long per = (block_units + span - 1) / span, pieces = 2 * per * live;
     for (long long w = blockIdx.x; w < pieces; w += gridDim.x) {
         const long long pair = w / (2 * per), rest = w - pair * 2 * per;
-        const int src = __ldg(pairs + 2 * pair), dst = __ldg(pairs + 2 * pair + 1);
+        const int src = pairs[2 * pair], dst = pairs[2 * pair + 1];
         if (src < 0 || src >= NB || dst < 0 || dst >= NB) {
             if (rest == 0 && threadIdx.x == 0) raise_error(err, PKV_DEVERR_PAIR);
             continue;

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     const int b = blockIdx.x / blocks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool lead = rank == 0 && threadIdx.x == 0;
-    const int c0 = __ldg(a.cu_drafts + b), c1 = __ldg(a.cu_drafts + b + 1);
+    const int c0 = a.cu_drafts[b], c1 = a.cu_drafts[b + 1];
     if (c0 < 0 || c1 < c0 || c1 > a.D) {   // the whole cluster leaves: nothing is written but what refuses
         if (lead) {
             raise_error(a.err, PKV_DEVERR_CU_SEQLENS);
@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
             const int i = i0 + lane;
             bool yes = true;
             if (i < k) {
-                const int x = __ldg(a.draft_tokens + c0 + i);
-                yes = accepts<T>(a, row0 + i, c0 + static_cast<long long>(i), x, __ldg(a.uniforms + row0 + i));
+                const int x = a.draft_tokens[c0 + i];
+                yes = accepts<T>(a, row0 + i, c0 + static_cast<long long>(i), x, a.uniforms[row0 + i]);
                 if (!yes && (x < 0 || x >= a.V) && rank == 0) raise_error(a.err, PKV_DEVERR_PROBS);
             }
             const unsigned no = __ballot_sync(kFull, !yes);
@@ -241,14 +241,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     r.p = static_cast<const T *>(a.target) + (row0 + acc) * a.target_stride;
     r.q = acc < k && a.draft != nullptr ? static_cast<const T *>(a.draft) + (c0 + static_cast<long long>(acc)) * a.draft_stride
                                         : nullptr;
-    r.not_this = acc < k && a.draft == nullptr ? __ldg(a.draft_tokens + c0 + acc) : -1;
+    r.not_this = acc < k && a.draft == nullptr ? a.draft_tokens[c0 + acc] : -1;
 
     // runs of whole pieces, one for each warp of the cluster
     const int runs = blocks * kWarps;
     const int run = ((a.V + runs - 1) / runs + 32 * N - 1) / (32 * N) * (32 * N);
     const long long at = static_cast<long long>(rank * kWarps + warp) * run;
     const int lo = static_cast<int>(min(at, static_cast<long long>(a.V))), hi = static_cast<int>(min(at + run, static_cast<long long>(a.V)));
-    const u64 u = share_of_turn(__ldg(a.uniforms + row0 + k));
+    const u64 u = share_of_turn(a.uniforms[row0 + k]);
     int token = -1;
     bool mine = false;   // this warp holds the border
     for (int pass = 0;; ++pass) {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     if (mine && lane == 0) a.tokens[row0 + acc] = token;
     if (rank == 0) {
         for (int i = threadIdx.x; i <= k; i += kThreads)
-            if (i != acc) a.tokens[row0 + i] = i < acc ? __ldg(a.draft_tokens + c0 + i) : -1;
+            if (i != acc) a.tokens[row0 + i] = i < acc ? a.draft_tokens[c0 + i] : -1;
         if (threadIdx.x == 0) {
             a.accepted[b] = acc;
             if (a.lens_out != nullptr) a.lens_out[b] = a.lens[b] - (k - acc);

@@ -157,3 +157,51 @@ def test_a_serving_loop(dtype, captured):
             loop.copy()
             assert int(loop.blocks.block_table.max()) < NB - int(loop.blocks.free_count)
         assert pkv.get_device_error() == 0
+
+
+def test_dependents_read_what_the_kernel_before_them_wrote():
+    # The attention lets the next kernel's blocks be scheduled while it runs, and writes its outputs last: they serve as
+    # positions, random numbers and a pair count here, each read by a call right behind the attention.
+    T, hq, hkv, d, bs, ctx = 64, 32, 8, 64, 16, 2048
+    g = torch.Generator().manual_seed(3)
+    nb = T * ctx // bs
+    kc, vc = (torch.rand((nb, hkv, bs, d), generator=g).bfloat16().cuda() for _ in range(2))
+    less = -vc
+    table = torch.arange(nb, **I32).view(T, -1)
+    lens = torch.full((T,), ctx, **I32)
+    q = torch.randn((T, hq, d), generator=g).cuda()
+    out = torch.empty((T, hq, d), device="cuda")
+    n = pkv.paged_attention_sinks_workspace_bytes(T, T, 1, hq, hkv, d, bs, ctx // bs, 1024, 4)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
+    bits = out.view(torch.int32).flatten()
+    turns, x = pkv.rope_turns(128), torch.randn((4096, 4, 128), generator=g).cuda()
+    probs = torch.softmax(torch.randn((T, 999), generator=g), 1).cuda()
+    cu = torch.arange(T + 1, **I32).mul_(0)
+    none = torch.zeros(0, **I32)
+    moved = torch.stack([torch.arange(100, **I32), torch.arange(100, 200, **I32)], 1)
+
+    def calls():
+        rotated, tokens, accepted = torch.empty_like(x), torch.full((T,), -9, **I32), torch.full((T,), -9, **I32)
+        k2, v2 = kc[:200].clone(), vc[:200].clone()
+        yield rotated, lambda: pkv.rope(rotated, x, None, None, bits[:4096], turns)
+        yield tokens, lambda: pkv.verify_drafts(accepted, tokens, probs, none, cu, out.flatten()[:T])
+        yield k2, lambda: pkv.kv_block_copy(k2, v2, moved, count=bits[:1])
+
+    def attend(values):
+        pkv.paged_attention_sinks(out, q, kc, values, table, lens, 0.125, 1024, 4, workspace=ws)
+
+    for i in range(3):
+        got = []
+        for waits in (True, False):
+            for j, (result, call) in enumerate(calls()):
+                if i == j:
+                    torch.cuda.synchronize()
+                    attend(less)                        # what stands there before: the same with the other sign
+                    attend(vc)
+                    if waits:
+                        torch.cuda.synchronize()
+                    call()
+                    got.append(result.clone())
+        torch.cuda.synchronize()
+        assert torch.equal(*got), i
+    pkv.get_device_error()                              # a count beyond the list
