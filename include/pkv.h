@@ -685,6 +685,7 @@ pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *tar
  *   MBS * bs < 2^31 - 4096
  *   everything else as pkv_paged_attention (PKV_F32 and PKV_BF16 caches), but that with window and sinks above 0
  *              cu_q[B] may be less than Tq: rows behind the last sequence's (a padded batch) are neither read nor written.
+ *              cu_q is therefore read whenever it is given (NULL: Tq == B and one row each)
  */
 size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
                                                  int window, int sinks, int num_splits);

@@ -339,11 +339,12 @@ static size_t attention_workspace(int B, int Tq, int max_q, int Hq, int Hkv, int
     if (device_state(&st) != PKV_OK) return 0;
     const bool one_per_seq = Tq == B && max_q <= 1;
     const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
-    if (sinks > 0) {   // whatever the caches' type and alignment
-        const size_t simt = one_per_seq
-                                ? plan_decode(B, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, false, false).workspace_bytes
-                                : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits,
-                                                      st->sm_count, false, false).workspace_bytes;
+    if (sinks > 0) {   // whatever the caches' type and alignment, and (one row a sequence) with cu_q or without
+        size_t simt = plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits, st->sm_count, false,
+                                          false).workspace_bytes;
+        if (one_per_seq)
+            simt = std::max(simt, plan_decode(B, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, false,
+                                              false).workspace_bytes);
         return std::max(simt, plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, num_splits, st->sm_count, true).workspace_bytes);
     }
     if (one_per_seq) return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, vis, num_splits, st->sm_count);
@@ -369,7 +370,8 @@ static pkv_status attention(const char *what, float *out, float *lse, const floa
         return fail(PKV_ERR_INVALID_ARG, "%s: NB=%d num_splits=%d window=%d Tq=%d max_q=%d",
                     what, NB, num_splits, window, Tq, max_q);
     if (B == 0 || Tq == 0) return PKV_OK;
-    const bool one_per_seq = Tq == B && max_q == 1;
+    // with sinks the rows may be a padded batch's, so that as many as sequences need not be one each
+    const bool one_per_seq = Tq == B && max_q == 1 && (sinks == 0 || cu_q == nullptr);
     if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens || (!one_per_seq && !cu_q))
         return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", what);
     if (reinterpret_cast<uintptr_t>(q) % 8 != 0)
@@ -432,7 +434,7 @@ static void bounded_window(int bs, int MBS, int *window, int *sinks) {
 }
 
 // Whether the two cover whatever a table can hold, so that the tensor-core kernels without a window do as well.  (The
-// CUDA-core kernel would not leave a padded batch's rows alone.)
+// CUDA-core kernel would not leave a padded batch's rows alone, nor a call that takes Tq = B for a row each.)
 static bool covers_tables(int bs, int MBS, int window, int sinks) {
     return sinks > 0 && static_cast<long long>(window) + sinks >= static_cast<long long>(MBS) * bs;
 }
@@ -458,7 +460,7 @@ pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, con
             return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: MBS=%d bs=%d (need MBS * bs < 2^31 - 4096)", MBS, bs);
         bounded_window(bs, MBS, &window, &sinks);
         // sizes that the call below refuses are not planned for
-        if (covers_tables(bs, MBS, window, sinks) && dt == PKV_BF16 && check_decode_sizes(B, Hq, Hkv, d, bs, MBS) == PKV_OK && NB >= 1 &&
+        if (covers_tables(bs, MBS, window, sinks) && !(Tq == B && max_q == 1 && cu_q != nullptr) && dt == PKV_BF16 && check_decode_sizes(B, Hq, Hkv, d, bs, MBS) == PKV_OK && NB >= 1 &&
             num_splits >= 0 && Tq >= 0 && max_q >= 0) {
             const bool aligned = aligned16(k_cache) && aligned16(v_cache);
             const DecodePlan plan =
