@@ -555,7 +555,7 @@ pkv_status pkv_block_tables_release(int32_t *block_table, const int32_t *first_b
  *
  *   block_table_out, context_lens_out   [B][MBS], [B]; may be block_table and context_lens
  *   held          int32 [NB] or NULL: blocks other than 0 are in use whatever the tables say (a prefix kept
- *                 for later requests)
+ *                 for later requests); apart from refs and free_list
  *   refs          int32 [NB], written: entries that name the block, plus one where it is held; 0: free
  *   free_list     int32 [NB], written: the free blocks in descending order (the lowest is handed out first),
  *                 -1 past free_count[0] of them
@@ -606,7 +606,7 @@ pkv_status pkv_kv_block_copy_counted(void *k_cache, void *v_cache, pkv_dtype dt,
  *   PKV_ROPE_BASE     base * factor^(rot / (rot - 2)) in place of base (rot > 2)
  *   PKV_ROPE_PARTS    f_j (r + (1 - r) / factor), r = (n - low) / (high - low) cut to [0, 1], n = original * f_j
  *                     the turns of the pair over the original context: fast pairs stay, slow ones are interpolated
- *   rot even, >= 2; base > 0; factor > 0; original > 0 and low < high for PKV_ROPE_PARTS.
+ *   rot even, 2 <= rot <= 256; base > 0; factor > 0; original > 0 and low < high for PKV_ROPE_PARTS; every angle finite.
  */
 typedef enum { PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_BASE = 2, PKV_ROPE_PARTS = 3 } pkv_rope_scaling;
 
@@ -623,7 +623,7 @@ pkv_status pkv_rope_turns(uint64_t *turns, int rot, double base, pkv_rope_scalin
  *   positions  int32 [T], any value
  *   turns      uint64 [rot / 2] in device memory (pkv_rope_turns); rot even, 2 <= rot <= d
  *   slot_mapping  int64 [T]: < 0: K and V of the token are not written (padding; q is rotated all the same);
- *              >= NB * bs sets PKV_DEVERR_SLOT, likewise
+ *              >= NB * bs sets PKV_DEVERR_SLOT, likewise; tokens that name the same slot race, as in pkv_kv_append
  *   k_cache, v_cache  [NB][Hkv][bs][d] of type dt
  * Angles as above; cosine and sine, products and their sum in fp32, rounded once to the output's type.  V and
  * K's dimensions past rot are copied bit by bit.  1 <= d <= 256.
@@ -661,12 +661,13 @@ pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q,
  *                 x_i, and r is p_a without x_a)
  *   draft_tokens  int32 [D];  uniforms  fp32 [D + B], in [0, 1)
  *   cu_drafts     int32 [B + 1], non-decreasing from 0 to D; k = 0: one token drawn from p_0
- *   context_lens, context_lens_out   int32 [B] or NULL both; may be the same: L - (k - a), the length of a cache
+ *   context_lens, context_lens_out   int32 [B] or NULL both; the same or apart: L - (k - a), the length of a cache
  *                 that holds the drafts' K and V without those of the rejected ones
  * A drafted token outside [0, V) is rejected and sets PKV_DEVERR_PROBS; probabilities without mass (zero,
- * negative or NaN everywhere) set it too, and the token is -1.  Probabilities count as at most 1.  An
- * inconsistent cu_drafts sets PKV_DEVERR_CU_SEQLENS: the sequence accepts nothing, its length stays and its
- * tokens are not written.  B <= 65535, V < 2^30.
+ * negative or NaN everywhere) set it too, and the token is -1.  In the sums probabilities count as at most 1, negative
+ * ones and NaN as 0; a draft whose p or q is infinite or NaN is rejected.  An inconsistent cu_drafts sets
+ * PKV_DEVERR_CU_SEQLENS: the sequence accepts nothing, its length stays and its tokens are not written.
+ * B <= 65535, V < 2^30.
  */
 pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *target_probs, const void *draft_probs,
                              pkv_dtype dt, long long target_stride, long long draft_stride, const int32_t *draft_tokens,

@@ -136,6 +136,8 @@ class BlockManager:
         ``window`` tokens and none of the first ``sinks``; returns their ids.  The current
         query (position len - 1) sees positions len - window .. len - 1, and later queries
         see later ones."""
+        if sinks < 0:
+            raise ValueError(f"sinks={sinks} is negative")
         if window <= 0:
             return []
         lo = self.lengths[seq] - window

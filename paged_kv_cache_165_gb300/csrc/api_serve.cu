@@ -67,13 +67,16 @@ pkv_status check_in_place(const char *what, const char *name, const void *out, u
 }
 
 pkv_status check_share(const char *what, int B, int MBS, int bs, int NB, const void *table, const void *lens, const void *table_out,
-                       const void *refs, const void *free_list, const void *free_count, const void *pairs, const void *pair_count,
-                       bool want_pairs, const void *workspace, size_t workspace_bytes) {
+                       const void *held, const void *refs, const void *free_list, const void *free_count, const void *pairs,
+                       const void *pair_count, bool want_pairs, const void *workspace, size_t workspace_bytes) {
     if (B < 0 || B > 65536 || MBS < 1 || bs < 1 || NB < 1 || static_cast<long long>(MBS) * bs > 0x7fffffffll - bs)
         return fail(PKV_ERR_INVALID_ARG, "%s: B=%d MBS=%d bs=%d NB=%d (need B <= 65536)", what, B, MBS, bs, NB);
     if (!refs || !free_list || !free_count || !pair_count || (want_pairs && !pairs) || (B > 0 && (!table || !lens || !table_out)))
         return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", what);
     if (want_pairs && !aligned_to(pairs, 8)) return fail(PKV_ERR_INVALID_ARG, "%s: pairs must be 8-byte aligned", what);
+    const size_t ids = static_cast<size_t>(NB) * sizeof(int32_t);   // held is still read when the others are written
+    if (overlap(held, ids, refs, ids) || overlap(held, ids, free_list, ids))
+        return fail(PKV_ERR_INVALID_ARG, "%s: held overlaps refs or free_list", what);
     const size_t need = share_workspace_bytes(B, MBS, NB);
     if (workspace == nullptr || workspace_bytes < need || !aligned_to(workspace, 4))
         return fail(PKV_ERR_WORKSPACE, "%s: needs %zu bytes of 4-byte aligned workspace, got %zu", what, need,
@@ -97,7 +100,8 @@ pkv_status pkv_rope_turns(uint64_t *turns, int rot, double base, pkv_rope_scalin
         (scaling == PKV_ROPE_PARTS && (!(original > 0) || !std::isfinite(original) || !(low < high) || !std::isfinite(high - low))))
         return fail(PKV_ERR_INVALID_ARG, "rope_turns: rot=%d base=%g factor=%g original=%g low=%g high=%g", rot, base, factor,
                     original, low, high);
-    rope_turns(turns, rot, base, scaling, factor, original, low, high);
+    if (!rope_turns(turns, rot, base, scaling, factor, original, low, high))
+        return fail(PKV_ERR_INVALID_ARG, "rope_turns: base=%g factor=%g: an angle is not finite", base, factor);
     return PKV_OK;
 }
 
@@ -198,6 +202,9 @@ pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *tar
         return fail(PKV_ERR_INVALID_ARG, "verify_drafts: null pointer");
     if (overlap(tokens, (static_cast<size_t>(D) + B) * 4, draft_tokens, static_cast<size_t>(D) * 4))
         return fail(PKV_ERR_INVALID_ARG, "verify_drafts: tokens overlaps draft_tokens");
+    const size_t row_bytes = static_cast<size_t>(B) * 4;
+    if (context_lens != context_lens_out && overlap(context_lens, row_bytes, context_lens_out, row_bytes))
+        return fail(PKV_ERR_INVALID_ARG, "verify_drafts: context_lens_out overlaps context_lens");
     int sm_count = 0;
     unsigned *err = nullptr;
     const pkv_status s = current_device_info(&sm_count, &err);
@@ -215,8 +222,8 @@ pkv_status pkv_block_tables_fork(const int32_t *block_table, const int32_t *cont
                                  const int32_t *held, int32_t *block_table_out, int32_t *context_lens_out, int32_t *refs,
                                  int32_t *free_list, int32_t *free_count, int32_t *pairs, int32_t *pair_count, int B, int MBS,
                                  int bs, int NB, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
-    pkv_status s = check_share("block_tables_fork", B, MBS, bs, NB, block_table, context_lens, block_table_out, refs, free_list,
-                               free_count, pairs, pair_count, B > 0, workspace, workspace_bytes);
+    pkv_status s = check_share("block_tables_fork", B, MBS, bs, NB, block_table, context_lens, block_table_out, held, refs,
+                               free_list, free_count, pairs, pair_count, B > 0, workspace, workspace_bytes);
     if (s != PKV_OK) return s;
     if (B > 0 && !context_lens_out) return fail(PKV_ERR_INVALID_ARG, "block_tables_fork: null pointer");
     const size_t bytes = static_cast<size_t>(B) * MBS * sizeof(int32_t);
@@ -237,8 +244,8 @@ pkv_status pkv_block_tables_compact(const int32_t *block_table, const int32_t *c
                                     int32_t *block_table_out, int32_t *refs, int32_t *free_list, int32_t *free_count,
                                     int32_t *pairs, int32_t *pair_count, int B, int MBS, int bs, int NB, void *workspace,
                                     size_t workspace_bytes, pkv_stream_t stream) {
-    pkv_status s = check_share("block_tables_compact", B, MBS, bs, NB, block_table, context_lens, block_table_out, refs, free_list,
-                               free_count, pairs, pair_count, NB > 1, workspace, workspace_bytes);
+    pkv_status s = check_share("block_tables_compact", B, MBS, bs, NB, block_table, context_lens, block_table_out, held, refs,
+                               free_list, free_count, pairs, pair_count, NB > 1, workspace, workspace_bytes);
     if (s != PKV_OK) return s;
     const size_t bytes = static_cast<size_t>(B) * MBS * sizeof(int32_t);
     if (block_table != block_table_out && overlap(block_table, bytes, block_table_out, bytes))

@@ -279,7 +279,7 @@ struct RopeArgs {
 
 cudaError_t launch_rope(const RopeArgs &a, pkv_dtype dt, pkv_dtype q_out_dt, bool interleaved, int sm_count,
                         cudaStream_t stream);
-void rope_turns(uint64_t *turns, int rot, double base, int scaling, double factor, double original, double low, double high);
+bool rope_turns(uint64_t *turns, int rot, double base, int scaling, double factor, double original, double low, double high);
 
 // ------------------------------------------------------------------- drafted tokens
 

@@ -217,8 +217,9 @@ cudaError_t launch_rope(const RopeArgs &a, pkv_dtype dt, pkv_dtype q_out_dt, boo
                           : launch_types<float>(a, q_out_dt, interleaved, sm_count, stream);
 }
 
-// The angles per position of every pair, as fractions of a turn in 2^-64 units (host arithmetic in fp64).
-void rope_turns(uint64_t *turns, int rot, double base, int scaling, double factor, double original, double low, double high) {
+// The angles per position of every pair, as fractions of a turn in 2^-64 units (host arithmetic in fp64).  False: one is
+// not finite.
+bool rope_turns(uint64_t *turns, int rot, double base, int scaling, double factor, double original, double low, double high) {
     constexpr double kTurn = 6.283185307179586476925286766559;
     if (scaling == PKV_ROPE_BASE) base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
     for (int j = 0; j < rot / 2; ++j) {
@@ -228,9 +229,11 @@ void rope_turns(uint64_t *turns, int rot, double base, int scaling, double facto
             const double r = std::min(1.0, std::max(0.0, (original * f - low) / (high - low)));
             f *= r + (1.0 - r) / factor;
         }
+        if (!std::isfinite(f)) return false;
         f -= std::floor(f);
         turns[j] = static_cast<uint64_t>(std::ldexp(f, 63)) << 1;   // f < 1; 63 bits hold fp64's 53
     }
+    return true;
 }
 
 }  // namespace pkv

@@ -67,14 +67,16 @@ struct Parts {
     }
 };
 
-// u in [0, 1) in units of 2^-64 (rounded down).
-__device__ __forceinline__ u64 share_of_turn(float u) {
+// u * total rounded down, from the exact product (24 bits times 64): what a sum of whole numbers has to exceed.  u of 1
+// and more counts as just below it, and one below 0 or NaN as 0.
+__device__ __forceinline__ u64 border_of(float u, u64 total) {
     if (!(u > 0.f)) return 0;
-    if (u >= 1.f) return ~0ull;
-    const unsigned b = __float_as_uint(u);
-    const int s = static_cast<int>(b >> 23) - 86;
-    const u64 m = (b & 0x7fffffu) | 0x800000u;
-    return s >= 0 ? m << s : (s > -24 ? m >> -s : 0ull);
+    if (u >= 1.f) return total - 1;
+    const unsigned b = __float_as_uint(u), e = b >> 23;   // u = m 2^-n
+    const u64 m = (b & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
+    const int n = 150 - static_cast<int>(max(e, 1u));     // 24 .. 149
+    const u64 hi = __umul64hi(m, total), lo = m * total;
+    return n < 64 ? lo >> n | hi << (64 - n) : n < 128 ? hi >> (n - 64) : 0;
 }
 
 template <typename T>
@@ -193,7 +195,7 @@ __device__ __forceinline__ bool accepts(const VerifyArgs &a, long long target_ro
     if (x < 0 || x >= a.V) return false;
     const float p = as_float(static_cast<const T *>(a.target)[target_row * a.target_stride + x]);
     const float q = a.draft != nullptr ? as_float(static_cast<const T *>(a.draft)[draft_row * a.draft_stride + x]) : 1.f;
-    return static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p);
+    return isfinite(p) && isfinite(q) && static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p);
 }
 
 template <typename T, int N>
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     const int run = ((a.V + runs - 1) / runs + 32 * N - 1) / (32 * N) * (32 * N);
     const long long at = static_cast<long long>(rank * kWarps + warp) * run;
     const int lo = static_cast<int>(min(at, static_cast<long long>(a.V))), hi = static_cast<int>(min(at + run, static_cast<long long>(a.V)));
-    const u64 u = share_of_turn(a.uniforms[row0 + k]);
+    const float u = a.uniforms[row0 + k];
     int token = -1;
     bool mine = false;   // this warp holds the border
     for (int pass = 0;; ++pass) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
         }
         cluster.barrier_arrive();   // every block has read the sums once all have arrived
         if (total > 0) {
-            const u64 border = __umul64hi(u, total);   // the sum has to exceed it; below the total
+            const u64 border = border_of(u, total);   // the sum has to exceed it; below the total
             if (before <= border && capped(before, sum) > border) {
                 mine = true;
                 token = has_q ? find<true, T>(r, lo, hi, border - before, lane) : find<false, T>(r, lo, hi, border - before, lane);

@@ -101,6 +101,33 @@ def test_borders_ties_and_extreme_numbers():
     assert pkv.get_device_error() == 0
 
 
+def test_small_numbers_are_multiplied_exactly():
+    # u with bits far below 2^-64, at borders between tokens of a few units of 2^-46: u * total is just above a whole
+    # number, at it, and just below
+    t = torch.full((1, 64), 3 * 2.0 ** -46, device="cuda")
+    t[0, 63] = 1 - 63 * 3 * 2.0 ** -46
+    t = t.double().float()
+    total = sum(serve.units(t[0].cpu()))
+    for border in (3, 6, 9, 30, 60, 186):
+        at = np.float32(border / total)
+        for u in (np.nextafter(at, np.float32(0)), at, np.nextafter(at, np.float32(1))):
+            assert run(t, None, [], [0, 0], [float(u)])[:2] == serve.verify_drafts(t, None, [], [0, 0], [float(u)]), (border, u)
+    g = np.random.default_rng(4)
+    for u in np.ldexp(g.random(200), -g.integers(30, 150, 200)).astype(np.float32):
+        assert run(t, None, [], [0, 0], [float(u)])[:2] == serve.verify_drafts(t, None, [], [0, 0], [float(u)]), u
+
+
+def test_infinite_probabilities_reject_a_draft():
+    inf = float("inf")
+    for p, q in ((inf, 0.5), (0.5, inf), (inf, inf), (0.5, -inf), (-inf, 0.5), (float("nan"), 0.5), (0.5, float("nan"))):
+        t = torch.tensor([[p, 0.25, 0.25], [0.0, 0.0, 1.0]], device="cuda")
+        d = torch.tensor([[q, 0.25, 0.25]], device="cuda")
+        for drafted in (d, None):
+            want = serve.verify_drafts(t, drafted, [0], [0, 1], [0.25, 0.5])
+            assert run(t, drafted, [0], [0, 1], [0.25, 0.5])[:2] == want and (want[0] == [0]) == (drafted is not None or p != 0.5), (p, q)
+    pkv.get_device_error()
+
+
 def test_nothing_left_and_no_mass():
     flags = pkv.DEVERR["probs"]
     t = torch.tensor([[0.25, 0.0, 0.0], [1.0, 0.0, 0.0]], device="cuda")

@@ -74,6 +74,14 @@ def test_rope_turns_refuses(L):
         pkv.rope_turns(8, scaling="other", device="cpu")
 
 
+def test_rope_turns_that_are_not_finite(L):
+    buf = (ctypes.c_uint64 * 128)()
+    for base, kind, factor in ((1e-320, 0, 1.0), (1e4, 1, 1e-320), (1e4, 2, 1e-320), (1e4, 3, 1e-320)):
+        assert L.pkv_rope_turns(buf, 256, base, kind, factor, 1.0, 1e9, 2e9) == INVALID, (base, kind, factor)
+        assert b"finite" in L.pkv_last_error()
+    assert L.pkv_rope_turns(buf, 256, 1e-300, 0, 1.0, 1.0, 1.0, 2.0) == 0
+
+
 P = ctypes.c_void_p
 NZ = P(1 << 20)   # never dereferenced: the call is refused first
 
@@ -192,6 +200,12 @@ def test_verify_drafts_refuses(L):
     assert call(toks=P((1 << 20) + 8)) == INVALID and b"overlaps" in L.pkv_last_error()
 
 
+def test_verify_drafts_refuses_lengths_that_overlap(L):
+    call = lambda lens, out: L.pkv_verify_drafts(NZ, NZ, NZ, NZ, 0, 100, 100, P(1 << 22), NZ, NZ, P(lens), P(out), 4, 3, 100, None)
+    assert call(1 << 23, (1 << 23) + 4) == INVALID and b"overlaps" in L.pkv_last_error()
+    assert call((1 << 23) + 12, 1 << 23) == INVALID
+
+
 # --------------------------------------------------------- tables that share blocks
 
 def host_and_fork(seed, bs=4, nb=64):
@@ -267,6 +281,23 @@ def test_share_calls_refuse(L):
     assert copy(dt=9) == UNSUPPORTED and copy(n=0) == 0
     for kw in (dict(n=-1), dict(pairs=None), dict(count=None), dict(NB=0)):
         assert copy(**kw) == INVALID, kw
+
+
+def test_share_calls_refuse_held_that_they_write(L):
+    ws, n = P(1 << 21), 1 << 20
+    refs, free = 1 << 23, 1 << 24
+    for held in (refs, refs + 4, refs - 124, free, free + 64):
+        assert L.pkv_block_tables_fork(NZ, NZ, None, P(held), NZ, NZ, P(refs), P(free), NZ, NZ, NZ, 4, 8, 16, 32, ws, n, None) == INVALID
+        assert b"held" in L.pkv_last_error()
+        assert L.pkv_block_tables_compact(NZ, NZ, P(held), NZ, P(refs), P(free), NZ, NZ, NZ, 4, 8, 16, 32, ws, n, None) == INVALID
+
+
+def test_release_outside_window_refuses_negative_sinks():
+    m = BlockManager(8, 4)
+    m.add_sequence(0, 20)
+    with pytest.raises(ValueError, match="sinks"):
+        m.release_outside_window(0, 4, sinks=-4)
+    assert -1 not in m.tables[0]
 
 
 def test_python_calls_refuse_host_tensors(L):
