@@ -339,14 +339,9 @@ static size_t attention_workspace(int B, int Tq, int max_q, int Hq, int Hkv, int
     if (device_state(&st) != PKV_OK) return 0;
     const bool one_per_seq = Tq == B && max_q <= 1;
     const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
-    if (sinks > 0) {   // whatever the caches' type and alignment, and (one row a sequence) with cu_q or without
-        size_t simt = plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, window, num_splits, st->sm_count, false,
-                                          false).workspace_bytes;
-        if (one_per_seq)
-            simt = std::max(simt, plan_decode(B, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, false,
-                                              false).workspace_bytes);
-        return std::max(simt, plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, num_splits, st->sm_count, true).workspace_bytes);
-    }
+    if (sinks > 0)   // whatever the caches' type and alignment
+        return std::max(plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, true).workspace_bytes,
+                        plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, num_splits, st->sm_count, true).workspace_bytes);
     if (one_per_seq) return decode_workspace_upper_bound(B, Hq, Hkv, d, bs, vis, num_splits, st->sm_count);
     // query rows: cover the tcgen05 and the CUDA-core plans
     return std::max(plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, window, num_splits,
@@ -385,13 +380,11 @@ static pkv_status attention(const char *what, float *out, float *lse, const floa
     if (sinks > 0)
         with_sinks = plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, dt, num_splits, st->sm_count, caches_aligned);
     DecodePlan plan{};
-    if (!with_sinks.mma) {
-        const pkv_dtype plan_dt = sinks > 0 ? PKV_F32 : dt;   // sinks: the CUDA-core kernel
-        plan = one_per_seq ? plan_decode(B, Hq, Hkv, d, bs, vis, NB, plan_dt, num_splits, st->sm_count, caches_aligned, aligned16(q))
-                           : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, plan_dt, window, num_splits, st->sm_count,
+    if (sinks == 0)
+        plan = one_per_seq ? plan_decode(B, Hq, Hkv, d, bs, vis, NB, dt, num_splits, st->sm_count, caches_aligned, aligned16(q))
+                           : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, vis, NB, dt, window, num_splits, st->sm_count,
                                                  caches_aligned, aligned16(q));
-    }
-    const size_t need = with_sinks.mma ? with_sinks.workspace_bytes : plan.workspace_bytes;
+    const size_t need = sinks > 0 ? with_sinks.workspace_bytes : plan.workspace_bytes;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
         return fail(PKV_ERR_WORKSPACE,
                     "%s: needs %zu bytes of 16-byte aligned workspace, got %zu",
@@ -403,7 +396,7 @@ static pkv_status attention(const char *what, float *out, float *lse, const floa
     a.cu_q = one_per_seq ? nullptr : cu_q;
     a.rows = one_per_seq ? B : Tq;
     a.max_q = max_q;
-    const cudaError_t e = with_sinks.mma ? launch_decode_sinks(a, with_sinks, stream) : launch_decode(a, plan, dt, stream);
+    const cudaError_t e = sinks > 0 ? launch_decode_sinks(a, with_sinks, dt, stream) : launch_decode(a, plan, dt, stream);
     if (e == cudaSuccess) return PKV_OK;
     return fail(PKV_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
@@ -433,19 +426,11 @@ static void bounded_window(int bs, int MBS, int *window, int *sinks) {
     *sinks = *window == 0 ? 0 : static_cast<int>(std::min<long long>(*sinks, tokens));
 }
 
-// Whether the two cover whatever a table can hold, so that the tensor-core kernels without a window do as well.  (The
-// CUDA-core kernel would not leave a padded batch's rows alone, nor a call that takes Tq = B for a row each.)
-static bool covers_tables(int bs, int MBS, int window, int sinks) {
-    return sinks > 0 && static_cast<long long>(window) + sinks >= static_cast<long long>(MBS) * bs;
-}
-
 size_t pkv_paged_attention_sinks_workspace_bytes(int B, int Tq, int max_q, int Hq, int Hkv, int d, int bs, int MBS,
                                                  int window, int sinks, int num_splits) {
     if (window < 0 || sinks < 0 || bs < 1 || MBS < 1 || static_cast<long long>(MBS) * bs > kSinksTokens) return 0;
     bounded_window(bs, MBS, &window, &sinks);
-    const size_t n = attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits);
-    if (!covers_tables(bs, MBS, window, sinks)) return n;
-    return std::max(n, attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, 0, 0, num_splits));
+    return attention_workspace(B, Tq, max_q, Hq, Hkv, d, bs, MBS, window, sinks, num_splits);
 }
 
 pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, const void *k_cache, const void *v_cache,
@@ -459,16 +444,6 @@ pkv_status pkv_paged_attention_sinks(float *out, float *lse, const float *q, con
         if (static_cast<long long>(MBS) * bs > kSinksTokens)
             return fail(PKV_ERR_INVALID_ARG, "paged_attention_sinks: MBS=%d bs=%d (need MBS * bs < 2^31 - 4096)", MBS, bs);
         bounded_window(bs, MBS, &window, &sinks);
-        // sizes that the call below refuses are not planned for
-        if (covers_tables(bs, MBS, window, sinks) && !(Tq == B && max_q == 1 && cu_q != nullptr) && dt == PKV_BF16 && check_decode_sizes(B, Hq, Hkv, d, bs, MBS) == PKV_OK && NB >= 1 &&
-            num_splits >= 0 && Tq >= 0 && max_q >= 0) {
-            const bool aligned = aligned16(k_cache) && aligned16(v_cache);
-            const DecodePlan plan =
-                Tq == B && max_q == 1
-                    ? plan_decode(B, Hq, Hkv, d, bs, MBS, NB, dt, num_splits, 1, aligned, aligned16(q))
-                    : plan_attention_rows(B, Tq, max_q, Hq, Hkv, d, bs, MBS, NB, dt, 0, num_splits, 1, aligned, aligned16(q));
-            if (plan.tensor_core) window = sinks = 0;
-        }
     }
     return attention("paged_attention_sinks", out, lse, q, k_cache, v_cache, dt, block_table, context_lens, cu_q, B, Tq, max_q,
                      Hq, Hkv, d, bs, MBS, NB, scale, window, sinks, num_splits, workspace, workspace_bytes, stream);

@@ -576,7 +576,7 @@ __device__ __forceinline__ float load_f32<uint8_t>(const uint8_t *p) {
 
 // One warp per (query row, query head, chunk); lanes own head-dim elements lane + 32*j.
 // A row is a sequence (decode) or one of the query rows of a sequence (cu_q).
-template <typename T, int J, bool SINKS>
+template <typename T, int J>
 __global__ void __launch_bounds__(32)
     decode_simt_kernel(const T *__restrict__ kc, const T *__restrict__ vc, const DecodeKParams p,
                        int d, int bs) {
@@ -584,11 +584,7 @@ __global__ void __launch_bounds__(32)
     const int lane = threadIdx.x;
     const int row = blockIdx.x, i = blockIdx.y, split = blockIdx.z;
     const int kvh = i / p.m;
-    if (SINKS && p.cu_q != nullptr) {   // rows behind the last sequence's (a padded batch) are left as they are
-        const int end = __ldg(p.cu_q + p.B);
-        if (row >= end && end >= max(0, __ldg(p.cu_q + p.B - 1))) return;
-    }
-    const SeqSpan sp = row_span<SINKS>(p, row, bs, lane == 0 && split == 0 && i == 0);
+    const SeqSpan sp = row_span(p, row, bs, lane == 0 && split == 0 && i == 0);
     const int b = sp.b;
     const int len = sp.len;
     const int nc = (sp.cnpages + p.chunk_pages - 1) / p.chunk_pages;   // the sequence's chunks
@@ -618,16 +614,11 @@ __global__ void __launch_bounds__(32)
     }
     float m_run = -INFINITY, l_run = 0.f;
     for (int pg = pg0; pg < pg1; ++pg) {
-        const int phys = __ldg(p.block_table + static_cast<size_t>(b) * p.MBS + (SINKS ? page_entry(sp, pg) : pg));
+        const int phys = __ldg(p.block_table + static_cast<size_t>(b) * p.MBS + pg);
         const bool bad = phys < 0 || phys >= p.NB;
         if (bad && lane == 0) raise_error(p.err, PKV_DEVERR_BLOCK);
         const int valid = min(bs, len - pg * bs);
-        const int lo = sp.lo - pg * bs, held = SINKS ? p.sinks - pg * bs : 0;   // seen: off >= lo, and off < held
-        for (int off = SINKS && held > 0 ? 0 : max(0, lo); off < valid; ++off) {
-            if (SINKS && off >= held && off < lo) {
-                off = lo - 1;
-                continue;
-            }
+        for (int off = max(0, sp.lo - pg * bs); off < valid; ++off) {
             const size_t srow = bad ? 0 : (static_cast<size_t>(phys) * p.Hkv + kvh) * bs + off;
             const size_t base = srow * d;
             float dot = 0.f;
@@ -658,12 +649,10 @@ __global__ void __launch_bounds__(32)
     for (int j = 0; j < J; ++j) {
         const int e = lane + 32 * j;
         if (e >= d) continue;
-        // with sinks a chunk may hold keys of the sequence's other rows alone: an empty partial
-        const float o = SINKS && l_run == 0.f ? 0.f : acc[j] / l_run;
         if (nc == 1)
-            p.out[bi * d + e] = o;
+            p.out[bi * d + e] = acc[j] / l_run;
         else
-            p.ws_o[(bi * p.splits + split) * d + e] = o;
+            p.ws_o[(bi * p.splits + split) * d + e] = acc[j] / l_run;
     }
     if (lane == 0) {
         if (nc == 1) {
@@ -853,7 +842,7 @@ cudaError_t launch_group(const DecodeKParams &kp, const CUtensorMap &tk, const C
     return cudaGetLastError();
 }
 
-template <typename T, bool SINKS = false>
+template <typename T>
 cudaError_t launch_simt(const DecodeArgs &a, const DecodeKParams &kp, dim3 grid,
                         cudaStream_t stream) {
     const T *kc = static_cast<const T *>(a.k_cache);
@@ -862,7 +851,7 @@ cudaError_t launch_simt(const DecodeArgs &a, const DecodeKParams &kp, dim3 grid,
     switch (J) {
 #define PKV_SIMT_CASE(n)                                                                  \
     case n:                                                                               \
-        decode_simt_kernel<T, n, SINKS><<<grid, 32, 0, stream>>>(kc, vc, kp, a.d, a.bs);   \
+        decode_simt_kernel<T, n><<<grid, 32, 0, stream>>>(kc, vc, kp, a.d, a.bs);          \
         break;
         PKV_SIMT_CASE(1)
         PKV_SIMT_CASE(2)
@@ -1056,7 +1045,6 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
     kp.splits = plan.splits;
     kp.scale_log2 = a.scale * kLog2e;
     kp.window = a.window;
-    kp.sinks = a.sinks;
     kp.cu_q = a.cu_q;
     kp.rows = rows;
     kp.max_q = a.max_q;
@@ -1156,12 +1144,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype
         if (e != cudaSuccess || plan.splits == 1 || plan.fused_merge) return e;
     } else {
         const dim3 grid(rows, a.Hq, plan.splits);
-        if (kp.sinks > 0)
-            e = dt == PKV_F32    ? launch_simt<float, true>(a, kp, grid, stream)
-                : dt == PKV_BF16 ? launch_simt<__nv_bfloat16, true>(a, kp, grid, stream)
-                                 : cudaErrorInvalidValue;
-        else
-            e = dt == PKV_F32    ? launch_simt<float>(a, kp, grid, stream)
+        e = dt == PKV_F32    ? launch_simt<float>(a, kp, grid, stream)
             : dt == PKV_BF16 ? launch_simt<__nv_bfloat16>(a, kp, grid, stream)
                              : launch_simt<uint8_t>(a, kp, grid, stream);
         if (e != cudaSuccess || plan.splits == 1) return e;

@@ -1,5 +1,5 @@
 // decode_sinks.cu -- paged attention with a sliding window whose first tokens stay visible (sinks), for bf16
-// caches of d in {64, 128, 256} and bs in {16, 32}; other caches take the CUDA-core kernel of decode.cu.
+// caches of d in {64, 128, 256} and bs in {16, 32}; other caches: decode_sinks_simt.cu.
 //
 // The query row at position p of a sequence sees the keys t <= p with t < S or t > p - W: two runs of tokens.
 // The pages between them are left out of the count (sinks_span in decode_kparams.cuh), so that a chunk of
@@ -422,9 +422,20 @@ cudaError_t launch_tiles(const DecodeKParams &kp, const CUtensorMap &tk, const C
 SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs, int pages, int NB, pkv_dtype dt, int num_splits,
                      int sm_count, bool aligned) {
     SinksPlan plan{};
+    auto finish = [&] {
+        plan.workspace_bytes = plan.splits > 1 ? PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(rows) * Hq * plan.splits *
+                                                                                (static_cast<size_t>(d) + 1) * sizeof(float)
+                                               : 0;
+        return plan;
+    };
+    auto simt = [&] {
+        plan = SinksPlan{};
+        plan_sinks_simt(plan, rows, Hq, Hkv, d, bs, pages, num_splits, sm_count);
+        return finish();
+    };
     if (dt != PKV_BF16 || (d != 64 && d != 128 && d != 256) || (bs != 16 && bs != 32) || !aligned ||
         static_cast<long long>(NB + 1) * Hkv * bs >= (1ll << 31))
-        return plan;
+        return simt();
     const long long pairs = static_cast<long long>(max_q) * (Hq / Hkv), tiles = (pairs + 7) / 8;
     plan.umma = pairs > kSinksMmaPairs && d <= 128;
     // more than eight pairs on tcgen05 (16 heads a KV head 22.7 us against 24.8 on warp MMAs, 1 to 4 rows of 8 104
@@ -432,7 +443,7 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
     plan.tiles = plan.umma ? kSinksUmmaPairs / 8 : tiles == 1 ? 1 : 2;
     const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
     const long long units = static_cast<long long>(B) * Hkv * groups;
-    if (units < 1) return plan;
+    if (units < 1) return simt();
     const long long slots = 2ll * std::max(sm_count, 1);   // blocks at a time
     // Chunks of a sequence by a model of the time in tokens: a block costs its tokens and 512 more, a wave of blocks
     // as much as a block, a second wave at least half of one; more chunks than one cost a quarter of a wave where
@@ -463,20 +474,17 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
     if (plan.umma) chunk = (chunk + kSinksUmmaKeys / bs - 1) / (kSinksUmmaKeys / bs) * (kSinksUmmaKeys / bs);   // whole key tiles
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
     splits = (pages + chunk - 1) / chunk;
-    if (groups * splits > 0x7fffffffll) return plan;
+    if (groups * splits > 0x7fffffffll) return simt();
     plan.mma = true;
     plan.groups = static_cast<int>(groups);
     plan.chunk_pages = chunk;
     plan.splits = splits;
     plan.fused_merge = splits > 1 && splits <= kSinksFusedChunks &&
                        units <= static_cast<long long>(PKV_DECODE_COUNTER_BYTES / sizeof(unsigned));
-    plan.workspace_bytes =
-        splits > 1 ? PKV_DECODE_COUNTER_BYTES + static_cast<size_t>(rows) * Hq * splits * (static_cast<size_t>(d) + 1) * sizeof(float)
-                   : 0;
-    return plan;
+    return finish();
 }
 
-cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cudaStream_t stream) {
+cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, pkv_dtype dt, cudaStream_t stream) {
     DecodeKParams kp{};
     kp.out = a.out;
     kp.lse = a.lse;
@@ -504,13 +512,18 @@ cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cuda
         kp.ws_o = reinterpret_cast<float *>(ws + PKV_DECODE_COUNTER_BYTES);
         kp.ws_lse = kp.ws_o + static_cast<size_t>(a.rows) * a.Hq * plan.splits * a.d;
     }
+    cudaError_t e;
+    if (!plan.mma) {
+        e = launch_decode_sinks_simt(kp, a.k_cache, a.v_cache, dt, a.d, a.bs, plan.block_heads, stream);
+        if (e != cudaSuccess || plan.splits == 1 || plan.fused_merge) return e;
+        return launch_decode_merge(kp, a.d, a.bs, static_cast<unsigned>(a.rows * a.Hq), stream);
+    }
     CUtensorMap tk, tv;
     const uint64_t dims[2] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.NB) * a.Hkv * a.bs};
     const uint64_t strides[1] = {static_cast<uint64_t>(a.d) * 2};
     const uint32_t box[2] = {64, static_cast<uint32_t>(a.bs)};
     if (!encode_map_bf16(&tk, a.k_cache, 2, dims, strides, box) || !encode_map_bf16(&tv, a.v_cache, 2, dims, strides, box))
         return cudaErrorInvalidValue;
-    cudaError_t e;
     if (plan.umma)
         e = launch_decode_sinks_umma(kp, tk, tv, a.d, a.bs, plan.groups, stream);
     else if (a.bs == 16)

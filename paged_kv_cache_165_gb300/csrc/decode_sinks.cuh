@@ -189,4 +189,9 @@ constexpr int kSinksMmaPairs = 8;   // up to here the warp-MMA kernel
 cudaError_t launch_decode_sinks_umma(const DecodeKParams &kp, const CUtensorMap &tk, const CUtensorMap &tv, int d, int bs, int groups,
                                      cudaStream_t stream);
 
+// The kernel on CUDA cores (decode_sinks_simt.cu): every type, size and alignment.
+void plan_sinks_simt(SinksPlan &plan, int rows, int Hq, int Hkv, int d, int bs, int pages, int num_splits, int sm_count);
+cudaError_t launch_decode_sinks_simt(const DecodeKParams &kp, const void *k_cache, const void *v_cache, pkv_dtype dt, int d, int bs,
+                                     int block_heads, cudaStream_t stream);
+
 }  // namespace pkv

@@ -145,11 +145,12 @@ inline int visible_blocks_with_sinks(int MBS, int bs, int window, int sinks, int
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, pkv_dtype dt,
                           cudaStream_t stream);
 
-// Windows with first tokens that stay visible (decode_sinks.cu); mma false: the CUDA-core kernel.
+// Windows with first tokens that stay visible (decode_sinks.cu).
 struct SinksPlan {
-    bool mma;            // on tensor cores: warp MMAs, or
+    bool mma;            // on tensor cores (else CUDA cores): warp MMAs, or
     bool umma;           // tcgen05
     int tiles, groups;   // tiles of 8 (query row, head) pairs of a block, blocks for the pairs of a KV head
+    int block_heads;     // on CUDA cores: heads of a block
     int splits, chunk_pages;
     bool fused_merge;
     size_t workspace_bytes;
@@ -158,7 +159,7 @@ struct SinksPlan {
 // pages: the blocks any row can see; aligned: caches on 16-byte boundaries (q on 8).
 SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs, int pages, int NB, pkv_dtype dt, int num_splits,
                      int sm_count, bool aligned);
-cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, cudaStream_t stream);
+cudaError_t launch_decode_sinks(const DecodeArgs &a, const SinksPlan &plan, pkv_dtype dt, cudaStream_t stream);
 
 // ------------------------------------------------- attention over a 4-bit cache
 
