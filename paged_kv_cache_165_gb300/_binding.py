@@ -121,24 +121,27 @@ def lib() -> ctypes.CDLL:
     L.pkv_block_tables_release.restype = I
     L.pkv_block_tables_share_workspace_bytes.argtypes = [I, I, I]
     L.pkv_block_tables_share_workspace_bytes.restype = Z
-    L.pkv_block_tables_fork.argtypes = [P] * 11 + [I] * 4 + [P, Z, P]
+    # The whole numbers of the calls of a decode step are declared as pointers, whose conversion takes half as long: an
+    # argument of 32 bits is the lower half of a 64-bit register or stack slot on both of x86-64 and aarch64.
+    N = P
+    L.pkv_block_tables_fork.argtypes = [P] * 11 + [N] * 4 + [P, N, P]
     L.pkv_block_tables_fork.restype = I
-    L.pkv_block_tables_compact.argtypes = [P] * 9 + [I] * 4 + [P, Z, P]
+    L.pkv_block_tables_compact.argtypes = [P] * 9 + [N] * 4 + [P, N, P]
     L.pkv_block_tables_compact.restype = I
-    L.pkv_kv_block_copy_counted.argtypes = [P, P, I, P, I, P, I, I, I, I, P]
+    L.pkv_kv_block_copy_counted.argtypes = [P, P, N, P, N, P, N, N, N, N, P]
     L.pkv_kv_block_copy_counted.restype = I
-    LL, D = ctypes.c_longlong, ctypes.c_double
+    D = ctypes.c_double
     L.pkv_rope_turns.argtypes = [P, I, D, I, D, D, D, D]
     L.pkv_rope_turns.restype = I
-    L.pkv_rope_append.argtypes = [P, I, P, P, P, I, LL, LL, LL, P, P, I, I, F, P, P, P] + [I] * 6 + [P]
+    L.pkv_rope_append.argtypes = [P, N, P, P, P, N, N, N, N, P, P, N, N, F, P, P, P] + [N] * 6 + [P]
     L.pkv_rope_append.restype = I
-    L.pkv_rope.argtypes = [P, I, P, P, P, I, LL, LL, P, P, I, I, F, I, I, I, I, I, P]
+    L.pkv_rope.argtypes = [P, N, P, P, P, N, N, N, P, P, N, N, F, N, N, N, N, N, P]
     L.pkv_rope.restype = I
-    L.pkv_verify_drafts.argtypes = [P, P, P, P, I, LL, LL, P, P, P, P, P, I, I, I, P]
+    L.pkv_verify_drafts.argtypes = [P, P, P, P, N, N, N, P, P, P, P, P, N, N, N, P]
     L.pkv_verify_drafts.restype = I
     L.pkv_paged_attention_sinks_workspace_bytes.argtypes = [I] * 11
     L.pkv_paged_attention_sinks_workspace_bytes.restype = Z
-    L.pkv_paged_attention_sinks.argtypes = [P, P, P, P, P, I, P, P, P] + [I] * 9 + [F, I, I, I, P, Z, P]
+    L.pkv_paged_attention_sinks.argtypes = [P, P, P, P, P, N, P, P, P] + [N] * 9 + [F, N, N, N, P, N, P]
     L.pkv_paged_attention_sinks.restype = I
     L.pkv_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, I, I, P, P]
     L.pkv_selftest_bounded_wait.restype = I
@@ -922,12 +925,12 @@ def rope_turns(rot, base=10000.0, scaling="none", factor=1.0, original=1, low=1.
     return turns.to(device)
 
 
-def _heads(what, name, t, H, d) -> int:
+def _heads(what, name, t, T, H, d) -> int:
     """Elements between the tokens of t [T][H][d], whose rows [H][d] are contiguous."""
     token, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and H > 1):
         raise ValueError(f"{what}: the heads of a token of {name} must be contiguous")
-    return token if t.shape[0] > 1 else H * d
+    return token if T > 1 else H * d
 
 
 def _rope_check(what, q_out, q, positions, turns, here, **more):
@@ -974,8 +977,8 @@ def rope_append(q_out, q, k_new, v_new, k_cache, v_cache, positions, slot_mappin
         raise ValueError("rope_append: shapes do not match (k_new, v_new [T][Hkv][d], caches [NB][Hkv][bs][d], slot_mapping [T])")
     NB, Hkv, bs, _ = cache
     status = lib().pkv_rope_append(
-        q_out.data_ptr(), _dtype(q_out), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype(q), _heads(what, "q", q, Hq, d),
-        _heads(what, "k_new", k_new, Hkv, d), _heads(what, "v_new", v_new, Hkv, d), positions.data_ptr(), turns.data_ptr(),
+        q_out.data_ptr(), _dtype(q_out), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype(k_cache), _heads(what, "q", q, T, Hq, d),
+        _heads(what, "k_new", k_new, T, Hkv, d), _heads(what, "v_new", v_new, T, Hkv, d), positions.data_ptr(), turns.data_ptr(),
         2 * turns.numel(), 1 if interleaved else 0, float(mscale), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq,
         Hkv, d, bs, NB, _stream(stream, here))
     if status:
@@ -1005,9 +1008,9 @@ def rope(q_out, q, k_out, k, positions, turns, interleaved=False, mscale=1.0, in
         if len(rows) != 3 or k_out.shape != rows or rows[0] != T or rows[2] != d:
             raise ValueError("rope: k and k_out must be [T][Hkv][d]")
         Hkv = rows[1]
-        k_stride = _heads(what, "k", k, Hkv, d)
+        k_stride = _heads(what, "k", k, T, Hkv, d)
     status = lib().pkv_rope(
-        q_out.data_ptr(), _dtype(q_out), _ptr(k_out), q.data_ptr(), _ptr(k), _dtype(q), _heads(what, "q", q, Hq, d), k_stride,
+        q_out.data_ptr(), _dtype(q_out), _ptr(k_out), q.data_ptr(), _ptr(k), _dtype(q), _heads(what, "q", q, T, Hq, d), k_stride,
         positions.data_ptr(), turns.data_ptr(), 2 * turns.numel(), 1 if interleaved else 0, float(mscale), 1 if inverse else 0, T, Hq, Hkv,
         d, _stream(stream, here))
     if status:
@@ -1096,14 +1099,12 @@ def paged_attention_sinks(out, q, k_cache, v_cache, block_table, context_lens, s
         _refuse(what, here, q=(q, _F32), out=(out, _F32), k_cache=(k_cache, None),
                 v_cache=(v_cache, getattr(k_cache, "dtype", None)), block_table=(block_table, _I32),
                 context_lens=(context_lens, _I32), lse=(lse, _F32), cu_q=(cu_q, _I32), workspace=(workspace, None))
-    dt = _dtype(k_cache)
-    if q.dim() != 3 or k_cache.dim() != 4:
+    dt, rows, cache, table, B = _dtype(k_cache), q.shape, k_cache.shape, block_table.shape, context_lens.numel()
+    if len(rows) != 3 or len(cache) != 4:
         raise ValueError(f"{what}: q must be [rows][Hq][d] and the caches [NB][Hkv][bs][d]")
-    NB, Hkv, bs, d = k_cache.shape
-    Tq, Hq, dq = q.shape
-    B = context_lens.numel()
-    table = block_table.shape
-    if dq != d or out.shape != q.shape or v_cache.shape != k_cache.shape or len(table) != 2 or table[0] != B or \
+    NB, Hkv, bs, d = cache
+    Tq, Hq, dq = rows
+    if dq != d or out.shape != rows or v_cache.shape != cache or len(table) != 2 or table[0] != B or \
             (cu_q.numel() != B + 1 if cu_q is not None else Tq != B) or (lse is not None and lse.numel() != Tq * Hq):
         raise ValueError(f"{what}: shapes do not match")
     status = lib().pkv_paged_attention_sinks(
