@@ -22,9 +22,11 @@
 // Every wait is bounded and shares an abort flag, as in decode_umma.cu.
 //
 // 64 sequences of 512 to 8192 tokens, 1 to 4 rows of 64 heads on 8 of 128, window 2048 + 16: 104 us, 5.3 TB/s of what the
-// rows see (the warp-MMA kernel: 155).  What bounds it: a tile's chain -- P.V, its rows out of tensor memory, the next
-// weights announced -- takes about 3500 cycles a block with two blocks an SM, where HBM would want 2800; the tensor pipe
-// is 30% busy.  Four tile slots a block instead of five: 106 us.
+// rows see (the warp-MMA kernel: 155).  What bounds it: 512 blocks on 304 places, so that the second wave is two thirds
+// full, and a block alone on its SM takes 1.4 us a tile, the latency of its rings of five 16 KB slots (four slots: 106 us;
+// more do not fit beside the queries).  The first wave runs at 6.3 TB/s.  The chain of a tile is not the bound: four more
+// warps for the outputs measured 104 us, two groups of softmax warps with tiles in turn 103 (and 16 heads a KV head 24 for
+// 23 us); the tensor pipe is 30% busy.  Two chunks a sequence: 116 us.
 #include <atomic>
 #include <math.h>
 
