@@ -22,11 +22,12 @@
 // Every wait is bounded and shares an abort flag, as in decode_umma.cu.
 //
 // 64 sequences of 512 to 8192 tokens, 1 to 4 rows of 64 heads on 8 of 128, window 2048 + 16: 104 us, 5.3 TB/s of what the
-// rows see (the warp-MMA kernel: 155).  What bounds it: 512 blocks on 304 places, so that the second wave is two thirds
-// full, and a block alone on its SM takes 1.4 us a tile, the latency of its rings of five 16 KB slots (four slots: 106 us;
-// more do not fit beside the queries).  The first wave runs at 6.3 TB/s.  The chain of a tile is not the bound: four more
-// warps for the outputs measured 104 us, two groups of softmax warps with tiles in turn 103 (and 16 heads a KV head 24 for
-// 23 us); the tensor pipe is 30% busy.  Two chunks a sequence: 116 us.
+// rows see (the warp-MMA kernel: 155).  What bounds it: one full wave of 304 long blocks runs at 6.45 TB/s, 95% of the
+// measured copy rate (198 us; 148 with the pages in L2), but 512 blocks of 33 tiles are one and two thirds, each with its
+// start and end; a block alone on its SM takes 0.9 us a tile with its pages in L2 and 1.1 from HBM.  Measured without
+// gain: four more warps for the outputs (104 us), two groups of softmax warps with tiles in turn (103; 16 heads a KV head
+// 24 for 23), queries in tensor memory, seven slots and O by 64 columns (114), two chunks a sequence (116), four slots
+// instead of five (106).
 #include <atomic>
 #include <math.h>
 
