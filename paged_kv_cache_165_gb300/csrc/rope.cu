@@ -11,9 +11,10 @@
 // sincospif.  The cosines and sines of a token are computed once, into shared memory, for all its heads.
 //
 // Every element is read and written once, in 16-byte units where pointers and strides allow: bound by HBM for
-// prompts and by launch latency for a decode step.  17153 tokens of 64 + 8 + 8 heads of 128 in bf16: 118 us, 5.96 TB/s
-// (88% of the measured copy rate), at eight blocks an SM (122 us at six; cache hints, eight tokens a block and
-// units dealt over a block's tokens by number, two at a time, measured slower: 122, 122 and 147); 64 tokens 2.9 us.
+// prompts and by launch latency for a decode step.  17153 tokens of 64 + 8 + 8 heads of 128 in bf16: 115 us, 6.09 TB/s
+// (90% of the measured copy rate), at eight blocks an SM (122 us at six, then); cache hints and units dealt over a block's
+// tokens by number, two at a time, measured slower (122 and 147 against 118), rows fetched towards L2 ahead of the angles
+// too (126 to 150); 64 tokens 2.9 us.
 #include <algorithm>
 #include <cmath>
 
@@ -178,7 +179,18 @@ cudaError_t launch(const RopeArgs &given, int sm_count, cudaStream_t stream) {
     // a token's units over several blocks while there are too few tokens to fill the GPU
     const long long want = 4ll * std::max(sm_count, 1);
     const long long split = std::max(1ll, std::min((units + kThreads - 1) / kThreads, want / std::max(1, a.T)));
-    a.block_tokens = static_cast<int>(std::max(1ll, std::min<long long>(kMaxTokens, a.T / want)));
+    // tokens of a block by a model of the time: a wave of blocks (eight an SM) takes as long as a block's tokens and 192
+    // units.  (17153 tokens of 640 units, 1 to 4 a block: 121, 120, 115 and 118 us; 4900: 39, 42, 42 and 49.)
+    const long long slots = 8ll * std::max(sm_count, 1);
+    double best = 0;
+    for (int n = 1; n <= kMaxTokens; ++n) {
+        const long long blocks = (a.T + n - 1ll) / n * split;
+        const double cost = static_cast<double>((blocks + slots - 1) / slots) * (n + 192.0 / units);
+        if (n == 1 || cost < best) {
+            best = cost;
+            a.block_tokens = n;
+        }
+    }
     const dim3 grid(static_cast<unsigned>((a.T + static_cast<long long>(a.block_tokens) - 1) / a.block_tokens),
                     static_cast<unsigned>(split));
     return launch_dependent(rope_kernel<T, Tq, INTER, N>, grid, dim3(kThreads),
