@@ -41,42 +41,62 @@ constexpr int kRowsEach = 8;                               // rows of a thread, 
 // what one block takes: two numbers an id and two a row in shared memory, four entries a thread
 constexpr int kOneIds = 24576, kOneRows = 2048, kOneEntries = 4096;
 
-// Exclusive ranks of N flags counted over a block's threads; totals[i]: the block's.  All threads call it.
+// Of N counts of a warp each: their sums over the block's earlier warps (base) and over all (total).  All threads call
+// it, once for an s_warp.
 template <int N>
-__device__ __forceinline__ void block_ranks(int (&x)[N], int (&s_warp)[N][32], int (&totals)[N]) {
+__device__ __forceinline__ void warp_bases(const int (&mine)[N], int (&s_warp)[N][32], int (&base)[N], int (&total)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int in[N];
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        in[i] = x[i];
-#pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-            const int y = __shfl_up_sync(kFull, x[i], sh);
-            if (lane >= sh) x[i] += y;
-        }
-    }
-    __syncthreads();   // the sums of an earlier call have been read
-    if (lane == 31) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s_warp[i][warp] = x[i];
-    }
-    __syncthreads();
-    if (warp < N) {
-        int w = s_warp[warp][lane];
-#pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-            const int y = __shfl_up_sync(kFull, w, sh);
-            if (lane >= sh) w += y;
-        }
-        s_warp[warp][lane] = w;
+        for (int n = 0; n < N; ++n) s_warp[n][warp] = mine[n];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (warp > 0) x[i] += s_warp[i][warp - 1];
-        x[i] -= in[i];
-        totals[i] = s_warp[i][31];
+    for (int n = 0; n < N; ++n) {
+        const int x = s_warp[n][lane];
+        base[n] = __reduce_add_sync(kFull, lane < warp ? x : 0);
+        total[n] = __reduce_add_sync(kFull, x);
     }
+}
+
+// Items [begin, end) of a block, dealt to its warps in runs of 32 * rounds: a lane has first + 32 r, r < rounds.
+struct Run {
+    unsigned first, end, rounds;
+    __device__ __forceinline__ explicit Run(uint2 part) : end(part.y), rounds((part.y - part.x + kThreads - 1) / kThreads) {
+        first = part.x + (threadIdx.x >> 5) * 32 * rounds + (threadIdx.x & 31);
+    }
+    __device__ __forceinline__ unsigned at(unsigned r) const { return first + 32 * r; }
+};
+
+// flag(i) of a lane's items, kept as bits for the first 32 of them; its warp's count.  Eight loads ahead of their use.
+struct Flags {
+    unsigned bits = 0;
+    int count = 0;
+    template <typename Flag>
+    __device__ __forceinline__ Flags(const Run &run, Flag flag) {
+        for (unsigned r0 = 0; r0 < run.rounds; r0 += 8) {
+            bool f[8];
+#pragma unroll
+            for (unsigned k = 0; k < 8; ++k) f[k] = r0 + k < run.rounds && run.at(r0 + k) < run.end && flag(run.at(r0 + k));
+#pragma unroll
+            for (unsigned k = 0; k < 8; ++k) {
+                if (r0 + k < 32) bits |= static_cast<unsigned>(f[k]) << (r0 + k);
+                count += __popc(__ballot_sync(kFull, f[k]));
+            }
+        }
+    }
+    template <typename Flag>
+    __device__ __forceinline__ bool of(const Run &run, unsigned r, Flag flag) const {
+        return r < 32 ? bits >> r & 1 : run.at(r) < run.end && flag(run.at(r));
+    }
+};
+
+// A lane's rank among its warp's flags, counted on from `base`, which moves past them.
+__device__ __forceinline__ int rank_of(bool f, int &base) {
+    const unsigned b = __ballot_sync(kFull, f);
+    const int rank = base + __popc(b & ((1u << (threadIdx.x & 31)) - 1u));
+    base += __popc(b);
+    return rank;
 }
 
 // The blocks of a launch: one, or the cluster.
@@ -96,38 +116,6 @@ struct Team {
         return make_uint2(min(n, rank * each), min(n, (rank + 1) * each));
     }
 };
-
-// Items [begin, end) in index order, four a thread: flags(i, f) says which of N kinds an item is, use(i, f, rank)
-// gets its rank among them, counted on from `rank0`.  All threads call it.
-template <int N, typename Flags, typename Use>
-__device__ __forceinline__ void rank_items(unsigned begin, unsigned end, int (&rank0)[N], int (&s_warp)[N][32], Flags flags, Use use) {
-    for (unsigned i0 = begin; i0 < end; i0 += 4 * kThreads) {
-        int f[4][N], r[N] = {}, total[N];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const unsigned i = i0 + 4 * threadIdx.x + k;
-#pragma unroll
-            for (int n = 0; n < N; ++n) f[k][n] = 0;
-            if (i < end) flags(i, f[k]);
-#pragma unroll
-            for (int n = 0; n < N; ++n) r[n] += f[k][n];
-        }
-        block_ranks<N>(r, s_warp, total);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const unsigned i = i0 + 4 * threadIdx.x + k;
-            int at[N];
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                at[n] = rank0[n] + r[n];
-                r[n] += f[k][n];
-            }
-            if (i < end) use(i, f[k], at);
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) rank0[n] += total[n];
-    }
-}
 
 // The sums of N counts over the blocks before this one (before) and over all (all), by way of s_part, which
 // is not written again.  Ends with a barrier of the team.
@@ -284,7 +272,7 @@ __device__ __forceinline__ void clear(const ShareArgs &a, const Team<ONE> &team,
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     extern __shared__ int s_ids[];
-    __shared__ int s_warp[1][32], s_part[2];
+    __shared__ int s_warp[2][32], s_part[2];
     pdl_wait();
     const Team<ONE> team;
     const unsigned tid = team.tid(), NB = a.NB, B = a.B;
@@ -311,48 +299,44 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
                 });
     team.sync();
     // rows that get a copy of their last block, and free blocks; a thread keeps its rows to the end
-    const uint2 my_rows = team.part(B), my_ids = team.part(NB);
-    int len[kRowsEach], old[kRowsEach], mine[2] = {0, 0}, before[2], all[2], total[1];
+    const Run my_rows(team.part(B)), my_ids(team.part(NB));
+    int len[kRowsEach], old[kRowsEach], mine[2] = {0, 0}, base[2], total[2], before[2], all[2];
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const unsigned b = my_rows.x + k * kThreads + threadIdx.x;
-        len[k] = b < my_rows.y ? a.place[b] : 0;
-        old[k] = b < my_rows.y ? a.last[b] : -1;      // written where the length asks for it
+        const unsigned b = my_rows.at(k);
+        const bool there = k < static_cast<int>(my_rows.rounds) && b < my_rows.end;
+        len[k] = there ? a.place[b] : 0;
+        old[k] = there ? a.last[b] : -1;      // written where the length asks for it
     }
+    auto unused = [&](unsigned i) {
+        const int inside = refs[i], ends = first[i];   // both loads at once
+        return inside == 0 && ends == kNobody;
+    };
+    const Flags spare(my_ids, unused);
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const int b = static_cast<int>(my_rows.x + k * kThreads + threadIdx.x);
+        const int b = static_cast<int>(my_rows.at(k));
         if (len[k] % a.bs == 0 || old[k] < 0 || (refs[old[k]] == 0 && first[old[k]] == b)) old[k] = -1;
-        mine[0] += old[k] >= 0;
+        mine[0] += __popc(__ballot_sync(kFull, old[k] >= 0));
     }
-    auto unused = [&](unsigned i) { return refs[i] == 0 && first[i] == kNobody; };
-#pragma unroll 4
-    for (unsigned i = my_ids.x + threadIdx.x; i < my_ids.y; i += kThreads) mine[1] += unused(i);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        int x[1] = {mine[n]};
-        block_ranks<1>(x, s_warp, total);
-        mine[n] = total[0];
-    }
-    share_counts(team, mine, s_part, before, all);
+    mine[1] = spare.count;
+    warp_bases(mine, s_warp, base, total);
+    share_counts(team, total, s_part, before, all);
     const int served = min(all[0], all[1]), left = all[1] - served;
-    int id_rank[1] = {before[1]}, nth[kRowsEach];
+    int row_base = before[0] + base[0], id_base = before[1] + base[1], nth[kRowsEach];
 #pragma unroll
-    for (int k = 0; k < kRowsEach; ++k) {
-        if (my_rows.x + k * kThreads >= my_rows.y) break;   // (the whole block)
-        int x[1] = {old[k] >= 0};
-        block_ranks<1>(x, s_warp, total);
-        nth[k] = before[0] + x[0];
-        before[0] += total[0];
+    for (int k = 0; k < kRowsEach; ++k) nth[k] = rank_of(old[k] >= 0, row_base);
+    for (unsigned r = 0; r < my_ids.rounds; ++r) {
+        const unsigned i = my_ids.at(r);
+        const bool f = spare.of(my_ids, r, unused);
+        const int at = rank_of(f, id_base);
+        if (i >= my_ids.end) continue;
+        const bool handed = f && at < served;
+        if (handed) a.fresh[at] = static_cast<int>(i);
+        else if (f) a.free_list[all[1] - 1 - at] = static_cast<int>(i);
+        const int inside = f ? 0 : refs[i];   // of the rows that end in a block one at most still names it
+        a.refs[i] = inside != 0 ? inside : handed || !f;
     }
-    rank_items<1>(my_ids.x, my_ids.y, id_rank, s_warp, [&](unsigned i, int (&f)[1]) { f[0] = unused(i); },
-                  [&](unsigned i, const int (&f)[1], const int (&at)[1]) {
-                      const bool handed = f[0] && at[0] < served;
-                      if (handed) a.fresh[at[0]] = static_cast<int>(i);
-                      else if (f[0]) a.free_list[all[1] - 1 - at[0]] = static_cast<int>(i);
-                      const int inside = refs[i];   // of the rows that end in a block one at most still names it
-                      a.refs[i] = inside != 0 ? inside : handed || !f[0];
-                  });
     for (unsigned i = left + tid; i < NB; i += team.kAll) a.free_list[i] = -1;
     for (unsigned i = served + tid; i < B; i += team.kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
@@ -363,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     team.sync();
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
-        const unsigned b = my_rows.x + k * kThreads + threadIdx.x;
-        if (b >= my_rows.y) break;
+        const unsigned b = my_rows.at(k);
+        if (k >= static_cast<int>(my_rows.rounds) || b >= my_rows.end) break;
         if (old[k] >= 0 && nth[k] < served) {
             const int to = a.fresh[nth[k]];
             reinterpret_cast<int2 *>(a.pairs)[nth[k]] = make_int2(old[k], to);
@@ -409,27 +393,46 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         if (x >= 0) atomicAdd(refs + x, 1);
     });
     team.sync();
-    const uint2 part = team.part(NB);
-    int mine[1] = {0}, before1[1], all1[1], total[1];
-#pragma unroll 4
-    for (unsigned i = part.x + threadIdx.x; i < part.y; i += kThreads) mine[0] += refs[i] != 0;
-    block_ranks<1>(mine, s_warp1, total);
-    mine[0] = total[0];
-    share_counts(team, mine, s_part1, before1, all1);
+    const Run ids(team.part(NB));
+    auto in_use = [&](unsigned i) { return refs[i] != 0; };
+    const Flags using_it(ids, in_use), holding(a.held != nullptr ? ids : Run(make_uint2(0, 0)), held);
+    int base1[1], total1[1], before1[1], all1[1];
+    {
+        const int mine[1] = {using_it.count};
+        warp_bases(mine, s_warp1, base1, total1);
+    }
+    share_counts(team, total1, s_part1, before1, all1);
     const unsigned used = all1[0];
     // blocks that move (in use, not held, from `used` on), free ids below, free or vacated ids from there on
-    auto kinds = [&](unsigned i, int (&f)[3]) {
-        const bool in_use = refs[i] != 0, high = i >= used, fixed = high && held(i);
-        f[0] = in_use && high && !fixed;
-        f[1] = !in_use && !high;
+    auto kinds = [&](unsigned r, bool (&f)[3]) {
+        const unsigned i = ids.at(r);
+        const bool there = i < ids.end, busy = using_it.of(ids, r, in_use), high = there && i >= used;
+        const bool fixed = high && a.held != nullptr && holding.of(ids, r, held);
+        f[0] = busy && high && !fixed;
+        f[1] = there && !busy && !high;
         f[2] = high && !fixed;
     };
-    int count[3] = {0, 0, 0}, before[3], all[3];
-    rank_items<3>(part.x, part.y, count, s_warp, kinds, [](unsigned, const int (&)[3], const int (&)[3]) {});
-    share_counts(team, count, s_part, before, all);
+    int count[3] = {0, 0, 0}, base[3], total[3], before[3], all[3];
+    for (unsigned r = 0; r < ids.rounds; ++r) {
+        bool f[3];
+        kinds(r, f);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) count[n] += __popc(__ballot_sync(kFull, f[n]));
+    }
+    warp_bases(count, s_warp, base, total);
+    share_counts(team, total, s_part, before, all);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) base[n] += before[n];
     // as many ids are free below `used` as are taken from there on, so every mover has a place
     const int moves = all[0], spare = all[1] - moves, free_all = spare + all[2];
-    rank_items<3>(part.x, part.y, before, s_warp, kinds, [&](unsigned i, const int (&f)[3], const int (&at)[3]) {
+    for (unsigned r = 0; r < ids.rounds; ++r) {
+        const unsigned i = ids.at(r);
+        bool f[3];
+        int at[3];
+        kinds(r, f);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) at[n] = rank_of(f[n], base[n]);
+        if (i >= ids.end) continue;
         moved[i] = f[0] ? -1 - at[0] : static_cast<int>(i);
         if (f[1]) {
             if (at[1] < moves) a.fresh[at[1]] = static_cast<int>(i);
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         if (f[2]) a.free_list[free_all - 1 - (spare + at[2])] = static_cast<int>(i);
         // what stays; blocks that move write both ends below
         if (ONE && !f[0] && !(f[1] && at[1] < moves)) a.refs[i] = refs[i];
-    });
+    }
     for (unsigned i = free_all + tid; i < NB; i += team.kAll) a.free_list[i] = -1;
     for (unsigned i = moves + tid; i < NB / 2; i += team.kAll) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
     if (tid == 0) {
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         *a.pair_count = moves;
     }
     team.sync();
+    const uint2 part = team.part(NB);
     for (unsigned i0 = max(part.x, used) + threadIdx.x; i0 < part.y; i0 += 4 * kThreads) {   // four a thread: their loads overlap
         int nth[4], n[4], to[4];
 #pragma unroll

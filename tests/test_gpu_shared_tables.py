@@ -133,6 +133,32 @@ def test_compact_matches_the_row_by_row_form(B, bs, hi, spare, in_place):
             same(dict(table=to, refs=refs, free_list=free, free_count=fc, pairs=pairs, pair_count=pc), want)
 
 
+@pytest.mark.parametrize("nb", [24576, 24577, 262144, 262145, 700001])
+def test_pools_at_the_borders_of_the_ways_to_count(nb):
+    # one block's shared memory, a lane's bits for 32 ids, and past them; blocks used at both ends of the pool
+    rng = np.random.default_rng(nb)
+    B, bs, width = 40, 8, 30
+    lens = rng.integers(0, width * bs + 1, B)
+    ids = np.concatenate([rng.permutation(600), nb - 1 - rng.permutation(600)])
+    table = ids[:B * width].reshape(B, width)
+    table[3] = table[2]
+    held = np.zeros(nb, int)
+    held[[5, 700, nb - 7, nb // 2]] = 1
+    parents = rng.integers(-1, B, B)
+    for h in (None, held):
+        want = serve.block_tables_fork(table, lens, parents, bs, nb, h)
+        same(fork(table, lens, parents, bs, nb, h), want)
+        want = serve.block_tables_compact(table, lens, bs, nb, h)
+        t, to = dev(table), torch.full((B, width), -9, dtype=torch.int32, device="cuda")
+        refs, free = (torch.full((nb,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        fc, pc = (torch.full((1,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        pairs = torch.full((nb // 2, 2), -9, dtype=torch.int32, device="cuda")
+        ws = torch.randint(-99, 99, (pkv.block_tables_share_workspace_bytes(B, width, nb) // 4,), dtype=torch.int32, device="cuda")
+        pkv.block_tables_compact(t, dev(lens), to, refs, free, fc, pairs, pc, bs, held=None if h is None else dev(h), workspace=ws)
+        same(dict(table=to, refs=refs, free_list=free, free_count=fc, pairs=pairs, pair_count=pc), want)
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("shape,dtype", [((9, 2, 16, 64), torch.bfloat16), ((9, 3, 5, 7), torch.float32), ((9, 1, 3, 5), torch.bfloat16),
                                          ((9, 8, 32, 128), torch.float32), ((9, 2, 16, 72), torch.uint8), ((9, 4, 16, 1), torch.float32)])
 def test_counted_copies(shape, dtype):
