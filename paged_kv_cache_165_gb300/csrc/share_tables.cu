@@ -16,11 +16,13 @@
 // Both are one launch and bound by the latency of their phases (clear, count, scan, write): tables of a serving
 // batch are some 10^2 to 10^5 entries.  Small ones run as one block of 1024 threads that keeps the counts in
 // shared memory, where a phase ends with __syncthreads.  Larger ones run as a cluster of eight such blocks with
-// the counts in global memory and hardware cluster barriers (about 0.9 us each); counts spread over the
-// cluster's shared memories measured no faster (a pool of 25234 ids 25.7 us, 23.4 in global memory).  Device time:
-// eight rows of 20 blocks forked 7.2 us, 256 of 129 15.4 (one block: 31.5); six rows of 55 compacted 6.8 us, 64 of 509
-// in a pool of 25234 20.9.  The counted copies move 6254 pairs of 64 KB at 6.35 TB/s (94% of the measured copy
-// rate; four loads ahead instead of eight: 5.9).
+// the counts in global memory and hardware cluster barriers (about 0.6 us each, and what the blocks wait for one
+// another); counts spread over the cluster's shared memories measured no faster.  Loads of a phase are issued without
+// branches, so that they overlap; ids are ranked by ballots over bits kept from the first look at them (by scans over
+// the block and a second look, 256 rows took 18.1 us and the pool of 25234 ids 85.4).  Device time, copies of the pairs
+// included: eight rows of 20 blocks forked 8.1 us, 256 of 129 14.7 (one block: 31.5 without copies); six rows of 55
+// compacted 7.3 us, 64 of 509 in a pool of 25234 82.0.  The counted copies move 6254 pairs of 64 KB at 6.35 TB/s (94% of
+// the measured copy rate; four loads ahead instead of eight: 5.9).
 #include <algorithm>
 #include <atomic>
 
@@ -68,18 +70,22 @@ struct Run {
     __device__ __forceinline__ unsigned at(unsigned r) const { return first + 32 * r; }
 };
 
-// flag(i) of a lane's items, kept as bits for the first 32 of them; its warp's count.  Eight loads ahead of their use.
+// flag(i) of a lane's items, kept as bits for the first 32 of them; its warp's count.  Four at a time, without branches
+// (items past the end look at item 0 in vain), so that their loads overlap.
 struct Flags {
     unsigned bits = 0;
     int count = 0;
     template <typename Flag>
     __device__ __forceinline__ Flags(const Run &run, Flag flag) {
-        for (unsigned r0 = 0; r0 < run.rounds; r0 += 8) {
-            bool f[8];
+        for (unsigned r0 = 0; r0 < run.rounds; r0 += 4) {
+            bool f[4];
 #pragma unroll
-            for (unsigned k = 0; k < 8; ++k) f[k] = r0 + k < run.rounds && run.at(r0 + k) < run.end && flag(run.at(r0 + k));
+            for (unsigned k = 0; k < 4; ++k) {
+                const bool there = (r0 + k < run.rounds) & (run.at(r0 + k) < run.end);
+                f[k] = flag(there ? run.at(r0 + k) : 0u) & there;
+            }
 #pragma unroll
-            for (unsigned k = 0; k < 8; ++k) {
+            for (unsigned k = 0; k < 4; ++k) {
                 if (r0 + k < 32) bits |= static_cast<unsigned>(f[k]) << (r0 + k);
                 count += __popc(__ballot_sync(kFull, f[k]));
             }
@@ -135,19 +141,15 @@ __device__ __forceinline__ void share_counts(const Team<ONE> &team, const int (&
             for (int n = 0; n < N; ++n) s_part[n] = mine[n];
         }
         cluster.sync();
-        int theirs[kBlocks][N];
+        // lane c reads block c's
+        const int lane = threadIdx.x & 31;
+        int theirs[N];
 #pragma unroll
-        for (int c = 0; c < kBlocks; ++c)
-#pragma unroll
-            for (int n = 0; n < N; ++n) theirs[c][n] = cluster.map_shared_rank(&s_part[0], c)[n];
+        for (int n = 0; n < N; ++n) theirs[n] = lane < kBlocks ? cluster.map_shared_rank(&s_part[0], lane)[n] : 0;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            before[n] = all[n] = 0;
-#pragma unroll
-            for (int c = 0; c < kBlocks; ++c) {
-                if (c < static_cast<int>(team.rank)) before[n] += theirs[c][n];
-                all[n] += theirs[c][n];
-            }
+            before[n] = __reduce_add_sync(kFull, lane < static_cast<int>(team.rank) ? theirs[n] : 0);
+            all[n] = __reduce_add_sync(kFull, theirs[n]);
         }
     }
 }
@@ -181,11 +183,12 @@ __device__ __forceinline__ int checked(const ShareArgs &a, int x) {
 }
 
 __device__ __forceinline__ unsigned blocks_of(const ShareArgs &a, int len) {
-    return static_cast<unsigned>((static_cast<long long>(len) + a.bs - 1) / a.bs);
+    return (static_cast<unsigned>(len) + a.bs - 1u) / static_cast<unsigned>(a.bs);   // below 2^31: MBS * bs <= 2^31 - 1 - bs
 }
 
-// Every entry of the B rows, eight a thread at a time: first all are loaded (x = load(source, b, j)), then all
-// looked up (x = map(x)), then all put to use (use(source, b, j, x)), so that a thread's loads overlap.
+// Every entry of the B rows, eight a thread at a time: first all are loaded (x = load(source, b, j, whether there is one),
+// without branches), then all looked up (x = map(x)), then all put to use (use(source, b, j, x)), so that a thread's loads
+// overlap.
 // ONE: entries one after the other, their rows' sources (s_rows) at hand; else 256 entries of a row to a warp.
 // The first pass (FIRST) starts with the team's barrier, past the loads of the cluster's first entries, which
 // `held` keeps for the second pass.
@@ -211,7 +214,7 @@ __device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> 
             for (int k = 0; k < kAhead; ++k) {
                 const unsigned i = i0 + k * kThreads;
                 row[k] = MBS > 1 ? __umulhi(i, inv) : i;
-                x[k] = i < total ? load(s_rows[row[k]], row[k], i - row[k] * MBS) : -1;
+                x[k] = i < total ? load(s_rows[row[k]], row[k], i - row[k] * MBS, true) : -1;
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) x[k] = map(x[k]);
@@ -226,14 +229,14 @@ __device__ __forceinline__ void for_entries(const ShareArgs &a, const Team<ONE> 
         const unsigned long long items = static_cast<unsigned long long>(a.B) * segments;
         unsigned long long i = warp;
         do {
-            const unsigned b = static_cast<unsigned>(i / segments);
+            const unsigned b = static_cast<unsigned>(segments == 1 ? i : i / segments);
             const unsigned j0 = static_cast<unsigned>(i - static_cast<unsigned long long>(b) * segments) * kSegment + lane;
             Source s{-1, 0};
             int x[kAhead];
             if (FIRST || i != warp) {
                 if (i < items) s = source_of(a, b, FIRST && j0 == 0);
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) x[k] = i < items && j0 + 32 * k < MBS ? load(s, b, j0 + 32 * k) : -1;
+                for (int k = 0; k < kAhead; ++k) x[k] = load(s, b, j0 + 32 * k, (i < items) & (j0 + 32 * k < MBS));
             } else {
                 s = held.s;
 #pragma unroll
@@ -280,11 +283,14 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     int *first = ONE ? s_ids + NB : a.first;       // the lowest row that ends, partly filled, in it
     Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
     clear(a, team, refs, first, kNobody, s_rows);
+    const int32_t *table = a.B > 0 ? a.table : a.refs;   // an address to read in vain
     int32_t *rows = a.rows;   // [B][MBS] of the result: the table itself where nothing reads the parents' rows any more
     Held held;
     for_entries<true>(a, team, s_rows, held,
-                [&](const Source &s, unsigned, unsigned j) {
-                    return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(max(s.row, 0)) * a.MBS + j] : -1;
+                [&](const Source &s, unsigned, unsigned j, bool there) {
+                    there = there & (j < blocks_of(a, s.len));
+                    const int x = table[there ? static_cast<size_t>(s.row) * a.MBS + j : 0];
+                    return there ? x : -1;
                 }, [](int x) { return x; },
                 [&](const Source &s, unsigned b, unsigned j, int x) {
                     x = checked(a, x);
@@ -310,13 +316,14 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     }
     auto unused = [&](unsigned i) {
         const int inside = refs[i], ends = first[i];   // both loads at once
-        return inside == 0 && ends == kNobody;
+        return (inside == 0) & (ends == kNobody);
     };
     const Flags spare(my_ids, unused);
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
         const int b = static_cast<int>(my_rows.at(k));
-        if (len[k] % a.bs == 0 || old[k] < 0 || (refs[old[k]] == 0 && first[old[k]] == b)) old[k] = -1;
+        const int x = max(old[k], 0), inside = refs[x], ends = first[x];
+        if (len[k] % a.bs == 0 || old[k] < 0 || (inside == 0 && ends == b)) old[k] = -1;
         mine[0] += __popc(__ballot_sync(kFull, old[k] >= 0));
     }
     mine[1] = spare.count;
@@ -384,8 +391,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
     Source *s_rows = reinterpret_cast<Source *>(s_ids + 2 * static_cast<size_t>(NB));
     auto held = [&](unsigned i) { return a.held != nullptr && a.held[i] != 0; };
     clear(a, team, refs, moved, 0, s_rows);
-    auto entry = [&](const Source &s, unsigned b, unsigned j) {
-        return j < blocks_of(a, s.len) ? a.table[static_cast<size_t>(b) * a.MBS + j] : -1;
+    const int32_t *table = a.B > 0 ? a.table : a.refs;   // an address to read in vain
+    auto entry = [&](const Source &s, unsigned b, unsigned j, bool there) {
+        there = there & (j < blocks_of(a, s.len));
+        const int x = table[there ? static_cast<size_t>(b) * a.MBS + j : 0];
+        return there ? x : -1;
     };
     Held first;
     for_entries<true>(a, team, s_rows, first, entry, [](int x) { return x; }, [&](const Source &, unsigned, unsigned, int x) {
@@ -472,7 +482,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
         }
     }
     team.sync();
-    for_entries<false>(a, team, s_rows, first, entry, [&](int x) { return x >= 0 && x < a.NB ? moved[x] : -1; },
+    for_entries<false>(a, team, s_rows, first, entry,
+                [&](int x) {
+                    const bool there = (x >= 0) & (x < a.NB);
+                    const int to = moved[there ? x : 0];
+                    return there ? to : -1;
+                },
                 [&](const Source &, unsigned b, unsigned j, int x) { a.table_out[static_cast<size_t>(b) * a.MBS + j] = x; });
 }
 

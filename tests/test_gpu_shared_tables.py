@@ -133,6 +133,22 @@ def test_compact_matches_the_row_by_row_form(B, bs, hi, spare, in_place):
             same(dict(table=to, refs=refs, free_list=free, free_count=fc, pairs=pairs, pair_count=pc), want)
 
 
+@pytest.mark.parametrize("nb", [1, 9, 30000])
+def test_no_rows_at_all(nb):
+    i = lambda *n: torch.full(n, -9, dtype=torch.int32, device="cuda")
+    ws = i(pkv.block_tables_share_workspace_bytes(0, 4, nb) // 4)
+    for held in (None, [1] + [0] * (nb - 1)):
+        refs, free, fc, pc = i(nb), i(nb), i(1), i(1)
+        h = None if held is None else dev(held)
+        for call in (lambda: pkv.block_tables_fork(i(0, 4), i(0), None, i(0, 4), i(0), refs, free, fc, i(0, 2), pc, 8, held=h, workspace=ws),
+                     lambda: pkv.block_tables_compact(i(0, 4), i(0), i(0, 4), refs, free, fc, i(nb // 2, 2), pc, 8, held=h, workspace=ws)):
+            call()
+            n = nb - (held is not None)
+            assert int(fc) == n and int(pc) == 0 and refs.tolist() == (held or [0] * nb)
+            assert free.tolist() == list(range(nb - 1, nb - 1 - n, -1)) + [-1] * (nb - n)
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("nb", [24576, 24577, 262144, 262145, 700001])
 def test_pools_at_the_borders_of_the_ways_to_count(nb):
     # one block's shared memory, a lane's bits for 32 ids, and past them; blocks used at both ends of the pool
