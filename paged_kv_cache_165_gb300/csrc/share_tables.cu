@@ -21,7 +21,7 @@
 // branches, so that they overlap; ids are ranked by ballots over bits kept from the first look at them (by scans over
 // the block and a second look, 256 rows took 18.1 us and the pool of 25234 ids 85.4).  Device time, copies of the pairs
 // included: eight rows of 20 blocks forked 8.1 us, 256 of 129 14.7 (one block: 31.5 without copies); six rows of 55
-// compacted 7.3 us, 64 of 509 in a pool of 25234 82.0.  The counted copies move 6254 pairs of 64 KB at 6.35 TB/s (94% of
+// compacted 7.3 us, 64 of 509 in a pool of 25234 81.  The counted copies move 6254 pairs of 64 KB at 6.48 TB/s (95% of
 // the measured copy rate; four loads ahead instead of eight: 5.9).
 #include <algorithm>
 #include <atomic>
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const ShareArgs a) {
 constexpr int kCopyThreads = 256, kCopyAhead = 8;
 
 template <typename U>
-__global__ void __launch_bounds__(kCopyThreads)
+__global__ void __launch_bounds__(kCopyThreads, 5)
     kv_block_copy_counted_kernel(U *kc, U *vc, const int32_t *pairs, int n, const int32_t *count, long long block_units, int NB,
                                  unsigned *err) {
     pdl_wait();
@@ -599,7 +599,9 @@ cudaError_t launch_kv_block_copy_counted(void *k_cache, void *v_cache, int elem_
     size_t at = bytes | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
     const int u = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : at % 2 == 0 ? 2 : 1;
     const long long units = static_cast<long long>(bytes / u), span = kCopyThreads * kCopyAhead;
-    const unsigned grid = static_cast<unsigned>(std::min(2ll * n * ((units + span - 1) / span), 8ll * std::max(sm_count, 1)));
+    // fifteen blocks an SM, three times what it holds, so that none of few long ones ends alone (6254 pairs: eight 64.7 us,
+    // fifteen 63.3; forty 61.7, but a list without pairs then costs their start)
+    const unsigned grid = static_cast<unsigned>(std::min(2ll * n * ((units + span - 1) / span), 15ll * std::max(sm_count, 1)));
 #define PKV_COPY(UT)                                                                                                     \
     return launch_dependent(kv_block_copy_counted_kernel<UT>, dim3(grid), dim3(kCopyThreads), 0, stream,                 \
                             static_cast<UT *>(k_cache), static_cast<UT *>(v_cache), pairs, n, count, units, NB, err)

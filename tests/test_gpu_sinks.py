@@ -258,3 +258,24 @@ def test_streams_and_a_graph_over_growing_lengths():
         ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, ld.cpu(), cu, 0.1, 32, 5)
         assert_attn_close(out, ref, f"step {n}")
         assert_attn_close(lse, ref_lse, f"step {n}")
+
+
+def test_two_calls_at_once():
+    # one path each, chunks merged by their last block, on two streams with a workspace each
+    cases = []
+    for hq, dtype, nqs, splits in ((16, BF16, [1, 1], 4), (64, BF16, [3, 2], 3), (4, F32, [1, 2], 5)):
+        q, kc, vc, _, _, table, _, clens, cu = make_case(hq, [700, 900], nqs, hq, 2, 128, 16, dtype, 300, 20)
+        ref, _ = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 0.1, 300, 20)
+        Tq, mq = sum(nqs), max(nqs)
+        n = pkv.paged_attention_sinks_workspace_bytes(2, Tq, mq, hq, 2, 128, 16, table.shape[1], 300, 20, splits)
+        t = [dev(x) for x in (q, kc, vc, table, clens, cu)]
+        for _ in range(2):
+            cases.append((t, mq, splits, torch.zeros(max(16, n), dtype=torch.uint8, device="cuda"), torch.empty_like(t[0]), ref, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (q, kc, vc, table, clens, cu), mq, splits, ws, out, _, s in cases:
+            pkv.paged_attention_sinks(out, q, kc, vc, table, clens, 0.1, 300, 20, cu_q=cu, max_q=mq, num_splits=splits, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for t, _, _, _, out, ref, _ in cases:
+        assert_attn_close(out, ref, "out", 1e-4)
+    assert pkv.get_device_error() == 0
