@@ -205,3 +205,56 @@ def test_dependents_read_what_the_kernel_before_them_wrote():
         torch.cuda.synchronize()
         assert torch.equal(*got), i
     pkv.get_device_error()                              # a count beyond the list
+
+
+def test_graphs_in_which_copies_and_fills_come_before_the_calls():
+    # memory nodes right before kernels that start as dependents: inputs copied in, outputs filled, every replay
+    g = torch.Generator().manual_seed(8)
+    x, turns = torch.randn((500, 4, 64), generator=g).cuda(), pkv.rope_turns(64)
+    given, positions = torch.zeros(500, **I32), torch.zeros(500, **I32)
+    rotated = torch.zeros_like(x)
+    u_given, u, cu = torch.zeros(6, device="cuda"), torch.zeros(6, device="cuda"), torch.arange(7, **I32).mul_(0)
+    probs = torch.softmax(torch.randn((6, 300), generator=g), 1).cuda()
+    accepted, tokens, none = torch.zeros(6, **I32), torch.zeros(6, **I32), torch.zeros(0, **I32)
+    table, lens = torch.arange(12, **I32).view(3, 4), torch.zeros(3, **I32)
+    lens_given, blocks = torch.zeros(3, **I32), DeviceBlocks(20, 4, 3, 4, 0)
+    cache = torch.randn((20, 1, 4, 8), generator=g).cuda()
+    k, v = torch.zeros_like(cache), torch.zeros_like(cache)
+
+    def step():
+        positions.copy_(given)
+        pkv.rope(rotated, x, None, None, positions, turns)
+        u.copy_(u_given)
+        pkv.verify_drafts(accepted, tokens, probs, none, cu, u)
+        blocks.block_table.copy_(table)
+        blocks.context_lens.copy_(lens_given)
+        blocks.fork(lens)                              # every row takes row 0's sequence
+        k.copy_(cache)
+        v.zero_()
+        blocks.copy(k, v)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(5):
+        given.copy_(torch.randint(0, 10 ** 6, (500,), generator=g, dtype=torch.int32))
+        u_given.copy_(torch.rand(6, generator=g))
+        lens_given.copy_(torch.tensor([n + 5, 3, 1], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.empty_like(x)
+        pkv.rope(want, x, None, None, given, turns)
+        assert torch.equal(rotated, want)
+        assert tokens.tolist() == serve.verify_drafts(probs, None, [], [0] * 7, u_given)[1]
+        forked = serve.block_tables_fork(table.cpu(), [n + 5, 3, 1], [0, 0, 0], 4, 20)
+        assert blocks.block_table.tolist() == forked["table"] and blocks.context_lens.tolist() == forked["lens"]
+        wanted = cache.clone()
+        for a, b in forked["pairs"]:
+            wanted[b] = cache[a]
+        assert torch.equal(k, wanted) and not v.any()
+    assert pkv.get_device_error() == 0
