@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
         const unsigned b = my_rows.at(k);
         const bool there = k < static_cast<int>(my_rows.rounds) && b < my_rows.end;
         len[k] = there ? a.place[b] : 0;
-        old[k] = there ? a.last[b] : -1;      // written where the length asks for it
+        const int last = there ? a.last[b] : -1;
+        old[k] = len[k] % a.bs != 0 ? last : -1;   // of other rows this call has written none: whatever the workspace held
     }
     auto unused = [&](unsigned i) {
         const int inside = refs[i], ends = first[i];   // both loads at once
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ShareArgs a) {
     for (int k = 0; k < kRowsEach; ++k) {
         const int b = static_cast<int>(my_rows.at(k));
         const int x = max(old[k], 0), inside = refs[x], ends = first[x];
-        if (len[k] % a.bs == 0 || old[k] < 0 || (inside == 0 && ends == b)) old[k] = -1;
+        if (inside == 0 && ends == b) old[k] = -1;   // it keeps its block (old[k] of -1 stays)
         mine[0] += __popc(__ballot_sync(kFull, old[k] >= 0));
     }
     mine[1] = spare.count;

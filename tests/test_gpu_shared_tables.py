@@ -288,3 +288,44 @@ def test_refusals_on_the_gpu():
         with pytest.raises((ValueError, TypeError, pkv.PkvError)):
             pkv.block_tables_fork(**{**ok, **bad})
     pkv.get_device_error()
+
+
+@pytest.mark.parametrize("fill", ["largest", "lowest", "any"])
+@pytest.mark.parametrize("B,bs,hi,spare", [(1, 16, 16, 3), (9, 16, 90, 9), (64, 4, 40, 70), (300, 16, 300, 300), (2100, 4, 12, 2100), (8, 16, 300, 25000)])
+def test_workspaces_of_any_contents(B, bs, hi, spare, fill):
+    """Rows without a partly filled last block (idle ones, and whole blocks) leave their scratch unwritten."""
+    rng = np.random.default_rng(B)
+    lens = np.where(rng.random(B) < 0.4, 0, np.where(rng.random(B) < 0.5, rng.integers(0, hi // bs + 1, B) * bs, rng.integers(0, hi + 1, B)))
+    width = -(-hi // bs) + 1
+    table, nb = tables(rng, B, bs, width, lens, spare=spare)
+    n = pkv.block_tables_share_workspace_bytes(B, width, nb) // 4
+    most = 2 ** 31 - 1
+    lo, end = {"largest": (most, most + 1), "lowest": (-most - 1, -most), "any": (-most - 1, most + 1)}[fill]
+    i = lambda *shape: torch.full(shape, -9, dtype=torch.int32, device="cuda")
+    ws = lambda: torch.randint(lo, end, (n,), dtype=torch.int32, device="cuda")
+    for parents in (None, rng.integers(-1, B, B)):
+        want = serve.block_tables_fork(table, lens, parents, bs, nb)
+        for in_place in (False, True):
+            t, l = dev(table), dev(lens)
+            got = dict(table=t if in_place else i(B, width), lens=l if in_place else i(B), refs=i(nb), free_list=i(nb), free_count=i(1),
+                       pairs=i(B, 2), pair_count=i(1))
+            pkv.block_tables_fork(t, l, None if parents is None else dev(parents), *got.values(), bs, workspace=ws())
+            assert pkv.get_device_error() == 0
+            same(got, want)
+    got = dict(table=i(B, width), refs=i(nb), free_list=i(nb), free_count=i(1), pairs=i(nb // 2, 2), pair_count=i(1))
+    pkv.block_tables_compact(dev(table), dev(lens), *got.values(), bs, workspace=ws())
+    assert pkv.get_device_error() == 0
+    same(got, serve.block_tables_compact(table, lens, bs, nb))
+
+
+def test_device_blocks_over_recycled_memory():
+    blocks = DeviceBlocks(40, 4, 6, 6, 32)
+    blocks._share_ws.fill_(2 ** 31 - 1)   # what torch.empty may find
+    blocks.extend(dev([6, 8, 0, 0, 9, 0]))
+    before = blocks.block_table.tolist()
+    blocks.settle()                       # idle rows and whole blocks: nothing to do
+    assert int(blocks.pair_count) == 0 and int(blocks.free_count) == 40 - 2 - 2 - 3
+    lens = blocks.context_lens.tolist()
+    assert lens == [6, 8, 0, 0, 9, 0]
+    assert [row[:-(-n // 4)] for row, n in zip(blocks.block_table.tolist(), lens)] == [row[:-(-n // 4)] for row, n in zip(before, lens)]
+    assert pkv.get_device_error() == 0
