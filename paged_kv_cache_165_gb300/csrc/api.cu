@@ -339,6 +339,7 @@ static size_t attention_workspace(int B, int Tq, int max_q, int Hq, int Hkv, int
     if (device_state(&st) != PKV_OK) return 0;
     const bool one_per_seq = Tq == B && max_q <= 1;
     const int vis = visible_blocks_with_sinks(MBS, bs, window, sinks, one_per_seq ? 1 : max_q);
+    if (sinks > 0 && (B == 0 || Tq == 0)) return 0;   // the call returns at once
     if (sinks > 0)   // whatever the caches' type and alignment
         return std::max(plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_F32, num_splits, st->sm_count, true).workspace_bytes,
                         plan_sinks(B, Tq, max_q, Hq, Hkv, d, bs, vis, 1, PKV_BF16, num_splits, st->sm_count, true).workspace_bytes);

@@ -284,7 +284,8 @@ void plan_sinks_simt(SinksPlan &plan, int rows, int Hq, int Hkv, int d, int bs, 
     const int m = Hq / Hkv;
     const long long tokens = static_cast<long long>(pages) * bs, slots = static_cast<long long>(d <= 64 ? 5 : 3) * std::max(sm_count, 1);
     const long long most = std::min<long long>(pages, kDecodeMaxChunks);
-    auto units = [&](int heads) { return static_cast<long long>(rows) * Hkv * ((m + heads - 1) / heads); };
+    // at least one, so that no count of rows divides by zero
+    auto units = [&](int heads) { return std::max(1ll, static_cast<long long>(rows) * Hkv * ((m + heads - 1) / heads)); };
     double best = -1;
     long long splits = 1;
     auto consider = [&](int heads, long long k) {
@@ -305,7 +306,7 @@ void plan_sinks_simt(SinksPlan &plan, int rows, int Hq, int Hkv, int d, int bs, 
         }
         for (long long k = least; k <= kSinksFusedChunks; ++k) consider(heads, k);
         consider(heads, least);
-        if (slots / std::max(units(heads), 1ll) > std::max<long long>(kSinksFusedChunks, least))
+        if (slots / units(heads) > std::max<long long>(kSinksFusedChunks, least))
             consider(heads, std::min(slots / units(heads), std::max(least, tokens / 256)));
     }
     plan.chunk_pages = static_cast<int>((pages + splits - 1) / splits);

@@ -279,3 +279,14 @@ def test_two_calls_at_once():
     for t, _, _, _, out, ref, _ in cases:
         assert_attn_close(out, ref, "out", 1e-4)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,d,bs", [(F32, 64, 16), (BF16, 128, 16), (BF16, 256, 32), (BF16, 96, 24)])
+@pytest.mark.parametrize("B", [0, 3])
+def test_batches_without_rows(B, dtype, d, bs):
+    for max_q in (0, 1, 4):
+        assert pkv.paged_attention_sinks_workspace_bytes(B, 0, max_q, 8, 2, d, bs, 64, 100, 4) == 0
+    t = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")
+    cache = t(5, 2, bs, d, dt=dtype)
+    pkv.paged_attention_sinks(t(0, 8, d, dt=F32), t(0, 8, d, dt=F32), cache, cache, t(B, 64), t(B), 1.0, 100, 4, cu_q=t(B + 1), max_q=4)
+    assert pkv.get_device_error() == 0
