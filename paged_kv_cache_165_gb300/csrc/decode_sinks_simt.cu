@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int x = 0; x < E; ++x) dot[i] += qv[h][x] * widen(k[i][x / V].x[x % V]);
             }
-            const float s = i0 + mine < n ? sum_each<KB, M>(dot, lane) * p.scale_log2 : (sum_each<KB, M>(dot, lane), -INFINITY);
+            const float sum_of_mine = sum_each<KB, M>(dot, lane);   // shuffles of the whole warp, past its last token too
+            const float s = i0 + mine < n ? sum_of_mine * p.scale_log2 : -INFINITY;
             float mx = s;
 #pragma unroll
             for (int m = 0; m < M; ++m) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16 >> m));

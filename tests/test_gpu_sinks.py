@@ -290,3 +290,16 @@ def test_batches_without_rows(B, dtype, d, bs):
     cache = t(5, 2, bs, d, dt=dtype)
     pkv.paged_attention_sinks(t(0, 8, d, dt=F32), t(0, 8, d, dt=F32), cache, cache, t(B, 64), t(B), 1.0, 100, 4, cu_q=t(B + 1), max_q=4)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs", [(4, 2, 64, F32, 16), (4, 1, 128, F32, 16), (2, 2, 256, F32, 16), (6, 2, 33, BF16, 8)])
+def test_the_last_batch_of_tokens_of_every_size(hq, hkv, d, dtype, bs):
+    # 1 to 40 visible tokens: a warp's last batch of four or eight holds every number of them, none included
+    lens = list(range(1, 41))
+    q, kc, vc, kp, vp, table, tp, clens, cu = make_case(d, lens, [1] * 40, hq, hkv, d, bs, dtype, 29, 11)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / math.sqrt(d), 29, 11)
+    for splits in (1, 2):
+        out, lse = run(q, kp, vp, tp, clens, cu, 29, 11, splits)
+        assert pkv.get_device_error() == 0
+        assert_attn_close(out, ref, f"splits {splits} out", atol(dtype, d))
+        assert_attn_close(lse, ref_lse, f"splits {splits} lse", atol(dtype, d))
