@@ -44,8 +44,8 @@ __device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1,
 
 template <int D, int BS, int TILES>
 struct SinksCfg {
-    // two blocks an SM with 96 KB of rings each (d = 256: 64 KB to 128 KB): a deeper ring and fewer, longer blocks than
-    // three of 64 KB (window decode 171 us against 181)
+    // two blocks an SM with 96 KB of rings each: a deeper ring and fewer, longer blocks than three of 64 KB (window decode
+    // 171 us against 181).  d = 256: rings of 64 KB, two blocks; with pages of 32, 128 KB and one block (kBlocks)
     static constexpr int NW = D == 256 ? 2 : BS * D == 4096 ? 3 : 4;                          // warps
     static constexpr int ST = D == 256 ? 2 : 98304 / (NW * 4 * BS * D);                       // stages of a warp's ring
     static constexpr int NT = BS / 8, KT = BS / 16, KS = D / 16;     // score tiles, k-steps of P.V and of q.K
@@ -59,8 +59,12 @@ struct SinksCfg {
     static constexpr int kQBytes = kQShared ? TILES * KS * 32 * 24 : 0;
     static constexpr int kOffBar = (kOffQ + kQBytes + 15) / 16 * 16;
     static constexpr int kSmemBytes = 1024 + kOffBar + NW * ST * 8;
-    static constexpr int kBlocks = 2;                                // per SM
+    static constexpr int kBlocks = 2 * (kSmemBytes + 1024) <= 233472 ? 2 : 1;   // per SM
 };
+static_assert(SinksCfg<64, 16, 1>::kBlocks == 2 && SinksCfg<64, 32, 1>::kBlocks == 2 && SinksCfg<128, 16, 1>::kBlocks == 2 &&
+                  SinksCfg<128, 32, 1>::kBlocks == 2 && SinksCfg<256, 16, 1>::kBlocks == 2 && SinksCfg<256, 16, 2>::kBlocks == 2 &&
+                  SinksCfg<256, 32, 1>::kBlocks == SinksCfg<256, 32, 2>::kBlocks,
+              "plan_sinks");
 
 // One warp's pages for T tiles of pairs (MAXT: of the CTA's layout); leaves its states (running maximum and sum in
 // base 2, unnormalised outputs) in shared memory.
@@ -444,11 +448,14 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
     const long long groups = (tiles + plan.tiles - 1) / plan.tiles;
     const long long units = static_cast<long long>(B) * Hkv * groups;
     if (units < 1) return simt();
-    const long long slots = 2ll * std::max(sm_count, 1);   // blocks at a time
+    // blocks at a time: two an SM, but where their rings are too large for that
+    const int per_sm = d == 256 && bs == 32 ? SinksCfg<256, 32, 2>::kBlocks : 2;
+    const long long slots = static_cast<long long>(per_sm) * std::max(sm_count, 1);
     // Chunks of a sequence by a model of the time in tokens: a block costs its tokens and 512 more, a wave of blocks
     // as much as a block, a second wave at least half of one; more chunks than one cost a quarter of a wave where
     // they make several, and more than eight the merge kernel, 256 tokens.  (512 units of 4112 tokens, 1 to 4
-    // chunks: 172, 187, 190 and 184 us; 64 units of 2096: 37, 25, 24 and 22 us, five chunks 29.)  No chunk is longer
+    // chunks: 172, 187, 190 and 184 us; 64 units of 2096: 37, 25, 24 and 22 us, five chunks 29; with d = 256, pages of 32
+    // and one block an SM 152 units of 2080: 78, 90 and 96, 64 units of 8220: 273, 145 and 192.)  No chunk is longer
     // than 16384 tokens, so that a long sequence among short ones does not end the launch alone.
     int splits = 1;
     if (num_splits > 0) {

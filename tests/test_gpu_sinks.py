@@ -303,3 +303,20 @@ def test_the_last_batch_of_tokens_of_every_size(hq, hkv, d, dtype, bs):
         assert pkv.get_device_error() == 0
         assert_attn_close(out, ref, f"splits {splits} out", atol(dtype, d))
         assert_attn_close(lse, ref_lse, f"splits {splits} lse", atol(dtype, d))
+
+
+@pytest.mark.parametrize("nq", [1, 2])
+def test_sequences_that_fill_the_sms_once_are_not_split(nq):
+    # heads of 256 in pages of 32: one block an SM fits, so a second chunk would only be a second wave
+    B, nb, width = torch.cuda.get_device_properties(0).multi_processor_count, 70, 64
+    g = gen.generator(3)
+    kc, vc = (gen.randn(g, (nb, 1, 32, 256), BF16) for _ in range(2))
+    q = gen.randn(g, (B * nq, 8, 256), F32)
+    table = torch.randint(0, nb, (B, width), generator=g, dtype=torch.int32)
+    lens = torch.full((B,), width * 32, dtype=torch.int32)
+    cu = torch.arange(0, B * nq + 1, nq, dtype=torch.int32)
+    ref, _ = serve.paged_attention_sinks(q[:nq], kc, vc, table[:1], lens[:1], cu[:2], 1 / 16, 2000, 8)
+    out = torch.empty(B * nq, 8, 256, device="cuda")
+    pkv.paged_attention_sinks(out, dev(q), dev(kc), dev(vc), dev(table), dev(lens), 1 / 16, 2000, 8, cu_q=dev(cu), max_q=nq)   # no workspace
+    assert pkv.get_device_error() == 0
+    assert_attn_close(out[:nq], ref, "out", atol(BF16, 256))
