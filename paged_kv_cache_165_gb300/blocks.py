@@ -295,11 +295,13 @@ class DeviceBlocks:
         ws = max(16, _binding.block_tables_extend_workspace_bytes(rows, max_tokens),
                  _binding.block_tables_release_workspace_bytes(rows))
         self.refs = torch.zeros(num_blocks, dtype=torch.int32, device=device)
-        self.fork_pairs = torch.full((rows, 2), -1, dtype=torch.int32, device=device)
-        self.compact_pairs = torch.full((num_blocks // 2, 2), -1, dtype=torch.int32, device=device)
+        # one list for forks and compactions: with the one count, what a replayed graph or a call wrote last is what copy reads
+        self._all_pairs = torch.full((max(rows, num_blocks // 2), 2), -1, dtype=torch.int32, device=device)
+        self.fork_pairs, self.compact_pairs = self._all_pairs[:rows], self._all_pairs[:num_blocks // 2]
         self.pair_count = torch.zeros(1, dtype=torch.int32, device=device)
         self._share_ws = torch.empty(_binding.block_tables_share_workspace_bytes(rows, max_blocks, num_blocks) // 4,
                                      dtype=torch.int32, device=device)
+        # a longer list costs the copies of an empty one 1 us: no list is longer than the rows before the first compaction
         self._pairs = self.fork_pairs
         # two pieces: extend's stays zero, release's may hold anything
         self._extend_ws = torch.zeros(16, dtype=torch.uint8, device=device)
@@ -344,7 +346,6 @@ class DeviceBlocks:
         for are run by ``copy``, on every layer's caches, before anything is written.  Blocks that no row
         names any more are free; ``held`` (int32 [num_blocks]): blocks that stay in use besides."""
         from . import _binding
-        self._pairs = self.fork_pairs
         _binding.block_tables_fork(self.block_table, self.context_lens, parents, self.block_table, self.context_lens,
                                    self.refs, self.free_list, self.free_count, self.fork_pairs, self.pair_count,
                                    self.block_size, held=held, workspace=self._share_ws, stream=stream)
@@ -358,13 +359,15 @@ class DeviceBlocks:
     def compact(self, held: Optional[torch.Tensor] = None, stream=None) -> None:
         """The blocks in use move to the lowest ids; ``copy`` moves their contents."""
         from . import _binding
-        self._pairs = self.compact_pairs
+        self._pairs = self._all_pairs
         _binding.block_tables_compact(self.block_table, self.context_lens, self.block_table, self.refs, self.free_list,
                                       self.free_count, self.compact_pairs, self.pair_count, self.block_size, held=held,
                                       workspace=self._share_ws, stream=stream)
 
     def copy(self, k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
-        """The block copies of the last ``fork``, ``settle`` or ``compact``, in one layer's caches
-        ([num_blocks][Hkv][bs][d]; quantised ones as kv_block_copy takes them)."""
+        """The block copies of the last ``fork``, ``settle`` or ``compact`` to run, called or replayed in a
+        graph, in one layer's caches ([num_blocks][Hkv][bs][d]; quantised ones as kv_block_copy takes
+        them).  A graph that was captured before the first ``compact`` takes lists of up to ``rows`` pairs:
+        a longer one, compacted outside it, sets the device error "pair"."""
         from . import _binding
         _binding.kv_block_copy(k_cache, v_cache, self._pairs, stream=stream, count=self.pair_count)

@@ -329,3 +329,68 @@ def test_device_blocks_over_recycled_memory():
     assert lens == [6, 8, 0, 0, 9, 0]
     assert [row[:-(-n // 4)] for row, n in zip(blocks.block_table.tolist(), lens)] == [row[:-(-n // 4)] for row, n in zip(before, lens)]
     assert pkv.get_device_error() == 0
+
+
+def rows_of(blocks, k):
+    bs, flat, table = blocks.block_size, k.flatten().tolist(), blocks.block_table.tolist()
+    return [[flat[table[b][p // bs] * bs + p % bs] for p in range(n)] for b, n in enumerate(blocks.context_lens.tolist())]
+
+
+def captured(call):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    return g
+
+
+def test_copies_of_a_list_that_a_replayed_graph_wrote():
+    B, bs, nb = 4, 4, 60
+    k, v = (torch.arange(nb * bs, dtype=torch.float32, device="cuda").view(nb, 1, bs, 1).clone() for _ in range(2))
+    blocks = DeviceBlocks(nb, bs, B, 6, 32, order=[int(i) for i in np.random.default_rng(4).permutation(nb)])
+    parents = dev([0, 1, 0, 1])
+    forking = captured(lambda: blocks.fork(parents))
+    blocks.extend(dev([6, 9, 0, 0]))
+    first = rows_of(blocks, k)
+    blocks.compact()                    # the last call from Python
+    blocks.copy(k, v)
+    assert rows_of(blocks, k) == first
+    forking.replay()                    # the last to run
+    blocks.copy(k, v)
+    assert rows_of(blocks, k) == [first[p] for p in (0, 1, 0, 1)] and rows_of(blocks, v) == rows_of(blocks, k)
+
+    # and the other way round: a compaction in a graph, a fork called
+    blocks.context_lens.copy_(dev([6, 0, 6, 0]))
+    blocks.settle()
+    blocks.copy(k, v)
+    compacting = captured(blocks.compact)
+    blocks.fork(dev([-1, 2, 2, 2]))
+    blocks.copy(k, v)
+    before = rows_of(blocks, k)
+    assert before == [[], first[0], first[0], first[0]]
+    blocks.extend(dev([20, 3, 3, 3]))
+    blocks.context_lens.copy_(dev([0, 9, 9, 9]))
+    blocks.settle()
+    blocks.copy(k, v)
+    before = rows_of(blocks, k)
+    compacting.replay()
+    blocks.copy(k, v)
+    assert rows_of(blocks, k) == before and rows_of(blocks, v) == before
+    used = nb - int(blocks.free_count)
+    assert all(x < used for row in blocks.block_table.tolist() for x in row)
+    assert pkv.get_device_error() == 0
+
+
+def test_a_captured_copy_refuses_a_longer_list():
+    nb = 40
+    k, v = (torch.arange(nb, dtype=torch.float32, device="cuda").view(nb, 1, 1, 1).clone() for _ in range(2))
+    blocks = DeviceBlocks(nb, 1, 1, 8, 8, order=list(range(nb - 1, -1, -1)))
+    copying = captured(lambda: blocks.copy(k, v))
+    blocks.extend(dev([5]))
+    row = rows_of(blocks, k)
+    blocks.compact()
+    assert int(blocks.pair_count) == 5
+    copying.replay()
+    torch.cuda.synchronize()
+    assert pkv.get_device_error() == pkv.DEVERR["pair"]
+    blocks.copy(k, v)
+    assert rows_of(blocks, k) == row and pkv.get_device_error() == 0
