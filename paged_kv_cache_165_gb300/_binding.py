@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import platform
 import re
 
 import torch
@@ -45,6 +46,8 @@ def lib() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
+    if platform.machine() not in ("x86_64", "aarch64"):
+        raise RuntimeError(f"the binding passes arguments as x86-64 and aarch64 do; this machine is {platform.machine()}")
     path = library_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it first with "
@@ -122,7 +125,8 @@ def lib() -> ctypes.CDLL:
     L.pkv_block_tables_share_workspace_bytes.argtypes = [I, I, I]
     L.pkv_block_tables_share_workspace_bytes.restype = Z
     # The whole numbers of the calls of a decode step are declared as pointers, whose conversion takes half as long: an
-    # argument of 32 bits is the lower half of a 64-bit register or stack slot on both of x86-64 and aarch64.
+    # argument of 32 bits is the lower half of a 64-bit register or stack slot on both of x86-64 and aarch64 (lib() refuses
+    # other machines).
     N = P
     L.pkv_block_tables_fork.argtypes = [P] * 11 + [N] * 4 + [P, N, P]
     L.pkv_block_tables_fork.restype = I

@@ -316,3 +316,13 @@ def test_python_calls_refuse_host_tensors(L):
         pkv.block_tables_fork(t(1, 3), t(1), None, t(1, 3), t(1), t(4), t(4), t(1), t(1, 2), t(1), 4, workspace=t(40))
     with pytest.raises((ValueError, TypeError)):
         pkv.kv_block_copy(t(3, 1, 4, 8, dt=f), t(3, 1, 4, 8, dt=f), t(1, 2), count=t(1))
+
+
+def test_the_binding_refuses_other_machines(L, monkeypatch):
+    from paged_kv_cache_165_gb300 import _binding
+    monkeypatch.setattr(_binding, "_lib", None)
+    monkeypatch.setattr("platform.machine", lambda: "riscv64")
+    with pytest.raises(RuntimeError, match="riscv64"):
+        pkv.lib()
+    monkeypatch.undo()
+    assert pkv.lib() is L
