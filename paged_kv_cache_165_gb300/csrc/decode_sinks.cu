@@ -481,9 +481,12 @@ SinksPlan plan_sinks(int B, int rows, int max_q, int Hq, int Hkv, int d, int bs,
     if (plan.umma) chunk = (chunk + kSinksUmmaKeys / bs - 1) / (kSinksUmmaKeys / bs) * (kSinksUmmaKeys / bs);   // whole key tiles
     chunk = std::max(chunk, (pages + kDecodeMaxChunks - 1) / kDecodeMaxChunks);
     splits = (pages + chunk - 1) / chunk;
-    if (groups * splits > 0x7fffffffll) return simt();
+    // no more blocks than the call's rows can fill: max_q may be any bound (2^31 - 1 for none at all), and a block's first pair,
+    // group * pairs of a block, has to stay below 2^31
+    const long long launched = std::min(groups, (static_cast<long long>(rows) * (Hq / Hkv) + 8 * plan.tiles - 1) / (8 * plan.tiles));
+    if (launched * splits > 0x7fffffffll) return simt();
     plan.mma = true;
-    plan.groups = static_cast<int>(groups);
+    plan.groups = static_cast<int>(launched);
     plan.chunk_pages = chunk;
     plan.splits = splits;
     plan.fused_merge = splits > 1 && splits <= kSinksFusedChunks &&

@@ -320,3 +320,17 @@ def test_sequences_that_fill_the_sms_once_are_not_split(nq):
     pkv.paged_attention_sinks(out, dev(q), dev(kc), dev(vc), dev(table), dev(lens), 1 / 16, 2000, 8, cu_q=dev(cu), max_q=nq)   # no workspace
     assert pkv.get_device_error() == 0
     assert_attn_close(out[:nq], ref, "out", atol(BF16, 256))
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,bs", PATHS)
+def test_any_bound_of_the_rows_of_a_sequence(hq, hkv, d, dtype, bs):
+    # max_q says how many rows a sequence may have, not how many it has
+    lens, nqs = [300, 17, 90], [3, 0, 2]
+    q, kc, vc, kp, vp, table, tp, clens, cu = make_case(hq, lens, nqs, hq, hkv, d, bs, dtype, 40, 6)
+    ref, ref_lse = serve.paged_attention_sinks(q, kc, vc, table, clens, cu, 1 / math.sqrt(d), 40, 6)
+    for max_q in (3, 5, 1000, 10 ** 6, 2 ** 31 - 1):
+        for splits in (0, 1, 3):
+            out, lse = run(q, kp, vp, tp, clens, cu, 40, 6, splits, max_q=max_q)
+            assert pkv.get_device_error() == 0
+            assert_attn_close(out, ref, f"max_q {max_q} out", atol(dtype, d))
+            assert_attn_close(lse, ref_lse, f"max_q {max_q} lse", atol(dtype, d))
