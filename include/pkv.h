@@ -600,8 +600,8 @@ pkv_status pkv_kv_block_copy_counted(void *k_cache, void *v_cache, pkv_dtype dt,
  *
  * pkv_rope_turns -- the angles per position of the pairs, as fractions of a turn in 2^-64 units (turns: HOST
  * memory, [rot / 2]; f_j = base^(-2j / rot) / (2 pi) turns, computed in fp64).  The product of a position and
- * such a number, modulo 2^64, is the position's angle to within fp64's rounding of f_j, for every 32-bit
- * position.  Scaled for contexts `factor` times as long:
+ * such a number, modulo 2^64, is the position's angle to within fp64's rounding of f_j and its cut to 2^-63 (2^-32 of a
+ * turn at the farthest position), for every 32-bit position.  Scaled for contexts `factor` times as long:
  *   PKV_ROPE_LINEAR   f_j / factor
  *   PKV_ROPE_BASE     base * factor^(rot / (rot - 2)) in place of base (rot > 2)
  *   PKV_ROPE_PARTS    f_j (r + (1 - r) / factor), r = (n - low) / (high - low) cut to [0, 1], n = original * f_j
@@ -663,10 +663,11 @@ pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q,
  *   cu_drafts     int32 [B + 1], non-decreasing from 0 to D; k = 0: one token drawn from p_0
  *   context_lens, context_lens_out   int32 [B] or NULL both; the same or apart: L - (k - a), the length of a cache
  *                 that holds the drafts' K and V without those of the rejected ones
+ * Sums stay at 2^17 where they would pass it (no probabilities add up to that).
  * A drafted token outside [0, V) is rejected and sets PKV_DEVERR_PROBS; probabilities without mass (zero,
  * negative or NaN everywhere) set it too, and the token is -1.  In the sums probabilities count as at most 1, negative
- * ones and NaN as 0; a draft whose p or q is infinite or NaN is rejected.  An inconsistent cu_drafts sets
- * PKV_DEVERR_CU_SEQLENS: the sequence accepts nothing, its length stays and its tokens are not written.
+ * ones and NaN as 0; a draft whose p or q is infinite or NaN is rejected.  A sequence whose cu_drafts decrease or
+ * leave [0, D] sets PKV_DEVERR_CU_SEQLENS: it accepts nothing, its length stays and its tokens are not written.
  * B <= 65535, V < 2^30.
  */
 pkv_status pkv_verify_drafts(int32_t *accepted, int32_t *tokens, const void *target_probs, const void *draft_probs,

@@ -115,8 +115,6 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// ----------------------------------------------------------------------- TMA
-
 // A launch whose blocks may be scheduled while the kernel before it on the stream drains; the kernel calls
 // pdl_wait() before it reads or writes anything that an earlier kernel may touch, and reads it by plain loads: __ldg and
 // __restrict__ promise memory that does not change, and loads of that may be moved ahead of the wait.
@@ -135,6 +133,8 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 b
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
+
+// ----------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -11,7 +11,8 @@
 //
 // Small calls are bound by this chain's latency, larger ones by loads in flight (12 warps of 145 registers an SM).  2 sequences
 // of 18 to 41 tokens, 8 heads on 2 of 64 in fp32: 6.3 us (a warp a head and one token at a time: 10.4); 32 of 4000 to 8000,
-// window 2048 + 4, of 128 in fp32: 8 heads on 8 118 us (299), 4.55 TB/s, 32 on 8 162 (566).
+// window 2048 + 4, of 128 in fp32: 8 heads on 8 114 us (299), 4.7 TB/s, 32 on 8 149 (566): K and V come again for each four heads
+// and each row.
 #include <algorithm>
 #include <cmath>
 

@@ -14,7 +14,7 @@
 // prompts and by launch latency for a decode step.  17153 tokens of 64 + 8 + 8 heads of 128 in bf16: 115 us, 6.09 TB/s
 // (90% of the measured copy rate), at eight blocks an SM (122 us at six, then); cache hints and units dealt over a block's
 // tokens by number, two at a time, measured slower (122 and 147 against 118), rows fetched towards L2 ahead of the angles
-// too (126 to 150); 64 tokens 2.9 us.
+// too (126 to 150); 64 tokens 3 us.
 #include <algorithm>
 #include <cmath>
 
@@ -243,7 +243,7 @@ bool rope_turns(uint64_t *turns, int rot, double base, int scaling, double facto
         }
         if (!std::isfinite(f)) return false;
         f -= std::floor(f);
-        turns[j] = static_cast<uint64_t>(std::ldexp(f, 63)) << 1;   // f < 1; 63 bits hold fp64's 53
+        turns[j] = static_cast<uint64_t>(std::ldexp(f, 63)) << 1;   // f < 1; below 2^-11 its last bits are cut, by less than 2^-63
     }
     return true;
 }

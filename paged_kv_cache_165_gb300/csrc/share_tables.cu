@@ -20,8 +20,8 @@
 // another); counts spread over the cluster's shared memories measured no faster.  Loads of a phase are issued without
 // branches, so that they overlap; ids are ranked by ballots over bits kept from the first look at them (by scans over
 // the block and a second look, 256 rows took 18.1 us and the pool of 25234 ids 85.4).  Device time, copies of the pairs
-// included: eight rows of 20 blocks forked 8.1 us, 256 of 129 14.7 (one block: 31.5 without copies); six rows of 55
-// compacted 7.3 us, 64 of 509 in a pool of 25234 81.  The counted copies move 6254 pairs of 64 KB at 6.48 TB/s (95% of
+// included: eight rows of 20 blocks forked 8.4 us, 256 of 129 15.0 (one block: 31.5 without copies); six rows of 55
+// compacted 7.4 us, 64 of 509 in a pool of 25234 81.  The counted copies move 6254 pairs of 64 KB at 6.48 TB/s (95% of
 // the measured copy rate; four loads ahead instead of eight: 5.9).
 #include <algorithm>
 #include <atomic>

@@ -17,8 +17,9 @@
 // One cluster per sequence: each block sums its share of the row (a contiguous run for each warp), the totals
 // meet in distributed shared memory, and the warp whose run holds the border reads it once more, from L2.
 // One row of p, and one of q where a draft was rejected, is all that is read of the V-long rows.  64 sequences of
-// 131072 tokens: 15.6 us (56 MB, a floor of 8.2), of which the chain offsets - drafts - their probabilities before the
-// first load of a row and the border's search after the last take about half; one of 50001 tokens 6.8 us.  (Mantissas
+// 131072 tokens: 18.6 us (56 MB from HBM, a floor of 8.2; 15.9 with the rows in L2), of which the chain offsets - drafts - their
+// probabilities before the first load of a row and the border's search after the last take about half; one of 50001 tokens
+// 7.0 us.  (Mantissas
 // shifted in 64 bits instead of fp32: 33 us; the border sought 32 elements at a time: 48.)
 #include <algorithm>
 

@@ -198,3 +198,12 @@ def test_refusals_on_the_gpu():
                 dict(context_lens_out=i([1, 2])), dict(draft_tokens=torch.tensor(toks)), dict(target_probs=target.cpu())):
         with pytest.raises((ValueError, TypeError, pkv.PkvError)):
             pkv.verify_drafts(**{**ok, **bad})
+
+
+def test_sums_stay_at_two_to_the_seventeen():
+    # no distribution: ones past 2^17 elements no longer add to the sums
+    for V in (1 << 17, (1 << 18) + 5):
+        t = torch.ones((1, V), device="cuda")
+        for u, want in ((0.0, 0), (0.25, 1 << 15), (0.5, 1 << 16), (1 - 2.0 ** -24, (1 << 17) - 1)):
+            assert run(t, None, [], [0, 0], [u])[:2] == ([0], [want]), (V, u)
+    assert pkv.get_device_error() == 0
