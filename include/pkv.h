@@ -652,7 +652,7 @@ pkv_status pkv_rope(void *q_out, pkv_dtype q_out_dt, void *k_out, const void *q,
  *   that fails;  the next token is the lowest v with r_0 + .. + r_v > u_k * (r_0 + .. + r_{V-1}), where
  *   r = max(p_a - q_a, 0) for a < k (p_a itself where that is 0 everywhere) and r = p_k for a = k.
  * Sums are of whole multiples of 2^-46, to the nearest of which each probability is rounded (ties to even; exact
- * from 2^-22 on), so that the token depends neither on the order of summation nor on the GPU.
+ * from 2^-22 on, 0 below 2^-47), so that the token depends neither on the order of summation nor on the GPU.
  *   accepted      int32 [B]
  *   tokens        int32 [D + B], apart from draft_tokens: the accepted drafts of a sequence, its next token, -1 in the
  *                 rest of its k + 1 places
